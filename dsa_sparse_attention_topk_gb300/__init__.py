@@ -10,14 +10,20 @@ Functions (same names as the C entry points, without the ``dsa_`` prefix):
 * ``quant_kv_mxfp8(k, slot_mapping, k_cache)``  -- cache writer, MXFP8 indexer keys
 * ``quant_kv_fp8(kv, slot_mapping, kv_cache)``   -- cache writer, FP8 MLA latent rows
 * ``quant_kv(k, kv, slot_mapping, k_cache, kv_cache)`` -- both writers in one launch
+* ``rope(x, pos, turns, ...)``  -- rotary positions: turn part of every head
+* ``rope_quant_kv(k, kv, pos, slot_mapping, k_cache, kv_cache, turns, ...)`` -- the cache
+  writers with the rotation on the way
 * ``decode_step(...)``  -- writers, indexer + Top-K and SFA of one decode step in one call
 * ``indexer_topk(...)``                          -- fused Lightning Indexer + Top-K
 * ``indexer_scores(...)``                        -- the same scores written in full
 * ``sparse_attn(...)``                           -- Sparse Flash Attention
+* ``rope_turns(rot, ...)``                       -- the frequency table the two rotary calls
+  take, plain or scaled for long contexts (host arithmetic)
 * ``device_status()``                            -- read and clear the device status word
 """
 
 import ctypes
+import math
 import os
 
 import torch
@@ -69,6 +75,10 @@ _SIGS = {
     "dsa_decode_step": (ctypes.c_int, [_P, _P, _P, _I32, _P, _P, _I64, _P, _I32, _P, _I32, _I32, _I32,
                                        _P, _P, _I32, _P, _P, _I32, _I32, _P, _P, _I32, _F32, _P, _P, _P, _SZ,
                                        _P]),
+    "dsa_rope": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _I32, _I64, _I64, _I64, _I64, _P, _P, _I32, _I32, _I32,
+                                _F32, _I32, _P]),
+    "dsa_rope_quant_kv": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _I32, _P, _P, _I64, _P, _F32, _I32, _I32, _I32,
+                                         _P]),
     "dsa_device_status": (ctypes.c_int, [_P]),
     "dsa_test_stall_indexer": (ctypes.c_int, [_I32]),
     "dsa_topk_merge": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P]),
@@ -115,6 +125,25 @@ def _need(t, dtype, name):
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
 
 
+def _same_device(what, first, *others):
+    """Every tensor on the first one's CUDA device."""
+    if not first.is_cuda:
+        raise ValueError(f"{what}: tensors must be CUDA tensors")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{what}: tensors must be on one device ({t.device} and {first.device})")
+
+
+def _call_on(device, stream, fn, *args):
+    """Call a C entry point with `device` current, on `stream` (that device's current one)."""
+    s = ctypes.c_void_p((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, s))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, s))
+
+
 # ---- cache allocation (plain torch allocations of the documented layouts) ----------
 
 def alloc_k_cache(num_pages, device="cuda"):
@@ -157,6 +186,120 @@ def quant_kv(k, kv, slot_mapping, k_cache, kv_cache, stream=None):
                     kv_cache.numel() // (PAGE_SIZE * KVCACHE_TOKEN_BYTES)) * PAGE_SIZE
     _check(lib().dsa_quant_kv(_ptr(k), _ptr(kv), _ptr(slot_mapping), k.shape[0], _ptr(k_cache), _ptr(kv_cache),
                               num_slots, _stream(stream)))
+
+
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def rope_turns(rot, base=10000.0, scaling=None, factor=1.0, original_len=4096, beta_fast=32.0, beta_slow=1.0,
+               device="cuda"):
+    """Frequency table of a rotary part of ``rot`` dims: (turns int64 [rot / 2] on `device`,
+    amplitude).  Frequency i is base^(-2 i / rot) radians a position; ``turns`` holds it as
+    2^-64 turns.  ``scaling`` stretches it to `factor` times the original context length:
+
+    * None      as it is;
+    * "linear"  every frequency / factor;
+    * "ntk"     base * factor^(rot / (rot - 2)): the lowest frequency is divided by factor;
+    * "yarn"    by parts: a frequency that makes beta_fast turns or more in original_len
+                positions stays, one that makes beta_slow or fewer is divided by factor, a
+                linear ramp over the index in between; amplitude 0.1 ln(factor) + 1.
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rope_turns: rot must be even and at least 2 (got {rot})")
+    if not (base > 1.0 and math.isfinite(base)) or not (factor >= 1.0 and math.isfinite(factor)):
+        raise ValueError("rope_turns: base must be above 1 and factor at least 1")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"rope_turns: unknown scaling {scaling!r}")
+    if scaling == "ntk":
+        if rot < 4:
+            raise ValueError("rope_turns: ntk scaling needs rot >= 4")
+        base = base * factor ** (rot / (rot - 2))
+    freq = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    amplitude = 1.0
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    elif scaling == "yarn":
+        if original_len < 1 or not 0.0 < beta_slow < beta_fast:
+            raise ValueError("rope_turns: yarn needs original_len >= 1 and 0 < beta_slow < beta_fast")
+
+        def index_of(n_turns):  # the (fractional) index whose frequency makes n_turns in original_len
+            return rot * math.log(original_len / (2.0 * math.pi * n_turns)) / (2.0 * math.log(base))
+
+        low = max(math.floor(index_of(beta_fast)), 0)
+        high = min(math.ceil(index_of(beta_slow)), rot - 1)
+        width = max(high - low, 1e-3)
+        ramp = [min(max((i - low) / width, 0.0), 1.0) for i in range(rot // 2)]
+        freq = [f * (1.0 - r) + f / factor * r for f, r in zip(freq, ramp)]
+        amplitude = 0.1 * math.log(factor) + 1.0
+    turns = [round(f / (2.0 * math.pi) * 2.0 ** 64) for f in freq]
+    return torch.tensor(turns, dtype=torch.int64, device=device), amplitude
+
+
+def _layout(name):
+    if name not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)} (got {name!r})")
+    return ROPE_LAYOUTS[name]
+
+
+def rope(x, pos, turns, offset=0, layout="interleaved", amplitude=1.0, transpose=False, out=None, stream=None):
+    """Rotary positions: dims [offset, offset + 2 len(turns)) of every head of x turned to
+    pos.  x: bf16, fp16 or fp32 [n, d] or [n, h, d], last dim contiguous, any other strides;
+    pos: int32 [n]; turns, amplitude: from rope_turns; layout: "interleaved" (pairs 2i, 2i+1)
+    or "half" (pairs i, i + rot / 2).  transpose=True gives the gradient with respect to x,
+    given that of the result.  out=x works in place (only the rotary part is touched);
+    otherwise out must not overlap x.  Returns out."""
+    if x.dim() not in (2, 3) or x.dtype not in _DTYPES:
+        raise ValueError("rope: x must be [n, d] or [n, h, d] of bf16, fp16 or fp32")
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("rope: out must have x's shape and dtype")
+    _same_device("rope", x, pos, turns, out)
+    _need(pos, torch.int32, "pos")
+    _need(turns, torch.int64, "turns")
+    n, d = x.shape[0], x.shape[-1]
+    if pos.shape != (n,) or turns.dim() != 1:
+        raise ValueError("rope: pos must be [n] and turns [rot / 2]")
+    if (x.stride(-1) != 1 or out.stride(-1) != 1) and d > 1:
+        raise ValueError("rope: the last dim of x and out must be contiguous")
+    h, xh, oh = (x.shape[1], x.stride(1), out.stride(1)) if x.dim() == 3 else (1, 0, 0)
+    _call_on(x.device, stream, lib().dsa_rope, _ptr(x), _ptr(out), _DTYPES[x.dtype], n, h, d, x.stride(0), xh,
+             out.stride(0), oh, _ptr(pos), _ptr(turns), 2 * turns.shape[0], offset, _layout(layout),
+             float(amplitude), int(bool(transpose)))
+    return out
+
+
+def rope_quant_kv(k, kv, pos, slot_mapping, k_cache, kv_cache, turns, amplitude=1.0, k_offset=0, k_layout="half",
+                  kv_layout="interleaved", stream=None):
+    """quant_kv with the rotation on the way: k bf16 [n, 128] (rotary dims [k_offset,
+    k_offset + 64), layout k_layout) -> k_cache, kv bf16 [n, 576] (rotary dims [512, 576),
+    layout kv_layout) -> kv_cache, turned to the positions pos int32 [n] and quantised from
+    fp32, at the int64 slots [n] (negative: skipped).  Rows may lie further apart than their
+    width (a slice of a wider projection).  k and k_cache, or kv and kv_cache, may be None."""
+    if k is None and kv is None:
+        raise ValueError("rope_quant_kv: k or kv must be given")
+    first = k if k is not None else kv
+    n = first.shape[0]
+    for t, cache, width, name in ((k, k_cache, INDEX_DIM, "k"), (kv, kv_cache, LATENT_DIM, "kv")):
+        if (t is None) != (cache is None):
+            raise ValueError(f"rope_quant_kv: {name} and {name}_cache go together")
+        if t is None:
+            continue
+        if t.dtype != torch.bfloat16 or t.shape != (n, width) or t.stride(1) != 1:
+            raise ValueError(f"{name} must be bf16 [n, {width}] with contiguous rows")
+        _need(cache, torch.uint8, f"{name}_cache")
+    _same_device("rope_quant_kv", first, k, kv, pos, slot_mapping, k_cache, kv_cache, turns)
+    _need(pos, torch.int32, "pos")
+    _need(slot_mapping, torch.int64, "slot_mapping")
+    _need(turns, torch.int64, "turns")
+    if pos.shape != (n,) or slot_mapping.shape != (n,) or turns.shape != (32,):
+        raise ValueError("rope_quant_kv: pos and slot_mapping must be [n] and turns [32]")
+    pages = min(k_cache.numel() // KCACHE_PAGE_BYTES if k is not None else 1 << 48,
+                kv_cache.numel() // (PAGE_SIZE * KVCACHE_TOKEN_BYTES) if kv is not None else 1 << 48)
+    _call_on(first.device, stream, lib().dsa_rope_quant_kv, _ptr(k), 0 if k is None else k.stride(0), _ptr(kv),
+             0 if kv is None else kv.stride(0), _ptr(pos), _ptr(slot_mapping), n, _ptr(k_cache), _ptr(kv_cache),
+             pages * PAGE_SIZE, _ptr(turns), float(amplitude), k_offset, _layout(k_layout), _layout(kv_layout))
 
 
 def indexer_topk(q, w, k_cache, page_table, seq_lens, q_seq, q_pos, topk, max_ctx,

@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <cstdarg>
 #include <cstdio>
+#include <cmath>
 #include <mutex>
 #include <string>
 
@@ -146,6 +147,78 @@ int dsa_quant_kv(const void* k_bf16, const void* kv_bf16, const int64_t* slot_ma
   cudaError_t e = dsa::launch_quant_both(k_bf16, kv_bf16, slot_mapping, n_tokens, k_cache, kv_cache, num_slots, st,
                                          static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "quant_kv launch");
+}
+
+int dsa_rope(const void* x, void* out, int32_t dtype, int32_t n, int32_t h, int32_t d, int64_t x_stride_t,
+             int64_t x_stride_h, int64_t out_stride_t, int64_t out_stride_h, const int32_t* pos,
+             const int64_t* turns, int32_t rot, int32_t offset, int32_t layout, float amplitude,
+             int32_t transpose, void* stream) {
+  if (n < 0 || h < 0) return fail(DSA_ERR_INVALID_ARG, "rope: negative n or h");
+  if (dtype < DSA_DTYPE_BF16 || dtype > DSA_DTYPE_FP32)
+    return fail(DSA_ERR_UNSUPPORTED, "rope: dtype must be bf16, fp16 or fp32");
+  if (d < 2 || d > 65536) return fail(DSA_ERR_UNSUPPORTED, "rope: d must be 2..65536 (got %d)", d);
+  if (rot < 2 || rot % 2 || rot > d || offset < 0 || offset > d - rot)
+    return fail(DSA_ERR_INVALID_ARG, "rope: rot must be even and [offset, offset + rot) lie in [0, %d)", d);
+  if (layout != DSA_ROPE_INTERLEAVED && layout != DSA_ROPE_HALF)
+    return fail(DSA_ERR_INVALID_ARG, "rope: unknown layout %d", layout);
+  if (!std::isfinite(amplitude)) return fail(DSA_ERR_INVALID_ARG, "rope: amplitude must be finite");
+  if (n == 0 || h == 0) return DSA_OK;
+  if (static_cast<int64_t>(n) * h > INT32_MAX)
+    return fail(DSA_ERR_UNSUPPORTED, "rope: n * h must be below 2^31");
+  if (!x || !out || !pos || !turns) return fail(DSA_ERR_INVALID_ARG, "rope: null pointer");
+  const size_t size = dtype == DSA_DTYPE_FP32 ? 4 : 2;
+  if (!aligned(x, size) || !aligned(out, size) || !aligned(pos, 4) || !aligned(turns, 8))
+    return fail(DSA_ERR_INVALID_ARG, "rope: a pointer is not aligned to its element");
+  // (strides below 2^40 elements keep every offset far from overflow)
+  const int64_t most = int64_t{1} << 40;
+  if (x_stride_t < 0 || x_stride_h < 0 || x_stride_t > most || x_stride_h > most || out_stride_t < 0 ||
+      out_stride_h < 0 || out_stride_t > most || out_stride_h > most)
+    return fail(DSA_ERR_INVALID_ARG, "rope: a stride is negative or above 2^40");
+  // strides of an axis of length 1 are never used
+  if (n == 1) x_stride_t = out_stride_t = 0;
+  if (h == 1) x_stride_h = out_stride_h = 0;
+  auto nests = [](int64_t in, int n_in, int64_t over, int n_over, int64_t width) {
+    return (n_in == 1 || in >= width) && (n_over == 1 || over >= (n_in - 1) * in + width);
+  };
+  if (!nests(out_stride_h, h, out_stride_t, n, d) && !nests(out_stride_t, n, out_stride_h, h, d))
+    return fail(DSA_ERR_INVALID_ARG, "rope: the strides of out let its elements overlap");
+  if (x == out && (x_stride_t != out_stride_t || x_stride_h != out_stride_h))
+    return fail(DSA_ERR_INVALID_ARG, "rope: in place, x and out need the same strides");
+  dsa::RopeArgs a{x, out, dtype, n, h, d, x_stride_t, x_stride_h, out_stride_t, out_stride_h, pos, turns, rot, offset,
+                  layout, amplitude, transpose};
+  cudaError_t e = dsa::launch_rope(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "rope launch");
+}
+
+int dsa_rope_quant_kv(const void* k_bf16, int64_t k_stride, const void* kv_bf16, int64_t kv_stride,
+                      const int32_t* pos, const int64_t* slot_mapping, int32_t n_tokens, uint8_t* k_cache,
+                      uint8_t* kv_cache, int64_t num_slots, const int64_t* turns, float amplitude,
+                      int32_t k_offset, int32_t k_layout, int32_t kv_layout, void* stream) {
+  if (n_tokens < 0) return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: n_tokens < 0");
+  if (k_offset < 0 || k_offset > DSA_INDEX_DIM - 64 || k_offset % 4)
+    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: k_offset must be a multiple of 4 in 0..64 (got %d)", k_offset);
+  if ((k_layout != DSA_ROPE_INTERLEAVED && k_layout != DSA_ROPE_HALF) ||
+      (kv_layout != DSA_ROPE_INTERLEAVED && kv_layout != DSA_ROPE_HALF))
+    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: unknown layout");
+  if (!std::isfinite(amplitude)) return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: amplitude must be finite");
+  if (n_tokens == 0) return DSA_OK;
+  if (!pos || !slot_mapping || !turns || (!k_bf16 && !kv_bf16) || (k_bf16 && !k_cache) || (kv_bf16 && !kv_cache))
+    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: null pointer");
+  if (!aligned(k_bf16, 8) || !aligned(kv_bf16, 8) || !aligned(k_cache, 16) || !aligned(kv_cache, 16) ||
+      !aligned(slot_mapping, 8) || !aligned(turns, 8) || !aligned(pos, 4))
+    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: rows must be 8-byte and caches 16-byte aligned");
+  const int64_t most = int64_t{1} << 40;
+  if ((k_bf16 && (k_stride < 0 || k_stride > most || k_stride % 4)) ||
+      (kv_bf16 && (kv_stride < 0 || kv_stride > most || kv_stride % 4)))
+    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: row strides must be multiples of 4 elements");
+  if (num_slots <= 0 || num_slots % DSA_PAGE_SIZE)
+    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: num_slots must be a positive multiple of 64");
+  unsigned* st = status_ptr();
+  if (!st) return fail(DSA_ERR_CUDA, "rope_quant_kv: no CUDA device");
+  dsa::RopeQuantArgs a{k_bf16, k_stride, kv_bf16, kv_stride, pos, slot_mapping, n_tokens, k_cache, kv_cache, num_slots,
+                       turns, amplitude, k_offset, k_layout, kv_layout, st};
+  cudaError_t e = dsa::launch_rope_quant(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "rope_quant_kv launch");
 }
 
 static int check_indexer(const char* who, const void* q_bf16, const float* w, int32_t n_q, int32_t h_i,

@@ -111,6 +111,38 @@ struct TopkMergeArgs {
   int32_t* out_local;           // [n_q][topk] or null: out_idx - local_lo inside the range, else -1
   unsigned* status;
 };
+struct RopeArgs {
+  const void* x;             // [n][h][d], element strides x_stride_t, x_stride_h, 1
+  void* out;                 // the same shape; == x: in place
+  int dtype;                 // DSA_DTYPE_*
+  int n, h, d;
+  int64_t x_stride_t, x_stride_h, out_stride_t, out_stride_h;
+  const int32_t* pos;        // [n]
+  const int64_t* turns;      // [rot / 2] 2^-64 turns per position
+  int rot, offset, layout;   // rotary part [offset, offset + rot), DSA_ROPE_*
+  float amplitude;
+  int transpose;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+
+struct RopeQuantArgs {
+  const void* k;             // bf16 [n][128], row stride k_stride, or null
+  int64_t k_stride;
+  const void* kv;            // bf16 [n][576], row stride kv_stride, or null
+  int64_t kv_stride;
+  const int32_t* pos;
+  const int64_t* slots;
+  int n_tokens;
+  uint8_t* k_cache;
+  uint8_t* kv_cache;
+  int64_t num_slots;
+  const int64_t* turns;      // [32]
+  float amplitude;
+  int k_offset, k_layout, kv_layout;
+  unsigned* status;
+};
+cudaError_t launch_rope_quant(const RopeQuantArgs& a, cudaStream_t s);
+
 int topk_merge_pow2(int n);
 cudaError_t launch_topk_merge(const TopkMergeArgs& a, cudaStream_t s);
 cudaError_t launch_lse_combine(const void* o_parts, const float* lse_parts, int n_parts, int n_q, int h, void* out,

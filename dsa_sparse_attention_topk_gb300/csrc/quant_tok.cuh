@@ -24,18 +24,15 @@ __device__ __forceinline__ KTok load_k_token(const __nv_bfloat16* __restrict__ k
   const int lane = threadIdx.x & 31;
   return KTok{*reinterpret_cast<const uint2*>(k + t * kIdxDim + 4 * lane), slots[t]};
 }
-__device__ __forceinline__ void store_k_token(const KTok& in, uint8_t* __restrict__ cache, int64_t num_slots,
-                                              unsigned* status) {
+// Store one token's key from its fp32 values (this lane's dims 4 lane ..).
+__device__ __forceinline__ void store_k_values(const float (&x)[4], int64_t slot, uint8_t* __restrict__ cache,
+                                               int64_t num_slots, unsigned* status) {
   const int lane = threadIdx.x & 31;
-  const int64_t slot = in.slot;
   if (slot < 0) return;
   if (slot >= num_slots) {
     if (lane == 0) flag(status, DSA_STATUS_BAD_PAGE);
     return;
   }
-  const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&in.raw.x);
-  const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&in.raw.y);
-  float x[4] = {__low2float(a), __high2float(a), __low2float(b), __high2float(b)};
   float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -50,6 +47,17 @@ __device__ __forceinline__ void store_k_token(const KTok& in, uint8_t* __restric
   const int row = static_cast<int>(slot % kPage);
   *reinterpret_cast<uint32_t*>(page + row * kIdxDim + 4 * lane) = codes;
   if ((lane & 7) == 0) page[kKScaleOff + row * 4 + (lane >> 3)] = static_cast<uint8_t>(e + 127);
+}
+// two packed bf16 values -> fp32 (exact)
+__device__ __forceinline__ float2 bf16x2_to_f32(uint32_t v) {
+  const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&v);
+  return make_float2(__low2float(b), __high2float(b));
+}
+__device__ __forceinline__ void store_k_token(const KTok& in, uint8_t* __restrict__ cache, int64_t num_slots,
+                                              unsigned* status) {
+  const float2 a = bf16x2_to_f32(in.raw.x), b = bf16x2_to_f32(in.raw.y);
+  const float x[4] = {a.x, a.y, b.x, b.y};
+  store_k_values(x, in.slot, cache, num_slots, status);
 }
 
 // |x| / s rounded to the nearest float and then nudged to "round to odd" when inexact:
@@ -84,10 +92,11 @@ __device__ __forceinline__ KvTok load_kv_token(const __nv_bfloat16* __restrict__
   in.slot = slots[t];
   return in;
 }
-__device__ __forceinline__ void store_kv_token(const KvTok& in, uint8_t* __restrict__ cache, int64_t num_slots,
-                                               unsigned* status) {
+// Store one token's latent row: the four full tiles as read, the rope tile from its fp32
+// values (this lane's dims 512 + 2 lane ..).
+__device__ __forceinline__ void store_kv_values(const uint2 (&raws)[4], float x0, float x1, int64_t slot,
+                                                uint8_t* __restrict__ cache, int64_t num_slots, unsigned* status) {
   const int lane = threadIdx.x & 31;
-  const int64_t slot = in.slot;
   if (slot < 0) return;
   if (slot >= num_slots) {
     if (lane == 0) flag(status, DSA_STATUS_BAD_PAGE);
@@ -97,10 +106,8 @@ __device__ __forceinline__ void store_kv_token(const KvTok& in, uint8_t* __restr
   float scales[kKvTiles];
 #pragma unroll
   for (int tile = 0; tile < 4; ++tile) {  // four full 128-wide tiles: 4 elements per lane
-    const uint2 raw = in.raws[tile];
-    const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&raw.x);
-    const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&raw.y);
-    float x[4] = {__low2float(a), __high2float(a), __low2float(b), __high2float(b)};
+    const float2 a = bf16x2_to_f32(raws[tile].x), b = bf16x2_to_f32(raws[tile].y);
+    const float x[4] = {a.x, a.y, b.x, b.y};
     float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -116,7 +123,6 @@ __device__ __forceinline__ void store_kv_token(const KvTok& in, uint8_t* __restr
     scales[tile] = s;
   }
   {  // the 64-wide rope tile: 2 elements per lane
-    float x0 = __low2float(in.rope), x1 = __high2float(in.rope);
     float amax = fmaxf(fabsf(x0), fabsf(x1));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -133,6 +139,10 @@ __device__ __forceinline__ void store_kv_token(const KvTok& in, uint8_t* __restr
   } else if (lane == 1) {
     *reinterpret_cast<uint4*>(rec + kKvScaleOff + 16) = make_uint4(__float_as_uint(scales[4]), 0u, 0u, 0u);
   }
+}
+__device__ __forceinline__ void store_kv_token(const KvTok& in, uint8_t* __restrict__ cache, int64_t num_slots,
+                                               unsigned* status) {
+  store_kv_values(in.raws, __low2float(in.rope), __high2float(in.rope), in.slot, cache, num_slots, status);
 }
 
 }  // namespace dsa

@@ -126,6 +126,66 @@ int dsa_quant_kv(const void* k_bf16, const void* kv_bf16, const int64_t* slot_ma
                  uint8_t* k_cache, uint8_t* kv_cache, int64_t num_slots, void* stream);
 
 /*
+ * Rotary positions.  The pages give the latent row as 512 "nope" + 64 "rope" dims and say
+ * nothing more; the rotation is the usual one.  A pair (a, b) of the rotary part with
+ * frequency f at position p becomes
+ *     amplitude * (a cos(p f) - b sin(p f),  a sin(p f) + b cos(p f)),
+ * pairs being neighbours (2i, 2i + 1) or half a rotary part apart (i, i + rot / 2).
+ * The frequencies come as `turns`: int64 round(f / (2 pi) * 2^64), wrapped to 64 bits, so
+ * that the product with a position is the angle modulo a turn in fixed point and far
+ * positions lose nothing.  Scaled tables for long contexts are other numbers in `turns`
+ * (and an amplitude other than 1).  Negative positions turn the other way.
+ */
+enum { DSA_ROPE_INTERLEAVED = 0, DSA_ROPE_HALF = 1 };
+enum { DSA_DTYPE_BF16 = 0, DSA_DTYPE_FP16 = 1, DSA_DTYPE_FP32 = 2 };
+
+/*
+ * dsa_rope -- turn part of every head of x by its token's position.
+ *   x, out     [n][h][d] of `dtype`; element (t, j, e) lies at t * stride_t + j * stride_h
+ *              + e elements.  out == x with the same strides works in place and touches only
+ *              the rotary part; otherwise out gets the whole heads (the rest copied) and must
+ *              not overlap x.  No two elements of out may share memory: its strides must
+ *              nest (stride_h >= d and stride_t >= (h - 1) stride_h + d, or the other way
+ *              round).  Strides of x may be 0 (broadcast) out of place.
+ *   pos        [n] int32.
+ *   turns      [rot / 2] int64, see above.
+ *   rot        rotary dims, even, 2..d; they are dims [offset, offset + rot) of a head.
+ *   layout     DSA_ROPE_INTERLEAVED or DSA_ROPE_HALF.
+ *   transpose  1: the transposed map (turns the other way, same amplitude): the gradient
+ *              of the rotation with respect to its input, given the output's.
+ * Computed in fp32 and rounded once to dtype.  16-byte loads and stores where x, out, their
+ * strides, offset and rot allow (d too, out of place); any alignment of whole elements works.
+ * n * h must be below 2^31.
+ */
+int dsa_rope(const void* x, void* out, int32_t dtype, int32_t n, int32_t h, int32_t d, int64_t x_stride_t,
+             int64_t x_stride_h, int64_t out_stride_t, int64_t out_stride_h, const int32_t* pos,
+             const int64_t* turns, int32_t rot, int32_t offset, int32_t layout, float amplitude,
+             int32_t transpose, void* stream);
+
+/*
+ * dsa_rope_quant_kv -- the cache writers with the rotation on the way: token i's key and
+ * latent row are turned to position pos[i] and stored as dsa_quant_kv stores them.  The
+ * turned values are quantised from fp32 (not rounded to bf16 in between); dims outside the
+ * rotary parts get exactly dsa_quant_kv's codes, and so do scales of groups without any.
+ *   k_bf16       nullable [n_tokens] rows of 128 bfloat16, k_stride elements apart; its
+ *                rotary part is dims [k_offset, k_offset + 64), k_offset a multiple of 4 in
+ *                0..64, in layout k_layout.
+ *   kv_bf16      nullable rows of 576 bfloat16, kv_stride elements apart; its rotary part is
+ *                dims [512, 576) in layout kv_layout.
+ *                Rows must be 8-byte aligned (strides multiples of 4).  At least one of the
+ *                two is given, each with its cache.
+ *   pos          [n_tokens] int32.
+ *   slot_mapping, k_cache, kv_cache, num_slots   as for dsa_quant_kv; a token with a negative
+ *                slot is skipped.  Slots must differ: which of two tokens of one call wins a
+ *                slot is not defined.
+ *   turns        [32] int64; amplitude as above.
+ */
+int dsa_rope_quant_kv(const void* k_bf16, int64_t k_stride, const void* kv_bf16, int64_t kv_stride,
+                      const int32_t* pos, const int64_t* slot_mapping, int32_t n_tokens, uint8_t* k_cache,
+                      uint8_t* kv_cache, int64_t num_slots, const int64_t* turns, float amplitude,
+                      int32_t k_offset, int32_t k_layout, int32_t kv_layout, void* stream);
+
+/*
  * dsa_indexer_topk -- fused Lightning Indexer + Top-K over the paged MXFP8 K-cache.
  * Follows "Deep Dive into Sparse Attention ..." section 2.1 (score, weighting and Top-K
  * fused in one kernel that reads the paged K-cache directly) and "Kimi K3.1 Pro Inference
