@@ -126,22 +126,32 @@ def _need(t, dtype, name):
 
 
 def _same_device(what, first, *others):
-    """Every tensor on the first one's CUDA device."""
-    if not first.is_cuda:
+    """Every tensor on the first one's CUDA device, which is returned."""
+    dev = first.device
+    if dev.type != "cuda":
         raise ValueError(f"{what}: tensors must be CUDA tensors")
     for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{what}: tensors must be on one device ({t.device} and {first.device})")
+        if t is not None and t.device != dev:
+            raise ValueError(f"{what}: tensors must be on one device ({t.device} and {dev})")
+    return dev
+
+
+def _need_shaped(t, dtype, shape, name):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
 
 
 def _call_on(device, stream, fn, *args):
-    """Call a C entry point with `device` current, on `stream` (that device's current one)."""
-    s = ctypes.c_void_p((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, s))
+    """Call a C entry point with `device` current, on `stream` (that device's current one).
+    Pointers come as plain integers: a step of small launches is bound by this host code."""
+    s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if device.index == torch._C._cuda_getDevice():
+        rc = fn(*args, s)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, s))
+            rc = fn(*args, s)
+    if rc:
+        _check(rc)
 
 
 # ---- cache allocation (plain torch allocations of the documented layouts) ----------
@@ -249,24 +259,23 @@ def rope(x, pos, turns, offset=0, layout="interleaved", amplitude=1.0, transpose
     or "half" (pairs i, i + rot / 2).  transpose=True gives the gradient with respect to x,
     given that of the result.  out=x works in place (only the rotary part is touched);
     otherwise out must not overlap x.  Returns out."""
-    if x.dim() not in (2, 3) or x.dtype not in _DTYPES:
+    shape, code = x.shape, _DTYPES.get(x.dtype)
+    if len(shape) not in (2, 3) or code is None:
         raise ValueError("rope: x must be [n, d] or [n, h, d] of bf16, fp16 or fp32")
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    elif out.shape != x.shape or out.dtype != x.dtype:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    elif out.shape != shape or out.dtype != x.dtype:
         raise ValueError("rope: out must have x's shape and dtype")
-    _same_device("rope", x, pos, turns, out)
-    _need(pos, torch.int32, "pos")
-    _need(turns, torch.int64, "turns")
-    n, d = x.shape[0], x.shape[-1]
-    if pos.shape != (n,) or turns.dim() != 1:
-        raise ValueError("rope: pos must be [n] and turns [rot / 2]")
-    if (x.stride(-1) != 1 or out.stride(-1) != 1) and d > 1:
+    dev = _same_device("rope", x, pos, turns, out)
+    _need_shaped(pos, torch.int32, shape[:1], "rope: pos")
+    _need_shaped(turns, torch.int64, turns.shape[:1], "rope: turns")
+    xs, os_ = x.stride(), out.stride()
+    if (xs[-1] != 1 or os_[-1] != 1) and shape[-1] > 1:
         raise ValueError("rope: the last dim of x and out must be contiguous")
-    h, xh, oh = (x.shape[1], x.stride(1), out.stride(1)) if x.dim() == 3 else (1, 0, 0)
-    _call_on(x.device, stream, lib().dsa_rope, _ptr(x), _ptr(out), _DTYPES[x.dtype], n, h, d, x.stride(0), xh,
-             out.stride(0), oh, _ptr(pos), _ptr(turns), 2 * turns.shape[0], offset, _layout(layout),
-             float(amplitude), int(bool(transpose)))
+    h, xh, oh = (shape[1], xs[1], os_[1]) if len(shape) == 3 else (1, 0, 0)
+    _call_on(dev, stream, lib().dsa_rope, x.data_ptr(), out.data_ptr(), code, shape[0], h, shape[-1], xs[0], xh,
+             os_[0], oh, pos.data_ptr(), turns.data_ptr(), 2 * turns.shape[0], offset, _layout(layout), amplitude,
+             1 if transpose else 0)
     return out
 
 
@@ -280,26 +289,29 @@ def rope_quant_kv(k, kv, pos, slot_mapping, k_cache, kv_cache, turns, amplitude=
     if k is None and kv is None:
         raise ValueError("rope_quant_kv: k or kv must be given")
     first = k if k is not None else kv
-    n = first.shape[0]
-    for t, cache, width, name in ((k, k_cache, INDEX_DIM, "k"), (kv, kv_cache, LATENT_DIM, "kv")):
+    rows = first.shape[:1]
+    pages = 1 << 48
+    for t, cache, width, page_bytes, name in ((k, k_cache, INDEX_DIM, KCACHE_PAGE_BYTES, "k"),
+                                              (kv, kv_cache, LATENT_DIM, PAGE_SIZE * KVCACHE_TOKEN_BYTES, "kv")):
         if (t is None) != (cache is None):
             raise ValueError(f"rope_quant_kv: {name} and {name}_cache go together")
         if t is None:
             continue
-        if t.dtype != torch.bfloat16 or t.shape != (n, width) or t.stride(1) != 1:
+        if t.dtype != torch.bfloat16 or t.shape != (*rows, width) or t.stride(1) != 1:
             raise ValueError(f"{name} must be bf16 [n, {width}] with contiguous rows")
-        _need(cache, torch.uint8, f"{name}_cache")
-    _same_device("rope_quant_kv", first, k, kv, pos, slot_mapping, k_cache, kv_cache, turns)
-    _need(pos, torch.int32, "pos")
-    _need(slot_mapping, torch.int64, "slot_mapping")
-    _need(turns, torch.int64, "turns")
-    if pos.shape != (n,) or slot_mapping.shape != (n,) or turns.shape != (32,):
-        raise ValueError("rope_quant_kv: pos and slot_mapping must be [n] and turns [32]")
-    pages = min(k_cache.numel() // KCACHE_PAGE_BYTES if k is not None else 1 << 48,
-                kv_cache.numel() // (PAGE_SIZE * KVCACHE_TOKEN_BYTES) if kv is not None else 1 << 48)
-    _call_on(first.device, stream, lib().dsa_rope_quant_kv, _ptr(k), 0 if k is None else k.stride(0), _ptr(kv),
-             0 if kv is None else kv.stride(0), _ptr(pos), _ptr(slot_mapping), n, _ptr(k_cache), _ptr(kv_cache),
-             pages * PAGE_SIZE, _ptr(turns), float(amplitude), k_offset, _layout(k_layout), _layout(kv_layout))
+        if cache.dtype != torch.uint8 or not cache.is_contiguous():
+            raise ValueError(f"{name}_cache must be a contiguous uint8 tensor")
+        pages = min(pages, cache.numel() // page_bytes)
+    dev = _same_device("rope_quant_kv", first, k, kv, pos, slot_mapping, k_cache, kv_cache, turns)
+    _need_shaped(pos, torch.int32, rows, "rope_quant_kv: pos")
+    _need_shaped(slot_mapping, torch.int64, rows, "rope_quant_kv: slot_mapping")
+    _need_shaped(turns, torch.int64, (32,), "rope_quant_kv: turns")
+    _call_on(dev, stream, lib().dsa_rope_quant_kv,
+             *((None, 0) if k is None else (k.data_ptr(), k.stride(0))),
+             *((None, 0) if kv is None else (kv.data_ptr(), kv.stride(0))),
+             pos.data_ptr(), slot_mapping.data_ptr(), rows[0], None if k is None else k_cache.data_ptr(),
+             None if kv is None else kv_cache.data_ptr(), pages * PAGE_SIZE, turns.data_ptr(), amplitude, k_offset,
+             _layout(k_layout), _layout(kv_layout))
 
 
 def indexer_topk(q, w, k_cache, page_table, seq_lens, q_seq, q_pos, topk, max_ctx,

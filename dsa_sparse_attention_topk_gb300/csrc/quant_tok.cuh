@@ -65,10 +65,12 @@ __device__ __forceinline__ void store_k_token(const KTok& in, uint8_t* __restric
 // rounded E4M3 value of the exact quotient (Boldo & Melquiond, "Emulation of FMA and
 // correctly rounded sums: proved algorithms using rounding to odd", 2008: rounding to
 // odd with p+2 or more bits followed by round-to-nearest is a correct rounding).
-__device__ __forceinline__ float quotient_round_to_odd(float x, float s) {
+// A value known as x + low (low at most half an ulp of x) gives the code of that sum.
+__device__ __forceinline__ float quotient_round_to_odd(float x, float s, float low = 0.f) {
   const float a = fabsf(x);
   const float q = __fdiv_rn(a, s);
-  const float r = __fmaf_rn(-q, s, a);  // exact remainder a - q*s
+  float r = __fmaf_rn(-q, s, a);  // exact remainder a - q*s
+  if (low != 0.f) r += x < 0.f ? -low : low;
   uint32_t qb = __float_as_uint(q);
   if (r != 0.f && (qb & 1u) == 0u) qb += (r > 0.f) ? 1u : 0xFFFFFFFFu;
   return copysignf(__uint_as_float(qb), x);
@@ -92,11 +94,10 @@ __device__ __forceinline__ KvTok load_kv_token(const __nv_bfloat16* __restrict__
   in.slot = slots[t];
   return in;
 }
-// Store one token's latent row: the four full tiles as read, the rope tile from its fp32
-// values (this lane's dims 512 + 2 lane ..).
-__device__ __forceinline__ void store_kv_values(const uint2 (&raws)[4], float x0, float x1, int64_t slot,
-                                                uint8_t* __restrict__ cache, int64_t num_slots, unsigned* status) {
+__device__ __forceinline__ void store_kv_token(const KvTok& in, uint8_t* __restrict__ cache, int64_t num_slots,
+                                               unsigned* status) {
   const int lane = threadIdx.x & 31;
+  const int64_t slot = in.slot;
   if (slot < 0) return;
   if (slot >= num_slots) {
     if (lane == 0) flag(status, DSA_STATUS_BAD_PAGE);
@@ -106,8 +107,10 @@ __device__ __forceinline__ void store_kv_values(const uint2 (&raws)[4], float x0
   float scales[kKvTiles];
 #pragma unroll
   for (int tile = 0; tile < 4; ++tile) {  // four full 128-wide tiles: 4 elements per lane
-    const float2 a = bf16x2_to_f32(raws[tile].x), b = bf16x2_to_f32(raws[tile].y);
-    const float x[4] = {a.x, a.y, b.x, b.y};
+    const uint2 raw = in.raws[tile];
+    const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&raw.x);
+    const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&raw.y);
+    float x[4] = {__low2float(a), __high2float(a), __low2float(b), __high2float(b)};
     float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -123,6 +126,7 @@ __device__ __forceinline__ void store_kv_values(const uint2 (&raws)[4], float x0
     scales[tile] = s;
   }
   {  // the 64-wide rope tile: 2 elements per lane
+    float x0 = __low2float(in.rope), x1 = __high2float(in.rope);
     float amax = fmaxf(fabsf(x0), fabsf(x1));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -139,10 +143,6 @@ __device__ __forceinline__ void store_kv_values(const uint2 (&raws)[4], float x0
   } else if (lane == 1) {
     *reinterpret_cast<uint4*>(rec + kKvScaleOff + 16) = make_uint4(__float_as_uint(scales[4]), 0u, 0u, 0u);
   }
-}
-__device__ __forceinline__ void store_kv_token(const KvTok& in, uint8_t* __restrict__ cache, int64_t num_slots,
-                                               unsigned* status) {
-  store_kv_values(in.raws, __low2float(in.rope), __high2float(in.rope), in.slot, cache, num_slots, status);
 }
 
 }  // namespace dsa

@@ -5,11 +5,16 @@
 // p becomes  amp * (a cos(p f) - b sin(p f),  a sin(p f) + b cos(p f)).
 //
 // The angle.  p f is taken modulo a whole turn in 64-bit fixed point: the table holds
-// f / 2 pi * 2^64, the integer product with p wraps exactly where the angle does, and its
-// top 32 bits are the phase as a signed fraction of a turn.  A far position costs no
-// accuracy (the phase is off by at most p * 2^-65 of a turn from the table's rounding and
-// 2^-32 from the cut, where p * f in fp32 is off by 2^-24 p f radians), and no double
-// arithmetic is needed; sincospif of the fraction is then within an ulp or two.
+// f / 2 pi * 2^64, and the integer product with p wraps exactly where the angle does, so a
+// far position costs no accuracy (p f in fp32 would be off by 2^-24 p f radians) and no
+// double arithmetic, which is slow on this GPU, is needed.
+//
+// Sine and cosine.  The phase is split into quarter turns and a rest of at most an eighth of
+// a turn; the rest becomes radians as an unevaluated sum hi + lo of two floats, and the
+// Taylor polynomials of sine and cosine (to degree 11 and 10: the first terms left out are
+// below 7e-12 and 1.2e-10) are summed so that each result is again hi + lo, good to about
+// 2^-27.  dsa_rope uses the sum rounded to fp32; the writers, whose results are cut to four
+// bits and must land on the right side of a border, keep the low parts.
 //
 // Both kernels are bound by memory: a rotation is 3 multiply-adds per pair.
 
@@ -22,15 +27,58 @@
 namespace dsa {
 namespace {
 
+// an unevaluated sum of two floats, |lo| at most half an ulp of hi
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum_ordered(float a, float b) {  // |a| >= |b| or a == 0
+  const float h = a + b;
+  return {h, (a - h) + b};
+}
+struct CosSin {
+  Two c, s;
+};
+
 // cos and sin (times the amplitude) of position p at a frequency of `turns` 2^-64 turns per
 // position
-__device__ __forceinline__ float2 phase_cs(int pos, int64_t turns, float amp) {
+__device__ __forceinline__ CosSin phase_cs(int pos, int64_t turns, float amp) {
   const uint64_t p = static_cast<uint64_t>(static_cast<int64_t>(pos)) * static_cast<uint64_t>(turns);
-  const float half_turns = static_cast<float>(static_cast<int32_t>(p >> 32)) * 4.656612873077393e-10f;  // 2^-31
-  float s, c;
-  sincospif(half_turns, &s, &c);
-  return make_float2(amp * c, amp * s);
+  const uint64_t near = p + (1ull << 61);  // + an eighth of a turn: the nearest quarter is the top two bits
+  const uint32_t quarter = static_cast<uint32_t>(near >> 62);
+  // the rest, in 2^-33 turns: |rest| <= 2^30
+  const int rest = static_cast<int>(static_cast<int64_t>(p - (static_cast<uint64_t>(quarter) << 62)) >> 31);
+  const float rh = static_cast<float>(rest);
+  const float rl = static_cast<float>(rest - static_cast<int>(rh));
+  constexpr double kRad = 6.283185307179586476925 / 8589934592.0;  // 2 pi 2^-33
+  constexpr float kHi = static_cast<float>(kRad);
+  constexpr float kLo = static_cast<float>(kRad - static_cast<double>(kHi));
+  const float x = rh * kHi;
+  const float xl = fmaf(rh, kHi, -x) + fmaf(rl, kHi, rh * kLo);
+  const float z = x * x;
+  // sin = x + (x^3 S(z) + xl cos x),  cos = 1 + (-z/2 + z^2 C(z) - rounding of z / 2 - x xl)
+  float S = -1.0f / 39916800.0f, C = -1.0f / 3628800.0f;
+  S = fmaf(S, z, 1.0f / 362880.0f);
+  S = fmaf(S, z, -1.0f / 5040.0f);
+  S = fmaf(S, z, 1.0f / 120.0f);
+  S = fmaf(S, z, -1.0f / 6.0f);
+  C = fmaf(C, z, 1.0f / 40320.0f);
+  C = fmaf(C, z, -1.0f / 720.0f);
+  C = fmaf(C, z, 1.0f / 24.0f);
+  const Two sn = two_sum_ordered(x, fmaf(x * z, S, fmaf(-0.5f * z, xl, xl)));
+  const float zl = fmaf(x, x, -z);
+  const Two cn = two_sum_ordered(1.0f, fmaf(z * z, C, -0.5f * z) - fmaf(x, xl, 0.5f * zl));
+  // a quarter turn: (c, s) -> (-s, c)
+  const bool swap = quarter & 1u;
+  Two c = swap ? sn : cn, s = swap ? cn : sn;
+  const float cf = ((quarter + 1u) & 2u) ? -amp : amp, sf = (quarter & 2u) ? -amp : amp;
+  CosSin r;
+  r.c.hi = c.hi * cf;
+  r.c.lo = fmaf(c.hi, cf, -r.c.hi) + c.lo * cf;
+  r.s.hi = s.hi * sf;
+  r.s.lo = fmaf(s.hi, sf, -r.s.hi) + s.lo * sf;
+  return r;
 }
+__device__ __forceinline__ float2 rounded(const CosSin& v) { return make_float2(v.c.hi + v.c.lo, v.s.hi + v.s.lo); }
 
 template <typename T> struct Elem;
 template <> struct Elem<__nv_bfloat16> {
@@ -106,7 +154,7 @@ rope_vec_kernel(RopeArgs a, RopeGeom g) {
         const int f0 = HALF ? e0 - a.offset : (e0 - a.offset) >> 1;
         const int pos = a.pos[t];
 #pragma unroll
-        for (int i = 0; i < P; ++i) cs[i] = phase_cs(pos, a.turns[f0 + i], a.amplitude);
+        for (int i = 0; i < P; ++i) cs[i] = rounded(phase_cs(pos, a.turns[f0 + i], a.amplitude));
         if (a.transpose) {
 #pragma unroll
           for (int i = 0; i < P; ++i) cs[i].y = -cs[i].y;
@@ -152,7 +200,7 @@ rope_pair_kernel(RopeArgs a, RopeGeom g, int half_layout) {
   const int half = a.rot >> 1;
   if (slot < half) {
     const int i0 = a.offset + (half_layout ? slot : 2 * slot), i1 = half_layout ? i0 + half : i0 + 1;
-    float2 cs = phase_cs(a.pos[t], a.turns[slot], a.amplitude);
+    float2 cs = rounded(phase_cs(a.pos[t], a.turns[slot], a.amplitude));
     if (a.transpose) cs.y = -cs.y;
     const float p = Elem<T>::get(src[i0]), q = Elem<T>::get(src[i1]);
     dst[i0] = Elem<T>::put(p * cs.x - q * cs.y);
@@ -199,63 +247,260 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
 // ---- the cache writers with the rotation on the way ---------------------------------
 // One warp per token, as in the plain writers: lane i computes the sine and cosine of
 // frequency i of the token's position, and the lanes that hold a pair's values fetch them
-// by shuffle.  The rotated values are quantised from fp32: they are never rounded to bf16.
+// by shuffle.  The turned values are quantised from hi + lo, never rounded to bf16 or to
+// fp32 in between: each code is the nearest of the turned value to about 2^-27.
 constexpr int kWarpsPerBlock = 8;
 constexpr int kRot = 64;
 
-// the k values of this lane (dims 4 lane ..) turned where they lie in [offset, offset + 64)
-__device__ __forceinline__ void turn_k(float (&x)[4], float2 cs, int offset, bool half_layout) {
+// a c + b s as hi + lo (a, b exact inputs)
+__device__ __forceinline__ Two dot2(float a, const Two& c, float b, const Two& s) {
+  const float p = a * c.hi, q = b * s.hi;
+  const float e = fmaf(a, c.hi, -p) + fmaf(b, s.hi, -q);   // the products' roundings
+  const float h = p + q, t = h - p;
+  const float f = (p - (h - t)) + (q - t);                 // the sum's rounding (Knuth's two-sum)
+  const float l = f + e + fmaf(a, c.lo, b * s.lo);
+  return two_sum_ordered(h, l);
+}
+__device__ __forceinline__ Two neg(const Two& v) { return {-v.hi, -v.lo}; }
+__device__ __forceinline__ Two shfl(const Two& v, int lane) {
+  return {__shfl_sync(0xffffffffu, v.hi, lane), __shfl_sync(0xffffffffu, v.lo, lane)};
+}
+
+// the k values of this lane (dims 4 lane ..) turned where they lie in [offset, offset + 64),
+// rounded to odd (see quotient_round_to_odd): their E4M3 codes and the exponent of the
+// largest are then those of the unrounded values
+__device__ __forceinline__ float to_odd(const Two& v) {
+  uint32_t b = __float_as_uint(v.hi);
+  if (v.lo != 0.f && (b & 1u) == 0u) b += ((v.lo > 0.f) == (v.hi > 0.f)) ? 1u : 0xFFFFFFFFu;
+  return __uint_as_float(b);
+}
+__device__ __forceinline__ void turn_k(float (&x)[4], const CosSin& cs, int offset, bool half_layout) {
   const int lane = threadIdx.x & 31;
   const int li = lane - (offset >> 2);  // 0..15 inside the rotary part
   const bool mine = li >= 0 && li < kRot / 4;
   if (half_layout) {
     const bool first = li < 8;
-    float other[4], c[4], s[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      other[j] = __shfl_sync(0xffffffffu, x[j], first ? lane + 8 : lane - 8);
-      c[j] = __shfl_sync(0xffffffffu, cs.x, 4 * (li & 7) + j);
-      s[j] = __shfl_sync(0xffffffffu, cs.y, 4 * (li & 7) + j);
-    }
-    if (mine) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = first ? x[j] * c[j] - other[j] * s[j] : other[j] * s[j] + x[j] * c[j];
+      const float other = __shfl_sync(0xffffffffu, x[j], first ? lane + 8 : lane - 8);
+      const Two c = shfl(cs.c, 4 * (li & 7) + j), s = shfl(cs.s, 4 * (li & 7) + j);
+      const float y = to_odd(dot2(x[j], c, other, first ? neg(s) : s));
+      // (the partner's shuffle of this j has read x[j] already)
+      if (mine) x[j] = y;
     }
   } else {
-    float c[2], s[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      c[j] = __shfl_sync(0xffffffffu, cs.x, 2 * li + j);
-      s[j] = __shfl_sync(0xffffffffu, cs.y, 2 * li + j);
-    }
-    if (mine) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float p = x[2 * j], q = x[2 * j + 1];
-        x[2 * j] = p * c[j] - q * s[j];
-        x[2 * j + 1] = p * s[j] + q * c[j];
+      const Two c = shfl(cs.c, 2 * li + j), s = shfl(cs.s, 2 * li + j);
+      const float p = x[2 * j], q = x[2 * j + 1];
+      const float y0 = to_odd(dot2(p, c, q, neg(s))), y1 = to_odd(dot2(q, c, p, s));
+      if (mine) {
+        x[2 * j] = y0;
+        x[2 * j + 1] = y1;
       }
     }
   }
 }
 
 // the rope tile's values of this lane (2 lane, 2 lane + 1 of 64), turned
-__device__ __forceinline__ void turn_kv(float& x0, float& x1, float2 cs, bool half_layout) {
+__device__ __forceinline__ void turn_kv(float x0, float x1, const CosSin& cs, bool half_layout, Two& y0, Two& y1) {
   const int lane = threadIdx.x & 31;
   if (half_layout) {
     const float o0 = __shfl_xor_sync(0xffffffffu, x0, 16), o1 = __shfl_xor_sync(0xffffffffu, x1, 16);
-    const float c0 = __shfl_sync(0xffffffffu, cs.x, 2 * lane), c1 = __shfl_sync(0xffffffffu, cs.x, 2 * lane + 1);
-    const float s0 = __shfl_sync(0xffffffffu, cs.y, 2 * lane), s1 = __shfl_sync(0xffffffffu, cs.y, 2 * lane + 1);
-    x0 = lane < 16 ? x0 * c0 - o0 * s0 : o0 * s0 + x0 * c0;
-    x1 = lane < 16 ? x1 * c1 - o1 * s1 : o1 * s1 + x1 * c1;
+    const Two c0 = shfl(cs.c, 2 * lane), c1 = shfl(cs.c, 2 * lane + 1);
+    const Two s0 = shfl(cs.s, 2 * lane), s1 = shfl(cs.s, 2 * lane + 1);
+    y0 = dot2(x0, c0, o0, lane < 16 ? neg(s0) : s0);
+    y1 = dot2(x1, c1, o1, lane < 16 ? neg(s1) : s1);
   } else {
-    const float p = x0, q = x1;
-    x0 = p * cs.x - q * cs.y;
-    x1 = p * cs.y + q * cs.x;
+    y0 = dot2(x0, cs.c, x1, neg(cs.s));
+    y1 = dot2(x1, cs.c, x0, cs.s);
   }
 }
 
-__global__ void __launch_bounds__(kWarpsPerBlock * 32)
+// largest of the warp's non-negative floats (a NaN is ignored, as fmaxf does)
+__device__ __forceinline__ float warp_amax(float v) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v, 0.f))));
+}
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  return static_cast<uint32_t>(f32x2_to_e4m3x2(a, b)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(c, d)) << 16);
+}
+
+// What the screened forms below allow for: 2^-22 of |a c| + |b s| covers the roundings of
+// the fp32 rotation (c, s, the products and the sum, half an ulp each).
+constexpr float kTurnErr = 2.384185791015625e-07f;
+
+// One token's key.  The fp32 rotation decides every code and exponent that is the same at
+// both ends of its error interval; a token with any other (one in some 10^4) is done again
+// from hi + lo.
+__device__ __forceinline__ void turn_store_k(uint2 raw, const CosSin& cs, const RopeQuantArgs& a, int64_t slot) {
+  const int lane = threadIdx.x & 31;
+  const float2 r0 = bf16x2_to_f32(raw.x), r1 = bf16x2_to_f32(raw.y);
+  float x[4] = {r0.x, r0.y, r1.x, r1.y};
+  const float2 cr = rounded(cs);
+  const int li = lane - (a.k_offset >> 2);
+  const bool mine = li >= 0 && li < kRot / 4;
+  float y[4], err[4];
+  if (a.k_layout == DSA_ROPE_HALF) {
+    const bool first = li < 8;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float other = __shfl_sync(0xffffffffu, x[j], first ? lane + 8 : lane - 8);
+      const float c = __shfl_sync(0xffffffffu, cr.x, 4 * (li & 7) + j);
+      const float s = __shfl_sync(0xffffffffu, cr.y, 4 * (li & 7) + j);
+      const float p = other * (first ? -s : s);
+      y[j] = fmaf(x[j], c, p);
+      err[j] = fmaf(fabsf(x[j]), fabsf(c), fabsf(p)) * kTurnErr;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float c = __shfl_sync(0xffffffffu, cr.x, 2 * li + j);
+      const float s = __shfl_sync(0xffffffffu, cr.y, 2 * li + j);
+      const float p = x[2 * j], q = x[2 * j + 1], u = q * -s, v = p * s;
+      y[2 * j] = fmaf(p, c, u);
+      y[2 * j + 1] = fmaf(q, c, v);
+      err[2 * j] = fmaf(fabsf(p), fabsf(c), fabsf(u)) * kTurnErr;
+      err[2 * j + 1] = fmaf(fabsf(q), fabsf(c), fabsf(v)) * kTurnErr;
+    }
+  }
+  if (!mine) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      y[j] = x[j];
+      err[j] = 0.f;
+    }
+  }
+  float amax = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
+  float emax = fmaxf(fmaxf(err[0], err[1]), fmaxf(err[2], err[3]));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    emax = fmaxf(emax, __shfl_xor_sync(0xffffffffu, emax, o));
+  }
+  const int e = mx_shared_exp(amax);
+  const float inv = exp2i(-e);
+  uint32_t lo[2], hi[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    lo[j] = f32x2_to_e4m3x2((y[2 * j] - err[2 * j]) * inv, (y[2 * j + 1] - err[2 * j + 1]) * inv);
+    hi[j] = f32x2_to_e4m3x2((y[2 * j] + err[2 * j]) * inv, (y[2 * j + 1] + err[2 * j + 1]) * inv);
+  }
+  const bool same = lo[0] == hi[0] && lo[1] == hi[1] && mx_shared_exp(amax - emax) == e &&
+                    mx_shared_exp(amax + emax) == e && amax > 0.f;
+  if (__any_sync(0xffffffffu, !same && emax > 0.f)) {  // (a group without rotary dims is exact as it is)
+    turn_k(x, cs, a.k_offset, a.k_layout == DSA_ROPE_HALF);
+    store_k_values(x, slot, a.k_cache, a.num_slots, a.status);
+    return;
+  }
+  uint8_t* page = a.k_cache + (slot / kPage) * kKPageBytes;
+  const int row = static_cast<int>(slot % kPage);
+  *reinterpret_cast<uint32_t*>(page + row * kIdxDim + 4 * lane) = amax > 0.f ? lo[0] | (lo[1] << 16) : 0u;
+  if ((lane & 7) == 0) page[kKScaleOff + row * 4 + (lane >> 3)] = static_cast<uint8_t>(e + 127);
+}
+
+// One token's latent row.
+//
+// The four unturned tiles.  Code = E4M3(x / s), s = fp32(amax / 448), x and amax of 8
+// significant bits.  Unless 448 x = B amax for a border B between two codes (of 5 bits or
+// fewer), the two sides are integers of at most 13 bits and differ by 2^-13 or more of
+// their size, so x times an approximate 1 / s decides.  If they are equal, x / s lies beside
+// B by as little as s's own rounding, on the side that the sign of amax - 448 s gives for
+// the whole tile: a reciprocal pushed that way by 2^-18 decides both cases with one
+// product per value.  Where s is exact (amax a multiple of 7, one tile in seven) the tie is a true
+// one, and the corrected quotient (exact where it is representable: Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990) leaves it to the
+// conversion.  Division instead of this took 60% of the writer's instructions.
+//
+// The rope tile goes like the key: the fp32 rotation decides where its error interval, widened
+// by the scale's, holds one code; else hi + lo does.
+//
+// Lane t works out tile t's scale and reciprocal, so that the five cost one division.
+__device__ __forceinline__ void turn_store_kv(const uint2 (&raws)[4], uint32_t rope, const CosSin& cs,
+                                              const RopeQuantArgs& a, int64_t slot) {
+  const int lane = threadIdx.x & 31;
+  uint8_t* rec = a.kv_cache + slot * kKvTokBytes;
+  const bool half_layout = a.kv_layout == DSA_ROPE_HALF;
+  const float2 x = bf16x2_to_f32(rope);
+  float y0, y1, err0, err1;
+  {
+    const float2 cr = rounded(cs);
+    if (half_layout) {
+      const float o0 = __shfl_xor_sync(0xffffffffu, x.x, 16), o1 = __shfl_xor_sync(0xffffffffu, x.y, 16);
+      const float c0 = __shfl_sync(0xffffffffu, cr.x, 2 * lane), c1 = __shfl_sync(0xffffffffu, cr.x, 2 * lane + 1);
+      const float s0 = __shfl_sync(0xffffffffu, cr.y, 2 * lane), s1 = __shfl_sync(0xffffffffu, cr.y, 2 * lane + 1);
+      const float p0 = o0 * (lane < 16 ? -s0 : s0), p1 = o1 * (lane < 16 ? -s1 : s1);
+      y0 = fmaf(x.x, c0, p0);
+      y1 = fmaf(x.y, c1, p1);
+      err0 = fmaf(fabsf(x.x), fabsf(c0), fabsf(p0)) * kTurnErr;
+      err1 = fmaf(fabsf(x.y), fabsf(c1), fabsf(p1)) * kTurnErr;
+    } else {
+      const float p0 = -x.y * cr.y, p1 = x.x * cr.y;
+      y0 = fmaf(x.x, cr.x, p0);
+      y1 = fmaf(x.y, cr.x, p1);
+      err0 = fmaf(fabsf(x.x), fabsf(cr.x), fabsf(p0)) * kTurnErr;
+      err1 = fmaf(fabsf(x.y), fabsf(cr.x), fabsf(p1)) * kTurnErr;
+    }
+  }
+  float amax = warp_amax(fmaxf(fabsf(y0), fabsf(y1)));  // lane t: tile t's from here on
+#pragma unroll
+  for (int tile = 0; tile < 4; ++tile) {
+    const __nv_bfloat162 m = __hmax2(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&raws[tile].x)),
+                                     __habs2(*reinterpret_cast<const __nv_bfloat162*>(&raws[tile].y)));
+    const float v = warp_amax(fmaxf(__low2float(m), __high2float(m)));
+    if (lane == tile) amax = v;
+  }
+  float s = __fdiv_rn(amax, 448.0f);
+  const bool usable = s > 1e-30f && s < 1e30f;  // 1 / s and s itself are far from the range's ends
+  const float rem = fmaf(-448.0f, s, amax);
+  float inv = usable ? __fdividef(1.0f, s) : 0.f;
+  if (lane < 4 && rem != 0.f) inv = fmaf(inv, copysignf(3.814697265625e-06f, rem), inv);  // 2^-18
+  const uint32_t exact = __ballot_sync(0xffffffffu, rem == 0.f);
+  const uint32_t fast = __ballot_sync(0xffffffffu, usable);
+#pragma unroll
+  for (int tile = 0; tile < 4; ++tile) {
+    const float2 p = bf16x2_to_f32(raws[tile].x), q = bf16x2_to_f32(raws[tile].y);
+    const float ti = __shfl_sync(0xffffffffu, inv, tile);
+    float v[4] = {p.x * ti, p.y * ti, q.x * ti, q.y * ti};
+    if (!((fast >> tile) & 1u) || ((exact >> tile) & 1u)) {
+      const float ts = __shfl_sync(0xffffffffu, s, tile);
+      const float xs[4] = {p.x, p.y, q.x, q.y};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = (fast >> tile) & 1u ? fmaf(fmaf(-v[i], ts, xs[i]), ti, v[i])
+                                   : ts > 0.f ? quotient_round_to_odd(xs[i], ts) : 0.f;
+    }
+    *reinterpret_cast<uint32_t*>(rec + tile * 128 + 4 * lane) = codes4(v[0], v[1], v[2], v[3]);
+  }
+  {
+    float rs = __shfl_sync(0xffffffffu, s, 4);
+    const float ri = __shfl_sync(0xffffffffu, inv, 4);
+    // (2^-20 of the value: the scale's and the reciprocal's own errors)
+    const float d0 = fmaf(fabsf(y0), 4.0f * kTurnErr, err0), d1 = fmaf(fabsf(y1), 4.0f * kTurnErr, err1);
+    uint16_t codes = f32x2_to_e4m3x2((y0 - d0) * ri, (y1 - d1) * ri);
+    const bool same = codes == f32x2_to_e4m3x2((y0 + d0) * ri, (y1 + d1) * ri);
+    if (!((fast >> 4) & 1u) || __any_sync(0xffffffffu, !same)) {
+      Two t0, t1;
+      turn_kv(x.x, x.y, cs, half_layout, t0, t1);
+      const float top = warp_amax(fmaxf(fabsf(t0.hi), fabsf(t1.hi)));
+      // the low part that goes with the largest: the scale is (top + low) / 448 rounded once
+      float low = -INFINITY;
+      if (fabsf(t0.hi) == top) low = t0.hi < 0.f ? -t0.lo : t0.lo;
+      if (fabsf(t1.hi) == top) low = fmaxf(low, t1.hi < 0.f ? -t1.lo : t1.lo);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) low = fmaxf(low, __shfl_xor_sync(0xffffffffu, low, o));
+      rs = __fdiv_rn(top, 448.0f);
+      const float rest = fmaf(-448.0f, rs, top) + low;
+      if (fabsf(rest) < top) rs += rest * (1.0f / 448.0f);  // (not where either is 0, infinite or NaN)
+      codes = rs > 0.f ? f32x2_to_e4m3x2(quotient_round_to_odd(t0.hi, rs, t0.lo),
+                                         quotient_round_to_odd(t1.hi, rs, t1.lo)) : 0;
+      if (lane == 4) s = rs;
+    }
+    *reinterpret_cast<uint16_t*>(rec + 512 + 2 * lane) = codes;
+  }
+  if (lane < 8) *reinterpret_cast<float*>(rec + kKvScaleOff + 4 * lane) = lane < 5 ? s : 0.f;
+}
+
+__global__ void __launch_bounds__(kWarpsPerBlock * 32, 4)
 rope_quant_kernel(RopeQuantArgs a) {
   pdl_launch_dependents();
   pdl_wait();
@@ -264,28 +509,22 @@ rope_quant_kernel(RopeQuantArgs a) {
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarpsPerBlock + (threadIdx.x >> 5); t < a.n_tokens;
        t += static_cast<int64_t>(gridDim.x) * kWarpsPerBlock) {
     const int64_t slot = a.slots[t];
-    if (slot < 0) continue;
-    uint2 kraw = make_uint2(0u, 0u), raws[4];
-    uint32_t rope = 0;
-    if (a.k) kraw = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.k) + t * a.k_stride + 4 * lane);
+    const int pos = a.pos[t];
+    uint2 k, kv[4];
+    uint32_t rope;
+    if (a.k) k = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.k) + t * a.k_stride + 4 * lane);
     if (a.kv) {
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.kv) + t * a.kv_stride;
 #pragma unroll
-      for (int tile = 0; tile < 4; ++tile) raws[tile] = *reinterpret_cast<const uint2*>(src + tile * 128 + 4 * lane);
+      for (int tile = 0; tile < 4; ++tile) kv[tile] = *reinterpret_cast<const uint2*>(src + tile * 128 + 4 * lane);
       rope = *reinterpret_cast<const uint32_t*>(src + 512 + 2 * lane);
     }
-    const float2 cs = phase_cs(a.pos[t], turns, a.amplitude);
-    if (a.k) {
-      const float2 p = bf16x2_to_f32(kraw.x), q = bf16x2_to_f32(kraw.y);
-      float x[4] = {p.x, p.y, q.x, q.y};
-      turn_k(x, cs, a.k_offset, a.k_layout == DSA_ROPE_HALF);
-      store_k_values(x, slot, a.k_cache, a.num_slots, a.status);
-    }
-    if (a.kv) {
-      const float2 p = bf16x2_to_f32(rope);
-      float x0 = p.x, x1 = p.y;
-      turn_kv(x0, x1, cs, a.kv_layout == DSA_ROPE_HALF);
-      store_kv_values(raws, x0, x1, slot, a.kv_cache, a.num_slots, a.status);
+    if (slot >= a.num_slots) {
+      if (lane == 0) flag(a.status, DSA_STATUS_BAD_PAGE);
+    } else if (slot >= 0) {
+      const CosSin cs = phase_cs(pos, turns, a.amplitude);
+      if (a.k) turn_store_k(k, cs, a, slot);
+      if (a.kv) turn_store_kv(kv, rope, cs, a, slot);
     }
   }
 }
