@@ -17,6 +17,7 @@ Functions (same names as the C entry points, without the ``dsa_`` prefix):
 * ``indexer_topk(...)``                          -- fused Lightning Indexer + Top-K
 * ``indexer_scores(...)``                        -- the same scores written in full
 * ``sparse_attn(...)``                           -- Sparse Flash Attention
+* ``prefix_attn(...)``                           -- dense attention of a batch that shares a prefix
 * ``rope_turns(rot, ...)``                       -- the frequency table the two rotary calls
   take, plain or scaled for long contexts (host arithmetic)
 * ``device_status()``                            -- read and clear the device status word
@@ -79,6 +80,9 @@ _SIGS = {
                                 _F32, _I32, _P]),
     "dsa_rope_quant_kv": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _I32, _P, _P, _I64, _P, _F32, _I32, _I32, _I32,
                                          _P]),
+    "dsa_prefix_attn_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
+    "dsa_prefix_attn": (ctypes.c_int, [_P, _I32, _I32, _P, _I64, _P, _I32, _P, _I32, _P, _I32, _P, _P, _I32, _F32, _P,
+                                       _P, _P, _SZ, _P]),
     "dsa_device_status": (ctypes.c_int, [_P]),
     "dsa_test_stall_indexer": (ctypes.c_int, [_I32]),
     "dsa_topk_merge": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P]),
@@ -413,6 +417,61 @@ def sparse_attn_noalloc(q, kv_cache, page_table, seq_lens, q_seq, topk_idx, sm_s
                                          page_table.shape[1], _ptr(seq_lens), _ptr(q_seq), seq_lens.shape[0],
                                          _ptr(topk_idx), topk, float(sm_scale), _ptr(out), _ptr(out_lse),
                                          _stream(stream)))
+    return out, out_lse
+
+
+def prefix_attn_workspace_size(n_q, h_s, n_seq, prefix_len, max_ctx):
+    return int(lib().dsa_prefix_attn_workspace_size(n_q, h_s, n_seq, prefix_len, max_ctx))
+
+
+def prefix_attn(q, kv_cache, prefix_pages, prefix_len, page_table, seq_lens, q_seq, q_pos, max_ctx, sm_scale,
+                out=None, out_lse=None, workspace=None, stream=None):
+    """Dense attention of query rows whose sequences share their first prefix_len positions,
+    read once for all from prefix_pages (int32 [ceil(prefix_len / 64)]); each row then sees
+    its own sequence's positions up to q_pos.  q: bf16 [n_q, h_s, 576]; page_table: int32
+    [n_seq, max_pages] (entries before prefix_len / 64 are not read); seq_lens: int32 [n_seq],
+    prefix included; q_seq, q_pos: int32 [n_q]; max_ctx: host-side bound of seq_lens.
+    Returns (out bf16 [n_q, h_s, 512], out_lse or None)."""
+    if q.dim() != 3 or q.shape[2] != LATENT_DIM:
+        raise ValueError("prefix_attn: q must be [n_q, h_s, 576]")
+    n_q, h_s, _ = q.shape
+    n_seq = seq_lens.shape[0]
+    dev = _same_device("prefix_attn", q, kv_cache, prefix_pages, page_table, seq_lens, q_seq, q_pos, out, out_lse,
+                       workspace)
+    _need_shaped(q, torch.bfloat16, q.shape, "prefix_attn: q")
+    _need_shaped(kv_cache, torch.uint8, kv_cache.shape, "prefix_attn: kv_cache")
+    _need_shaped(seq_lens, torch.int32, (n_seq,), "prefix_attn: seq_lens")
+    _need_shaped(q_seq, torch.int32, (n_q,), "prefix_attn: q_seq")
+    _need_shaped(q_pos, torch.int32, (n_q,), "prefix_attn: q_pos")
+    if prefix_pages is not None:
+        _need_shaped(prefix_pages, torch.int32, prefix_pages.shape, "prefix_attn: prefix_pages")
+    if prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() < (prefix_len + PAGE_SIZE - 1) // PAGE_SIZE):
+        raise ValueError("prefix_attn: prefix_pages must name ceil(prefix_len / 64) pages")
+    max_pages = 0
+    if page_table is not None:
+        max_pages = page_table.shape[-1]
+        _need_shaped(page_table, torch.int32, (n_seq, max_pages), "prefix_attn: page_table")
+    if out is None:
+        out = torch.empty(n_q, h_s, V_DIM, dtype=torch.bfloat16, device=dev)
+    else:
+        _need_shaped(out, torch.bfloat16, (n_q, h_s, V_DIM), "prefix_attn: out")
+    if out_lse is not None:
+        _need_shaped(out_lse, torch.float32, (n_q, h_s), "prefix_attn: out_lse")
+    if workspace is None:
+        # (the plan goes by the device's multiprocessors: ask with that device current)
+        size = lib().dsa_prefix_attn_workspace_size
+        if dev.index == torch._C._cuda_getDevice():
+            need = size(n_q, h_s, n_seq, prefix_len, max_ctx)
+        else:
+            with torch.cuda.device(dev):
+                need = size(n_q, h_s, n_seq, prefix_len, max_ctx)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call_on(dev, stream, lib().dsa_prefix_attn, q.data_ptr(), n_q, h_s, kv_cache.data_ptr(),
+             kv_cache.numel() // (PAGE_SIZE * KVCACHE_TOKEN_BYTES),
+             None if prefix_pages is None else prefix_pages.data_ptr(), prefix_len,
+             None if page_table is None else page_table.data_ptr(), max_pages, seq_lens.data_ptr(), n_seq,
+             q_seq.data_ptr(), q_pos.data_ptr(), max_ctx, sm_scale, out.data_ptr(),
+             None if out_lse is None else out_lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out, out_lse
 
 

@@ -422,6 +422,52 @@ int dsa_sparse_attn_noalloc(const void* q_bf16, int32_t n_q, int32_t h_s, const 
   return DSA_OK;
 }
 
+static bool prefix_sizes_ok(int32_t n_q, int32_t h_s, int32_t n_seq, int32_t prefix_len, int32_t max_ctx) {
+  return n_q > 0 && h_s >= 1 && h_s <= 128 && n_seq >= 1 && max_ctx >= 1 && max_ctx <= 1048576 && prefix_len >= 0 &&
+         prefix_len <= max_ctx;
+}
+
+size_t dsa_prefix_attn_workspace_size(int32_t n_q, int32_t h_s, int32_t n_seq, int32_t prefix_len, int32_t max_ctx) {
+  if (!prefix_sizes_ok(n_q, h_s, n_seq, prefix_len, max_ctx)) return 0;
+  return dsa::prefix_workspace_bytes(n_q, h_s, n_seq, prefix_len, max_ctx);
+}
+
+int dsa_prefix_attn(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t* kv_cache, int64_t num_pages,
+                    const int32_t* prefix_pages, int32_t prefix_len, const int32_t* page_table, int32_t max_pages,
+                    const int32_t* seq_lens, int32_t n_seq, const int32_t* q_seq, const int32_t* q_pos,
+                    int32_t max_ctx, float sm_scale, void* out_bf16, float* out_lse, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (n_q < 0 || n_seq < 0) return fail(DSA_ERR_INVALID_ARG, "prefix_attn: negative n_q or n_seq");
+  if (h_s < 1 || h_s > 128) return fail(DSA_ERR_UNSUPPORTED, "prefix_attn: h_s must be 1..128 (got %d)", h_s);
+  if (max_ctx < 1 || max_ctx > 1048576) return fail(DSA_ERR_UNSUPPORTED, "prefix_attn: max_ctx must be 1..1048576");
+  if (prefix_len < 0 || prefix_len > max_ctx)
+    return fail(DSA_ERR_INVALID_ARG, "prefix_attn: prefix_len must lie in 0..max_ctx");
+  if (num_pages < 1) return fail(DSA_ERR_INVALID_ARG, "prefix_attn: num_pages must be >= 1");
+  if (!(sm_scale > 0.f) || !std::isfinite(sm_scale))
+    return fail(DSA_ERR_INVALID_ARG, "prefix_attn: sm_scale must be positive and finite");
+  if (n_q == 0) return DSA_OK;
+  if (n_seq == 0) return fail(DSA_ERR_INVALID_ARG, "prefix_attn: query rows without sequences");
+  const bool tails = max_ctx > prefix_len;
+  if (tails && max_pages < (max_ctx + DSA_PAGE_SIZE - 1) / DSA_PAGE_SIZE)
+    return fail(DSA_ERR_INVALID_ARG, "prefix_attn: max_pages < ceil(max_ctx / 64)");
+  if (!q_bf16 || !kv_cache || !seq_lens || !q_seq || !q_pos || !out_bf16 || (prefix_len && !prefix_pages) ||
+      (tails && !page_table) || !workspace)
+    return fail(DSA_ERR_INVALID_ARG, "prefix_attn: null pointer");
+  if (!aligned(q_bf16, 16) || !aligned(kv_cache, 16) || !aligned(out_bf16, 16))
+    return fail(DSA_ERR_INVALID_ARG, "prefix_attn: q, kv_cache and out must be 16-byte aligned");
+  const size_t need = dsa::prefix_workspace_bytes(n_q, h_s, n_seq, prefix_len, max_ctx);
+  if (workspace_bytes < need || !aligned(workspace, 256))
+    return fail(DSA_ERR_INVALID_ARG, "prefix_attn: workspace must be >= %zu bytes and 256-byte aligned", need);
+  unsigned* st = status_ptr();
+  if (!st) return fail(DSA_ERR_CUDA, "prefix_attn: no CUDA device");
+  dsa::PrefixArgs a{q_bf16, n_q, h_s, kv_cache, num_pages, prefix_pages, prefix_len, page_table, max_pages, seq_lens,
+                    n_seq, q_seq, q_pos, max_ctx, sm_scale, out_bf16, out_lse, workspace, st};
+  const char* why = nullptr;
+  cudaError_t e = dsa::launch_prefix_attn(a, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return why ? fail(DSA_ERR_UNSUPPORTED, "%s", why) : cuda_fail(e, "prefix_attn launch");
+  return DSA_OK;
+}
+
 int dsa_topk_merge(const int32_t* cand_idx, const float* cand_scores, const int32_t* part_offsets, int32_t n_parts,
                    int32_t n_q, int32_t k_in, int32_t topk, int32_t* out_idx, float* out_scores,
                    const int32_t* local_lo, const int32_t* local_hi, int32_t* out_local, void* stream) {

@@ -143,6 +143,29 @@ struct RopeQuantArgs {
 };
 cudaError_t launch_rope_quant(const RopeQuantArgs& a, cudaStream_t s);
 
+struct PrefixArgs {
+  const void* q;              // bf16 [n_q][h_s][576]
+  int n_q, h_s;
+  const uint8_t* kv_cache;
+  int64_t num_pages;
+  const int32_t* prefix_pages;  // [ceil(prefix_len / 64)]
+  int prefix_len;
+  const int32_t* page_table;  // [n_seq][max_pages]
+  int max_pages;
+  const int32_t* seq_lens;
+  int n_seq;
+  const int32_t* q_seq;
+  const int32_t* q_pos;
+  int max_ctx;
+  float sm_scale;
+  void* out;                  // bf16 [n_q][h_s][512]
+  float* out_lse;             // [n_q][h_s] or null
+  void* workspace;
+  unsigned* status;
+};
+cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char** err);
+size_t prefix_workspace_bytes(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx);
+
 int topk_merge_pow2(int n);
 cudaError_t launch_topk_merge(const TopkMergeArgs& a, cudaStream_t s);
 cudaError_t launch_lse_combine(const void* o_parts, const float* lse_parts, int n_parts, int n_q, int h, void* out,

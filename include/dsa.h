@@ -323,6 +323,47 @@ int dsa_sparse_attn_noalloc(const void* q_bf16, int32_t n_q, int32_t h_s, const 
                             float* out_lse, void* stream);
 
 /*
+ * dsa_prefix_attn -- dense attention of query rows whose sequences share a prefix, over the
+ * FP8 latent cache.  The pages describe the sparse path alone; this is the dense absorbed-MLA
+ * attention under it, for a batch behind one long system prompt or document.
+ * Row t of sequence b = q_seq[t] sees the positions p < min(q_pos[t] + 1, seq_lens[b]).  Those
+ * below prefix_len are read from the shared pages, once for all rows; the others (the row's
+ * tail) from the sequence's own page-table row:
+ *     l_p = sm_scale * q[t, h] . kv[p];  o[t, h] = sum_p softmax(l)_p kv[p][0:512]
+ *     lse[t, h] = log sum_p exp(l_p)
+ * A row that sees nothing gets o = 0 and lse = -inf.  Dequantised values and softmax weights
+ * are rounded to bf16 for the tensor cores, sums kept in fp32.
+ *   q_bf16        [n_q][h_s][576] bfloat16, 16-byte aligned; h_s 1..128.
+ *   kv_cache      the FP8 latent cache (layout above), num_pages pages, 16-byte aligned.
+ *   prefix_pages  [ceil(prefix_len / 64)] int32 physical pages of the shared positions (the
+ *                 last one may be partial; it need not be the page that the sequences' own
+ *                 rows name for it).  May be NULL when prefix_len is 0.
+ *   prefix_len    0..max_ctx, the same for every sequence (a host value).
+ *   page_table    [n_seq][max_pages] int32 pages by logical position, as for
+ *                 dsa_indexer_topk; only entries from prefix_len / 64 on are read.  May be
+ *                 NULL when max_ctx equals prefix_len.
+ *   seq_lens      [n_seq] int32, each in [0, max_ctx] (prefix included; one below prefix_len
+ *                 sees that much of the prefix).
+ *   q_seq, q_pos  [n_q] int32.  Rows of one sequence may come in any number and order.
+ *   max_ctx       host-side upper bound of seq_lens, 1..1048576.
+ *   out_bf16      [n_q][h_s][512] bfloat16, 16-byte aligned.
+ *   out_lse       nullable [n_q][h_s] fp32.
+ *   workspace     device scratch of at least dsa_prefix_attn_workspace_size bytes for the same
+ *                 sizes, 256-byte aligned: the expanded rows (1152 bytes a position of the
+ *                 prefix and of n_seq tails of max_ctx - prefix_len) and the splits' partial
+ *                 results.  Nothing in it outlives the call.
+ * A position whose page is out of range is not seen and flags DSA_STATUS_BAD_PAGE; a row whose
+ * sequence or length is out of range sees nothing and flags DSA_STATUS_BAD_SEQ or _BAD_LEN.
+ * A cached position with NaN or infinite values makes the rows that see it NaN, and no others.
+ */
+size_t dsa_prefix_attn_workspace_size(int32_t n_q, int32_t h_s, int32_t n_seq, int32_t prefix_len, int32_t max_ctx);
+int dsa_prefix_attn(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t* kv_cache, int64_t num_pages,
+                    const int32_t* prefix_pages, int32_t prefix_len, const int32_t* page_table, int32_t max_pages,
+                    const int32_t* seq_lens, int32_t n_seq, const int32_t* q_seq, const int32_t* q_pos,
+                    int32_t max_ctx, float sm_scale, void* out_bf16, float* out_lse, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
  * dsa_device_status -- synchronise `stream`, return the device status word (an OR of
  * DSA_STATUS_* bits recorded by kernels since the last call on this device) and clear
  * it.  Returns a negative DSA_ERR_CUDA if the synchronisation itself failed.
