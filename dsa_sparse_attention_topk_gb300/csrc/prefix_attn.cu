@@ -10,12 +10,14 @@
 // bound by the tensor cores.
 //
 // Three kernels.
-//   expand   dequantises the prefix once for all rows, and each tail once, into bf16 rows in
-//            the workspace (the same rounding the sparse attention makes), so that the main
-//            kernel can feed its MMAs by TMA alone.  A position whose page is out of range
-//            becomes a zero row that a bit marks invalid; one with NaN or infinite
-//            values a zero row marked poisonous, whose logit is NaN for the rows that see it
-//            and nothing to the others.
+//   expand   dequantises the prefix once for all rows, and each tail once, into fp16 rows in
+//            the workspace, so that the main kernel can feed its MMAs by TMA alone.  A tile of 64
+//            positions shares one power of two, taken from its largest scale, which keeps fp16's
+//            11 bits for everything within 2^-29 of the tile's largest value; bf16 operands
+//            would cost three more bits, in the logits above all.  A position whose page
+//            is out of range becomes a zero row that a bit marks invalid; one with NaN or
+//            infinite values a zero row marked poisonous, whose logit is NaN for the rows
+//            that see it and nothing to the others.
 //   attend   one CTA pair per item: 128 rows of (query row, head) against a run of 64-position
 //            tiles of the prefix (a tile of the flattened rows, shared by all sequences) or of
 //            one query row's tail.
@@ -24,22 +26,29 @@
 // The pair.  The output accumulator of 128 rows x 512 columns would fill tensor memory, so
 // each CTA of the pair holds one half of the value columns.  Computing the logits in both
 // would cost half as much again; instead CTA c computes logits and weights of the tiles
-// j = c (mod 2) and sends the weights (bf16, 16 KB) to its peer by a bulk copy into
-// distributed shared memory; both then run P V over every tile, each on its half.
+// j = c (mod 2) and sends the weights (fp16, 16 KB) to its peer by a bulk copy into
+// distributed shared memory; both then run P V over every tile, each on its half, in the
+// order own 0, peer 0, own 1, peer 1 ...
 //
-// The softmax reference.  Weights are 2^(x - r) with one fixed r per row, the row's
-// largest logit (in units of log 2) in the item's first tile.  A weight may then exceed 1:
-// fp32 and bf16 hold it up to 2^127 with unchanged relative precision, so nothing has to be
-// rescaled inside the loop and the two CTAs need no agreement per tile.  At the end the pair
-// compares each row's true maximum M with r, and if they lie further apart than 2^64 anywhere
-// it runs the item again with r = M.
+// The softmax reference.  With e the exponent of its tile, a position's weight is stored as
+// 2^(x + e - rho), x its logit in powers of two and rho the row's reference: the first tile's
+// largest x + e, which CTA 0 also sends to CTA 1.  Weights may exceed 1 (up to 2^14 before
+// fp16 runs out), so rho hardly ever changes; the sum of 2^(x - rho) is kept in fp32 from
+// the unrounded weights.  When a tile's largest weight would pass 2^14 its owner raises rho for
+// that row and rescales its accumulator; the references travel with the weights, and the
+// receiving CTA raises its own (rescaling its accumulator) or, where it has itself gone
+// ahead, scales the received row down.  After each tile in the order above both CTAs hold the
+// largest reference used so far, so the results do not depend on timing.
 //
-// Per CTA (9 warps): 0 loads the own tiles' blocks, 8 the peer tiles' value blocks, 1 issues
-// Q K^T, 2 issues P V, 3 sends the weights, 4-7 turn logits into weights (one row a thread).
+// Per CTA (12 warps): 0 loads the own tiles, 1 issues Q K^T, 2 issues P V, 3 sends the weights
+// and loads the peer tiles' value blocks, 4-11 turn logits into weights (a row's 64 positions
+// in two threads).  Descriptors and tensor-memory addresses are constants of the unrolled
+// issue loops: with addresses computed per MMA the issue took 110-200 cycles each.
 // Tensor memory (512 columns): O in 0..255, the logits in 256..319, the query's dims 0..383
-// as bf16 pairs in 320..511.  Shared memory: the query's dims 384..575, both weight buffers,
-// and 18 blocks of 64 positions x 64 dims: the value blocks of two own tiles (8), those of one
-// peer tile (4), and a ring of 6 for the own tile's other five blocks, which only Q K^T reads.
+// as fp16 pairs in 320..511.  Shared memory: the query's dims 384..575, both weight buffers
+// with their references, and 17 blocks of 64 positions x 64 dims: the value blocks of two own
+// tiles (8), those of one peer tile (4), and the own tile's other five, which only Q K^T reads.
+// The query is scaled to fp16 by a power of two per row (exact: bf16 has 8 bits).
 
 #include <algorithm>
 #include <cuda.h>
@@ -54,63 +63,72 @@ namespace {
 constexpr int kTile = 64;                     // positions per tile
 constexpr int kRows = 128;                    // (query row, head) rows per item
 constexpr int kHalfV = kVDim / 2;
-constexpr int kBlock = kTile * 128;           // 64 positions x 64 dims, bf16: 8 KB
+constexpr int kBlock = kTile * 128;           // 64 positions x 64 dims, fp16: 8 KB
 constexpr int kQBlock = kRows * 128;          // 128 rows x 64 dims: 16 KB
-constexpr int kQTmemSteps = 24;               // K-steps of 16 with the query in tensor memory
+constexpr int kQTmemBlocks = 6;               // 64-dim blocks with the query in tensor memory
 constexpr int kQSmemBlocks = 3;
-constexpr int kRing = 6, kLoose = 5;          // blocks only Q K^T reads: ring slots, per tile
-constexpr int kThreads = 32 * 9;
+constexpr int kLoose = 5;                     // blocks of a tile that only Q K^T reads
+constexpr int kThreads = 32 * 12;
+constexpr int kSoftWarps = 8;                 // warps 4..11
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 constexpr uint32_t kPBytes = kRows * 128;     // the weights of a tile
-constexpr float kRange = 64.0f;               // |M - r| a row may have, in powers of two
+constexpr uint32_t kPMsg = kPBytes + kRows * 4;  // with the rows' references
+constexpr uint32_t kPStride = (kPMsg + 1023) / 1024 * 1024;
+constexpr float kHeadroom = 14.0f;            // powers of two a weight may reach
 
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffPOwn = kOffQ + kQSmemBlocks * kQBlock;
-constexpr uint32_t kOffPIn = kOffPOwn + kPBytes;
-constexpr uint32_t kOffVOwn = kOffPIn + kPBytes;
+constexpr uint32_t kOffPIn = kOffPOwn + kPStride;
+constexpr uint32_t kOffVOwn = kOffPIn + kPStride;
 constexpr uint32_t kOffVPeer = kOffVOwn + 8 * kBlock;
-constexpr uint32_t kOffRing = kOffVPeer + 4 * kBlock;
-constexpr uint32_t kOffCtl = kOffRing + kRing * kBlock;
+constexpr uint32_t kOffLoose = kOffVPeer + 4 * kBlock;
+constexpr uint32_t kOffCtl = kOffLoose + kLoose * kBlock;
 
 struct PairCtl {
-  uint64_t q_full, q_tmem;
-  uint64_t ring_full[kRing], ring_empty[kRing];
-  uint64_t vown_full[2], vown_empty[2];
+  uint64_t q_ready;                            // the query is in tensor and shared memory
+  uint64_t loose_full[kLoose], loose_empty[kLoose];
+  uint64_t vown_full[2], vown_empty[2];        // full; read by the own P V
   uint64_t vpeer_full, vpeer_empty;
-  uint64_t s_full, s_free;   // logits written / read into registers
-  uint64_t p_full;           // own weights in shared memory
-  uint64_t p_empty;          // own weights read: by the own P V and by the peer's (its copy's)
-  uint64_t pin_full;         // the peer's weights have landed
+  uint64_t s_full, s_free;                     // logits written / read into registers
+  uint64_t p_full;                             // own weights in shared memory, O at their reference
+  uint64_t p_empty;                            // own weights read: by the own P V and by the peer's (of its copy)
+  uint64_t pin_full;                           // the peer's weights have landed
+  uint64_t pin_go;                             // they and O are at one reference
   uint64_t o_done;
-  uint64_t r_full;           // CTA 1: the references have landed
-  uint64_t fin_full;         // the peer's (max, sums) have landed
+  uint64_t r_full;                             // CTA 1: the first references have landed
+  uint64_t fin_full;                           // the peer's sums have landed
   uint32_t tmem_base;
   int abort;
-  int redo;
-  volatile uint32_t peer_vote[2];  // per attempt: 1: run again, 2: a wait ran out there
-  float r[kRows];            // CTA 1: from CTA 0
-  float2 fin2[kRows];        // the peer's max and sum of rounded weights
-  float fin1[kRows];         // the peer's sum of unrounded weights
+  float r[kRows];                              // CTA 1: from CTA 0
+  float fin[kRows];                            // the peer's sum of weights
+  float part[2][2][kRows];                     // tile maxima of a row's two threads, by tile parity
 };
-constexpr uint32_t kSmemBytes = kOffCtl + 3072;
-static_assert(sizeof(PairCtl) <= 3072 && kSmemBytes <= 232448, "shared memory");
+constexpr uint32_t kSmemBytes = kOffCtl + 4096;
+static_assert(sizeof(PairCtl) <= 4096 && kSmemBytes <= 232448, "shared memory");
 // the output rows are staged where the tiles' blocks were
 constexpr int kStagePitch = kHalfV * 2 + 16;
-static_assert(kRows * kStagePitch <= 18 * kBlock, "output staging");
+static_assert(kRows * kStagePitch <= 17 * kBlock, "output staging");
+
+// What expand writes per tile.
+struct alignas(32) TileInfo {
+  uint64_t valid, poison;    // a bit per position
+  int32_t e;                 // stored value = value * 2^-e
+  int32_t pad[3];
+};
 
 struct PrefixPlan {
   int tiles_p, tiles_t;      // tiles of the prefix, and of the longest possible tail
   int sp, st;                // splits of the prefix and of each tail
   int mt;                    // 128-row tiles of the flattened rows
   int64_t rows_kv;           // rows of the expanded cache
-  size_t off_words, off_o, off_ml, bytes;
+  size_t off_info, off_o, off_ml, bytes;
 };
 
 struct PrefixWs {
-  __nv_bfloat16* kv;         // [tiles_p * 64 + n_seq * tiles_t * 64][576]
-  uint64_t* words;           // [tiles][2]: valid, poisonous
-  __nv_bfloat16* o;          // [n_q * h_s][sp + st][512]
-  float4* ml;                // [n_q * h_s][sp + st]: reference, sum of rounded weights, of unrounded ones
+  __half* kv;                // [tiles_p * 64 + n_seq * tiles_t * 64][576]
+  TileInfo* info;            // [tiles]
+  __half* o;                 // [n_q * h_s][sp + st][512], times 2^-(its exponent)
+  float4* ml;                // [n_q * h_s][sp + st]: reference, sum, the outputs' exponent
 };
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -147,13 +165,18 @@ PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, i
   }
   p.rows_kv = static_cast<int64_t>(p.tiles_p) * kTile + static_cast<int64_t>(n_seq) * p.tiles_t * kTile;
   const size_t parts = p.sp + p.st > 1 ? static_cast<size_t>(n_q) * h_s * (p.sp + p.st) : 0;
-  p.off_words = round_up(static_cast<size_t>(p.rows_kv) * kLatent * 2, 256);
-  p.off_o = p.off_words + round_up(static_cast<size_t>(p.rows_kv / kTile) * 16, 256);
+  p.off_info = round_up(static_cast<size_t>(p.rows_kv) * kLatent * 2, 256);
+  p.off_o = p.off_info + round_up(static_cast<size_t>(p.rows_kv / kTile) * sizeof(TileInfo), 256);
   p.off_ml = p.off_o + parts * kVDim * 2;
   p.bytes = p.off_ml + round_up(parts * 16, 256);
   return p;
 }
 
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -184,9 +207,14 @@ __device__ __forceinline__ int row_limit(const PrefixArgs& a, int t, bool report
 // Bound by memory: 608 bytes read and 1152 written a position.
 constexpr int kExpandThreads = 288;
 constexpr int kChunks = kLatent / 16;  // 16-code chunks of a record
+__device__ __forceinline__ bool has_nan_code(uint32_t w) {  // a byte 0x7F or 0xFF
+  const uint32_t m = w & 0x7F7F7F7Fu;
+  return ((m + 0x01010101u) & 0x80808080u) != 0u;
+}
 __global__ void __launch_bounds__(kExpandThreads)
 expand_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
   __shared__ unsigned s_word[4];  // valid (2 words), poisonous (2 words)
+  __shared__ unsigned s_scale;    // the largest finite scale's bits
   pdl_launch_dependents();
   pdl_wait();
   const int tile = blockIdx.x;
@@ -206,6 +234,7 @@ expand_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
     pages = a.page_table + static_cast<int64_t>(b) * a.max_pages;
   }
   if (tid < 4) s_word[tid] = 0;
+  if (tid == 4) s_scale = 0;
   __syncthreads();
   constexpr int kPer = kTile * kChunks / kExpandThreads;  // 8
   static_assert(kTile * kChunks % kExpandThreads == 0, "chunks per thread");
@@ -228,66 +257,101 @@ expand_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
     scale[i] = *reinterpret_cast<const float*>(rec + kKvScaleOff + 4 * (c >> 3));
     if (c == 0) atomicOr(&s_word[tok >> 5], 1u << (tok & 31));
   }
-  uint4 lo[kPer], hi[kPer];
+  float top = 0.f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int tok = (i * kExpandThreads + tid) / kChunks;
-    const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-    uint32_t o[8];
-    bool bad = false;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float f[4];
-      e4m3x4_to_f32(w[q], f);
-      o[2 * q] = pack2(f[0] * scale[i], f[1] * scale[i]);
-      o[2 * q + 1] = pack2(f[2] * scale[i], f[3] * scale[i]);
+    const bool bad = !(fabsf(scale[i]) * 448.0f < INFINITY) || has_nan_code(code[i].x) || has_nan_code(code[i].y) ||
+                     has_nan_code(code[i].z) || has_nan_code(code[i].w);
+    if (bad) {
+      atomicOr(&s_word[2 + (tok >> 5)], 1u << (tok & 31));
+      scale[i] = 0.f;
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q)  // an exponent of all ones in either half: infinite or NaN
-      bad |= (o[q] & 0x7F80u) == 0x7F80u || (o[q] & 0x7F800000u) == 0x7F800000u;
-    if (bad) atomicOr(&s_word[2 + (tok >> 5)], 1u << (tok & 31));
-    lo[i] = make_uint4(o[0], o[1], o[2], o[3]);
-    hi[i] = make_uint4(o[4], o[5], o[6], o[7]);
+    top = fmaxf(top, fabsf(scale[i]));
   }
+  const unsigned warp_top = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+  if ((tid & 31) == 0) atomicMax(&s_scale, warp_top);
   __syncthreads();
-  __nv_bfloat16* dst = ws.kv + static_cast<int64_t>(tile) * kTile * kLatent;
+  // 448 * scale < 2^(floor(log2 scale) + 10): below 2^15 once stored
+  // (not below -120: powers of two up and down from there stay inside fp32's normal range)
+  const int e = s_scale ? max(static_cast<int>(s_scale >> 23) - 127 - 5, -120) : 0;
+  uint4* dst = reinterpret_cast<uint4*>(ws.kv + static_cast<int64_t>(tile) * kTile * kLatent);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int w = i * kExpandThreads + tid, tok = w / kChunks;
-    if ((s_word[2 + (tok >> 5)] >> (tok & 31)) & 1u) lo[i] = hi[i] = make_uint4(0u, 0u, 0u, 0u);
-    uint4* out = reinterpret_cast<uint4*>(dst + static_cast<int64_t>(w) * 16);
-    out[0] = lo[i];
-    out[1] = hi[i];
+    const bool drop = (s_word[2 + (tok >> 5)] >> (tok & 31)) & 1u;
+    const float f = drop ? 0.f : scale[i] * exp2i(-e);
+    const uint32_t u[4] = {drop ? 0u : code[i].x, drop ? 0u : code[i].y, drop ? 0u : code[i].z, drop ? 0u : code[i].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v[4];
+      e4m3x4_to_f32(u[q], v);
+      o[2 * q] = pack_half2(v[0] * f, v[1] * f);
+      o[2 * q + 1] = pack_half2(v[2] * f, v[3] * f);
+    }
+    dst[2 * w] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[2 * w + 1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
-  if (tid < 4) reinterpret_cast<unsigned*>(ws.words + 2 * static_cast<int64_t>(tile))[tid] = s_word[tid];
+  if (tid == 0) {
+    TileInfo t;
+    t.valid = s_word[0] | static_cast<uint64_t>(s_word[1]) << 32;
+    t.poison = s_word[2] | static_cast<uint64_t>(s_word[3]) << 32;
+    t.e = e;
+    ws.info[tile] = t;
+  }
 }
 
 // ---- attend ----------------------------------------------------------------------------------
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-      :: "r"(d), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)) : "memory");
+// fp16 MMAs with operand descriptors given by their low word (address and leading offset); the
+// high word is the same for every operand here: 8-row groups 1024 bytes apart, 128-byte swizzle.
+// One elected lane of the converged warp issues (`leader`, found once).
+#define DSA_DESC_HI "0x40004040"
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+static_assert(kDescHi == 0x40004040u, "descriptor high word");
+// (a shared address carries the CTA's rank in the cluster above its 18 bits)
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+  return ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+template <bool ACC>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t leader) {
   asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-      :: "r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)) : "memory");
+      "{\n .reg .pred p, e;\n .reg .b64 b;\n setp.ne.b32 e, %4, 0;\n setp.ne.b32 p, %5, 0;\n"
+      "mov.b64 b, {%2, " DSA_DESC_HI "};\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}"
+      :: "r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(leader), "n"(ACC ? 1 : 0) : "memory");
 }
-// arrive on a barrier once the MMAs this warp's elected lane issued have completed: of this
-// CTA, or (multicast) of the CTAs in the mask
-__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t leader) {
   asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n setp.ne.b32 e, %4, 0;\n setp.ne.b32 p, %5, 0;\n"
+      "mov.b64 a, {%1, " DSA_DESC_HI "};\n mov.b64 b, {%2, " DSA_DESC_HI "};\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}"
+      :: "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(leader), "n"(ACC ? 1 : 0) : "memory");
+}
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}" : "=r"(r));
+  return r;
+}
+// arrive on a barrier once the MMAs the leader issued have completed: of this CTA, or
+// (multicast) of the CTAs in the mask
+__device__ __forceinline__ void commit_leader(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
-      :: "r"(smem_u32(bar)) : "memory");
+      :: "r"(smem_u32(bar)), "r"(leader) : "memory");
 }
-__device__ __forceinline__ void commit_elected_to(uint64_t* bar, uint16_t mask) {
+__device__ __forceinline__ void commit_leader_to(uint64_t* bar, uint16_t mask, uint32_t leader) {
   asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}"
-      :: "r"(smem_u32(bar)), "h"(mask) : "memory");
+      :: "r"(smem_u32(bar)), "h"(mask), "r"(leader) : "memory");
+}
+// fp16 A and B, fp32 accumulator, M = 128
+__host__ __device__ constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
+  return (1u << 4) | (static_cast<uint32_t>(b_mn_major) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(128 >> 4) << 24);
 }
 __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -309,9 +373,79 @@ __device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t ba
                :: "r"(addr), "r"(__float_as_uint(v)), "r"(bar) : "memory");
 }
 
+// S = Q K^T of 64-dim block KB of a tile (four K-steps of 16 dims), its rows at descriptor k_lo.
+template <int KB, bool FIRST>
+__device__ __forceinline__ void qk_block(uint32_t q_lo, uint32_t k_lo, uint32_t leader) {
+  constexpr uint32_t id = idesc_f16(kTile, false);
+  if constexpr (KB < kQTmemBlocks) {
+    mma_ts<!FIRST>(kColS, kColQ + 32 * KB, k_lo, id, leader);
+    mma_ts<true>(kColS, kColQ + 32 * KB + 8, k_lo + 2, id, leader);
+    mma_ts<true>(kColS, kColQ + 32 * KB + 16, k_lo + 4, id, leader);
+    mma_ts<true>(kColS, kColQ + 32 * KB + 24, k_lo + 6, id, leader);
+  } else {
+    constexpr uint32_t off = (KB - kQTmemBlocks) * (kQBlock >> 4);
+    mma_ss<!FIRST>(kColS, q_lo + off, k_lo, id, leader);
+    mma_ss<true>(kColS, q_lo + off + 2, k_lo + 2, id, leader);
+    mma_ss<true>(kColS, q_lo + off + 4, k_lo + 4, id, leader);
+    mma_ss<true>(kColS, q_lo + off + 6, k_lo + 6, id, leader);
+  }
+}
+// O (+)= P V of one tile: four K-steps of 16 positions, 256 value columns
+template <bool ACC>
+__device__ __forceinline__ void pv_tile(uint32_t p_addr, uint32_t v_addr, uint32_t leader) {
+  constexpr uint32_t id = idesc_f16(kHalfV, true);
+  const uint32_t p = desc_lo(p_addr, 16), v = desc_lo(v_addr, kBlock);
+  mma_ss<ACC>(kColO, p, v, id, leader);
+  mma_ss<true>(kColO, p + 2, v + (2048 >> 4), id, leader);
+  mma_ss<true>(kColO, p + 4, v + 2 * (2048 >> 4), id, leader);
+  mma_ss<true>(kColO, p + 6, v + 3 * (2048 >> 4), id, leader);
+}
+
+// The Q K^T warp of CTA C: the own tiles' value blocks (dims 256 C ..) first, the other five
+// blocks as they come.
+template <int C, typename Wait>
+__device__ __forceinline__ void qk_loop(PairCtl& ctl, uint32_t smem0, int n_own, Wait wait_warp) {
+  const uint32_t leader = elect_leader();
+  const uint32_t q_lo = desc_lo(smem0 + kOffQ, 16);
+  const uint32_t v_lo = desc_lo(smem0 + kOffVOwn, 16), l_lo = desc_lo(smem0 + kOffLoose, 16);
+  constexpr uint32_t kStep = kBlock >> 4;
+  for (int i = 0; i < n_own; ++i) {
+    const int b = i & 1;
+    if (!wait_warp(&ctl.s_free, i + 1) || !wait_warp(&ctl.vown_full[b], i >> 1)) return;
+    tc::fence_after_sync();
+    if (b == 0) {
+      qk_block<4 * C, true>(q_lo, v_lo, leader);
+      qk_block<4 * C + 1, false>(q_lo, v_lo + kStep, leader);
+      qk_block<4 * C + 2, false>(q_lo, v_lo + 2 * kStep, leader);
+      qk_block<4 * C + 3, false>(q_lo, v_lo + 3 * kStep, leader);
+    } else {
+      qk_block<4 * C, true>(q_lo, v_lo + 4 * kStep, leader);
+      qk_block<4 * C + 1, false>(q_lo, v_lo + 5 * kStep, leader);
+      qk_block<4 * C + 2, false>(q_lo, v_lo + 6 * kStep, leader);
+      qk_block<4 * C + 3, false>(q_lo, v_lo + 7 * kStep, leader);
+    }
+    constexpr int L = 4 * (1 - C);
+    if (!wait_warp(&ctl.loose_full[0], i)) return;
+    qk_block<L, false>(q_lo, l_lo, leader);
+    commit_leader(&ctl.loose_empty[0], leader);
+    if (!wait_warp(&ctl.loose_full[1], i)) return;
+    qk_block<L + 1, false>(q_lo, l_lo + kStep, leader);
+    commit_leader(&ctl.loose_empty[1], leader);
+    if (!wait_warp(&ctl.loose_full[2], i)) return;
+    qk_block<L + 2, false>(q_lo, l_lo + 2 * kStep, leader);
+    commit_leader(&ctl.loose_empty[2], leader);
+    if (!wait_warp(&ctl.loose_full[3], i)) return;
+    qk_block<L + 3, false>(q_lo, l_lo + 3 * kStep, leader);
+    commit_leader(&ctl.loose_empty[3], leader);
+    if (!wait_warp(&ctl.loose_full[4], i)) return;
+    qk_block<8, false>(q_lo, l_lo + 4 * kStep, leader);
+    commit_leader(&ctl.loose_empty[4], leader);
+    commit_leader(&ctl.s_full, leader);
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
-attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kvmap, PrefixArgs a,
-              PrefixPlan pl, PrefixWs ws) {
+attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
   extern __shared__ __align__(1024) uint8_t smem[];
   PairCtl& ctl = *reinterpret_cast<PairCtl*>(smem + kOffCtl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -365,20 +499,17 @@ attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
     return;
   }
   const int n_own = (nt - c + 1) / 2, n_peer = nt - n_own;  // own tile i: 2 i + c; peer tile i: 2 i + peer
-
-  const bool aligned = (smem_u32(smem) & 1023u) == 0;  // the same in both CTAs
-  if (!aligned) {
+  const uint32_t smem0 = smem_u32(smem);
+  if (smem0 & 1023u) {  // (the same in both CTAs)
     if (tid == 0) flag(a.status, DSA_STATUS_INTERNAL);
     return;
   }
   if (tid == 0) {
     ctl.abort = 0;
-    ctl.redo = 0;
-    tc::mbar_init(&ctl.q_full, 1);
-    tc::mbar_init(&ctl.q_tmem, 4);
-    for (int k = 0; k < kRing; ++k) {
-      tc::mbar_init(&ctl.ring_full[k], 1);
-      tc::mbar_init(&ctl.ring_empty[k], 1);
+    tc::mbar_init(&ctl.q_ready, kSoftWarps);
+    for (int k = 0; k < kLoose; ++k) {
+      tc::mbar_init(&ctl.loose_full[k], 1);
+      tc::mbar_init(&ctl.loose_empty[k], 1);
     }
     for (int k = 0; k < 2; ++k) {
       tc::mbar_init(&ctl.vown_full[k], 1);
@@ -387,25 +518,31 @@ attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
     tc::mbar_init(&ctl.vpeer_full, 1);
     tc::mbar_init(&ctl.vpeer_empty, 1);
     tc::mbar_init(&ctl.s_full, 1);
-    tc::mbar_init(&ctl.s_free, 4);
-    tc::mbar_init(&ctl.p_full, 4);
+    tc::mbar_init(&ctl.s_free, kSoftWarps);
+    tc::mbar_init(&ctl.p_full, kSoftWarps);
     tc::mbar_init(&ctl.p_empty, 2);
     tc::mbar_init(&ctl.pin_full, 1);
+    tc::mbar_init(&ctl.pin_go, kSoftWarps);
     tc::mbar_init(&ctl.o_done, 1);
     tc::mbar_init(&ctl.r_full, 1);
     tc::mbar_init(&ctl.fin_full, 1);
     tc::mbar_fence_init();
     // what the peer will send
     if (c == 1) tc::mbar_arrive_expect_tx(&ctl.r_full, kRows * 4);
-    tc::mbar_arrive_expect_tx(&ctl.fin_full, kRows * 12);
-    tc::mbar_arrive_expect_tx(&ctl.pin_full, kPBytes);
+    tc::mbar_arrive_expect_tx(&ctl.fin_full, kRows * 4);
+    tc::mbar_arrive_expect_tx(&ctl.pin_full, kPMsg);
   }
   if (warp == 1) tc::tmem_alloc(&ctl.tmem_base, 512);
   tc::fence_before_sync();
   __syncthreads();
+  // all 512 columns are this CTA's, so its addresses start at 0 and are constants below
+  if (tid == 0 && ctl.tmem_base != 0) {
+    flag(a.status, DSA_STATUS_INTERNAL);
+    ctl.abort = 1;
+  }
+  __syncwarp();
   cluster_sync();  // the peer's barriers are ready
   tc::fence_after_sync();
-  const uint32_t tmem = ctl.tmem_base;
   volatile int* abort = &ctl.abort;
   // (bounded) wait of one thread, and of a converged warp: there the lanes agree on the outcome
   auto wait = [&](uint64_t* bar, uint32_t parity) { return tc::mbar_wait(bar, parity & 1u, abort, a.status); };
@@ -415,339 +552,363 @@ attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   };
 
   // softmax threads: their row's state, kept from the loop to the output
-  float r = 0.f, l = 0.f, lx = 0.f;
-  // steps done in earlier attempts, by role (barrier phases run on)
-  int g_own = 0, g_peer = 0;
-  bool gave_up = false;  // a wait ran out, here or in the peer
-  for (int attempt = 0; attempt < 2; ++attempt) {
-    if (warp == 0) {
-      // ---------------- own tiles: the half of the value blocks this CTA keeps, then the rest ----------------
-      if (lane == 0) {
-        if (attempt == 0) {
-          tc::prefetch_tmap(&qmap);
-          tc::prefetch_tmap(&kvmap);
-          tc::mbar_arrive_expect_tx(&ctl.q_full, kQSmemBlocks * kQBlock);
-          for (int kb = 0; kb < kQSmemBlocks; ++kb)
-            tc::tma_load_3d(smem + kOffQ + kb * kQBlock, &qmap, kQTmemSteps * 16 + 64 * kb, static_cast<int>(row0), 0,
-                            &ctl.q_full);
-        }
-        for (int i = 0; i < n_own; ++i) {
-          const int g = g_own + i, b = g & 1;
-          const int y = (tile_base + tile0 + 2 * i + c) * kTile;
-          if (!wait(&ctl.vown_empty[b], (g >> 1) + 1)) break;
-          tc::mbar_arrive_expect_tx(&ctl.vown_full[b], 4 * kBlock);
-          for (int k = 0; k < 4; ++k)
-            tc::tma_load_3d(smem + kOffVOwn + (4 * b + k) * kBlock, &kvmap, 64 * (4 * c + k), y, 0, &ctl.vown_full[b]);
-          bool ok = true;
-          for (int k = 0; k < kLoose && ok; ++k) {
-            const int n = kLoose * g + k, slot_k = n % kRing;
-            ok = wait(&ctl.ring_empty[slot_k], n / kRing + 1);
-            if (!ok) break;
-            tc::mbar_arrive_expect_tx(&ctl.ring_full[slot_k], kBlock);
-            tc::tma_load_3d(smem + kOffRing + slot_k * kBlock, &kvmap, 64 * (k < 4 ? 4 * peer + k : 8), y, 0,
-                            &ctl.ring_full[slot_k]);
-          }
+  float rho = -INFINITY, l = 0.f;
+  int e_top = -1000;
+  if (warp == 0) {
+    // ---------------- own tiles: the half of the value blocks this CTA keeps, then the rest ----------------
+    if (lane == 0) {
+      tc::prefetch_tmap(&kvmap);
+      bool ok = true;
+      for (int i = 0; i < n_own && ok; ++i) {
+        const int b = i & 1, y = (tile_base + tile0 + 2 * i + c) * kTile;
+        if (!wait(&ctl.vown_empty[b], (i >> 1) + 1)) break;
+        tc::mbar_arrive_expect_tx(&ctl.vown_full[b], 4 * kBlock);
+        for (int k = 0; k < 4; ++k)
+          tc::tma_load_3d(smem + kOffVOwn + (4 * b + k) * kBlock, &kvmap, 64 * (4 * c + k), y, 0, &ctl.vown_full[b]);
+        for (int k = 0; k < kLoose; ++k) {
+          ok = wait(&ctl.loose_empty[k], i + 1);
           if (!ok) break;
+          tc::mbar_arrive_expect_tx(&ctl.loose_full[k], kBlock);
+          tc::tma_load_3d(smem + kOffLoose + k * kBlock, &kvmap, 64 * (k < 4 ? 4 * peer + k : 8), y, 0,
+                          &ctl.loose_full[k]);
         }
       }
-      __syncwarp();
-    } else if (warp == 8) {
-      // ---------------- the peer's tiles: this CTA's value blocks ----------------
-      if (lane == 0) {
-        for (int i = 0; i < n_peer; ++i) {
-          const int g = g_peer + i;
-          const int y = (tile_base + tile0 + 2 * i + peer) * kTile;
-          if (!wait(&ctl.vpeer_empty, g + 1)) break;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- Q K^T ----------------
+    if (wait_warp(&ctl.q_ready, 0)) {
+      tc::fence_after_sync();
+      if (c == 0) qk_loop<0>(ctl, smem0, n_own, wait_warp);
+      else qk_loop<1>(ctl, smem0, n_own, wait_warp);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------- P V: this CTA's value half, over own and peer tiles in turn ----------------
+    const uint32_t leader = elect_leader();
+    for (int i = 0; i < n_own || i < n_peer; ++i) {
+      if (i < n_own) {
+        if (!wait_warp(&ctl.p_full, i)) break;
+        tc::fence_after_sync();
+        if (i == 0) pv_tile<false>(smem0 + kOffPOwn, smem0 + kOffVOwn, leader);
+        else if (i & 1) pv_tile<true>(smem0 + kOffPOwn, smem0 + kOffVOwn + 4 * kBlock, leader);
+        else pv_tile<true>(smem0 + kOffPOwn, smem0 + kOffVOwn, leader);
+        commit_leader(&ctl.vown_empty[i & 1], leader);
+        commit_leader(&ctl.p_empty, leader);
+      }
+      if (i < n_peer) {
+        if (!wait_warp(&ctl.vpeer_full, i) || !wait_warp(&ctl.pin_go, i)) break;
+        if (leader) tc::mbar_arrive_expect_tx(&ctl.pin_full, kPMsg);  // the next weights
+        __syncwarp();
+        tc::fence_after_sync();
+        if (i == 0 && n_own == 0) pv_tile<false>(smem0 + kOffPIn, smem0 + kOffVPeer, leader);
+        else pv_tile<true>(smem0 + kOffPIn, smem0 + kOffVPeer, leader);
+        commit_leader(&ctl.vpeer_empty, leader);
+        commit_leader_to(&ctl.p_empty, static_cast<uint16_t>(1u << peer), leader);
+      }
+    }
+    commit_leader(&ctl.o_done, leader);
+    __syncwarp();
+  } else if (warp == 3) {
+    // ---------------- own weights to the peer; value blocks of the peer's tiles ----------------
+    if (lane == 0) {
+      const uint32_t dst = dsmem_addr(smem + kOffPIn, peer), bar = dsmem_addr(&ctl.pin_full, peer);
+      for (int i = 0; i < n_own || i < n_peer; ++i) {
+        if (i < n_peer) {
+          if (!wait(&ctl.vpeer_empty, i + 1)) break;
           tc::mbar_arrive_expect_tx(&ctl.vpeer_full, 4 * kBlock);
           for (int k = 0; k < 4; ++k)
-            tc::tma_load_3d(smem + kOffVPeer + k * kBlock, &kvmap, 64 * (4 * c + k), y, 0, &ctl.vpeer_full);
+            tc::tma_load_3d(smem + kOffVPeer + k * kBlock, &kvmap, 64 * (4 * c + k),
+                            (tile_base + tile0 + 2 * i + peer) * kTile, 0, &ctl.vpeer_full);
         }
-      }
-      __syncwarp();
-    } else if (warp == 1) {
-      // ---------------- Q K^T ----------------
-      const uint32_t id = tc::idesc_bf16(kTile, false, false);
-      const uint64_t qd = tc::desc_kmajor_sw128(smem_u32(smem + kOffQ));
-      const uint32_t d = tmem + kColS;
-      bool ok = wait_warp(&ctl.q_full, 0) && wait_warp(&ctl.q_tmem, 0);
-      // the four K-steps of 64-dim block kb
-      auto block = [&](int kb, uint64_t kd, bool first) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          if (kb < kQTmemSteps / 4)
-            mma_ts(d, tmem + kColQ + 32 * kb + 8 * s, kd + 2 * s, id, !(first && s == 0));
-          else
-            mma_ss(d, qd + (kb - kQTmemSteps / 4) * (kQBlock >> 4) + 2 * s, kd + 2 * s, id, !(first && s == 0));
-        }
-      };
-      for (int i = 0; i < n_own && ok; ++i) {
-        const int g = g_own + i, b = g & 1;
-        ok = wait_warp(&ctl.s_free, g + 1) && wait_warp(&ctl.vown_full[b], g >> 1);
-        if (!ok) break;
-        __syncwarp();
-        tc::fence_after_sync();
-        const uint64_t vd = tc::desc_kmajor_sw128(smem_u32(smem + kOffVOwn + 4 * b * kBlock));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) block(4 * c + k, vd + k * (kBlock >> 4), k == 0);
-        for (int k = 0; k < kLoose; ++k) {
-          const int n = kLoose * g + k, slot_k = n % kRing;
-          ok = wait_warp(&ctl.ring_full[slot_k], n / kRing);
-          if (!ok) break;
-          __syncwarp();
-          tc::fence_after_sync();
-          block(k < 4 ? 4 * peer + k : 8, tc::desc_kmajor_sw128(smem_u32(smem + kOffRing + slot_k * kBlock)), false);
-          commit_elected(&ctl.ring_empty[slot_k]);
-        }
-        commit_elected(&ctl.s_full);
-      }
-      __syncwarp();
-    } else if (warp == 2) {
-      // ---------------- P V: this CTA's value half, over own and peer tiles in turn ----------------
-      const uint32_t id = tc::idesc_bf16(kHalfV, false, true);
-      bool any = false, ok = true;
-      auto pv = [&](uint32_t off_p, uint32_t off_v) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {  // 16 positions a step
-          const uint64_t pd = tc::desc_kmajor_sw128(smem_u32(smem + off_p)) + 2 * s;
-          const uint64_t vd = tc::smem_desc(smem_u32(smem + off_v) + s * 2048, kBlock, 1024, 2);
-          mma_ss(tmem + kColO, pd, vd, id, any || s > 0);
-        }
-        any = true;
-      };
-      for (int i = 0; i < n_own || i < n_peer; ++i) {
         if (i < n_own) {
-          const int g = g_own + i;
-          ok = wait_warp(&ctl.p_full, g);
-          if (!ok) break;
-          __syncwarp();
-          tc::fence_after_sync();
-          pv(kOffPOwn, kOffVOwn + 4 * (g & 1) * kBlock);
-          commit_elected(&ctl.vown_empty[g & 1]);
-          commit_elected(&ctl.p_empty);
-        }
-        if (i < n_peer) {
-          const int g = g_peer + i;
-          ok = wait_warp(&ctl.pin_full, g);
-          if (!ok) break;
-          if (lane == 0) tc::mbar_arrive_expect_tx(&ctl.pin_full, kPBytes);  // the next weights
-          ok = wait_warp(&ctl.vpeer_full, g);
-          if (!ok) break;
-          __syncwarp();
-          tc::fence_after_sync();
-          pv(kOffPIn, kOffVPeer);
-          commit_elected(&ctl.vpeer_empty);
-          commit_elected_to(&ctl.p_empty, static_cast<uint16_t>(1u << peer));
-        }
-      }
-      commit_elected(&ctl.o_done);
-      __syncwarp();
-    } else if (warp == 3) {
-      // ---------------- own weights to the peer ----------------
-      if (lane == 0) {
-        const uint32_t dst = dsmem_addr(smem + kOffPIn, peer), bar = dsmem_addr(&ctl.pin_full, peer);
-        for (int i = 0; i < n_own; ++i) {
           // (the warps that wrote them waited until the peer had read the last ones)
-          if (!wait(&ctl.p_full, g_own + i)) break;
-          bulk_to_peer(dst, smem + kOffPOwn, kPBytes, bar);
+          if (!wait(&ctl.p_full, i)) break;
+          bulk_to_peer(dst, smem + kOffPOwn, kPMsg, bar);
         }
       }
-      __syncwarp();
-    } else {
-      // ---------------- logits -> weights, one row a thread (warps 4..7) ----------------
-      const int quarter = warp & 3, m = quarter * 32 + lane;
-      const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-      const bool live = m < n_rows;
-      if (attempt == 0) {  // the query's first 384 dims into tensor memory
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (row0 + m) * kLatent);
-#pragma unroll
-        for (int h = 0; h < 6; ++h) {
-          uint32_t v[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            if (live) u = __ldg(src + 8 * h + i);
-            v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
-          }
-          tmem_store32(tmem + lane_base + kColQ + 32 * h, v);
-        }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ctl.q_tmem);
-      }
-      // positions of this part the row sees
-      int lim = 0;
+    }
+    __syncwarp();
+  } else {
+    // ---------------- logits -> weights (warps 4..11): row m, positions 32 hv .. of each tile ----------------
+    const int quarter = warp & 3, hv = (warp - 4) >> 2, m = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t pair_bar = 1 + quarter;  // named barrier of the row's two warps
+    const bool live = m < n_rows;
+    // the larger of v over a row's two threads (slot: alternates, so that a value is read before it
+    // is written again)
+    auto row_max = [&](float v, int slot_k) {
+      ctl.part[slot_k][hv][m] = v;
+      asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
+      return fmaxf(v, ctl.part[slot_k][hv ^ 1][m]);
+    };
+    float k2;  // logit (in powers of two) = S * k2 * 2^(tile's exponent)
+    {  // the query as fp16 by a power of two per row: dims 0..319 by hv 0, the rest by hv 1
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (row0 + m) * kLatent);
+      const int first = hv ? 40 : 0, last = hv ? 72 : 40;
+      __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
       if (live) {
-        lim = row_limit(a, static_cast<int>((row0 + m) / a.h_s), !tail && split == 0 && c == 0) - first_pos;
-        if (!tail) lim = min(lim, a.prefix_len);
+#pragma unroll 8
+        for (int i = first; i < last; ++i) {
+          const uint4 u = __ldg(src + i);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[j])));
+        }
       }
-      const float c2 = a.sm_scale * 1.4426950408889634f;  // logits in powers of two
-      float top = -INFINITY;
-      l = lx = 0.f;
-      if (attempt == 0 && c == 1) {
-        wait_warp(&ctl.r_full, 0);
-        r = ctl.r[m];
+      const float top = row_max(fmaxf(__low2float(top2), __high2float(top2)), 1);
+      // top * 2^-qe in [2^14, 2^15); zero, subnormal and infinite rows stay within the exponents
+      const int qe = top > 0.f ? min(max(static_cast<int>(__float_as_uint(top) >> 23), 1), 254) - 127 - 14 : 0;
+      const float f0 = exp2i(-(qe / 2)), f1 = exp2i(-(qe - qe / 2));
+      k2 = a.sm_scale * 1.4426950408889634f * exp2i(qe / 2) * exp2i(qe - qe / 2);
+      auto scaled = [&](int i) {
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (live) u = __ldg(src + i);
+        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = pack_half2(__uint_as_float(w[j] << 16) * f0 * f1, __uint_as_float(w[j] & 0xFFFF0000u) * f0 * f1);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+      };
+      for (int h = hv ? 5 : 0; h < (hv ? 6 : 5); ++h) {
+        uint32_t v[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 u = scaled(8 * h + i);
+          v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
+        }
+        tmem_store32(lane_base + kColQ + 32 * h, v);
       }
-      for (int i = 0; i < n_own; ++i) {
-        const int g = g_own + i, tile = tile0 + 2 * i + c;
-        const ulonglong2 w = __ldcg(reinterpret_cast<const ulonglong2*>(ws.words) + tile_base + tile);
+      if (hv) {
+#pragma unroll 4
+        for (int i = 0; i < 8 * kQSmemBlocks; ++i)
+          *reinterpret_cast<uint4*>(smem + kOffQ + (i >> 3) * kQBlock + m * 128 + (((i & 7) ^ (m & 7)) << 4)) =
+              scaled(8 * kQTmemBlocks + i);
+        tc::fence_async_smem();
+      }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&ctl.q_ready);
+    }
+    // positions of this part the row sees
+    int lim = 0;
+    if (live) {
+      lim = row_limit(a, static_cast<int>((row0 + m) / a.h_s), !tail && split == 0 && c == 0 && hv == 0) - first_pos;
+      if (!tail) lim = min(lim, a.prefix_len);
+    }
+    // O's row (this thread's 128 columns) and the sum times 2^-by
+    auto rescale = [&](float by, bool any_product) {
+      const float f = exp2f(-by);
+      l *= f;
+      if (!any_product) return;
+      tc::fence_after_sync();
+      for (int col = 128 * hv; col < 128 * hv + 128; col += 16) {
+        uint32_t v[16];
+        tc::tmem_ld16(lane_base + kColO + col, v);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+        tc::tmem_st16(lane_base + kColO + col, v);
+      }
+      tc::tmem_wait_st();
+    };
+    if (c == 1) {
+      wait_warp(&ctl.r_full, 0);
+      rho = ctl.r[m];
+    }
+    float* own_r = reinterpret_cast<float*>(smem + kOffPOwn + kPBytes);
+    const float* in_r = reinterpret_cast<const float*>(smem + kOffPIn + kPBytes);
+    // (after a wait that ran out these warps still go through every step, each wait returning at
+    // once: the named barriers need both of a row's warps)
+    for (int i = 0; i < n_own || i < n_peer; ++i) {
+      if (i < n_own) {
+        const int tile = tile0 + 2 * i + c;
+        const TileInfo* info = ws.info + tile_base + tile;
+        const ulonglong2 w = __ldcg(reinterpret_cast<const ulonglong2*>(info));
+        const int e = __ldcg(&info->e);
         const int nv = lim - tile * kTile;
-        const uint64_t seen = w.x & (nv >= kTile ? ~0ull : nv <= 0 ? 0ull : (1ull << nv) - 1ull);
-        if (!wait_warp(&ctl.s_full, g)) break;
+        const uint64_t seen64 = w.x & (nv >= kTile ? ~0ull : nv <= 0 ? 0ull : (1ull << nv) - 1ull);
+        const uint32_t seen = static_cast<uint32_t>(seen64 >> (32 * hv)), poison = static_cast<uint32_t>(w.y >> (32 * hv));
+        e_top = max(e_top, e);
+        // (held inside fp32's range: a factor of 0 would turn an unseen position's -inf into NaN)
+        const float kt = fminf(fmaxf(k2 * exp2i(e), 1.2e-38f), 3.0e38f);
+        const float fe = static_cast<float>(e);
+        wait_warp(&ctl.s_full, i);
         tc::fence_after_sync();
-        uint32_t s0[32], s1[32];
-        tc::tmem_ld32(tmem + lane_base + kColS, s0);
-        tc::tmem_ld32(tmem + lane_base + kColS + 32, s1);
+        uint32_t s[32];
+        tc::tmem_ld32(lane_base + kColS + 32 * hv, s);
         tc::tmem_wait_ld();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ctl.s_free);
-        if (!__all_sync(0xffffffffu, seen == ~0ull && w.y == 0)) {
-          const uint32_t inf = 0xFF800000u, nan = 0x7FFFFFFFu;
+        if (!__all_sync(0xffffffffu, seen == ~0u && poison == 0u)) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            if ((w.y >> k) & 1u) s0[k] = nan;
-            if ((w.y >> (32 + k)) & 1u) s1[k] = nan;
-            if (!((seen >> k) & 1u)) s0[k] = inf;
-            if (!((seen >> (32 + k)) & 1u)) s1[k] = inf;
+            if ((poison >> k) & 1u) s[k] = 0x7FFFFFFFu;
+            if (!((seen >> k) & 1u)) s[k] = 0xFF800000u;
           }
         }
-        float mt = -INFINITY;
+        float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) mt = fmaxf(mt, fmaxf(__uint_as_float(s0[k]), __uint_as_float(s1[k])));
-        mt *= c2;
-        top = fmaxf(top, mt);
-        if (attempt == 0 && c == 0 && i == 0) {
-          r = mt == -INFINITY ? 0.f : mt;  // nothing seen in the first tile: any guess
-          st_async_f32(dsmem_addr(&ctl.r[m], 1), r, dsmem_addr(&ctl.r_full, 1));
+        for (int k = 0; k < 32; k += 4) {
+          t0 = fmaxf(t0, fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
+          t1 = fmaxf(t1, fmaxf(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
         }
-        // weights, rounded to the bf16 that the tensor cores read; l sums the rounded ones (it
-        // normalises O), lx the unrounded ones (it gives the log-sum-exp)
-        uint32_t p[32];
-        float la = 0.f, lb = 0.f, xa = 0.f, xb = 0.f;
+        const float mt = row_max(fmaf(fmaxf(t0, t1), kt, fe), i & 1);
+        if (i == 0 && c == 0) {
+          rho = mt;
+          if (hv == 0) st_async_f32(dsmem_addr(&ctl.r[m], 1), rho, dsmem_addr(&ctl.r_full, 1));
+        }
+        // the row's reference rises when a weight would pass 2^14, or at its first position
+        const bool raise = mt > rho + kHeadroom || (rho == -INFINITY && mt > -INFINITY);
+        if (__any_sync(0xffffffffu, raise)) {
+          const bool any_product = i > 0;
+          if (any_product) wait_warp(&ctl.vpeer_empty, i - 1);  // the last product was the peer tile's
+          rescale(raise ? mt - rho : 0.f, any_product);
+          if (raise) rho = mt;
+        }
+        const float off = fe - (rho == -INFINITY ? 0.f : rho);
+        uint32_t p[16];
+        float x0 = 0.f, x1 = 0.f;
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
-          const float a0 = exp2_approx(fmaf(__uint_as_float(s0[k]), c2, -r));
-          const float a1 = exp2_approx(fmaf(__uint_as_float(s0[k + 1]), c2, -r));
-          const float b0 = exp2_approx(fmaf(__uint_as_float(s1[k]), c2, -r));
-          const float b1 = exp2_approx(fmaf(__uint_as_float(s1[k + 1]), c2, -r));
-          p[k >> 1] = pack2(a0, a1);
-          p[16 + (k >> 1)] = pack2(b0, b1);
-          xa += a0 + a1;
-          xb += b0 + b1;
-          la += __uint_as_float(p[k >> 1] << 16) + __uint_as_float(p[k >> 1] & 0xFFFF0000u);
-          lb += __uint_as_float(p[16 + (k >> 1)] << 16) + __uint_as_float(p[16 + (k >> 1)] & 0xFFFF0000u);
+          const float a0 = exp2_approx(fmaf(__uint_as_float(s[k]), kt, off));
+          const float a1 = exp2_approx(fmaf(__uint_as_float(s[k + 1]), kt, off));
+          p[k >> 1] = pack_half2(a0, a1);
+          x0 += a0;
+          x1 += a1;
         }
-        l += la + lb;
-        lx += xa + xb;
-        if (!wait_warp(&ctl.p_empty, g + 1)) break;
+        l = fmaf(x0 + x1, exp2i(-e), l);
+        wait_warp(&ctl.p_empty, i + 1);
         uint8_t* row = smem + kOffPOwn + m * 128;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<uint4*>(row + ((k ^ (m & 7)) << 4)) = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(row + (((4 * hv + k) ^ (m & 7)) << 4)) =
+              make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+        if (hv == 0) own_r[m] = rho;
         tc::fence_async_smem();
+        tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ctl.p_full);
       }
-      // the last weights have been read, here and by the peer (whose word of it has then arrived)
-      if (n_own > 0) wait_warp(&ctl.p_empty, g_own + n_own - 1);
-      // ---- both CTAs' maxima and sums ----
-      {
-        const uint32_t bar = dsmem_addr(&ctl.fin_full, peer);
-        dsmem_st_async_v2(dsmem_addr(&ctl.fin2[m], peer), make_uint2(__float_as_uint(top), __float_as_uint(l)), bar);
-        st_async_f32(dsmem_addr(&ctl.fin1[m], peer), lx, bar);
-      }
-      if (wait_warp(&ctl.fin_full, attempt)) {
-        const float2 f2 = ctl.fin2[m];
-        const float f1 = ctl.fin1[m];
-        top = fmaxf(top, f2.x);
-        l = c == 0 ? l + f2.y : f2.y + l;  // the same order in both CTAs
-        lx = c == 0 ? lx + f1 : f1 + lx;
-      }
-      const bool far = live && top != -INFINITY && fabsf(top - r) > kRange;
-      if (attempt == 0 && far) atomicOr(&ctl.redo, 1);
-      if (attempt == 0) {
-        // (a second phase is expected only if there is a second attempt)
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (ctl.redo) {
-          if (tid == 4 * 32) tc::mbar_arrive_expect_tx(&ctl.fin_full, kRows * 12);
-          r = top == -INFINITY ? 0.f : top;
+      if (i < n_peer) {
+        e_top = max(e_top, __ldcg(&ws.info[tile_base + tile0 + 2 * i + peer].e));
+        wait_warp(&ctl.pin_full, i);
+        const float r_in = in_r[m];
+        if (__any_sync(0xffffffffu, r_in != rho)) {
+          const bool any_product = i < n_own || i > 0;
+          // every product so far: the last was the own tile's, or the peer's before it
+          if (i < n_own) wait_warp(&ctl.vown_empty[i & 1], i >> 1);
+          else if (i > 0) wait_warp(&ctl.vpeer_empty, i - 1);
+          const bool raise = r_in > rho;
+          rescale(raise ? r_in - rho : 0.f, any_product);
+          if (raise) rho = r_in;
+          if (r_in < rho) {  // sent before the peer learned of this reference (2^-inf = 0)
+            const float f = exp2f(r_in - rho);
+            uint8_t* row = smem + kOffPIn + m * 128;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint4* at = reinterpret_cast<uint4*>(row + (((4 * hv + k) ^ (m & 7)) << 4));
+              const uint4 u = *at;
+              uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 h = unpack_half2(v[j]);
+                v[j] = pack_half2(h.x * f, h.y * f);
+              }
+              *at = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          }
+          tc::fence_async_smem();
+          tc::fence_before_sync();
+          __syncwarp();
         }
+        if (lane == 0) tc::mbar_arrive(&ctl.pin_go);
       }
     }
-    // every product of this attempt is complete, and nothing the peer sent is still on its way
-    wait(&ctl.o_done, attempt);
-    __syncthreads();
-    if (tid == 0) dsmem_st_u32(dsmem_addr(const_cast<uint32_t*>(&ctl.peer_vote[attempt]), peer), (*abort ? 2u : 0u) | (ctl.redo ? 1u : 0u));
-    __syncwarp();
-    cluster_sync();
-    gave_up = *abort || (ctl.peer_vote[attempt] & 2u);
-    if (attempt == 1 || gave_up || !(ctl.redo && (ctl.peer_vote[0] & 1u))) break;
-    g_own += n_own;
-    g_peer += n_peer;
+    // the last weights have been read, here and by the peer (whose word of it has then arrived)
+    if (n_own > 0) wait_warp(&ctl.p_empty, n_own - 1);
+    // ---- the row's sum over its two threads and both CTAs ----
+    ctl.part[0][hv][m] = l;
+    asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
+    l = ctl.part[0][0][m] + ctl.part[0][1][m];
+    if (hv == 0) st_async_f32(dsmem_addr(&ctl.fin[m], peer), l, dsmem_addr(&ctl.fin_full, peer));
+    if (wait_warp(&ctl.fin_full, 0)) l = c == 0 ? l + ctl.fin[m] : ctl.fin[m] + l;  // the same in both CTAs
   }
+  // every product is complete, and nothing the peer sends is still on its way
+  wait(&ctl.o_done, 0);
+  __syncthreads();
   tc::fence_after_sync();
 
-  // ---- output: O / l as bf16, through the tiles' shared memory, in whole rows ----
+  // ---- output: O / l through the tiles' shared memory, in whole rows: bf16, or with several
+  // splits fp16 times 2^-(e_out), e_out the largest exponent of the item's tiles: |O / l| is at
+  // most the largest value, below 2^15 2^e_out ----
   uint8_t* stage = smem + kOffVOwn;
-  if (warp >= 4 && warp < 8) {
-    const int m = (warp & 3) * 32 + lane;
+  if (warp >= 4) {
+    const int hv = (warp - 4) >> 2, m = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int e_out = e_top;
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const float down = exp2i(-e_out);
     uint8_t* row = stage + m * kStagePitch;
 #pragma unroll
-    for (int col = 0; col < kHalfV; col += 32) {
+    for (int k = 0; k < 4; ++k) {
+      const int col = 128 * hv + 32 * k;
       uint32_t v[32];
-      tc::tmem_ld32(tmem + lane_base + kColO + col, v);
+      tc::tmem_ld32(lane_base + kColO + col, v);
       tc::tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 32; i += 8)
-        *reinterpret_cast<uint4*>(row + 2 * (col + i)) =
-            make_uint4(pack2(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv),
-                       pack2(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv),
-                       pack2(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv),
-                       pack2(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv));
+      for (int i = 0; i < 32; i += 8) {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float y0 = __uint_as_float(v[i + 2 * j]) * inv, y1 = __uint_as_float(v[i + 2 * j + 1]) * inv;
+          o[j] = ns == 1 ? pack2(y0, y1) : pack_half2(y0 * down, y1 * down);
+        }
+        *reinterpret_cast<uint4*>(row + 2 * (col + i)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
-    if (c == 0 && m < n_rows) {
+    if (c == 0 && hv == 0 && m < n_rows) {
       if (ns == 1) {
-        if (a.out_lse)
-          a.out_lse[row0 + m] = lx > 0.f || lx != lx ? (r + log2f(lx)) * 0.6931471805599453f : -INFINITY;
+        if (a.out_lse) a.out_lse[row0 + m] = l > 0.f || l != l ? (rho + log2f(l)) * 0.6931471805599453f : -INFINITY;
       } else {
         // the sum's own exponent joins the reference, so that the merge compares true sizes
-        const int e = l > 0.f && l < INFINITY ? static_cast<int>(__float_as_uint(l) >> 23) - 127 : 0;
-        const float f = exp2i(-e);
-        ws.ml[(row0 + m) * ns + slot] =
-            l == 0.f ? make_float4(-INFINITY, 0.f, 0.f, 0.f) : make_float4(r + static_cast<float>(e), l * f, lx * f, 0.f);
+        const int el = l > 0.f && l < INFINITY ? static_cast<int>(__float_as_uint(l) >> 23) - 127 : 0;
+        // (NaN logits leave no reference; the merge takes -inf for an empty split)
+        const float ref = l != l ? 0.f : rho + static_cast<float>(el);
+        ws.ml[(row0 + m) * ns + slot] = l == 0.f ? make_float4(-INFINITY, 0.f, 0.f, 0.f)
+                                                 : make_float4(ref, l * exp2i(-max(el, -126)), static_cast<float>(e_out), 0.f);
       }
     }
   }
   __syncthreads();
   {
     const int piece = tid & 31;
+    uint16_t* const base = ns == 1 ? static_cast<uint16_t*>(a.out) : reinterpret_cast<uint16_t*>(ws.o);
     for (int m = tid >> 5; m < n_rows; m += kThreads / 32) {
-      __nv_bfloat16* dst = ns == 1 ? static_cast<__nv_bfloat16*>(a.out) + (row0 + m) * kVDim
-                                   : ws.o + ((row0 + m) * ns + slot) * kVDim;
-      *reinterpret_cast<uint4*>(dst + kHalfV * c + 8 * piece) =
+      const int64_t at = ns == 1 ? row0 + m : (row0 + m) * ns + slot;
+      *reinterpret_cast<uint4*>(base + at * kVDim + kHalfV * c + 8 * piece) =
           *reinterpret_cast<const uint4*>(stage + m * kStagePitch + 16 * piece);
     }
   }
   // after a wait that ran out, copies and products may still be in flight: give them time to
-  // land before shared and tensor memory are given back
-  if (gave_up) {
+  // land before either CTA of the pair gives its memory back
+  if (*abort) {
     const uint64_t t0 = tc::global_ns();
     while (tc::global_ns() - t0 < 100000ull) {
     }
-    cluster_sync();
   }
   tc::fence_before_sync();
   __syncthreads();
+  cluster_sync();
   tc::fence_after_sync();
-  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+  if (warp == 1) tc::tmem_dealloc(ctl.tmem_base, 512);
 }
 
 // ---- merge ---------------------------------------------------------------------------------
-// Split s holds O_s / l_s with reference m_s; with M = max m_s and w_s = 2^(m_s - M) l_s the
-// output is sum_s w_s (O_s / l_s) / sum_s w_s.  64 threads a row, 8 columns each, four
+// Split s holds o_s = O_s / l_s (fp16 times a power of two) with reference m_s; with
+// M = max m_s and w_s = 2^(m_s - M) l_s the output is sum_s w_s o_s / sum_s w_s.  64 threads a row, 8 columns each, four
 // rows a block, four splits' loads in flight.
 constexpr int kMergeRows = 4, kMergeBatch = 4;
 __global__ void __launch_bounds__(64 * kMergeRows)
@@ -758,7 +919,7 @@ prefix_merge_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
   if (row >= static_cast<int64_t>(a.n_q) * a.h_s) return;
   const int d = 8 * static_cast<int>(threadIdx.x & 63);
   const int ns = pl.sp + pl.st;
-  float M = -INFINITY, sum = 0.f, sum_x = 0.f, acc[8] = {};
+  float M = -INFINITY, sum = 0.f, acc[8] = {};
   for (int s0 = 0; s0 < ns; s0 += kMergeBatch) {
     float4 ml[kMergeBatch];
     uint4 v[kMergeBatch];
@@ -777,7 +938,6 @@ prefix_merge_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
     if (top != M) {
       const float f = M == -INFINITY ? 0.f : exp2f(M - top);
       sum *= f;
-      sum_x *= f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] *= f;
       M = top;
@@ -785,14 +945,15 @@ prefix_merge_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
 #pragma unroll
     for (int i = 0; i < kMergeBatch; ++i) {
       if (ml[i].x == -INFINITY) continue;  // an empty split: its output was never written
-      const float w = exp2f(ml[i].x - M), wl = w * ml[i].y;
+      const float wl = exp2f(ml[i].x - M) * ml[i].y;
       sum += wl;
-      sum_x += w * ml[i].z;
+      const float f = wl * exp2f(ml[i].z);
       const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        acc[2 * k] += wl * __uint_as_float(u[k] << 16);
-        acc[2 * k + 1] += wl * __uint_as_float(u[k] & 0xFFFF0000u);
+        const float2 h = unpack_half2(u[k]);
+        acc[2 * k] = fmaf(f, h.x, acc[2 * k]);
+        acc[2 * k + 1] = fmaf(f, h.y, acc[2 * k + 1]);
       }
     }
   }
@@ -801,7 +962,7 @@ prefix_merge_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
       make_uint4(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv),
                  pack2(acc[4] * inv, acc[5] * inv), pack2(acc[6] * inv, acc[7] * inv));
   if (a.out_lse && d == 0)
-    a.out_lse[row] = sum_x > 0.f || sum_x != sum_x ? (M + log2f(sum_x)) * 0.6931471805599453f : -INFINITY;
+    a.out_lse[row] = sum > 0.f || sum != sum ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -818,14 +979,14 @@ EncodeFn encode_fn() {
   }();
   return fn;
 }
-// rows of 576 bf16 in boxes of 64 dims x box_rows, 128-byte swizzle; rows past the end read 0
-bool encode_rows(EncodeFn enc, CUtensorMap* map, const void* base, int64_t rows, int box_rows) {
+// rows of 576 fp16 in boxes of 64 dims x 64 rows, 128-byte swizzle
+bool encode_rows(EncodeFn enc, CUtensorMap* map, void* base, int64_t rows) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kLatent), static_cast<cuuint64_t>(rows), 1};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kLatent) * 2,
                                  static_cast<cuuint64_t>(kLatent) * 2 * static_cast<cuuint64_t>(rows)};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t box[3] = {64, kTile, 1};
   const cuuint32_t one[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box, one,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -845,8 +1006,8 @@ size_t prefix_workspace_bytes(int n_q, int h_s, int n_seq, int prefix_len, int m
 cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char** err) {
   const PrefixPlan pl = make_plan(a.n_q, a.h_s, a.n_seq, a.prefix_len, a.max_ctx, sm_count());
   uint8_t* base = static_cast<uint8_t*>(a.workspace);
-  PrefixWs ws{reinterpret_cast<__nv_bfloat16*>(base), reinterpret_cast<uint64_t*>(base + pl.off_words),
-              reinterpret_cast<__nv_bfloat16*>(base + pl.off_o), reinterpret_cast<float4*>(base + pl.off_ml)};
+  PrefixWs ws{reinterpret_cast<__half*>(base), reinterpret_cast<TileInfo*>(base + pl.off_info),
+              reinterpret_cast<__half*>(base + pl.off_o), reinterpret_cast<float4*>(base + pl.off_ml)};
   const int64_t rows = static_cast<int64_t>(a.n_q) * a.h_s;
   const int64_t items = static_cast<int64_t>(pl.sp) * pl.mt + static_cast<int64_t>(pl.st) * a.n_q;
   if (pl.rows_kv > INT32_MAX - kTile || rows > INT32_MAX - kRows || items > INT32_MAX / 2) {
@@ -858,8 +1019,8 @@ cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char**
     *err = "prefix_attn: cuTensorMapEncodeTiled is not available";
     return cudaErrorNotSupported;
   }
-  CUtensorMap qmap, kvmap;
-  if (!encode_rows(enc, &qmap, a.q, rows, kRows) || !encode_rows(enc, &kvmap, ws.kv, pl.rows_kv, kTile)) {
+  CUtensorMap kvmap;
+  if (!encode_rows(enc, &kvmap, ws.kv, pl.rows_kv)) {
     *err = "prefix_attn: tensor map encoding failed";
     return cudaErrorInvalidValue;
   }
@@ -868,8 +1029,8 @@ cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char**
   if (e != cudaSuccess) return e;
   e = launch_pdl(expand_kernel, dim3(static_cast<unsigned>(pl.rows_kv / kTile)), dim3(kExpandThreads), 0, s, 1, a, pl, ws);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attend_kernel, dim3(static_cast<unsigned>(2 * items)), dim3(kThreads), kSmemBytes, s, 2, qmap, kvmap, a,
-                 pl, ws);
+  e = launch_pdl(attend_kernel, dim3(static_cast<unsigned>(2 * items)), dim3(kThreads), kSmemBytes, s, 2, kvmap, a, pl,
+                 ws);
   if (e != cudaSuccess || pl.sp + pl.st == 1) return e;
   return launch_pdl(prefix_merge_kernel, dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows)),
                     dim3(64 * kMergeRows), 0, s, 1, a, pl, ws);

@@ -331,8 +331,9 @@ int dsa_sparse_attn_noalloc(const void* q_bf16, int32_t n_q, int32_t h_s, const 
  * tail) from the sequence's own page-table row:
  *     l_p = sm_scale * q[t, h] . kv[p];  o[t, h] = sum_p softmax(l)_p kv[p][0:512]
  *     lse[t, h] = log sum_p exp(l_p)
- * A row that sees nothing gets o = 0 and lse = -inf.  Dequantised values and softmax weights
- * are rounded to bf16 for the tensor cores, sums kept in fp32.
+ * A row that sees nothing gets o = 0 and lse = -inf.  For the tensor cores the query (by a
+ * power of two per row), the dequantised values (by one per 64 positions) and the softmax
+ * weights are held in fp16, 11 bits for whatever lies within 2^-29 of the largest; sums in fp32.
  *   q_bf16        [n_q][h_s][576] bfloat16, 16-byte aligned; h_s 1..128.
  *   kv_cache      the FP8 latent cache (layout above), num_pages pages, 16-byte aligned.
  *   prefix_pages  [ceil(prefix_len / 64)] int32 physical pages of the shared positions (the

@@ -1,17 +1,20 @@
 """Attention of a batch that shares a prefix (prefix_attn) against the formula in 64 bits.
 
-The reference reads the cache's own bytes.  Two gates for o, both against the float64
-attention over the latent rows rounded to bf16, as the kernel's tensor-core operands are:
+The reference reads the cache's own bytes.  Gates for o against the float64 attention over the
+latent rows rounded to 11 significant bits, as the kernel's fp16 operands are:
 
-* per value: a weight is rounded to bf16 (2^-8 of it) and normalised by the sum of the rounded
-  ones (2^-8 again), a split's partial result and the result are rounded to bf16 (2^-8 of each),
-  and the logits carry the rounding of 576 fp32 additions, sm_scale sum|q kv| 576 2^-24 =: D, which
-  moves a weight by up to 2 D of it, and the hardware 2^x 2^-21 of it.  So with S = sum_j p_j |v_j|
-  |o - ref| <= (3 * 2^-8 + 2 D + 2^-20) S + 2^-8 |ref|;
-* per call: those roundings are independent of each other, so the 2-norm of the difference stays
-  below 2^-7 of the result's.
+* per value: a weight is rounded to fp16 (2^-11 of it, or 2^-25 of the row's largest weight if
+  subnormal), a split's partial result too (2^-11), the result to bf16 (2^-8); the
+  logits carry the rounding of 576 fp32 additions, sm_scale sum|q kv| 576 2^-24 =: D, which moves a
+  weight by up to 2 D of it, and the hardware 2^x 2^-21 of it.  With S = sum_j p_j |v_j| over n
+  positions
+  |o - ref| <= (2 * 2^-11 + 2 D + 2^-20) S + n 2^-25 max|v| + 2^-8 |ref|;
+* per call: those roundings are independent of each other and the last one, of at most 2^-8 and
+  2^-8 / sqrt(3) in the mean square, is the largest, so the 2-norm of the difference stays below
+  2^-8 of the result's.
 
-lse within 1e-4 of the same reference (the sparse attention's gate).
+On the ordinary inputs the second gate also holds against the unrounded rows: 11 bits move a
+logit by some 2^-11.  lse within 1e-4 of the rounded reference (the sparse attention's gate).
 """
 
 import ctypes
@@ -22,7 +25,7 @@ import pytest
 import torch
 
 import oracle
-from dsa_testlib import bf16_round, ensure_built, LSE_BF16_ATOL
+from dsa_testlib import ensure_built, LSE_BF16_ATOL
 
 SM = 1.0 / math.sqrt(192.0)
 
@@ -30,6 +33,12 @@ SM = 1.0 / math.sqrt(192.0)
 @pytest.fixture(scope="module")
 def dsa():
     return ensure_built()
+
+
+def round11(x):
+    """float64 rounded to 11 significant bits, ties to even."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.round(m * 2048.0) / 2048.0, e)
 
 
 class Batch:
@@ -82,15 +91,16 @@ class Batch:
         r = rec[np.where(ok, pages, 0).astype(np.int64) * 64 + p % 64]
         return oracle.fp8_tile_dequantize(r[:, :576], r[:, 576:596].copy().view(np.float32)), ok
 
-    def check(self, out, lse):
+    def check(self, out, lse, unrounded=False):
         o, e = out.double().cpu().numpy(), lse.double().cpu().numpy()
-        err2 = ref2 = 0.0
+        err2 = ref2 = raw2 = 0.0
         for t in range(self.q.shape[0]):
             b, pos = int(self.q_seq[t]), int(self.q_pos[t])
             good = 0 <= b < len(self.lens) and 0 <= int(self.lens[b]) <= self.max_ctx
             n = max(0, min(pos + 1, int(self.lens[b]))) if good else 0
             kv, ok = self.rows64(b) if good else (np.zeros((0, 576)), np.zeros(0, bool))
-            kv = bf16_round(kv[:n][ok[:n]])
+            raw = kv[:n][ok[:n]]
+            kv = round11(raw)
             if not len(kv):
                 assert not o[t].any() and np.all(np.isneginf(e[t]))
                 continue
@@ -102,13 +112,18 @@ class Batch:
             p = w / z
             ref, size = p @ kv[:, :512], p @ np.abs(kv[:, :512])
             d = SM * (np.abs(q) @ np.abs(kv).T).max() * 576 * 2.0 ** -24
-            tol = (3 * 2.0 ** -8 + 2 * d + 2.0 ** -20) * size + 2.0 ** -8 * np.abs(ref) + 1e-30
+            tol = ((2 * 2.0 ** -11 + 2 * d + 2.0 ** -20) * size + len(kv) * 2.0 ** -25 * np.abs(kv[:, :512]).max()
+                   + 2.0 ** -8 * np.abs(ref) + 1e-30)
             bad = np.abs(o[t] - ref) / tol
             assert bad.max() <= 1, (t, bad.max())
             assert np.abs(e[t] - (m + np.log(z))[:, 0]).max() <= LSE_BF16_ATOL + d
             err2 += ((o[t] - ref) ** 2).sum()
             ref2 += (ref ** 2).sum()
-        assert err2 <= 2.0 ** -14 * ref2, math.sqrt(err2 / ref2)
+            if unrounded:
+                w = np.exp(SM * (q @ raw.T) - m)
+                raw2 += ((o[t] - w @ raw[:, :512] / w.sum(1, keepdims=True)) ** 2).sum()
+        assert err2 <= 2.0 ** -16 * ref2, math.sqrt(err2 / ref2)
+        assert raw2 <= 2.0 ** -16 * ref2, math.sqrt(raw2 / ref2)
 
 
 # ---- refusals (no GPU) ------------------------------------------------------------------
@@ -173,7 +188,7 @@ def test_matches_the_formula(dsa, lens, prefix, h):
     b = Batch(dsa, lens, prefix, h, seed=len(lens) + prefix)
     out, lse = b.call(dsa)
     assert dsa.device_status() == 0
-    b.check(out, lse)
+    b.check(out, lse, unrounded=True)
 
 
 @pytest.mark.gpu
@@ -335,6 +350,8 @@ def test_agrees_with_the_sparse_attention_over_every_position(dsa):
     ref_lse = torch.empty(2, 128, device="cuda")
     ref, _ = dsa.sparse_attn(b.q.cuda(), b.cache, full.cuda(), b.lens.cuda(), b.q_seq.cuda(), idx.cuda(), SM,
                              out_lse=ref_lse)
-    # each within 3 2^-8 of sizes around sum p |v| < 1 of the same reference
-    assert float((out.float() - ref.float()).abs().max()) <= 2 * 3 * 2.0 ** -8
-    assert float((lse - ref_lse).abs().max()) <= 2 * LSE_BF16_ATOL
+    # the sparse path's own gates (its latent rows are rounded to bf16: up to sm_scale sum|q kv| 2^-8,
+    # at most some 0.1 for these rows, in a logit)
+    assert float((out.float() - ref.float()).abs().max()) <= 2e-2
+    assert float((out.float() - ref.float()).abs().mean()) <= 2e-3
+    assert float((lse - ref_lse).abs().max()) <= 0.1
