@@ -303,16 +303,22 @@ expand_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
 }
 
 // ---- attend ----------------------------------------------------------------------------------
+// A bounded wait (as mbar_wait) in two parts: one attempt in line, the rest out of line, so
+// that the warps' loops, two dozen waits between them, stay within the instruction cache.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort, unsigned* status) {
+  return tc::mbar_wait(bar, parity, abort, status);
+}
+
 // fp16 MMAs with operand descriptors given by their low word (address and leading offset); the
 // high word is the same for every operand here: 8-row groups 1024 bytes apart, 128-byte swizzle.
 // One elected lane of the converged warp issues (`leader`, found once).
 #define DSA_DESC_HI "0x40004040"
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 static_assert(kDescHi == 0x40004040u, "descriptor high word");
-// (a shared address carries the CTA's rank in the cluster above its 18 bits)
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
-  return ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16;
-}
+// Dynamic shared memory starts behind the block's reserved 1 KB (the kernel checks it), so the
+// descriptors are constants of the code.
+constexpr uint32_t kSmemBase = 1024;
+constexpr uint32_t desc_lo(uint32_t off, uint32_t lead) { return (kSmemBase + off) >> 4 | (lead >> 4) << 16; }
 template <bool ACC>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t leader) {
   asm volatile(
@@ -375,7 +381,7 @@ __device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t ba
 
 // S = Q K^T of 64-dim block KB of a tile (four K-steps of 16 dims), its rows at descriptor k_lo.
 template <int KB, bool FIRST>
-__device__ __forceinline__ void qk_block(uint32_t q_lo, uint32_t k_lo, uint32_t leader) {
+__device__ __forceinline__ void qk_block(uint32_t k_lo, uint32_t leader) {
   constexpr uint32_t id = idesc_f16(kTile, false);
   if constexpr (KB < kQTmemBlocks) {
     mma_ts<!FIRST>(kColS, kColQ + 32 * KB, k_lo, id, leader);
@@ -383,62 +389,60 @@ __device__ __forceinline__ void qk_block(uint32_t q_lo, uint32_t k_lo, uint32_t 
     mma_ts<true>(kColS, kColQ + 32 * KB + 16, k_lo + 4, id, leader);
     mma_ts<true>(kColS, kColQ + 32 * KB + 24, k_lo + 6, id, leader);
   } else {
-    constexpr uint32_t off = (KB - kQTmemBlocks) * (kQBlock >> 4);
-    mma_ss<!FIRST>(kColS, q_lo + off, k_lo, id, leader);
-    mma_ss<true>(kColS, q_lo + off + 2, k_lo + 2, id, leader);
-    mma_ss<true>(kColS, q_lo + off + 4, k_lo + 4, id, leader);
-    mma_ss<true>(kColS, q_lo + off + 6, k_lo + 6, id, leader);
+    constexpr uint32_t q = desc_lo(kOffQ + (KB - kQTmemBlocks) * kQBlock, 16);
+    mma_ss<!FIRST>(kColS, q, k_lo, id, leader);
+    mma_ss<true>(kColS, q + 2, k_lo + 2, id, leader);
+    mma_ss<true>(kColS, q + 4, k_lo + 4, id, leader);
+    mma_ss<true>(kColS, q + 6, k_lo + 6, id, leader);
   }
 }
 // O (+)= P V of one tile: four K-steps of 16 positions, 256 value columns
 template <bool ACC>
-__device__ __forceinline__ void pv_tile(uint32_t p_addr, uint32_t v_addr, uint32_t leader) {
+__device__ __forceinline__ void pv_tile(uint32_t p_lo, uint32_t v_lo, uint32_t leader) {
   constexpr uint32_t id = idesc_f16(kHalfV, true);
-  const uint32_t p = desc_lo(p_addr, 16), v = desc_lo(v_addr, kBlock);
-  mma_ss<ACC>(kColO, p, v, id, leader);
-  mma_ss<true>(kColO, p + 2, v + (2048 >> 4), id, leader);
-  mma_ss<true>(kColO, p + 4, v + 2 * (2048 >> 4), id, leader);
-  mma_ss<true>(kColO, p + 6, v + 3 * (2048 >> 4), id, leader);
+  mma_ss<ACC>(kColO, p_lo, v_lo, id, leader);
+  mma_ss<true>(kColO, p_lo + 2, v_lo + (2048 >> 4), id, leader);
+  mma_ss<true>(kColO, p_lo + 4, v_lo + 2 * (2048 >> 4), id, leader);
+  mma_ss<true>(kColO, p_lo + 6, v_lo + 3 * (2048 >> 4), id, leader);
 }
 
 // The Q K^T warp of CTA C: the own tiles' value blocks (dims 256 C ..) first, the other five
 // blocks as they come.
 template <int C, typename Wait>
-__device__ __forceinline__ void qk_loop(PairCtl& ctl, uint32_t smem0, int n_own, Wait wait_warp) {
+__device__ __forceinline__ void qk_loop(PairCtl& ctl, int n_own, Wait wait_warp) {
   const uint32_t leader = elect_leader();
-  const uint32_t q_lo = desc_lo(smem0 + kOffQ, 16);
-  const uint32_t v_lo = desc_lo(smem0 + kOffVOwn, 16), l_lo = desc_lo(smem0 + kOffLoose, 16);
-  constexpr uint32_t kStep = kBlock >> 4;
+  constexpr uint32_t kStep = kBlock >> 4, v0 = desc_lo(kOffVOwn, 16), v1 = v0 + 4 * kStep, lo = desc_lo(kOffLoose, 16);
+#pragma unroll 1
   for (int i = 0; i < n_own; ++i) {
     const int b = i & 1;
     if (!wait_warp(&ctl.s_free, i + 1) || !wait_warp(&ctl.vown_full[b], i >> 1)) return;
     tc::fence_after_sync();
     if (b == 0) {
-      qk_block<4 * C, true>(q_lo, v_lo, leader);
-      qk_block<4 * C + 1, false>(q_lo, v_lo + kStep, leader);
-      qk_block<4 * C + 2, false>(q_lo, v_lo + 2 * kStep, leader);
-      qk_block<4 * C + 3, false>(q_lo, v_lo + 3 * kStep, leader);
+      qk_block<4 * C, true>(v0, leader);
+      qk_block<4 * C + 1, false>(v0 + kStep, leader);
+      qk_block<4 * C + 2, false>(v0 + 2 * kStep, leader);
+      qk_block<4 * C + 3, false>(v0 + 3 * kStep, leader);
     } else {
-      qk_block<4 * C, true>(q_lo, v_lo + 4 * kStep, leader);
-      qk_block<4 * C + 1, false>(q_lo, v_lo + 5 * kStep, leader);
-      qk_block<4 * C + 2, false>(q_lo, v_lo + 6 * kStep, leader);
-      qk_block<4 * C + 3, false>(q_lo, v_lo + 7 * kStep, leader);
+      qk_block<4 * C, true>(v1, leader);
+      qk_block<4 * C + 1, false>(v1 + kStep, leader);
+      qk_block<4 * C + 2, false>(v1 + 2 * kStep, leader);
+      qk_block<4 * C + 3, false>(v1 + 3 * kStep, leader);
     }
     constexpr int L = 4 * (1 - C);
     if (!wait_warp(&ctl.loose_full[0], i)) return;
-    qk_block<L, false>(q_lo, l_lo, leader);
+    qk_block<L, false>(lo, leader);
     commit_leader(&ctl.loose_empty[0], leader);
     if (!wait_warp(&ctl.loose_full[1], i)) return;
-    qk_block<L + 1, false>(q_lo, l_lo + kStep, leader);
+    qk_block<L + 1, false>(lo + kStep, leader);
     commit_leader(&ctl.loose_empty[1], leader);
     if (!wait_warp(&ctl.loose_full[2], i)) return;
-    qk_block<L + 2, false>(q_lo, l_lo + 2 * kStep, leader);
+    qk_block<L + 2, false>(lo + 2 * kStep, leader);
     commit_leader(&ctl.loose_empty[2], leader);
     if (!wait_warp(&ctl.loose_full[3], i)) return;
-    qk_block<L + 3, false>(q_lo, l_lo + 3 * kStep, leader);
+    qk_block<L + 3, false>(lo + 3 * kStep, leader);
     commit_leader(&ctl.loose_empty[3], leader);
     if (!wait_warp(&ctl.loose_full[4], i)) return;
-    qk_block<8, false>(q_lo, l_lo + 4 * kStep, leader);
+    qk_block<8, false>(lo + 4 * kStep, leader);
     commit_leader(&ctl.loose_empty[4], leader);
     commit_leader(&ctl.s_full, leader);
   }
@@ -499,8 +503,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
     return;
   }
   const int n_own = (nt - c + 1) / 2, n_peer = nt - n_own;  // own tile i: 2 i + c; peer tile i: 2 i + peer
-  const uint32_t smem0 = smem_u32(smem);
-  if (smem0 & 1023u) {  // (the same in both CTAs)
+  // (the CTA's rank in the cluster stands above a shared address's 24 bits)
+  if ((smem_u32(smem) & 0xFFFFFFu) != kSmemBase) {  // (the same in both CTAs)
     if (tid == 0) flag(a.status, DSA_STATUS_INTERNAL);
     return;
   }
@@ -545,10 +549,12 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
   tc::fence_after_sync();
   volatile int* abort = &ctl.abort;
   // (bounded) wait of one thread, and of a converged warp: there the lanes agree on the outcome
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return tc::mbar_wait(bar, parity & 1u, abort, a.status); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return tc::mbar_try_wait(bar, parity & 1u) || wait_on(bar, parity & 1u, &ctl.abort, a.status);
+  };
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = wait(bar, parity);
-    return __all_sync(0xffffffffu, ok) != 0;
+    if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity & 1u))) return true;
+    return __all_sync(0xffffffffu, wait_on(bar, parity & 1u, &ctl.abort, a.status)) != 0;
   };
 
   // softmax threads: their row's state, kept from the loop to the output
@@ -559,12 +565,14 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
     if (lane == 0) {
       tc::prefetch_tmap(&kvmap);
       bool ok = true;
+#pragma unroll 1
       for (int i = 0; i < n_own && ok; ++i) {
         const int b = i & 1, y = (tile_base + tile0 + 2 * i + c) * kTile;
         if (!wait(&ctl.vown_empty[b], (i >> 1) + 1)) break;
         tc::mbar_arrive_expect_tx(&ctl.vown_full[b], 4 * kBlock);
         for (int k = 0; k < 4; ++k)
           tc::tma_load_3d(smem + kOffVOwn + (4 * b + k) * kBlock, &kvmap, 64 * (4 * c + k), y, 0, &ctl.vown_full[b]);
+#pragma unroll 1
         for (int k = 0; k < kLoose; ++k) {
           ok = wait(&ctl.loose_empty[k], i + 1);
           if (!ok) break;
@@ -579,20 +587,23 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
     // ---------------- Q K^T ----------------
     if (wait_warp(&ctl.q_ready, 0)) {
       tc::fence_after_sync();
-      if (c == 0) qk_loop<0>(ctl, smem0, n_own, wait_warp);
-      else qk_loop<1>(ctl, smem0, n_own, wait_warp);
+      if (c == 0) qk_loop<0>(ctl, n_own, wait_warp);
+      else qk_loop<1>(ctl, n_own, wait_warp);
     }
     __syncwarp();
   } else if (warp == 2) {
     // ---------------- P V: this CTA's value half, over own and peer tiles in turn ----------------
     const uint32_t leader = elect_leader();
+    constexpr uint32_t p_own = desc_lo(kOffPOwn, 16), p_in = desc_lo(kOffPIn, 16);
+    constexpr uint32_t v_own = desc_lo(kOffVOwn, kBlock), v_peer = desc_lo(kOffVPeer, kBlock);
+#pragma unroll 1
     for (int i = 0; i < n_own || i < n_peer; ++i) {
       if (i < n_own) {
         if (!wait_warp(&ctl.p_full, i)) break;
         tc::fence_after_sync();
-        if (i == 0) pv_tile<false>(smem0 + kOffPOwn, smem0 + kOffVOwn, leader);
-        else if (i & 1) pv_tile<true>(smem0 + kOffPOwn, smem0 + kOffVOwn + 4 * kBlock, leader);
-        else pv_tile<true>(smem0 + kOffPOwn, smem0 + kOffVOwn, leader);
+        if (i == 0) pv_tile<false>(p_own, v_own, leader);
+        else if (i & 1) pv_tile<true>(p_own, v_own + 4 * (kBlock >> 4), leader);
+        else pv_tile<true>(p_own, v_own, leader);
         commit_leader(&ctl.vown_empty[i & 1], leader);
         commit_leader(&ctl.p_empty, leader);
       }
@@ -601,8 +612,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
         if (leader) tc::mbar_arrive_expect_tx(&ctl.pin_full, kPMsg);  // the next weights
         __syncwarp();
         tc::fence_after_sync();
-        if (i == 0 && n_own == 0) pv_tile<false>(smem0 + kOffPIn, smem0 + kOffVPeer, leader);
-        else pv_tile<true>(smem0 + kOffPIn, smem0 + kOffVPeer, leader);
+        if (i == 0 && n_own == 0) pv_tile<false>(p_in, v_peer, leader);
+        else pv_tile<true>(p_in, v_peer, leader);
         commit_leader(&ctl.vpeer_empty, leader);
         commit_leader_to(&ctl.p_empty, static_cast<uint16_t>(1u << peer), leader);
       }
@@ -613,6 +624,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
     // ---------------- own weights to the peer; value blocks of the peer's tiles ----------------
     if (lane == 0) {
       const uint32_t dst = dsmem_addr(smem + kOffPIn, peer), bar = dsmem_addr(&ctl.pin_full, peer);
+#pragma unroll 1
       for (int i = 0; i < n_own || i < n_peer; ++i) {
         if (i < n_peer) {
           if (!wait(&ctl.vpeer_empty, i + 1)) break;
@@ -721,6 +733,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
     const float* in_r = reinterpret_cast<const float*>(smem + kOffPIn + kPBytes);
     // (after a wait that ran out these warps still go through every step, each wait returning at
     // once: the named barriers need both of a row's warps)
+#pragma unroll 1
     for (int i = 0; i < n_own || i < n_peer; ++i) {
       if (i < n_own) {
         const int tile = tile0 + 2 * i + c;
