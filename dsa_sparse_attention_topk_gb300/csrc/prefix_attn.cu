@@ -76,30 +76,44 @@ constexpr uint32_t kPMsg = kPBytes + kRows * 4;  // with the rows' references
 constexpr uint32_t kPStride = (kPMsg + 1023) / 1024 * 1024;
 constexpr float kHeadroom = 14.0f;            // powers of two a weight may reach
 
+// Shared memory.  G = 1: the value blocks (64 positions x 64 dims) of two own tiles and one peer
+// tile, and the own tile's other five blocks.  G = 2: each CTA of an MMA pair holds half of every
+// B operand: of two own tiles 32 positions x 576 dims for Q K^T, and of two own and two peer tiles
+// 64 positions x 128 dims for P V.
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffPOwn = kOffQ + kQSmemBlocks * kQBlock;
 constexpr uint32_t kOffPIn = kOffPOwn + kPStride;
-constexpr uint32_t kOffVOwn = kOffPIn + kPStride;
-constexpr uint32_t kOffVPeer = kOffVOwn + 8 * kBlock;
-constexpr uint32_t kOffLoose = kOffVPeer + 4 * kBlock;
-constexpr uint32_t kOffCtl = kOffLoose + kLoose * kBlock;
+constexpr uint32_t kOffKv = kOffPIn + kPStride;
+constexpr int kHalfK = 9 * kBlock / 2;        // G = 2: half a tile's rows
+template <int G> struct Layout;
+template <> struct Layout<1> {
+  static constexpr int kVBytes = 4 * kBlock, kPeerBufs = 1;
+  static constexpr uint32_t vown = kOffKv, vpeer = vown + 2 * kVBytes, k = vpeer + kVBytes, ctl = k + kLoose * kBlock;
+};
+template <> struct Layout<2> {
+  static constexpr int kVBytes = 2 * kBlock, kPeerBufs = 2;
+  static constexpr uint32_t vown = kOffKv, vpeer = vown + 2 * kVBytes, k = vpeer + 2 * kVBytes, ctl = k + 2 * kHalfK;
+};
+static_assert(Layout<1>::ctl == Layout<2>::ctl, "one control offset");
+constexpr uint32_t kOffCtl = Layout<1>::ctl;
 
 struct PairCtl {
   uint64_t q_ready;                            // the query is in tensor and shared memory
-  uint64_t loose_full[kLoose], loose_empty[kLoose];
+  uint64_t k_full[kLoose], k_empty[kLoose];    // G = 1: the five loose blocks; G = 2: two tiles' halves
   uint64_t vown_full[2], vown_empty[2];        // full; read by the own P V
-  uint64_t vpeer_full, vpeer_empty;
+  uint64_t vpeer_full[2], vpeer_empty[2];
   uint64_t s_full, s_free;                     // logits written / read into registers
-  uint64_t p_full;                             // own weights in shared memory, O at their reference
+  uint64_t p_mine;                             // this CTA's weights are in shared memory
+  uint64_t p_full;                             // every row's weights are, and O is at their reference
   uint64_t p_empty;                            // own weights read: by the own P V and by the peer's (of its copy)
   uint64_t pin_full;                           // the peer's weights have landed
   uint64_t pin_go;                             // they and O are at one reference
   uint64_t o_done;
-  uint64_t r_full;                             // CTA 1: the first references have landed
+  uint64_t r_full;                             // parity 1: the first references have landed
   uint64_t fin_full;                           // the peer's sums have landed
   uint32_t tmem_base;
   int abort;
-  float r[kRows];                              // CTA 1: from CTA 0
+  float r[kRows];                              // parity 1: from parity 0
   float fin[kRows];                            // the peer's sum of weights
   float part[2][2][kRows];                     // tile maxima of a row's two threads, by tile parity
 };
@@ -120,6 +134,7 @@ struct PrefixPlan {
   int tiles_p, tiles_t;      // tiles of the prefix, and of the longest possible tail
   int sp, st;                // splits of the prefix and of each tail
   int mt;                    // 128-row tiles of the flattened rows
+  int g;                     // of them in one item: MMAs of one CTA or of a pair
   int64_t rows_kv;           // rows of the expanded cache
   size_t off_info, off_o, off_ml, bytes;
 };
@@ -133,35 +148,42 @@ struct PrefixWs {
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-// Splits: the plan of least estimated time.  An item of n tiles takes about 5 + 0.65 n us
-// on one of the n_sm / 2 CTA pairs; a further split costs every row its partial output, once
-// written and once read.
+// The plan of least estimated time: MMAs of one CTA (128 rows an item, two CTAs) or of CTA
+// pairs (256 rows, four CTAs), and the splits.  An item of n tiles takes about fix + per n us on
+// one of the clusters that fit at once; a further split costs every row its partial output,
+// once written and once read.  Pairs halve what each tile costs in shared memory, but few items
+// or tails, whose rows share no tiles, leave half of a pair idle.
 PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, int n_sm) {
   PrefixPlan p{};
   p.tiles_p = (prefix_len + kTile - 1) / kTile;
   p.tiles_t = (max_ctx - prefix_len + kTile - 1) / kTile;
   p.mt = static_cast<int>((static_cast<int64_t>(n_q) * h_s + kRows - 1) / kRows);
-  const int pairs = std::max(1, n_sm / 2);
-  const double fix = 5.0, per = 0.65;
   const double join = 2048.0 * n_q * h_s / 5.0e6;  // us a split
   double best = 1e30;
-  for (int sp = p.tiles_p ? 1 : 0; sp <= std::min(p.tiles_p, 48); ++sp) {
-    for (int st = p.tiles_t ? 1 : 0; st <= std::min(p.tiles_t, 16); st = st ? 2 * st : 1) {
-      const double lp = sp ? fix + per * ((p.tiles_p + sp - 1) / sp) : 0.0;
-      const double lt = st ? fix + per * ((p.tiles_t + st - 1) / st) : 0.0;
-      const double np = static_cast<double>(p.mt) * sp, nt = static_cast<double>(n_q) * st;
-      const double waves = static_cast<double>(static_cast<int64_t>((np + pairs - 1) / pairs));
-      // the tails are counted half full: their lengths are known to the device alone
-      const double total = (np * lp + nt * (fix + 0.5 * (lt - fix))) / pairs;
-      const double t = std::max({waves * lp, total + (st ? 0.5 * lt : 0.0), lt}) + (sp + st > 1 ? join * (sp + st) + 3.0 : 0.0);
-      if (t < best) {
-        best = t;
-        p.sp = sp;
-        p.st = st;
+  for (int g = 1; g <= 2; ++g) {
+    if (g == 2 && (p.mt < 2 || !p.tiles_p)) break;
+    // (152 SMs hold 76 clusters of two CTAs of this size, 36 of four)
+    const int fit = std::max(1, g == 1 ? n_sm / 2 : n_sm / 4 - n_sm / 76);
+    const double fix = 6.0, per = g == 1 ? 1.05 : 0.75;
+    for (int sp = p.tiles_p ? 1 : 0; sp <= std::min(p.tiles_p, 48); ++sp) {
+      for (int st = p.tiles_t ? 1 : 0; st <= std::min(p.tiles_t, 16); st = st ? 2 * st : 1) {
+        const double lp = sp ? fix + per * ((p.tiles_p + sp - 1) / sp) : 0.0;
+        const double lt = st ? fix + per * ((p.tiles_t + st - 1) / st) : 0.0;
+        const double np = static_cast<double>((p.mt + g - 1) / g) * sp, nt = static_cast<double>(n_q) * st;
+        const double waves = static_cast<double>(static_cast<int64_t>((np + fit - 1) / fit));
+        // the tails are counted half full: their lengths are known to the device alone
+        const double total = (np * lp + nt * (fix + 0.5 * (lt - fix))) / fit;
+        const double t = std::max({waves * lp, total + (st ? 0.5 * lt : 0.0), lt}) + (sp + st > 1 ? join * (sp + st) + 3.0 : 0.0);
+        if (t < best) {
+          best = t;
+          p.g = g;
+          p.sp = sp;
+          p.st = st;
+        }
+        if (!st) break;
       }
-      if (!st) break;
+      if (!p.tiles_p) break;
     }
-    if (!p.tiles_p) break;
   }
   p.rows_kv = static_cast<int64_t>(p.tiles_p) * kTile + static_cast<int64_t>(n_seq) * p.tiles_t * kTile;
   const size_t parts = p.sp + p.st > 1 ? static_cast<size_t>(n_q) * h_s * (p.sp + p.st) : 0;
@@ -304,60 +326,113 @@ expand_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
 
 // ---- attend ----------------------------------------------------------------------------------
 // A bounded wait (as mbar_wait) in two parts: one attempt in line, the rest out of line, so
-// that the warps' loops, two dozen waits between them, stay within the instruction cache.
-__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort, unsigned* status) {
-  return tc::mbar_wait(bar, parity, abort, status);
+// that the warps' loops, two dozen waits between them, stay within the instruction cache (with the
+// whole wait in line a third of all warp cycles went into fetching instructions).
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* status) {
+  const uint64_t t0 = tc::global_ns();
+  for (uint32_t it = 0;; ++it) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if ((it & 15u) == 15u) {
+      if (*abort) return false;
+      if (tc::global_ns() - t0 > tc::kWaitLimitNs) {
+        *abort = 1;
+        flag(status, DSA_STATUS_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+// Arrive on the same barrier of the cluster's CTA `rank`.  What the arrival announces is read by
+// tensor cores alone, behind the writer's proxy fence or tcgen05 fence, so it needs no release at
+// cluster scope (which took some 1500 cycles here).
+__device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(dsmem_addr(bar, rank)) : "memory");
+}
+
+// tcgen05 for one CTA (G = 1) or for the pair of CTAs 2 i, 2 i + 1 (G = 2).  The pair's even CTA
+// issues: an MMA then has 256 rows, 128 in each CTA's tensor memory, and each CTA's shared memory
+// holds half of B.
+template <int G>
+__device__ __forceinline__ void tmem_alloc_all(uint32_t* slot) {
+  if constexpr (G == 1) {
+    tc::tmem_alloc(slot, 512);
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int G>
+__device__ __forceinline__ void tmem_dealloc_all(uint32_t base) {
+  if constexpr (G == 1) tc::tmem_dealloc(base, 512);
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(base) : "memory");
+}
+// A box of the expanded rows; in a pair it counts on the even CTA's barrier (the same offset
+// there: bit 24 of a shared address is the lowest of the CTA's rank).
+template <int G>
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  if constexpr (G == 1) {
+    tc::tma_load_3d(dst, map, x, y, 0, bar);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(0),
+           "r"(smem_u32(bar) & 0xFEFFFFFFu)
+        : "memory");
+  }
 }
 
 // fp16 MMAs with operand descriptors given by their low word (address and leading offset); the
 // high word is the same for every operand here: 8-row groups 1024 bytes apart, 128-byte swizzle.
-// One elected lane of the converged warp issues (`leader`, found once).
+// Dynamic shared memory starts behind the block's reserved 1 KB (the kernel checks it), so the
+// descriptors are constants of the code.  One elected lane of the converged warp issues
+// (`leader`, found once).
 #define DSA_DESC_HI "0x40004040"
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 static_assert(kDescHi == 0x40004040u, "descriptor high word");
-// Dynamic shared memory starts behind the block's reserved 1 KB (the kernel checks it), so the
-// descriptors are constants of the code.
 constexpr uint32_t kSmemBase = 1024;
 constexpr uint32_t desc_lo(uint32_t off, uint32_t lead) { return (kSmemBase + off) >> 4 | (lead >> 4) << 16; }
-template <bool ACC>
+template <int G, bool ACC>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t leader) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b64 b;\n setp.ne.b32 e, %4, 0;\n setp.ne.b32 p, %5, 0;\n"
-      "mov.b64 b, {%2, " DSA_DESC_HI "};\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}"
-      :: "r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(leader), "n"(ACC ? 1 : 0) : "memory");
+#define DSA_MMA_TS(group)                                                                             \
+  asm volatile(                                                                                       \
+      "{\n .reg .pred p, e;\n .reg .b64 b;\n setp.ne.b32 e, %4, 0;\n setp.ne.b32 p, %5, 0;\n"         \
+      "mov.b64 b, {%2, " DSA_DESC_HI "};\n"                                                           \
+      "@e tcgen05.mma.cta_group::" group ".kind::f16 [%0], [%1], b, %3, p;\n}"                        \
+      :: "r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(leader), "n"(ACC ? 1 : 0) : "memory")
+  if constexpr (G == 1) DSA_MMA_TS("1"); else DSA_MMA_TS("2");
+#undef DSA_MMA_TS
 }
-template <bool ACC>
+template <int G, bool ACC>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t leader) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n setp.ne.b32 e, %4, 0;\n setp.ne.b32 p, %5, 0;\n"
-      "mov.b64 a, {%1, " DSA_DESC_HI "};\n mov.b64 b, {%2, " DSA_DESC_HI "};\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}"
-      :: "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(leader), "n"(ACC ? 1 : 0) : "memory");
+#define DSA_MMA_SS(group)                                                                             \
+  asm volatile(                                                                                       \
+      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n setp.ne.b32 e, %4, 0;\n setp.ne.b32 p, %5, 0;\n"      \
+      "mov.b64 a, {%1, " DSA_DESC_HI "};\n mov.b64 b, {%2, " DSA_DESC_HI "};\n"                       \
+      "@e tcgen05.mma.cta_group::" group ".kind::f16 [%0], a, b, %3, p;\n}"                           \
+      :: "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(leader), "n"(ACC ? 1 : 0) : "memory")
+  if constexpr (G == 1) DSA_MMA_SS("1"); else DSA_MMA_SS("2");
+#undef DSA_MMA_SS
 }
 __device__ __forceinline__ uint32_t elect_leader() {
   uint32_t r;
   asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}" : "=r"(r));
   return r;
 }
-// arrive on a barrier once the MMAs the leader issued have completed: of this CTA, or
-// (multicast) of the CTAs in the mask
-__device__ __forceinline__ void commit_leader(uint64_t* bar, uint32_t leader) {
-  asm volatile(
-      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
-      :: "r"(smem_u32(bar)), "r"(leader) : "memory");
+// arrive on a barrier of the CTAs in the mask once the MMAs the leader issued have completed
+template <int G>
+__device__ __forceinline__ void commit_to(uint64_t* bar, uint16_t mask, uint32_t leader) {
+#define DSA_COMMIT(group)                                                                                            \
+  asm volatile(                                                                                                      \
+      "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"                                                                  \
+      "@e tcgen05.commit.cta_group::" group ".mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" \
+      :: "r"(smem_u32(bar)), "h"(mask), "r"(leader) : "memory")
+  if constexpr (G == 1) DSA_COMMIT("1"); else DSA_COMMIT("2");
+#undef DSA_COMMIT
 }
-__device__ __forceinline__ void commit_leader_to(uint64_t* bar, uint16_t mask, uint32_t leader) {
-  asm volatile(
-      "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}"
-      :: "r"(smem_u32(bar)), "h"(mask), "r"(leader) : "memory");
-}
-// fp16 A and B, fp32 accumulator, M = 128
-__host__ __device__ constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
+// fp16 A and B, fp32 accumulator, M = 128 G
+__host__ __device__ constexpr uint32_t idesc_f16(int g, int n, bool b_mn_major) {
   return (1u << 4) | (static_cast<uint32_t>(b_mn_major) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
-         (static_cast<uint32_t>(128 >> 4) << 24);
+         (static_cast<uint32_t>(128 * g >> 4) << 24);
 }
 __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -380,107 +455,147 @@ __device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t ba
 }
 
 // S = Q K^T of 64-dim block KB of a tile (four K-steps of 16 dims), its rows at descriptor k_lo.
-template <int KB, bool FIRST>
+template <int G, int KB, bool FIRST>
 __device__ __forceinline__ void qk_block(uint32_t k_lo, uint32_t leader) {
-  constexpr uint32_t id = idesc_f16(kTile, false);
+  constexpr uint32_t id = idesc_f16(G, kTile, false);
   if constexpr (KB < kQTmemBlocks) {
-    mma_ts<!FIRST>(kColS, kColQ + 32 * KB, k_lo, id, leader);
-    mma_ts<true>(kColS, kColQ + 32 * KB + 8, k_lo + 2, id, leader);
-    mma_ts<true>(kColS, kColQ + 32 * KB + 16, k_lo + 4, id, leader);
-    mma_ts<true>(kColS, kColQ + 32 * KB + 24, k_lo + 6, id, leader);
+    mma_ts<G, !FIRST>(kColS, kColQ + 32 * KB, k_lo, id, leader);
+    mma_ts<G, true>(kColS, kColQ + 32 * KB + 8, k_lo + 2, id, leader);
+    mma_ts<G, true>(kColS, kColQ + 32 * KB + 16, k_lo + 4, id, leader);
+    mma_ts<G, true>(kColS, kColQ + 32 * KB + 24, k_lo + 6, id, leader);
   } else {
     constexpr uint32_t q = desc_lo(kOffQ + (KB - kQTmemBlocks) * kQBlock, 16);
-    mma_ss<!FIRST>(kColS, q, k_lo, id, leader);
-    mma_ss<true>(kColS, q + 2, k_lo + 2, id, leader);
-    mma_ss<true>(kColS, q + 4, k_lo + 4, id, leader);
-    mma_ss<true>(kColS, q + 6, k_lo + 6, id, leader);
+    mma_ss<G, !FIRST>(kColS, q, k_lo, id, leader);
+    mma_ss<G, true>(kColS, q + 2, k_lo + 2, id, leader);
+    mma_ss<G, true>(kColS, q + 4, k_lo + 4, id, leader);
+    mma_ss<G, true>(kColS, q + 6, k_lo + 6, id, leader);
   }
 }
 // O (+)= P V of one tile: four K-steps of 16 positions, 256 value columns
-template <bool ACC>
+template <int G, bool ACC>
 __device__ __forceinline__ void pv_tile(uint32_t p_lo, uint32_t v_lo, uint32_t leader) {
-  constexpr uint32_t id = idesc_f16(kHalfV, true);
-  mma_ss<ACC>(kColO, p_lo, v_lo, id, leader);
-  mma_ss<true>(kColO, p_lo + 2, v_lo + (2048 >> 4), id, leader);
-  mma_ss<true>(kColO, p_lo + 4, v_lo + 2 * (2048 >> 4), id, leader);
-  mma_ss<true>(kColO, p_lo + 6, v_lo + 3 * (2048 >> 4), id, leader);
+  constexpr uint32_t id = idesc_f16(G, kHalfV, true);
+  mma_ss<G, ACC>(kColO, p_lo, v_lo, id, leader);
+  mma_ss<G, true>(kColO, p_lo + 2, v_lo + (2048 >> 4), id, leader);
+  mma_ss<G, true>(kColO, p_lo + 4, v_lo + 2 * (2048 >> 4), id, leader);
+  mma_ss<G, true>(kColO, p_lo + 6, v_lo + 3 * (2048 >> 4), id, leader);
 }
 
-// The Q K^T warp of CTA C: the own tiles' value blocks (dims 256 C ..) first, the other five
-// blocks as they come.
+// The Q K^T warp, G = 1, of CTA C: the own tiles' value blocks (dims 256 C ..) first, the other
+// five blocks as they come.
 template <int C, typename Wait>
-__device__ __forceinline__ void qk_loop(PairCtl& ctl, int n_own, Wait wait_warp) {
+__device__ __forceinline__ void qk_loop_single(PairCtl& ctl, int n_own, Wait wait_warp) {
   const uint32_t leader = elect_leader();
-  constexpr uint32_t kStep = kBlock >> 4, v0 = desc_lo(kOffVOwn, 16), v1 = v0 + 4 * kStep, lo = desc_lo(kOffLoose, 16);
+  constexpr uint32_t kStep = kBlock >> 4, v0 = desc_lo(Layout<1>::vown, 16), v1 = v0 + 4 * kStep;
+  constexpr uint32_t lo = desc_lo(Layout<1>::k, 16);
+  constexpr uint16_t me = 1u << C;
 #pragma unroll 1
   for (int i = 0; i < n_own; ++i) {
     const int b = i & 1;
     if (!wait_warp(&ctl.s_free, i + 1) || !wait_warp(&ctl.vown_full[b], i >> 1)) return;
     tc::fence_after_sync();
     if (b == 0) {
-      qk_block<4 * C, true>(v0, leader);
-      qk_block<4 * C + 1, false>(v0 + kStep, leader);
-      qk_block<4 * C + 2, false>(v0 + 2 * kStep, leader);
-      qk_block<4 * C + 3, false>(v0 + 3 * kStep, leader);
+      qk_block<1, 4 * C, true>(v0, leader);
+      qk_block<1, 4 * C + 1, false>(v0 + kStep, leader);
+      qk_block<1, 4 * C + 2, false>(v0 + 2 * kStep, leader);
+      qk_block<1, 4 * C + 3, false>(v0 + 3 * kStep, leader);
     } else {
-      qk_block<4 * C, true>(v1, leader);
-      qk_block<4 * C + 1, false>(v1 + kStep, leader);
-      qk_block<4 * C + 2, false>(v1 + 2 * kStep, leader);
-      qk_block<4 * C + 3, false>(v1 + 3 * kStep, leader);
+      qk_block<1, 4 * C, true>(v1, leader);
+      qk_block<1, 4 * C + 1, false>(v1 + kStep, leader);
+      qk_block<1, 4 * C + 2, false>(v1 + 2 * kStep, leader);
+      qk_block<1, 4 * C + 3, false>(v1 + 3 * kStep, leader);
     }
     constexpr int L = 4 * (1 - C);
-    if (!wait_warp(&ctl.loose_full[0], i)) return;
-    qk_block<L, false>(lo, leader);
-    commit_leader(&ctl.loose_empty[0], leader);
-    if (!wait_warp(&ctl.loose_full[1], i)) return;
-    qk_block<L + 1, false>(lo + kStep, leader);
-    commit_leader(&ctl.loose_empty[1], leader);
-    if (!wait_warp(&ctl.loose_full[2], i)) return;
-    qk_block<L + 2, false>(lo + 2 * kStep, leader);
-    commit_leader(&ctl.loose_empty[2], leader);
-    if (!wait_warp(&ctl.loose_full[3], i)) return;
-    qk_block<L + 3, false>(lo + 3 * kStep, leader);
-    commit_leader(&ctl.loose_empty[3], leader);
-    if (!wait_warp(&ctl.loose_full[4], i)) return;
-    qk_block<8, false>(lo + 4 * kStep, leader);
-    commit_leader(&ctl.loose_empty[4], leader);
-    commit_leader(&ctl.s_full, leader);
+    if (!wait_warp(&ctl.k_full[0], i)) return;
+    qk_block<1, L, false>(lo, leader);
+    commit_to<1>(&ctl.k_empty[0], me, leader);
+    if (!wait_warp(&ctl.k_full[1], i)) return;
+    qk_block<1, L + 1, false>(lo + kStep, leader);
+    commit_to<1>(&ctl.k_empty[1], me, leader);
+    if (!wait_warp(&ctl.k_full[2], i)) return;
+    qk_block<1, L + 2, false>(lo + 2 * kStep, leader);
+    commit_to<1>(&ctl.k_empty[2], me, leader);
+    if (!wait_warp(&ctl.k_full[3], i)) return;
+    qk_block<1, L + 3, false>(lo + 3 * kStep, leader);
+    commit_to<1>(&ctl.k_empty[3], me, leader);
+    if (!wait_warp(&ctl.k_full[4], i)) return;
+    qk_block<1, 8, false>(lo + 4 * kStep, leader);
+    commit_to<1>(&ctl.k_empty[4], me, leader);
+    commit_to<1>(&ctl.s_full, me, leader);
+  }
+}
+// G = 2: a tile's rows lie together, half in each CTA.
+template <uint32_t K>
+__device__ __forceinline__ void qk_tile_pair(uint32_t leader) {
+  constexpr uint32_t k = desc_lo(K, 16), kStep = kBlock / 2 >> 4;
+  qk_block<2, 0, true>(k, leader);
+  qk_block<2, 1, false>(k + kStep, leader);
+  qk_block<2, 2, false>(k + 2 * kStep, leader);
+  qk_block<2, 3, false>(k + 3 * kStep, leader);
+  qk_block<2, 4, false>(k + 4 * kStep, leader);
+  qk_block<2, 5, false>(k + 5 * kStep, leader);
+  qk_block<2, 6, false>(k + 6 * kStep, leader);
+  qk_block<2, 7, false>(k + 7 * kStep, leader);
+  qk_block<2, 8, false>(k + 8 * kStep, leader);
+}
+template <typename Wait>
+__device__ __forceinline__ void qk_loop_pair(PairCtl& ctl, int n_own, uint16_t pair, Wait wait_warp) {
+  const uint32_t leader = elect_leader();
+#pragma unroll 1
+  for (int i = 0; i < n_own; ++i) {
+    const int b = i & 1;
+    if (!wait_warp(&ctl.k_full[b], i >> 1) || !wait_warp(&ctl.s_free, i + 1)) return;
+    tc::fence_after_sync();
+    if (b == 0) qk_tile_pair<Layout<2>::k>(leader);
+    else qk_tile_pair<Layout<2>::k + kHalfK>(leader);
+    commit_to<2>(&ctl.k_empty[b], pair, leader);
+    commit_to<2>(&ctl.s_full, pair, leader);
   }
 }
 
+template <int G>
 __global__ void __launch_bounds__(kThreads, 1)
-attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
+attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constant__ CUtensorMap half_map, PrefixArgs a,
+              PrefixPlan pl, PrefixWs ws) {
+  using Lay = Layout<G>;
   extern __shared__ __align__(1024) uint8_t smem[];
   PairCtl& ctl = *reinterpret_cast<PairCtl*>(smem + kOffCtl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int c = static_cast<int>(cluster_ctarank()), peer = c ^ 1;
+  // rank = G c + g: c the parity of the own tiles and the half of the value columns, g the CTA's
+  // 128 rows of the item's 128 G.  Its peer has the same rows; the pair's even CTA issues MMAs.
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int c = rank / G, g = rank % G, peer = rank ^ G, other = c ^ 1, chief = G * c;
+  const uint16_t mine = static_cast<uint16_t>(((1 << G) - 1) << (G * c));            // the CTAs of this parity
+  const uint16_t theirs = static_cast<uint16_t>(((1 << G) - 1) << (G * (c ^ 1)));  // and of the other
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- this pair's item: rows row0 .. of the flattened (query row, head), tiles tile0 .. ----
-  const int item = blockIdx.x >> 1;
-  const int n_prefix = pl.sp * pl.mt;
+  // ---- the item: rows row0 .. of the flattened (query row, head), tiles tile0 .. ----
+  const int item = blockIdx.x / (2 * G);
+  const int mt = (pl.mt + G - 1) / G;
+  const int n_prefix = pl.sp * mt;
   const bool tail = item >= n_prefix;
   const int64_t rows_all = static_cast<int64_t>(a.n_q) * a.h_s;
   const int ns = pl.sp + pl.st;
   int64_t row0;
   int n_rows, part, split, tiles, tile_base, first_pos;
   if (!tail) {
-    split = item / pl.mt;
-    row0 = static_cast<int64_t>(item - split * pl.mt) * kRows;
-    n_rows = static_cast<int>(min(static_cast<int64_t>(kRows), rows_all - row0));
+    split = item / mt;
+    row0 = (static_cast<int64_t>(item - split * mt) * G + g) * kRows;
+    n_rows = static_cast<int>(max(min(static_cast<int64_t>(kRows), rows_all - row0), static_cast<int64_t>(0)));
     part = pl.sp;
     tiles = pl.tiles_p;
     tile_base = 0;
     first_pos = 0;
   } else {
+    // (in a pair the second CTA has no rows here: tails of two query rows differ)
     const int k = item - n_prefix;
     split = k / a.n_q;
     const int t = k - split * a.n_q;
     row0 = static_cast<int64_t>(t) * a.h_s;
-    n_rows = a.h_s;
+    n_rows = g == 0 ? a.h_s : 0;
     part = pl.st;
-    const int lim = row_limit(a, t, tid == 0 && c == 0 && split == 0);
+    const int lim = row_limit(a, t, tid == 0 && rank == 0 && split == 0);
     tiles = lim > a.prefix_len ? (lim - a.prefix_len + kTile - 1) / kTile : 0;
     // (a row that sees anything has a sequence in range)
     tile_base = tiles ? pl.tiles_p + a.q_seq[t] * pl.tiles_t : 0;
@@ -489,7 +604,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
   const int tile0 = static_cast<int>(static_cast<int64_t>(split) * tiles / part);
   const int nt = static_cast<int>(static_cast<int64_t>(split + 1) * tiles / part) - tile0;
   const int slot = tail ? pl.sp + split : split;
-  if (nt == 0) {  // both CTAs alike: nothing of this row lies in this split
+  if (nt == 0) {  // all CTAs alike: nothing of these rows lies in this split
     if (c == 0 && ns > 1) {
       for (int m = tid; m < n_rows; m += kThreads)
         ws.ml[(row0 + m) * ns + slot] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
@@ -502,31 +617,32 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
     }
     return;
   }
-  const int n_own = (nt - c + 1) / 2, n_peer = nt - n_own;  // own tile i: 2 i + c; peer tile i: 2 i + peer
+  const int n_own = (nt - c + 1) / 2, n_peer = nt - n_own;  // own tile i: 2 i + c; peer tile i: 2 i + other
   // (the CTA's rank in the cluster stands above a shared address's 24 bits)
-  if ((smem_u32(smem) & 0xFFFFFFu) != kSmemBase) {  // (the same in both CTAs)
+  if ((smem_u32(smem) & 0xFFFFFFu) != kSmemBase) {  // (the same in all CTAs)
     if (tid == 0) flag(a.status, DSA_STATUS_INTERNAL);
     return;
   }
   if (tid == 0) {
     ctl.abort = 0;
-    tc::mbar_init(&ctl.q_ready, kSoftWarps);
+    tc::mbar_init(&ctl.q_ready, G * kSoftWarps);
     for (int k = 0; k < kLoose; ++k) {
-      tc::mbar_init(&ctl.loose_full[k], 1);
-      tc::mbar_init(&ctl.loose_empty[k], 1);
+      tc::mbar_init(&ctl.k_full[k], 1);
+      tc::mbar_init(&ctl.k_empty[k], 1);
     }
     for (int k = 0; k < 2; ++k) {
       tc::mbar_init(&ctl.vown_full[k], 1);
       tc::mbar_init(&ctl.vown_empty[k], 1);
+      tc::mbar_init(&ctl.vpeer_full[k], 1);
+      tc::mbar_init(&ctl.vpeer_empty[k], 1);
     }
-    tc::mbar_init(&ctl.vpeer_full, 1);
-    tc::mbar_init(&ctl.vpeer_empty, 1);
     tc::mbar_init(&ctl.s_full, 1);
-    tc::mbar_init(&ctl.s_free, kSoftWarps);
-    tc::mbar_init(&ctl.p_full, kSoftWarps);
+    tc::mbar_init(&ctl.s_free, G * kSoftWarps);
+    tc::mbar_init(&ctl.p_mine, kSoftWarps);
+    tc::mbar_init(&ctl.p_full, G * kSoftWarps);
     tc::mbar_init(&ctl.p_empty, 2);
     tc::mbar_init(&ctl.pin_full, 1);
-    tc::mbar_init(&ctl.pin_go, kSoftWarps);
+    tc::mbar_init(&ctl.pin_go, G * kSoftWarps);
     tc::mbar_init(&ctl.o_done, 1);
     tc::mbar_init(&ctl.r_full, 1);
     tc::mbar_init(&ctl.fin_full, 1);
@@ -536,17 +652,18 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
     tc::mbar_arrive_expect_tx(&ctl.fin_full, kRows * 4);
     tc::mbar_arrive_expect_tx(&ctl.pin_full, kPMsg);
   }
-  if (warp == 1) tc::tmem_alloc(&ctl.tmem_base, 512);
+  __syncthreads();
+  cluster_sync();  // every CTA's barriers are ready
+  if (warp == 1) tmem_alloc_all<G>(&ctl.tmem_base);
   tc::fence_before_sync();
   __syncthreads();
+  tc::fence_after_sync();
   // all 512 columns are this CTA's, so its addresses start at 0 and are constants below
   if (tid == 0 && ctl.tmem_base != 0) {
     flag(a.status, DSA_STATUS_INTERNAL);
     ctl.abort = 1;
   }
   __syncwarp();
-  cluster_sync();  // the peer's barriers are ready
-  tc::fence_after_sync();
   volatile int* abort = &ctl.abort;
   // (bounded) wait of one thread, and of a converged warp: there the lanes agree on the outcome
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -556,86 +673,115 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
     if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity & 1u))) return true;
     return __all_sync(0xffffffffu, wait_on(bar, parity & 1u, &ctl.abort, a.status)) != 0;
   };
+  // an arrival that the issuing CTA waits for
+  auto tell_chief = [&](uint64_t* bar) {
+    if constexpr (G == 1) tc::mbar_arrive(bar);
+    else arrive_at(bar, chief);
+  };
 
   // softmax threads: their row's state, kept from the loop to the output
   float rho = -INFINITY, l = 0.f;
   int e_top = -1000;
   if (warp == 0) {
-    // ---------------- own tiles: the half of the value blocks this CTA keeps, then the rest ----------------
+    // ---------------- own tiles ----------------
     if (lane == 0) {
-      tc::prefetch_tmap(&kvmap);
+      tc::prefetch_tmap(&tile_map);
+      if constexpr (G == 2) tc::prefetch_tmap(&half_map);
       bool ok = true;
 #pragma unroll 1
       for (int i = 0; i < n_own && ok; ++i) {
         const int b = i & 1, y = (tile_base + tile0 + 2 * i + c) * kTile;
-        if (!wait(&ctl.vown_empty[b], (i >> 1) + 1)) break;
-        tc::mbar_arrive_expect_tx(&ctl.vown_full[b], 4 * kBlock);
-        for (int k = 0; k < 4; ++k)
-          tc::tma_load_3d(smem + kOffVOwn + (4 * b + k) * kBlock, &kvmap, 64 * (4 * c + k), y, 0, &ctl.vown_full[b]);
+        if constexpr (G == 1) {
+          // the half of the value blocks this CTA keeps, then the other blocks
+          if (!wait(&ctl.vown_empty[b], (i >> 1) + 1)) break;
+          tc::mbar_arrive_expect_tx(&ctl.vown_full[b], Lay::kVBytes);
+          for (int k = 0; k < 4; ++k)
+            load_box<G>(smem + Lay::vown + (4 * b + k) * kBlock, &tile_map, 64 * (4 * c + k), y, &ctl.vown_full[b]);
 #pragma unroll 1
-        for (int k = 0; k < kLoose; ++k) {
-          ok = wait(&ctl.loose_empty[k], i + 1);
-          if (!ok) break;
-          tc::mbar_arrive_expect_tx(&ctl.loose_full[k], kBlock);
-          tc::tma_load_3d(smem + kOffLoose + k * kBlock, &kvmap, 64 * (k < 4 ? 4 * peer + k : 8), y, 0,
-                          &ctl.loose_full[k]);
+          for (int k = 0; k < kLoose; ++k) {
+            ok = wait(&ctl.k_empty[k], i + 1);
+            if (!ok) break;
+            tc::mbar_arrive_expect_tx(&ctl.k_full[k], kBlock);
+            load_box<G>(smem + Lay::k + k * kBlock, &tile_map, 64 * (k < 4 ? 4 * other + k : 8), y, &ctl.k_full[k]);
+          }
+        } else {
+          // this CTA's 32 positions for Q K^T, then its 128 value columns
+          if (!wait(&ctl.k_empty[b], (i >> 1) + 1)) break;
+          if (g == 0) tc::mbar_arrive_expect_tx(&ctl.k_full[b], 2 * kHalfK);
+#pragma unroll 1
+          for (int k = 0; k < 9; ++k)
+            load_box<G>(smem + Lay::k + b * kHalfK + k * (kBlock / 2), &half_map, 64 * k, y + 32 * g, &ctl.k_full[b]);
+          if (!wait(&ctl.vown_empty[b], (i >> 1) + 1)) break;
+          if (g == 0) tc::mbar_arrive_expect_tx(&ctl.vown_full[b], 2 * Lay::kVBytes);
+          for (int k = 0; k < 2; ++k)
+            load_box<G>(smem + Lay::vown + (2 * b + k) * kBlock, &tile_map, 64 * (4 * c + 2 * g + k), y, &ctl.vown_full[b]);
         }
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- Q K^T ----------------
-    if (wait_warp(&ctl.q_ready, 0)) {
+    if (g == 0 && wait_warp(&ctl.q_ready, 0)) {
       tc::fence_after_sync();
-      if (c == 0) qk_loop<0>(ctl, n_own, wait_warp);
-      else qk_loop<1>(ctl, n_own, wait_warp);
+      if constexpr (G == 2) qk_loop_pair(ctl, n_own, mine, wait_warp);
+      else if (c == 0) qk_loop_single<0>(ctl, n_own, wait_warp);
+      else qk_loop_single<1>(ctl, n_own, wait_warp);
     }
     __syncwarp();
   } else if (warp == 2) {
-    // ---------------- P V: this CTA's value half, over own and peer tiles in turn ----------------
-    const uint32_t leader = elect_leader();
-    constexpr uint32_t p_own = desc_lo(kOffPOwn, 16), p_in = desc_lo(kOffPIn, 16);
-    constexpr uint32_t v_own = desc_lo(kOffVOwn, kBlock), v_peer = desc_lo(kOffVPeer, kBlock);
+    // ---------------- P V: this parity's value half, over own and peer tiles in turn ----------------
+    if (g == 0) {
+      const uint32_t leader = elect_leader();
+      constexpr uint32_t p_own = desc_lo(kOffPOwn, 16), p_in = desc_lo(kOffPIn, 16), step = Lay::kVBytes >> 4;
+      constexpr uint32_t v_own = desc_lo(Lay::vown, kBlock), v_peer = desc_lo(Lay::vpeer, kBlock);
 #pragma unroll 1
-    for (int i = 0; i < n_own || i < n_peer; ++i) {
-      if (i < n_own) {
-        if (!wait_warp(&ctl.p_full, i)) break;
-        tc::fence_after_sync();
-        if (i == 0) pv_tile<false>(p_own, v_own, leader);
-        else if (i & 1) pv_tile<true>(p_own, v_own + 4 * (kBlock >> 4), leader);
-        else pv_tile<true>(p_own, v_own, leader);
-        commit_leader(&ctl.vown_empty[i & 1], leader);
-        commit_leader(&ctl.p_empty, leader);
+      for (int i = 0; i < n_own || i < n_peer; ++i) {
+        if (i < n_own) {
+          if (G == 2 && !wait_warp(&ctl.vown_full[i & 1], i >> 1)) break;
+          if (!wait_warp(&ctl.p_full, i)) break;
+          tc::fence_after_sync();
+          if (i == 0) pv_tile<G, false>(p_own, v_own, leader);
+          else if (i & 1) pv_tile<G, true>(p_own, v_own + step, leader);
+          else pv_tile<G, true>(p_own, v_own, leader);
+          commit_to<G>(&ctl.vown_empty[i & 1], mine, leader);
+          commit_to<G>(&ctl.p_empty, mine, leader);
+        }
+        if (i < n_peer) {
+          const int b = i % Lay::kPeerBufs;
+          if (!wait_warp(&ctl.vpeer_full[b], i / Lay::kPeerBufs) || !wait_warp(&ctl.pin_go, i)) break;
+          tc::fence_after_sync();
+          if (i == 0 && n_own == 0) pv_tile<G, false>(p_in, v_peer, leader);
+          else if (b == 0) pv_tile<G, true>(p_in, v_peer, leader);
+          else pv_tile<G, true>(p_in, v_peer + step, leader);
+          commit_to<G>(&ctl.vpeer_empty[b], mine, leader);
+          commit_to<G>(&ctl.p_empty, theirs, leader);
+        }
       }
-      if (i < n_peer) {
-        if (!wait_warp(&ctl.vpeer_full, i) || !wait_warp(&ctl.pin_go, i)) break;
-        if (leader) tc::mbar_arrive_expect_tx(&ctl.pin_full, kPMsg);  // the next weights
-        __syncwarp();
-        tc::fence_after_sync();
-        if (i == 0 && n_own == 0) pv_tile<false>(p_in, v_peer, leader);
-        else pv_tile<true>(p_in, v_peer, leader);
-        commit_leader(&ctl.vpeer_empty, leader);
-        commit_leader_to(&ctl.p_empty, static_cast<uint16_t>(1u << peer), leader);
-      }
+      commit_to<G>(&ctl.o_done, mine, leader);
     }
-    commit_leader(&ctl.o_done, leader);
     __syncwarp();
   } else if (warp == 3) {
     // ---------------- own weights to the peer; value blocks of the peer's tiles ----------------
     if (lane == 0) {
       const uint32_t dst = dsmem_addr(smem + kOffPIn, peer), bar = dsmem_addr(&ctl.pin_full, peer);
+      auto load_peer = [&](int i) {
+        const int b = i % Lay::kPeerBufs, y = (tile_base + tile0 + 2 * i + other) * kTile;
+        if (!wait(&ctl.vpeer_empty[b], i / Lay::kPeerBufs + 1)) return false;
+        if (g == 0) tc::mbar_arrive_expect_tx(&ctl.vpeer_full[b], G * Lay::kVBytes);
+        for (int k = 0; k < 4 / G; ++k)
+          load_box<G>(smem + Lay::vpeer + b * Lay::kVBytes + k * kBlock, &tile_map, 64 * (4 * c + 4 / G * g + k), y,
+                      &ctl.vpeer_full[b]);
+        return true;
+      };
+      bool ok = true;
+      if (Lay::kPeerBufs == 2 && n_peer > 0) ok = load_peer(0);
 #pragma unroll 1
-      for (int i = 0; i < n_own || i < n_peer; ++i) {
-        if (i < n_peer) {
-          if (!wait(&ctl.vpeer_empty, i + 1)) break;
-          tc::mbar_arrive_expect_tx(&ctl.vpeer_full, 4 * kBlock);
-          for (int k = 0; k < 4; ++k)
-            tc::tma_load_3d(smem + kOffVPeer + k * kBlock, &kvmap, 64 * (4 * c + k),
-                            (tile_base + tile0 + 2 * i + peer) * kTile, 0, &ctl.vpeer_full);
-        }
+      for (int i = 0; ok && (i < n_own || i < n_peer); ++i) {
+        const int ahead = i + Lay::kPeerBufs - 1;
+        if (ahead < n_peer && !load_peer(ahead)) break;
         if (i < n_own) {
           // (the warps that wrote them waited until the peer had read the last ones)
-          if (!wait(&ctl.p_full, i)) break;
+          if (!wait(&ctl.p_mine, i)) break;
           bulk_to_peer(dst, smem + kOffPOwn, kPMsg, bar);
         }
       }
@@ -701,7 +847,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&ctl.q_ready);
+      if (lane == 0) tell_chief(&ctl.q_ready);
     }
     // positions of this part the row sees
     int lim = 0;
@@ -754,7 +900,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
         tc::tmem_wait_ld();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ctl.s_free);
+        if (lane == 0) tell_chief(&ctl.s_free);
         if (!__all_sync(0xffffffffu, seen == ~0u && poison == 0u)) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
@@ -771,13 +917,14 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
         const float mt = row_max(fmaf(fmaxf(t0, t1), kt, fe), i & 1);
         if (i == 0 && c == 0) {
           rho = mt;
-          if (hv == 0) st_async_f32(dsmem_addr(&ctl.r[m], 1), rho, dsmem_addr(&ctl.r_full, 1));
+          if (hv == 0) st_async_f32(dsmem_addr(&ctl.r[m], peer), rho, dsmem_addr(&ctl.r_full, peer));
         }
         // the row's reference rises when a weight would pass 2^14, or at its first position
         const bool raise = mt > rho + kHeadroom || (rho == -INFINITY && mt > -INFINITY);
         if (__any_sync(0xffffffffu, raise)) {
           const bool any_product = i > 0;
-          if (any_product) wait_warp(&ctl.vpeer_empty, i - 1);  // the last product was the peer tile's
+          // the last product was the peer tile's
+          if (any_product) wait_warp(&ctl.vpeer_empty[(i - 1) % Lay::kPeerBufs], (i - 1) / Lay::kPeerBufs);
           rescale(raise ? mt - rho : 0.f, any_product);
           if (raise) rho = mt;
         }
@@ -803,17 +950,22 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
         tc::fence_async_smem();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ctl.p_full);
+        if (lane == 0) {
+          tc::mbar_arrive(&ctl.p_mine);
+          tell_chief(&ctl.p_full);
+        }
       }
       if (i < n_peer) {
-        e_top = max(e_top, __ldcg(&ws.info[tile_base + tile0 + 2 * i + peer].e));
+        e_top = max(e_top, __ldcg(&ws.info[tile_base + tile0 + 2 * i + other].e));
         wait_warp(&ctl.pin_full, i);
+        if (tid == 4 * 32) tc::mbar_arrive_expect_tx(&ctl.pin_full, kPMsg);  // the next weights
+        __syncwarp();
         const float r_in = in_r[m];
         if (__any_sync(0xffffffffu, r_in != rho)) {
           const bool any_product = i < n_own || i > 0;
           // every product so far: the last was the own tile's, or the peer's before it
           if (i < n_own) wait_warp(&ctl.vown_empty[i & 1], i >> 1);
-          else if (i > 0) wait_warp(&ctl.vpeer_empty, i - 1);
+          else if (i > 0) wait_warp(&ctl.vpeer_empty[(i - 1) % Lay::kPeerBufs], (i - 1) / Lay::kPeerBufs);
           const bool raise = r_in > rho;
           rescale(raise ? r_in - rho : 0.f, any_product);
           if (raise) rho = r_in;
@@ -837,7 +989,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
           tc::fence_before_sync();
           __syncwarp();
         }
-        if (lane == 0) tc::mbar_arrive(&ctl.pin_go);
+        if (lane == 0) tell_chief(&ctl.pin_go);
       }
     }
     // the last weights have been read, here and by the peer (whose word of it has then arrived)
@@ -857,7 +1009,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
   // ---- output: O / l through the tiles' shared memory, in whole rows: bf16, or with several
   // splits fp16 times 2^-(e_out), e_out the largest exponent of the item's tiles: |O / l| is at
   // most the largest value, below 2^15 2^e_out ----
-  uint8_t* stage = smem + kOffVOwn;
+  uint8_t* stage = smem + kOffKv;
   if (warp >= 4) {
     const int hv = (warp - 4) >> 2, m = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -916,7 +1068,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kvmap, PrefixArgs a, PrefixPla
   __syncthreads();
   cluster_sync();
   tc::fence_after_sync();
-  if (warp == 1) tc::tmem_dealloc(ctl.tmem_base, 512);
+  if (warp == 1) tmem_dealloc_all<G>(ctl.tmem_base);
 }
 
 // ---- merge ---------------------------------------------------------------------------------
@@ -992,12 +1144,12 @@ EncodeFn encode_fn() {
   }();
   return fn;
 }
-// rows of 576 fp16 in boxes of 64 dims x 64 rows, 128-byte swizzle
-bool encode_rows(EncodeFn enc, CUtensorMap* map, void* base, int64_t rows) {
+// rows of 576 fp16 in boxes of 64 dims x box_rows, 128-byte swizzle
+bool encode_rows(EncodeFn enc, CUtensorMap* map, void* base, int64_t rows, int box_rows) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kLatent), static_cast<cuuint64_t>(rows), 1};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kLatent) * 2,
                                  static_cast<cuuint64_t>(kLatent) * 2 * static_cast<cuuint64_t>(rows)};
-  const cuuint32_t box[3] = {64, kTile, 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t one[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box, one,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1022,8 +1174,8 @@ cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char**
   PrefixWs ws{reinterpret_cast<__half*>(base), reinterpret_cast<TileInfo*>(base + pl.off_info),
               reinterpret_cast<__half*>(base + pl.off_o), reinterpret_cast<float4*>(base + pl.off_ml)};
   const int64_t rows = static_cast<int64_t>(a.n_q) * a.h_s;
-  const int64_t items = static_cast<int64_t>(pl.sp) * pl.mt + static_cast<int64_t>(pl.st) * a.n_q;
-  if (pl.rows_kv > INT32_MAX - kTile || rows > INT32_MAX - kRows || items > INT32_MAX / 2) {
+  const int64_t items = static_cast<int64_t>(pl.sp) * ((pl.mt + pl.g - 1) / pl.g) + static_cast<int64_t>(pl.st) * a.n_q;
+  if (pl.rows_kv > INT32_MAX - kTile || rows > INT32_MAX - kRows || items > INT32_MAX / 4) {
     *err = "prefix_attn: more rows than 32 bits count";
     return cudaErrorInvalidValue;
   }
@@ -1032,18 +1184,18 @@ cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char**
     *err = "prefix_attn: cuTensorMapEncodeTiled is not available";
     return cudaErrorNotSupported;
   }
-  CUtensorMap kvmap;
-  if (!encode_rows(enc, &kvmap, ws.kv, pl.rows_kv)) {
+  CUtensorMap tile_map, half_map;
+  if (!encode_rows(enc, &tile_map, ws.kv, pl.rows_kv, kTile) || !encode_rows(enc, &half_map, ws.kv, pl.rows_kv, kTile / 2)) {
     *err = "prefix_attn: tensor map encoding failed";
     return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSmemBytes));
+  const auto attend = pl.g == 2 ? attend_kernel<2> : attend_kernel<1>;
+  cudaError_t e = cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
   if (e != cudaSuccess) return e;
   e = launch_pdl(expand_kernel, dim3(static_cast<unsigned>(pl.rows_kv / kTile)), dim3(kExpandThreads), 0, s, 1, a, pl, ws);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attend_kernel, dim3(static_cast<unsigned>(2 * items)), dim3(kThreads), kSmemBytes, s, 2, kvmap, a, pl,
-                 ws);
+  e = launch_pdl(attend, dim3(static_cast<unsigned>(2 * pl.g * items)), dim3(kThreads), kSmemBytes, s, 2 * pl.g, tile_map,
+                 half_map, a, pl, ws);
   if (e != cudaSuccess || pl.sp + pl.st == 1) return e;
   return launch_pdl(prefix_merge_kernel, dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows)),
                     dim3(64 * kMergeRows), 0, s, 1, a, pl, ws);
