@@ -26,8 +26,8 @@
 // The pair.  The output accumulator of 128 rows x 512 columns would fill tensor memory, so
 // each CTA of the pair holds one half of the value columns.  Computing the logits in both
 // would cost half as much again; instead CTA c computes logits and weights of the tiles
-// j = c (mod 2) and sends the weights (fp16, 16 KB) to its peer by a bulk copy into
-// distributed shared memory; both then run P V over every tile, each on its half, in the
+// j = c (mod 2) and stores the weights (fp16, 16 KB) into its peer's shared memory as well as
+// its own; both then run P V over every tile, each on its half, in the
 // order own 0, peer 0, own 1, peer 1 ...
 //
 // The softmax reference.  With e the exponent of its tile, a position's weight is stored as
@@ -40,14 +40,18 @@
 // ahead, scales the received row down.  After each tile in the order above both CTAs hold the
 // largest reference used so far, so the results do not depend on timing.
 //
-// Per CTA (12 warps): 0 loads the own tiles, 1 issues Q K^T, 2 issues P V, 3 sends the weights
-// and loads the peer tiles' value blocks, 4-11 turn logits into weights (a row's 64 positions
-// in two threads).  Descriptors and tensor-memory addresses are constants of the unrolled
-// issue loops: with addresses computed per MMA the issue took 110-200 cycles each.
+// MMA pairs.  Where there are rows enough, four CTAs share an item of 256 rows: two per parity,
+// whose tensor cores work as one (cta_group::2) on 128 rows each, every B operand split between
+// their shared memories.  With one CTA per parity an SM moves some 370 KB through its shared
+// memory in a step of two tiles (operand reads, tile loads, weights), more than its 128 bytes a
+// cycle allow in the 2270 cycles of the products; with pairs it is 260 KB.
+//
+// Per CTA (13 warps): 0 loads the tiles for Q K^T, 3 the others, 1 issues Q K^T, 2 issues P V,
+// 4-11 turn logits into weights (a row's 64 positions in two threads), 12 copies the weights.
+// Descriptors and
+// tensor-memory addresses are constants of the unrolled issue loops.
 // Tensor memory (512 columns): O in 0..255, the logits in 256..319, the query's dims 0..383
-// as fp16 pairs in 320..511.  Shared memory: the query's dims 384..575, both weight buffers
-// with their references, and 17 blocks of 64 positions x 64 dims: the value blocks of two own
-// tiles (8), those of one peer tile (4), and the own tile's other five, which only Q K^T reads.
+// as fp16 pairs in 320..511; shared memory as in Layout below.
 // The query is scaled to fp16 by a power of two per row (exact: bf16 has 8 bits).
 
 #include <algorithm>
@@ -68,7 +72,7 @@ constexpr int kQBlock = kRows * 128;          // 128 rows x 64 dims: 16 KB
 constexpr int kQTmemBlocks = 6;               // 64-dim blocks with the query in tensor memory
 constexpr int kQSmemBlocks = 3;
 constexpr int kLoose = 5;                     // blocks of a tile that only Q K^T reads
-constexpr int kThreads = 32 * 12;
+constexpr int kThreads = 32 * 13;
 constexpr int kSoftWarps = 8;                 // warps 4..11
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 constexpr uint32_t kPBytes = kRows * 128;     // the weights of a tile
@@ -76,52 +80,57 @@ constexpr uint32_t kPMsg = kPBytes + kRows * 4;  // with the rows' references
 constexpr uint32_t kPStride = (kPMsg + 1023) / 1024 * 1024;
 constexpr float kHeadroom = 14.0f;            // powers of two a weight may reach
 
-// Shared memory.  G = 1: the value blocks (64 positions x 64 dims) of two own tiles and one peer
-// tile, and the own tile's other five blocks.  G = 2: each CTA of an MMA pair holds half of every
-// B operand: of two own tiles 32 positions x 576 dims for Q K^T, and of two own and two peer tiles
-// 64 positions x 128 dims for P V.
+// Shared memory behind the query's part: own weights, the peer's weights, value tiles, tiles for
+// Q K^T.  Loads and copies between CTAs take some 2000 cycles, nearly a step of two tiles, so
+// what crosses has buffers to spare.  G = 1: the value blocks (64 positions x 64 dims) of two own
+// tiles (slots 0, 1; Q K^T reads them too) and one peer tile (slot 2), and the own tile's other
+// five blocks.  G = 2: each CTA of an MMA pair holds half of every B operand: 64 positions x 128
+// dims of own and peer tiles in turn (a ring of three slots), and 32 positions of tiles for Q K^T
+// (a ring of five pieces of 192 dims, three pieces a tile); two buffers each way for the weights.
 constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffPOwn = kOffQ + kQSmemBlocks * kQBlock;
-constexpr uint32_t kOffPIn = kOffPOwn + kPStride;
-constexpr uint32_t kOffKv = kOffPIn + kPStride;
-constexpr int kHalfK = 9 * kBlock / 2;        // G = 2: half a tile's rows
-template <int G> struct Layout;
-template <> struct Layout<1> {
-  static constexpr int kVBytes = 4 * kBlock, kPeerBufs = 1;
-  static constexpr uint32_t vown = kOffKv, vpeer = vown + 2 * kVBytes, k = vpeer + kVBytes, ctl = k + kLoose * kBlock;
+constexpr uint32_t kOffP = kOffQ + kQSmemBlocks * kQBlock;
+constexpr int kPiece = 3 * kBlock / 2, kPieces = 5;  // G = 2: 32 positions x 192 dims, ring slots
+template <int G> struct Layout {
+  static constexpr int kVBytes = 4 * kBlock / G, kVSlots = 3, kBufs = G;
+  static constexpr uint32_t p_own = kOffP, p_in = p_own + kBufs * kPStride, v = p_in + kBufs * kPStride;
+  static constexpr uint32_t k = v + kVSlots * kVBytes, ctl = k + (G == 1 ? kLoose * kBlock : kPieces * kPiece);
+  // slot of a tile's values and how often the slot was filled before: own tile i is product 2 i, peer
+  // tile i follows it (or, where there is none, the last one)
+  static __host__ __device__ constexpr int own_slot(int i) { return G == 1 ? i % 2 : 2 * i % 3; }
+  static __host__ __device__ constexpr int own_phase(int i) { return G == 1 ? i / 2 : 2 * i / 3; }
+  static __host__ __device__ constexpr int peer_slot(int i, int n_own) {
+    return G == 1 ? 2 : (i + (i < n_own ? i + 1 : n_own)) % 3;
+  }
+  static __host__ __device__ constexpr int peer_phase(int i, int n_own) {
+    return G == 1 ? i : (i + (i < n_own ? i + 1 : n_own)) / 3;
+  }
 };
-template <> struct Layout<2> {
-  static constexpr int kVBytes = 2 * kBlock, kPeerBufs = 2;
-  static constexpr uint32_t vown = kOffKv, vpeer = vown + 2 * kVBytes, k = vpeer + 2 * kVBytes, ctl = k + 2 * kHalfK;
-};
-static_assert(Layout<1>::ctl == Layout<2>::ctl, "one control offset");
-constexpr uint32_t kOffCtl = Layout<1>::ctl;
 
 struct PairCtl {
   uint64_t q_ready;                            // the query is in tensor and shared memory
-  uint64_t k_full[kLoose], k_empty[kLoose];    // G = 1: the five loose blocks; G = 2: two tiles' halves
-  uint64_t vown_full[2], vown_empty[2];        // full; read by the own P V
-  uint64_t vpeer_full[2], vpeer_empty[2];
+  uint64_t k_full[kLoose], k_empty[kLoose];    // G = 1: the five loose blocks; G = 2: the five pieces
+  uint64_t v_full[3], v_empty[3];              // value tiles: landed; read by their P V
   uint64_t s_full, s_free;                     // logits written / read into registers
-  uint64_t p_mine;                             // this CTA's weights are in shared memory
-  uint64_t p_full;                             // every row's weights are, and O is at their reference
-  uint64_t p_empty;                            // own weights read: by the own P V and by the peer's (of its copy)
-  uint64_t pin_full;                           // the peer's weights have landed
-  uint64_t pin_go;                             // they and O are at one reference
+  // per weight buffer:
+  uint64_t p_mine[2];                          // this CTA's weights are in shared memory
+  uint64_t p_full[2];                          // every row's weights are, and O is at their reference
+  uint64_t p_empty[2];                         // own weights read: by the own P V and by the peer's (of its copy)
+  uint64_t pin_full[2];                        // the peer's weights have landed
+  uint64_t pin_go[2];                          // they and O are at one reference
   uint64_t o_done;
   uint64_t r_full;                             // parity 1: the first references have landed
   uint64_t fin_full;                           // the peer's sums have landed
   uint32_t tmem_base;
   int abort;
-  float r[kRows];                              // parity 1: from parity 0
-  float fin[kRows];                            // the peer's sum of weights
+  float sent[kRows];                           // by the peer: the first references (to parity 1), at the end the sums
   float part[2][2][kRows];                     // tile maxima of a row's two threads, by tile parity
 };
-constexpr uint32_t kSmemBytes = kOffCtl + 4096;
-static_assert(sizeof(PairCtl) <= 4096 && kSmemBytes <= 232448, "shared memory");
+template <int G> constexpr uint32_t kSmemBytes = Layout<G>::ctl + 3072;
+static_assert(sizeof(PairCtl) <= 3072 && kPieces == kLoose && kSmemBytes<1> <= 232448 && kSmemBytes<2> <= 232448, "shared memory");
 // the output rows are staged where the tiles' blocks were
 constexpr int kStagePitch = kHalfV * 2 + 16;
-static_assert(kRows * kStagePitch <= 17 * kBlock, "output staging");
+static_assert(kRows * kStagePitch <= Layout<1>::ctl - Layout<1>::v && kRows * kStagePitch <= Layout<2>::ctl - Layout<2>::v,
+              "output staging");
 
 // What expand writes per tile.
 struct alignas(32) TileInfo {
@@ -486,13 +495,13 @@ __device__ __forceinline__ void pv_tile(uint32_t p_lo, uint32_t v_lo, uint32_t l
 template <int C, typename Wait>
 __device__ __forceinline__ void qk_loop_single(PairCtl& ctl, int n_own, Wait wait_warp) {
   const uint32_t leader = elect_leader();
-  constexpr uint32_t kStep = kBlock >> 4, v0 = desc_lo(Layout<1>::vown, 16), v1 = v0 + 4 * kStep;
+  constexpr uint32_t kStep = kBlock >> 4, v0 = desc_lo(Layout<1>::v, 16), v1 = v0 + 4 * kStep;
   constexpr uint32_t lo = desc_lo(Layout<1>::k, 16);
   constexpr uint16_t me = 1u << C;
 #pragma unroll 1
   for (int i = 0; i < n_own; ++i) {
     const int b = i & 1;
-    if (!wait_warp(&ctl.s_free, i + 1) || !wait_warp(&ctl.vown_full[b], i >> 1)) return;
+    if (!wait_warp(&ctl.s_free, i + 1) || !wait_warp(&ctl.v_full[b], i >> 1)) return;
     tc::fence_after_sync();
     if (b == 0) {
       qk_block<1, 4 * C, true>(v0, leader);
@@ -524,32 +533,41 @@ __device__ __forceinline__ void qk_loop_single(PairCtl& ctl, int n_own, Wait wai
     commit_to<1>(&ctl.s_full, me, leader);
   }
 }
-// G = 2: a tile's rows lie together, half in each CTA.
-template <uint32_t K>
-__device__ __forceinline__ void qk_tile_pair(uint32_t leader) {
-  constexpr uint32_t k = desc_lo(K, 16), kStep = kBlock / 2 >> 4;
-  qk_block<2, 0, true>(k, leader);
-  qk_block<2, 1, false>(k + kStep, leader);
-  qk_block<2, 2, false>(k + 2 * kStep, leader);
-  qk_block<2, 3, false>(k + 3 * kStep, leader);
-  qk_block<2, 4, false>(k + 4 * kStep, leader);
-  qk_block<2, 5, false>(k + 5 * kStep, leader);
-  qk_block<2, 6, false>(k + 6 * kStep, leader);
-  qk_block<2, 7, false>(k + 7 * kStep, leader);
-  qk_block<2, 8, false>(k + 8 * kStep, leader);
+// G = 2: a tile comes in three pieces of 192 dims, half of its positions in each CTA.
+template <int PIECE>
+__device__ __forceinline__ void qk_piece(uint32_t k_lo, uint32_t leader) {
+  constexpr uint32_t kStep = kBlock / 2 >> 4;
+  qk_block<2, 3 * PIECE, PIECE == 0>(k_lo, leader);
+  qk_block<2, 3 * PIECE + 1, false>(k_lo + kStep, leader);
+  qk_block<2, 3 * PIECE + 2, false>(k_lo + 2 * kStep, leader);
 }
 template <typename Wait>
 __device__ __forceinline__ void qk_loop_pair(PairCtl& ctl, int n_own, uint16_t pair, Wait wait_warp) {
   const uint32_t leader = elect_leader();
+  constexpr uint32_t k0 = desc_lo(Layout<2>::k, 16);
+  int slot = 0, phase = 0;
+  auto next = [&] {
+    if (++slot == kPieces) {
+      slot = 0;
+      ++phase;
+    }
+  };
 #pragma unroll 1
   for (int i = 0; i < n_own; ++i) {
-    const int b = i & 1;
-    if (!wait_warp(&ctl.k_full[b], i >> 1) || !wait_warp(&ctl.s_free, i + 1)) return;
+    if (!wait_warp(&ctl.k_full[slot], phase) || !wait_warp(&ctl.s_free, i + 1)) return;
     tc::fence_after_sync();
-    if (b == 0) qk_tile_pair<Layout<2>::k>(leader);
-    else qk_tile_pair<Layout<2>::k + kHalfK>(leader);
-    commit_to<2>(&ctl.k_empty[b], pair, leader);
+    qk_piece<0>(k0 + slot * (kPiece >> 4), leader);
+    commit_to<2>(&ctl.k_empty[slot], pair, leader);
+    next();
+    if (!wait_warp(&ctl.k_full[slot], phase)) return;
+    qk_piece<1>(k0 + slot * (kPiece >> 4), leader);
+    commit_to<2>(&ctl.k_empty[slot], pair, leader);
+    next();
+    if (!wait_warp(&ctl.k_full[slot], phase)) return;
+    qk_piece<2>(k0 + slot * (kPiece >> 4), leader);
     commit_to<2>(&ctl.s_full, pair, leader);
+    commit_to<2>(&ctl.k_empty[slot], pair, leader);
+    next();
   }
 }
 
@@ -559,7 +577,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constan
               PrefixPlan pl, PrefixWs ws) {
   using Lay = Layout<G>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  PairCtl& ctl = *reinterpret_cast<PairCtl*>(smem + kOffCtl);
+  PairCtl& ctl = *reinterpret_cast<PairCtl*>(smem + Lay::ctl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // rank = G c + g: c the parity of the own tiles and the half of the value columns, g the CTA's
   // 128 rows of the item's 128 G.  Its peer has the same rows; the pair's even CTA issues MMAs.
@@ -630,19 +648,19 @@ attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constan
       tc::mbar_init(&ctl.k_full[k], 1);
       tc::mbar_init(&ctl.k_empty[k], 1);
     }
-    for (int k = 0; k < 2; ++k) {
-      tc::mbar_init(&ctl.vown_full[k], 1);
-      tc::mbar_init(&ctl.vown_empty[k], 1);
-      tc::mbar_init(&ctl.vpeer_full[k], 1);
-      tc::mbar_init(&ctl.vpeer_empty[k], 1);
+    for (int k = 0; k < Lay::kVSlots; ++k) {
+      tc::mbar_init(&ctl.v_full[k], 1);
+      tc::mbar_init(&ctl.v_empty[k], 1);
+    }
+    for (int k = 0; k < Lay::kBufs; ++k) {
+      tc::mbar_init(&ctl.p_mine[k], kSoftWarps);
+      tc::mbar_init(&ctl.p_full[k], G * kSoftWarps);
+      tc::mbar_init(&ctl.p_empty[k], 2);
+      tc::mbar_init(&ctl.pin_full[k], 1);
+      tc::mbar_init(&ctl.pin_go[k], G * kSoftWarps);
     }
     tc::mbar_init(&ctl.s_full, 1);
     tc::mbar_init(&ctl.s_free, G * kSoftWarps);
-    tc::mbar_init(&ctl.p_mine, kSoftWarps);
-    tc::mbar_init(&ctl.p_full, G * kSoftWarps);
-    tc::mbar_init(&ctl.p_empty, 2);
-    tc::mbar_init(&ctl.pin_full, 1);
-    tc::mbar_init(&ctl.pin_go, G * kSoftWarps);
     tc::mbar_init(&ctl.o_done, 1);
     tc::mbar_init(&ctl.r_full, 1);
     tc::mbar_init(&ctl.fin_full, 1);
@@ -650,7 +668,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constan
     // what the peer will send
     if (c == 1) tc::mbar_arrive_expect_tx(&ctl.r_full, kRows * 4);
     tc::mbar_arrive_expect_tx(&ctl.fin_full, kRows * 4);
-    tc::mbar_arrive_expect_tx(&ctl.pin_full, kPMsg);
+    for (int k = 0; k < Lay::kBufs; ++k) tc::mbar_arrive_expect_tx(&ctl.pin_full[k], kPMsg);
   }
   __syncthreads();
   cluster_sync();  // every CTA's barriers are ready
@@ -693,10 +711,10 @@ attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constan
         const int b = i & 1, y = (tile_base + tile0 + 2 * i + c) * kTile;
         if constexpr (G == 1) {
           // the half of the value blocks this CTA keeps, then the other blocks
-          if (!wait(&ctl.vown_empty[b], (i >> 1) + 1)) break;
-          tc::mbar_arrive_expect_tx(&ctl.vown_full[b], Lay::kVBytes);
+          if (!wait(&ctl.v_empty[b], (i >> 1) + 1)) break;
+          tc::mbar_arrive_expect_tx(&ctl.v_full[b], Lay::kVBytes);
           for (int k = 0; k < 4; ++k)
-            load_box<G>(smem + Lay::vown + (4 * b + k) * kBlock, &tile_map, 64 * (4 * c + k), y, &ctl.vown_full[b]);
+            load_box<G>(smem + Lay::v + (4 * b + k) * kBlock, &tile_map, 64 * (4 * c + k), y, &ctl.v_full[b]);
 #pragma unroll 1
           for (int k = 0; k < kLoose; ++k) {
             ok = wait(&ctl.k_empty[k], i + 1);
@@ -705,16 +723,17 @@ attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constan
             load_box<G>(smem + Lay::k + k * kBlock, &tile_map, 64 * (k < 4 ? 4 * other + k : 8), y, &ctl.k_full[k]);
           }
         } else {
-          // this CTA's 32 positions for Q K^T, then its 128 value columns
-          if (!wait(&ctl.k_empty[b], (i >> 1) + 1)) break;
-          if (g == 0) tc::mbar_arrive_expect_tx(&ctl.k_full[b], 2 * kHalfK);
+          // this CTA's 32 positions for Q K^T
 #pragma unroll 1
-          for (int k = 0; k < 9; ++k)
-            load_box<G>(smem + Lay::k + b * kHalfK + k * (kBlock / 2), &half_map, 64 * k, y + 32 * g, &ctl.k_full[b]);
-          if (!wait(&ctl.vown_empty[b], (i >> 1) + 1)) break;
-          if (g == 0) tc::mbar_arrive_expect_tx(&ctl.vown_full[b], 2 * Lay::kVBytes);
-          for (int k = 0; k < 2; ++k)
-            load_box<G>(smem + Lay::vown + (2 * b + k) * kBlock, &tile_map, 64 * (4 * c + 2 * g + k), y, &ctl.vown_full[b]);
+          for (int k = 0; k < 3; ++k) {
+            const int n = 3 * i + k, slot_k = n % kPieces;
+            ok = wait(&ctl.k_empty[slot_k], n / kPieces + 1);
+            if (!ok) break;
+            if (g == 0) tc::mbar_arrive_expect_tx(&ctl.k_full[slot_k], 2 * kPiece);
+            for (int j = 0; j < 3; ++j)
+              load_box<G>(smem + Lay::k + slot_k * kPiece + j * (kBlock / 2), &half_map, 64 * (3 * k + j), y + 32 * g,
+                          &ctl.k_full[slot_k]);
+          }
         }
       }
     }
@@ -732,58 +751,63 @@ attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constan
     // ---------------- P V: this parity's value half, over own and peer tiles in turn ----------------
     if (g == 0) {
       const uint32_t leader = elect_leader();
-      constexpr uint32_t p_own = desc_lo(kOffPOwn, 16), p_in = desc_lo(kOffPIn, 16), step = Lay::kVBytes >> 4;
-      constexpr uint32_t v_own = desc_lo(Lay::vown, kBlock), v_peer = desc_lo(Lay::vpeer, kBlock);
+      constexpr uint32_t p_own = desc_lo(Lay::p_own, 16), p_in = desc_lo(Lay::p_in, 16);
+      constexpr uint32_t v0 = desc_lo(Lay::v, kBlock), v_step = Lay::kVBytes >> 4, p_step = kPStride >> 4;
 #pragma unroll 1
       for (int i = 0; i < n_own || i < n_peer; ++i) {
+        const int b = i % Lay::kBufs, ph = i / Lay::kBufs;
         if (i < n_own) {
-          if (G == 2 && !wait_warp(&ctl.vown_full[i & 1], i >> 1)) break;
-          if (!wait_warp(&ctl.p_full, i)) break;
+          const int vs = Lay::own_slot(i);
+          if (G == 2 && !wait_warp(&ctl.v_full[vs], Lay::own_phase(i))) break;
+          if (!wait_warp(&ctl.p_full[b], ph)) break;
           tc::fence_after_sync();
-          if (i == 0) pv_tile<G, false>(p_own, v_own, leader);
-          else if (i & 1) pv_tile<G, true>(p_own, v_own + step, leader);
-          else pv_tile<G, true>(p_own, v_own, leader);
-          commit_to<G>(&ctl.vown_empty[i & 1], mine, leader);
-          commit_to<G>(&ctl.p_empty, mine, leader);
+          if (i == 0) pv_tile<G, false>(p_own, v0, leader);
+          else pv_tile<G, true>(p_own + b * p_step, v0 + vs * v_step, leader);
+          commit_to<G>(&ctl.p_empty[b], mine, leader);
+          commit_to<G>(&ctl.v_empty[vs], mine, leader);
         }
         if (i < n_peer) {
-          const int b = i % Lay::kPeerBufs;
-          if (!wait_warp(&ctl.vpeer_full[b], i / Lay::kPeerBufs) || !wait_warp(&ctl.pin_go, i)) break;
+          const int vs = Lay::peer_slot(i, n_own);
+          if (!wait_warp(&ctl.v_full[vs], Lay::peer_phase(i, n_own)) || !wait_warp(&ctl.pin_go[b], ph)) break;
           tc::fence_after_sync();
-          if (i == 0 && n_own == 0) pv_tile<G, false>(p_in, v_peer, leader);
-          else if (b == 0) pv_tile<G, true>(p_in, v_peer, leader);
-          else pv_tile<G, true>(p_in, v_peer + step, leader);
-          commit_to<G>(&ctl.vpeer_empty[b], mine, leader);
-          commit_to<G>(&ctl.p_empty, theirs, leader);
+          if (i == 0 && n_own == 0) pv_tile<G, false>(p_in, v0 + vs * v_step, leader);
+          else pv_tile<G, true>(p_in + b * p_step, v0 + vs * v_step, leader);
+          commit_to<G>(&ctl.p_empty[b], theirs, leader);
+          commit_to<G>(&ctl.v_empty[vs], mine, leader);
         }
       }
       commit_to<G>(&ctl.o_done, mine, leader);
     }
     __syncwarp();
   } else if (warp == 3) {
-    // ---------------- own weights to the peer; value blocks of the peer's tiles ----------------
+    // ---------------- value blocks of the peer's tiles, and in a pair of the own ones, in the products' order ----
     if (lane == 0) {
-      const uint32_t dst = dsmem_addr(smem + kOffPIn, peer), bar = dsmem_addr(&ctl.pin_full, peer);
-      auto load_peer = [&](int i) {
-        const int b = i % Lay::kPeerBufs, y = (tile_base + tile0 + 2 * i + other) * kTile;
-        if (!wait(&ctl.vpeer_empty[b], i / Lay::kPeerBufs + 1)) return false;
-        if (g == 0) tc::mbar_arrive_expect_tx(&ctl.vpeer_full[b], G * Lay::kVBytes);
-        for (int k = 0; k < 4 / G; ++k)
-          load_box<G>(smem + Lay::vpeer + b * Lay::kVBytes + k * kBlock, &tile_map, 64 * (4 * c + 4 / G * g + k), y,
-                      &ctl.vpeer_full[b]);
-        return true;
-      };
-      bool ok = true;
-      if (Lay::kPeerBufs == 2 && n_peer > 0) ok = load_peer(0);
 #pragma unroll 1
-      for (int i = 0; ok && (i < n_own || i < n_peer); ++i) {
-        const int ahead = i + Lay::kPeerBufs - 1;
-        if (ahead < n_peer && !load_peer(ahead)) break;
-        if (i < n_own) {
-          // (the warps that wrote them waited until the peer had read the last ones)
-          if (!wait(&ctl.p_mine, i)) break;
-          bulk_to_peer(dst, smem + kOffPOwn, kPMsg, bar);
-        }
+      for (int i = 0; i < n_peer || (G == 2 && i < n_own); ++i) {
+        const int y = (tile_base + tile0 + 2 * i) * kTile;
+        auto load = [&](int vs, int phase, int y_tile) {
+          if (!wait(&ctl.v_empty[vs], phase + 1)) return false;
+          if (g == 0) tc::mbar_arrive_expect_tx(&ctl.v_full[vs], G * Lay::kVBytes);
+          for (int k = 0; k < 4 / G; ++k)
+            load_box<G>(smem + Lay::v + vs * Lay::kVBytes + k * kBlock, &tile_map, 64 * (4 * c + 4 / G * g + k), y_tile,
+                        &ctl.v_full[vs]);
+          return true;
+        };
+        if (G == 2 && i < n_own && !load(Lay::own_slot(i), Lay::own_phase(i), y + c * kTile)) break;
+        if (i < n_peer && !load(Lay::peer_slot(i, n_own), Lay::peer_phase(i, n_own), y + other * kTile)) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 12) {
+    // ---------------- own weights to the peer ----------------
+    if (lane == 0) {
+      const uint32_t dst = dsmem_addr(smem + Lay::p_in, peer), bar = dsmem_addr(&ctl.pin_full[0], peer);
+#pragma unroll 1
+      for (int i = 0; i < n_own; ++i) {
+        const int b = i % Lay::kBufs;
+        // (the warps that wrote them waited until the peer had read what this buffer held before)
+        if (!wait(&ctl.p_mine[b], i / Lay::kBufs)) break;
+        bulk_to_peer(dst + b * kPStride, smem + Lay::p_own + b * kPStride, kPMsg, bar + b * 8);
       }
     }
     __syncwarp();
@@ -873,133 +897,147 @@ attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constan
     };
     if (c == 1) {
       wait_warp(&ctl.r_full, 0);
-      rho = ctl.r[m];
+      rho = ctl.sent[m];
     }
-    float* own_r = reinterpret_cast<float*>(smem + kOffPOwn + kPBytes);
-    const float* in_r = reinterpret_cast<const float*>(smem + kOffPIn + kPBytes);
-    // (after a wait that ran out these warps still go through every step, each wait returning at
-    // once: the named barriers need both of a row's warps)
-#pragma unroll 1
-    for (int i = 0; i < n_own || i < n_peer; ++i) {
-      if (i < n_own) {
-        const int tile = tile0 + 2 * i + c;
-        const TileInfo* info = ws.info + tile_base + tile;
-        const ulonglong2 w = __ldcg(reinterpret_cast<const ulonglong2*>(info));
-        const int e = __ldcg(&info->e);
-        const int nv = lim - tile * kTile;
-        const uint64_t seen64 = w.x & (nv >= kTile ? ~0ull : nv <= 0 ? 0ull : (1ull << nv) - 1ull);
-        const uint32_t seen = static_cast<uint32_t>(seen64 >> (32 * hv)), poison = static_cast<uint32_t>(w.y >> (32 * hv));
-        e_top = max(e_top, e);
-        // (held inside fp32's range: a factor of 0 would turn an unseen position's -inf into NaN)
-        const float kt = fminf(fmaxf(k2 * exp2i(e), 1.2e-38f), 3.0e38f);
-        const float fe = static_cast<float>(e);
-        wait_warp(&ctl.s_full, i);
-        tc::fence_after_sync();
-        uint32_t s[32];
-        tc::tmem_ld32(lane_base + kColS + 32 * hv, s);
-        tc::tmem_wait_ld();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tell_chief(&ctl.s_free);
-        if (!__all_sync(0xffffffffu, seen == ~0u && poison == 0u)) {
+    // Bring the peer's tile i (landed, or waited for) and O to one reference.
+    auto reconcile = [&](int i) {
+      const int b = i % Lay::kBufs;
+      uint8_t* p_in = smem + Lay::p_in + b * kPStride;
+      e_top = max(e_top, __ldcg(&ws.info[tile_base + tile0 + 2 * i + other].e));
+      wait_warp(&ctl.pin_full[b], i / Lay::kBufs);
+      if (tid == 4 * 32) tc::mbar_arrive_expect_tx(&ctl.pin_full[b], kPMsg);  // the buffer's next weights
+      __syncwarp();
+      const float r_in = reinterpret_cast<const float*>(p_in + kPBytes)[m];
+      if (__any_sync(0xffffffffu, r_in != rho)) {
+        // every product so far: the last was the own tile's, or the peer's before it
+        if (i < n_own) wait_warp(&ctl.v_empty[Lay::own_slot(i)], Lay::own_phase(i));
+        else if (i > 0) wait_warp(&ctl.v_empty[Lay::peer_slot(i - 1, n_own)], Lay::peer_phase(i - 1, n_own));
+        const bool raise = r_in > rho;
+        rescale(raise ? r_in - rho : 0.f, i < n_own || i > 0);
+        if (raise) rho = r_in;
+        if (r_in < rho) {  // sent before the peer learned of this reference (2^-inf = 0)
+          const float f = exp2f(r_in - rho);
+          uint8_t* row = p_in + m * 128;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            if ((poison >> k) & 1u) s[k] = 0x7FFFFFFFu;
-            if (!((seen >> k) & 1u)) s[k] = 0xFF800000u;
+          for (int k = 0; k < 4; ++k) {
+            uint4* at = reinterpret_cast<uint4*>(row + (((4 * hv + k) ^ (m & 7)) << 4));
+            const uint4 u = *at;
+            uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 h = unpack_half2(v[j]);
+              v[j] = pack_half2(h.x * f, h.y * f);
+            }
+            *at = make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
-        float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          t0 = fmaxf(t0, fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
-          t1 = fmaxf(t1, fmaxf(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
-        }
-        const float mt = row_max(fmaf(fmaxf(t0, t1), kt, fe), i & 1);
-        if (i == 0 && c == 0) {
-          rho = mt;
-          if (hv == 0) st_async_f32(dsmem_addr(&ctl.r[m], peer), rho, dsmem_addr(&ctl.r_full, peer));
-        }
-        // the row's reference rises when a weight would pass 2^14, or at its first position
-        const bool raise = mt > rho + kHeadroom || (rho == -INFINITY && mt > -INFINITY);
-        if (__any_sync(0xffffffffu, raise)) {
-          const bool any_product = i > 0;
-          // the last product was the peer tile's
-          if (any_product) wait_warp(&ctl.vpeer_empty[(i - 1) % Lay::kPeerBufs], (i - 1) / Lay::kPeerBufs);
-          rescale(raise ? mt - rho : 0.f, any_product);
-          if (raise) rho = mt;
-        }
-        const float off = fe - (rho == -INFINITY ? 0.f : rho);
-        uint32_t p[16];
-        float x0 = 0.f, x1 = 0.f;
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          const float a0 = exp2_approx(fmaf(__uint_as_float(s[k]), kt, off));
-          const float a1 = exp2_approx(fmaf(__uint_as_float(s[k + 1]), kt, off));
-          p[k >> 1] = pack_half2(a0, a1);
-          x0 += a0;
-          x1 += a1;
-        }
-        l = fmaf(x0 + x1, exp2i(-e), l);
-        wait_warp(&ctl.p_empty, i + 1);
-        uint8_t* row = smem + kOffPOwn + m * 128;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<uint4*>(row + (((4 * hv + k) ^ (m & 7)) << 4)) =
-              make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
-        if (hv == 0) own_r[m] = rho;
         tc::fence_async_smem();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(&ctl.p_mine);
-          tell_chief(&ctl.p_full);
+      }
+      if (lane == 0) tell_chief(&ctl.pin_go[b]);
+    };
+    // (after a wait that ran out these warps still go through every step, each wait returning at
+    // once: the named barriers need both of a row's warps)
+#pragma unroll 1
+    for (int i = 0; i < n_own; ++i) {
+      const int b = i % Lay::kBufs;
+      const int tile = tile0 + 2 * i + c;
+      const TileInfo* info = ws.info + tile_base + tile;
+      const ulonglong2 w = __ldcg(reinterpret_cast<const ulonglong2*>(info));
+      const int e = __ldcg(&info->e);
+      const int nv = lim - tile * kTile;
+      const uint64_t seen64 = w.x & (nv >= kTile ? ~0ull : nv <= 0 ? 0ull : (1ull << nv) - 1ull);
+      const uint32_t seen = static_cast<uint32_t>(seen64 >> (32 * hv)), poison = static_cast<uint32_t>(w.y >> (32 * hv));
+      e_top = max(e_top, e);
+      // (held inside fp32's range: a factor of 0 would turn an unseen position's -inf into NaN)
+      const float kt = fminf(fmaxf(k2 * exp2i(e), 1.2e-38f), 3.0e38f);
+      const float fe = static_cast<float>(e);
+      wait_warp(&ctl.s_full, i);
+      tc::fence_after_sync();
+      uint32_t s[32];
+      tc::tmem_ld32(lane_base + kColS + 32 * hv, s);
+      tc::tmem_wait_ld();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tell_chief(&ctl.s_free);
+      if (!__all_sync(0xffffffffu, seen == ~0u && poison == 0u)) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          if ((poison >> k) & 1u) s[k] = 0x7FFFFFFFu;
+          if (!((seen >> k) & 1u)) s[k] = 0xFF800000u;
         }
       }
-      if (i < n_peer) {
-        e_top = max(e_top, __ldcg(&ws.info[tile_base + tile0 + 2 * i + other].e));
-        wait_warp(&ctl.pin_full, i);
-        if (tid == 4 * 32) tc::mbar_arrive_expect_tx(&ctl.pin_full, kPMsg);  // the next weights
-        __syncwarp();
-        const float r_in = in_r[m];
-        if (__any_sync(0xffffffffu, r_in != rho)) {
-          const bool any_product = i < n_own || i > 0;
-          // every product so far: the last was the own tile's, or the peer's before it
-          if (i < n_own) wait_warp(&ctl.vown_empty[i & 1], i >> 1);
-          else if (i > 0) wait_warp(&ctl.vpeer_empty[(i - 1) % Lay::kPeerBufs], (i - 1) / Lay::kPeerBufs);
-          const bool raise = r_in > rho;
-          rescale(raise ? r_in - rho : 0.f, any_product);
-          if (raise) rho = r_in;
-          if (r_in < rho) {  // sent before the peer learned of this reference (2^-inf = 0)
-            const float f = exp2f(r_in - rho);
-            uint8_t* row = smem + kOffPIn + m * 128;
+      float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint4* at = reinterpret_cast<uint4*>(row + (((4 * hv + k) ^ (m & 7)) << 4));
-              const uint4 u = *at;
-              uint32_t v[4] = {u.x, u.y, u.z, u.w};
+      for (int k = 0; k < 32; k += 4) {
+        t0 = fmaxf(t0, fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
+        t1 = fmaxf(t1, fmaxf(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
+      }
+      const float mt = row_max(fmaf(fmaxf(t0, t1), kt, fe), i & 1);
+      if (i == 0 && c == 0) {
+        rho = mt;
+        if (hv == 0) st_async_f32(dsmem_addr(&ctl.sent[m], peer), rho, dsmem_addr(&ctl.r_full, peer));
+      }
+      // the reference these weights are made with: the row's, or a new one where a weight would pass
+      // 2^14 or at the row's first position
+      const bool raise = mt > rho + kHeadroom || (rho == -INFINITY && mt > -INFINITY);
+      const float rho_p = raise ? mt : rho;
+      const float off = fe - (rho_p == -INFINITY ? 0.f : rho_p);
+      uint32_t p[16];
+      float x0 = 0.f, x1 = 0.f;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float2 h = unpack_half2(v[j]);
-                v[j] = pack_half2(h.x * f, h.y * f);
-              }
-              *at = make_uint4(v[0], v[1], v[2], v[3]);
-            }
+      for (int k = 0; k < 32; k += 2) {
+        const float a0 = exp2_approx(fmaf(__uint_as_float(s[k]), kt, off));
+        const float a1 = exp2_approx(fmaf(__uint_as_float(s[k + 1]), kt, off));
+        p[k >> 1] = pack_half2(a0, a1);
+        x0 += a0;
+        x1 += a1;
+      }
+      float sum = x0 + x1;
+      // the tile before this one in the order of the products: its weights have had this tile's
+      // Q K^T and softmax to arrive
+      if (i > 0) reconcile(i - 1);
+      if (__any_sync(0xffffffffu, rho_p != rho)) {
+        if (i > 0) wait_warp(&ctl.v_empty[Lay::peer_slot(i - 1, n_own)], Lay::peer_phase(i - 1, n_own));  // every product so far
+        const bool up = rho_p > rho;
+        rescale(up ? rho_p - rho : 0.f, i > 0);
+        if (up) rho = rho_p;
+        if (rho_p < rho) {  // the peer went ahead meanwhile (2^-inf = 0)
+          const float f = exp2f(rho_p - rho);
+          sum *= f;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 h = unpack_half2(p[k]);
+            p[k] = pack_half2(h.x * f, h.y * f);
           }
-          tc::fence_async_smem();
-          tc::fence_before_sync();
-          __syncwarp();
         }
-        if (lane == 0) tell_chief(&ctl.pin_go);
+      }
+      l = fmaf(sum, exp2i(-e), l);
+      wait_warp(&ctl.p_empty[b], i / Lay::kBufs + 1);
+      uint8_t* p_own = smem + Lay::p_own + b * kPStride;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4*>(p_own + m * 128 + (((4 * hv + k) ^ (m & 7)) << 4)) =
+            make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+      if (hv == 0) reinterpret_cast<float*>(p_own + kPBytes)[m] = rho;
+      tc::fence_async_smem();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&ctl.p_mine[b]);
+        tell_chief(&ctl.p_full[b]);
       }
     }
+    for (int i = max(0, n_own - 1); i < n_peer; ++i) reconcile(i);
     // the last weights have been read, here and by the peer (whose word of it has then arrived)
-    if (n_own > 0) wait_warp(&ctl.p_empty, n_own - 1);
+    for (int i = max(0, n_own - Lay::kBufs); i < n_own; ++i) wait_warp(&ctl.p_empty[i % Lay::kBufs], i / Lay::kBufs);
     // ---- the row's sum over its two threads and both CTAs ----
     ctl.part[0][hv][m] = l;
     asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
     l = ctl.part[0][0][m] + ctl.part[0][1][m];
-    if (hv == 0) st_async_f32(dsmem_addr(&ctl.fin[m], peer), l, dsmem_addr(&ctl.fin_full, peer));
-    if (wait_warp(&ctl.fin_full, 0)) l = c == 0 ? l + ctl.fin[m] : ctl.fin[m] + l;  // the same in both CTAs
+    if (hv == 0) st_async_f32(dsmem_addr(&ctl.sent[m], peer), l, dsmem_addr(&ctl.fin_full, peer));
+    if (wait_warp(&ctl.fin_full, 0)) l = c == 0 ? l + ctl.sent[m] : ctl.sent[m] + l;  // the same in both CTAs
   }
   // every product is complete, and nothing the peer sends is still on its way
   wait(&ctl.o_done, 0);
@@ -1009,8 +1047,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constan
   // ---- output: O / l through the tiles' shared memory, in whole rows: bf16, or with several
   // splits fp16 times 2^-(e_out), e_out the largest exponent of the item's tiles: |O / l| is at
   // most the largest value, below 2^15 2^e_out ----
-  uint8_t* stage = smem + kOffKv;
-  if (warp >= 4) {
+  uint8_t* stage = smem + Lay::v;
+  if (warp >= 4 && warp < 12) {
     const int hv = (warp - 4) >> 2, m = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int e_out = e_top;
@@ -1190,11 +1228,12 @@ cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char**
     return cudaErrorInvalidValue;
   }
   const auto attend = pl.g == 2 ? attend_kernel<2> : attend_kernel<1>;
-  cudaError_t e = cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+  const uint32_t smem = pl.g == 2 ? kSmemBytes<2> : kSmemBytes<1>;
+  cudaError_t e = cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   e = launch_pdl(expand_kernel, dim3(static_cast<unsigned>(pl.rows_kv / kTile)), dim3(kExpandThreads), 0, s, 1, a, pl, ws);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attend, dim3(static_cast<unsigned>(2 * pl.g * items)), dim3(kThreads), kSmemBytes, s, 2 * pl.g, tile_map,
+  e = launch_pdl(attend, dim3(static_cast<unsigned>(2 * pl.g * items)), dim3(kThreads), smem, s, 2 * pl.g, tile_map,
                  half_map, a, pl, ws);
   if (e != cudaSuccess || pl.sp + pl.st == 1) return e;
   return launch_pdl(prefix_merge_kernel, dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows)),
