@@ -107,6 +107,8 @@ template <int G> struct Layout {
 };
 
 struct PairCtl {
+  uint64_t q_full;                             // the query's rows have landed
+  uint64_t q_moved;                            // and their staging space is free for tiles
   uint64_t q_ready;                            // the query is in tensor and shared memory
   uint64_t k_full[kLoose], k_empty[kLoose];    // G = 1: the five loose blocks; G = 2: the five pieces
   uint64_t v_full[3], v_empty[3];              // value tiles: landed; read by their P V
@@ -127,8 +129,10 @@ struct PairCtl {
 };
 template <int G> constexpr uint32_t kSmemBytes = Layout<G>::ctl + 3072;
 static_assert(sizeof(PairCtl) <= 3072 && kPieces == kLoose && kSmemBytes<1> <= 232448 && kSmemBytes<2> <= 232448, "shared memory");
-// the output rows are staged where the tiles' blocks were
+// the query's dims 0..383 and the output rows are staged where the tiles go
 constexpr int kStagePitch = kHalfV * 2 + 16;
+static_assert(kQTmemBlocks * kQBlock <= Layout<1>::ctl - Layout<1>::v && kQTmemBlocks * kQBlock <= Layout<2>::ctl - Layout<2>::v,
+              "query staging");
 static_assert(kRows * kStagePitch <= Layout<1>::ctl - Layout<1>::v && kRows * kStagePitch <= Layout<2>::ctl - Layout<2>::v,
               "output staging");
 
@@ -573,8 +577,8 @@ __device__ __forceinline__ void qk_loop_pair(PairCtl& ctl, int n_own, uint16_t p
 
 template <int G>
 __global__ void __launch_bounds__(kThreads, 1)
-attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constant__ CUtensorMap half_map, PrefixArgs a,
-              PrefixPlan pl, PrefixWs ws) {
+attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap tile_map,
+              const __grid_constant__ CUtensorMap half_map, PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
   using Lay = Layout<G>;
   extern __shared__ __align__(1024) uint8_t smem[];
   PairCtl& ctl = *reinterpret_cast<PairCtl*>(smem + Lay::ctl);
@@ -643,6 +647,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constan
   }
   if (tid == 0) {
     ctl.abort = 0;
+    tc::mbar_init(&ctl.q_full, 1);
+    tc::mbar_init(&ctl.q_moved, kSoftWarps);
     tc::mbar_init(&ctl.q_ready, G * kSoftWarps);
     for (int k = 0; k < kLoose; ++k) {
       tc::mbar_init(&ctl.k_full[k], 1);
@@ -703,9 +709,14 @@ attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constan
   if (warp == 0) {
     // ---------------- own tiles ----------------
     if (lane == 0) {
+      // the query's rows first (those past the last one read as zero), through the tiles' space
+      tc::mbar_arrive_expect_tx(&ctl.q_full, 9 * kQBlock);
+      for (int k = 0; k < 9; ++k)
+        tc::tma_load_3d(smem + (k < kQTmemBlocks ? Lay::v + k * kQBlock : kOffQ + (k - kQTmemBlocks) * kQBlock), &q_map, 64 * k,
+                        static_cast<int>(row0), 0, &ctl.q_full);
       tc::prefetch_tmap(&tile_map);
       if constexpr (G == 2) tc::prefetch_tmap(&half_map);
-      bool ok = true;
+      bool ok = wait(&ctl.q_moved, 0);
 #pragma unroll 1
       for (int i = 0; i < n_own && ok; ++i) {
         const int b = i & 1, y = (tile_base + tile0 + 2 * i + c) * kTile;
@@ -781,7 +792,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constan
     __syncwarp();
   } else if (warp == 3) {
     // ---------------- value blocks of the peer's tiles, and in a pair of the own ones, in the products' order ----
-    if (lane == 0) {
+    if (lane == 0 && wait(&ctl.q_moved, 0)) {
 #pragma unroll 1
       for (int i = 0; i < n_peer || (G == 2 && i < n_own); ++i) {
         const int y = (tile_base + tile0 + 2 * i) * kTile;
@@ -826,16 +837,21 @@ attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constan
     };
     float k2;  // logit (in powers of two) = S * k2 * 2^(tile's exponent)
     {  // the query as fp16 by a power of two per row: dims 0..319 by hv 0, the rest by hv 1
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (row0 + m) * kLatent);
-      const int first = hv ? 40 : 0, last = hv ? 72 : 40;
+      const int first = hv ? 5 : 0, last = hv ? 9 : 5;  // 64-dim blocks
+      auto chunk = [&](int kb, int j) {  // 8 dims of this row
+        uint8_t* base = smem + (kb < kQTmemBlocks ? Lay::v + kb * kQBlock : kOffQ + (kb - kQTmemBlocks) * kQBlock);
+        return reinterpret_cast<uint4*>(base + m * 128 + ((j ^ (m & 7)) << 4));
+      };
+      wait_warp(&ctl.q_full, 0);
       __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
-      if (live) {
-#pragma unroll 8
-        for (int i = first; i < last; ++i) {
-          const uint4 u = __ldg(src + i);
+#pragma unroll 1
+      for (int kb = first; kb < last; ++kb) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 u = *chunk(kb, j);
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[j])));
+          for (int n = 0; n < 4; ++n) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[n])));
         }
       }
       const float top = row_max(fmaxf(__low2float(top2), __high2float(top2)), 1);
@@ -843,35 +859,32 @@ attend_kernel(const __grid_constant__ CUtensorMap tile_map, const __grid_constan
       const int qe = top > 0.f ? min(max(static_cast<int>(__float_as_uint(top) >> 23), 1), 254) - 127 - 14 : 0;
       const float f0 = exp2i(-(qe / 2)), f1 = exp2i(-(qe - qe / 2));
       k2 = a.sm_scale * 1.4426950408889634f * exp2i(qe / 2) * exp2i(qe - qe / 2);
-      auto scaled = [&](int i) {
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (live) u = __ldg(src + i);
-        uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = pack_half2(__uint_as_float(w[j] << 16) * f0 * f1, __uint_as_float(w[j] & 0xFFFF0000u) * f0 * f1);
-        return make_uint4(w[0], w[1], w[2], w[3]);
-      };
-      for (int h = hv ? 5 : 0; h < (hv ? 6 : 5); ++h) {
+#pragma unroll 1
+      for (int kb = first; kb < last; ++kb) {
         uint32_t v[32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 u = scaled(8 * h + i);
-          v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
+        for (int j = 0; j < 8; ++j) {
+          const uint4 u = *chunk(kb, j);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int n = 0; n < 4; ++n)  // (rows past the item's are other rows' data: zero)
+            v[4 * j + n] = live ? pack_half2(__uint_as_float(w[n] << 16) * f0 * f1, __uint_as_float(w[n] & 0xFFFF0000u) * f0 * f1) : 0u;
         }
-        tmem_store32(lane_base + kColQ + 32 * h, v);
+        if (kb < kQTmemBlocks) {
+          tmem_store32(lane_base + kColQ + 32 * kb, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) *chunk(kb, j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
       }
-      if (hv) {
-#pragma unroll 4
-        for (int i = 0; i < 8 * kQSmemBlocks; ++i)
-          *reinterpret_cast<uint4*>(smem + kOffQ + (i >> 3) * kQBlock + m * 128 + (((i & 7) ^ (m & 7)) << 4)) =
-              scaled(8 * kQTmemBlocks + i);
-        tc::fence_async_smem();
-      }
+      tc::fence_async_smem();  // (also orders the reads above before the tiles that follow them)
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tell_chief(&ctl.q_ready);
+      if (lane == 0) {
+        tc::mbar_arrive(&ctl.q_moved);
+        tell_chief(&ctl.q_ready);
+      }
     }
     // positions of this part the row sees
     int lim = 0;
@@ -1182,14 +1195,15 @@ EncodeFn encode_fn() {
   }();
   return fn;
 }
-// rows of 576 fp16 in boxes of 64 dims x box_rows, 128-byte swizzle
-bool encode_rows(EncodeFn enc, CUtensorMap* map, void* base, int64_t rows, int box_rows) {
+// rows of 576 16-bit values in boxes of 64 dims x box_rows, 128-byte swizzle; rows past the end
+// read as zero
+bool encode_rows(EncodeFn enc, CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows, int box_rows) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kLatent), static_cast<cuuint64_t>(rows), 1};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kLatent) * 2,
                                  static_cast<cuuint64_t>(kLatent) * 2 * static_cast<cuuint64_t>(rows)};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t one[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box, one,
+  return enc(map, type, 3, const_cast<void*>(base), dims, strides, box, one,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1222,8 +1236,10 @@ cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char**
     *err = "prefix_attn: cuTensorMapEncodeTiled is not available";
     return cudaErrorNotSupported;
   }
-  CUtensorMap tile_map, half_map;
-  if (!encode_rows(enc, &tile_map, ws.kv, pl.rows_kv, kTile) || !encode_rows(enc, &half_map, ws.kv, pl.rows_kv, kTile / 2)) {
+  CUtensorMap q_map, tile_map, half_map;
+  if (!encode_rows(enc, &q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, rows, kRows) ||
+      !encode_rows(enc, &tile_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws.kv, pl.rows_kv, kTile) ||
+      !encode_rows(enc, &half_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws.kv, pl.rows_kv, kTile / 2)) {
     *err = "prefix_attn: tensor map encoding failed";
     return cudaErrorInvalidValue;
   }
@@ -1233,8 +1249,8 @@ cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char**
   if (e != cudaSuccess) return e;
   e = launch_pdl(expand_kernel, dim3(static_cast<unsigned>(pl.rows_kv / kTile)), dim3(kExpandThreads), 0, s, 1, a, pl, ws);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attend, dim3(static_cast<unsigned>(2 * pl.g * items)), dim3(kThreads), smem, s, 2 * pl.g, tile_map,
-                 half_map, a, pl, ws);
+  e = launch_pdl(attend, dim3(static_cast<unsigned>(2 * pl.g * items)), dim3(kThreads), smem, s, 2 * pl.g, q_map,
+                 tile_map, half_map, a, pl, ws);
   if (e != cudaSuccess || pl.sp + pl.st == 1) return e;
   return launch_pdl(prefix_merge_kernel, dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows)),
                     dim3(64 * kMergeRows), 0, s, 1, a, pl, ws);
