@@ -94,6 +94,13 @@ template <int G> struct Layout {
   static constexpr int kVBytes = 4 * kBlock / G, kVSlots = 3, kBufs = G;
   static constexpr uint32_t p_own = kOffP, p_in = p_own + kBufs * kPStride, v = p_in + kBufs * kPStride;
   static constexpr uint32_t k = v + kVSlots * kVBytes, ctl = k + (G == 1 ? kLoose * kBlock : kPieces * kPiece);
+  // the query's 64-dim blocks: dims 0..383 staged where the first tiles for Q K^T do not go, so that
+  // these load meanwhile (G = 1: value slot 0; G = 2: pieces 0..2)
+  static __host__ __device__ constexpr uint32_t q_block(int kb) {
+    return kb >= kQTmemBlocks ? kOffQ + (kb - kQTmemBlocks) * kQBlock
+           : G == 1           ? (kb < 4 ? v + kVBytes + kb * kQBlock : kb == 4 ? p_own : k)
+                              : (kb < 3 ? v + kb * kQBlock : kb < 5 ? p_own + (kb - 3) * kPStride : k + 3 * kPiece);
+  }
   // slot of a tile's values and how often the slot was filled before: own tile i is product 2 i, peer
   // tile i follows it (or, where there is none, the last one)
   static __host__ __device__ constexpr int own_slot(int i) { return G == 1 ? i % 2 : 2 * i % 3; }
@@ -131,7 +138,8 @@ template <int G> constexpr uint32_t kSmemBytes = Layout<G>::ctl + 3072;
 static_assert(sizeof(PairCtl) <= 3072 && kPieces == kLoose && kSmemBytes<1> <= 232448 && kSmemBytes<2> <= 232448, "shared memory");
 // the query's dims 0..383 and the output rows are staged where the tiles go
 constexpr int kStagePitch = kHalfV * 2 + 16;
-static_assert(kQTmemBlocks * kQBlock <= Layout<1>::ctl - Layout<1>::v && kQTmemBlocks * kQBlock <= Layout<2>::ctl - Layout<2>::v,
+static_assert(4 * kQBlock == 2 * Layout<1>::kVBytes && kQBlock <= kLoose * kBlock && 3 * kQBlock == 3 * Layout<2>::kVBytes &&
+                  kQBlock <= 2 * kPiece && Layout<2>::q_block(5) % 1024 == 0,
               "query staging");
 static_assert(kRows * kStagePitch <= Layout<1>::ctl - Layout<1>::v && kRows * kStagePitch <= Layout<2>::ctl - Layout<2>::v,
               "output staging");
@@ -163,9 +171,9 @@ size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // The plan of least estimated time: MMAs of one CTA (128 rows an item, two CTAs) or of CTA
 // pairs (256 rows, four CTAs), and the splits.  An item of n tiles takes about fix + per n us on
-// one of the clusters that fit at once; a further split costs every row its partial output,
-// once written and once read.  Pairs halve what each tile costs in shared memory, but few items
-// or tails, whose rows share no tiles, leave half of a pair idle.
+// one of the clusters that fit at once (measured: 8 + 1.33 n with one CTA, 8 + 0.62 n with pairs); a
+// further split costs every row its partial output, once written and once read.  Tails, whose
+// rows share no tiles, leave half of a pair idle.
 PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, int n_sm) {
   PrefixPlan p{};
   p.tiles_p = (prefix_len + kTile - 1) / kTile;
@@ -177,16 +185,18 @@ PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, i
     if (g == 2 && (p.mt < 2 || !p.tiles_p)) break;
     // (152 SMs hold 76 clusters of two CTAs of this size, 36 of four)
     const int fit = std::max(1, g == 1 ? n_sm / 2 : n_sm / 4 - n_sm / 76);
-    const double fix = 6.0, per = g == 1 ? 1.05 : 0.75;
-    for (int sp = p.tiles_p ? 1 : 0; sp <= std::min(p.tiles_p, 48); ++sp) {
+    const int mt = (p.mt + g - 1) / g;
+    const double fix = 8.0, per = g == 1 ? 1.33 : 0.62;
+    for (int waves = 1; waves <= 6; ++waves) {  // as many splits as fill so many waves
+      const int sp = p.tiles_p ? std::min({p.tiles_p, std::max(1, static_cast<int>(static_cast<int64_t>(waves) * fit / mt)), 64}) : 0;
       for (int st = p.tiles_t ? 1 : 0; st <= std::min(p.tiles_t, 16); st = st ? 2 * st : 1) {
         const double lp = sp ? fix + per * ((p.tiles_p + sp - 1) / sp) : 0.0;
         const double lt = st ? fix + per * ((p.tiles_t + st - 1) / st) : 0.0;
-        const double np = static_cast<double>((p.mt + g - 1) / g) * sp, nt = static_cast<double>(n_q) * st;
-        const double waves = static_cast<double>(static_cast<int64_t>((np + fit - 1) / fit));
+        const int64_t np = static_cast<int64_t>(mt) * sp;
         // the tails are counted half full: their lengths are known to the device alone
-        const double total = (np * lp + nt * (fix + 0.5 * (lt - fix))) / fit;
-        const double t = std::max({waves * lp, total + (st ? 0.5 * lt : 0.0), lt}) + (sp + st > 1 ? join * (sp + st) + 3.0 : 0.0);
+        const double total = (np * lp + static_cast<double>(n_q) * st * (fix + 0.5 * (lt - fix))) / fit;
+        const double t = std::max({static_cast<double>((np + fit - 1) / fit) * lp, total + 0.5 * lt, lt}) +
+                         (sp + st > 1 ? join * (sp + st) + 3.0 : 0.0);
         if (t < best) {
           best = t;
           p.g = g;
@@ -649,7 +659,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     ctl.abort = 0;
     tc::mbar_init(&ctl.q_full, 1);
     tc::mbar_init(&ctl.q_moved, kSoftWarps);
-    tc::mbar_init(&ctl.q_ready, G * kSoftWarps);
+    tc::mbar_init(&ctl.q_ready, G * 12);
     for (int k = 0; k < kLoose; ++k) {
       tc::mbar_init(&ctl.k_full[k], 1);
       tc::mbar_init(&ctl.k_empty[k], 1);
@@ -675,12 +685,20 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     if (c == 1) tc::mbar_arrive_expect_tx(&ctl.r_full, kRows * 4);
     tc::mbar_arrive_expect_tx(&ctl.fin_full, kRows * 4);
     for (int k = 0; k < Lay::kBufs; ++k) tc::mbar_arrive_expect_tx(&ctl.pin_full[k], kPMsg);
+    // the query's rows (those past the last one read as zero)
+    tc::fence_async_smem();
+    tc::mbar_arrive_expect_tx(&ctl.q_full, 9 * kQBlock);
+#pragma unroll 1
+    for (int k = 0; k < 9; ++k)
+      tc::tma_load_3d(smem + Lay::q_block(k), &q_map, 64 * k, static_cast<int>(row0), 0, &ctl.q_full);
+    tc::prefetch_tmap(&tile_map);
+    if constexpr (G == 2) tc::prefetch_tmap(&half_map);
   }
-  __syncthreads();
-  cluster_sync();  // every CTA's barriers are ready
+  __syncwarp();
   if (warp == 1) tmem_alloc_all<G>(&ctl.tmem_base);
   tc::fence_before_sync();
   __syncthreads();
+  cluster_sync();  // every CTA's barriers are ready
   tc::fence_after_sync();
   // all 512 columns are this CTA's, so its addresses start at 0 and are constants below
   if (tid == 0 && ctl.tmem_base != 0) {
@@ -703,29 +721,110 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     else arrive_at(bar, chief);
   };
 
+  // ---- the query as fp16 by a power of two per row: warps 4..7 take dims 0..191 and warps 8..11
+  // 192..383 into tensor memory, warps 0..3 the rest, in place; three threads a row ----
+  float k2 = 0.f;  // logit (in powers of two) = S * k2 * 2^(tile's exponent)
+  auto turn_query = [&] {
+    const int quarter = warp & 3, m = quarter * 32 + lane, third = warp >> 2;
+    const int first = third == 0 ? 6 : 3 * (third - 1);  // 64-dim blocks
+    auto chunk = [&](int kb, int j) {                    // 8 dims of this row
+      return reinterpret_cast<uint4*>(smem + Lay::q_block(kb) + m * 128 + ((j ^ (m & 7)) << 4));
+    };
+    wait_warp(&ctl.q_full, 0);
+    __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll 1
+    for (int kb = first; kb < first + 3; ++kb) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint4 u = *chunk(kb, j);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[n])));
+      }
+    }
+    float top = fmaxf(__low2float(top2), __high2float(top2));
+    float* part = &ctl.part[0][0][0];  // (three of the four rows of maxima; free again after the second barrier)
+    part[third * kRows + m] = top;
+    asm volatile("bar.sync %0, 96;" :: "r"(1 + quarter) : "memory");
+    top = fmaxf(fmaxf(part[m], part[kRows + m]), part[2 * kRows + m]);
+    asm volatile("bar.sync %0, 96;" :: "r"(1 + quarter) : "memory");
+    // top * 2^-qe in [2^14, 2^15) (below that for a row of values under 2^-112 alone)
+    const int qe = top > 0.f ? min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -126), 113) : 0;
+    // (a row past the item's is another item's data: zero)
+    const float f = exp2i(-qe);
+    k2 = a.sm_scale * 1.4426950408889634f * exp2i(qe);
+    const bool live = m < n_rows;
+#pragma unroll 1
+    for (int kb = first; kb < first + 3; ++kb) {
+      uint32_t v[32];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint4 u = *chunk(kb, j);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          v[4 * j + n] = live ? pack_half2(__uint_as_float(w[n] << 16) * f, __uint_as_float(w[n] & 0xFFFF0000u) * f) : 0u;
+      }
+      if (third > 0) {
+        tmem_store32((static_cast<uint32_t>(quarter * 32) << 16) + kColQ + 32 * kb, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) *chunk(kb, j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      }
+    }
+    tc::fence_async_smem();  // (also orders the reads above before the tiles that follow them)
+    tc::tmem_wait_st();
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) {
+      if (third > 0) tc::mbar_arrive(&ctl.q_moved);
+      tell_chief(&ctl.q_ready);
+    }
+  };
+  // loads of own tile i: G = 1: its kept value blocks; G = 2: this CTA's positions for Q K^T
+  auto load_values = [&](int i) {
+    const int b = i & 1;
+    if (!wait(&ctl.v_empty[b], (i >> 1) + 1)) return false;
+    tc::mbar_arrive_expect_tx(&ctl.v_full[b], Lay::kVBytes);
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k)
+      load_box<G>(smem + Lay::v + (4 * b + k) * kBlock, &tile_map, 64 * (4 * c + k), (tile_base + tile0 + 2 * i + c) * kTile,
+                  &ctl.v_full[b]);
+    return true;
+  };
+  auto load_pieces = [&](int i) {
+#pragma unroll 1
+    for (int k = 0; k < 3; ++k) {
+      const int n = 3 * i + k, slot_k = n % kPieces;
+      if (!wait(&ctl.k_empty[slot_k], n / kPieces + 1)) return false;
+      if (g == 0) tc::mbar_arrive_expect_tx(&ctl.k_full[slot_k], 2 * kPiece);
+#pragma unroll 1
+      for (int j = 0; j < 3; ++j)
+        load_box<G>(smem + Lay::k + slot_k * kPiece + j * (kBlock / 2), &half_map, 64 * (3 * k + j),
+                    (tile_base + tile0 + 2 * i + c) * kTile + 32 * g, &ctl.k_full[slot_k]);
+    }
+    return true;
+  };
+  if (tid == 0 && n_own > 0) {  // the first tile's, beside the query
+    if constexpr (G == 1) load_values(0);
+    else load_pieces(0);
+  }
+  __syncwarp();
+  if (warp < 12) turn_query();
+
   // softmax threads: their row's state, kept from the loop to the output
   float rho = -INFINITY, l = 0.f;
   int e_top = -1000;
   if (warp == 0) {
     // ---------------- own tiles ----------------
-    if (lane == 0) {
-      // the query's rows first (those past the last one read as zero), through the tiles' space
-      tc::mbar_arrive_expect_tx(&ctl.q_full, 9 * kQBlock);
-      for (int k = 0; k < 9; ++k)
-        tc::tma_load_3d(smem + (k < kQTmemBlocks ? Lay::v + k * kQBlock : kOffQ + (k - kQTmemBlocks) * kQBlock), &q_map, 64 * k,
-                        static_cast<int>(row0), 0, &ctl.q_full);
-      tc::prefetch_tmap(&tile_map);
-      if constexpr (G == 2) tc::prefetch_tmap(&half_map);
-      bool ok = wait(&ctl.q_moved, 0);
+    if (lane == 0 && wait(&ctl.q_moved, 0)) {
+      bool ok = true;
 #pragma unroll 1
       for (int i = 0; i < n_own && ok; ++i) {
-        const int b = i & 1, y = (tile_base + tile0 + 2 * i + c) * kTile;
         if constexpr (G == 1) {
           // the half of the value blocks this CTA keeps, then the other blocks
-          if (!wait(&ctl.v_empty[b], (i >> 1) + 1)) break;
-          tc::mbar_arrive_expect_tx(&ctl.v_full[b], Lay::kVBytes);
-          for (int k = 0; k < 4; ++k)
-            load_box<G>(smem + Lay::v + (4 * b + k) * kBlock, &tile_map, 64 * (4 * c + k), y, &ctl.v_full[b]);
+          if (i > 0 && !load_values(i)) break;
+          const int y = (tile_base + tile0 + 2 * i + c) * kTile;
 #pragma unroll 1
           for (int k = 0; k < kLoose; ++k) {
             ok = wait(&ctl.k_empty[k], i + 1);
@@ -733,18 +832,8 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             tc::mbar_arrive_expect_tx(&ctl.k_full[k], kBlock);
             load_box<G>(smem + Lay::k + k * kBlock, &tile_map, 64 * (k < 4 ? 4 * other + k : 8), y, &ctl.k_full[k]);
           }
-        } else {
-          // this CTA's 32 positions for Q K^T
-#pragma unroll 1
-          for (int k = 0; k < 3; ++k) {
-            const int n = 3 * i + k, slot_k = n % kPieces;
-            ok = wait(&ctl.k_empty[slot_k], n / kPieces + 1);
-            if (!ok) break;
-            if (g == 0) tc::mbar_arrive_expect_tx(&ctl.k_full[slot_k], 2 * kPiece);
-            for (int j = 0; j < 3; ++j)
-              load_box<G>(smem + Lay::k + slot_k * kPiece + j * (kBlock / 2), &half_map, 64 * (3 * k + j), y + 32 * g,
-                          &ctl.k_full[slot_k]);
-          }
+        } else if (i > 0) {
+          ok = load_pieces(i);
         }
       }
     }
@@ -835,57 +924,6 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
       return fmaxf(v, ctl.part[slot_k][hv ^ 1][m]);
     };
-    float k2;  // logit (in powers of two) = S * k2 * 2^(tile's exponent)
-    {  // the query as fp16 by a power of two per row: dims 0..319 by hv 0, the rest by hv 1
-      const int first = hv ? 5 : 0, last = hv ? 9 : 5;  // 64-dim blocks
-      auto chunk = [&](int kb, int j) {  // 8 dims of this row
-        uint8_t* base = smem + (kb < kQTmemBlocks ? Lay::v + kb * kQBlock : kOffQ + (kb - kQTmemBlocks) * kQBlock);
-        return reinterpret_cast<uint4*>(base + m * 128 + ((j ^ (m & 7)) << 4));
-      };
-      wait_warp(&ctl.q_full, 0);
-      __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll 1
-      for (int kb = first; kb < last; ++kb) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 u = *chunk(kb, j);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int n = 0; n < 4; ++n) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[n])));
-        }
-      }
-      const float top = row_max(fmaxf(__low2float(top2), __high2float(top2)), 1);
-      // top * 2^-qe in [2^14, 2^15); zero, subnormal and infinite rows stay within the exponents
-      const int qe = top > 0.f ? min(max(static_cast<int>(__float_as_uint(top) >> 23), 1), 254) - 127 - 14 : 0;
-      const float f0 = exp2i(-(qe / 2)), f1 = exp2i(-(qe - qe / 2));
-      k2 = a.sm_scale * 1.4426950408889634f * exp2i(qe / 2) * exp2i(qe - qe / 2);
-#pragma unroll 1
-      for (int kb = first; kb < last; ++kb) {
-        uint32_t v[32];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 u = *chunk(kb, j);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int n = 0; n < 4; ++n)  // (rows past the item's are other rows' data: zero)
-            v[4 * j + n] = live ? pack_half2(__uint_as_float(w[n] << 16) * f0 * f1, __uint_as_float(w[n] & 0xFFFF0000u) * f0 * f1) : 0u;
-        }
-        if (kb < kQTmemBlocks) {
-          tmem_store32(lane_base + kColQ + 32 * kb, v);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) *chunk(kb, j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        }
-      }
-      tc::fence_async_smem();  // (also orders the reads above before the tiles that follow them)
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(&ctl.q_moved);
-        tell_chief(&ctl.q_ready);
-      }
-    }
     // positions of this part the row sees
     int lim = 0;
     if (live) {
@@ -1068,7 +1106,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
     const float down = exp2i(-e_out);
     uint8_t* row = stage + m * kStagePitch;
-#pragma unroll
+#pragma unroll 2
     for (int k = 0; k < 4; ++k) {
       const int col = 128 * hv + 32 * k;
       uint32_t v[32];
@@ -1102,6 +1140,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   {
     const int piece = tid & 31;
     uint16_t* const base = ns == 1 ? static_cast<uint16_t*>(a.out) : reinterpret_cast<uint16_t*>(ws.o);
+#pragma unroll 5
     for (int m = tid >> 5; m < n_rows; m += kThreads / 32) {
       const int64_t at = ns == 1 ? row0 + m : (row0 + m) * ns + slot;
       *reinterpret_cast<uint4*>(base + at * kVDim + kHalfV * c + 8 * piece) =
