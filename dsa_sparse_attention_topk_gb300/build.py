@@ -14,7 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdsa.so")
-SOURCES = ["api.cu", "quant.cu", "indexer_tc.cu", "sfa_tc.cu", "cp_merge.cu", "rope.cu", "prefix_attn.cu"]
+SOURCES = ["api.cu", "quant.cu", "indexer_tc.cu", "sfa_tc.cu", "cp_merge.cu", "rope.cu", "prefix_attn.cu", "prefix_few.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",

@@ -57,8 +57,7 @@
 #include <algorithm>
 #include <cuda.h>
 
-#include "dsa_common.cuh"
-#include "dsa_launch.h"
+#include "prefix_common.cuh"
 #include "tc_utils.cuh"
 
 namespace dsa {
@@ -144,6 +143,9 @@ static_assert(4 * kQBlock == 2 * Layout<1>::kVBytes && kQBlock <= kLoose * kBloc
 static_assert(kRows * kStagePitch <= Layout<1>::ctl - Layout<1>::v && kRows * kStagePitch <= Layout<2>::ctl - Layout<2>::v,
               "output staging");
 
+// A split costs every row its partial output, once written and once read, at some 5 TB/s.
+constexpr double kJoinUs = 2048.0 / 5.0e6, kFewUs16 = 1.2, kFewUs32 = 1.2;
+
 // What expand writes per tile.
 struct alignas(32) TileInfo {
   uint64_t valid, poison;    // a bit per position
@@ -153,8 +155,11 @@ struct alignas(32) TileInfo {
 
 struct PrefixPlan {
   int tiles_p, tiles_t;      // tiles of the prefix, and of the longest possible tail
-  int sp, st;                // splits of the prefix and of each tail
+  int sp, st;                // splits of the prefix and of each tail on the tensor-memory path
+  int few_lo, few;           // first position and splits of each row on the path for few heads (0: not taken)
+  int ns;                    // all splits of a row
   int mt;                    // 128-row tiles of the flattened rows
+  int n_seq, h_s;
   int g;                     // of them in one item: MMAs of one CTA or of a pair
   int64_t rows_kv;           // rows of the expanded cache
   size_t off_info, off_o, off_ml, bytes;
@@ -169,24 +174,19 @@ struct PrefixWs {
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-// The plan of least estimated time: MMAs of one CTA (128 rows an item, two CTAs) or of CTA
-// pairs (256 rows, four CTAs), and the splits.  An item of n tiles takes about fix + per n us on
-// one of the clusters that fit at once (measured: 8 + 1.33 n with one CTA, 8 + 0.62 n with pairs); a
-// further split costs every row its partial output, once written and once read.  Tails, whose
-// rows share no tiles, leave half of a pair idle.
-PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, int n_sm) {
-  PrefixPlan p{};
-  p.tiles_p = (prefix_len + kTile - 1) / kTile;
-  p.tiles_t = (max_ctx - prefix_len + kTile - 1) / kTile;
-  p.mt = static_cast<int>((static_cast<int64_t>(n_q) * h_s + kRows - 1) / kRows);
-  const double join = 2048.0 * n_q * h_s / 5.0e6;  // us a split
+// The tensor-memory path's plan of least estimated time: MMAs of one CTA (128 rows an item, two
+// CTAs) or of CTA pairs (256 rows, four CTAs), and the splits.  An item of n tiles takes about
+// 9 + 1.33 n us with one CTA per parity and 11 + 0.62 n us with pairs, on one of the clusters that
+// fit at once.  Tails, whose rows share no tiles, leave half of a pair idle.  Returns the us.
+double plan_tiles(PrefixPlan& p, int n_q, int n_sm) {
   double best = 1e30;
+  if (!p.tiles_p && !p.tiles_t) return 0.0;
   for (int g = 1; g <= 2; ++g) {
     if (g == 2 && (p.mt < 2 || !p.tiles_p)) break;
     // (152 SMs hold 76 clusters of two CTAs of this size, 36 of four)
     const int fit = std::max(1, g == 1 ? n_sm / 2 : n_sm / 4 - n_sm / 76);
     const int mt = (p.mt + g - 1) / g;
-    const double fix = 8.0, per = g == 1 ? 1.33 : 0.62;
+    const double fix = g == 1 ? 9.0 : 11.0, per = g == 1 ? 1.33 : 0.62;
     for (int waves = 1; waves <= 6; ++waves) {  // as many splits as fill so many waves
       const int sp = p.tiles_p ? std::min({p.tiles_p, std::max(1, static_cast<int>(static_cast<int64_t>(waves) * fit / mt)), 64}) : 0;
       for (int st = p.tiles_t ? 1 : 0; st <= std::min(p.tiles_t, 16); st = st ? 2 * st : 1) {
@@ -195,8 +195,7 @@ PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, i
         const int64_t np = static_cast<int64_t>(mt) * sp;
         // the tails are counted half full: their lengths are known to the device alone
         const double total = (np * lp + static_cast<double>(n_q) * st * (fix + 0.5 * (lt - fix))) / fit;
-        const double t = std::max({static_cast<double>((np + fit - 1) / fit) * lp, total + 0.5 * lt, lt}) +
-                         (sp + st > 1 ? join * (sp + st) + 3.0 : 0.0);
+        const double t = std::max({static_cast<double>((np + fit - 1) / fit) * lp, total + 0.5 * lt, lt}) + kJoinUs * n_q * p.h_s * (sp + st);
         if (t < best) {
           best = t;
           p.g = g;
@@ -208,54 +207,61 @@ PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, i
       if (!p.tiles_p) break;
     }
   }
+  // the expansion, at some 5 TB/s (tails half full), and two more launches
+  const double positions = 64.0 * p.tiles_p + 32.0 * p.tiles_t * p.n_seq;
+  return best + positions * (kKvTokBytes + 2 * kLatent) / 5.0e6 + 5.0;
+}
+
+// All of it on the tensor-memory path, or (up to 32 heads) the tails or everything on the path for
+// few heads, which takes kFewUs per 32 positions of a row, on two blocks per SM (16 heads) or
+// one: it reads nothing twice but a prefix, once for every row.
+PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, int n_sm) {
+  PrefixPlan p{};
+  p.n_seq = n_seq;
+  p.h_s = h_s;
+  p.tiles_p = (prefix_len + kTile - 1) / kTile;
+  p.tiles_t = (max_ctx - prefix_len + kTile - 1) / kTile;
+  p.mt = static_cast<int>((static_cast<int64_t>(n_q) * h_s + kRows - 1) / kRows);
+  double best = plan_tiles(p, n_q, n_sm);
+  if (h_s <= kFewHeads) {
+    const int fit = h_s <= 16 ? 2 * n_sm : n_sm;
+    const double step_us = h_s <= 16 ? kFewUs16 : kFewUs32;
+    for (int whole = 0; whole < 2; ++whole) {  // the tails, then everything
+      const int lo = whole ? 0 : prefix_len;
+      if ((!whole && !prefix_len) || lo == max_ctx) continue;
+      PrefixPlan q = p;
+      q.sp = q.st = 0;
+      q.tiles_t = 0;
+      if (whole) q.tiles_p = 0;
+      const double rest = plan_tiles(q, n_q, n_sm);
+      const int steps = (max_ctx - lo + 31) / 32, sure = whole ? prefix_len / 32 : 0;
+      for (int few = 1; few <= std::min(steps, 64); few *= 2) {
+        const double each = 4.0 + step_us * ((steps + few - 1) / few), mean = 4.0 + step_us * (0.5 * (steps + sure) / few);
+        const double blocks = static_cast<double>(n_q) * few;
+        const double t = rest + std::max(each, blocks * mean / fit + (blocks > fit ? 0.5 * each : 0.0)) + kJoinUs * n_q * h_s * few + 3.0;
+        if (t < best) {
+          best = t;
+          q.few_lo = lo;
+          q.few = few;
+          p = q;
+        }
+      }
+    }
+  }
+  p.ns = p.sp + p.st + p.few;
   p.rows_kv = static_cast<int64_t>(p.tiles_p) * kTile + static_cast<int64_t>(n_seq) * p.tiles_t * kTile;
-  const size_t parts = p.sp + p.st > 1 ? static_cast<size_t>(n_q) * h_s * (p.sp + p.st) : 0;
+  const size_t parts = p.ns > 1 ? static_cast<size_t>(n_q) * h_s * p.ns : 0;
   p.off_info = round_up(static_cast<size_t>(p.rows_kv) * kLatent * 2, 256);
   p.off_o = p.off_info + round_up(static_cast<size_t>(p.rows_kv / kTile) * sizeof(TileInfo), 256);
   p.off_ml = p.off_o + parts * kVDim * 2;
-  p.bytes = p.off_ml + round_up(parts * 16, 256);
+  p.bytes = std::max<size_t>(256, p.off_ml + round_up(parts * 16, 256));
   return p;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-  const __half2 v = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ float2 unpack_half2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ float exp2_approx(float x) {  // relative error ~2^-22; 2^-inf = 0
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Positions row t sees: 0 for a row whose sequence or length is out of range (flagged).
-__device__ __forceinline__ int row_limit(const PrefixArgs& a, int t, bool report) {
-  const int b = a.q_seq[t];
-  if (b < 0 || b >= a.n_seq) {
-    if (report) flag(a.status, DSA_STATUS_BAD_SEQ);
-    return 0;
-  }
-  const int len = a.seq_lens[b];
-  if (len < 0 || len > a.max_ctx) {
-    if (report) flag(a.status, DSA_STATUS_BAD_LEN);
-    return 0;
-  }
-  const int pos = a.q_pos[t];
-  return pos < 0 ? 0 : min(pos, len - 1) + 1;
 }
 
 // ---- expand: one block per 64-position tile ------------------------------------------------
 // Bound by memory: 608 bytes read and 1152 written a position.
 constexpr int kExpandThreads = 288;
 constexpr int kChunks = kLatent / 16;  // 16-code chunks of a record
-__device__ __forceinline__ bool has_nan_code(uint32_t w) {  // a byte 0x7F or 0xFF
-  const uint32_t m = w & 0x7F7F7F7Fu;
-  return ((m + 0x01010101u) & 0x80808080u) != 0u;
-}
 __global__ void __launch_bounds__(kExpandThreads)
 expand_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
   __shared__ unsigned s_word[4];  // valid (2 words), poisonous (2 words)
@@ -608,7 +614,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   const int n_prefix = pl.sp * mt;
   const bool tail = item >= n_prefix;
   const int64_t rows_all = static_cast<int64_t>(a.n_q) * a.h_s;
-  const int ns = pl.sp + pl.st;
+  const int ns = pl.ns;
   int64_t row0;
   int n_rows, part, split, tiles, tile_base, first_pos;
   if (!tail) {
@@ -627,7 +633,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     row0 = static_cast<int64_t>(t) * a.h_s;
     n_rows = g == 0 ? a.h_s : 0;
     part = pl.st;
-    const int lim = row_limit(a, t, tid == 0 && rank == 0 && split == 0);
+    const int lim = prefix_row_limit(a, t, tid == 0 && rank == 0 && split == 0);
     tiles = lim > a.prefix_len ? (lim - a.prefix_len + kTile - 1) / kTile : 0;
     // (a row that sees anything has a sequence in range)
     tile_base = tiles ? pl.tiles_p + a.q_seq[t] * pl.tiles_t : 0;
@@ -639,7 +645,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   if (nt == 0) {  // all CTAs alike: nothing of these rows lies in this split
     if (c == 0 && ns > 1) {
       for (int m = tid; m < n_rows; m += kThreads)
-        ws.ml[(row0 + m) * ns + slot] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        ws.ml[(row0 + m) * ns + slot] = split_state(0.f, 0.f, 0);
     } else if (ns == 1) {
       for (int i = tid; i < n_rows * (kHalfV / 8); i += kThreads)
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (row0 + i / (kHalfV / 8)) * kVDim + kHalfV * c +
@@ -927,7 +933,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     // positions of this part the row sees
     int lim = 0;
     if (live) {
-      lim = row_limit(a, static_cast<int>((row0 + m) / a.h_s), !tail && split == 0 && c == 0 && hv == 0) - first_pos;
+      lim = prefix_row_limit(a, static_cast<int>((row0 + m) / a.h_s), !tail && split == 0 && c == 0 && hv == 0) - first_pos;
       if (!tail) lim = min(lim, a.prefix_len);
     }
     // O's row (this thread's 128 columns) and the sum times 2^-by
@@ -1118,22 +1124,14 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float y0 = __uint_as_float(v[i + 2 * j]) * inv, y1 = __uint_as_float(v[i + 2 * j + 1]) * inv;
-          o[j] = ns == 1 ? pack2(y0, y1) : pack_half2(y0 * down, y1 * down);
+          o[j] = ns == 1 ? pack_bf162(y0, y1) : pack_half2(y0 * down, y1 * down);
         }
         *reinterpret_cast<uint4*>(row + 2 * (col + i)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
     if (c == 0 && hv == 0 && m < n_rows) {
-      if (ns == 1) {
-        if (a.out_lse) a.out_lse[row0 + m] = l > 0.f || l != l ? (rho + log2f(l)) * 0.6931471805599453f : -INFINITY;
-      } else {
-        // the sum's own exponent joins the reference, so that the merge compares true sizes
-        const int el = l > 0.f && l < INFINITY ? static_cast<int>(__float_as_uint(l) >> 23) - 127 : 0;
-        // (NaN logits leave no reference; the merge takes -inf for an empty split)
-        const float ref = l != l ? 0.f : rho + static_cast<float>(el);
-        ws.ml[(row0 + m) * ns + slot] = l == 0.f ? make_float4(-INFINITY, 0.f, 0.f, 0.f)
-                                                 : make_float4(ref, l * exp2i(-max(el, -126)), static_cast<float>(e_out), 0.f);
-      }
+      if (ns > 1) ws.ml[(row0 + m) * ns + slot] = split_state(rho, l, e_out);
+      else if (a.out_lse) a.out_lse[row0 + m] = natural_lse(rho, l);
     }
   }
   __syncthreads();
@@ -1173,7 +1171,7 @@ prefix_merge_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x >> 6);
   if (row >= static_cast<int64_t>(a.n_q) * a.h_s) return;
   const int d = 8 * static_cast<int>(threadIdx.x & 63);
-  const int ns = pl.sp + pl.st;
+  const int ns = pl.ns;
   float M = -INFINITY, sum = 0.f, acc[8] = {};
   for (int s0 = 0; s0 < ns; s0 += kMergeBatch) {
     float4 ml[kMergeBatch];
@@ -1214,10 +1212,10 @@ prefix_merge_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
   }
   const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * kVDim + d) =
-      make_uint4(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv),
-                 pack2(acc[4] * inv, acc[5] * inv), pack2(acc[6] * inv, acc[7] * inv));
+      make_uint4(pack_bf162(acc[0] * inv, acc[1] * inv), pack_bf162(acc[2] * inv, acc[3] * inv),
+                 pack_bf162(acc[4] * inv, acc[5] * inv), pack_bf162(acc[6] * inv, acc[7] * inv));
   if (a.out_lse && d == 0)
-    a.out_lse[row] = sum > 0.f || sum != sum ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    a.out_lse[row] = natural_lse(M, sum);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1265,32 +1263,41 @@ cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char**
   PrefixWs ws{reinterpret_cast<__half*>(base), reinterpret_cast<TileInfo*>(base + pl.off_info),
               reinterpret_cast<__half*>(base + pl.off_o), reinterpret_cast<float4*>(base + pl.off_ml)};
   const int64_t rows = static_cast<int64_t>(a.n_q) * a.h_s;
-  const int64_t items = static_cast<int64_t>(pl.sp) * ((pl.mt + pl.g - 1) / pl.g) + static_cast<int64_t>(pl.st) * a.n_q;
-  if (pl.rows_kv > INT32_MAX - kTile || rows > INT32_MAX - kRows || items > INT32_MAX / 4) {
+  const int64_t items = static_cast<int64_t>(pl.sp) * ((pl.mt + pl.g - 1) / std::max(1, pl.g)) + static_cast<int64_t>(pl.st) * a.n_q;
+  if (pl.rows_kv > INT32_MAX - kTile || rows > INT32_MAX - kRows || items > INT32_MAX / 4 ||
+      static_cast<int64_t>(pl.few) * a.n_q > INT32_MAX) {
     *err = "prefix_attn: more rows than 32 bits count";
     return cudaErrorInvalidValue;
   }
-  const EncodeFn enc = encode_fn();
-  if (!enc) {
-    *err = "prefix_attn: cuTensorMapEncodeTiled is not available";
-    return cudaErrorNotSupported;
+  cudaError_t e = cudaSuccess;
+  if (pl.few) {
+    e = launch_prefix_few({a, pl.few_lo, pl.few, pl.sp + pl.st, pl.ns, ws.o, ws.ml}, s);
+    if (e != cudaSuccess) return e;
   }
-  CUtensorMap q_map, tile_map, half_map;
-  if (!encode_rows(enc, &q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, rows, kRows) ||
-      !encode_rows(enc, &tile_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws.kv, pl.rows_kv, kTile) ||
-      !encode_rows(enc, &half_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws.kv, pl.rows_kv, kTile / 2)) {
-    *err = "prefix_attn: tensor map encoding failed";
-    return cudaErrorInvalidValue;
+  if (items) {
+    const EncodeFn enc = encode_fn();
+    if (!enc) {
+      *err = "prefix_attn: cuTensorMapEncodeTiled is not available";
+      return cudaErrorNotSupported;
+    }
+    CUtensorMap q_map, tile_map, half_map;
+    if (!encode_rows(enc, &q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, rows, kRows) ||
+        !encode_rows(enc, &tile_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws.kv, pl.rows_kv, kTile) ||
+        !encode_rows(enc, &half_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws.kv, pl.rows_kv, kTile / 2)) {
+      *err = "prefix_attn: tensor map encoding failed";
+      return cudaErrorInvalidValue;
+    }
+    const auto attend = pl.g == 2 ? attend_kernel<2> : attend_kernel<1>;
+    const uint32_t smem = pl.g == 2 ? kSmemBytes<2> : kSmemBytes<1>;
+    e = cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(expand_kernel, dim3(static_cast<unsigned>(pl.rows_kv / kTile)), dim3(kExpandThreads), 0, s, 1, a, pl, ws);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(attend, dim3(static_cast<unsigned>(2 * pl.g * items)), dim3(kThreads), smem, s, 2 * pl.g, q_map, tile_map,
+                   half_map, a, pl, ws);
+    if (e != cudaSuccess) return e;
   }
-  const auto attend = pl.g == 2 ? attend_kernel<2> : attend_kernel<1>;
-  const uint32_t smem = pl.g == 2 ? kSmemBytes<2> : kSmemBytes<1>;
-  cudaError_t e = cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(expand_kernel, dim3(static_cast<unsigned>(pl.rows_kv / kTile)), dim3(kExpandThreads), 0, s, 1, a, pl, ws);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(attend, dim3(static_cast<unsigned>(2 * pl.g * items)), dim3(kThreads), smem, s, 2 * pl.g, q_map,
-                 tile_map, half_map, a, pl, ws);
-  if (e != cudaSuccess || pl.sp + pl.st == 1) return e;
+  if (pl.ns == 1) return cudaSuccess;
   return launch_pdl(prefix_merge_kernel, dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows)),
                     dim3(64 * kMergeRows), 0, s, 1, a, pl, ws);
 }

@@ -1,17 +1,17 @@
 """Attention of a batch that shares a prefix (prefix_attn) against the formula in 64 bits.
 
 The reference reads the cache's own bytes.  Gates for o against the float64 attention over the
-latent rows rounded to 11 significant bits, as the kernel's fp16 operands are:
+latent rows, rounded to 11 significant bits for more than 32 heads, as the fp16 operands are then:
 
 * per value: a weight is rounded to fp16 (2^-11 of it, or 2^-25 of the row's largest weight if
-  subnormal), a split's partial result too (2^-11), the result to bf16 (2^-8); the
-  logits carry the rounding of 576 fp32 additions, sm_scale sum|q kv| 576 2^-24 =: D, which moves a
+  subnormal), or with up to 32 heads, times its position's scale, to bf16 (2^-8), a split's partial
+  result to fp16 (2^-11), the result to bf16 (2^-8); the logits carry the rounding of 576 fp32 additions, sm_scale sum|q kv| 576 2^-24 =: D, which moves a
   weight by up to 2 D of it, and the hardware 2^x 2^-21 of it.  With S = sum_j p_j |v_j| over n
   positions
-  |o - ref| <= (2 * 2^-11 + 2 D + 2^-20) S + n 2^-25 max|v| + 2^-8 |ref|;
-* per call: those roundings are independent of each other and the last one, of at most 2^-8 and
-  2^-8 / sqrt(3) in the mean square, is the largest, so the 2-norm of the difference stays below
-  2^-8 of the result's.
+  |o - ref| <= (2^-11 + w + 2 D + 2^-20) S + n 2^-25 max|v| + 2^-8 |ref|,  w = 2^-11 or 2^-8;
+* per call: those roundings are independent of each other, two of at most 2^-8 of a value and so
+  2^-8 / sqrt(3) in the mean square, the others far smaller, so the 2-norm of the difference stays
+  below 2^-8 of the result's.
 
 On the ordinary inputs the second gate also holds against the unrounded rows: 11 bits move a
 logit by some 2^-11.  lse within 1e-4 of the rounded reference (the sparse attention's gate).
@@ -100,7 +100,7 @@ class Batch:
             n = max(0, min(pos + 1, int(self.lens[b]))) if good else 0
             kv, ok = self.rows64(b) if good else (np.zeros((0, 576)), np.zeros(0, bool))
             raw = kv[:n][ok[:n]]
-            kv = round11(raw)
+            kv = raw if self.h <= 32 else round11(raw)
             if not len(kv):
                 assert not o[t].any() and np.all(np.isneginf(e[t]))
                 continue
@@ -112,7 +112,7 @@ class Batch:
             p = w / z
             ref, size = p @ kv[:, :512], p @ np.abs(kv[:, :512])
             d = SM * (np.abs(q) @ np.abs(kv).T).max() * 576 * 2.0 ** -24
-            tol = ((2 * 2.0 ** -11 + 2 * d + 2.0 ** -20) * size + len(kv) * 2.0 ** -25 * np.abs(kv[:, :512]).max()
+            tol = ((2.0 ** -11 + (2.0 ** -8 if self.h <= 32 else 2.0 ** -11) + 2 * d + 2.0 ** -20) * size + len(kv) * 2.0 ** -25 * np.abs(kv[:, :512]).max()
                    + 2.0 ** -8 * np.abs(ref) + 1e-30)
             bad = np.abs(o[t] - ref) / tol
             assert bad.max() <= 1, (t, bad.max())
@@ -183,6 +183,9 @@ def test_python_refusals(dsa):
     ([700 + 37 * i for i in range(12)], 517, 33),
     ([5000, 4200], 4100, 128),        # several splits
     ([130 + i for i in range(40)], 100, 7),
+    ([3000, 2000, 1], 0, 32), ([33, 32, 31, 1], 0, 17), ([2048 + 100 * i for i in range(20)], 2040, 16),
+    ([6000 + i for i in range(64)], 5990, 16),   # a prefix on tensor memory, tails beside it
+    ([900 + 60 * i for i in range(24)], 700, 48),
 ])
 def test_matches_the_formula(dsa, lens, prefix, h):
     b = Batch(dsa, lens, prefix, h, seed=len(lens) + prefix)
@@ -192,22 +195,42 @@ def test_matches_the_formula(dsa, lens, prefix, h):
 
 
 @pytest.mark.gpu
-def test_rows_in_any_number_and_order(dsa):
-    # two-token steps, a chunk of one sequence, rows inside the prefix, rows that see nothing
-    lens, prefix = [700, 650, 655, 300], 640
-    rows = [(1, 649), (0, 698), (0, 699), (2, 654), (0, 100), (1, 0), (2, -1), (3, 299), (3, 800), (1, 2147483647),
-            (0, 639), (0, 640), (2, 63), (2, 64)] + [(0, 660 + i) for i in range(40)]
-    b = Batch(dsa, lens, prefix, 24, rows=rows, seed=3, max_ctx=1000)
+@pytest.mark.parametrize("h", [8, 64])
+def test_every_code_and_scale(dsa, h):
+    # random codes (all but the NaN ones, subnormals among them) and scales over 2^16
+    b = Batch(dsa, [130, 100], 70, h, seed=11)
+    g = torch.Generator().manual_seed(12)
+    rec = b.cache.view(-1, 608)
+    codes = torch.randint(0, 256, (rec.shape[0], 576), generator=g, dtype=torch.uint8)
+    codes[(codes & 0x7F) == 0x7F] = 0x38
+    scale = torch.exp2(torch.rand(rec.shape[0], 5, generator=g) * 16 - 20)
+    rec[:, :576] = codes.cuda()
+    rec[:, 576:596] = scale.view(torch.uint8).cuda()
+    b.q *= 2.0 ** -4
     out, lse = b.call(dsa)
     assert dsa.device_status() == 0
     b.check(out, lse)
 
 
 @pytest.mark.gpu
-def test_bad_pages_sequences_and_lengths_are_skipped_and_flagged(dsa):
+@pytest.mark.parametrize("h", [24, 40])
+def test_rows_in_any_number_and_order(dsa, h):
+    # two-token steps, a chunk of one sequence, rows inside the prefix, rows that see nothing
+    lens, prefix = [700, 650, 655, 300], 640
+    rows = [(1, 649), (0, 698), (0, 699), (2, 654), (0, 100), (1, 0), (2, -1), (3, 299), (3, 800), (1, 2147483647),
+            (0, 639), (0, 640), (2, 63), (2, 64)] + [(0, 660 + i) for i in range(40)]
+    b = Batch(dsa, lens, prefix, h, rows=rows, seed=3, max_ctx=1000)
+    out, lse = b.call(dsa)
+    assert dsa.device_status() == 0
+    b.check(out, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("h", [16, 48])
+def test_bad_pages_sequences_and_lengths_are_skipped_and_flagged(dsa, h):
     lens, prefix = [900, 800, 2000, 850, -3], 700
     rows = [(0, 899), (1, 799), (2, 750), (3, 849), (4, 10), (5, 100), (-1, 100)]
-    b = Batch(dsa, lens, prefix, 16, rows=rows, seed=4, max_ctx=1000)
+    b = Batch(dsa, lens, prefix, h, rows=rows, seed=4, max_ctx=1000)
     out, lse = b.call(dsa)
     assert dsa.device_status() == 2 | 4      # BAD_SEQ, BAD_LEN and nothing else
     b.check(out, lse)
@@ -221,10 +244,11 @@ def test_bad_pages_sequences_and_lengths_are_skipped_and_flagged(dsa):
 
 
 @pytest.mark.gpu
-def test_non_finite_positions_reach_only_the_rows_that_see_them(dsa):
+@pytest.mark.parametrize("h", [16, 64])
+def test_non_finite_positions_reach_only_the_rows_that_see_them(dsa, h):
     lens, prefix = [400, 410, 390], 320
     rows = [(0, 399), (1, 409), (2, 389), (0, 349), (0, 30), (1, 200)]
-    b = Batch(dsa, lens, prefix, 16, rows=rows, seed=5)
+    b = Batch(dsa, lens, prefix, h, rows=rows, seed=5)
     clean, clean_lse = b.call(dsa)
     rec = b.cache.view(-1, 608)
 
@@ -250,15 +274,16 @@ def test_non_finite_positions_reach_only_the_rows_that_see_them(dsa):
     b.q[1, 3, 5] = float("nan")
     out, _ = b.call(dsa)
     assert torch.isnan(out[1, 3]).all()
-    keep = torch.ones(6, 16, dtype=torch.bool, device="cuda")
+    keep = torch.ones(6, h, dtype=torch.bool, device="cuda")
     keep[1, 3] = False
     assert torch.equal(out[keep], clean[keep])
     assert dsa.device_status() == 0
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("h", [16, 64, 128])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
-def test_logits_far_from_the_first_tile(dsa, sign):
+def test_logits_far_from_the_first_tile(dsa, sign, h):
     # the logits grow (or fall) by hundreds of powers of two from tile to tile, in half of the
     # heads: the references of the first tile do not serve
     def kv(n, g):
@@ -267,11 +292,11 @@ def test_logits_far_from_the_first_tile(dsa, sign):
         return v
 
     def q(n, g):
-        v = torch.randn(n, 16, 576, generator=g)
+        v = torch.randn(n, h, 576, generator=g)
         v[:, ::2, 0] = 300.0 * sign
         return v
 
-    b = Batch(dsa, [600, 610], 500, 16, seed=6, kv=kv, q=q)
+    b = Batch(dsa, [600, 610], 500, h, seed=6, kv=kv, q=q)
     # dim 0 of position p: p / 4 (the FP8 tile scale of 128 dims then is set by it; the bytes rule)
     vals = torch.randn(b.num_pages * 64, 576, generator=torch.Generator().manual_seed(7))
     where = torch.zeros(b.num_pages * 64)
@@ -287,7 +312,8 @@ def test_logits_far_from_the_first_tile(dsa, sign):
 
 
 @pytest.mark.gpu
-def test_first_tile_unseen_and_logits_far_below_zero(dsa):
+@pytest.mark.parametrize("h", [8, 64])
+def test_first_tile_unseen_and_logits_far_below_zero(dsa, h):
     # nothing of the first tile is there to take a reference from, and every logit is some -3000
     def kv(n, g):
         v = torch.randn(n, 576, generator=g)
@@ -295,11 +321,11 @@ def test_first_tile_unseen_and_logits_far_below_zero(dsa):
         return v
 
     def q(n, g):
-        v = torch.randn(n, 8, 576, generator=g)
+        v = torch.randn(n, h, 576, generator=g)
         v[:, :, 0] = -1000.0
         return v
 
-    b = Batch(dsa, [300, 310], 256, 8, seed=8, kv=kv, q=q)
+    b = Batch(dsa, [300, 310], 256, h, seed=8, kv=kv, q=q)
     b.pages[0] = -1
     out, lse = b.call(dsa)
     assert dsa.device_status() == 1
