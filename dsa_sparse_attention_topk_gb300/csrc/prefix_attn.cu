@@ -156,20 +156,22 @@ struct alignas(32) TileInfo {
 struct PrefixPlan {
   int tiles_p, tiles_t;      // tiles of the prefix, and of the longest possible tail
   int sp, st;                // splits of the prefix and of each tail on the tensor-memory path
-  int few_lo, few;           // first position and splits of each row on the path for few heads (0: not taken)
+  int few_lo, few;           // the path for few heads: first position and most parts of a row (0: not taken)
+  int few_blocks;
   int ns;                    // all splits of a row
   int mt;                    // 128-row tiles of the flattened rows
   int n_seq, h_s;
   int g;                     // of them in one item: MMAs of one CTA or of a pair
   int64_t rows_kv;           // rows of the expanded cache
-  size_t off_info, off_o, off_ml, bytes;
+  size_t off_info, off_o, off_ml, off_used, bytes;
 };
 
 struct PrefixWs {
   __half* kv;                // [tiles_p * 64 + n_seq * tiles_t * 64][576]
   TileInfo* info;            // [tiles]
-  __half* o;                 // [n_q * h_s][sp + st][512], times 2^-(its exponent)
-  float4* ml;                // [n_q * h_s][sp + st]: reference, sum, the outputs' exponent
+  __half* o;                 // [n_q * h_s][ns][512], times 2^-(its exponent)
+  float4* ml;                // [n_q * h_s][ns]: reference, sum, the outputs' exponent
+  int* used;                 // [n_q]: parts of the row on the path for few heads
 };
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -234,15 +236,19 @@ PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, i
       q.tiles_t = 0;
       if (whole) q.tiles_p = 0;
       const double rest = plan_tiles(q, n_q, n_sm);
-      const int steps = (max_ctx - lo + 31) / 32, sure = whole ? prefix_len / 32 : 0;
-      for (int few = 1; few <= std::min(steps, 64); few *= 2) {
-        const double each = 4.0 + step_us * ((steps + few - 1) / few), mean = 4.0 + step_us * (0.5 * (steps + sure) / few);
-        const double blocks = static_cast<double>(n_q) * few;
-        const double t = rest + std::max(each, blocks * mean / fit + (blocks > fit ? 0.5 * each : 0.0)) + kJoinUs * n_q * h_s * few + 3.0;
+      const int steps = (max_ctx - lo + 63) / 64, sure = whole ? prefix_len / 64 : 0;
+      const double mean = 0.5 * (steps + sure) * n_q;  // of all rows, tails half full
+      const int even = static_cast<int>(std::min<int64_t>(fit, static_cast<int64_t>(steps) * n_q));
+      for (int few = 1; few <= std::min(2 * steps, 64); few *= 2) {
+        // a row a block, the longest one last; or even shares
+        const double t = rest + 4.0 + kJoinUs * n_q * h_s * few + (few > 1 || q.sp ? 3.0 : 0.0) +
+                         (few == 1 ? step_us * std::max<double>(steps, mean / fit + (n_q > fit ? 0.5 * steps : 0.0))
+                                   : 1.5 + 1.5 * (1.0 + n_q / even) + step_us * std::max({mean / even, steps / (few - 1.0), 1.0}));
         if (t < best) {
           best = t;
           q.few_lo = lo;
           q.few = few;
+          q.few_blocks = few == 1 ? n_q : even;
           p = q;
         }
       }
@@ -254,7 +260,8 @@ PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, i
   p.off_info = round_up(static_cast<size_t>(p.rows_kv) * kLatent * 2, 256);
   p.off_o = p.off_info + round_up(static_cast<size_t>(p.rows_kv / kTile) * sizeof(TileInfo), 256);
   p.off_ml = p.off_o + parts * kVDim * 2;
-  p.bytes = std::max<size_t>(256, p.off_ml + round_up(parts * 16, 256));
+  p.off_used = p.off_ml + round_up(parts * 16, 256);
+  p.bytes = std::max<size_t>(256, p.off_used + (p.ns > 1 && p.few ? round_up(static_cast<size_t>(n_q) * 4, 256) : 0));
   return p;
 }
 
@@ -1171,7 +1178,7 @@ prefix_merge_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x >> 6);
   if (row >= static_cast<int64_t>(a.n_q) * a.h_s) return;
   const int d = 8 * static_cast<int>(threadIdx.x & 63);
-  const int ns = pl.ns;
+  const int ns = pl.sp + pl.st + (pl.few ? min(__ldcg(ws.used + row / a.h_s), pl.few) : 0);
   float M = -INFINITY, sum = 0.f, acc[8] = {};
   for (int s0 = 0; s0 < ns; s0 += kMergeBatch) {
     float4 ml[kMergeBatch];
@@ -1181,8 +1188,8 @@ prefix_merge_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
       ml[i] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
       v[i] = make_uint4(0u, 0u, 0u, 0u);
       if (s0 + i < ns) {
-        ml[i] = __ldcg(ws.ml + row * ns + s0 + i);
-        v[i] = __ldcg(reinterpret_cast<const uint4*>(ws.o + (row * ns + s0 + i) * kVDim + d));
+        ml[i] = __ldcg(ws.ml + row * pl.ns + s0 + i);
+        v[i] = __ldcg(reinterpret_cast<const uint4*>(ws.o + (row * pl.ns + s0 + i) * kVDim + d));
       }
     }
     float top = M;
@@ -1261,7 +1268,8 @@ cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char**
   const PrefixPlan pl = make_plan(a.n_q, a.h_s, a.n_seq, a.prefix_len, a.max_ctx, sm_count());
   uint8_t* base = static_cast<uint8_t*>(a.workspace);
   PrefixWs ws{reinterpret_cast<__half*>(base), reinterpret_cast<TileInfo*>(base + pl.off_info),
-              reinterpret_cast<__half*>(base + pl.off_o), reinterpret_cast<float4*>(base + pl.off_ml)};
+              reinterpret_cast<__half*>(base + pl.off_o), reinterpret_cast<float4*>(base + pl.off_ml),
+              reinterpret_cast<int*>(base + pl.off_used)};
   const int64_t rows = static_cast<int64_t>(a.n_q) * a.h_s;
   const int64_t items = static_cast<int64_t>(pl.sp) * ((pl.mt + pl.g - 1) / std::max(1, pl.g)) + static_cast<int64_t>(pl.st) * a.n_q;
   if (pl.rows_kv > INT32_MAX - kTile || rows > INT32_MAX - kRows || items > INT32_MAX / 4 ||
@@ -1271,7 +1279,7 @@ cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char**
   }
   cudaError_t e = cudaSuccess;
   if (pl.few) {
-    e = launch_prefix_few({a, pl.few_lo, pl.few, pl.sp + pl.st, pl.ns, ws.o, ws.ml}, s);
+    e = launch_prefix_few({a, pl.few_lo, pl.few, pl.few_blocks, pl.sp + pl.st, pl.ns, ws.o, ws.ml, ws.used}, s);
     if (e != cudaSuccess) return e;
   }
   if (items) {

@@ -52,13 +52,16 @@ __device__ __forceinline__ float natural_lse(float ref, float l) {
   return l > 0.f || l != l ? (ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-// The kernel for few heads (prefix_few.cu): positions lo .. of every query row, in `splits`
-// shares written to the slots slot0 .. of ns; directly to the output when ns is 1.
+// The kernel for few heads (prefix_few.cu): positions lo .. of every query row.  With splits = 1 a
+// block takes a row; otherwise `blocks` blocks take equal shares of all rows' steps, which cuts a
+// row into at most `splits` parts.  Row t's parts go to the slots slot0 .. slot0 + used[t] of ns;
+// directly to the output when ns is 1.
 struct FewArgs {
   PrefixArgs a;
-  int lo, splits, slot0, ns;
+  int lo, splits, blocks, slot0, ns;
   __half* o;
   float4* ml;
+  int* used;
 };
 constexpr int kFewHeads = 32;
 cudaError_t launch_prefix_few(const FewArgs& f, cudaStream_t s);

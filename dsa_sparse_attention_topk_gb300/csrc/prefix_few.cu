@@ -4,69 +4,92 @@
 // With 16 heads a position is 596 bytes for 35 K flop: memory sets the floor, and the 128-row
 // tiles of the tensor-memory path would be seven eighths empty, after an expansion that
 // moves three times the bytes.  Here a block takes one query row's heads (one or two tiles of
-// 16) and a share of its positions, 32 at a time: it copies their records to shared memory
-// (cp.async, one tile ahead), widens the codes to bf16, and feeds mma.sync.m16n8k16.
+// 16) and a run of its positions, 64 at a time: it copies their records to shared memory
+// (cp.async, one step ahead) and feeds mma.sync.m16n8k16 in fp16 from the codes themselves, which
+// each thread widens for its own fragment.  The order of the products' inner index is free, so
+// a thread's fragments are eight neighbouring codes of a position (logits) or of four
+// positions (output), and no widened tile goes through shared memory.
 //
-//   logits   S[h, j] = sum over the five scale tiles of scale[j, tile] (q_tile . codes_tile): codes are
-//            exact in bf16, as the query is, and each tile's scale multiplies its partial sum in
-//            fp32, so nothing is rounded before the softmax.  Warp w takes positions 16 (w & 1) ..
-//            and scale tile w / 2 (the last: tiles 3 and 4); its share of the query stays in
-//            registers.
+//   logits   S[h, j] = sum over the five scale tiles of scale[j, tile] (q_tile . codes_tile): codes
+//            are exact in fp16, the query too after a power of two per head (what falls below
+//            2^-39 of the head's largest is lost), and each tile's scale multiplies its partial
+//            sum in fp32.  Warp w takes positions 32 (w & 1) .., scale tile w / 2 and a quarter
+//            of the fifth; its share of the query stays in registers.
 //   weights  one warp per two rows of 16: running maximum and sum in fp32; per scale tile the
-//            weight times the position's scale, as bf16 (2^-8: the one rounding).
+//            weight times the position's scale, in fp16 (2^-11: the one rounding) with a power of two per
+//            row that follows the largest of them.
 //   output   O[h, d] += weights(tile of d) . codes: warp w takes dims 64 w .., in registers.
 //
-// Two blocks per SM for one head tile (91 KB of shared memory each), so that one's barriers
+// Two blocks per SM for one head tile (111 KB of shared memory each), so that one's barriers
 // hide behind the other's work.
 
 #include "prefix_common.cuh"
+#include "tc_utils.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kTok = 32;                          // positions per step
+constexpr int kTok = 64;                          // positions per step
 constexpr int kThreads = 256;
-constexpr int kRec = kKvTokBytes;                 // 608
-constexpr int kPitch = kLatent + 8;               // widened row, elements (rows shift by 16 bytes mod 128)
-constexpr int kPPitch = kTok + 8;
-constexpr int kSPitch = kTok + 4;
+constexpr int kPitch = kKvTokBytes;               // a position's record: four rows start 96 bytes apart mod 128
+constexpr int kKs = 9;                            // K-steps of 16 dims a warp
+// A step's positions stand in the products in this order: columns 2 q and 2 q + 1 of eight are the
+// positions q and 4 + (q ^ 2), so that four threads' eight positions start in different banks both
+// where columns go along them (logits) and where rows do (output).
+__device__ __forceinline__ int second(int q) { return 4 + (q ^ 2); }
+constexpr int kNoUnit = -112;                     // smallest unit of the output's sums
+constexpr int kPPitch = kTok + 8, kSPitch = kTok + 8;
 
 template <int HT> struct FewSmem {
-  static constexpr uint32_t raw = 0, tile = raw + 2 * kTok * kRec, p = tile + kTok * kPitch * 2;
-  static constexpr uint32_t s = p + 4 * HT * 16 * kPPitch * 2, alpha = s + 4 * HT * 16 * kSPitch * 4;
-  static constexpr uint32_t top = alpha + HT * 16 * 4, sum = top + HT * 16 * 4, ref = sum + HT * 16 * 4;
-  static constexpr uint32_t words = ref + HT * 16 * 4, bytes = words + 16;
+  // two steps' records; weights; partial logits
+  static constexpr uint32_t codes = 0, p = codes + 2 * kTok * kPitch, s = p + 4 * HT * 16 * kPPitch * 2;
+  static constexpr uint32_t alpha = s + 4 * HT * 16 * kSPitch * 4, top = alpha + HT * 16 * 4, sum = top + HT * 16 * 4;
+  static constexpr uint32_t ref = sum + HT * 16 * 4, unit = ref + HT * 16 * 4, bytes = unit + HT * 16 * 4;
 };
 static_assert(FewSmem<1>::bytes * 2 <= 232448 - 2048 && FewSmem<2>::bytes <= 232448, "shared memory");
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two E4M3 codes, in the upper bytes of w's halves, as bf16 (exact): the seven bits below the sign
-// are shifted to the bottom of bf16's exponent and the top of its fraction, and 2^120 makes up
-// for the exponents' offsets (127 and 7), subnormals included.  A NaN code becomes 480: such
-// positions are marked before.
-__device__ __forceinline__ uint32_t widen(uint32_t w) {
-  const uint32_t v = (w & 0x80008000u) | ((w & 0x7F007F00u) >> 4);
-  const __nv_bfloat162 p = *reinterpret_cast<const __nv_bfloat162*>(&v);
-  const uint32_t up = 0x7B807B80u;  // 2^120 twice
-  const __nv_bfloat162 r = __hmul2(p, *reinterpret_cast<const __nv_bfloat162*>(&up));
-  return *reinterpret_cast<const uint32_t*>(&r);
+// the same from zero sums
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
+// two products, or products and sums, in one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(*reinterpret_cast<unsigned long long*>(&r))
+      : "l"(*reinterpret_cast<const unsigned long long*>(&a)), "l"(*reinterpret_cast<const unsigned long long*>(&b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(*reinterpret_cast<unsigned long long*>(&r))
+      : "l"(*reinterpret_cast<const unsigned long long*>(&a)), "l"(*reinterpret_cast<const unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<const unsigned long long*>(&c)));
+  return r;
+}
+// Four E4M3 codes as two pairs of fp16: exact, and NaN stays NaN.
+__device__ __forceinline__ void widen(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+      : "=r"(lo), "=r"(hi) : "r"(codes));
+}
+__device__ __forceinline__ float warp_max(float x) {  // NaN lanes do not take part
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ int exponent(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127; }
 
 template <int HT>
 __global__ void __launch_bounds__(kThreads, HT == 1 ? 2 : 1)
@@ -75,288 +98,426 @@ few_kernel(FewArgs f) {
   extern __shared__ __align__(128) uint8_t smem[];
   const PrefixArgs& a = f.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int t = blockIdx.x / f.splits, split = blockIdx.x - t * f.splits;
   float* s_s = reinterpret_cast<float*>(smem + Sm::s);
   float* s_alpha = reinterpret_cast<float*>(smem + Sm::alpha);
   unsigned* s_top = reinterpret_cast<unsigned*>(smem + Sm::top);
   float* s_sum = reinterpret_cast<float*>(smem + Sm::sum);
   float* s_ref = reinterpret_cast<float*>(smem + Sm::ref);
-  unsigned* s_words = reinterpret_cast<unsigned*>(smem + Sm::words);  // poisonous positions, by step parity
+  int* s_unit = reinterpret_cast<int*>(smem + Sm::unit);
+  __shared__ uint64_t s_full[2];          // a step's records are there
+  __shared__ uint16_t s_mask[kTok / 8];   // of eight positions: which exist, and in the upper byte which are poisonous
+  __shared__ int s_abort;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&s_full[i], kTok);
+    s_abort = 0;
+    tc::mbar_fence_init();
+  }
   pdl_launch_dependents();
   pdl_wait();
 
-  const int lim = prefix_row_limit(a, t, tid == 0 && split == 0);
-  const int steps_all = lim > f.lo ? (lim - f.lo + kTok - 1) / kTok : 0;
-  const int step0 = static_cast<int>(static_cast<int64_t>(split) * steps_all / f.splits);
-  const int steps = static_cast<int>(static_cast<int64_t>(split + 1) * steps_all / f.splits) - step0;
-  const int64_t row0 = static_cast<int64_t>(t) * a.h_s;
-  if (steps == 0) {
-    if (f.ns > 1) {
-      for (int h = tid; h < a.h_s; h += kThreads) f.ml[(row0 + h) * f.ns + f.slot0 + split] = split_state(0.f, 0.f, 0);
-    } else {
+  auto steps_of = [&](int lim) { return lim > f.lo ? (lim - f.lo + kTok - 1) / kTok : 0; };
+  // ---- this block's share: a row, or `share` steps of all rows' steps end to end ----
+  int t = blockIdx.x, step0 = 0, slot = 0;
+  int64_t left;
+  if (f.splits == 1) {
+    left = steps_of(prefix_row_limit(a, t, tid == 0));
+    if (left == 0) {
+      if (f.ns > 1) {
+        if (tid == 0) f.used[t] = 0;
+        return;
+      }
+      const int64_t row0 = static_cast<int64_t>(t) * a.h_s;
       for (int i = tid; i < a.h_s * (kVDim / 8); i += kThreads)
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row0 * kVDim + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
       if (a.out_lse)
         for (int h = tid; h < a.h_s; h += kThreads) a.out_lse[row0 + h] = -INFINITY;
+      return;
     }
-    return;
-  }
-  const int32_t* table = a.page_table + static_cast<int64_t>(a.q_seq[t]) * a.max_pages;
-
-  // ---- copies: eight threads a position, up to five 16-byte chunks each ----
-  const int c_tok = tid >> 3, c_sub = tid & 7;
-  // physical page of this thread's position of a step (-1: none)
-  auto page_of = [&](int step) -> int {
-    const int p = f.lo + (step0 + step) * kTok + c_tok;
-    if (step >= steps || p >= lim) return -1;
-    return p < a.prefix_len ? a.prefix_pages[p / kPage] : table[p / kPage];
-  };
-  auto copy = [&](int step, int page) {
-    const int p = f.lo + (step0 + step) * kTok + c_tok;
-    const bool inside = step < steps && p < lim;
-    const bool real = inside && page >= 0 && page < a.num_pages;
-    if (inside && !real && c_sub == 0) flag(a.status, DSA_STATUS_BAD_PAGE);
-    const uint8_t* src = a.kv_cache + (real ? (static_cast<int64_t>(page) * kPage + p % kPage) * kRec : 0);
-    const uint32_t dst = smem_u32(smem + Sm::raw) + ((step & 1) * kTok + c_tok) * kRec;
-#pragma unroll
-    for (int k = 0; k < 5; ++k) {
-      const int ch = c_sub + 8 * k;
-      if (ch < kRec / 16) cp_async16(dst + 16 * ch, src + 16 * ch, real);
+  } else {
+    __shared__ int64_t s_sum64[kThreads / 32];
+    __shared__ int s_most[kThreads / 32], s_first[3];
+    // every thread adds up a run of rows, and the block their sums
+    const int run = (a.n_q + kThreads - 1) / kThreads;
+    const int64_t first = static_cast<int64_t>(tid) * run, last = min(first + run, static_cast<int64_t>(a.n_q));
+    int64_t sum = 0;
+    int most = 0;
+    for (int64_t r = first; r < last; ++r) {
+      const int n = steps_of(prefix_row_limit(a, static_cast<int>(r), blockIdx.x == 0));
+      sum += n;
+      most = max(most, n);
+      if (n == 0 && r % gridDim.x == blockIdx.x) f.used[r] = 0;
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    return real;
-  };
-  bool real_next = copy(0, page_of(0));
-  int page_next = page_of(1);
-
-  // ---- this warp's share of the query: K-steps of scale tile w / 2 (the last: tiles 3 and 4) ----
-  const int g = lane >> 2, q4 = lane & 3;
-  const int tg = warp & 1, ks = warp >> 1, n_k = ks == 3 ? 12 : 8;
-  uint32_t qf[HT][12][4];
-  {
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + row0 * kLatent;
+    int64_t upto = sum;
 #pragma unroll
-    for (int h = 0; h < HT; ++h)
+    for (int z = 1; z < 32; z <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, upto, z);
+      if (lane >= z) upto += v;
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 31) {
+      s_sum64[warp] = upto;
+      s_most[warp] = most;
+    }
+    if (tid == 0) s_first[0] = a.n_q;
+    __syncthreads();
+    int64_t before = upto - sum, total = 0;
 #pragma unroll
-      for (int k = 0; k < 12; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int head = 16 * h + g + 8 * (i & 1), d = 128 * ks + 16 * k + 2 * q4 + 8 * (i >> 1);
-          qf[h][k][i] = head < a.h_s && k < n_k ? *reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(head) * kLatent + d) : 0u;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += s_sum64[w];
+      total += s_sum64[w];
+      most = max(most, s_most[w]);
+    }
+    // a row of n steps reaches into at most (n - 1) / share + 2 shares
+    const int64_t share = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>((most + f.splits - 2) / (f.splits - 1)));
+    const int64_t from = blockIdx.x * share;
+    left = min(share, total - from);
+    if (left <= 0) return;
+    if (before <= from && from < before + sum) {
+      for (int64_t r = first; r < last; ++r) {
+        const int n = steps_of(prefix_row_limit(a, static_cast<int>(r), false));
+        if (from < before + n) {
+          s_first[0] = static_cast<int>(r);
+          s_first[1] = static_cast<int>(from - before);
+          s_first[2] = static_cast<int>(blockIdx.x - before / share);
+          break;
         }
+        before += n;
+      }
+    }
+    __syncthreads();
+    t = s_first[0];
+    step0 = s_first[1];
+    slot = s_first[2];
   }
-  float o[HT][8][4] = {};
-  // the weights' warp: rows 2 HT warp .. of the 16 HT, lane = position
-  float m_ref[2 * HT], l_sum[2 * HT];
-#pragma unroll
-  for (int i = 0; i < 2 * HT; ++i) {
-    m_ref[i] = -INFINITY;
-    l_sum[i] = 0.f;
-  }
+
+  const int g = lane >> 2, q4 = lane & 3;
+  __syncthreads();
+  const int tg = warp & 1, ks = warp >> 1;   // logits: positions 32 tg .., scale tile ks
+  const int c_tok = 8 * warp + lane;         // copies: the first eight lanes, a position each
+  uint32_t it = 0;                           // steps so far: the records of step i go to buffer i % 2
+  bool zeroed = false;
   const float c2 = a.sm_scale * 1.4426950408889634f;  // logits in powers of two
-  if (tid < 2) s_words[tid] = 0;
-  // (a position's validity goes to the weights' warps by a word per step)
-  __shared__ unsigned s_valid[2];
+#pragma unroll 1
+  while (t < a.n_q) {
+    const int lim = prefix_row_limit(a, t, false), rest = steps_of(lim) - step0;
+    const int steps = static_cast<int>(min(static_cast<int64_t>(rest), left));
+    const int64_t row0 = static_cast<int64_t>(t) * a.h_s;
+    if (f.ns > 1 && steps == rest && tid == 0) f.used[t] = slot + 1;
+    const int32_t* table = a.page_table + static_cast<int64_t>(a.q_seq[t]) * a.max_pages;
+
+    // the copying lanes' positions p0 + 64 j, below `end`
+    const int p0 = f.lo + step0 * kTok + c_tok, end = min(lim, f.lo + (step0 + steps) * kTok);
+    static_assert(kTok == kPage, "a lane's place in the page stays");
+    const uint8_t* src0 = a.kv_cache + p0 % kPage * kKvTokBytes;
+    auto page_of = [&](int step) {
+      const int p = p0 + step * kTok;
+      return lane >= 8 || p >= end ? -1 : p < a.prefix_len ? a.prefix_pages[p / kPage] : table[p / kPage];
+    };
+    // (in the first eight lanes) whether the position exists; what does not becomes zero
+    auto copy = [&](int step, uint32_t nth, int page) {
+      const bool real = page >= 0 && page < a.num_pages;
+      if (lane < 8) {
+        uint8_t* dst = smem + Sm::codes + ((nth & 1) * kTok + c_tok) * kPitch;
+        uint64_t* full = &s_full[nth & 1];
+        if (real && !*static_cast<volatile int*>(&s_abort)) {
+          if (zeroed) tc::fence_async_smem();
+          tc::mbar_arrive_expect_tx(full, kKvTokBytes);
+          tc::bulk_load(dst, src0 + static_cast<int64_t>(page) * (kPage * kKvTokBytes), kKvTokBytes, full);
+        } else {
+          if (!real && p0 + step * kTok < end) flag(a.status, DSA_STATUS_BAD_PAGE);
+          zeroed = true;
+#pragma unroll 1
+          for (int i = 0; i < kKvTokBytes; i += 16) *reinterpret_cast<uint4*>(dst + i) = make_uint4(0u, 0u, 0u, 0u);
+          tc::mbar_arrive(full);
+        }
+      }
+      return real;
+    };
+    bool real_next = copy(0, it, page_of(0));
+    int page_next = page_of(1);
+
+    // ---- this warp's share of the query, as fp16 times a power of two per head ----
+    // K-steps 2 j and 2 j + 1: dims 128 ks + 32 j + 8 q4 + 0 .. 3 and 4 .. 7; the ninth: 512 + 16 ks + 4 q4 ..
+    uint32_t qf[HT][kKs][4];
+    float q_back[HT][2];  // the power's inverse, for heads g and g + 8
+    {
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + row0 * kLatent;
+#pragma unroll
+      for (int h = 0; h < HT; ++h) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int head = 16 * h + g + 8 * i;
+          uint32_t top = 0;
+#pragma unroll
+          for (int k = 0; k < kKs; ++k) {
+            const int d = k < 8 ? 128 * ks + 16 * (k & 6) + 8 * q4 + 4 * (k & 1) : kVDim + 16 * ks + 4 * q4;
+            const uint2 v = head < a.h_s ? *reinterpret_cast<const uint2*>(q + static_cast<int64_t>(head) * kLatent + d) : make_uint2(0u, 0u);
+            qf[h][k][i] = v.x;
+            qf[h][k][i + 2] = v.y;
+            top = max(max(top, max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu)), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu));
+          }
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = min(max(static_cast<int>(top >> 7) - 127 - 14, -126), 112);  // the largest below 2^15 (infinities and NaN stay)
+          const float up = exp2i(-e);
+          q_back[h][i] = exp2i(e);
+#pragma unroll
+          for (int k = 0; k < kKs; ++k)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              uint32_t& v = qf[h][k][i + 2 * z];
+              v = pack_half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+            }
+        }
+      }
+    }
+    float o[HT][8][4] = {};
+    // the weights' warp: rows 2 HT warp .. of the 16 HT, lane = columns 2 lane and 2 lane + 1; the sum is the lane's own
+    float m_ref[2 * HT], l_sum[2 * HT];
+    int unit[2 * HT];  // the output's unit is 2^(unit - 14)
+#pragma unroll
+    for (int i = 0; i < 2 * HT; ++i) {
+      m_ref[i] = -INFINITY;
+      l_sum[i] = 0.f;
+      unit[i] = kNoUnit;
+    }
 
 #pragma unroll 1
-  for (int j = 0; j < steps; ++j) {
-    const int par = j & 1;
-    const uint8_t* raw = smem + Sm::raw + par * kTok * kRec;
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (tid == 0) s_valid[par] = 0, s_words[par] = 0;
-    const bool real = real_next;
-    __syncthreads();  // this step's records are there; the last step's products are done
-    if (c_sub == 0 && real) atomicOr(&s_valid[par], 1u << c_tok);
-    real_next = copy(j + 1, page_next);
-    page_next = page_of(j + 2);
-    // ---- widen: 16 codes a piece, and mark positions with NaN codes or scales that are not finite ----
-#pragma unroll
-    for (int k = 0; k < 5; ++k) {
-      const int i = k * kThreads + tid;
-      if (i < kTok * (kLatent / 16)) {
-        const int tok = i / (kLatent / 16), ch = i - tok * (kLatent / 16);
-        const uint4 u = *reinterpret_cast<const uint4*>(raw + tok * kRec + 16 * ch);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        uint32_t v[8];
-        bool bad = false;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          v[2 * n] = widen(__byte_perm(w[n], 0u, 0x1404));
-          v[2 * n + 1] = widen(__byte_perm(w[n], 0u, 0x3424));
-          bad |= has_nan_code(w[n]);
-        }
-        if ((ch & 7) == 0) bad |= !(fabsf(*reinterpret_cast<const float*>(raw + tok * kRec + kKvScaleOff + 4 * (ch >> 3))) * 448.0f < INFINITY);
-        if (bad) atomicOr(&s_words[par], 1u << tok);
-        uint4* dst = reinterpret_cast<uint4*>(smem + Sm::tile + (tok * kPitch + 16 * ch) * 2);
-        dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
-        dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    for (int j = 0; j < steps; ++j) {
+      const uint8_t* codes = smem + Sm::codes + (it & 1) * kTok * kPitch;
+      auto scale = [&](int tok) { return reinterpret_cast<const float*>(codes + tok * kPitch + kKvScaleOff); };
+      tc::mbar_wait(&s_full[it & 1], (it >> 1) & 1, &s_abort, a.status);
+      __syncthreads();  // this step's records are there; the last step's products are done
+      const bool real = real_next;
+      ++it;
+      if (j + 1 < steps) {
+        real_next = copy(j + 1, it, page_next);
+        page_next = page_of(j + 2);
       }
-    }
-    __syncthreads();
-    // ---- logits ----
-    {
-      const float* scale0 = reinterpret_cast<const float*>(raw + kKvScaleOff);  // of position 0; the next record + kRec bytes
-      auto scale = [&](int tok, int tile) { return *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(scale0) + tok * kRec + 4 * tile); };
-      const int i = lane >> 3, r = lane & 7;
-      const uint32_t base = smem_u32(smem + Sm::tile) + ((16 * tg + (i >> 1) * 8 + r) * kPitch + 128 * ks + (i & 1) * 8) * 2;
-      float acc[HT][2][4] = {}, tot[HT][2][4] = {};
-      auto fold = [&](int tile) {
+      // eight positions a warp: a scale that makes a value infinite poisons the position, as a NaN
+      // code does through its logit
+      {
+        const float* sc = scale(8 * warp + (lane & 7));
+        float sum = 0.f, top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 5; ++k) {
+          sum += fabsf(sc[k]);
+          top = fmaxf(top, fabsf(sc[k]));
+        }
+        const unsigned bad = __ballot_sync(0xffffffffu, sum != sum || !(top * 448.f < INFINITY)), some = __ballot_sync(0xffffffffu, real);
+        if (lane == 0) s_mask[warp] = static_cast<uint16_t>((some & 0xFFu) | (bad & 0xFFu) << 8);
+      }
+      // ---- logits ----
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int tok0 = 32 * tg + 16 * half;
+        const uint8_t* src = codes + (tok0 + (g & 1 ? second(g >> 1) : g >> 1)) * kPitch + 8 * q4;
+        float acc[HT][2][4];
+        float2 tot[HT][2][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint2 u = *reinterpret_cast<const uint2*>(src + 8 * n * kPitch + 128 * ks + 32 * i);
+            uint32_t b0, b1, b2, b3;
+            widen(u.x, b0, b1);
+            widen(u.y, b2, b3);
+#pragma unroll
+            for (int h = 0; h < HT; ++h) {
+              if (i == 0) mma16816_first(acc[h][n], qf[h][0], b0, b1);
+              else mma16816(acc[h][n], qf[h][2 * i], b0, b1);
+              mma16816(acc[h][n], qf[h][2 * i + 1], b2, b3);
+            }
+          }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const int tok = 16 * tg + 8 * n + 2 * q4;
-          const float sa = scale(tok, tile), sb = scale(tok + 1, tile);
+          const int tok_a = tok0 + 8 * n + q4, tok_b = tok0 + 8 * n + second(q4);
+          const float2 sc = make_float2(scale(tok_a)[ks], scale(tok_b)[ks]), sc4 = make_float2(scale(tok_a)[4], scale(tok_b)[4]);
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(src + 8 * n * kPitch + kVDim + 16 * ks - 4 * q4);
+          uint32_t b0, b1;
+          widen(u, b0, b1);
 #pragma unroll
           for (int h = 0; h < HT; ++h) {
-            tot[h][n][0] = fmaf(acc[h][n][0], sa, tot[h][n][0]);
-            tot[h][n][1] = fmaf(acc[h][n][1], sb, tot[h][n][1]);
-            tot[h][n][2] = fmaf(acc[h][n][2], sa, tot[h][n][2]);
-            tot[h][n][3] = fmaf(acc[h][n][3], sb, tot[h][n][3]);
 #pragma unroll
-            for (int z = 0; z < 4; ++z) acc[h][n][z] = 0.f;
+            for (int z = 0; z < 2; ++z)
+              tot[h][n][z] = mul2(mul2(make_float2(acc[h][n][2 * z], acc[h][n][2 * z + 1]), make_float2(q_back[h][z], q_back[h][z])), sc);
+            mma16816_first(acc[h][n], qf[h][8], b0, b1);
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+              *reinterpret_cast<float2*>(s_s + (ks * HT * 16 + 16 * h + g + 8 * z) * kSPitch + tok0 + 8 * n + 2 * q4) =
+                  fma2(mul2(make_float2(acc[h][n][2 * z], acc[h][n][2 * z + 1]), make_float2(q_back[h][z], q_back[h][z])), sc4, tot[h][n][z]);
           }
         }
-      };
+      }
+      __syncthreads();
+      // ---- weights ----
+      {
+        const unsigned mask = s_mask[lane >> 2];
+        bool seen[2], poison[2];
+        float4 sc[2];
+        float sc_top[2];
 #pragma unroll
-      for (int k = 0; k < 12; ++k) {
-        if (k < 8 || ks == 3) {
-          uint32_t b[4];
-          ldmatrix4(base + 32 * k, b);
+        for (int u = 0; u < 2; ++u) {
+          const int k = u ? second(lane & 3) : lane & 3;
+          seen[u] = mask >> k & 1u;
+          poison[u] = mask >> (8 + k) & 1u;
+          sc[u] = *reinterpret_cast<const float4*>(scale(8 * (lane >> 2) + k));
+          sc_top[u] = fmaxf(fmaxf(fabsf(sc[u].x), fabsf(sc[u].y)), fmaxf(fabsf(sc[u].z), fabsf(sc[u].w)));
+        }
 #pragma unroll
-          for (int h = 0; h < HT; ++h) {
-            mma16816(acc[h][0], qf[h][k], b[0], b[1]);
-            mma16816(acc[h][1], qf[h][k], b[2], b[3]);
+        for (int i = 0; i < 2 * HT; ++i) {
+          const int row = 2 * HT * warp + i;
+          const float* s = s_s + row * kSPitch + 2 * lane;
+          float x[2] = {0.f, 0.f};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const float2 part = *reinterpret_cast<const float2*>(s + z * HT * 16 * kSPitch);
+            x[0] += part.x;
+            x[1] += part.y;
           }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) x[u] = !seen[u] ? -INFINITY : poison[u] ? __uint_as_float(0x7FFFFFFFu) : x[u] * c2;
+          const float m_new = fmaxf(m_ref[i], warp_max(fmaxf(x[0], x[1])));
+          const float ref = m_new == -INFINITY ? 0.f : m_new;
+          const float alpha = exp2_approx(m_ref[i] - ref), p0 = exp2_approx(x[0] - ref), p1 = exp2_approx(x[1] - ref);
+          l_sum[i] = fmaf(l_sum[i], alpha, p0 + p1);
+          m_ref[i] = m_new;
+          // the unit: the larger of what was there, shrunk by alpha, and this step's largest weight
+          const float big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(p0 * sc_top[0], p1 * sc_top[1]))));
+          const int was = alpha > 0.f ? unit[i] + exponent(alpha) : kNoUnit;
+          const int now = max(max(was, kNoUnit), exponent(big));
+          const float up = exp2i(14 - now);
+          if (lane == 0) s_alpha[row] = alpha * exp2i(min(max(unit[i] - now, -126), 126));
+          unit[i] = now;
+          const float w0 = p0 * up, w1 = p1 * up;
+          uint32_t* dst = reinterpret_cast<uint32_t*>(smem + Sm::p) + (row * kPPitch + 2 * lane) / 2;
+          constexpr int kStride = HT * 16 * kPPitch / 2;
+          dst[0] = pack_half2(w0 * sc[0].x, w1 * sc[1].x);
+          dst[kStride] = pack_half2(w0 * sc[0].y, w1 * sc[1].y);
+          dst[2 * kStride] = pack_half2(w0 * sc[0].z, w1 * sc[1].z);
+          dst[3 * kStride] = pack_half2(w0 * sc[0].w, w1 * sc[1].w);
         }
-        if (k == 7) fold(ks);
       }
-      if (ks == 3) fold(4);
-#pragma unroll
-      for (int h = 0; h < HT; ++h)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          float* dst = s_s + (ks * HT * 16 + 16 * h + g) * kSPitch + 16 * tg + 8 * n + 2 * q4;
-          *reinterpret_cast<float2*>(dst) = make_float2(tot[h][n][0], tot[h][n][1]);
-          *reinterpret_cast<float2*>(dst + 8 * kSPitch) = make_float2(tot[h][n][2], tot[h][n][3]);
-        }
-    }
-    __syncthreads();
-    // ---- weights ----
-    {
-      const bool seen = (s_valid[par] >> lane) & 1u, poison = (s_words[par] >> lane) & 1u;
-      float sc[4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) sc[n] = *reinterpret_cast<const float*>(raw + lane * kRec + kKvScaleOff + 4 * n);
-#pragma unroll
-      for (int i = 0; i < 2 * HT; ++i) {
-        const int row = 2 * HT * warp + i;
-        float x = 0.f;
-#pragma unroll
-        for (int z = 0; z < 4; ++z) x += s_s[(z * HT * 16 + row) * kSPitch + lane];
-        x = !seen ? -INFINITY : poison ? __uint_as_float(0x7FFFFFFFu) : x * c2;
-        float mt = x;
-#pragma unroll
-        for (int z = 16; z; z >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, z));
-        const float m_new = fmaxf(m_ref[i], mt);
-        const float ref = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = exp2_approx(m_ref[i] - ref), p = exp2_approx(x - ref);
-        float sum = p;
-#pragma unroll
-        for (int z = 16; z; z >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
-        l_sum[i] = fmaf(l_sum[i], alpha, sum);
-        m_ref[i] = m_new;
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(smem + Sm::p) + row * kPPitch + lane;
-#pragma unroll
-        for (int n = 0; n < 4; ++n)  // (no scale of a position that is not seen may come in: 0 times it could be NaN)
-          dst[n * HT * 16 * kPPitch] = __float2bfloat16_rn(!seen ? 0.f : poison ? p : p * sc[n]);
-        if (lane == 0) s_alpha[row] = alpha;
-      }
-    }
-    __syncthreads();
-    // ---- output ----
-    {
-      const int i = lane >> 3, r = lane & 7;
+      __syncthreads();
+      // ---- output: dims 64 warp + 8 (column of the product) + n of the n-th product ----
 #pragma unroll
       for (int h = 0; h < HT; ++h) {
         const float f0 = s_alpha[16 * h + g], f1 = s_alpha[16 * h + g + 8];
         if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
-            o[h][n][0] *= f0;
-            o[h][n][1] *= f0;
-            o[h][n][2] *= f1;
-            o[h][n][3] *= f1;
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const float2 v = mul2(make_float2(o[h][n][2 * z], o[h][n][2 * z + 1]), z ? make_float2(f1, f1) : make_float2(f0, f0));
+              o[h][n][2 * z] = v.x;
+              o[h][n][2 * z + 1] = v.y;
+            }
           }
         }
       }
-      const uint32_t pb = smem_u32(smem + Sm::p) + (((warp >> 1) * HT * 16 + (i & 1) * 8 + r) * kPPitch + (i >> 1) * 8) * 2;
-      const uint32_t vb = smem_u32(smem + Sm::tile) + (((i & 1) * 8 + r) * kPitch + 64 * warp + (i >> 1) * 8) * 2;
+      const uint32_t pb = smem_u32(smem + Sm::p) + (((warp >> 1) * HT * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * kPPitch + (lane >> 4) * 8) * 2;
+      const uint8_t* src_a = codes + q4 * kPitch + 64 * warp + 8 * g;
+      const uint8_t* src_b = codes + second(q4) * kPitch + 64 * warp + 8 * g;
 #pragma unroll
       for (int k = 0; k < kTok / 16; ++k) {
         uint32_t pa[HT][4];
 #pragma unroll
         for (int h = 0; h < HT; ++h) ldmatrix4(pb + (16 * h * kPPitch + 16 * k) * 2, pa[h]);
+        uint2 u[4];  // the inner indices 2 q4, 2 q4 + 1, 2 q4 + 8, 2 q4 + 9
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          uint32_t b[4];
-          ldmatrix4_trans(vb + (16 * k * kPitch + 16 * n) * 2, b);
+        for (int r = 0; r < 4; ++r) u[r] = *reinterpret_cast<const uint2*>((r & 1 ? src_b : src_a) + (16 * k + 8 * (r >> 1)) * kPitch);
+#pragma unroll
+        for (int n = 0; n < 8; n += 2) {
+          const uint32_t order = n & 2 ? 0x7362 : 0x5140;
+          uint32_t b[2][2];
+          widen(__byte_perm(n < 4 ? u[0].x : u[0].y, n < 4 ? u[1].x : u[1].y, order), b[0][0], b[1][0]);
+          widen(__byte_perm(n < 4 ? u[2].x : u[2].y, n < 4 ? u[3].x : u[3].y, order), b[0][1], b[1][1]);
 #pragma unroll
           for (int h = 0; h < HT; ++h) {
-            mma16816(o[h][2 * n], pa[h], b[0], b[1]);
-            mma16816(o[h][2 * n + 1], pa[h], b[2], b[3]);
+            mma16816(o[h][n], pa[h], b[0][0], b[0][1]);
+            mma16816(o[h][n + 1], pa[h], b[1][0], b[1][1]);
           }
         }
       }
     }
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  // ---- this split's result ----
-  if (lane == 0) {
+    // ---- this part's result ----
 #pragma unroll
     for (int i = 0; i < 2 * HT; ++i) {
-      s_ref[2 * HT * warp + i] = m_ref[i];
-      s_sum[2 * HT * warp + i] = l_sum[i];
-    }
-  }
-  if (tid < HT * 16) s_top[tid] = 0;
-  __syncthreads();
+      float l = l_sum[i];
 #pragma unroll
-  for (int h = 0; h < HT; ++h) {
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const int row = 16 * h + g + 8 * z;
-      const float l = s_sum[row], inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      float top = 0.f;
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        o[h][n][2 * z] *= inv;
-        o[h][n][2 * z + 1] *= inv;
-        top = fmaxf(top, fmaxf(fabsf(o[h][n][2 * z]), fabsf(o[h][n][2 * z + 1])));
-      }
-      if (f.ns > 1 && top < INFINITY) atomicMax(&s_top[row], __float_as_uint(top));
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int h = 0; h < HT; ++h) {
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const int row = 16 * h + g + 8 * z;
-      if (row >= a.h_s) continue;
-      // the row's largest value below 2^15 in what is stored
-      const int e = f.ns > 1 ? max(static_cast<int>(s_top[row] >> 23) - 127 - 14, -120) : 0;
-      const float down = exp2i(-e);
-      const int64_t at = f.ns > 1 ? (row0 + row) * f.ns + f.slot0 + split : row0 + row;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(f.ns > 1 ? static_cast<void*>(f.o) : a.out) + (at * kVDim + 64 * warp) / 2 + q4;
-#pragma unroll
-      for (int n = 0; n < 8; ++n)
-        dst[4 * n] = f.ns > 1 ? pack_half2(o[h][n][2 * z] * down, o[h][n][2 * z + 1] * down)
-                              : pack_bf162(o[h][n][2 * z], o[h][n][2 * z + 1]);
-      if (warp == 0 && q4 == 0) {
-        if (f.ns > 1) f.ml[at] = split_state(s_ref[row], s_sum[row], e);
-        else if (a.out_lse) a.out_lse[at] = natural_lse(s_ref[row], s_sum[row]);
+      for (int z = 16; z; z >>= 1) l += __shfl_xor_sync(0xffffffffu, l, z);
+      if (lane == 0) {
+        s_ref[2 * HT * warp + i] = m_ref[i];
+        s_sum[2 * HT * warp + i] = l;
+        s_unit[2 * HT * warp + i] = unit[i];
       }
     }
+    if (tid < HT * 16) s_top[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < HT; ++h) {
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int row = 16 * h + g + 8 * z;
+        const float l = s_sum[row], inv = l > 0.f || l != l ? 1.f / l : 0.f, unit_size = exp2i(s_unit[row] - 14);
+        float top = 0.f;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          o[h][n][2 * z] = o[h][n][2 * z] * inv * unit_size;
+          o[h][n][2 * z + 1] = o[h][n][2 * z + 1] * inv * unit_size;
+          top = fmaxf(top, fmaxf(fabsf(o[h][n][2 * z]), fabsf(o[h][n][2 * z + 1])));
+        }
+        if (f.ns > 1 && top < INFINITY) atomicMax(&s_top[row], __float_as_uint(top));
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < HT; ++h) {
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int row = 16 * h + g + 8 * z;
+        if (row >= a.h_s) continue;
+        // the row's largest value below 2^15 in what is stored
+        const int e = f.ns > 1 ? max(static_cast<int>(s_top[row] >> 23) - 127 - 14, -120) : 0;
+        const float down = exp2i(-e);
+        const int64_t at = f.ns > 1 ? (row0 + row) * f.ns + f.slot0 + min(slot, f.splits - 1) : row0 + row;
+        uint4* dst = reinterpret_cast<uint4*>((f.ns > 1 ? static_cast<uint16_t*>(static_cast<void*>(f.o)) : static_cast<uint16_t*>(a.out)) +
+                                              at * kVDim + 64 * warp + 16 * q4);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {  // dims 8 c .. of this thread's 16
+          uint32_t v[4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const float x = o[h][2 * n][2 * z + c], y = o[h][2 * n + 1][2 * z + c];
+            v[n] = f.ns > 1 ? pack_half2(x * down, y * down) : pack_bf162(x, y);
+          }
+          dst[c] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        if (warp == 0 && q4 == 0) {
+          if (f.ns > 1) f.ml[at] = split_state(s_ref[row], s_sum[row], e);
+          else if (a.out_lse) a.out_lse[at] = natural_lse(s_ref[row], s_sum[row]);
+        }
+      }
+    }
+    // ---- the next row with positions, if the share goes on ----
+    left -= steps;
+    if (left <= 0 || f.splits == 1) break;
+    step0 = slot = 0;
+    for (++t; t < a.n_q; t += 32) {
+      const int r = t + lane;
+      const unsigned some = __ballot_sync(0xffffffffu, r < a.n_q && steps_of(prefix_row_limit(a, r, false)) > 0);
+      if (some) {
+        t += __ffs(some) - 1;
+        break;
+      }
+    }
   }
+  // after a wait that gave up, copies may still be in flight
+  if (tid == 0 && *static_cast<volatile int*>(&s_abort))
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t uses = (it + 1 - i) / 2;
+      if (uses) tc::mbar_drain(&s_full[i], (uses - 1) & 1, tc::kWaitLimitNs);
+    }
 }
 
 template <int HT>
@@ -364,7 +525,7 @@ cudaError_t launch(const FewArgs& f, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(few_kernel<HT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(FewSmem<HT>::bytes));
   if (e != cudaSuccess) return e;
-  return launch_pdl(few_kernel<HT>, dim3(static_cast<unsigned>(f.splits) * f.a.n_q), dim3(kThreads), FewSmem<HT>::bytes, s, 1, f);
+  return launch_pdl(few_kernel<HT>, dim3(static_cast<unsigned>(f.blocks)), dim3(kThreads), FewSmem<HT>::bytes, s, 1, f);
 }
 
 }  // namespace

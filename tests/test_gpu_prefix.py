@@ -112,7 +112,7 @@ class Batch:
             p = w / z
             ref, size = p @ kv[:, :512], p @ np.abs(kv[:, :512])
             d = SM * (np.abs(q) @ np.abs(kv).T).max() * 576 * 2.0 ** -24
-            tol = ((2.0 ** -11 + (2.0 ** -8 if self.h <= 32 else 2.0 ** -11) + 2 * d + 2.0 ** -20) * size + len(kv) * 2.0 ** -25 * np.abs(kv[:, :512]).max()
+            tol = ((2.0 ** -11 + 2.0 ** -11 + 2 * d + 2.0 ** -20) * size + len(kv) * 2.0 ** -25 * np.abs(kv[:, :512]).max()
                    + 2.0 ** -8 * np.abs(ref) + 1e-30)
             bad = np.abs(o[t] - ref) / tol
             assert bad.max() <= 1, (t, bad.max())
@@ -134,6 +134,9 @@ def _raw(lib, **kw):
              max_ctx=200, scale=0.07, out=8, lse=None, ws=9, ws_bytes=1 << 40, shift=0)
     a.update(kw)
     p = lambda v, s=0: None if v is None else P(v * 65536 + s)  # noqa: E731
+    if a["ws_bytes"] < 0:  # one byte too few
+        lib.dsa_prefix_attn_workspace_size.restype = ctypes.c_size_t
+        a["ws_bytes"] += lib.dsa_prefix_attn_workspace_size(a["n_q"], a["h_s"], a["n_seq"], a["prefix"], a["max_ctx"])
     return lib.dsa_prefix_attn(p(a["q"], a["shift"]), a["n_q"], a["h_s"], p(a["cache"]), a["pages"], p(a["pp"]),
                                a["prefix"], p(a["pt"]), a["max_pages"], p(a["lens"]), a["n_seq"], p(a["qs"]), p(a["qp"]),
                                a["max_ctx"], ctypes.c_float(a["scale"]), p(a["out"]), p(a["lse"]), p(a["ws"]),
@@ -146,7 +149,7 @@ def _raw(lib, **kw):
     (dict(pages=0), -1), (dict(max_pages=3), -1), (dict(scale=0.0), -1), (dict(scale=float("nan")), -1),
     (dict(scale=float("inf")), -1), (dict(q=None), -1), (dict(cache=None), -1), (dict(pp=None), -1),
     (dict(pt=None), -1), (dict(lens=None), -1), (dict(qs=None), -1), (dict(qp=None), -1), (dict(out=None), -1),
-    (dict(ws=None), -1), (dict(ws_bytes=1000), -1), (dict(shift=8), -1),
+    (dict(ws=None), -1), (dict(ws_bytes=-1), -1), (dict(ws_bytes=-1, h_s=128), -1), (dict(shift=8), -1),
     (dict(n_q=0, q=None, out=None, ws=None), 0),
 ])
 def test_refusals(dsa, kw, code):
