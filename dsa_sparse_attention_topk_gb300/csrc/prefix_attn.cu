@@ -144,7 +144,7 @@ static_assert(kRows * kStagePitch <= Layout<1>::ctl - Layout<1>::v && kRows * kS
               "output staging");
 
 // A split costs every row its partial output, once written and once read, at some 5 TB/s.
-constexpr double kJoinUs = 2048.0 / 5.0e6, kFewUs16 = 1.2, kFewUs32 = 1.2;
+constexpr double kJoinUs = 2048.0 / 5.0e6, kFewUs16 = 1.5, kFewUs16Pair = 3.6, kFewUs32 = 2.2;
 
 // What expand writes per tile.
 struct alignas(32) TileInfo {
@@ -215,8 +215,9 @@ double plan_tiles(PrefixPlan& p, int n_q, int n_sm) {
 }
 
 // All of it on the tensor-memory path, or (up to 32 heads) the tails or everything on the path for
-// few heads, which takes kFewUs per 32 positions of a row, on two blocks per SM (16 heads) or
-// one: it reads nothing twice but a prefix, once for every row.
+// few heads.  There 64 positions of a row take 1.5 us alone on an SM and 3.6 us with two blocks on
+// it (17 heads and more: 2.2 us, one block), a block's start and end some 5 us and a further row in
+// it 4.5 us; it reads nothing twice but a prefix, once for every row.
 PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, int n_sm) {
   PrefixPlan p{};
   p.n_seq = n_seq;
@@ -227,7 +228,6 @@ PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, i
   double best = plan_tiles(p, n_q, n_sm);
   if (h_s <= kFewHeads) {
     const int fit = h_s <= 16 ? 2 * n_sm : n_sm;
-    const double step_us = h_s <= 16 ? kFewUs16 : kFewUs32;
     for (int whole = 0; whole < 2; ++whole) {  // the tails, then everything
       const int lo = whole ? 0 : prefix_len;
       if ((!whole && !prefix_len) || lo == max_ctx) continue;
@@ -239,11 +239,13 @@ PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, i
       const int steps = (max_ctx - lo + 63) / 64, sure = whole ? prefix_len / 64 : 0;
       const double mean = 0.5 * (steps + sure) * n_q;  // of all rows, tails half full
       const int even = static_cast<int>(std::min<int64_t>(fit, static_cast<int64_t>(steps) * n_q));
-      for (int few = 1; few <= std::min(2 * steps, 64); few *= 2) {
+      for (int few = 1; few <= (n_q > kFewCutRows ? 1 : std::min(2 * steps, 64)); few *= 2) {
         // a row a block, the longest one last; or even shares
-        const double t = rest + 4.0 + kJoinUs * n_q * h_s * few + (few > 1 || q.sp ? 3.0 : 0.0) +
-                         (few == 1 ? step_us * std::max<double>(steps, mean / fit + (n_q > fit ? 0.5 * steps : 0.0))
-                                   : 1.5 + 1.5 * (1.0 + n_q / even) + step_us * std::max({mean / even, steps / (few - 1.0), 1.0}));
+        const int blocks = few == 1 ? n_q : even;
+        const double step = h_s > 16 ? kFewUs32 : blocks <= n_sm ? kFewUs16 : kFewUs16Pair, parts = std::min<double>(few, 1.0 + even / n_q);
+        const double t = rest + 5.0 + kJoinUs * n_q * h_s * (few == 1 ? 1 : parts) + (few > 1 || q.sp ? 3.0 : 0.0) +
+                         (few == 1 ? step * std::max<double>(steps, mean / fit + (n_q > fit ? 0.5 * steps : 0.0)) + 4.5 * (n_q / fit)
+                                   : step * std::max({mean / even, steps / (few - 1.0), 1.0}) + 4.5 * n_q / even);
         if (t < best) {
           best = t;
           q.few_lo = lo;

@@ -64,6 +64,7 @@ struct FewArgs {
   int* used;
 };
 constexpr int kFewHeads = 32;
+constexpr int kFewCutRows = 65536;  // with more rows none is cut: 2^16 rows of 2^14 steps are what 31 bits count
 cudaError_t launch_prefix_few(const FewArgs& f, cudaStream_t s);
 
 }  // namespace dsa

@@ -43,8 +43,7 @@ constexpr int kPPitch = kTok + 8, kSPitch = kTok + 8;
 template <int HT> struct FewSmem {
   // two steps' records; weights; partial logits
   static constexpr uint32_t codes = 0, p = codes + 2 * kTok * kPitch, s = p + 4 * HT * 16 * kPPitch * 2;
-  static constexpr uint32_t alpha = s + 4 * HT * 16 * kSPitch * 4, top = alpha + HT * 16 * 4, sum = top + HT * 16 * 4;
-  static constexpr uint32_t ref = sum + HT * 16 * 4, unit = ref + HT * 16 * 4, bytes = unit + HT * 16 * 4;
+  static constexpr uint32_t alpha = s + 4 * HT * 16 * kSPitch * 4, inv = alpha + HT * 16 * 4, bytes = inv + HT * 16 * 4;
 };
 static_assert(FewSmem<1>::bytes * 2 <= 232448 - 2048 && FewSmem<2>::bytes <= 232448, "shared memory");
 
@@ -100,15 +99,13 @@ few_kernel(FewArgs f) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float* s_s = reinterpret_cast<float*>(smem + Sm::s);
   float* s_alpha = reinterpret_cast<float*>(smem + Sm::alpha);
-  unsigned* s_top = reinterpret_cast<unsigned*>(smem + Sm::top);
-  float* s_sum = reinterpret_cast<float*>(smem + Sm::sum);
-  float* s_ref = reinterpret_cast<float*>(smem + Sm::ref);
-  int* s_unit = reinterpret_cast<int*>(smem + Sm::unit);
+  float* s_inv = reinterpret_cast<float*>(smem + Sm::inv);
   __shared__ uint64_t s_full[2];          // a step's records are there
-  __shared__ uint16_t s_mask[kTok / 8];   // of eight positions: which exist, and in the upper byte which are poisonous
+  __shared__ uint8_t s_seen[2][kTok / 8];  // and which of eight positions exist
+  __shared__ uint8_t s_bad[kTok / 8];     // of eight positions: which are poisonous
   __shared__ int s_abort;
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&s_full[i], kTok);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&s_full[i], 2 * kThreads / 32);
     s_abort = 0;
     tc::mbar_fence_init();
   }
@@ -118,7 +115,7 @@ few_kernel(FewArgs f) {
   auto steps_of = [&](int lim) { return lim > f.lo ? (lim - f.lo + kTok - 1) / kTok : 0; };
   // ---- this block's share: a row, or `share` steps of all rows' steps end to end ----
   int t = blockIdx.x, step0 = 0, slot = 0;
-  int64_t left;
+  int left;
   if (f.splits == 1) {
     left = steps_of(prefix_row_limit(a, t, tid == 0));
     if (left == 0) {
@@ -134,51 +131,52 @@ few_kernel(FewArgs f) {
       return;
     }
   } else {
-    __shared__ int64_t s_sum64[kThreads / 32];
-    __shared__ int s_most[kThreads / 32], s_first[3];
-    // every thread adds up a run of rows, and the block their sums
-    const int run = (a.n_q + kThreads - 1) / kThreads;
-    const int64_t first = static_cast<int64_t>(tid) * run, last = min(first + run, static_cast<int64_t>(a.n_q));
-    int64_t sum = 0;
-    int most = 0;
-    for (int64_t r = first; r < last; ++r) {
-      const int n = steps_of(prefix_row_limit(a, static_cast<int>(r), blockIdx.x == 0));
+    __shared__ int s_total[kThreads / 32], s_most[kThreads / 32], s_first[3];
+    // every thread adds up a run of rows, and the block their sums (below 2^31: kFewCutRows)
+    const int run = (a.n_q + kThreads - 1) / kThreads, first = min(tid * run, a.n_q), last = min(first + run, a.n_q);
+    int sum = 0, most = 0;
+#pragma unroll 1
+    for (int r = first; r < last; ++r) {
+      const int n = steps_of(prefix_row_limit(a, r, blockIdx.x == 0));
       sum += n;
       most = max(most, n);
       if (n == 0 && r % gridDim.x == blockIdx.x) f.used[r] = 0;
     }
-    int64_t upto = sum;
+    int upto = sum;
 #pragma unroll
     for (int z = 1; z < 32; z <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, upto, z);
+      const int v = __shfl_up_sync(0xffffffffu, upto, z);
       if (lane >= z) upto += v;
     }
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 31) {
-      s_sum64[warp] = upto;
+      s_total[warp] = upto;
       s_most[warp] = most;
     }
     if (tid == 0) s_first[0] = a.n_q;
     __syncthreads();
-    int64_t before = upto - sum, total = 0;
+    int before = upto - sum, total = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += s_sum64[w];
-      total += s_sum64[w];
+      if (w < warp) before += s_total[w];
+      total += s_total[w];
       most = max(most, s_most[w]);
     }
     // a row of n steps reaches into at most (n - 1) / share + 2 shares
-    const int64_t share = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>((most + f.splits - 2) / (f.splits - 1)));
-    const int64_t from = blockIdx.x * share;
+    const int blocks = gridDim.x, block = blockIdx.x;
+    const int share = max((total + blocks - 1) / blocks, (most + f.splits - 2) / (f.splits - 1));
+    // (total <= blocks * share, but share times the block's number may pass 2^31 in the blocks left over)
+    if (share == 0 || block > (total - 1) / share) return;
+    const int from = block * share;
     left = min(share, total - from);
-    if (left <= 0) return;
     if (before <= from && from < before + sum) {
-      for (int64_t r = first; r < last; ++r) {
-        const int n = steps_of(prefix_row_limit(a, static_cast<int>(r), false));
+#pragma unroll 1
+      for (int r = first; r < last; ++r) {
+        const int n = steps_of(prefix_row_limit(a, r, false));
         if (from < before + n) {
-          s_first[0] = static_cast<int>(r);
-          s_first[1] = static_cast<int>(from - before);
-          s_first[2] = static_cast<int>(blockIdx.x - before / share);
+          s_first[0] = r;
+          s_first[1] = from - before;
+          s_first[2] = block - before / share;
           break;
         }
         before += n;
@@ -193,107 +191,132 @@ few_kernel(FewArgs f) {
   const int g = lane >> 2, q4 = lane & 3;
   __syncthreads();
   const int tg = warp & 1, ks = warp >> 1;   // logits: positions 32 tg .., scale tile ks
-  const int c_tok = 8 * warp + lane;         // copies: the first eight lanes, a position each
-  uint32_t it = 0;                           // steps so far: the records of step i go to buffer i % 2
-  bool zeroed = false;
+  uint32_t it = ~0u;                         // steps so far less 1: the records of step i go to buffer i % 2
   const float c2 = a.sm_scale * 1.4426950408889634f;  // logits in powers of two
 #pragma unroll 1
   while (t < a.n_q) {
-    const int lim = prefix_row_limit(a, t, false), rest = steps_of(lim) - step0;
-    const int steps = static_cast<int>(min(static_cast<int64_t>(rest), left));
     const int64_t row0 = static_cast<int64_t>(t) * a.h_s;
+    // ---- this warp's share of the query (used last of what is read here, so asked for first) ----
+    // K-steps 2 j and 2 j + 1: dims 128 ks + 32 j + 8 q4 + 0 .. 3 and 4 .. 7; the ninth: 512 + 16 ks + 4 q4 ..
+    uint32_t qf[HT][kKs][4];
+#pragma unroll
+    for (int h = 0; h < HT; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int head = 16 * h + g + 8 * i;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (row0 + head) * kLatent;
+#pragma unroll
+        for (int k = 0; k < kKs; ++k) {
+          const int d = k < 8 ? 128 * ks + 16 * (k & 6) + 8 * q4 + 4 * (k & 1) : kVDim + 16 * ks + 4 * q4;
+          uint2 v = make_uint2(0u, 0u);
+          if (head < a.h_s) v = *reinterpret_cast<const uint2*>(q + d);
+          qf[h][k][i] = v.x;
+          qf[h][k][i + 2] = v.y;
+        }
+      }
+    const int lim = prefix_row_limit(a, t, false), rest = steps_of(lim) - step0;
+    const int steps = min(rest, left);
     if (f.ns > 1 && steps == rest && tid == 0) f.used[t] = slot + 1;
     const int32_t* table = a.page_table + static_cast<int64_t>(a.q_seq[t]) * a.max_pages;
 
-    // the copying lanes' positions p0 + 64 j, below `end`
-    const int p0 = f.lo + step0 * kTok + c_tok, end = min(lim, f.lo + (step0 + steps) * kTok);
-    static_assert(kTok == kPage, "a lane's place in the page stays");
-    const uint8_t* src0 = a.kv_cache + p0 % kPage * kKvTokBytes;
+    // Copies: a warp's eight positions of a step lie in one page, or in two where a page or the prefix
+    // ends among them: lane 0 or 1 copies n positions from `first` on.
+    static_assert(kTok == 8 * (kThreads / 32), "eight positions a warp");
+    const int end = min(lim, f.lo + (step0 + steps) * kTok);
+    auto run_of = [&](int step, int& first) {
+      const int p = f.lo + (step0 + step) * kTok + 8 * warp, e = min(p + 8, end);
+      const int cut = min(e, p < a.prefix_len ? min(a.prefix_len, p / kPage * kPage + kPage) : p / kPage * kPage + kPage);
+      first = lane == 0 ? p : cut;
+      return lane == 0 ? cut - p : lane == 1 ? e - cut : 0;
+    };
     auto page_of = [&](int step) {
-      const int p = p0 + step * kTok;
-      return lane >= 8 || p >= end ? -1 : p < a.prefix_len ? a.prefix_pages[p / kPage] : table[p / kPage];
+      int first, page = -1;
+      const int n = run_of(step, first);
+      const int32_t* at = (first < a.prefix_len ? a.prefix_pages : table) + first / kPage;
+      if (step < steps && n > 0) page = *at;
+      return page;
     };
-    // (in the first eight lanes) whether the position exists; what does not becomes zero
+    // what does not exist becomes zero
     auto copy = [&](int step, uint32_t nth, int page) {
-      const bool real = page >= 0 && page < a.num_pages;
-      if (lane < 8) {
-        uint8_t* dst = smem + Sm::codes + ((nth & 1) * kTok + c_tok) * kPitch;
-        uint64_t* full = &s_full[nth & 1];
-        if (real && !*static_cast<volatile int*>(&s_abort)) {
-          if (zeroed) tc::fence_async_smem();
-          tc::mbar_arrive_expect_tx(full, kKvTokBytes);
-          tc::bulk_load(dst, src0 + static_cast<int64_t>(page) * (kPage * kKvTokBytes), kKvTokBytes, full);
-        } else {
-          if (!real && p0 + step * kTok < end) flag(a.status, DSA_STATUS_BAD_PAGE);
-          zeroed = true;
+      int first;
+      const int n = run_of(step, first), place = first - (f.lo + (step0 + step) * kTok);
+      const bool found = n > 0 && page >= 0 && page < a.num_pages, real = found && !*static_cast<volatile int*>(&s_abort);
+      if (n > 0 && !found) flag(a.status, DSA_STATUS_BAD_PAGE);
+      const unsigned seen = __reduce_or_sync(0xffffffffu, real ? (255u >> (8 - n)) << (place & 7) : 0u);
+      uint8_t* dst = smem + Sm::codes + (nth & 1) * kTok * kPitch;
+      if (seen != 255u) {
 #pragma unroll 1
-          for (int i = 0; i < kKvTokBytes; i += 16) *reinterpret_cast<uint4*>(dst + i) = make_uint4(0u, 0u, 0u, 0u);
-          tc::mbar_arrive(full);
+        for (unsigned rest = ~seen & 255u; rest; rest &= rest - 1) {
+          uint8_t* row = dst + (8 * warp + __ffs(rest) - 1) * kPitch;
+          for (int i = 16 * lane; i < kPitch; i += 512) *reinterpret_cast<uint4*>(row + i) = make_uint4(0u, 0u, 0u, 0u);
         }
+        tc::fence_async_smem();  // before later copies to the same place
+        __syncwarp();
       }
-      return real;
+      uint64_t* full = &s_full[nth & 1];
+      if (lane == 0) s_seen[nth & 1][warp] = static_cast<uint8_t>(seen);
+      if (real) {
+        tc::mbar_arrive_expect_tx(full, n * kPitch);
+        tc::bulk_load(dst + place * kPitch, a.kv_cache + (static_cast<int64_t>(page) * kPage + first % kPage) * kPitch, n * kPitch, full);
+      } else if (lane < 2) {
+        tc::mbar_arrive(full);
+      }
+      __syncwarp();
     };
-    bool real_next = copy(0, it, page_of(0));
-    int page_next = page_of(1);
-
-    // ---- this warp's share of the query, as fp16 times a power of two per head ----
-    // K-steps 2 j and 2 j + 1: dims 128 ks + 32 j + 8 q4 + 0 .. 3 and 4 .. 7; the ninth: 512 + 16 ks + 4 q4 ..
-    uint32_t qf[HT][kKs][4];
+    int page_next = page_of(0);
+    // the query as fp16 times a power of two per head
     float q_back[HT][2];  // the power's inverse, for heads g and g + 8
-    {
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + row0 * kLatent;
 #pragma unroll
-      for (int h = 0; h < HT; ++h) {
+    for (int h = 0; h < HT; ++h) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int head = 16 * h + g + 8 * i;
-          uint32_t top = 0;
+      for (int i = 0; i < 2; ++i) {
+        __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
-          for (int k = 0; k < kKs; ++k) {
-            const int d = k < 8 ? 128 * ks + 16 * (k & 6) + 8 * q4 + 4 * (k & 1) : kVDim + 16 * ks + 4 * q4;
-            const uint2 v = head < a.h_s ? *reinterpret_cast<const uint2*>(q + static_cast<int64_t>(head) * kLatent + d) : make_uint2(0u, 0u);
-            qf[h][k][i] = v.x;
-            qf[h][k][i + 2] = v.y;
-            top = max(max(top, max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu)), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu));
+        for (int k = 0; k < kKs; ++k)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&qf[h][k][i + 2 * z])));
+        float top = fmaxf(__low2float(top2), __high2float(top2));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = min(max(exponent(top) - 14, -126), 112);  // the largest below 2^15 (infinities and NaN stay)
+        const float up = exp2i(-e);
+        q_back[h][i] = exp2i(e);
+#pragma unroll
+        for (int k = 0; k < kKs; ++k)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            uint32_t& v = qf[h][k][i + 2 * z];
+            const float2 x = mul2(make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u)), make_float2(up, up));
+            v = pack_half2(x.x, x.y);
           }
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int e = min(max(static_cast<int>(top >> 7) - 127 - 14, -126), 112);  // the largest below 2^15 (infinities and NaN stay)
-          const float up = exp2i(-e);
-          q_back[h][i] = exp2i(e);
-#pragma unroll
-          for (int k = 0; k < kKs; ++k)
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              uint32_t& v = qf[h][k][i + 2 * z];
-              v = pack_half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
-            }
-        }
       }
     }
     float o[HT][8][4] = {};
     // the weights' warp: rows 2 HT warp .. of the 16 HT, lane = columns 2 lane and 2 lane + 1; the sum is the lane's own
-    float m_ref[2 * HT], l_sum[2 * HT];
+    float m_ref[2 * HT], l_sum[2 * HT], w_sum[2 * HT];  // reference, and the sums of weights and of weights times largest scales
     int unit[2 * HT];  // the output's unit is 2^(unit - 14)
 #pragma unroll
     for (int i = 0; i < 2 * HT; ++i) {
       m_ref[i] = -INFINITY;
-      l_sum[i] = 0.f;
+      l_sum[i] = w_sum[i] = 0.f;
       unit[i] = kNoUnit;
     }
 
 #pragma unroll 1
-    for (int j = 0; j < steps; ++j) {
-      const uint8_t* codes = smem + Sm::codes + (it & 1) * kTok * kPitch;
-      auto scale = [&](int tok) { return reinterpret_cast<const float*>(codes + tok * kPitch + kKvScaleOff); };
-      tc::mbar_wait(&s_full[it & 1], (it >> 1) & 1, &s_abort, a.status);
-      __syncthreads();  // this step's records are there; the last step's products are done
-      const bool real = real_next;
-      ++it;
+    for (int j = -1; j < steps; ++j, ++it) {
+      // this step's records are there, the last step's products are done, and the next step's records
+      // are asked for
+      if (j >= 0) {
+        tc::mbar_wait(&s_full[it & 1], (it >> 1) & 1, &s_abort, a.status);
+        __syncthreads();
+      }
       if (j + 1 < steps) {
-        real_next = copy(j + 1, it, page_next);
+        copy(j + 1, it + 1, page_next);
         page_next = page_of(j + 2);
       }
+      if (j < 0) continue;
+      const uint8_t* codes = smem + Sm::codes + (it & 1) * kTok * kPitch;
+      auto scale = [&](int tok) { return reinterpret_cast<const float*>(codes + tok * kPitch + kKvScaleOff); };
       // eight positions a warp: a scale that makes a value infinite poisons the position, as a NaN
       // code does through its logit
       {
@@ -304,8 +327,8 @@ few_kernel(FewArgs f) {
           sum += fabsf(sc[k]);
           top = fmaxf(top, fabsf(sc[k]));
         }
-        const unsigned bad = __ballot_sync(0xffffffffu, sum != sum || !(top * 448.f < INFINITY)), some = __ballot_sync(0xffffffffu, real);
-        if (lane == 0) s_mask[warp] = static_cast<uint16_t>((some & 0xFFu) | (bad & 0xFFu) << 8);
+        const unsigned bad = __ballot_sync(0xffffffffu, sum != sum || !(top * 448.f < INFINITY));
+        if (lane == 0) s_bad[warp] = static_cast<uint8_t>(bad);
       }
       // ---- logits ----
 #pragma unroll
@@ -352,15 +375,15 @@ few_kernel(FewArgs f) {
       __syncthreads();
       // ---- weights ----
       {
-        const unsigned mask = s_mask[lane >> 2];
+        const unsigned some = s_seen[it & 1][lane >> 2], bad = s_bad[lane >> 2];
         bool seen[2], poison[2];
         float4 sc[2];
         float sc_top[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int k = u ? second(lane & 3) : lane & 3;
-          seen[u] = mask >> k & 1u;
-          poison[u] = mask >> (8 + k) & 1u;
+          seen[u] = some >> k & 1u;
+          poison[u] = bad >> k & 1u;
           sc[u] = *reinterpret_cast<const float4*>(scale(8 * (lane >> 2) + k));
           sc_top[u] = fmaxf(fmaxf(fabsf(sc[u].x), fabsf(sc[u].y)), fmaxf(fabsf(sc[u].z), fabsf(sc[u].w)));
         }
@@ -383,7 +406,8 @@ few_kernel(FewArgs f) {
           l_sum[i] = fmaf(l_sum[i], alpha, p0 + p1);
           m_ref[i] = m_new;
           // the unit: the larger of what was there, shrunk by alpha, and this step's largest weight
-          const float big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(p0 * sc_top[0], p1 * sc_top[1]))));
+          const float b0 = p0 * sc_top[0], b1 = p1 * sc_top[1], big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(b0, b1))));
+          w_sum[i] = fmaf(w_sum[i], alpha, b0 + b1);
           const int was = alpha > 0.f ? unit[i] + exponent(alpha) : kNoUnit;
           const int now = max(max(was, kNoUnit), exponent(big));
           const float up = exp2i(14 - now);
@@ -441,68 +465,60 @@ few_kernel(FewArgs f) {
       }
     }
     // ---- this part's result ----
+    const int out_slot = f.slot0 + min(slot, f.splits - 1);
+    float l = 0.f, w = 0.f, m = 0.f;  // lane i has row i of this warp's
+    int u = 0;
 #pragma unroll
     for (int i = 0; i < 2 * HT; ++i) {
-      float l = l_sum[i];
 #pragma unroll
-      for (int z = 16; z; z >>= 1) l += __shfl_xor_sync(0xffffffffu, l, z);
-      if (lane == 0) {
-        s_ref[2 * HT * warp + i] = m_ref[i];
-        s_sum[2 * HT * warp + i] = l;
-        s_unit[2 * HT * warp + i] = unit[i];
+      for (int z = 16; z; z >>= 1) {
+        l_sum[i] += __shfl_xor_sync(0xffffffffu, l_sum[i], z);
+        w_sum[i] += __shfl_xor_sync(0xffffffffu, w_sum[i], z);
       }
+      if (lane == i) l = l_sum[i], w = w_sum[i], m = m_ref[i], u = unit[i];
     }
-    if (tid < HT * 16) s_top[tid] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < HT; ++h) {
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const int row = 16 * h + g + 8 * z;
-        const float l = s_sum[row], inv = l > 0.f || l != l ? 1.f / l : 0.f, unit_size = exp2i(s_unit[row] - 14);
-        float top = 0.f;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          o[h][n][2 * z] = o[h][n][2 * z] * inv * unit_size;
-          o[h][n][2 * z + 1] = o[h][n][2 * z + 1] * inv * unit_size;
-          top = fmaxf(top, fmaxf(fabsf(o[h][n][2 * z]), fabsf(o[h][n][2 * z + 1])));
-        }
-        if (f.ns > 1 && top < INFINITY) atomicMax(&s_top[row], __float_as_uint(top));
+    if (lane < 2 * HT) {
+      const int row = 2 * HT * warp + lane;
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      // no output is above 448 w / l: a part's goes below 2^15
+      const int e = f.ns > 1 ? max(exponent(w * inv) - 5, -120) : 0;
+      s_inv[row] = inv * exp2i(u - 14 - e);
+      if (row < a.h_s) {
+        if (f.ns > 1) f.ml[(row0 + row) * f.ns + out_slot] = split_state(m, l, e);
+        else if (a.out_lse) a.out_lse[row0 + row] = natural_lse(m, l);
       }
     }
     __syncthreads();
+    // (halves of 16 bits; from here on a part's rows are ns apart)
+    uint16_t* out = (f.ns > 1 ? reinterpret_cast<uint16_t*>(f.o) + (row0 * f.ns + out_slot) * kVDim : static_cast<uint16_t*>(a.out) + row0 * kVDim) +
+                    64 * warp + 16 * q4;
 #pragma unroll
     for (int h = 0; h < HT; ++h) {
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
         const int row = 16 * h + g + 8 * z;
         if (row >= a.h_s) continue;
-        // the row's largest value below 2^15 in what is stored
-        const int e = f.ns > 1 ? max(static_cast<int>(s_top[row] >> 23) - 127 - 14, -120) : 0;
-        const float down = exp2i(-e);
-        const int64_t at = f.ns > 1 ? (row0 + row) * f.ns + f.slot0 + min(slot, f.splits - 1) : row0 + row;
-        uint4* dst = reinterpret_cast<uint4*>((f.ns > 1 ? static_cast<uint16_t*>(static_cast<void*>(f.o)) : static_cast<uint16_t*>(a.out)) +
-                                              at * kVDim + 64 * warp + 16 * q4);
+        const float inv = s_inv[row];
+        uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(row) * f.ns * kVDim);
+        float2 x[8];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {  // dims 8 c .. of this thread's 16
-          uint32_t v[4];
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const float x = o[h][2 * n][2 * z + c], y = o[h][2 * n + 1][2 * z + c];
-            v[n] = f.ns > 1 ? pack_half2(x * down, y * down) : pack_bf162(x, y);
-          }
-          dst[c] = make_uint4(v[0], v[1], v[2], v[3]);
-        }
-        if (warp == 0 && q4 == 0) {
-          if (f.ns > 1) f.ml[at] = split_state(s_ref[row], s_sum[row], e);
-          else if (a.out_lse) a.out_lse[at] = natural_lse(s_ref[row], s_sum[row]);
+        for (int n = 0; n < 8; ++n)  // dims 2 n and 2 n + 1 of this thread's 16
+          x[n] = mul2(make_float2(o[h][2 * n % 8][2 * z + n / 4], o[h][2 * n % 8 + 1][2 * z + n / 4]), make_float2(inv, inv));
+        if (f.ns > 1) {
+          dst[0] = make_uint4(pack_half2(x[0].x, x[0].y), pack_half2(x[1].x, x[1].y), pack_half2(x[2].x, x[2].y), pack_half2(x[3].x, x[3].y));
+          dst[1] = make_uint4(pack_half2(x[4].x, x[4].y), pack_half2(x[5].x, x[5].y), pack_half2(x[6].x, x[6].y), pack_half2(x[7].x, x[7].y));
+        } else {
+          dst[0] = make_uint4(pack_bf162(x[0].x, x[0].y), pack_bf162(x[1].x, x[1].y), pack_bf162(x[2].x, x[2].y), pack_bf162(x[3].x, x[3].y));
+          dst[1] = make_uint4(pack_bf162(x[4].x, x[4].y), pack_bf162(x[5].x, x[5].y), pack_bf162(x[6].x, x[6].y), pack_bf162(x[7].x, x[7].y));
         }
       }
     }
     // ---- the next row with positions, if the share goes on ----
+    --it;
     left -= steps;
     if (left <= 0 || f.splits == 1) break;
     step0 = slot = 0;
+#pragma unroll 1
     for (++t; t < a.n_q; t += 32) {
       const int r = t + lane;
       const unsigned some = __ballot_sync(0xffffffffu, r < a.n_q && steps_of(prefix_row_limit(a, r, false)) > 0);
@@ -515,7 +531,7 @@ few_kernel(FewArgs f) {
   // after a wait that gave up, copies may still be in flight
   if (tid == 0 && *static_cast<volatile int*>(&s_abort))
     for (int i = 0; i < 2; ++i) {
-      const uint32_t uses = (it + 1 - i) / 2;
+      const uint32_t uses = (it + 2 - i) / 2;
       if (uses) tc::mbar_drain(&s_full[i], (uses - 1) & 1, tc::kWaitLimitNs);
     }
 }
