@@ -94,9 +94,14 @@ template <> struct Elem<float> {
   static __device__ float put(float v) { return v; }
 };
 
-template <typename T> union Vec {
-  uint4 u;
-  T e[16 / sizeof(T)];
+template <int BYTES> struct Word;
+template <> struct Word<16> { using type = uint4; };
+template <> struct Word<8> { using type = uint2; };
+template <> struct Word<4> { using type = uint32_t; };
+template <> struct Word<2> { using type = uint16_t; };
+template <typename T, int V> union Vec {
+  typename Word<V * sizeof(T)>::type u;
+  T e[V];
 };
 
 struct RopeGeom {
@@ -105,13 +110,15 @@ struct RopeGeom {
   int lo;            // first element an item covers (the rotary part's start in place, else 0)
 };
 
-// A thread owns one 16-byte vector position of a head (with its partner half a rotary part
-// further on in the half layout) and takes R consecutive (token, head) rows, so that the
+// A thread owns one vector position of a head, V elements (with its partner half a rotary part
+// further on in the half layout), and takes R consecutive (token, head) rows, so that the
 // sines of its pairs are computed once per token and the R loads are in flight together.
-template <typename T, bool HALF, int R>
+// V elements are the widest power of two, up to 16 bytes, that divides every address, stride and
+// part of a head.
+template <typename T, bool HALF, int V, int R>
 __global__ void __launch_bounds__(256)
 rope_vec_kernel(RopeArgs a, RopeGeom g) {
-  constexpr int V = 16 / sizeof(T);
+  using W = typename Word<V * sizeof(T)>::type;
   constexpr int P = HALF ? V : V / 2;  // pairs per item
   pdl_launch_dependents();
   pdl_wait();
@@ -131,13 +138,13 @@ rope_vec_kernel(RopeArgs a, RopeGeom g) {
   int t = static_cast<int>(static_cast<uint32_t>(r0) / static_cast<uint32_t>(a.h));
   int hh = static_cast<int>(static_cast<uint32_t>(r0) - static_cast<uint32_t>(t) * static_cast<uint32_t>(a.h));
   const int t0 = t, h0 = hh;
-  Vec<T> v[R], w[R];
+  Vec<T, V> v[R], w[R];
 #pragma unroll
   for (int k = 0; k < R; ++k) {
     if (r0 + k < rows) {
       const T* src = xb + t * a.x_stride_t + hh * a.x_stride_h;
-      v[k].u = *reinterpret_cast<const uint4*>(src);
-      if (HALF && turn) w[k].u = *reinterpret_cast<const uint4*>(src + half);
+      v[k].u = *reinterpret_cast<const W*>(src);
+      if (HALF && turn) w[k].u = *reinterpret_cast<const W*>(src + half);
     }
     if (++hh == a.h) { hh = 0; ++t; }
   }
@@ -174,52 +181,83 @@ rope_vec_kernel(RopeArgs a, RopeGeom g) {
           v[k].e[2 * i + 1] = y1;
         }
       }
-      if (HALF) *reinterpret_cast<uint4*>(dst + half) = w[k].u;
+      if (HALF) *reinterpret_cast<W*>(dst + half) = w[k].u;
     }
-    *reinterpret_cast<uint4*>(dst) = v[k].u;
+    *reinterpret_cast<W*>(dst) = v[k].u;
     if (++hh == a.h) { hh = 0; ++t; }
   }
 }
 
-// Any alignment, stride and size: a work item is one pair or, out of place, one element
-// beside the rotary part.
-template <typename T>
+// Pairs of neighbours that no vector boundary holds (an odd offset, stride or head): a work item
+// is one pair or, out of place, one element beside the rotary part; R rows a thread as above.
+template <typename T, int R>
 __global__ void __launch_bounds__(256)
-rope_pair_kernel(RopeArgs a, RopeGeom g, int half_layout) {
+rope_pair_kernel(RopeArgs a, RopeGeom g) {
   pdl_launch_dependents();
   pdl_wait();
   const int grp = threadIdx.x / g.slots_block;
   const int slot = blockIdx.y * g.slots_block + threadIdx.x % g.slots_block;
   if (grp >= static_cast<int>(blockDim.x) / g.slots_block || slot >= g.slots) return;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * (blockDim.x / g.slots_block) + grp;
-  if (r >= static_cast<int64_t>(a.n) * a.h) return;
-  const int t = static_cast<int>(static_cast<uint32_t>(r) / static_cast<uint32_t>(a.h));
-  const int hh = static_cast<int>(r - static_cast<int64_t>(t) * a.h);
-  const T* src = static_cast<const T*>(a.x) + t * a.x_stride_t + hh * a.x_stride_h;
-  T* dst = static_cast<T*>(a.out) + t * a.out_stride_t + hh * a.out_stride_h;
+  const int64_t rows = static_cast<int64_t>(a.n) * a.h;
+  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x / g.slots_block) + grp) * R;
+  if (r0 >= rows) return;
   const int half = a.rot >> 1;
-  if (slot < half) {
-    const int i0 = a.offset + (half_layout ? slot : 2 * slot), i1 = half_layout ? i0 + half : i0 + 1;
-    float2 cs = rounded(phase_cs(a.pos[t], a.turns[slot], a.amplitude));
-    if (a.transpose) cs.y = -cs.y;
-    const float p = Elem<T>::get(src[i0]), q = Elem<T>::get(src[i1]);
-    dst[i0] = Elem<T>::put(p * cs.x - q * cs.y);
-    dst[i1] = Elem<T>::put(p * cs.y + q * cs.x);
-  } else {
-    const int c = slot - half;
-    const int e = c < a.offset ? c : c + a.rot;
-    dst[e] = src[e];
+  const bool turn = slot < half;
+  const int c = slot - half;
+  const int e0 = turn ? a.offset + 2 * slot : c < a.offset ? c : c + a.rot;
+  int t = static_cast<int>(static_cast<uint32_t>(r0) / static_cast<uint32_t>(a.h));
+  int hh = static_cast<int>(static_cast<uint32_t>(r0) - static_cast<uint32_t>(t) * static_cast<uint32_t>(a.h));
+  const int t0 = t, h0 = hh;
+  T v[R], w[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (r0 + k < rows) {
+      const T* src = static_cast<const T*>(a.x) + t * a.x_stride_t + hh * a.x_stride_h + e0;
+      v[k] = src[0];
+      if (turn) w[k] = src[1];
+    }
+    if (++hh == a.h) { hh = 0; ++t; }
   }
+  float2 cs = make_float2(1.f, 0.f);
+  int have = -1;
+  t = t0;
+  hh = h0;
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (r0 + k >= rows) break;
+    T* dst = static_cast<T*>(a.out) + t * a.out_stride_t + hh * a.out_stride_h + e0;
+    if (turn) {
+      if (t != have) {
+        cs = rounded(phase_cs(a.pos[t], a.turns[slot], a.amplitude));
+        if (a.transpose) cs.y = -cs.y;
+        have = t;
+      }
+      const float p = Elem<T>::get(v[k]), q = Elem<T>::get(w[k]);
+      dst[0] = Elem<T>::put(p * cs.x - q * cs.y);
+      dst[1] = Elem<T>::put(p * cs.y + q * cs.x);
+    } else {
+      dst[0] = v[k];
+    }
+    if (++hh == a.h) { hh = 0; ++t; }
+  }
+}
+
+template <typename T, bool HALF, int V>
+cudaError_t launch_rope_v(const RopeArgs& a, const RopeGeom& g, dim3 grid, dim3 block, int R, cudaStream_t s) {
+  return R == 4 ? launch_pdl(rope_vec_kernel<T, HALF, V, 4>, grid, block, 0, s, 1, a, g)
+                : launch_pdl(rope_vec_kernel<T, HALF, V, 1>, grid, block, 0, s, 1, a, g);
 }
 
 template <typename T>
 cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
-  constexpr int V = 16 / sizeof(T);
+  constexpr int kMost = 16 / sizeof(T);
   const bool in_place = a.x == a.out, half = a.layout == DSA_ROPE_HALF;
-  auto whole = [](int64_t v) { return v % V == 0; };
-  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
-                   whole(a.x_stride_t) && whole(a.x_stride_h) && whole(a.out_stride_t) && whole(a.out_stride_h) &&
-                   whole(a.offset) && whole(half ? a.rot / 2 : a.rot) && (in_place || whole(a.d));
+  // the widest vector that divides everything, in elements
+  const uint64_t all = (reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out)) / sizeof(T) |
+                       static_cast<uint64_t>(a.x_stride_t | a.x_stride_h | a.out_stride_t | a.out_stride_h | a.offset |
+                                             (half ? a.rot / 2 : a.rot) | (in_place ? 0 : a.d)) | kMost;
+  const int V = static_cast<int>(all & (~all + 1));
+  const bool vec = half || V >= 2;
   const int64_t rows = static_cast<int64_t>(a.n) * a.h;
   RopeGeom g;
   if (vec) {
@@ -233,15 +271,18 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
   const int groups = 256 / g.slots_block;
   const int threads = (groups * g.slots_block + 31) / 32 * 32;
   // four rows a thread once one row each would fill every SM four times over
-  const int R = vec && rows * g.slots >= 4ll * 152 * 2048 ? 4 : 1;
+  const int R = rows * g.slots >= 4ll * 152 * 2048 ? 4 : 1;
   const dim3 grid(static_cast<unsigned>((rows + static_cast<int64_t>(groups) * R - 1) / (static_cast<int64_t>(groups) * R)),
                   static_cast<unsigned>((g.slots + g.slots_block - 1) / g.slots_block));
-  if (!vec) return launch_pdl(rope_pair_kernel<T>, grid, dim3(threads), 0, s, 1, a, g, half ? 1 : 0);
-  if (half)
-    return R == 4 ? launch_pdl(rope_vec_kernel<T, true, 4>, grid, dim3(threads), 0, s, 1, a, g)
-                  : launch_pdl(rope_vec_kernel<T, true, 1>, grid, dim3(threads), 0, s, 1, a, g);
-  return R == 4 ? launch_pdl(rope_vec_kernel<T, false, 4>, grid, dim3(threads), 0, s, 1, a, g)
-                : launch_pdl(rope_vec_kernel<T, false, 1>, grid, dim3(threads), 0, s, 1, a, g);
+  if (!vec)
+    return R == 4 ? launch_pdl(rope_pair_kernel<T, 4>, grid, dim3(threads), 0, s, 1, a, g)
+                  : launch_pdl(rope_pair_kernel<T, 1>, grid, dim3(threads), 0, s, 1, a, g);
+  if constexpr (kMost == 8) {
+    if (V == 8) return half ? launch_rope_v<T, true, 8>(a, g, grid, threads, R, s) : launch_rope_v<T, false, 8>(a, g, grid, threads, R, s);
+  }
+  if (V == 4) return half ? launch_rope_v<T, true, 4>(a, g, grid, threads, R, s) : launch_rope_v<T, false, 4>(a, g, grid, threads, R, s);
+  if (V == 2) return half ? launch_rope_v<T, true, 2>(a, g, grid, threads, R, s) : launch_rope_v<T, false, 2>(a, g, grid, threads, R, s);
+  return launch_rope_v<T, true, 1>(a, g, grid, threads, R, s);
 }
 
 // ---- the cache writers with the rotation on the way ---------------------------------
