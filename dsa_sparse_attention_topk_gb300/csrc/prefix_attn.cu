@@ -7,7 +7,8 @@
 //     l_p = sm_scale * q[t, h] . kv[p],  o[t, h] = sum_p softmax(l)_p kv[p][0:512].
 // The work is 2 (576 + 512) flop per (row, head, position) against 596 bytes per position:
 // with 128 heads or more per position (rows of several sequences, for the prefix) it is
-// bound by the tensor cores.
+// bound by the tensor cores; with up to 32 heads a path of its own (prefix_few.cu) may take the
+// tails, or everything, straight from the cache: make_plan chooses.
 //
 // Three kernels.
 //   expand   dequantises the prefix once for all rows, and each tail once, into fp16 rows in
@@ -26,8 +27,8 @@
 // The pair.  The output accumulator of 128 rows x 512 columns would fill tensor memory, so
 // each CTA of the pair holds one half of the value columns.  Computing the logits in both
 // would cost half as much again; instead CTA c computes logits and weights of the tiles
-// j = c (mod 2) and stores the weights (fp16, 16 KB) into its peer's shared memory as well as
-// its own; both then run P V over every tile, each on its half, in the
+// j = c (mod 2), stores the weights (fp16, 16 KB) in its own shared memory and copies them to its
+// peer's (one bulk copy a tile); both then run P V over every tile, each on its half, in the
 // order own 0, peer 0, own 1, peer 1 ...
 //
 // The softmax reference.  With e the exponent of its tile, a position's weight is stored as
@@ -48,11 +49,14 @@
 //
 // Per CTA (13 warps): 0 loads the tiles for Q K^T, 3 the others, 1 issues Q K^T, 2 issues P V,
 // 4-11 turn logits into weights (a row's 64 positions in two threads), 12 copies the weights.
-// Descriptors and
-// tensor-memory addresses are constants of the unrolled issue loops.
+// Descriptors and tensor-memory addresses are constants of the unrolled issue loops.
 // Tensor memory (512 columns): O in 0..255, the logits in 256..319, the query's dims 0..383
 // as fp16 pairs in 320..511; shared memory as in Layout below.
 // The query is scaled to fp16 by a power of two per row (exact: bf16 has 8 bits).
+//
+// Measured (128 heads): 32 rows behind 32K positions 201 us, of it 8 us expand, some 11 us before an
+// item's first and behind its last product, and 2400 cycles a step of two tiles against
+// the products' 2270; 512 causal rows behind 16K 1.55 ms, 78% of the cuBLAS bf16 rate.
 
 #include <algorithm>
 #include <cuda.h>

@@ -24,15 +24,18 @@ __device__ __forceinline__ KTok load_k_token(const __nv_bfloat16* __restrict__ k
   const int lane = threadIdx.x & 31;
   return KTok{*reinterpret_cast<const uint2*>(k + t * kIdxDim + 4 * lane), slots[t]};
 }
-// Store one token's key from its fp32 values (this lane's dims 4 lane ..).
-__device__ __forceinline__ void store_k_values(const float (&x)[4], int64_t slot, uint8_t* __restrict__ cache,
-                                               int64_t num_slots, unsigned* status) {
+__device__ __forceinline__ void store_k_token(const KTok& in, uint8_t* __restrict__ cache, int64_t num_slots,
+                                              unsigned* status) {
   const int lane = threadIdx.x & 31;
+  const int64_t slot = in.slot;
   if (slot < 0) return;
   if (slot >= num_slots) {
     if (lane == 0) flag(status, DSA_STATUS_BAD_PAGE);
     return;
   }
+  const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&in.raw.x);
+  const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&in.raw.y);
+  float x[4] = {__low2float(a), __high2float(a), __low2float(b), __high2float(b)};
   float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -48,29 +51,16 @@ __device__ __forceinline__ void store_k_values(const float (&x)[4], int64_t slot
   *reinterpret_cast<uint32_t*>(page + row * kIdxDim + 4 * lane) = codes;
   if ((lane & 7) == 0) page[kKScaleOff + row * 4 + (lane >> 3)] = static_cast<uint8_t>(e + 127);
 }
-// two packed bf16 values -> fp32 (exact)
-__device__ __forceinline__ float2 bf16x2_to_f32(uint32_t v) {
-  const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&v);
-  return make_float2(__low2float(b), __high2float(b));
-}
-__device__ __forceinline__ void store_k_token(const KTok& in, uint8_t* __restrict__ cache, int64_t num_slots,
-                                              unsigned* status) {
-  const float2 a = bf16x2_to_f32(in.raw.x), b = bf16x2_to_f32(in.raw.y);
-  const float x[4] = {a.x, a.y, b.x, b.y};
-  store_k_values(x, in.slot, cache, num_slots, status);
-}
 
 // |x| / s rounded to the nearest float and then nudged to "round to odd" when inexact:
 // converting the result to E4M3 with round-to-nearest-even then gives the correctly
 // rounded E4M3 value of the exact quotient (Boldo & Melquiond, "Emulation of FMA and
 // correctly rounded sums: proved algorithms using rounding to odd", 2008: rounding to
 // odd with p+2 or more bits followed by round-to-nearest is a correct rounding).
-// A value known as x + low (low at most half an ulp of x) gives the code of that sum.
-__device__ __forceinline__ float quotient_round_to_odd(float x, float s, float low = 0.f) {
+__device__ __forceinline__ float quotient_round_to_odd(float x, float s) {
   const float a = fabsf(x);
   const float q = __fdiv_rn(a, s);
-  float r = __fmaf_rn(-q, s, a);  // exact remainder a - q*s
-  if (low != 0.f) r += x < 0.f ? -low : low;
+  const float r = __fmaf_rn(-q, s, a);  // exact remainder a - q*s
   uint32_t qb = __float_as_uint(q);
   if (r != 0.f && (qb & 1u) == 0u) qb += (r > 0.f) ? 1u : 0xFFFFFFFFu;
   return copysignf(__uint_as_float(qb), x);

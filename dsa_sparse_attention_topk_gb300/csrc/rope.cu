@@ -370,6 +370,20 @@ __device__ __forceinline__ void turn_kv(float x0, float x1, const CosSin& cs, bo
   }
 }
 
+// two packed bf16 values -> fp32 (exact)
+__device__ __forceinline__ float2 bf16x2_to_f32(uint32_t v) {
+  const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&v);
+  return make_float2(__low2float(b), __high2float(b));
+}
+// |x| / s rounded to odd as quotient_round_to_odd does, for a value known as x + low (low at
+// most half an ulp of x): the remainder's sign decides, and low has its share in it.
+__device__ __forceinline__ float sum_quotient_round_to_odd(float x, float low, float s) {
+  const float a = fabsf(x), q = __fdiv_rn(a, s);
+  const float r = __fmaf_rn(-q, s, a) + (x < 0.f ? -low : low);
+  uint32_t qb = __float_as_uint(q);
+  if (r != 0.f && (qb & 1u) == 0u) qb += (r > 0.f) ? 1u : 0xFFFFFFFFu;
+  return copysignf(__uint_as_float(qb), x);
+}
 // largest of the warp's non-negative floats (a NaN is ignored, as fmaxf does)
 __device__ __forceinline__ float warp_amax(float v) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v, 0.f))));
@@ -423,15 +437,17 @@ __device__ __forceinline__ void turn_store_k(uint2 raw, const CosSin& cs, const 
       err[j] = 0.f;
     }
   }
-  float amax = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
-  float emax = fmaxf(fmaxf(err[0], err[1]), fmaxf(err[2], err[3]));
+  // (the maxima of a group of 32 dims, eight lanes)
+  auto group_max = [](float v) {
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    emax = fmaxf(emax, __shfl_xor_sync(0xffffffffu, emax, o));
-  }
-  const int e = mx_shared_exp(amax);
-  const float inv = exp2i(-e);
+    for (int o = 1; o < 8; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  };
+  auto top4 = [](const float (&v)[4]) { return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))); };
+  float amax = group_max(top4(y));
+  const float emax = group_max(top4(err));
+  int e = mx_shared_exp(amax);
+  float inv = exp2i(-e);  // exact power of two: y * inv is exact
   uint32_t lo[2], hi[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -442,8 +458,11 @@ __device__ __forceinline__ void turn_store_k(uint2 raw, const CosSin& cs, const 
                     mx_shared_exp(amax + emax) == e && amax > 0.f;
   if (__any_sync(0xffffffffu, !same && emax > 0.f)) {  // (a group without rotary dims is exact as it is)
     turn_k(x, cs, a.k_offset, a.k_layout == DSA_ROPE_HALF);
-    store_k_values(x, slot, a.k_cache, a.num_slots, a.status);
-    return;
+    amax = group_max(top4(x));
+    e = mx_shared_exp(amax);
+    inv = exp2i(-e);
+    lo[0] = f32x2_to_e4m3x2(x[0] * inv, x[1] * inv);
+    lo[1] = f32x2_to_e4m3x2(x[2] * inv, x[3] * inv);
   }
   uint8_t* page = a.k_cache + (slot / kPage) * kKPageBytes;
   const int row = static_cast<int>(slot % kPage);
@@ -544,8 +563,8 @@ __device__ __forceinline__ void turn_store_kv(const uint2 (&raws)[4], uint32_t r
       rs = __fdiv_rn(top, 448.0f);
       const float rest = fmaf(-448.0f, rs, top) + low;
       if (fabsf(rest) < top) rs += rest * (1.0f / 448.0f);  // (not where either is 0, infinite or NaN)
-      codes = rs > 0.f ? f32x2_to_e4m3x2(quotient_round_to_odd(t0.hi, rs, t0.lo),
-                                         quotient_round_to_odd(t1.hi, rs, t1.lo)) : 0;
+      codes = rs > 0.f ? f32x2_to_e4m3x2(sum_quotient_round_to_odd(t0.hi, t0.lo, rs),
+                                         sum_quotient_round_to_odd(t1.hi, t1.lo, rs)) : 0;
       if (lane == 4) s = rs;
     }
     *reinterpret_cast<uint16_t*>(rec + 512 + 2 * lane) = codes;

@@ -334,6 +334,8 @@ int dsa_sparse_attn_noalloc(const void* q_bf16, int32_t n_q, int32_t h_s, const 
  * A row that sees nothing gets o = 0 and lse = -inf.  For the tensor cores the query (by a
  * power of two per row), the dequantised values (by one per 64 positions) and the softmax
  * weights are held in fp16, 11 bits for whatever lies within 2^-29 of the largest; sums in fp32.
+ * With up to 32 heads, where no more memory is read for it, the codes are used as they are and
+ * their scales stay in fp32: there the weights times the scales are held in fp16.
  *   q_bf16        [n_q][h_s][576] bfloat16, 16-byte aligned; h_s 1..128.
  *   kv_cache      the FP8 latent cache (layout above), num_pages pages, 16-byte aligned.
  *   prefix_pages  [ceil(prefix_len / 64)] int32 physical pages of the shared positions (the
@@ -350,9 +352,9 @@ int dsa_sparse_attn_noalloc(const void* q_bf16, int32_t n_q, int32_t h_s, const 
  *   out_bf16      [n_q][h_s][512] bfloat16, 16-byte aligned.
  *   out_lse       nullable [n_q][h_s] fp32.
  *   workspace     device scratch of at least dsa_prefix_attn_workspace_size bytes for the same
- *                 sizes, 256-byte aligned: the expanded rows (1152 bytes a position of the
- *                 prefix and of n_seq tails of max_ctx - prefix_len) and the splits' partial
- *                 results.  Nothing in it outlives the call.
+ *                 sizes and device, 256-byte aligned: the expanded rows (1152 bytes a position
+ *                 of the prefix and of n_seq tails of max_ctx - prefix_len; less with up to 32
+ *                 heads) and the splits' partial results.  Nothing in it outlives the call.
  * A position whose page is out of range is not seen and flags DSA_STATUS_BAD_PAGE; a row whose
  * sequence or length is out of range sees nothing and flags DSA_STATUS_BAD_SEQ or _BAD_LEN.
  * A cached position with NaN or infinite values makes the rows that see it NaN, and no others.
