@@ -216,6 +216,41 @@ def test_every_code_and_scale(dsa, h):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("prefix,h", [(0, 16), (129, 8), (0, 32)])
+def test_many_ragged_rows_of_few_heads(dsa, prefix, h):
+    # blocks take equal shares of all rows' positions: rows are cut, several meet in one block, and
+    # runs of rows that see nothing lie between them
+    g = torch.Generator().manual_seed(h + prefix)
+    lens = torch.randint(0, 900, (50,), generator=g).tolist()
+    rows = [(b, L - 1 - k) for b, L in enumerate(lens) for k in range(3)]
+    for i in list(range(20, 60)) + list(range(0, 150, 4)) + [149]:
+        rows[i] = (rows[i][0], -1)
+    b = Batch(dsa, lens, prefix, h, rows=rows, seed=8, max_ctx=1000)
+    out, lse = b.call(dsa)
+    assert dsa.device_status() == 0
+    b.check(out, lse)
+    again, again_lse = b.call(dsa)
+    assert torch.equal(out, again) and torch.equal(lse, again_lse)
+    b.q_pos[:] = -1
+    out, lse = b.call(dsa)
+    assert not out.any() and torch.isneginf(lse).all()
+
+
+@pytest.mark.gpu
+def test_value_scales_apart_from_the_logits(dsa):
+    # the logits come from the last 64 dims alone; the value tiles' scales span 2^120 and do not follow them
+    b = Batch(dsa, [700, 650], 80, 16, seed=13)
+    b.q[..., :512] = 0
+    g = torch.Generator().manual_seed(14)
+    rec = b.cache.view(-1, 608)
+    scale = torch.exp2(torch.randint(-60, 60, (rec.shape[0], 4), generator=g).float())
+    rec[:, 576:592] = scale.view(torch.uint8).cuda()
+    out, lse = b.call(dsa)
+    assert dsa.device_status() == 0
+    b.check(out, lse)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("h", [24, 40])
 def test_rows_in_any_number_and_order(dsa, h):
     # two-token steps, a chunk of one sequence, rows inside the prefix, rows that see nothing
