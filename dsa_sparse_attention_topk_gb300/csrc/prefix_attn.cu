@@ -137,8 +137,8 @@ struct PairCtl {
   float sent[kRows];                           // by the peer: the first references (to parity 1), at the end the sums
   float part[2][2][kRows];                     // tile maxima of a row's two threads, by tile parity
 };
-template <int G> constexpr uint32_t kSmemBytes = Layout<G>::ctl + 3072;
-static_assert(sizeof(PairCtl) <= 3072 && kPieces == kLoose && kSmemBytes<1> <= 232448 && kSmemBytes<2> <= 232448, "shared memory");
+template <int G> constexpr uint32_t kSmemBytes = Layout<G>::ctl + 3 * 1024;
+static_assert(sizeof(PairCtl) <= 3 * 1024 && kPieces == kLoose && kSmemBytes<1> <= 232448 && kSmemBytes<2> <= 232448, "shared memory");
 // the query's dims 0..383 and the output rows are staged where the tiles go
 constexpr int kStagePitch = kHalfV * 2 + 16;
 static_assert(4 * kQBlock == 2 * Layout<1>::kVBytes && kQBlock <= kLoose * kBlock && 3 * kQBlock == 3 * Layout<2>::kVBytes &&

@@ -28,11 +28,11 @@
 // equal share, which may end one row and begin the next; a row's parts meet in the merge.
 //
 // Measured (16 heads, two blocks an SM): 3.6 us a step of 64 positions and block, 5 us before and
-// behind a block's steps; 128 rows of 1..2048 own positions 42 us, 2.1 TB/s.  A step is bound by
+// behind a block's steps; 128 rows of 1..2048 own positions 42 us, 1.8 TB/s.  A step is bound by
 // the latency of its three dependent stages: half of all issue slots are filled, the
 // tensor pipe is busy for a quarter of the time; without the logits' products 128 rows of
-// 4096 positions take 66 instead of 80 us, without the output's 70, without the weights 73, and the
-// copies alone 49.
+// 2048..4096 positions take 66 instead of 80 us, without the output's 70, without the weights 73,
+// and the copies alone 49.
 
 #include "prefix_common.cuh"
 #include "tc_utils.cuh"
