@@ -148,6 +148,7 @@ static_assert(kRows * kStagePitch <= Layout<1>::ctl - Layout<1>::v && kRows * kS
               "output staging");
 
 // A split costs every row its partial output, once written and once read, at some 5 TB/s.
+constexpr int kShortPrefix = 1024;  // (expanded for every sequence, it should not fill the workspace)
 constexpr double kJoinUs = 2048.0 / 5.0e6, kFewUs16 = 1.5, kFewUs16Pair = 3.6, kFewUs32 = 2.2;
 
 // What expand writes per tile.
@@ -159,6 +160,7 @@ struct alignas(32) TileInfo {
 
 struct PrefixPlan {
   int tiles_p, tiles_t;      // tiles of the prefix, and of the longest possible tail
+  int tail_lo, tail_sure;    // the tails' first position (0: a short prefix goes with them), tiles all of them have
   int sp, st;                // splits of the prefix and of each tail on the tensor-memory path
   int few_lo, few;           // the path for few heads: first position and most parts of a row (0: not taken)
   int few_blocks;
@@ -200,7 +202,8 @@ double plan_tiles(PrefixPlan& p, int n_q, int n_sm) {
         const double lt = st ? fix + per * ((p.tiles_t + st - 1) / st) : 0.0;
         const int64_t np = static_cast<int64_t>(mt) * sp;
         // the tails are counted half full: their lengths are known to the device alone
-        const double total = (np * lp + static_cast<double>(n_q) * st * (fix + 0.5 * (lt - fix))) / fit;
+        const double full = p.tiles_t ? 0.5 + 0.5 * p.tail_sure / p.tiles_t : 0.0;
+        const double total = (np * lp + static_cast<double>(n_q) * st * (fix + full * (lt - fix))) / fit;
         const double t = std::max({static_cast<double>((np + fit - 1) / fit) * lp, total + 0.5 * lt, lt}) + kJoinUs * n_q * p.h_s * (sp + st);
         if (t < best) {
           best = t;
@@ -213,9 +216,9 @@ double plan_tiles(PrefixPlan& p, int n_q, int n_sm) {
       if (!p.tiles_p) break;
     }
   }
-  // the expansion, at some 5 TB/s (tails half full), and two more launches
-  const double positions = 64.0 * p.tiles_p + 32.0 * p.tiles_t * p.n_seq;
-  return best + positions * (kKvTokBytes + 2 * kLatent) / 5.0e6 + 5.0;
+  // the expansion, at some 5 TB/s, and one or two more launches
+  const double positions = 64.0 * p.tiles_p + 32.0 * (p.tiles_t + p.tail_sure) * p.n_seq;
+  return best + positions * (kKvTokBytes + 2 * kLatent) / 5.0e6 + (p.sp + p.st > 1 ? 5.0 : 2.5);
 }
 
 // All of it on the tensor-memory path, or (up to 32 heads) the tails or everything on the path for
@@ -228,22 +231,35 @@ PrefixPlan make_plan(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, i
   p.h_s = h_s;
   p.tiles_p = (prefix_len + kTile - 1) / kTile;
   p.tiles_t = (max_ctx - prefix_len + kTile - 1) / kTile;
+  p.tail_lo = prefix_len;
   p.mt = static_cast<int>((static_cast<int64_t>(n_q) * h_s + kRows - 1) / kRows);
   double best = plan_tiles(p, n_q, n_sm);
+  // A short prefix may go with every row's tail instead: expanded once a sequence, but no items and
+  // partial results of its own (208 rows of 128 heads, 8 + 486..662 positions: 156 -> 102 us).
+  if (prefix_len > 0 && prefix_len <= kShortPrefix && max_ctx > prefix_len) {
+    PrefixPlan q = p;
+    q.tiles_p = q.sp = q.tail_lo = 0;
+    q.tiles_t = (max_ctx + kTile - 1) / kTile;
+    q.tail_sure = prefix_len / kTile;
+    const double t = plan_tiles(q, n_q, n_sm);
+    if (t < best) {
+      best = t;
+      p = q;
+    }
+  }
   if (h_s <= kFewHeads) {
     const int fit = h_s <= 16 ? 2 * n_sm : n_sm;
     for (int whole = 0; whole < 2; ++whole) {  // the tails, then everything
       const int lo = whole ? 0 : prefix_len;
       if ((!whole && !prefix_len) || lo == max_ctx) continue;
       PrefixPlan q = p;
-      q.sp = q.st = 0;
-      q.tiles_t = 0;
-      if (whole) q.tiles_p = 0;
+      q.sp = q.st = q.tiles_t = q.tail_sure = 0;
+      q.tiles_p = whole ? 0 : (prefix_len + kTile - 1) / kTile;
       const double rest = plan_tiles(q, n_q, n_sm);
       const int steps = (max_ctx - lo + 63) / 64, sure = whole ? prefix_len / 64 : 0;
       const double mean = 0.5 * (steps + sure) * n_q;  // of all rows, tails half full
       const int even = static_cast<int>(std::min<int64_t>(fit, static_cast<int64_t>(steps) * n_q));
-      for (int few = 1; few <= (n_q > kFewCutRows ? 1 : std::min(2 * steps, 64)); few *= 2) {
+      for (int few = 1; few <= (n_q > kFewCutRows ? 1 : std::min(2 * steps, 512)); few *= 2) {
         // a row a block, the longest one last; or even shares
         const int blocks = few == 1 ? n_q : even;
         const double step = h_s > 16 ? kFewUs32 : blocks <= n_sm ? kFewUs16 : kFewUs16Pair, parts = std::min<double>(few, 1.0 + even / n_q);
@@ -284,18 +300,17 @@ expand_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
   const int tile = blockIdx.x;
   const int tid = threadIdx.x;
   int pos0, len;
-  const int32_t* pages;
+  const int32_t* table = nullptr;
   if (tile < pl.tiles_p) {
     pos0 = tile * kTile;
     len = a.prefix_len;
-    pages = a.prefix_pages;
   } else {
     const int b = (tile - pl.tiles_p) / pl.tiles_t;
-    pos0 = a.prefix_len + (tile - pl.tiles_p) % pl.tiles_t * kTile;
+    pos0 = pl.tail_lo + (tile - pl.tiles_p) % pl.tiles_t * kTile;
     len = a.seq_lens[b];
     if (len < 0 || len > a.max_ctx) len = 0;
     if (pos0 >= len) return;
-    pages = a.page_table + static_cast<int64_t>(b) * a.max_pages;
+    table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
   }
   if (tid < 4) s_word[tid] = 0;
   if (tid == 4) s_scale = 0;
@@ -311,7 +326,7 @@ expand_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
     code[i] = make_uint4(0u, 0u, 0u, 0u);
     scale[i] = 0.f;
     if (p >= len) continue;
-    const int pg = pages[p / kPage];
+    const int pg = (p < a.prefix_len ? a.prefix_pages : table)[p / kPage];
     if (pg < 0 || pg >= a.num_pages) {
       if (c == 0) flag(a.status, DSA_STATUS_BAD_PAGE);
       continue;
@@ -647,10 +662,10 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     n_rows = g == 0 ? a.h_s : 0;
     part = pl.st;
     const int lim = prefix_row_limit(a, t, tid == 0 && rank == 0 && split == 0);
-    tiles = lim > a.prefix_len ? (lim - a.prefix_len + kTile - 1) / kTile : 0;
+    tiles = lim > pl.tail_lo ? (lim - pl.tail_lo + kTile - 1) / kTile : 0;
     // (a row that sees anything has a sequence in range)
     tile_base = tiles ? pl.tiles_p + a.q_seq[t] * pl.tiles_t : 0;
-    first_pos = a.prefix_len;
+    first_pos = pl.tail_lo;
   }
   const int tile0 = static_cast<int>(static_cast<int64_t>(split) * tiles / part);
   const int nt = static_cast<int>(static_cast<int64_t>(split + 1) * tiles / part) - tile0;
@@ -1174,19 +1189,33 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 
 // ---- merge ---------------------------------------------------------------------------------
 // Split s holds o_s = O_s / l_s (fp16 times a power of two) with reference m_s; with
-// M = max m_s and w_s = 2^(m_s - M) l_s the output is sum_s w_s o_s / sum_s w_s.  64 threads a row, 8 columns each, four
-// rows a block, four splits' loads in flight.
-constexpr int kMergeRows = 4, kMergeBatch = 4;
-__global__ void __launch_bounds__(64 * kMergeRows)
+// M = max m_s and w_s = 2^(m_s - M) l_s the output is sum_s w_s o_s / sum_s w_s.  64 threads a row, 8
+// columns each, four splits' loads in flight; for few rows of many splits four such groups a row.
+constexpr int kMergeBatch = 4;
+struct MergeSum {
+  float top = -INFINITY, sum = 0.f, acc[8] = {};
+  __device__ __forceinline__ void raise(float to) {
+    if (to == top) return;
+    const float f = top == -INFINITY ? 0.f : exp2f(top - to);
+    sum *= f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] *= f;
+    top = to;
+  }
+};
+template <int GROUPS>
+__global__ void __launch_bounds__(256)
 prefix_merge_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
+  constexpr int kRowsBlock = 4 / GROUPS;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x >> 6);
-  if (row >= static_cast<int64_t>(a.n_q) * a.h_s) return;
-  const int d = 8 * static_cast<int>(threadIdx.x & 63);
+  const int grp = threadIdx.x >> 6 & (GROUPS - 1), lane64 = threadIdx.x & 63;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsBlock + (threadIdx.x >> 6) / GROUPS;
+  if (row >= static_cast<int64_t>(a.n_q) * a.h_s) return;  // (whole blocks, where groups meet)
+  const int d = 8 * lane64;
   const int ns = pl.sp + pl.st + (pl.few ? min(__ldcg(ws.used + row / a.h_s), pl.few) : 0);
-  float M = -INFINITY, sum = 0.f, acc[8] = {};
-  for (int s0 = 0; s0 < ns; s0 += kMergeBatch) {
+  MergeSum m;
+  for (int s0 = kMergeBatch * grp; s0 < ns; s0 += kMergeBatch * GROUPS) {
     float4 ml[kMergeBatch];
     uint4 v[kMergeBatch];
 #pragma unroll
@@ -1198,37 +1227,46 @@ prefix_merge_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
         v[i] = __ldcg(reinterpret_cast<const uint4*>(ws.o + (row * pl.ns + s0 + i) * kVDim + d));
       }
     }
-    float top = M;
+    float top = m.top;
 #pragma unroll
     for (int i = 0; i < kMergeBatch; ++i) top = fmaxf(top, ml[i].x);
-    if (top != M) {
-      const float f = M == -INFINITY ? 0.f : exp2f(M - top);
-      sum *= f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] *= f;
-      M = top;
-    }
+    m.raise(top);
 #pragma unroll
     for (int i = 0; i < kMergeBatch; ++i) {
       if (ml[i].x == -INFINITY) continue;  // an empty split: its output was never written
-      const float wl = exp2f(ml[i].x - M) * ml[i].y;
-      sum += wl;
+      const float wl = exp2f(ml[i].x - m.top) * ml[i].y;
+      m.sum += wl;
       const float f = wl * exp2f(ml[i].z);
       const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 h = unpack_half2(u[k]);
-        acc[2 * k] = fmaf(f, h.x, acc[2 * k]);
-        acc[2 * k + 1] = fmaf(f, h.y, acc[2 * k + 1]);
+        m.acc[2 * k] = fmaf(f, h.x, m.acc[2 * k]);
+        m.acc[2 * k + 1] = fmaf(f, h.y, m.acc[2 * k + 1]);
       }
     }
   }
-  const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+  if constexpr (GROUPS > 1) {
+    __shared__ MergeSum s_part[GROUPS - 1][64];
+    if (grp > 0) s_part[grp - 1][lane64] = m;
+    __syncthreads();
+    if (grp > 0) return;
+    for (int i = 0; i < GROUPS - 1; ++i) {
+      const MergeSum& other = s_part[i][lane64];
+      if (other.top == -INFINITY) continue;
+      m.raise(fmaxf(m.top, other.top));
+      const float f = exp2f(other.top - m.top);
+      m.sum = fmaf(f, other.sum, m.sum);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m.acc[k] = fmaf(f, other.acc[k], m.acc[k]);
+    }
+  }
+  const float inv = m.sum > 0.f || m.sum != m.sum ? 1.f / m.sum : 0.f;
   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * kVDim + d) =
-      make_uint4(pack_bf162(acc[0] * inv, acc[1] * inv), pack_bf162(acc[2] * inv, acc[3] * inv),
-                 pack_bf162(acc[4] * inv, acc[5] * inv), pack_bf162(acc[6] * inv, acc[7] * inv));
+      make_uint4(pack_bf162(m.acc[0] * inv, m.acc[1] * inv), pack_bf162(m.acc[2] * inv, m.acc[3] * inv),
+                 pack_bf162(m.acc[4] * inv, m.acc[5] * inv), pack_bf162(m.acc[6] * inv, m.acc[7] * inv));
   if (a.out_lse && d == 0)
-    a.out_lse[row] = natural_lse(M, sum);
+    a.out_lse[row] = natural_lse(m.top, m.sum);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1312,8 +1350,10 @@ cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char**
     if (e != cudaSuccess) return e;
   }
   if (pl.ns == 1) return cudaSuccess;
-  return launch_pdl(prefix_merge_kernel, dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows)),
-                    dim3(64 * kMergeRows), 0, s, 1, a, pl, ws);
+  // (one row of 16 heads, 60000 positions: 52 us with 64 parts at most, 32 with 256 and four groups a row)
+  if (pl.ns >= 16 && rows <= 2048)
+    return launch_pdl(prefix_merge_kernel<4>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, 1, a, pl, ws);
+  return launch_pdl(prefix_merge_kernel<1>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, s, 1, a, pl, ws);
 }
 
 }  // namespace dsa
