@@ -110,6 +110,41 @@ struct RopeGeom {
   int lo;            // first element an item covers (the rotary part's start in place, else 0)
 };
 
+// The sines of a block's tokens, each computed once, by all threads: the heads of a token share
+// them, and few lanes of a warp hold rotary dims.  It pays with one row a thread (1842 x 16 heads of
+// 192 bf16: 17 -> 8.3 us) and with full vectors in the half layout, as many pairs a thread as rows
+// (4096 x 64 x 128 bf16, all rotary: 29 -> 23 us); elsewhere several rows share a thread's sines,
+// and waiting for the table costs more (4096 x 128 x 576 interleaved: 174 -> 181 us; 4096 x 63 x 192,
+// 8-byte vectors: 76 -> 93).  Blocks whose tokens have more than kTableSize pairs, two a thread (few
+// heads), leave them to the threads that turn them (65536 x 1 x 64: 8.4 us, by a table 14.1).
+constexpr int kTableSize = 512;
+struct Table {
+  float2* cs;
+  int first, half;   // token of its first row; pairs a token
+  bool there;
+  __device__ __forceinline__ float2 at(int t, int i) const { return cs[(t - first) * half + i]; }
+};
+__device__ __forceinline__ float2 pair_cs(const RopeArgs& a, int t, int i) {
+  float2 cs = rounded(phase_cs(a.pos[t], a.turns[i], a.amplitude));
+  if (a.transpose) cs.y = -cs.y;
+  return cs;
+}
+// the table of the block's `rows` rows from row r0 on
+__device__ __forceinline__ Table fill_table(const RopeArgs& a, float2* cs, int64_t r0, int rows) {
+  const int64_t end = min(r0 + rows, static_cast<int64_t>(a.n) * a.h) - 1;
+  Table tab{cs, static_cast<int>(static_cast<uint32_t>(r0) / static_cast<uint32_t>(a.h)), a.rot >> 1, false};
+  const int last = static_cast<int>(static_cast<uint32_t>(end) / static_cast<uint32_t>(a.h));
+  const int64_t size = static_cast<int64_t>(last - tab.first + 1) * tab.half;
+  tab.there = size <= kTableSize;
+  if (tab.there)
+    for (int i = threadIdx.x; i < size; i += blockDim.x) {
+      const int t = i / tab.half;
+      cs[i] = pair_cs(a, tab.first + t, i - t * tab.half);
+    }
+  __syncthreads();
+  return tab;
+}
+
 // A thread owns one vector position of a head, V elements (with its partner half a rotary part
 // further on in the half layout), and takes R consecutive (token, head) rows, so that the
 // sines of its pairs are computed once per token and the R loads are in flight together.
@@ -119,19 +154,20 @@ template <typename T, bool HALF, int V, int R>
 __global__ void __launch_bounds__(256)
 rope_vec_kernel(RopeArgs a, RopeGeom g) {
   using W = typename Word<V * sizeof(T)>::type;
+  constexpr bool TABLE = R == 1 || (HALF && V * sizeof(T) == 16);
   constexpr int P = HALF ? V : V / 2;  // pairs per item
   pdl_launch_dependents();
   pdl_wait();
-  const int grp = threadIdx.x / g.slots_block;
+  const int groups = blockDim.x / g.slots_block, grp = threadIdx.x / g.slots_block;
   const int slot = blockIdx.y * g.slots_block + threadIdx.x % g.slots_block;
-  if (grp >= static_cast<int>(blockDim.x) / g.slots_block || slot >= g.slots) return;
-  const int64_t rows = static_cast<int64_t>(a.n) * a.h;
-  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x / g.slots_block) + grp) * R;
-  if (r0 >= rows) return;
+  const int64_t rows = static_cast<int64_t>(a.n) * a.h, block0 = static_cast<int64_t>(blockIdx.x) * groups * R;
+  const int64_t r0 = block0 + static_cast<int64_t>(grp) * R;
+  const bool active = grp < groups && slot < g.slots && r0 < rows;
+  if (!TABLE && !active) return;
   int e0 = g.lo + slot * V;
   const int half = a.rot >> 1;
   if (HALF && e0 >= a.offset + half) e0 += half;  // the second halves go with the first
-  const bool turn = e0 >= a.offset && e0 < a.offset + (HALF ? half : a.rot);
+  const bool turn = active && e0 >= a.offset && e0 < a.offset + (HALF ? half : a.rot);
   int t = static_cast<int>(static_cast<uint32_t>(r0) / static_cast<uint32_t>(a.h));
   int hh = static_cast<int>(static_cast<uint32_t>(r0) - static_cast<uint32_t>(t) * static_cast<uint32_t>(a.h));
   const int h0 = hh;
@@ -142,7 +178,7 @@ rope_vec_kernel(RopeArgs a, RopeGeom g) {
   Vec<T, V> v[R], w[R];
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    if (r0 + k < rows) {
+    if ((!TABLE || active) && r0 + k < rows) {
       v[k].u = *reinterpret_cast<const W*>(src);
       if (HALF && turn) w[k].u = *reinterpret_cast<const W*>(src + half);
     }
@@ -150,6 +186,12 @@ rope_vec_kernel(RopeArgs a, RopeGeom g) {
     src += last ? src_wrap : a.x_stride_h;
     if (last) hh = 0;
   }
+  Table tab{};
+  if constexpr (TABLE) {
+    __shared__ float2 s_cs[kTableSize];
+    tab = fill_table(a, s_cs, block0, groups * R);
+  }
+  if (!active) return;
   float2 cs[P];
   int have = -1;
   hh = h0;
@@ -159,12 +201,12 @@ rope_vec_kernel(RopeArgs a, RopeGeom g) {
     if (turn) {
       if (t != have) {
         const int f0 = HALF ? e0 - a.offset : (e0 - a.offset) >> 1;
-        const int pos = a.pos[t];
+        if (TABLE && tab.there) {
 #pragma unroll
-        for (int i = 0; i < P; ++i) cs[i] = rounded(phase_cs(pos, a.turns[f0 + i], a.amplitude));
-        if (a.transpose) {
+          for (int i = 0; i < P; ++i) cs[i] = tab.at(t, f0 + i);
+        } else {
 #pragma unroll
-          for (int i = 0; i < P; ++i) cs[i].y = -cs[i].y;
+          for (int i = 0; i < P; ++i) cs[i] = pair_cs(a, t, f0 + i);
         }
         have = t;
       }
@@ -195,14 +237,15 @@ rope_vec_kernel(RopeArgs a, RopeGeom g) {
 template <typename T, int R>
 __global__ void __launch_bounds__(256)
 rope_pair_kernel(RopeArgs a, RopeGeom g) {
+  constexpr bool TABLE = R == 1;
   pdl_launch_dependents();
   pdl_wait();
-  const int grp = threadIdx.x / g.slots_block;
+  const int groups = blockDim.x / g.slots_block, grp = threadIdx.x / g.slots_block;
   const int slot = blockIdx.y * g.slots_block + threadIdx.x % g.slots_block;
-  if (grp >= static_cast<int>(blockDim.x) / g.slots_block || slot >= g.slots) return;
-  const int64_t rows = static_cast<int64_t>(a.n) * a.h;
-  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x / g.slots_block) + grp) * R;
-  if (r0 >= rows) return;
+  const int64_t rows = static_cast<int64_t>(a.n) * a.h, block0 = static_cast<int64_t>(blockIdx.x) * groups * R;
+  const int64_t r0 = block0 + static_cast<int64_t>(grp) * R;
+  const bool active = grp < groups && slot < g.slots && r0 < rows;
+  if (!TABLE && !active) return;
   const int half = a.rot >> 1;
   const bool turn = slot < half;
   const int c = slot - half;
@@ -216,7 +259,7 @@ rope_pair_kernel(RopeArgs a, RopeGeom g) {
   T v[R], w[R];
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    if (r0 + k < rows) {
+    if ((!TABLE || active) && r0 + k < rows) {
       v[k] = src[0];
       if (turn) w[k] = src[1];
     }
@@ -224,6 +267,12 @@ rope_pair_kernel(RopeArgs a, RopeGeom g) {
     src += last ? src_wrap : a.x_stride_h;
     if (last) hh = 0;
   }
+  Table tab{};
+  if constexpr (TABLE) {
+    __shared__ float2 s_cs[kTableSize];
+    tab = fill_table(a, s_cs, block0, groups * R);
+  }
+  if (!active) return;
   float2 cs = make_float2(1.f, 0.f);
   int have = -1;
   hh = h0;
@@ -232,8 +281,7 @@ rope_pair_kernel(RopeArgs a, RopeGeom g) {
     if (r0 + k >= rows) break;
     if (turn) {
       if (t != have) {
-        cs = rounded(phase_cs(a.pos[t], a.turns[slot], a.amplitude));
-        if (a.transpose) cs.y = -cs.y;
+        cs = TABLE && tab.there ? tab.at(t, slot) : pair_cs(a, t, slot);
         have = t;
       }
       const float p = Elem<T>::get(v[k]), q = Elem<T>::get(w[k]);
