@@ -21,7 +21,7 @@
 //            that see it and nothing to the others.
 //   attend   one CTA pair per item: 128 rows of (query row, head) against a run of 64-position
 //            tiles of the prefix (a tile of the flattened rows, shared by all sequences) or of
-//            one query row's tail.
+//            one sequence's tail (as many of its adjacent query rows as fit).
 //   merge    joins a row's splits by their log-sum-exps.
 //
 // The pair.  The output accumulator of 128 rows x 512 columns would fill tensor memory, so
@@ -185,12 +185,14 @@ size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // The tensor-memory path's plan of least estimated time: MMAs of one CTA (128 rows an item, two
 // CTAs) or of CTA pairs (256 rows, four CTAs), and the splits.  An item of n tiles takes about
 // 9 + 1.33 n us with one CTA per parity and 11 + 0.62 n us with pairs, on one of the clusters that
-// fit at once.  Tails, whose rows share no tiles, leave half of a pair idle.  Returns the us.
+// fit at once.  A tail's item holds as many adjacent rows of its sequence as fit; the rows are
+// counted as if spread evenly over the sequences.  Returns the us.
 double plan_tiles(PrefixPlan& p, int n_q, int n_sm) {
   double best = 1e30;
   if (!p.tiles_p && !p.tiles_t) return 0.0;
   for (int g = 1; g <= 2; ++g) {
-    if (g == 2 && (p.mt < 2 || !p.tiles_p)) break;
+    const int run = std::max(1, std::min(kRows * g / p.h_s, n_q / p.n_seq));  // query rows in a tail's item
+    if (g == 2 && (p.mt < 2 || (!p.tiles_p && run * p.h_s <= kRows))) break;
     // (152 SMs hold 76 clusters of two CTAs of this size, 36 of four)
     const int fit = std::max(1, g == 1 ? n_sm / 2 : n_sm / 4 - n_sm / 76);
     const int mt = (p.mt + g - 1) / g;
@@ -203,7 +205,8 @@ double plan_tiles(PrefixPlan& p, int n_q, int n_sm) {
         const int64_t np = static_cast<int64_t>(mt) * sp;
         // the tails are counted half full: their lengths are known to the device alone
         const double full = p.tiles_t ? 0.5 + 0.5 * p.tail_sure / p.tiles_t : 0.0;
-        const double total = (np * lp + static_cast<double>(n_q) * st * (fix + full * (lt - fix))) / fit;
+        const int live = (n_q + run - 1) / run;  // (an empty item takes a cluster for 1 us)
+        const double total = (np * lp + static_cast<double>(st) * (live * (fix + full * (lt - fix)) + (n_q - live))) / fit;
         const double t = std::max({static_cast<double>((np + fit - 1) / fit) * lp, total + 0.5 * lt, lt}) + kJoinUs * n_q * p.h_s * (sp + st);
         if (t < best) {
           best = t;
@@ -654,17 +657,30 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     tile_base = 0;
     first_pos = 0;
   } else {
-    // (in a pair the second CTA has no rows here: tails of two query rows differ)
+    // Query rows in groups of as many as 128 G rows hold: the item of the first row of a run of one
+    // sequence's rows takes the run, the other rows' items are empty.
     const int k = item - n_prefix;
     split = k / a.n_q;
-    const int t = k - split * a.n_q;
-    row0 = static_cast<int64_t>(t) * a.h_s;
-    n_rows = g == 0 ? a.h_s : 0;
+    const int t = k - split * a.n_q, fit = kRows * G / a.h_s, group = t / fit * fit, group_end = min(group + fit, a.n_q);
+    const int seq = a.q_seq[t];
+    int run = 0, lim = 0;
+    if (t == group || a.q_seq[t - 1] != seq) {
+      for (int base = t;; base += 32) {
+        const int r = base + lane;
+        const unsigned same = __ballot_sync(0xffffffffu, r < group_end && a.q_seq[r] == seq);
+        const int more = same == ~0u ? 32 : __ffs(~same) - 1;
+        if (lane < more) lim = max(lim, prefix_row_limit(a, r, warp == 0 && rank == 0 && split == 0));
+        run += more;
+        if (more < 32) break;
+      }
+      lim = __reduce_max_sync(0xffffffffu, lim);
+    }
+    row0 = static_cast<int64_t>(t) * a.h_s + g * kRows;
+    n_rows = max(min(kRows, run * a.h_s - g * kRows), 0);
     part = pl.st;
-    const int lim = prefix_row_limit(a, t, tid == 0 && rank == 0 && split == 0);
     tiles = lim > pl.tail_lo ? (lim - pl.tail_lo + kTile - 1) / kTile : 0;
     // (a row that sees anything has a sequence in range)
-    tile_base = tiles ? pl.tiles_p + a.q_seq[t] * pl.tiles_t : 0;
+    tile_base = tiles ? pl.tiles_p + seq * pl.tiles_t : 0;
     first_pos = pl.tail_lo;
   }
   const int tile0 = static_cast<int>(static_cast<int64_t>(split) * tiles / part);

@@ -251,7 +251,7 @@ def test_value_scales_apart_from_the_logits(dsa):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("h", [24, 40])
+@pytest.mark.parametrize("h", [24, 40, 64, 128])
 def test_rows_in_any_number_and_order(dsa, h):
     # two-token steps, a chunk of one sequence, rows inside the prefix, rows that see nothing
     lens, prefix = [700, 650, 655, 300], 640
