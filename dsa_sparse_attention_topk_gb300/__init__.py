@@ -129,14 +129,17 @@ def _need(t, dtype, name):
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
 
 
-def _same_device(what, first, *others):
-    """Every tensor on the first one's CUDA device, which is returned."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"{what}: tensors must be CUDA tensors")
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{what}: tensors must be on one device ({t.device} and {dev})")
+def _same_device(what, *tensors):
+    """The index of the CUDA device that every tensor (None: absent) lies on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.get_device()  # (-1: not a CUDA tensor)
+        if dev is None:
+            dev = d
+        if d != dev or d < 0:
+            raise ValueError(f"{what}: tensors must be CUDA tensors on one device (got one on {t.device})")
     return dev
 
 
@@ -146,10 +149,10 @@ def _need_shaped(t, dtype, shape, name):
 
 
 def _call_on(device, stream, fn, *args):
-    """Call a C entry point with `device` current, on `stream` (that device's current one).
+    """Call a C entry point with device number `device` current, on `stream` (that device's current one).
     Pointers come as plain integers: a step of small launches is bound by this host code."""
-    s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    if device.index == torch._C._cuda_getDevice():
+    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if device == torch._C._cuda_getDevice():
         rc = fn(*args, s)
     else:
         with torch.cuda.device(device):
@@ -452,7 +455,7 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, page_table, seq_lens, q_s
         max_pages = page_table.shape[-1]
         _need_shaped(page_table, torch.int32, (n_seq, max_pages), "prefix_attn: page_table")
     if out is None:
-        out = torch.empty(n_q, h_s, V_DIM, dtype=torch.bfloat16, device=dev)
+        out = torch.empty((n_q, h_s, V_DIM), dtype=torch.bfloat16, device=q.device)
     else:
         _need_shaped(out, torch.bfloat16, (n_q, h_s, V_DIM), "prefix_attn: out")
     if out_lse is not None:
@@ -460,12 +463,12 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, page_table, seq_lens, q_s
     if workspace is None:
         # (the plan goes by the device's multiprocessors: ask with that device current)
         size = lib().dsa_prefix_attn_workspace_size
-        if dev.index == torch._C._cuda_getDevice():
+        if dev == torch._C._cuda_getDevice():
             need = size(n_q, h_s, n_seq, prefix_len, max_ctx)
         else:
             with torch.cuda.device(dev):
                 need = size(n_q, h_s, n_seq, prefix_len, max_ctx)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _call_on(dev, stream, lib().dsa_prefix_attn, q.data_ptr(), n_q, h_s, kv_cache.data_ptr(),
              kv_cache.numel() // (PAGE_SIZE * KVCACHE_TOKEN_BYTES),
              None if prefix_pages is None else prefix_pages.data_ptr(), prefix_len,
