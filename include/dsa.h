@@ -353,8 +353,9 @@ int dsa_sparse_attn_noalloc(const void* q_bf16, int32_t n_q, int32_t h_s, const 
  *   out_lse       nullable [n_q][h_s] fp32.
  *   workspace     device scratch of at least dsa_prefix_attn_workspace_size bytes for the same
  *                 sizes and device, 256-byte aligned: the expanded rows (1152 bytes a position
- *                 of the prefix and of n_seq tails of max_ctx - prefix_len; less with up to 32
- *                 heads) and the splits' partial results.  Nothing in it outlives the call.
+ *                 of the prefix and of n_seq tails of max_ctx - prefix_len; a prefix of up to
+ *                 1024 positions may count for every sequence; less with up to 32 heads) and the
+ *                 splits' partial results.  Nothing in it outlives the call.
  * A position whose page is out of range is not seen and flags DSA_STATUS_BAD_PAGE; a row whose
  * sequence or length is out of range sees nothing and flags DSA_STATUS_BAD_SEQ or _BAD_LEN.
  * A cached position with NaN or infinite values makes the rows that see it NaN, and no others.
