@@ -161,13 +161,13 @@ rope_vec_kernel(RopeArgs a, RopeGeom g) {
   const int groups = blockDim.x / g.slots_block, grp = threadIdx.x / g.slots_block;
   const int slot = blockIdx.y * g.slots_block + threadIdx.x % g.slots_block;
   const int64_t rows = static_cast<int64_t>(a.n) * a.h, block0 = static_cast<int64_t>(blockIdx.x) * groups * R;
-  const int64_t r0 = block0 + static_cast<int64_t>(grp) * R;
-  const bool active = grp < groups && slot < g.slots && r0 < rows;
-  if (!TABLE && !active) return;
+  // (a thread without an item helps with the table and takes the rows behind the last)
+  const int64_t r0 = grp < groups && slot < g.slots ? min(block0 + static_cast<int64_t>(grp) * R, rows) : rows;
+  if (!TABLE && r0 == rows) return;
   int e0 = g.lo + slot * V;
   const int half = a.rot >> 1;
   if (HALF && e0 >= a.offset + half) e0 += half;  // the second halves go with the first
-  const bool turn = active && e0 >= a.offset && e0 < a.offset + (HALF ? half : a.rot);
+  const bool turn = e0 >= a.offset && e0 < a.offset + (HALF ? half : a.rot);
   int t = static_cast<int>(static_cast<uint32_t>(r0) / static_cast<uint32_t>(a.h));
   int hh = static_cast<int>(static_cast<uint32_t>(r0) - static_cast<uint32_t>(t) * static_cast<uint32_t>(a.h));
   const int h0 = hh;
@@ -178,7 +178,7 @@ rope_vec_kernel(RopeArgs a, RopeGeom g) {
   Vec<T, V> v[R], w[R];
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    if ((!TABLE || active) && r0 + k < rows) {
+    if (r0 + k < rows) {
       v[k].u = *reinterpret_cast<const W*>(src);
       if (HALF && turn) w[k].u = *reinterpret_cast<const W*>(src + half);
     }
@@ -191,7 +191,6 @@ rope_vec_kernel(RopeArgs a, RopeGeom g) {
     __shared__ float2 s_cs[kTableSize];
     tab = fill_table(a, s_cs, block0, groups * R);
   }
-  if (!active) return;
   float2 cs[P];
   int have = -1;
   hh = h0;
@@ -243,9 +242,9 @@ rope_pair_kernel(RopeArgs a, RopeGeom g) {
   const int groups = blockDim.x / g.slots_block, grp = threadIdx.x / g.slots_block;
   const int slot = blockIdx.y * g.slots_block + threadIdx.x % g.slots_block;
   const int64_t rows = static_cast<int64_t>(a.n) * a.h, block0 = static_cast<int64_t>(blockIdx.x) * groups * R;
-  const int64_t r0 = block0 + static_cast<int64_t>(grp) * R;
-  const bool active = grp < groups && slot < g.slots && r0 < rows;
-  if (!TABLE && !active) return;
+  // (a thread without an item helps with the table and takes the rows behind the last)
+  const int64_t r0 = grp < groups && slot < g.slots ? min(block0 + static_cast<int64_t>(grp) * R, rows) : rows;
+  if (!TABLE && r0 == rows) return;
   const int half = a.rot >> 1;
   const bool turn = slot < half;
   const int c = slot - half;
@@ -259,7 +258,7 @@ rope_pair_kernel(RopeArgs a, RopeGeom g) {
   T v[R], w[R];
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    if ((!TABLE || active) && r0 + k < rows) {
+    if (r0 + k < rows) {
       v[k] = src[0];
       if (turn) w[k] = src[1];
     }
@@ -272,7 +271,6 @@ rope_pair_kernel(RopeArgs a, RopeGeom g) {
     __shared__ float2 s_cs[kTableSize];
     tab = fill_table(a, s_cs, block0, groups * R);
   }
-  if (!active) return;
   float2 cs = make_float2(1.f, 0.f);
   int have = -1;
   hh = h0;
@@ -297,8 +295,8 @@ rope_pair_kernel(RopeArgs a, RopeGeom g) {
 }
 
 // Rows a thread, where there are many: with vectors of 4 bytes or less eight keep more bytes in flight
-// (4096 x 64 heads of 100 bf16: 65 -> 50 us and 29 -> 22 us), with wider ones four do (8 bytes, 192
-// dims: 76 us, with eight rows 116 us).
+// (4096 x 64 heads of 100 bf16, elements: 65 -> 50 us; 60000 rows of 576, 4 bytes: 48 -> 38), with wider
+// ones four do (8 bytes, 4096 x 63 heads of 192 dims: 76 us, with eight rows 116).
 template <typename T, int V> constexpr int kManyRows = V * sizeof(T) <= 4 ? 8 : 4;
 
 template <typename T, bool HALF, int V>
