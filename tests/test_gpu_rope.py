@@ -176,7 +176,7 @@ def _check(got, x, turns, pos, offset, layout, amplitude, sign=1.0):
     (5, 2, 128, 32, 3, 0),        # the rotary part off any vector boundary
     (9, 3, 192, 128, 64, 4),      # row strides that break (bf16) or keep (fp32) 16-byte rows
     (2, 1, 2, 2, 0, 0), (4, 2, 2304, 2048, 256, 0),
-    (2000, 63, 128, 64, 64, 0),   # the four-rows-a-thread form (from 1.2M items), rows crossing tokens
+    (2000, 63, 128, 64, 64, 0),   # several rows a thread (from 311296 items), rows crossing tokens
     (500, 63, 100, 50, 50, 0), (500, 63, 101, 36, 3, 0), (700, 63, 130, 64, 2, 0), (900, 63, 128, 64, 64, 4),  # and narrow
 ])
 def test_rope_matches_the_formula(dsa, n, h, d, rot, offset, pad, dtype, layout):
