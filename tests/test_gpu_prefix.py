@@ -264,6 +264,19 @@ def test_rows_in_any_number_and_order(dsa, h):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("h", [48, 64, 128])
+def test_adjacent_rows_share_a_tail_behind_a_long_prefix(dsa, h):
+    # runs of one to six rows of a sequence, some cut by rows that see no tail or nothing
+    lens, prefix = [1500, 1400, 1130], 1100
+    rows = [(0, 1200 + 60 * i) for i in range(5)] + [(1, 1399), (0, 1499), (1, 1101), (1, 1100), (1, 1099), (1, -1), (1, 1300),
+                                                     (2, 1129), (2, 500), (2, 1128), (0, 1100)]
+    b = Batch(dsa, lens, prefix, h, rows=rows, seed=9, max_ctx=1600)
+    out, lse = b.call(dsa)
+    assert dsa.device_status() == 0
+    b.check(out, lse)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("h", [16, 48])
 def test_bad_pages_sequences_and_lengths_are_skipped_and_flagged(dsa, h):
     lens, prefix = [900, 800, 2000, 850, -3], 700
