@@ -5,6 +5,9 @@ stream) into the C ABI of ``libdsa.so`` (declared in ``include/dsa.h``); every s
 the path runs in the library's CUDA kernels.  If the library is missing or a call fails,
 an exception is raised -- there is no other implementation to fall back to.
 
+Where a call takes ``stream``, its inputs must be ready on that stream; a result or workspace that
+the caller does not pass is allocated on it, and the caller waits for it before reading a result.
+
 Functions (same names as the C entry points, without the ``dsa_`` prefix):
 
 * ``quant_kv_mxfp8(k, slot_mapping, k_cache)``  -- cache writer, MXFP8 indexer keys
@@ -148,6 +151,26 @@ def _need_shaped(t, dtype, shape, name):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
 
 
+def _scratch(stream, size, device):
+    """`size` bytes for a call on `stream` (None: the device's current one), which may be dropped once the call
+    is issued: the block belongs to that stream, so the allocator hands it to no other one meanwhile."""
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def _result(stream, shape, dtype, device):
+    """A result that a call on `stream` writes and its caller reads.  As `_scratch`; and since the caller's
+    current stream is another one, the block also waits for that one when it is dropped."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _call_on(device, stream, fn, *args):
     """Call a C entry point with device number `device` current, on `stream` (that device's current one).
     Pointers come as plain integers: a step of small launches is bound by this host code."""
@@ -270,7 +293,7 @@ def rope(x, pos, turns, offset=0, layout="interleaved", amplitude=1.0, transpose
     if len(shape) not in (2, 3) or code is None:
         raise ValueError("rope: x must be [n, d] or [n, h, d] of bf16, fp16 or fp32")
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _result(stream, shape, x.dtype, x.device)
     elif out.shape != shape or out.dtype != x.dtype:
         raise ValueError("rope: out must have x's shape and dtype")
     dev = _same_device("rope", x, pos, turns, out)
@@ -455,7 +478,7 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, page_table, seq_lens, q_s
         max_pages = page_table.shape[-1]
         _need_shaped(page_table, torch.int32, (n_seq, max_pages), "prefix_attn: page_table")
     if out is None:
-        out = torch.empty((n_q, h_s, V_DIM), dtype=torch.bfloat16, device=q.device)
+        out = _result(stream, (n_q, h_s, V_DIM), torch.bfloat16, q.device)
     else:
         _need_shaped(out, torch.bfloat16, (n_q, h_s, V_DIM), "prefix_attn: out")
     if out_lse is not None:
@@ -468,7 +491,7 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, page_table, seq_lens, q_s
         else:
             with torch.cuda.device(dev):
                 need = size(n_q, h_s, n_seq, prefix_len, max_ctx)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(stream, need, q.device)
     _call_on(dev, stream, lib().dsa_prefix_attn, q.data_ptr(), n_q, h_s, kv_cache.data_ptr(),
              kv_cache.numel() // (PAGE_SIZE * KVCACHE_TOKEN_BYTES),
              None if prefix_pages is None else prefix_pages.data_ptr(), prefix_len,
