@@ -351,7 +351,7 @@ def indexer_topk(q, w, k_cache, page_table, seq_lens, q_seq, q_pos, topk, max_ct
     [n_q].  Returns (out_idx int32 [n_q, topk], out_scores fp32 or None)."""
     n_q, h_i, _ = q.shape
     if out_idx is None:
-        out_idx = torch.empty(n_q, topk, dtype=torch.int32, device=q.device)
+        out_idx = _result(stream, (n_q, topk), torch.int32, q.device)
     num_pages = k_cache.numel() // KCACHE_PAGE_BYTES
     _check(lib().dsa_indexer_topk(_ptr(q), _ptr(w), n_q, h_i, q_group, _ptr(k_cache), num_pages,
                                   _ptr(page_table), page_table.shape[1], _ptr(seq_lens), _ptr(q_seq),
@@ -365,7 +365,7 @@ def indexer_scores(q, w, k_cache, page_table, seq_lens, q_seq, q_pos, max_ctx, q
     """All scores [n_q, max_ctx] fp32 (-inf where a row may not select)."""
     n_q, h_i, _ = q.shape
     if out is None:
-        out = torch.empty(n_q, max_ctx, dtype=torch.float32, device=q.device)
+        out = _result(stream, (n_q, max_ctx), torch.float32, q.device)
     num_pages = k_cache.numel() // KCACHE_PAGE_BYTES
     _check(lib().dsa_indexer_scores(_ptr(q), _ptr(w), n_q, h_i, q_group, _ptr(k_cache), num_pages,
                                     _ptr(page_table), page_table.shape[1], _ptr(seq_lens), _ptr(q_seq),
@@ -384,10 +384,10 @@ def sparse_attn(q, kv_cache, page_table, seq_lens, q_seq, topk_idx, sm_scale, ou
     n_q, h_s, _ = q.shape
     topk = topk_idx.shape[1]
     if out is None:
-        out = torch.empty(n_q, h_s, V_DIM, dtype=torch.bfloat16, device=q.device)
+        out = _result(stream, (n_q, h_s, V_DIM), torch.bfloat16, q.device)
     ws_need = sparse_attn_workspace_size(n_q, h_s, topk)
     if workspace is None and ws_need:
-        workspace = torch.empty(ws_need, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(stream, ws_need, q.device)
     num_pages = kv_cache.numel() // (PAGE_SIZE * KVCACHE_TOKEN_BYTES)
     _check(lib().dsa_sparse_attn(_ptr(q), n_q, h_s, _ptr(kv_cache), num_pages, _ptr(page_table),
                                  page_table.shape[1], _ptr(seq_lens), _ptr(q_seq), seq_lens.shape[0],
@@ -413,12 +413,12 @@ def decode_step(k_new, kv_new, slot_mapping, k_cache, kv_cache, q_idx, w, q_sfa,
     n_q, h_i, _ = q_idx.shape
     h_s = q_sfa.shape[1]
     if out_idx is None:
-        out_idx = torch.empty(n_q, topk, dtype=torch.int32, device=q_idx.device)
+        out_idx = _result(stream, (n_q, topk), torch.int32, q_idx.device)
     if out is None:
-        out = torch.empty(n_q, h_s, V_DIM, dtype=torch.bfloat16, device=q_idx.device)
+        out = _result(stream, (n_q, h_s, V_DIM), torch.bfloat16, q_idx.device)
     ws_need = sparse_attn_workspace_size(n_q, h_s, topk)
     if workspace is None and ws_need:
-        workspace = torch.empty(ws_need, dtype=torch.uint8, device=q_idx.device)
+        workspace = _scratch(stream, ws_need, q_idx.device)
     num_pages = min(k_cache.numel() // KCACHE_PAGE_BYTES, kv_cache.numel() // (PAGE_SIZE * KVCACHE_TOKEN_BYTES))
     _check(lib().dsa_decode_step(_ptr(k_new), _ptr(kv_new), _ptr(slot_mapping), n_new, _ptr(k_cache),
                                  _ptr(kv_cache), num_pages, _ptr(page_table), page_table.shape[1],
@@ -437,7 +437,7 @@ def sparse_attn_noalloc(q, kv_cache, page_table, seq_lens, q_seq, topk_idx, sm_s
     n_q, h_s, _ = q.shape
     topk = topk_idx.shape[1]
     if out is None:
-        out = torch.empty(n_q, h_s, V_DIM, dtype=torch.bfloat16, device=q.device)
+        out = _result(stream, (n_q, h_s, V_DIM), torch.bfloat16, q.device)
     num_pages = kv_cache.numel() // (PAGE_SIZE * KVCACHE_TOKEN_BYTES)
     _check(lib().dsa_sparse_attn_noalloc(_ptr(q), n_q, h_s, _ptr(kv_cache), num_pages, _ptr(page_table),
                                          page_table.shape[1], _ptr(seq_lens), _ptr(q_seq), seq_lens.shape[0],
@@ -515,12 +515,12 @@ def topk_merge(cand_idx, cand_scores, topk, part_offsets=None, local_lo=None, lo
     _need(cand_scores, torch.float32, "cand_scores")
     n_parts, n_q, k_in = cand_idx.shape
     if out_idx is None:
-        out_idx = torch.empty(n_q, topk, dtype=torch.int32, device=cand_idx.device)
+        out_idx = _result(stream, (n_q, topk), torch.int32, cand_idx.device)
     if out_scores is None:
-        out_scores = torch.empty(n_q, topk, dtype=torch.float32, device=cand_idx.device)
+        out_scores = _result(stream, (n_q, topk), torch.float32, cand_idx.device)
     out_local = None
     if local_lo is not None:
-        out_local = torch.empty(n_q, topk, dtype=torch.int32, device=cand_idx.device)
+        out_local = _result(stream, (n_q, topk), torch.int32, cand_idx.device)
     _check(lib().dsa_topk_merge(_ptr(cand_idx), _ptr(cand_scores), _ptr(part_offsets), n_parts, n_q, k_in, topk,
                                 _ptr(out_idx), _ptr(out_scores), _ptr(local_lo), _ptr(local_hi), _ptr(out_local),
                                 _stream(stream)))
@@ -534,9 +534,9 @@ def lse_combine(o_parts, lse_parts, out=None, out_lse=None, stream=None):
     _need(lse_parts, torch.float32, "lse_parts")
     n_parts, n_q, h, _ = o_parts.shape
     if out is None:
-        out = torch.empty(n_q, h, V_DIM, dtype=torch.bfloat16, device=o_parts.device)
+        out = _result(stream, (n_q, h, V_DIM), torch.bfloat16, o_parts.device)
     if out_lse is None:
-        out_lse = torch.empty(n_q, h, dtype=torch.float32, device=o_parts.device)
+        out_lse = _result(stream, (n_q, h), torch.float32, o_parts.device)
     _check(lib().dsa_lse_combine(_ptr(o_parts), _ptr(lse_parts), n_parts, n_q, h, _ptr(out), _ptr(out_lse),
                                  _stream(stream)))
     return out, out_lse

@@ -56,8 +56,9 @@ def traced(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: "current")
     monkeypatch.setattr(torch.Tensor, "record_stream", record)
+    monkeypatch.setattr(pkg, "_need", lambda t, dtype, name: None)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
-    return seen
+    yield seen
 
 
 def _i32(*shape):
@@ -75,13 +76,29 @@ CALLS = {
     "rope": lambda s: pkg.rope(torch.zeros(3, 64), _i32(3), torch.zeros(32, dtype=torch.int64), stream=s),
     "prefix_attn": lambda s: pkg.prefix_attn(_bf16(1, 16, 576), KV_CACHE, _i32(1), 10, _i32(1, 1), _i32(1), _i32(1),
                                              _i32(1), 20, SM, stream=s),
+    "sparse_attn": lambda s: pkg.sparse_attn(_bf16(1, 16, 576), KV_CACHE, _i32(1, 1), _i32(1), _i32(1), _i32(1, 8), SM,
+                                             stream=s),
+    "sparse_attn_noalloc": lambda s: pkg.sparse_attn_noalloc(_bf16(1, 16, 576), KV_CACHE, _i32(1, 1), _i32(1), _i32(1),
+                                                             _i32(1, 8), SM, stream=s),
+    "decode_step": lambda s: pkg.decode_step(_bf16(0, 128), _bf16(0, 576), torch.zeros(0, dtype=torch.int64), K_CACHE,
+                                             KV_CACHE, _bf16(1, 8, 128), torch.zeros(1, 8), _bf16(1, 16, 576), _i32(1, 1),
+                                             _i32(1), _i32(1), _i32(1), 8, 20, SM, stream=s),
+    "indexer_topk": lambda s: pkg.indexer_topk(_bf16(1, 8, 128), torch.zeros(1, 8), K_CACHE, _i32(1, 1), _i32(1), _i32(1),
+                                               _i32(1), 8, 20, stream=s),
+    "indexer_scores": lambda s: pkg.indexer_scores(_bf16(1, 8, 128), torch.zeros(1, 8), K_CACHE, _i32(1, 1), _i32(1),
+                                                   _i32(1), _i32(1), 20, stream=s),
+    "topk_merge": lambda s: pkg.topk_merge(_i32(2, 1, 8), torch.zeros(2, 1, 8), 8, local_lo=_i32(1), local_hi=_i32(1),
+                                           stream=s),
+    "lse_combine": lambda s: pkg.lse_combine(_bf16(2, 1, 16, 512), torch.zeros(2, 1, 16), stream=s),
 }
 
 
 @pytest.mark.parametrize("name", sorted(CALLS))
 def test_allocations_belong_to_the_calls_stream(traced, name):
     s = _Stream()
-    CALLS[name](s)
+    call = CALLS[name]
+    traced.clear()
+    call(s)
     assert traced and all(e[1] == [s] for e in traced)
     # what is returned is read on the caller's stream; a workspace (512 bytes here) is not
     assert all(e[2] == (e[0] != 512) for e in traced)
