@@ -433,9 +433,12 @@ __device__ __forceinline__ float sum_quotient_round_to_odd(float x, float low, f
   if (r != 0.f && (qb & 1u) == 0u) qb += (r > 0.f) ? 1u : 0xFFFFFFFFu;
   return copysignf(__uint_as_float(qb), x);
 }
-// largest of the warp's non-negative floats (a NaN is ignored, as fmaxf does)
+// largest of the warp's floats; a NaN is ignored unless every lane has one, as in a chain of fmaxf
+// (an integer maximum over the bits would do for numbers, but makes a tile of NaN one of zeros)
 __device__ __forceinline__ float warp_amax(float v) {
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v, 0.f))));
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(v));
+  return y;
 }
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return static_cast<uint32_t>(f32x2_to_e4m3x2(a, b)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(c, d)) << 16);
