@@ -354,11 +354,12 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
 constexpr int kWarpsPerBlock = 8;
 constexpr int kRot = 64;
 
-// a c + b s as hi + lo (a, b exact inputs)
+// a c + b s as hi + lo (a, b exact inputs); an infinity or NaN has no low part
 __device__ __forceinline__ Two dot2(float a, const Two& c, float b, const Two& s) {
   const float p = a * c.hi, q = b * s.hi;
   const float e = fmaf(a, c.hi, -p) + fmaf(b, s.hi, -q);   // the products' roundings
   const float h = p + q, t = h - p;
+  if (!(fabsf(h) < INFINITY)) return {h, 0.f};
   const float f = (p - (h - t)) + (q - t);                 // the sum's rounding (Knuth's two-sum)
   const float l = f + e + fmaf(a, c.lo, b * s.lo);
   return two_sum_ordered(h, l);

@@ -51,7 +51,7 @@ def _kv_cases(kv, top):
     kv[11, 512:] = -top
     kv[12, 512:576:2] = NAN
     kv[13] = NAN
-    kv[14, 575], kv[14, 512] = -top, 3 * top
+    kv[14, 575], kv[14, 512] = -top, 3e38
     return kv
 
 
@@ -70,7 +70,7 @@ def _k_cases(k, top):
     return k
 
 
-@pytest.mark.parametrize("top", [1.0])    # NaN alone
+@pytest.mark.parametrize("top", [1.0, math.inf])    # NaN alone, and infinities beside it
 @pytest.mark.parametrize("layout", ["interleaved", "half"])
 @pytest.mark.parametrize("k_offset", [0, 20, 64])
 def test_non_finite_values_are_stored_as_the_plain_writer_stores_them(dsa, k_offset, layout, top):
