@@ -88,6 +88,7 @@ _SIGS = {
                                        _P, _P, _SZ, _P]),
     "dsa_device_status": (ctypes.c_int, [_P]),
     "dsa_test_stall_indexer": (ctypes.c_int, [_I32]),
+    "dsa_test_prefix_plan": (ctypes.c_int, [_I32, _I32, _I32, _I32, _I32, _P]),
     "dsa_topk_merge": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P]),
     "dsa_lse_combine": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _P, _P, _P]),
     "dsa_last_error": (ctypes.c_char_p, []),
@@ -555,6 +556,14 @@ def test_stall_indexer(wait_limit_us):
     every following indexer launch stall its copy producer and give up waiting after that
     many microseconds; 0 restores normal operation."""
     _check(lib().dsa_test_stall_indexer(int(wait_limit_us)))
+
+
+def test_prefix_plan(n_q, h_s, n_seq, prefix_len, max_ctx):
+    """Testing aid (dsa_test_prefix_plan): how prefix_attn would split a call of these sizes."""
+    plan = (_I32 * 8)()
+    _check(lib().dsa_test_prefix_plan(n_q, h_s, n_seq, prefix_len, max_ctx, plan))
+    return dict(zip(("group", "tiles_prefix", "splits_prefix", "tail_first", "tiles_tail", "splits_tail", "few_parts",
+                     "few_first"), plan))
 
 
 def status_names(bits):

@@ -501,6 +501,13 @@ int dsa_lse_combine(const void* o_parts, const float* lse_parts, int32_t n_parts
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "lse_combine launch");
 }
 
+int dsa_test_prefix_plan(int32_t n_q, int32_t h_s, int32_t n_seq, int32_t prefix_len, int32_t max_ctx, int32_t* plan) {
+  if (!prefix_sizes_ok(n_q, h_s, n_seq, prefix_len, max_ctx) || !plan)
+    return fail(DSA_ERR_INVALID_ARG, "test_prefix_plan: sizes out of range, or null");
+  dsa::prefix_plan_numbers(n_q, h_s, n_seq, prefix_len, max_ctx, plan);
+  return DSA_OK;
+}
+
 int dsa_test_stall_indexer(int32_t wait_limit_us) {
   if (wait_limit_us < 0 || wait_limit_us > 10000000)
     return fail(DSA_ERR_INVALID_ARG, "test_stall_indexer: wait_limit_us must be 0..10000000");

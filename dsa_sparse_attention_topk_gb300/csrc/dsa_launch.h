@@ -165,6 +165,7 @@ struct PrefixArgs {
 };
 cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char** err);
 size_t prefix_workspace_bytes(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx);
+void prefix_plan_numbers(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, int32_t* out);
 
 int topk_merge_pow2(int n);
 cudaError_t launch_topk_merge(const TopkMergeArgs& a, cudaStream_t s);

@@ -434,6 +434,16 @@ int dsa_lse_combine(const void* o_parts, const float* lse_parts, int32_t n_parts
  */
 int dsa_test_stall_indexer(int32_t wait_limit_us);
 
+/*
+ * dsa_test_prefix_plan -- a testing aid: how dsa_prefix_attn would split a call of these sizes on
+ * the current device (host arithmetic; without a device, for 152 multiprocessors), so that a
+ * test can tell which kernel it reaches.  plan: 8 int32 in host memory: CTAs an MMA (1 or 2; 0:
+ * nothing on tensor memory), 64-position tiles of the prefix and their splits, first position of
+ * the tails, tiles of the longest tail and their splits, parts of a row on the path for few
+ * heads (0: not taken) and its first position.
+ */
+int dsa_test_prefix_plan(int32_t n_q, int32_t h_s, int32_t n_seq, int32_t prefix_len, int32_t max_ctx, int32_t* plan);
+
 /* dsa_last_error -- message for the last non-zero return on this host thread. */
 const char* dsa_last_error(void);
 
