@@ -32,14 +32,22 @@
 // order own 0, peer 0, own 1, peer 1 ...
 //
 // The softmax reference.  With e the exponent of its tile, a position's weight is stored as
-// 2^(x + e - rho), x its logit in powers of two and rho the row's reference: the first tile's
-// largest x + e, which CTA 0 also sends to CTA 1.  Weights may exceed 1 (up to 2^14 before
-// fp16 runs out), so rho hardly ever changes; the sum of 2^(x - rho) is kept in fp32 from
-// the unrounded weights.  When a tile's largest weight would pass 2^14 its owner raises rho for
-// that row and rescales its accumulator; the references travel with the weights, and the
+// 2^(x + e - rho), x its logit in powers of two and rho the row's reference.  fp16 has room for
+// weights up to 2^15 and 11 bits down to 2^-14, so rho goes by the level that the first tile's
+// positions share, not by its largest alone: the lowest of four maxima of 16, plus 2, at most 3
+// below the largest of all and at least 14 below it.  A position far above the rest (an attention
+// sink, often with next to nothing in its value) then keeps 2^14 and leaves the others their bits;
+// without one, later tiles may grow by 12 powers of two before rho changes.  CTA 0 sends the first
+// rho to CTA 1; the sum of 2^(x - rho) is kept in fp32 from the unrounded weights.  Where a tile's
+// largest weight would pass 2^15 its owner raises rho, to 5 below the largest so far, for all
+// rows of the warp that this would raise (waiting for the products is the cost, and the rows
+// share it), and rescales its accumulator; the references travel with the weights, and the
 // receiving CTA raises its own (rescaling its accumulator) or, where it has itself gone
 // ahead, scales the received row down.  After each tile in the order above both CTAs hold the
 // largest reference used so far, so the results do not depend on timing.
+// Measured, 32 rows behind 32K, logits of a spread of 2.5, 4, 6 and 10 powers of two: 201, 204, 216
+// and 240 us; raising single rows 238 at a spread of 6; 11 below instead of 5: 259 there, 0: 209;
+// rho 10 below the first largest whatever its tile looks like: 288 at 2.5.
 //
 // MMA pairs.  Where there are rows enough, four CTAs share an item of 256 rows: two per parity,
 // whose tensor cores work as one (cta_group::2) on 128 rows each, every B operand split between
@@ -81,7 +89,10 @@ constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 constexpr uint32_t kPBytes = kRows * 128;     // the weights of a tile
 constexpr uint32_t kPMsg = kPBytes + kRows * 4;  // with the rows' references
 constexpr uint32_t kPStride = (kPMsg + 1023) / 1024 * 1024;
-constexpr float kHeadroom = 14.0f;            // powers of two a weight may reach
+// Powers of two: what a weight may reach before its row's reference is raised (2^16 is too large for
+// fp16); the first tile's largest weight at most and at least, and its reference's height above the
+// lowest of four maxima in between; the largest weight behind a raise.
+constexpr float kHeadroom = 15.0f, kMost = 14.0f, kLeast = 3.0f, kAbove = 2.0f, kRaised = 5.0f;
 
 // Shared memory behind the query's part: own weights, the peer's weights, value tiles, tiles for
 // Q K^T.  Loads and copies between CTAs take some 2000 cycles, nearly a step of two tiles, so
@@ -863,7 +874,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   if (warp < 12) turn_query();
 
   // softmax threads: their row's state, kept from the loop to the output
-  float rho = -INFINITY, l = 0.f;
+  float rho = -INFINITY, top = -INFINITY, l = 0.f;
   int e_top = -1000;
   if (warp == 0) {
     // ---------------- own tiles ----------------
@@ -1010,12 +1021,14 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       __syncwarp();
       const float r_in = reinterpret_cast<const float*>(p_in + kPBytes)[m];
       if (__any_sync(0xffffffffu, r_in != rho)) {
-        // every product so far: the last was the own tile's, or the peer's before it
-        if (i < n_own) wait_warp(&ctl.v_empty[Lay::own_slot(i)], Lay::own_phase(i));
-        else if (i > 0) wait_warp(&ctl.v_empty[Lay::peer_slot(i - 1, n_own)], Lay::peer_phase(i - 1, n_own));
         const bool raise = r_in > rho;
-        rescale(raise ? r_in - rho : 0.f, i < n_own || i > 0);
-        if (raise) rho = r_in;
+        if (__any_sync(0xffffffffu, raise)) {
+          // every product so far: the last was the own tile's, or the peer's before it
+          if (i < n_own) wait_warp(&ctl.v_empty[Lay::own_slot(i)], Lay::own_phase(i));
+          else if (i > 0) wait_warp(&ctl.v_empty[Lay::peer_slot(i - 1, n_own)], Lay::peer_phase(i - 1, n_own));
+          rescale(raise ? r_in - rho : 0.f, i < n_own || i > 0);
+          if (raise) rho = r_in;
+        }
         if (r_in < rho) {  // sent before the peer learned of this reference (2^-inf = 0)
           const float f = exp2f(r_in - rho);
           uint8_t* row = p_in + m * 128;
@@ -1077,13 +1090,16 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       }
       const float mt = row_max(fmaf(fmaxf(t0, t1), kt, fe), i & 1);
       if (i == 0 && c == 0) {
-        rho = mt;
+        const float low = -row_max(-fmaf(fminf(t0, t1), kt, fe), 1);
+        asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");  // read before the next tile's maxima
+        rho = fmaxf(fminf(low + kAbove, mt - kLeast), mt - kMost);
         if (hv == 0) st_async_f32(dsmem_addr(&ctl.sent[m], peer), rho, dsmem_addr(&ctl.r_full, peer));
       }
-      // the reference these weights are made with: the row's, or a new one where a weight would pass
-      // 2^14 or at the row's first position
+      // the reference these weights are made with: the row's, or a new one where a weight of this warp
+      // would pass 2^15 or is a row's first
+      top = fmaxf(top, mt);
       const bool raise = mt > rho + kHeadroom || (rho == -INFINITY && mt > -INFINITY);
-      const float rho_p = raise ? mt : rho;
+      const float rho_p = __any_sync(0xffffffffu, raise) ? fmaxf(rho, top - kRaised) : rho;
       const float off = fe - (rho_p == -INFINITY ? 0.f : rho_p);
       uint32_t p[16];
       float x0 = 0.f, x1 = 0.f;
@@ -1100,10 +1116,12 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       // Q K^T and softmax to arrive
       if (i > 0) reconcile(i - 1);
       if (__any_sync(0xffffffffu, rho_p != rho)) {
-        if (i > 0) wait_warp(&ctl.v_empty[Lay::peer_slot(i - 1, n_own)], Lay::peer_phase(i - 1, n_own));  // every product so far
         const bool up = rho_p > rho;
-        rescale(up ? rho_p - rho : 0.f, i > 0);
-        if (up) rho = rho_p;
+        if (__any_sync(0xffffffffu, up)) {
+          if (i > 0) wait_warp(&ctl.v_empty[Lay::peer_slot(i - 1, n_own)], Lay::peer_phase(i - 1, n_own));  // every product so far
+          rescale(up ? rho_p - rho : 0.f, i > 0);
+          if (up) rho = rho_p;
+        }
         if (rho_p < rho) {  // the peer went ahead meanwhile (2^-inf = 0)
           const float f = exp2f(rho_p - rho);
           sum *= f;

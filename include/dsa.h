@@ -332,8 +332,11 @@ int dsa_sparse_attn_noalloc(const void* q_bf16, int32_t n_q, int32_t h_s, const 
  *     l_p = sm_scale * q[t, h] . kv[p];  o[t, h] = sum_p softmax(l)_p kv[p][0:512]
  *     lse[t, h] = log sum_p exp(l_p)
  * A row that sees nothing gets o = 0 and lse = -inf.  For the tensor cores the query (by a
- * power of two per row), the dequantised values (by one per 64 positions) and the softmax
- * weights are held in fp16, 11 bits for whatever lies within 2^-29 of the largest; sums in fp32.
+ * power of two per row) and the dequantised values (by one per 64 positions) are held in fp16, 11
+ * bits for whatever lies within 2^-29 of the largest, and so are the softmax weights: 11 bits down
+ * to 2^-17 of the row's largest, or to 2^-28 as far as that stands out of the 64 positions that the
+ * row (or a part of it that was worked on apart) begins with; below that in steps of 2^-10 of the
+ * bound.  Sums are fp32.
  * With up to 32 heads, where no more memory is read for it, the codes are used as they are and
  * their scales stay in fp32: there the weights times the scales are held in fp16.
  *   q_bf16        [n_q][h_s][576] bfloat16, 16-byte aligned; h_s 1..128.
