@@ -34,11 +34,12 @@
 // The softmax reference.  With e the exponent of its tile, a position's weight is stored as
 // 2^(x + e - rho), x its logit in powers of two and rho the row's reference.  fp16 has room for
 // weights up to 2^15 and 11 bits down to 2^-14, so rho goes by the level that the first tile's
-// positions share, not by its largest alone: the lowest of four maxima of 16, plus 2, at most 3
-// below the largest of all and at least 14 below it.  A position far above the rest (an attention
+// positions share, not by its largest alone: the lowest of four maxima of 16, plus 2, but at least
+// 3 and at most 14 below the largest of all.  A position far above the rest (an attention
 // sink, often with next to nothing in its value) then keeps 2^14 and leaves the others their bits;
 // without one, later tiles may grow by 12 powers of two before rho changes.  CTA 0 sends the first
-// rho to CTA 1; the sum of 2^(x - rho) is kept in fp32 from the unrounded weights.  Where a tile's
+// rho to CTA 1; the sum of 2^(x - rho) is kept in fp32 from the unrounded weights, in units of
+// 2^-e of the lowest e so far (in units of 1, values of 2^-106 would take it past 2^127).  Where a tile's
 // largest weight would pass 2^15 its owner raises rho, to 5 below the largest so far, for all
 // rows of the warp that this would raise (waiting for the products is the cost, and the rows
 // share it), and rescales its accumulator; the references travel with the weights, and the
@@ -875,7 +876,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 
   // softmax threads: their row's state, kept from the loop to the output
   float rho = -INFINITY, top = -INFINITY, l = 0.f;
-  int e_top = -1000;
+  int e_top = -1000, e_low = 1000, e_sum = 1000;  // largest and lowest exponent of the tiles; l is in units of 2^-e_sum
   if (warp == 0) {
     // ---------------- own tiles ----------------
     if (lane == 0 && wait(&ctl.q_moved, 0)) {
@@ -1015,7 +1016,9 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     auto reconcile = [&](int i) {
       const int b = i % Lay::kBufs;
       uint8_t* p_in = smem + Lay::p_in + b * kPStride;
-      e_top = max(e_top, __ldcg(&ws.info[tile_base + tile0 + 2 * i + other].e));
+      const int e_in = __ldcg(&ws.info[tile_base + tile0 + 2 * i + other].e);
+      e_top = max(e_top, e_in);
+      e_low = min(e_low, e_in);
       wait_warp(&ctl.pin_full[b], i / Lay::kBufs);
       if (tid == 4 * 32) tc::mbar_arrive_expect_tx(&ctl.pin_full[b], kPMsg);  // the buffer's next weights
       __syncwarp();
@@ -1064,6 +1067,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       const uint64_t seen64 = w.x & (nv >= kTile ? ~0ull : nv <= 0 ? 0ull : (1ull << nv) - 1ull);
       const uint32_t seen = static_cast<uint32_t>(seen64 >> (32 * hv)), poison = static_cast<uint32_t>(w.y >> (32 * hv));
       e_top = max(e_top, e);
+      e_low = min(e_low, e);
       // (held inside fp32's range: a factor of 0 would turn an unseen position's -inf into NaN)
       const float kt = fminf(fmaxf(k2 * exp2i(e), 1.2e-38f), 3.0e38f);
       const float fe = static_cast<float>(e);
@@ -1132,7 +1136,12 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
           }
         }
       }
-      l = fmaf(sum, exp2i(-e), l);
+      // (the sum's unit follows the lowest exponent, so that it stays below 2^15 a position)
+      if (e < e_sum) {
+        l *= exp2i(max(e - e_sum, -126));
+        e_sum = e;
+      }
+      l = fmaf(sum, exp2i(max(e_sum - e, -126)), l);
       wait_warp(&ctl.p_empty[b], i / Lay::kBufs + 1);
       uint8_t* p_own = smem + Lay::p_own + b * kPStride;
 #pragma unroll
@@ -1152,7 +1161,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     // the last weights have been read, here and by the peer (whose word of it has then arrived)
     for (int i = max(0, n_own - Lay::kBufs); i < n_own; ++i) wait_warp(&ctl.p_empty[i % Lay::kBufs], i / Lay::kBufs);
     // ---- the row's sum over its two threads and both CTAs ----
-    ctl.part[0][hv][m] = l;
+    ctl.part[0][hv][m] = l * exp2i(max(e_low - e_sum, -126));
     asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
     l = ctl.part[0][0][m] + ctl.part[0][1][m];
     if (hv == 0) st_async_f32(dsmem_addr(&ctl.sent[m], peer), l, dsmem_addr(&ctl.fin_full, peer));
@@ -1171,8 +1180,9 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     const int hv = (warp - 4) >> 2, m = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int e_out = e_top;
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    const float down = exp2i(-e_out);
+    // O / l is this times 2^e_out (O is in units of 1, l of 2^-e_low)
+    const float inv = (l > 0.f || l != l ? 1.f / l : 0.f) * exp2i(max(e_low - e_out, -126));
+    const float up = ns == 1 ? exp2i(e_out) : 1.f;
     uint8_t* row = stage + m * kStagePitch;
 #pragma unroll 2
     for (int k = 0; k < 4; ++k) {
@@ -1186,14 +1196,14 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float y0 = __uint_as_float(v[i + 2 * j]) * inv, y1 = __uint_as_float(v[i + 2 * j + 1]) * inv;
-          o[j] = ns == 1 ? pack_bf162(y0, y1) : pack_half2(y0 * down, y1 * down);
+          o[j] = ns == 1 ? pack_bf162(y0 * up, y1 * up) : pack_half2(y0, y1);
         }
         *reinterpret_cast<uint4*>(row + 2 * (col + i)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
     if (c == 0 && hv == 0 && m < n_rows) {
-      if (ns > 1) ws.ml[(row0 + m) * ns + slot] = split_state(rho, l, e_out);
-      else if (a.out_lse) a.out_lse[row0 + m] = natural_lse(rho, l);
+      if (ns > 1) ws.ml[(row0 + m) * ns + slot] = split_state(rho - static_cast<float>(e_low), l, e_out);
+      else if (a.out_lse) a.out_lse[row0 + m] = natural_lse(rho - static_cast<float>(e_low), l);
     }
   }
   __syncthreads();
