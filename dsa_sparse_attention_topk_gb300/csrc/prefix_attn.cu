@@ -39,7 +39,9 @@
 // sink, often with next to nothing in its value) then keeps 2^14 and leaves the others their bits;
 // without one, later tiles may grow by 12 powers of two before rho changes.  CTA 0 sends the first
 // rho to CTA 1; the sum of 2^(x - rho) is kept in fp32 from the unrounded weights, in units of
-// 2^-e of the lowest e so far (in units of 1, values of 2^-106 would take it past 2^127).  Where a tile's
+// 2^-e of the lowest e so far (in units of 1, values of 2^-106 would take it past 2^127).  A tile of
+// zeros has the lowest exponent of all, so that it sets no reference above the others' weights;
+// its positions, logit 0, are counted, and join the sum at the end.  Where a tile's
 // largest weight would pass 2^15 its owner raises rho, to 5 below the largest so far, for all
 // rows of the warp that this would raise (waiting for the products is the cost, and the rows
 // share it), and rescales its accumulator; the references travel with the weights, and the
@@ -164,9 +166,10 @@ constexpr int kShortPrefix = 1024;  // (expanded for every sequence, it should n
 constexpr double kJoinUs = 2048.0 / 5.0e6, kFewUs16 = 1.5, kFewUs16Pair = 3.6, kFewUs32 = 2.2;
 
 // What expand writes per tile.
+constexpr int kLowest = -120, kZeros = kLowest - 1;
 struct alignas(32) TileInfo {
   uint64_t valid, poison;    // a bit per position
-  int32_t e;                 // stored value = value * 2^-e
+  int32_t e;                 // stored value = value * 2^-e; kZeros where all are 0
   int32_t pad[3];
 };
 
@@ -368,7 +371,7 @@ expand_kernel(PrefixArgs a, PrefixPlan pl, PrefixWs ws) {
   __syncthreads();
   // 448 * scale < 2^(floor(log2 scale) + 10): below 2^15 once stored
   // (not below -120: powers of two up and down from there stay inside fp32's normal range)
-  const int e = s_scale ? max(static_cast<int>(s_scale >> 23) - 127 - 5, -120) : 0;
+  const int e = s_scale ? max(static_cast<int>(s_scale >> 23) - 127 - 5, kLowest) : kZeros;
   uint4* dst = reinterpret_cast<uint4*>(ws.kv + static_cast<int64_t>(tile) * kTile * kLatent);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -876,7 +879,11 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 
   // softmax threads: their row's state, kept from the loop to the output
   float rho = -INFINITY, top = -INFINITY, l = 0.f;
-  int e_top = -1000, e_low = 1000, e_sum = 1000;  // largest and lowest exponent of the tiles; l is in units of 2^-e_sum
+  int e_top = kZeros, e_sum = 1000;  // largest exponent of the tiles; l is in units of 2^-e_sum
+  // the lowest, tiles of zeros aside (unsigned: those have the largest number)
+  uint32_t e_low = ~0u;
+  auto above_lowest = [](int e) { return static_cast<uint32_t>(e - kLowest); };
+  int zeros = 0, e_end = 0;          // positions in tiles of zeros; the unit at the end
   if (warp == 0) {
     // ---------------- own tiles ----------------
     if (lane == 0 && wait(&ctl.q_moved, 0)) {
@@ -1018,7 +1025,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       uint8_t* p_in = smem + Lay::p_in + b * kPStride;
       const int e_in = __ldcg(&ws.info[tile_base + tile0 + 2 * i + other].e);
       e_top = max(e_top, e_in);
-      e_low = min(e_low, e_in);
+      e_low = min(e_low, above_lowest(e_in));
       wait_warp(&ctl.pin_full[b], i / Lay::kBufs);
       if (tid == 4 * 32) tc::mbar_arrive_expect_tx(&ctl.pin_full[b], kPMsg);  // the buffer's next weights
       __syncwarp();
@@ -1067,7 +1074,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       const uint64_t seen64 = w.x & (nv >= kTile ? ~0ull : nv <= 0 ? 0ull : (1ull << nv) - 1ull);
       const uint32_t seen = static_cast<uint32_t>(seen64 >> (32 * hv)), poison = static_cast<uint32_t>(w.y >> (32 * hv));
       e_top = max(e_top, e);
-      e_low = min(e_low, e);
+      e_low = min(e_low, above_lowest(e));
       // (held inside fp32's range: a factor of 0 would turn an unseen position's -inf into NaN)
       const float kt = fminf(fmaxf(k2 * exp2i(e), 1.2e-38f), 3.0e38f);
       const float fe = static_cast<float>(e);
@@ -1137,11 +1144,14 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         }
       }
       // (the sum's unit follows the lowest exponent, so that it stays below 2^15 a position)
-      if (e < e_sum) {
-        l *= exp2i(max(e - e_sum, -126));
-        e_sum = e;
-      }
-      l = fmaf(sum, exp2i(max(e_sum - e, -126)), l);
+      // (as arithmetic: branches here took 2% of the whole; 0 times the sum keeps
+      // a poisonous position among zeros)
+      const int unit = e == kZeros ? e_sum : min(e_sum, e);
+      zeros += e == kZeros ? __popc(seen) : 0;
+      const float was = __uint_as_float(static_cast<uint32_t>(max(unit - e_sum, -126) + 127) << 23);
+      const float now = __uint_as_float(e == kZeros ? 0u : static_cast<uint32_t>(max(unit - e, -126) + 127) << 23);
+      l = fmaf(sum, now, l * was);
+      e_sum = unit;
       wait_warp(&ctl.p_empty[b], i / Lay::kBufs + 1);
       uint8_t* p_own = smem + Lay::p_own + b * kPStride;
 #pragma unroll
@@ -1161,7 +1171,13 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     // the last weights have been read, here and by the peer (whose word of it has then arrived)
     for (int i = max(0, n_own - Lay::kBufs); i < n_own; ++i) wait_warp(&ctl.p_empty[i % Lay::kBufs], i / Lay::kBufs);
     // ---- the row's sum over its two threads and both CTAs ----
-    ctl.part[0][hv][m] = l * exp2i(max(e_low - e_sum, -126));
+    // (rho and the lowest exponent are the same in both CTAs.  A row that sees zeros has a rho of -136 or
+    // more; where they outweigh the rest by far the unit makes room for them.)
+    e_end = e_low == ~0u ? kZeros : static_cast<int>(e_low) + kLowest;
+    if (rho > -140.f) e_end -= static_cast<int>(fminf(fmaxf(static_cast<float>(e_end) - rho - 64.f, 0.f), 100.f));
+    l *= exp2i(max(min(e_end - e_sum, 0), -126));
+    if (zeros) l = fmaf(static_cast<float>(zeros), exp2f(static_cast<float>(e_end) - rho), l);
+    ctl.part[0][hv][m] = l;
     asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
     l = ctl.part[0][0][m] + ctl.part[0][1][m];
     if (hv == 0) st_async_f32(dsmem_addr(&ctl.sent[m], peer), l, dsmem_addr(&ctl.fin_full, peer));
@@ -1180,8 +1196,8 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     const int hv = (warp - 4) >> 2, m = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int e_out = e_top;
-    // O / l is this times 2^e_out (O is in units of 1, l of 2^-e_low)
-    const float inv = (l > 0.f || l != l ? 1.f / l : 0.f) * exp2i(max(e_low - e_out, -126));
+    // O / l is this times 2^e_out (O is in units of 1, l of 2^-e_end)
+    const float inv = (l > 0.f || l != l ? 1.f / l : 0.f) * exp2i(min(max(e_end - e_out, -126), 127));
     const float up = ns == 1 ? exp2i(e_out) : 1.f;
     uint8_t* row = stage + m * kStagePitch;
 #pragma unroll 2
@@ -1202,8 +1218,8 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       }
     }
     if (c == 0 && hv == 0 && m < n_rows) {
-      if (ns > 1) ws.ml[(row0 + m) * ns + slot] = split_state(rho - static_cast<float>(e_low), l, e_out);
-      else if (a.out_lse) a.out_lse[row0 + m] = natural_lse(rho - static_cast<float>(e_low), l);
+      if (ns > 1) ws.ml[(row0 + m) * ns + slot] = split_state(rho - static_cast<float>(e_end), l, e_out);
+      else if (a.out_lse) a.out_lse[row0 + m] = natural_lse(rho - static_cast<float>(e_end), l);
     }
   }
   __syncthreads();
