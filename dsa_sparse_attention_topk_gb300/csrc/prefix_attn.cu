@@ -1356,12 +1356,6 @@ bool encode_rows(EncodeFn enc, CUtensorMap* map, CUtensorMapDataType type, const
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {
-  DevInfo di;
-  const char* why = nullptr;
-  return device_info(&di, &why) ? di.n_sm : 152;
-}
-
 }  // namespace
 
 size_t prefix_workspace_bytes(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx) {
