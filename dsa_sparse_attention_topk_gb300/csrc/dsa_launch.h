@@ -43,7 +43,7 @@ struct DevInfo {
   int n_sm = 0, smem_optin = 0;
 };
 bool device_info(DevInfo* out, const char** err);
-inline int sm_count() {  // (without a device a GB300's)
+inline int multiprocessors() {  // (without a device a GB300's)
   DevInfo di;
   const char* why = nullptr;
   return device_info(&di, &why) ? di.n_sm : 152;

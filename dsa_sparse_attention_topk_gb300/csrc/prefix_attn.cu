@@ -1359,17 +1359,17 @@ bool encode_rows(EncodeFn enc, CUtensorMap* map, CUtensorMapDataType type, const
 }  // namespace
 
 size_t prefix_workspace_bytes(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx) {
-  return make_plan(n_q, h_s, n_seq, prefix_len, max_ctx, sm_count()).bytes;
+  return make_plan(n_q, h_s, n_seq, prefix_len, max_ctx, multiprocessors()).bytes;
 }
 
 void prefix_plan_numbers(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, int32_t* out) {
-  const PrefixPlan p = make_plan(n_q, h_s, n_seq, prefix_len, max_ctx, sm_count());
+  const PrefixPlan p = make_plan(n_q, h_s, n_seq, prefix_len, max_ctx, multiprocessors());
   const int numbers[8] = {p.sp + p.st ? p.g : 0, p.tiles_p, p.sp, p.tail_lo, p.tiles_t, p.st, p.few, p.few_lo};
   std::copy(numbers, numbers + 8, out);
 }
 
 cudaError_t launch_prefix_attn(const PrefixArgs& a, cudaStream_t s, const char** err) {
-  const PrefixPlan pl = make_plan(a.n_q, a.h_s, a.n_seq, a.prefix_len, a.max_ctx, sm_count());
+  const PrefixPlan pl = make_plan(a.n_q, a.h_s, a.n_seq, a.prefix_len, a.max_ctx, multiprocessors());
   uint8_t* base = static_cast<uint8_t*>(a.workspace);
   PrefixWs ws{reinterpret_cast<__half*>(base), reinterpret_cast<TileInfo*>(base + pl.off_info),
               reinterpret_cast<__half*>(base + pl.off_o), reinterpret_cast<float4*>(base + pl.off_ml),

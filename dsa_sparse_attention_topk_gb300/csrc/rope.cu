@@ -331,7 +331,7 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
   // Several rows a thread once one row each would fill every SM (1842 x 16 x 192 bf16: 8.6 -> 6.7 us).
   // A single head with full vectors in the half layout has one, so that a block's tokens fit the
   // table (60000 x 1 x 192: 32 us with four, 21 with one).
-  const bool single = rows * g.slots < static_cast<int64_t>(sm_count()) * 2048 || (half && V == kMost && a.h == 1);
+  const bool single = rows * g.slots < static_cast<int64_t>(multiprocessors()) * 2048 || (half && V == kMost && a.h == 1);
   const int R = single ? 1 : !vec || V * sizeof(T) <= 4 ? 8 : 4;
   const dim3 grid(static_cast<unsigned>((rows + static_cast<int64_t>(groups) * R - 1) / (static_cast<int64_t>(groups) * R)),
                   static_cast<unsigned>((g.slots + g.slots_block - 1) / g.slots_block));
@@ -663,7 +663,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_rope_quant(const RopeQuantArgs& a, cudaStream_t s) {
-  const int cap = sm_count() * 16;
+  const int cap = multiprocessors() * 16;
   const int blocks = a.n_tokens / kWarpsPerBlock + (a.n_tokens % kWarpsPerBlock != 0);
   return launch_pdl(rope_quant_kernel, dim3(blocks < cap ? blocks : cap), dim3(kWarpsPerBlock * 32), 0, s, 1, a);
 }
