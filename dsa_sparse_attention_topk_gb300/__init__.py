@@ -31,6 +31,7 @@ import math
 import os
 
 import torch
+import torch.autograd.forward_ad as forward_ad
 
 from . import workloads  # noqa: F401  (seeded inputs; no computation of the method)
 
@@ -145,6 +146,16 @@ def _same_device(what, *tensors):
         if d != dev or d < 0:
             raise ValueError(f"{what}: tensors must be CUDA tensors on one device (got one on {t.device})")
     return dev
+
+
+def _need_no_grad(what, hint, *tensors):
+    """Refuse a tensor whose gradient (or tangent) is asked for: the result would come back without."""
+    grad, tangents = torch.is_grad_enabled(), getattr(forward_ad, "_current_level", -1) >= 0
+    if not (grad or tangents):
+        return
+    for t in tensors:
+        if t is not None and ((grad and t.requires_grad) or (tangents and forward_ad.unpack_dual(t).tangent is not None)):
+            raise ValueError(f"{what}: a tensor needs a gradient, which this call does not record ({hint})")
 
 
 def _need_shaped(t, dtype, shape, name):
@@ -289,7 +300,9 @@ def rope(x, pos, turns, offset=0, layout="interleaved", amplitude=1.0, transpose
     pos: int32 [n]; turns, amplitude: from rope_turns; layout: "interleaved" (pairs 2i, 2i+1)
     or "half" (pairs i, i + rot / 2).  transpose=True gives the gradient with respect to x,
     given that of the result.  out=x works in place (only the rotary part is touched);
-    otherwise out must not overlap x.  Returns out."""
+    otherwise out must not overlap x.  Tensors that need a gradient are refused: call it under
+    torch.no_grad(), or in the two halves of an autograd function.  Returns out."""
+    _need_no_grad("rope", "transpose=True gives it", x, out)
     shape, code = x.shape, _DTYPES.get(x.dtype)
     if len(shape) not in (2, 3) or code is None:
         raise ValueError("rope: x must be [n, d] or [n, h, d] of bf16, fp16 or fp32")
@@ -458,7 +471,9 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, page_table, seq_lens, q_s
     its own sequence's positions up to q_pos.  q: bf16 [n_q, h_s, 576]; page_table: int32
     [n_seq, max_pages] (entries before prefix_len / 64 are not read); seq_lens: int32 [n_seq],
     prefix included; q_seq, q_pos: int32 [n_q]; max_ctx: host-side bound of seq_lens.
-    Returns (out bf16 [n_q, h_s, 512], out_lse or None)."""
+    Tensors that need a gradient are refused (there is no backward pass).  Returns
+    (out bf16 [n_q, h_s, 512], out_lse or None)."""
+    _need_no_grad("prefix_attn", "there is no backward pass", q, out, out_lse)
     if q.dim() != 3 or q.shape[2] != LATENT_DIM:
         raise ValueError("prefix_attn: q must be [n_q, h_s, 576]")
     n_q, h_s, _ = q.shape
