@@ -149,6 +149,12 @@ int dsa_quant_kv(const void* k_bf16, const void* kv_bf16, const int64_t* slot_ma
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "quant_kv launch");
 }
 
+// n elements `stride` apart, none more than 2^40 elements behind the first
+static bool spans(int64_t stride, int32_t n) {
+  const int64_t most = int64_t{1} << 40;
+  return stride >= 0 && stride <= (n > 1 ? most / (n - 1) : most);
+}
+
 int dsa_rope(const void* x, void* out, int32_t dtype, int32_t n, int32_t h, int32_t d, int64_t x_stride_t,
              int64_t x_stride_h, int64_t out_stride_t, int64_t out_stride_h, const int32_t* pos,
              const int64_t* turns, int32_t rot, int32_t offset, int32_t layout, float amplitude,
@@ -169,11 +175,9 @@ int dsa_rope(const void* x, void* out, int32_t dtype, int32_t n, int32_t h, int3
   const size_t size = dtype == DSA_DTYPE_FP32 ? 4 : 2;
   if (!aligned(x, size) || !aligned(out, size) || !aligned(pos, 4) || !aligned(turns, 8))
     return fail(DSA_ERR_INVALID_ARG, "rope: a pointer is not aligned to its element");
-  // (strides below 2^40 elements keep every offset far from overflow)
-  const int64_t most = int64_t{1} << 40;
-  if (x_stride_t < 0 || x_stride_h < 0 || x_stride_t > most || x_stride_h > most || out_stride_t < 0 ||
-      out_stride_h < 0 || out_stride_t > most || out_stride_h > most)
-    return fail(DSA_ERR_INVALID_ARG, "rope: a stride is negative or above 2^40");
+  // (axes of up to 2^40 elements keep every offset far from overflow)
+  if (!spans(x_stride_t, n) || !spans(x_stride_h, h) || !spans(out_stride_t, n) || !spans(out_stride_h, h))
+    return fail(DSA_ERR_INVALID_ARG, "rope: a stride is negative, or an axis longer than 2^40 elements");
   // strides of an axis of length 1 are never used
   if (n == 1) x_stride_t = out_stride_t = 0;
   if (h == 1) x_stride_h = out_stride_h = 0;
@@ -207,10 +211,9 @@ int dsa_rope_quant_kv(const void* k_bf16, int64_t k_stride, const void* kv_bf16,
   if (!aligned(k_bf16, 8) || !aligned(kv_bf16, 8) || !aligned(k_cache, 16) || !aligned(kv_cache, 16) ||
       !aligned(slot_mapping, 8) || !aligned(turns, 8) || !aligned(pos, 4))
     return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: rows must be 8-byte and caches 16-byte aligned");
-  const int64_t most = int64_t{1} << 40;
-  if ((k_bf16 && (k_stride < 0 || k_stride > most || k_stride % 4)) ||
-      (kv_bf16 && (kv_stride < 0 || kv_stride > most || kv_stride % 4)))
-    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: row strides must be multiples of 4 elements");
+  if ((k_bf16 && (!spans(k_stride, n_tokens) || k_stride % 4)) ||
+      (kv_bf16 && (!spans(kv_stride, n_tokens) || kv_stride % 4)))
+    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: row strides must be multiples of 4 elements, all rows within 2^40");
   if (num_slots <= 0 || num_slots % DSA_PAGE_SIZE)
     return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: num_slots must be a positive multiple of 64");
   unsigned* st = status_ptr();

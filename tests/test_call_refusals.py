@@ -7,6 +7,8 @@ import torch
 import torch.autograd.forward_ad as forward_ad
 
 import dsa_sparse_attention_topk_gb300 as pkg
+from dsa_testlib import ensure_built
+from test_gpu_rope import _append_call, _rope_call
 
 SM = 1.0 / math.sqrt(192.0)
 
@@ -44,3 +46,17 @@ def test_a_gradient_is_not_lost_in_silence(name):
     for quiet in (torch.no_grad, torch.inference_mode):
         with quiet(), pytest.raises(ValueError, match="CUDA"):
             call(x)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(xt=1 << 40, n=3), dict(xh=1 << 40, ot=1 << 30), dict(n=1 << 24, h=1, xt=1 << 39, ot=64),
+    dict(n=1 << 24, h=1, xt=64, ot=1 << 39),
+    dict(n=2, h=1 << 24, xh=64, xt=1 << 30, oh=1 << 40, ot=64),      # (h - 1) oh wraps in 64 bits
+])
+def test_rope_refuses_axes_whose_offsets_overflow(kw):
+    assert _rope_call(ensure_built().lib(), **kw) == -1
+
+
+@pytest.mark.parametrize("kw", [dict(n=3, ks=1 << 40), dict(n=1 << 24, kvs=1 << 39), dict(n=1 << 30, ks=1 << 12)])
+def test_rope_quant_kv_refuses_rows_whose_offsets_overflow(kw):
+    assert _append_call(ensure_built().lib(), **kw) == -1
