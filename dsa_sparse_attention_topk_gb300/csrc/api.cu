@@ -458,6 +458,9 @@ int dsa_prefix_attn(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t*
     return fail(DSA_ERR_INVALID_ARG, "prefix_attn: null pointer");
   if (!aligned(q_bf16, 16) || !aligned(kv_cache, 16) || !aligned(out_bf16, 16))
     return fail(DSA_ERR_INVALID_ARG, "prefix_attn: q, kv_cache and out must be 16-byte aligned");
+  if (!aligned(prefix_pages, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(q_seq, 4) ||
+      !aligned(q_pos, 4) || !aligned(out_lse, 4))
+    return fail(DSA_ERR_INVALID_ARG, "prefix_attn: tables, lengths, rows and out_lse must be 4-byte aligned");
   const size_t need = dsa::prefix_workspace_bytes(n_q, h_s, n_seq, prefix_len, max_ctx);
   if (workspace_bytes < need || !aligned(workspace, 256))
     return fail(DSA_ERR_INVALID_ARG, "prefix_attn: workspace must be >= %zu bytes and 256-byte aligned", need);

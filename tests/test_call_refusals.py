@@ -1,5 +1,6 @@
 """What rope and prefix_attn refuse on the host."""
 
+import ctypes
 import math
 
 import pytest
@@ -60,3 +61,12 @@ def test_rope_refuses_axes_whose_offsets_overflow(kw):
 @pytest.mark.parametrize("kw", [dict(n=3, ks=1 << 40), dict(n=1 << 24, kvs=1 << 39), dict(n=1 << 30, ks=1 << 12)])
 def test_rope_quant_kv_refuses_rows_whose_offsets_overflow(kw):
     assert _append_call(ensure_built().lib(), **kw) == -1
+
+
+@pytest.mark.parametrize("which", ["pages", "table", "lens", "q_seq", "q_pos", "out_lse"])
+def test_prefix_attn_refuses_misaligned_tables(which):
+    names = ["q", "cache", "pages", "table", "lens", "q_seq", "q_pos", "out", "out_lse", "ws"]
+    p = {n: ctypes.c_void_p((i + 1) * 65536 + (2 if n == which else 0)) for i, n in enumerate(names)}
+    assert ensure_built().lib().dsa_prefix_attn(
+        p["q"], 2, 16, p["cache"], 8, p["pages"], 100, p["table"], 4, p["lens"], 2, p["q_seq"], p["q_pos"], 200,
+        ctypes.c_float(0.07), p["out"], p["out_lse"], p["ws"], 1 << 40, None) == -1
