@@ -508,12 +508,14 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, page_table, seq_lens, q_s
             with torch.cuda.device(dev):
                 need = size(n_q, h_s, n_seq, prefix_len, max_ctx)
         workspace = _scratch(stream, need, q.device)
+    elif not workspace.is_contiguous():  # (its elements might lie on one another)
+        raise ValueError("prefix_attn: workspace must be contiguous")
     _call_on(dev, stream, lib().dsa_prefix_attn, q.data_ptr(), n_q, h_s, kv_cache.data_ptr(),
              kv_cache.numel() // (PAGE_SIZE * KVCACHE_TOKEN_BYTES),
              None if prefix_pages is None else prefix_pages.data_ptr(), prefix_len,
              None if page_table is None else page_table.data_ptr(), max_pages, seq_lens.data_ptr(), n_seq,
              q_seq.data_ptr(), q_pos.data_ptr(), max_ctx, sm_scale, out.data_ptr(),
-             None if out_lse is None else out_lse.data_ptr(), workspace.data_ptr(), workspace.numel())
+             None if out_lse is None else out_lse.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     return out, out_lse
 
 

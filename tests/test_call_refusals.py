@@ -70,3 +70,27 @@ def test_prefix_attn_refuses_misaligned_tables(which):
     assert ensure_built().lib().dsa_prefix_attn(
         p["q"], 2, 16, p["cache"], 8, p["pages"], 100, p["table"], 4, p["lens"], 2, p["q_seq"], p["q_pos"], 200,
         ctypes.c_float(0.07), p["out"], p["out_lse"], p["ws"], 1 << 40, None) == -1
+
+
+class _Library:
+    """Records the workspace size that an entry point is given."""
+    given = []
+
+    def __getattr__(self, name):
+        return (lambda *a: 512) if name.endswith("_workspace_size") else (lambda *a: self.given.append(a[-2]) or 0)
+
+
+def test_a_workspace_is_measured_in_bytes_of_its_own(monkeypatch):
+    monkeypatch.setattr(pkg, "lib", _Library)
+    monkeypatch.setattr(pkg, "_same_device", lambda what, *t: 0)
+    monkeypatch.setattr(pkg, "_call_on", lambda dev, stream, fn, *a: fn(*a, None))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    q = torch.zeros(1, 16, 576, dtype=torch.bfloat16)
+    # 512 elements that are one byte
+    with pytest.raises(ValueError, match="workspace"):
+        _prefix(q, workspace=torch.zeros(1, dtype=torch.uint8).expand(512))
+    with pytest.raises(ValueError, match="workspace"):
+        _prefix(q, workspace=torch.zeros(2048, dtype=torch.uint8)[::2])
+    _prefix(q, workspace=torch.zeros(512, dtype=torch.uint8))
+    _prefix(q, workspace=torch.zeros(128))
+    assert _Library.given == [512, 512]
