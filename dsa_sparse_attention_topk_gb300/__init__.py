@@ -148,11 +148,15 @@ def _same_device(what, *tensors):
     return dev
 
 
+def _tangents():
+    """Whether a level of forward-mode differentiation is open."""
+    return getattr(forward_ad, "_current_level", -1) >= 0
+
+
 def _need_no_grad(what, hint, *tensors):
-    """Refuse a tensor whose gradient (or tangent) is asked for: the result would come back without."""
-    grad, tangents = torch.is_grad_enabled(), getattr(forward_ad, "_current_level", -1) >= 0
-    if not (grad or tangents):
-        return
+    """Refuse a tensor whose gradient (or tangent) is asked for: the result would come back without.
+    (Called where one may be: a small call is bound by this host code.)"""
+    grad, tangents = torch.is_grad_enabled(), _tangents()
     for t in tensors:
         if t is not None and ((grad and t.requires_grad) or (tangents and forward_ad.unpack_dual(t).tangent is not None)):
             raise ValueError(f"{what}: a tensor needs a gradient, which this call does not record ({hint})")
@@ -302,7 +306,8 @@ def rope(x, pos, turns, offset=0, layout="interleaved", amplitude=1.0, transpose
     given that of the result.  out=x works in place (only the rotary part is touched);
     otherwise out must not overlap x.  Tensors that need a gradient are refused: call it under
     torch.no_grad(), or in the two halves of an autograd function.  Returns out."""
-    _need_no_grad("rope", "transpose=True gives it", x, out)
+    if x.requires_grad or _tangents() or (out is not None and out.requires_grad):
+        _need_no_grad("rope", "transpose=True gives it", x, out)
     shape, code = x.shape, _DTYPES.get(x.dtype)
     if len(shape) not in (2, 3) or code is None:
         raise ValueError("rope: x must be [n, d] or [n, h, d] of bf16, fp16 or fp32")
@@ -473,7 +478,9 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, page_table, seq_lens, q_s
     prefix included; q_seq, q_pos: int32 [n_q]; max_ctx: host-side bound of seq_lens.
     Tensors that need a gradient are refused (there is no backward pass).  Returns
     (out bf16 [n_q, h_s, 512], out_lse or None)."""
-    _need_no_grad("prefix_attn", "there is no backward pass", q, out, out_lse)
+    if q.requires_grad or _tangents() or (out is not None and out.requires_grad) or (
+            out_lse is not None and out_lse.requires_grad):
+        _need_no_grad("prefix_attn", "there is no backward pass", q, out, out_lse)
     if q.dim() != 3 or q.shape[2] != LATENT_DIM:
         raise ValueError("prefix_attn: q must be [n_q, h_s, 576]")
     n_q, h_s, _ = q.shape
