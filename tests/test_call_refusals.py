@@ -94,3 +94,32 @@ def test_a_workspace_is_measured_in_bytes_of_its_own(monkeypatch):
     _prefix(q, workspace=torch.zeros(512, dtype=torch.uint8))
     _prefix(q, workspace=torch.zeros(128))
     assert _Library.given == [512, 512]
+
+
+class _Rotary(torch.autograd.Function):
+    """The two halves that the refusal points to."""
+
+    @staticmethod
+    def forward(ctx, x, pos, turns):
+        ctx.save_for_backward(pos, turns)
+        return pkg.rope(x, pos, turns)
+
+    @staticmethod
+    def backward(ctx, grad):
+        return pkg.rope(grad, *ctx.saved_tensors, transpose=True), None, None
+
+
+@pytest.mark.gpu
+def test_rope_in_the_halves_of_an_autograd_function():
+    ensure_built()
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(5, 3, 64, generator=g).cuda().requires_grad_()
+    w = torch.randn(5, 3, 64, generator=g).cuda()
+    pos = torch.arange(5, dtype=torch.int32).cuda() * 1000
+    turns, _ = pkg.rope_turns(64)
+    (_Rotary.apply(x, pos, turns) * w).sum().backward()
+    assert torch.equal(x.grad, pkg.rope(w, pos, turns, transpose=True))
+    # a rotation keeps the product of two tensors turned alike: each of 64 terms off by 4e-7 of some units
+    with torch.no_grad():
+        same = (pkg.rope(x, pos, turns) * pkg.rope(w, pos, turns)).sum(-1) - (x * w).sum(-1)
+    assert float(same.abs().max()) < 64 * 4e-7 * 16

@@ -134,3 +134,37 @@ def test_memory_taken_right_after_a_call_on_another_stream(h):
         assert all(bool((t == 0xFF).all()) for t in taken)
         assert torch.equal(got, want)
     assert dsa.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_a_captured_call_on_a_stream_forked_from_the_capture():
+    dsa = ensure_built()
+    g = torch.Generator().manual_seed(3)
+    cache = dsa.alloc_kv_cache(40)
+    dsa.quant_kv_fp8(torch.randn(40 * 64, 576, generator=g).to(torch.bfloat16).cuda(), torch.arange(40 * 64).cuda(), cache)
+    table = torch.arange(40, dtype=torch.int32).view(2, 20).cuda()
+    q = torch.randn(2, 64, 576, generator=g).to(torch.bfloat16).cuda()
+    lens = torch.full((2,), 1200, dtype=torch.int32).cuda()
+    pos = torch.arange(2, dtype=torch.int32).cuda()
+    turns, _ = dsa.rope_turns(64)
+
+    def step(stream):
+        turned = dsa.rope(q, pos, turns, offset=512, stream=stream)
+        return dsa.prefix_attn(turned, cache, None, 0, table, lens, pos, lens - 1, 1280, SM, stream=stream)[0]
+
+    want = step(None)
+    torch.cuda.synchronize()
+    main, fork = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main, capture_error_mode="relaxed"):
+        fork.wait_stream(main)
+        got = step(fork)
+        main.wait_stream(fork)
+        same = got + 0
+        del got
+    for _ in range(3):
+        same.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(same, want)
+    assert dsa.device_status() == 0
