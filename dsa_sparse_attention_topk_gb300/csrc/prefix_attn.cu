@@ -39,9 +39,9 @@
 // sink, often with next to nothing in its value) then keeps 2^14 and leaves the others their bits;
 // without one, later tiles may grow by 12 powers of two before rho changes.  CTA 0 sends the first
 // rho to CTA 1; the sum of 2^(x - rho) is kept in fp32 from the unrounded weights, in units of
-// 2^-e of the lowest e so far (in units of 1, values of 2^-106 would take it past 2^127).  A tile of
-// zeros has the lowest exponent of all, so that it sets no reference above the others' weights;
-// its positions, logit 0, are counted, and join the sum at the end.  Where a tile's
+// 2^-e of the item's first tile (in units of 1, values of 2^-106 would take it past 2^127).  A tile of
+// zeros may have any exponent and takes that one too, so that it sets no reference far from the
+// others' weights.  Where a tile's
 // largest weight would pass 2^15 its owner raises rho, to 5 below the largest so far, for all
 // rows of the warp that this would raise (waiting for the products is the cost, and the rows
 // share it), and rescales its accumulator; the references travel with the weights, and the
@@ -879,11 +879,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 
   // softmax threads: their row's state, kept from the loop to the output
   float rho = -INFINITY, top = -INFINITY, l = 0.f;
-  int e_top = kZeros, e_sum = 1000;  // largest exponent of the tiles; l is in units of 2^-e_sum
-  // the lowest, tiles of zeros aside (unsigned: those have the largest number)
-  uint32_t e_low = ~0u;
-  auto above_lowest = [](int e) { return static_cast<uint32_t>(e - kLowest); };
-  int zeros = 0, e_end = 0;          // positions in tiles of zeros; the unit at the end
+  int e_top = kZeros, e_unit = 0;  // largest exponent of the tiles; l is in units of 2^-e_unit
   if (warp == 0) {
     // ---------------- own tiles ----------------
     if (lane == 0 && wait(&ctl.q_moved, 0)) {
@@ -1015,6 +1011,16 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       }
       tc::tmem_wait_st();
     };
+    // the exponent of the item's first tile that is not of zeros alone
+#pragma unroll 1
+    for (int base = 0; base < nt; base += 32) {
+      const int e = base + lane < nt ? __ldcg(&ws.info[tile_base + tile0 + base + lane].e) : kZeros;
+      const unsigned some = __ballot_sync(0xffffffffu, e != kZeros);
+      if (some) {
+        e_unit = __shfl_sync(0xffffffffu, e, __ffs(some) - 1);
+        break;
+      }
+    }
     if (c == 1) {
       wait_warp(&ctl.r_full, 0);
       rho = ctl.sent[m];
@@ -1024,8 +1030,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       const int b = i % Lay::kBufs;
       uint8_t* p_in = smem + Lay::p_in + b * kPStride;
       const int e_in = __ldcg(&ws.info[tile_base + tile0 + 2 * i + other].e);
-      e_top = max(e_top, e_in);
-      e_low = min(e_low, above_lowest(e_in));
+      e_top = max(e_top, e_in == kZeros ? e_unit : e_in);
       wait_warp(&ctl.pin_full[b], i / Lay::kBufs);
       if (tid == 4 * 32) tc::mbar_arrive_expect_tx(&ctl.pin_full[b], kPMsg);  // the buffer's next weights
       __syncwarp();
@@ -1069,12 +1074,11 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       const int tile = tile0 + 2 * i + c;
       const TileInfo* info = ws.info + tile_base + tile;
       const ulonglong2 w = __ldcg(reinterpret_cast<const ulonglong2*>(info));
-      const int e = __ldcg(&info->e);
+      const int e_tile = __ldcg(&info->e), e = e_tile == kZeros ? e_unit : e_tile;
       const int nv = lim - tile * kTile;
       const uint64_t seen64 = w.x & (nv >= kTile ? ~0ull : nv <= 0 ? 0ull : (1ull << nv) - 1ull);
       const uint32_t seen = static_cast<uint32_t>(seen64 >> (32 * hv)), poison = static_cast<uint32_t>(w.y >> (32 * hv));
       e_top = max(e_top, e);
-      e_low = min(e_low, above_lowest(e));
       // (held inside fp32's range: a factor of 0 would turn an unseen position's -inf into NaN)
       const float kt = fminf(fmaxf(k2 * exp2i(e), 1.2e-38f), 3.0e38f);
       const float fe = static_cast<float>(e);
@@ -1143,15 +1147,7 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
           }
         }
       }
-      // (the sum's unit follows the lowest exponent, so that it stays below 2^15 a position)
-      // (as arithmetic: branches here took 2% of the whole; 0 times the sum keeps
-      // a poisonous position among zeros)
-      const int unit = e == kZeros ? e_sum : min(e_sum, e);
-      zeros += e == kZeros ? __popc(seen) : 0;
-      const float was = __uint_as_float(static_cast<uint32_t>(max(unit - e_sum, -126) + 127) << 23);
-      const float now = __uint_as_float(e == kZeros ? 0u : static_cast<uint32_t>(max(unit - e, -126) + 127) << 23);
-      l = fmaf(sum, now, l * was);
-      e_sum = unit;
+      l = fmaf(sum, exp2i(min(max(e_unit - e, -126), 127)), l);
       wait_warp(&ctl.p_empty[b], i / Lay::kBufs + 1);
       uint8_t* p_own = smem + Lay::p_own + b * kPStride;
 #pragma unroll
@@ -1171,12 +1167,6 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     // the last weights have been read, here and by the peer (whose word of it has then arrived)
     for (int i = max(0, n_own - Lay::kBufs); i < n_own; ++i) wait_warp(&ctl.p_empty[i % Lay::kBufs], i / Lay::kBufs);
     // ---- the row's sum over its two threads and both CTAs ----
-    // (rho and the lowest exponent are the same in both CTAs.  A row that sees zeros has a rho of -136 or
-    // more; where they outweigh the rest by far the unit makes room for them.)
-    e_end = e_low == ~0u ? kZeros : static_cast<int>(e_low) + kLowest;
-    if (rho > -140.f) e_end -= static_cast<int>(fminf(fmaxf(static_cast<float>(e_end) - rho - 64.f, 0.f), 100.f));
-    l *= exp2i(max(min(e_end - e_sum, 0), -126));
-    if (zeros) l = fmaf(static_cast<float>(zeros), exp2f(static_cast<float>(e_end) - rho), l);
     ctl.part[0][hv][m] = l;
     asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
     l = ctl.part[0][0][m] + ctl.part[0][1][m];
@@ -1196,8 +1186,8 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     const int hv = (warp - 4) >> 2, m = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int e_out = e_top;
-    // O / l is this times 2^e_out (O is in units of 1, l of 2^-e_end)
-    const float inv = (l > 0.f || l != l ? 1.f / l : 0.f) * exp2i(min(max(e_end - e_out, -126), 127));
+    // O / l is this times 2^e_out (O is in units of 1, l of 2^-e_unit)
+    const float inv = (l > 0.f || l != l ? 1.f / l : 0.f) * exp2i(max(e_unit - e_out, -126));
     const float up = ns == 1 ? exp2i(e_out) : 1.f;
     uint8_t* row = stage + m * kStagePitch;
 #pragma unroll 2
@@ -1218,8 +1208,8 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       }
     }
     if (c == 0 && hv == 0 && m < n_rows) {
-      if (ns > 1) ws.ml[(row0 + m) * ns + slot] = split_state(rho - static_cast<float>(e_end), l, e_out);
-      else if (a.out_lse) a.out_lse[row0 + m] = natural_lse(rho - static_cast<float>(e_end), l);
+      if (ns > 1) ws.ml[(row0 + m) * ns + slot] = split_state(rho - static_cast<float>(e_unit), l, e_out);
+      else if (a.out_lse) a.out_lse[row0 + m] = natural_lse(rho - static_cast<float>(e_unit), l);
     }
   }
   __syncthreads();
