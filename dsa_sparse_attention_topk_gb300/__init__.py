@@ -259,7 +259,8 @@ def rope_turns(rot, base=10000.0, scaling=None, factor=1.0, original_len=4096, b
     * "ntk"     base * factor^(rot / (rot - 2)): the lowest frequency is divided by factor;
     * "yarn"    by parts: a frequency that makes beta_fast turns or more in original_len
                 positions stays, one that makes beta_slow or fewer is divided by factor, a
-                linear ramp over the index in between; amplitude 0.1 ln(factor) + 1.
+                linear ramp over the index in between; amplitude 0.1 ln(factor) + 1.  A model that
+                has this factor in its softmax scale already takes 1.0 in the amplitude's place.
     """
     if rot < 2 or rot % 2:
         raise ValueError(f"rope_turns: rot must be even and at least 2 (got {rot})")

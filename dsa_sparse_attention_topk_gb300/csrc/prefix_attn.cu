@@ -65,7 +65,7 @@
 // as fp16 pairs in 320..511; shared memory as in Layout below.
 // The query is scaled to fp16 by a power of two per row (exact: bf16 has 8 bits).
 //
-// Measured (128 heads): 32 rows behind 32K positions 201 us, of it 8 us expand, some 11 us before an
+// Measured (128 heads): 32 rows behind 32K positions 202 us, of it 8 us expand, some 11 us before an
 // item's first and behind its last product, and 2400 cycles a step of two tiles against
 // the products' 2270; 512 causal rows behind 16K 1.50 ms, 82% of the cuBLAS bf16 rate.
 
@@ -198,7 +198,8 @@ struct PrefixWs {
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // The tensor-memory path's plan of least estimated time: MMAs of one CTA (128 rows an item, two
-// CTAs) or of CTA pairs (256 rows, four CTAs), and the splits.  An item of n tiles takes about
+// CTAs) or of CTA pairs (256 rows, four CTAs), and the splits: of the prefix up to 64 and of a tail up
+// to 16, in powers of two, which bounds the search and the merge (more were not measured).  An item of n tiles takes about
 // 9 + 1.33 n us with one CTA per parity and 11 + 0.62 n us with pairs, on one of the clusters that
 // fit at once.  A tail's item holds as many adjacent rows of its sequence as fit; the rows are
 // counted as if spread evenly over the sequences.  Returns the us.

@@ -16,7 +16,7 @@ class DsaDecodeLayer:
     Top-K, then sparse attention over the selected entries.
 
     rope  None: queries, keys and latent rows come with their positions already in them.
-          (turns, amplitude) of rope_turns(64): they come without, and every call turns them:
+          (turns, amplitude), as rope_turns(64) returns them: they come without, and every call turns them:
           the 64 dims from index_offset of indexer queries and keys in index_layout, the last
           64 of attention queries and latent rows in latent_layout.
     """

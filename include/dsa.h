@@ -336,7 +336,10 @@ int dsa_sparse_attn_noalloc(const void* q_bf16, int32_t n_q, int32_t h_s, const 
  * bits for whatever lies within 2^-29 of the largest, and so are the softmax weights: 11 bits down
  * to 2^-17 of the row's largest, or to 2^-28 as far as that stands out of the 64 positions that the
  * row (or a part of it that was worked on apart) begins with; below that in steps of 2^-10 of the
- * bound.  Sums are fp32.
+ * bound.  A weight counts here times the power of two of its position's values.  Where a row is
+ * worked on in parts, each part's result is held in fp16 in units that its largest value fills.
+ * Sums are fp32, and hold as long as the largest scales of any two runs of 64 positions lie
+ * within a factor of 2^90 (zeros aside).
  * With up to 32 heads, where no more memory is read for it, the codes are used as they are and
  * their scales stay in fp32: there the weights times the scales are held in fp16.
  *   q_bf16        [n_q][h_s][576] bfloat16, 16-byte aligned; h_s 1..128.
