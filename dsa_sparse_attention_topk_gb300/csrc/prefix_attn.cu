@@ -41,14 +41,13 @@
 // rho to CTA 1; the sum of 2^(x - rho) is kept in fp32 from the unrounded weights, in units of
 // 2^-e of the item's first tile (in units of 1, values of 2^-106 would take it past 2^127).  A tile of
 // zeros may have any exponent and takes that one too, so that it sets no reference far from the
-// others' weights.  Where a tile's
-// largest weight would pass 2^15 its owner raises rho, to 5 below the largest so far, for all
-// rows of the warp that this would raise (waiting for the products is the cost, and the rows
-// share it), and rescales its accumulator; the references travel with the weights, and the
-// receiving CTA raises its own (rescaling its accumulator) or, where it has itself gone
-// ahead, scales the received row down.  After each tile in the order above both CTAs hold the
-// largest reference used so far, so the results do not depend on timing.
-// Measured, 32 rows behind 32K, logits of a spread of 2.5, 4, 6 and 10 powers of two: 201, 204, 216
+// others' weights.  Where a tile's largest weight would pass 2^15 its owner raises rho, to 5 below
+// the largest behind the first tile, for all rows of the warp that this would raise (waiting for
+// the products is the cost, and the rows share it), and rescales its accumulator; the references
+// travel with the weights, and the receiving CTA raises its own (rescaling its accumulator) or,
+// where it has itself gone ahead, scales the received row down.  After each tile in the order
+// above both CTAs hold the largest reference used so far, so the results do not depend on timing.
+// Measured, 32 rows behind 32K, logits of a spread of 2.5, 4, 6 and 10 powers of two: 202, 204, 216
 // and 240 us; raising single rows 238 at a spread of 6; 11 below instead of 5: 259 there, 0: 209;
 // rho 10 below the first largest whatever its tile looks like: 288 at 2.5.
 //
@@ -199,9 +198,9 @@ size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // The tensor-memory path's plan of least estimated time: MMAs of one CTA (128 rows an item, two
 // CTAs) or of CTA pairs (256 rows, four CTAs), and the splits: of the prefix up to 64 and of a tail up
-// to 16, in powers of two, which bounds the search and the merge (more were not measured).  An item of n tiles takes about
-// 9 + 1.33 n us with one CTA per parity and 11 + 0.62 n us with pairs, on one of the clusters that
-// fit at once.  A tail's item holds as many adjacent rows of its sequence as fit; the rows are
+// to 16, in powers of two, which bounds the search and the merge (more were not measured).  An item
+// of n tiles takes about 9 + 1.33 n us with one CTA per parity and 11 + 0.62 n us with pairs, on one
+// of the clusters that fit at once.  A tail's item holds as many adjacent rows of its sequence as fit; the rows are
 // counted as if spread evenly over the sequences.  Returns the us.
 double plan_tiles(PrefixPlan& p, int n_q, int n_sm) {
   double best = 1e30;
@@ -1112,8 +1111,8 @@ attend_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         if (hv == 0) st_async_f32(dsmem_addr(&ctl.sent[m], peer), rho, dsmem_addr(&ctl.r_full, peer));
       }
       // the reference these weights are made with: the row's, or a new one where a weight of this warp
-      // would pass 2^15 or is a row's first
-      top = fmaxf(top, mt);
+      // would pass 2^15 or is a row's first (a row that stands behind its first tile's largest stays there)
+      if (i > 0 || c > 0) top = fmaxf(top, mt);
       const bool raise = mt > rho + kHeadroom || (rho == -INFINITY && mt > -INFINITY);
       const float rho_p = __any_sync(0xffffffffu, raise) ? fmaxf(rho, top - kRaised) : rho;
       const float off = fe - (rho_p == -INFINITY ? 0.f : rho_p);

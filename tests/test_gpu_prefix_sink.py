@@ -63,3 +63,42 @@ def test_the_rest_behind_a_sink(dsa, shape, at, gaps):
         ref = w @ kv[:, :512] / w.sum(1, keepdims=True)
         d = np.abs(x).max() * 576 * 2.0 ** -24
         assert np.abs(o[t] / ref - 1).max() <= 2.0 ** -8 + 2.0 ** -10 + 2 * d + 2.0 ** -20
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", sorted(SHAPES))
+def test_a_sinks_row_beside_rows_whose_logits_rise(dsa, shape):
+    # even heads: a sink at position 0; odd heads, in the same warps: logits that rise from tile to tile
+    # and raise their references again and again
+    n, h, lens, prefix, max_ctx, plan = SHAPES[shape]
+    got = dsa.test_prefix_plan(n, h, len(lens), prefix, max_ctx)
+    assert all(got[k] == v for k, v in plan.items())
+    rows = [(i * len(lens) // n, lens[i * len(lens) // n] - 1 - i % 5) for i in range(n)]
+    b = Batch(dsa, lens, prefix, h, rows=rows, seed=5, max_ctx=max_ctx)
+    vals = torch.randn(b.num_pages * 64, 576, generator=torch.Generator().manual_seed(6)).abs() + 0.25
+    vals[:, 512:] = 0
+    for s in range(len(lens)):
+        p = torch.arange(max_ctx)
+        pages = torch.where(p < prefix, torch.cat([b.pages, b.pages.new_zeros(1)])[(p // 64).clamp(max=len(b.pages))],
+                            b.table[s][p // 64]).long()
+        vals[pages * 64 + p % 64, 513] = (p // 64).float()
+        vals[pages[0] * 64, :512], vals[pages[0] * 64, 512] = 0, 1.0
+    dsa.quant_kv_fp8(vals.to(torch.bfloat16).cuda(), torch.arange(b.num_pages * 64).cuda(), b.cache)
+    b.q[:] = 0
+    b.q[:, ::2, 512] = (torch.tensor([20.6, 24.6])[torch.arange(n * ((h + 1) // 2)) % 2].view(n, -1) / POWERS).to(torch.bfloat16)
+    b.q[:, 1::2, 513] = 17.0 / POWERS
+    out, lse = b.call(dsa)
+    assert dsa.device_status() == 0
+    rec = b.cache.cpu().numpy().reshape(-1, 608)
+    for t in {0, n // 2, n - 1}:
+        s, seen = int(b.q_seq[t]), np.arange(int(b.q_pos[t]) + 1)
+        pages = np.where(seen < prefix, np.r_[b.pages.numpy(), 0][np.minimum(seen // 64, len(b.pages))],
+                         b.table.numpy()[s][seen // 64])
+        r = rec[pages.astype(np.int64) * 64 + seen % 64]
+        kv = round11(oracle.fp8_tile_dequantize(r[:, :576], r[:, 576:596].copy().view(np.float32)))
+        x = SM * (b.q[t].double().numpy() @ kv.T)
+        w = np.exp(x - x.max(1, keepdims=True))
+        ref = w @ kv[:, :512] / w.sum(1, keepdims=True)
+        d = np.abs(x).max(1, keepdims=True) * 576 * 2.0 ** -24
+        bound = 2.0 ** -8 + 2.0 ** -10 + 2 * d + 2.0 ** -20
+        assert np.all(np.abs(out[t].double().cpu().numpy() / ref - 1) <= bound), t
