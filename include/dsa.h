@@ -146,7 +146,8 @@ enum { DSA_DTYPE_BF16 = 0, DSA_DTYPE_FP16 = 1, DSA_DTYPE_FP32 = 2 };
  *              the rotary part; otherwise out gets the whole heads (the rest copied) and must
  *              not overlap x.  No two elements of out may share memory: its strides must
  *              nest (stride_h >= d and stride_t >= (h - 1) stride_h + d, or the other way
- *              round).  Strides of x may be 0 (broadcast) out of place.
+ *              round).  Strides of x may be 0 (broadcast) out of place.  No axis may be longer
+ *              than 2^40 elements.
  *   pos        [n] int32.
  *   turns      [rot / 2] int64, see above.
  *   rot        rotary dims, even, 2..d; they are dims [offset, offset + rot) of a head.
@@ -338,8 +339,8 @@ int dsa_sparse_attn_noalloc(const void* q_bf16, int32_t n_q, int32_t h_s, const 
  * row (or a part of it that was worked on apart) begins with; below that in steps of 2^-10 of the
  * bound.  A weight counts here times the power of two of its position's values.  Where a row is
  * worked on in parts, each part's result is held in fp16 in units that its largest value fills.
- * Sums are fp32, and hold as long as the largest scales of any two runs of 64 positions lie
- * within a factor of 2^90 (zeros aside).
+ * Sums are fp32; on the tensor cores they hold as long as the largest scales of any two runs of 64
+ * positions lie within a factor of 2^90 (zeros aside).
  * With up to 32 heads, where no more memory is read for it, the codes are used as they are and
  * their scales stay in fp32: there the weights times the scales are held in fp16.
  *   q_bf16        [n_q][h_s][576] bfloat16, 16-byte aligned; h_s 1..128.
