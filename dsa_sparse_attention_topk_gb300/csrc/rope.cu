@@ -45,10 +45,12 @@ __device__ __forceinline__ CosSin phase_cs(int pos, int64_t turns, float amp) {
   const uint64_t p = static_cast<uint64_t>(static_cast<int64_t>(pos)) * static_cast<uint64_t>(turns);
   const uint64_t near = p + (1ull << 61);  // + an eighth of a turn: the nearest quarter is the top two bits
   const uint32_t quarter = static_cast<uint32_t>(near >> 62);
-  // the rest, in 2^-33 turns: |rest| <= 2^30
-  const int rest = static_cast<int>(static_cast<int64_t>(p - (static_cast<uint64_t>(quarter) << 62)) >> 31);
+  // the rest, in 2^-33 turns: |rest| <= 2^30, and what it leaves (of a small angle most of it)
+  const int64_t rest64 = static_cast<int64_t>(p - (static_cast<uint64_t>(quarter) << 62));
+  const int rest = static_cast<int>(rest64 >> 31);
   const float rh = static_cast<float>(rest);
-  const float rl = static_cast<float>(rest - static_cast<int>(rh));
+  const float rl = fmaf(static_cast<float>(static_cast<uint32_t>(rest64) & 0x7FFFFFFFu), 4.656612873077393e-10f,
+                        static_cast<float>(rest - static_cast<int>(rh)));
   constexpr double kRad = 6.283185307179586476925 / 8589934592.0;  // 2 pi 2^-33
   constexpr float kHi = static_cast<float>(kRad);
   constexpr float kLo = static_cast<float>(kRad - static_cast<double>(kHi));
