@@ -13,8 +13,8 @@
 // a turn; the rest becomes radians as an unevaluated sum hi + lo of two floats, and the
 // Taylor polynomials of sine and cosine (to degree 11 and 10: the first terms left out are
 // below 7e-12 and 1.2e-10) are summed so that each result is again hi + lo, good to about
-// 2^-27.  dsa_rope uses the sum rounded to fp32; the writers, whose results are cut to four
-// bits and must land on the right side of a border, keep the low parts.
+// 2^-27, and rounded once.  The writers, whose results are cut to four bits and must land on the
+// right side of a border, do again what that does not decide, in pairs of floats throughout.
 //
 // Both kernels are bound by memory: a rotation is 3 multiply-adds per pair.
 
@@ -35,18 +35,19 @@ __device__ __forceinline__ Two two_sum_ordered(float a, float b) {  // |a| >= |b
   const float h = a + b;
   return {h, (a - h) + b};
 }
-struct CosSin {
-  Two c, s;
-};
-
-// cos and sin (times the amplitude) of position p at a frequency of `turns` 2^-64 turns per
-// position
-__device__ __forceinline__ CosSin phase_cs(int pos, int64_t turns, float amp) {
+// position p at a frequency of `turns` 2^-64 turns per position: the nearest quarter turn, and the
+// rest, at most an eighth of a turn, in 2^-64 turns
+__device__ __forceinline__ int64_t phase_rest(int pos, int64_t turns, uint32_t& quarter) {
   const uint64_t p = static_cast<uint64_t>(static_cast<int64_t>(pos)) * static_cast<uint64_t>(turns);
-  const uint64_t near = p + (1ull << 61);  // + an eighth of a turn: the nearest quarter is the top two bits
-  const uint32_t quarter = static_cast<uint32_t>(near >> 62);
+  quarter = static_cast<uint32_t>((p + (1ull << 61)) >> 62);
+  return static_cast<int64_t>(p - (static_cast<uint64_t>(quarter) << 62));
+}
+
+// cos and sin, times the amplitude
+__device__ __forceinline__ float2 phase_cs(int pos, int64_t turns, float amp) {
+  uint32_t quarter;
+  const int64_t rest64 = phase_rest(pos, turns, quarter);
   // the rest, in 2^-33 turns: |rest| <= 2^30, and what it leaves (of a small angle most of it)
-  const int64_t rest64 = static_cast<int64_t>(p - (static_cast<uint64_t>(quarter) << 62));
   const int rest = static_cast<int>(rest64 >> 31);
   const float rh = static_cast<float>(rest);
   const float rl = fmaf(static_cast<float>(static_cast<uint32_t>(rest64) & 0x7FFFFFFFu), 4.656612873077393e-10f,
@@ -73,14 +74,9 @@ __device__ __forceinline__ CosSin phase_cs(int pos, int64_t turns, float amp) {
   const bool swap = quarter & 1u;
   Two c = swap ? sn : cn, s = swap ? cn : sn;
   const float cf = ((quarter + 1u) & 2u) ? -amp : amp, sf = (quarter & 2u) ? -amp : amp;
-  CosSin r;
-  r.c.hi = c.hi * cf;
-  r.c.lo = fmaf(c.hi, cf, -r.c.hi) + c.lo * cf;
-  r.s.hi = s.hi * sf;
-  r.s.lo = fmaf(s.hi, sf, -r.s.hi) + s.lo * sf;
-  return r;
+  const float ch = c.hi * cf, sh = s.hi * sf;
+  return make_float2(ch + (fmaf(c.hi, cf, -ch) + c.lo * cf), sh + (fmaf(s.hi, sf, -sh) + s.lo * sf));
 }
-__device__ __forceinline__ float2 rounded(const CosSin& v) { return make_float2(v.c.hi + v.c.lo, v.s.hi + v.s.lo); }
 
 template <typename T> struct Elem;
 template <> struct Elem<__nv_bfloat16> {
@@ -127,7 +123,7 @@ struct Table {
   __device__ __forceinline__ float2 at(int t, int i) const { return cs[(t - first) * half + i]; }
 };
 __device__ __forceinline__ float2 pair_cs(const RopeArgs& a, int t, int i) {
-  float2 cs = rounded(phase_cs(a.pos[t], a.turns[i], a.amplitude));
+  float2 cs = phase_cs(a.pos[t], a.turns[i], a.amplitude);
   if (a.transpose) cs.y = -cs.y;
   return cs;
 }
@@ -351,10 +347,57 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
 // ---- the cache writers with the rotation on the way ---------------------------------
 // One warp per token, as in the plain writers: lane i computes the sine and cosine of
 // frequency i of the token's position, and the lanes that hold a pair's values fetch them
-// by shuffle.  The turned values are quantised from hi + lo, never rounded to bf16 or to
-// fp32 in between: each code is the nearest of the turned value to about 2^-27.
+// by shuffle.  The turned values are not rounded to bf16 in between: each code is the nearest of
+// the turned value, known to 2^-41 of its pair's size (times the amplitude in fp32).
 constexpr int kWarpsPerBlock = 8;
 constexpr int kRot = 64;
+
+// Sums and products of such pairs of floats (Dekker, "A floating-point technique for extending the
+// available precision", 1971; Knuth's two-sum), good to some 2^-46.
+__device__ __forceinline__ Two mul(const Two& a, const Two& b) {
+  const float p = a.hi * b.hi;
+  return two_sum_ordered(p, fmaf(a.hi, b.hi, -p) + fmaf(a.hi, b.lo, a.lo * b.hi));
+}
+__device__ __forceinline__ Two add(const Two& a, const Two& b) {  // |a| >= |b|
+  const Two s = two_sum_ordered(a.hi, b.hi);
+  return two_sum_ordered(s.hi, s.lo + (a.lo + b.lo));
+}
+struct CosSin {
+  Two c, s;
+};
+// phase_cs to 2^-41: the terms down to x^7 and x^6 in pairs of floats, those behind them (below 4e-7 and
+// 4e-6 together, to x^15 and x^14) in floats.  Out of line, for one token in some 10^4.
+__device__ __noinline__ CosSin phase_two(int pos, int64_t turns, float amp) {
+  uint32_t quarter;
+  const int64_t rest = phase_rest(pos, turns, quarter);
+  const float rh = static_cast<float>(rest);
+  constexpr double kRad = 6.283185307179586476925 / 18446744073709551616.0;  // 2 pi 2^-64
+  constexpr float kHi = static_cast<float>(kRad);
+  const Two x = mul({rh, static_cast<float>(rest - static_cast<int64_t>(rh))}, {kHi, static_cast<float>(kRad - static_cast<double>(kHi))});
+  const Two z = mul(x, x);
+  auto fraction = [](int n) {  // 1 / n
+    const float h = static_cast<float>(1.0 / n);
+    return Two{h, static_cast<float>(1.0 / n - static_cast<double>(h))};
+  };
+  float S = -1.0f / 1307674368000.0f, C = -1.0f / 87178291200.0f;
+  S = fmaf(S, z.hi, 1.0f / 6227020800.0f);
+  S = fmaf(S, z.hi, -1.0f / 39916800.0f);
+  S = fmaf(S, z.hi, 1.0f / 362880.0f);
+  C = fmaf(C, z.hi, 1.0f / 479001600.0f);
+  C = fmaf(C, z.hi, -1.0f / 3628800.0f);
+  C = fmaf(C, z.hi, 1.0f / 40320.0f);
+  Two sn = add(fraction(-5040), {S * z.hi, 0.f}), cn = add(fraction(-720), {C * z.hi, 0.f});
+  sn = add(fraction(120), mul(sn, z));
+  sn = add(fraction(-6), mul(sn, z));
+  sn = add(x, mul(mul(x, z), sn));
+  cn = add(fraction(24), mul(cn, z));
+  cn = add({-0.5f, 0.f}, mul(cn, z));
+  cn = add({1.0f, 0.f}, mul(cn, z));
+  // a quarter turn: (c, s) -> (-s, c)
+  const bool swap = quarter & 1u;
+  const Two c = swap ? sn : cn, s = swap ? cn : sn;
+  return {mul(c, {((quarter + 1u) & 2u) ? -amp : amp, 0.f}), mul(s, {(quarter & 2u) ? -amp : amp, 0.f})};
+}
 
 // a c + b s as hi + lo (a, b exact inputs); an infinity or NaN has no low part
 __device__ __forceinline__ Two dot2(float a, const Two& c, float b, const Two& s) {
@@ -454,11 +497,11 @@ constexpr float kTurnErr = 2.384185791015625e-07f;
 // One token's key.  The fp32 rotation decides every code and exponent that is the same at
 // both ends of its error interval; a token with any other (one in some 10^4) is done again
 // from hi + lo.
-__device__ __forceinline__ void turn_store_k(uint2 raw, const CosSin& cs, const RopeQuantArgs& a, int64_t slot) {
+__device__ __forceinline__ void turn_store_k(uint2 raw, float2 cr, int pos, int64_t turns, const RopeQuantArgs& a,
+                                             int64_t slot) {
   const int lane = threadIdx.x & 31;
   const float2 r0 = bf16x2_to_f32(raw.x), r1 = bf16x2_to_f32(raw.y);
   float x[4] = {r0.x, r0.y, r1.x, r1.y};
-  const float2 cr = rounded(cs);
   const int li = lane - (a.k_offset >> 2);
   const bool mine = li >= 0 && li < kRot / 4;
   float y[4], err[4];
@@ -512,7 +555,7 @@ __device__ __forceinline__ void turn_store_k(uint2 raw, const CosSin& cs, const 
   const bool same = lo[0] == hi[0] && lo[1] == hi[1] && mx_shared_exp(amax - emax) == e &&
                     mx_shared_exp(amax + emax) == e && amax > 0.f;
   if (__any_sync(0xffffffffu, !same && emax > 0.f)) {  // (a group without rotary dims is exact as it is)
-    turn_k(x, cs, a.k_offset, a.k_layout == DSA_ROPE_HALF);
+    turn_k(x, phase_two(pos, turns, a.amplitude), a.k_offset, a.k_layout == DSA_ROPE_HALF);
     amax = group_max(top4(x));
     e = mx_shared_exp(amax);
     inv = exp2i(-e);
@@ -542,7 +585,7 @@ __device__ __forceinline__ void turn_store_k(uint2 raw, const CosSin& cs, const 
 // by the scale's, holds one code; else hi + lo does.
 //
 // Lane t works out tile t's scale and reciprocal, so that the five cost one division.
-__device__ __forceinline__ void turn_store_kv(const uint2 (&raws)[4], uint32_t rope, const CosSin& cs,
+__device__ __forceinline__ void turn_store_kv(const uint2 (&raws)[4], uint32_t rope, float2 cr, int pos, int64_t turns,
                                               const RopeQuantArgs& a, int64_t slot) {
   const int lane = threadIdx.x & 31;
   uint8_t* rec = a.kv_cache + slot * kKvTokBytes;
@@ -550,7 +593,6 @@ __device__ __forceinline__ void turn_store_kv(const uint2 (&raws)[4], uint32_t r
   const float2 x = bf16x2_to_f32(rope);
   float y0, y1, err0, err1;
   {
-    const float2 cr = rounded(cs);
     if (half_layout) {
       const float o0 = __shfl_xor_sync(0xffffffffu, x.x, 16), o1 = __shfl_xor_sync(0xffffffffu, x.y, 16);
       const float c0 = __shfl_sync(0xffffffffu, cr.x, 2 * lane), c1 = __shfl_sync(0xffffffffu, cr.x, 2 * lane + 1);
@@ -607,7 +649,7 @@ __device__ __forceinline__ void turn_store_kv(const uint2 (&raws)[4], uint32_t r
     const bool same = codes == f32x2_to_e4m3x2((y0 + d0) * ri, (y1 + d1) * ri);
     if (!((fast >> 4) & 1u) || __any_sync(0xffffffffu, !same)) {
       Two t0, t1;
-      turn_kv(x.x, x.y, cs, half_layout, t0, t1);
+      turn_kv(x.x, x.y, phase_two(pos, turns, a.amplitude), half_layout, t0, t1);
       const float top = warp_amax(fmaxf(fabsf(t0.hi), fabsf(t1.hi)));
       // the low part that goes with the largest: the scale is (top + low) / 448 rounded once
       float low = -INFINITY;
@@ -649,9 +691,9 @@ rope_quant_kernel(RopeQuantArgs a) {
     if (slot >= a.num_slots) {
       if (lane == 0) flag(a.status, DSA_STATUS_BAD_PAGE);
     } else if (slot >= 0) {
-      const CosSin cs = phase_cs(pos, turns, a.amplitude);
-      if (a.k) turn_store_k(k, cs, a, slot);
-      if (a.kv) turn_store_kv(kv, rope, cs, a, slot);
+      const float2 cs = phase_cs(pos, turns, a.amplitude);
+      if (a.k) turn_store_k(k, cs, pos, turns, a, slot);
+      if (a.kv) turn_store_kv(kv, rope, cs, pos, turns, a, slot);
     }
   }
 }
