@@ -471,10 +471,12 @@ __device__ __forceinline__ float2 bf16x2_to_f32(uint32_t v) {
   return make_float2(__low2float(b), __high2float(b));
 }
 // |x| / s rounded to odd as quotient_round_to_odd does, for a value known as x + low (low at
-// most half an ulp of x): the remainder's sign decides, and low has its share in it.
+// most half an ulp of x): the remainder's sign decides, and low has its share in it.  (low may move
+// the quotient by an ulp or more, past the neighbours of x's own: hence the second quotient.)
 __device__ __forceinline__ float sum_quotient_round_to_odd(float x, float low, float s) {
-  const float a = fabsf(x), q = __fdiv_rn(a, s);
-  const float r = __fmaf_rn(-q, s, a) + (x < 0.f ? -low : low);
+  const float a = fabsf(x), b = x < 0.f ? -low : low, q0 = __fdiv_rn(a, s);
+  const float q = q0 + __fdiv_rn(__fmaf_rn(-q0, s, a) + b, s);
+  const float r = __fmaf_rn(-q, s, a) + b;
   uint32_t qb = __float_as_uint(q);
   if (r != 0.f && (qb & 1u) == 0u) qb += (r > 0.f) ? 1u : 0xFFFFFFFFu;
   return copysignf(__uint_as_float(qb), x);

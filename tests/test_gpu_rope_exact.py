@@ -75,6 +75,20 @@ def test_every_code_of_a_keys_turned_dims(dsa, seed, k_layout, kv_layout):
     assert np.array_equal(got, want), np.argwhere(got != want)
 
 
+@SEEDS
+@LAYOUTS
+def test_every_code_of_a_turned_tile(dsa, seed, k_layout, kv_layout):
+    n, _, kv, turns, pos, _, cache = _written(dsa, seed, k_layout, kv_layout)
+    y = _turned(kv[:, 512:], turns, pos, kv_layout)
+    scale = (np.abs(y).max(1, keepdims=True) / 448).astype(np.float32).astype(np.float64)
+    rec = cache.reshape(n, 608)
+    got, want = oracle.codecs.e4m3_decode(rec[:, 512:576]), _e4m3(y / scale)
+    assert np.array_equal(got, want), np.argwhere(got != want)
+    # (the stored scale: the fp32 rotation's 4 roundings, and the quotient's)
+    mine = rec[:, 592:596].copy().view(np.float32).astype(np.float64)
+    assert np.all(np.abs(mine - scale) <= 5 * 2.0 ** -24 * scale)
+
+
 @pytest.mark.parametrize("layout", ["interleaved", "half"])
 @pytest.mark.parametrize("d", [64, 66])
 def test_small_angles_keep_their_relative_accuracy(dsa, layout, d):
