@@ -55,7 +55,7 @@ __device__ __forceinline__ float2 phase_cs(int pos, int64_t turns, float amp) {
   constexpr double kRad = 6.283185307179586476925 / 8589934592.0;  // 2 pi 2^-33
   constexpr float kHi = static_cast<float>(kRad);
   constexpr float kLo = static_cast<float>(kRad - static_cast<double>(kHi));
-  const float x = rh * kHi;
+  const float x = __fmul_rn(rh, kHi);  // (rounded here, whatever it is added to: so below)
   const float xl = fmaf(rh, kHi, -x) + fmaf(rl, kHi, rh * kLo);
   const float z = x * x;
   // sin = x + (x^3 S(z) + xl cos x),  cos = 1 + (-z/2 + z^2 C(z) - rounding of z / 2 - x xl)
@@ -74,7 +74,7 @@ __device__ __forceinline__ float2 phase_cs(int pos, int64_t turns, float amp) {
   const bool swap = quarter & 1u;
   Two c = swap ? sn : cn, s = swap ? cn : sn;
   const float cf = ((quarter + 1u) & 2u) ? -amp : amp, sf = (quarter & 2u) ? -amp : amp;
-  const float ch = c.hi * cf, sh = s.hi * sf;
+  const float ch = __fmul_rn(c.hi, cf), sh = __fmul_rn(s.hi, sf);
   return make_float2(ch + (fmaf(c.hi, cf, -ch) + c.lo * cf), sh + (fmaf(s.hi, sf, -sh) + s.lo * sf));
 }
 
@@ -355,7 +355,7 @@ constexpr int kRot = 64;
 // Sums and products of such pairs of floats (Dekker, "A floating-point technique for extending the
 // available precision", 1971; Knuth's two-sum), good to some 2^-46.
 __device__ __forceinline__ Two mul(const Two& a, const Two& b) {
-  const float p = a.hi * b.hi;
+  const float p = __fmul_rn(a.hi, b.hi);
   return two_sum_ordered(p, fmaf(a.hi, b.hi, -p) + fmaf(a.hi, b.lo, a.lo * b.hi));
 }
 __device__ __forceinline__ Two add(const Two& a, const Two& b) {  // |a| >= |b|
@@ -401,7 +401,7 @@ __device__ __noinline__ CosSin phase_two(int pos, int64_t turns, float amp) {
 
 // a c + b s as hi + lo (a, b exact inputs); an infinity or NaN has no low part
 __device__ __forceinline__ Two dot2(float a, const Two& c, float b, const Two& s) {
-  const float p = a * c.hi, q = b * s.hi;
+  const float p = __fmul_rn(a, c.hi), q = __fmul_rn(b, s.hi);
   const float e = fmaf(a, c.hi, -p) + fmaf(b, s.hi, -q);   // the products' roundings
   const float h = p + q, t = h - p;
   if (!(fabsf(h) < INFINITY)) return {h, 0.f};
