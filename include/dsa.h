@@ -165,9 +165,10 @@ int dsa_rope(const void* x, void* out, int32_t dtype, int32_t n, int32_t h, int3
 
 /*
  * dsa_rope_quant_kv -- the cache writers with the rotation on the way: token i's key and
- * latent row are turned to position pos[i] and stored as dsa_quant_kv stores them.  The
- * turned values are quantised from fp32 (not rounded to bf16 in between); dims outside the
- * rotary parts get exactly dsa_quant_kv's codes, and so do scales of groups without any.
+ * latent row are turned to position pos[i] and stored as dsa_quant_kv stores them, NaN and
+ * infinities too.  The turned values are not rounded in between: a code is the nearest of the
+ * turned value (with the amplitude in fp32), an fp32 scale is within 5 roundings of it.  Dims
+ * outside the rotary parts get exactly dsa_quant_kv's codes, and so do scales of groups without any.
  *   k_bf16       nullable [n_tokens] rows of 128 bfloat16, k_stride elements apart; its
  *                rotary part is dims [k_offset, k_offset + 64), k_offset a multiple of 4 in
  *                0..64, in layout k_layout.
