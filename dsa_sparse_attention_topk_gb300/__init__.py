@@ -16,11 +16,17 @@ Functions (same names as the C entry points, without the ``dsa_`` prefix):
 * ``rope(x, pos, turns, ...)``  -- rotary positions: turn part of every head
 * ``rope_quant_kv(k, kv, pos, slot_mapping, k_cache, kv_cache, turns, ...)`` -- the cache
   writers with the rotation on the way
+* ``norm_rope(x, pos, turns, ...)``  -- every head normed and turned in one pass
+* ``norm_rope_grad(dy, x, pos, turns, ...)``  -- its gradient
+* ``norm_rope_quant_kv(k, kv, pos, slot_mapping, k_cache, kv_cache, turns, ...)`` -- the cache
+  writers with norm and rotation on the way
 * ``decode_step(...)``  -- writers, indexer + Top-K and SFA of one decode step in one call
 * ``indexer_topk(...)``                          -- fused Lightning Indexer + Top-K
 * ``indexer_scores(...)``                        -- the same scores written in full
 * ``sparse_attn(...)``                           -- Sparse Flash Attention
 * ``prefix_attn(...)``                           -- dense attention of a batch that shares a prefix
+* ``evict_select(mass, seq_lens, budget, ...)``  -- the positions that stay, by accumulated weight
+* ``evict_compact(kept, page_table, ...)``       -- their records moved to the first positions
 * ``rope_turns(rot, ...)``                       -- the frequency table the two rotary calls
   take, plain or scaled for long contexts (host arithmetic)
 * ``device_status()``                            -- read and clear the device status word
@@ -87,6 +93,16 @@ _SIGS = {
     "dsa_prefix_attn_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
     "dsa_prefix_attn": (ctypes.c_int, [_P, _I32, _I32, _P, _I64, _P, _I32, _P, _I32, _P, _I32, _P, _P, _I32, _F32, _P,
                                        _P, _P, _SZ, _P]),
+    "dsa_norm_rope": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _I32, _I64, _I64, _I64, _I64, _P, _P, _I32, _I32, _I32, _F32,
+                                     _P, _P, _I32, _I32, _I32, _F32, _P]),
+    "dsa_norm_rope_grad_workspace_size": (_SZ, [_I32]),
+    "dsa_norm_rope_grad": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _I64, _I64, _I64, _I64, _I64, _I64, _P, _I32,
+                                          _I32, _I32, _F32, _P, _P, _I32, _I32, _I32, _F32, _P, _P, _P, _SZ, _P]),
+    "dsa_norm_rope_quant_kv": (ctypes.c_int, [_P, _I64, _P, _P, _I32, _P, _I64, _P, _F32, _P, _P, _I32, _P, _P, _I64, _P,
+                                              _F32, _I32, _I32, _I32, _P]),
+    "dsa_evict_select": (ctypes.c_int, [_P, _I64, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P]),
+    "dsa_evict_compact_workspace_size": (_SZ, [_I32, _I32]),
+    "dsa_evict_compact": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _I64, _P, _SZ, _P]),
     "dsa_device_status": (ctypes.c_int, [_P]),
     "dsa_test_stall_indexer": (ctypes.c_int, [_I32]),
     "dsa_test_prefix_plan": (ctypes.c_int, [_I32, _I32, _I32, _I32, _I32, _P]),
@@ -329,22 +345,118 @@ def rope(x, pos, turns, offset=0, layout="interleaved", amplitude=1.0, transpose
     return out
 
 
-def rope_quant_kv(k, kv, pos, slot_mapping, k_cache, kv_cache, turns, amplitude=1.0, k_offset=0, k_layout="half",
-                  kv_layout="interleaved", stream=None):
-    """quant_kv with the rotation on the way: k bf16 [n, 128] (rotary dims [k_offset,
-    k_offset + 64), layout k_layout) -> k_cache, kv bf16 [n, 576] (rotary dims [512, 576),
-    layout kv_layout) -> kv_cache, turned to the positions pos int32 [n] and quantised from
-    fp32, at the int64 slots [n] (negative: skipped).  Rows may lie further apart than their
-    width (a slice of a wider projection).  k and k_cache, or kv and kv_cache, may be None."""
+NORMS = {"rms": 0, "layer": 1}
+
+
+def _norm(name):
+    if name not in NORMS:
+        raise ValueError(f"norm must be one of {sorted(NORMS)} (got {name!r})")
+    return NORMS[name]
+
+
+def _norm_args(what, x, pos, turns, weight, bias, norm_dim):
+    """What norm_rope and its gradient check alike: (heads, stride of x's heads, dims normed, the weights' dtype code)."""
+    shape = x.shape
+    if len(shape) not in (2, 3) or x.dtype not in _DTYPES:
+        raise ValueError(f"{what}: x must be [n, d] or [n, h, d] of bf16, fp16 or fp32")
+    _need_shaped(pos, torch.int32, shape[:1], f"{what}: pos")
+    _need_shaped(turns, torch.int64, turns.shape[:1], f"{what}: turns")
+    span = shape[-1] if norm_dim is None else norm_dim
+    first = weight if weight is not None else bias
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            continue
+        if t.dtype not in _DTYPES or t.dtype != first.dtype:
+            raise ValueError(f"{what}: weight and bias must be bf16, fp16 or fp32, both the same")
+        _need_shaped(t, t.dtype, (span,), f"{what}: {name}")
+    return span, 2 if first is None else _DTYPES[first.dtype]
+
+
+def _row_strides(what, t, name, shape):
+    """(token stride, head stride) of [n, d] or [n, h, d], last dim contiguous."""
+    s = t.stride()
+    if s[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{what}: the last dim of {name} must be contiguous")
+    return (s[0], s[1]) if len(shape) == 3 else (s[0], 0)
+
+
+def norm_rope(x, pos, turns, weight=None, bias=None, norm="rms", norm_dim=None, eps=1e-6, offset=0, layout="interleaved",
+              amplitude=1.0, out=None, stream=None):
+    """Every head of x normed and turned in one pass: its first norm_dim dims (None: all) become
+    (x - mu) / sqrt(mean((x - mu)^2) + eps) * weight + bias, mu their mean with norm="layer" and 0 with "rms"; then dims
+    [offset, offset + 2 len(turns)) are turned to pos.  x, pos, turns, layout, amplitude, stream: as for rope (heads
+    of at most 1024 dims); weight, bias: [norm_dim] of bf16, fp16 or fp32, or None (1, 0).  out=x works in
+    place; otherwise out must not overlap x.  Tensors that need a gradient are refused: call it under
+    torch.no_grad(), or in an autograd function whose backward is norm_rope_grad.  Returns out."""
+    if _tangents() or torch.is_grad_enabled():
+        _need_no_grad("norm_rope", "norm_rope_grad gives it", x, weight, bias, out)
+    span, w_code = _norm_args("norm_rope", x, pos, turns, weight, bias, norm_dim)
+    shape = x.shape
+    if out is None:
+        out = _result(stream, shape, x.dtype, x.device)
+    elif out.shape != shape or out.dtype != x.dtype:
+        raise ValueError("norm_rope: out must have x's shape and dtype")
+    dev = _same_device("norm_rope", x, pos, turns, out, weight, bias)
+    xt, xh = _row_strides("norm_rope", x, "x", shape)
+    ot, oh = _row_strides("norm_rope", out, "out", shape)
+    _call_on(dev, stream, lib().dsa_norm_rope, x.data_ptr(), out.data_ptr(), _DTYPES[x.dtype], shape[0],
+             shape[1] if len(shape) == 3 else 1, shape[-1], xt, xh, ot, oh, None if weight is None else weight.data_ptr(),
+             None if bias is None else bias.data_ptr(), w_code, span, _norm(norm), eps, pos.data_ptr(), turns.data_ptr(),
+             2 * turns.shape[0], offset, _layout(layout), amplitude)
+    return out
+
+
+def norm_rope_grad_workspace_size(norm_dim):
+    return int(lib().dsa_norm_rope_grad_workspace_size(norm_dim))
+
+
+def norm_rope_grad(dy, x, pos, turns, weight=None, bias=None, norm="rms", norm_dim=None, eps=1e-6, offset=0,
+                   layout="interleaved", amplitude=1.0, dx=None, workspace=None, stream=None):
+    """The gradient of norm_rope: dy that of its result, x and the others what it was given.  Returns
+    (dx with x's shape and dtype, dweight fp32 [norm_dim] or None, dbias fp32 [norm_dim] or None), the last two
+    where weight and bias are given.  dx may be dy or x (in place), and otherwise must not overlap them.
+    Equal inputs give equal bits.  There is no second derivative: tensors that need a gradient are refused."""
+    if _tangents() or torch.is_grad_enabled():
+        _need_no_grad("norm_rope_grad", "there is no second derivative", dy, x, weight, bias, dx)
+    span, w_code = _norm_args("norm_rope_grad", x, pos, turns, weight, bias, norm_dim)
+    shape = x.shape
+    if dy.shape != shape or dy.dtype != x.dtype:
+        raise ValueError("norm_rope_grad: dy must have x's shape and dtype")
+    if dx is None:
+        dx = _result(stream, shape, x.dtype, x.device)
+    elif dx.shape != shape or dx.dtype != x.dtype:
+        raise ValueError("norm_rope_grad: dx must have x's shape and dtype")
+    dev = _same_device("norm_rope_grad", dy, x, pos, turns, dx, weight, bias, workspace)
+    dw = _result(stream, (span,), torch.float32, x.device) if weight is not None else None
+    db = _result(stream, (span,), torch.float32, x.device) if bias is not None else None
+    if workspace is None:
+        if dw is not None or db is not None:
+            workspace = _scratch(stream, norm_rope_grad_workspace_size(span), x.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("norm_rope_grad: workspace must be contiguous")
+    yt, yh = _row_strides("norm_rope_grad", dy, "dy", shape)
+    xt, xh = _row_strides("norm_rope_grad", x, "x", shape)
+    ot, oh = _row_strides("norm_rope_grad", dx, "dx", shape)
+    _call_on(dev, stream, lib().dsa_norm_rope_grad, dy.data_ptr(), x.data_ptr(), dx.data_ptr(), _DTYPES[x.dtype], shape[0],
+             shape[1] if len(shape) == 3 else 1, shape[-1], yt, yh, xt, xh, ot, oh,
+             None if weight is None else weight.data_ptr(), w_code, span, _norm(norm), eps, pos.data_ptr(),
+             turns.data_ptr(), 2 * turns.shape[0], offset, _layout(layout), amplitude, None if dw is None else dw.data_ptr(),
+             None if db is None else db.data_ptr(), None if workspace is None else workspace.data_ptr(),
+             0 if workspace is None else workspace.nbytes)
+    return dx, dw, db
+
+
+def _writer_args(what, k, kv, pos, slot_mapping, k_cache, kv_cache, turns, *others):
+    """What the rotating writers check alike: (device number, tokens, cache pages)."""
     if k is None and kv is None:
-        raise ValueError("rope_quant_kv: k or kv must be given")
+        raise ValueError(f"{what}: k or kv must be given")
     first = k if k is not None else kv
     rows = first.shape[:1]
     pages = 1 << 48
     for t, cache, width, page_bytes, name in ((k, k_cache, INDEX_DIM, KCACHE_PAGE_BYTES, "k"),
                                               (kv, kv_cache, LATENT_DIM, PAGE_SIZE * KVCACHE_TOKEN_BYTES, "kv")):
         if (t is None) != (cache is None):
-            raise ValueError(f"rope_quant_kv: {name} and {name}_cache go together")
+            raise ValueError(f"{what}: {name} and {name}_cache go together")
         if t is None:
             continue
         if t.dtype != torch.bfloat16 or t.shape != (*rows, width) or t.stride(1) != 1:
@@ -352,15 +464,46 @@ def rope_quant_kv(k, kv, pos, slot_mapping, k_cache, kv_cache, turns, amplitude=
         if cache.dtype != torch.uint8 or not cache.is_contiguous():
             raise ValueError(f"{name}_cache must be a contiguous uint8 tensor")
         pages = min(pages, cache.numel() // page_bytes)
-    dev = _same_device("rope_quant_kv", first, k, kv, pos, slot_mapping, k_cache, kv_cache, turns)
-    _need_shaped(pos, torch.int32, rows, "rope_quant_kv: pos")
-    _need_shaped(slot_mapping, torch.int64, rows, "rope_quant_kv: slot_mapping")
-    _need_shaped(turns, torch.int64, (32,), "rope_quant_kv: turns")
+    dev = _same_device(what, first, k, kv, pos, slot_mapping, k_cache, kv_cache, turns, *others)
+    _need_shaped(pos, torch.int32, rows, f"{what}: pos")
+    _need_shaped(slot_mapping, torch.int64, rows, f"{what}: slot_mapping")
+    _need_shaped(turns, torch.int64, (32,), f"{what}: turns")
+    return dev, rows[0], pages
+
+
+def rope_quant_kv(k, kv, pos, slot_mapping, k_cache, kv_cache, turns, amplitude=1.0, k_offset=0, k_layout="half",
+                  kv_layout="interleaved", stream=None):
+    """quant_kv with the rotation on the way: k bf16 [n, 128] (rotary dims [k_offset,
+    k_offset + 64), layout k_layout) -> k_cache, kv bf16 [n, 576] (rotary dims [512, 576),
+    layout kv_layout) -> kv_cache, turned to the positions pos int32 [n] and quantised from
+    fp32, at the int64 slots [n] (negative: skipped).  Rows may lie further apart than their
+    width (a slice of a wider projection).  k and k_cache, or kv and kv_cache, may be None."""
+    dev, n, pages = _writer_args("rope_quant_kv", k, kv, pos, slot_mapping, k_cache, kv_cache, turns)
     _call_on(dev, stream, lib().dsa_rope_quant_kv,
              *((None, 0) if k is None else (k.data_ptr(), k.stride(0))),
              *((None, 0) if kv is None else (kv.data_ptr(), kv.stride(0))),
-             pos.data_ptr(), slot_mapping.data_ptr(), rows[0], None if k is None else k_cache.data_ptr(),
+             pos.data_ptr(), slot_mapping.data_ptr(), n, None if k is None else k_cache.data_ptr(),
              None if kv is None else kv_cache.data_ptr(), pages * PAGE_SIZE, turns.data_ptr(), amplitude, k_offset,
+             _layout(k_layout), _layout(kv_layout))
+
+
+def norm_rope_quant_kv(k, kv, pos, slot_mapping, k_cache, kv_cache, turns, k_weight=None, k_bias=None, kv_weight=None,
+                       k_norm="rms", eps=1e-6, amplitude=1.0, k_offset=0, k_layout="half", kv_layout="interleaved",
+                       stream=None):
+    """rope_quant_kv with a norm before the rotation: k over its 128 dims (k_norm "rms" or "layer"; k_weight, k_bias
+    fp32 [128] or None), kv over its first 512 (rms; kv_weight fp32 [512] or None).  The others as for rope_quant_kv;
+    tensors that need a gradient are refused."""
+    if _tangents() or torch.is_grad_enabled():
+        _need_no_grad("norm_rope_quant_kv", "codes have none", k, kv, k_weight, k_bias, kv_weight)
+    dev, n, pages = _writer_args("norm_rope_quant_kv", k, kv, pos, slot_mapping, k_cache, kv_cache, turns, k_weight, k_bias,
+                                 kv_weight)
+    for t, width, name in ((k_weight, INDEX_DIM, "k_weight"), (k_bias, INDEX_DIM, "k_bias"), (kv_weight, V_DIM, "kv_weight")):
+        if t is not None:
+            _need_shaped(t, torch.float32, (width,), f"norm_rope_quant_kv: {name}")
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _call_on(dev, stream, lib().dsa_norm_rope_quant_kv, p(k), 0 if k is None else k.stride(0), p(k_weight), p(k_bias),
+             _norm(k_norm), p(kv), 0 if kv is None else kv.stride(0), p(kv_weight), eps, pos.data_ptr(),
+             slot_mapping.data_ptr(), n, p(k_cache), p(kv_cache), pages * PAGE_SIZE, turns.data_ptr(), amplitude, k_offset,
              _layout(k_layout), _layout(kv_layout))
 
 
@@ -525,6 +668,66 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, page_table, seq_lens, q_s
              q_seq.data_ptr(), q_pos.data_ptr(), max_ctx, sm_scale, out.data_ptr(),
              None if out_lse is None else out_lse.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     return out, out_lse
+
+
+def evict_select(mass, seq_lens, budget, sinks=0, recent=0, kept=None, new_lens=None, kept_mass=None, stream=None):
+    """The positions of each sequence that stay: all if they are at most budget; else the first `sinks`, the last
+    `recent` and, of those between, the ones with the largest accumulated weights, equal ones from the lowest position.
+    mass: int64 [n_seq, max_ctx], rows contiguous; seq_lens: int32 [n_seq].  Returns (kept int32 [n_seq, budget] in
+    ascending order, -1 behind the last; new_lens int32 [n_seq]; kept_mass int64 [n_seq, budget], their weights)."""
+    if mass.dim() != 2 or mass.dtype != torch.int64 or (mass.stride(1) != 1 and mass.shape[1] > 1):
+        raise ValueError("evict_select: mass must be int64 [n_seq, max_ctx] with contiguous rows")
+    n_seq, max_ctx = mass.shape
+    dev = _same_device("evict_select", mass, seq_lens, kept, new_lens, kept_mass)
+    _need_shaped(seq_lens, torch.int32, (n_seq,), "evict_select: seq_lens")
+    if budget < 1:
+        raise ValueError("evict_select: budget must be at least 1")
+    if kept is None:
+        kept = _result(stream, (n_seq, budget), torch.int32, mass.device)
+    if new_lens is None:
+        new_lens = _result(stream, (n_seq,), torch.int32, mass.device)
+    if kept_mass is None:
+        kept_mass = _result(stream, (n_seq, budget), torch.int64, mass.device)
+    _need_shaped(kept, torch.int32, (n_seq, budget), "evict_select: kept")
+    _need_shaped(new_lens, torch.int32, (n_seq,), "evict_select: new_lens")
+    _need_shaped(kept_mass, torch.int64, (n_seq, budget), "evict_select: kept_mass")
+    if new_lens.data_ptr() == seq_lens.data_ptr() and n_seq:
+        raise ValueError("evict_select: new_lens must not be seq_lens")
+    _call_on(dev, stream, lib().dsa_evict_select, mass.data_ptr(), mass.stride(0), seq_lens.data_ptr(), n_seq, max_ctx,
+             budget, sinks, recent, kept.data_ptr(), new_lens.data_ptr(), kept_mass.data_ptr())
+    return kept, new_lens, kept_mass
+
+
+def evict_compact_workspace_size(n_seq, budget):
+    return int(lib().dsa_evict_compact_workspace_size(n_seq, budget))
+
+
+def evict_compact(kept, page_table, k_cache=None, kv_cache=None, dst_table=None, workspace=None, stream=None):
+    """Copy the records of position kept[b, i] of each sequence to its position i, in the caches given: to the pages of
+    dst_table (int32 [n_seq, pages]; none of them may be read), or in place (None).  kept: int32 [n_seq, budget], -1:
+    none; page_table: int32 [n_seq, max_pages].  In place, sequences must not share pages that are written."""
+    if kept.dim() != 2:
+        raise ValueError("evict_compact: kept must be [n_seq, budget]")
+    n_seq, budget = kept.shape
+    dev = _same_device("evict_compact", kept, page_table, k_cache, kv_cache, dst_table, workspace)
+    _need_shaped(kept, torch.int32, kept.shape, "evict_compact: kept")
+    _need_shaped(page_table, torch.int32, (n_seq, page_table.shape[-1]), "evict_compact: page_table")
+    pages = 1 << 46
+    for t, page_bytes, name in ((k_cache, KCACHE_PAGE_BYTES, "k_cache"), (kv_cache, PAGE_SIZE * KVCACHE_TOKEN_BYTES, "kv_cache")):
+        if t is not None:
+            _need_shaped(t, torch.uint8, t.shape, f"evict_compact: {name}")
+            pages = min(pages, t.numel() // page_bytes)
+    if dst_table is not None:
+        _need_shaped(dst_table, torch.int32, (n_seq, dst_table.shape[-1]), "evict_compact: dst_table")
+    if workspace is None:
+        if dst_table is None or dst_table.data_ptr() == page_table.data_ptr():
+            workspace = _scratch(stream, evict_compact_workspace_size(n_seq, budget), kept.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("evict_compact: workspace must be contiguous")
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _call_on(dev, stream, lib().dsa_evict_compact, kept.data_ptr(), n_seq, budget, page_table.data_ptr(),
+             page_table.shape[-1], p(dst_table), 0 if dst_table is None else dst_table.shape[-1], p(k_cache), p(kv_cache),
+             pages, p(workspace), 0 if workspace is None else workspace.nbytes)
 
 
 NOALLOC_SCRATCH_BYTES = 40 * 1024 * 1024

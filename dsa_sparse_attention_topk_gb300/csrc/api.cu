@@ -155,6 +155,14 @@ static bool spans(int64_t stride, int32_t n) {
   return stride >= 0 && stride <= (n > 1 ? most / (n - 1) : most);
 }
 
+// [n][h] rows of d elements, of which no two share memory: the strides nest
+static bool rows_apart(int64_t stride_t, int n, int64_t stride_h, int h, int d) {
+  auto nests = [d](int64_t in, int n_in, int64_t over, int n_over) {
+    return (n_in == 1 || in >= d) && (n_over == 1 || over >= (n_in - 1) * in + d);
+  };
+  return nests(stride_h, h, stride_t, n) || nests(stride_t, n, stride_h, h);
+}
+
 int dsa_rope(const void* x, void* out, int32_t dtype, int32_t n, int32_t h, int32_t d, int64_t x_stride_t,
              int64_t x_stride_h, int64_t out_stride_t, int64_t out_stride_h, const int32_t* pos,
              const int64_t* turns, int32_t rot, int32_t offset, int32_t layout, float amplitude,
@@ -181,10 +189,7 @@ int dsa_rope(const void* x, void* out, int32_t dtype, int32_t n, int32_t h, int3
   // strides of an axis of length 1 are never used
   if (n == 1) x_stride_t = out_stride_t = 0;
   if (h == 1) x_stride_h = out_stride_h = 0;
-  auto nests = [](int64_t in, int n_in, int64_t over, int n_over, int64_t width) {
-    return (n_in == 1 || in >= width) && (n_over == 1 || over >= (n_in - 1) * in + width);
-  };
-  if (!nests(out_stride_h, h, out_stride_t, n, d) && !nests(out_stride_t, n, out_stride_h, h, d))
+  if (!rows_apart(out_stride_t, n, out_stride_h, h, d))
     return fail(DSA_ERR_INVALID_ARG, "rope: the strides of out let its elements overlap");
   if (x == out && (x_stride_t != out_stride_t || x_stride_h != out_stride_h))
     return fail(DSA_ERR_INVALID_ARG, "rope: in place, x and out need the same strides");
@@ -194,28 +199,123 @@ int dsa_rope(const void* x, void* out, int32_t dtype, int32_t n, int32_t h, int3
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "rope launch");
 }
 
+// What the norm with rotation and its gradient check alike; `who` names the entry.
+static int check_norm(const char* who, const dsa::NormArgs& a) {
+  if (a.n < 0 || a.h < 0) return fail(DSA_ERR_INVALID_ARG, "%s: negative n or h", who);
+  if (a.dtype < DSA_DTYPE_BF16 || a.dtype > DSA_DTYPE_FP32 || a.w_dtype < DSA_DTYPE_BF16 || a.w_dtype > DSA_DTYPE_FP32)
+    return fail(DSA_ERR_UNSUPPORTED, "%s: dtypes must be bf16, fp16 or fp32", who);
+  if (a.d < 2 || a.d > 1024) return fail(DSA_ERR_UNSUPPORTED, "%s: d must be 2..1024 (got %d)", who, a.d);
+  if (a.span < 1 || a.span > a.d) return fail(DSA_ERR_INVALID_ARG, "%s: norm_dim must lie in 1..%d (got %d)", who, a.d, a.span);
+  if (a.rot < 2 || a.rot % 2 || a.rot > a.d || a.offset < 0 || a.offset > a.d - a.rot)
+    return fail(DSA_ERR_INVALID_ARG, "%s: rot must be even and [offset, offset + rot) lie in [0, %d)", who, a.d);
+  if (a.layout != DSA_ROPE_INTERLEAVED && a.layout != DSA_ROPE_HALF)
+    return fail(DSA_ERR_INVALID_ARG, "%s: unknown layout %d", who, a.layout);
+  if (a.center != 0 && a.center != 1) return fail(DSA_ERR_INVALID_ARG, "%s: center must be 0 or 1", who);
+  if (!std::isfinite(a.amplitude) || !std::isfinite(a.eps) || a.eps < 0.f)
+    return fail(DSA_ERR_INVALID_ARG, "%s: amplitude must be finite, eps finite and not negative", who);
+  if (static_cast<int64_t>(a.n) * a.h > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "%s: n * h must be below 2^31", who);
+  const size_t wsize = a.w_dtype == DSA_DTYPE_FP32 ? 4 : 2;
+  if (!aligned(a.weight, wsize) || !aligned(a.bias, wsize) || !aligned(a.dweight, 4) || !aligned(a.dbias, 4))
+    return fail(DSA_ERR_INVALID_ARG, "%s: a pointer is not aligned to its element", who);
+  if (a.n == 0 || a.h == 0) return DSA_OK;
+  if (!a.x || !a.out || !a.pos || !a.turns) return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", who);
+  const size_t size = a.dtype == DSA_DTYPE_FP32 ? 4 : 2;
+  if (!aligned(a.x, size) || !aligned(a.dy, size) || !aligned(a.out, size) || !aligned(a.pos, 4) || !aligned(a.turns, 8))
+    return fail(DSA_ERR_INVALID_ARG, "%s: a pointer is not aligned to its element", who);
+  if (!spans(a.x_stride_t, a.n) || !spans(a.x_stride_h, a.h) || !spans(a.dy_stride_t, a.n) || !spans(a.dy_stride_h, a.h) ||
+      !spans(a.out_stride_t, a.n) || !spans(a.out_stride_h, a.h))
+    return fail(DSA_ERR_INVALID_ARG, "%s: a stride is negative, or an axis longer than 2^40 elements", who);
+  if (!rows_apart(a.out_stride_t, a.n, a.out_stride_h, a.h, a.d))
+    return fail(DSA_ERR_INVALID_ARG, "%s: the strides of the result let its elements overlap", who);
+  auto differ = [&](const void* p, int64_t st, int64_t sh) {
+    return p == a.out && ((a.n > 1 && st != a.out_stride_t) || (a.h > 1 && sh != a.out_stride_h));
+  };
+  if (differ(a.x, a.x_stride_t, a.x_stride_h) || differ(a.dy, a.dy_stride_t, a.dy_stride_h))
+    return fail(DSA_ERR_INVALID_ARG, "%s: in place, the result needs the strides of what it replaces", who);
+  return DSA_OK;
+}
+// strides of an axis of length 1 are never used
+static void drop_unused_strides(dsa::NormArgs& a) {
+  if (a.n == 1) a.x_stride_t = a.dy_stride_t = a.out_stride_t = 0;
+  if (a.h == 1) a.x_stride_h = a.dy_stride_h = a.out_stride_h = 0;
+}
+
+int dsa_norm_rope(const void* x, void* out, int32_t dtype, int32_t n, int32_t h, int32_t d, int64_t x_stride_t,
+                  int64_t x_stride_h, int64_t out_stride_t, int64_t out_stride_h, const void* weight, const void* bias,
+                  int32_t w_dtype, int32_t norm_dim, int32_t center, float eps, const int32_t* pos, const int64_t* turns,
+                  int32_t rot, int32_t offset, int32_t layout, float amplitude, void* stream) {
+  dsa::NormArgs a{x, nullptr, out, dtype, n, h, d, x_stride_t, x_stride_h, 0, 0, out_stride_t, out_stride_h, pos, turns, rot,
+                  offset, layout, amplitude, norm_dim, center, eps, weight, bias, w_dtype, nullptr, nullptr, nullptr};
+  const int rc = check_norm("norm_rope", a);
+  if (rc || n == 0 || h == 0) return rc;
+  drop_unused_strides(a);
+  cudaError_t e = dsa::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "norm_rope launch");
+}
+
+size_t dsa_norm_rope_grad_workspace_size(int32_t norm_dim) {
+  return norm_dim < 1 || norm_dim > 1024 ? 0 : dsa::norm_grad_workspace_bytes(norm_dim);
+}
+
+int dsa_norm_rope_grad(const void* dy, const void* x, void* dx, int32_t dtype, int32_t n, int32_t h, int32_t d,
+                       int64_t dy_stride_t, int64_t dy_stride_h, int64_t x_stride_t, int64_t x_stride_h,
+                       int64_t dx_stride_t, int64_t dx_stride_h, const void* weight, int32_t w_dtype, int32_t norm_dim,
+                       int32_t center, float eps, const int32_t* pos, const int64_t* turns, int32_t rot, int32_t offset,
+                       int32_t layout, float amplitude, float* dweight, float* dbias, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  dsa::NormArgs a{x, dy, dx, dtype, n, h, d, x_stride_t, x_stride_h, dy_stride_t, dy_stride_h, dx_stride_t, dx_stride_h, pos,
+                  turns, rot, offset, layout, amplitude, norm_dim, center, eps, weight, nullptr, w_dtype, dweight, dbias,
+                  static_cast<float*>(workspace)};
+  const int rc = check_norm("norm_rope_grad", a);
+  if (rc) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (n == 0 || h == 0) {  // the sums over no rows
+    if (dweight) e = cudaMemsetAsync(dweight, 0, sizeof(float) * norm_dim, s);
+    if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, sizeof(float) * norm_dim, s);
+    return e == cudaSuccess ? DSA_OK : cuda_fail(e, "norm_rope_grad");
+  }
+  if (!dy) return fail(DSA_ERR_INVALID_ARG, "norm_rope_grad: null pointer");
+  const size_t need = dsa::norm_grad_workspace_bytes(norm_dim);
+  if ((dweight || dbias) && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return fail(DSA_ERR_INVALID_ARG, "norm_rope_grad: workspace must be >= %zu bytes and 256-byte aligned", need);
+  drop_unused_strides(a);
+  e = dsa::launch_norm_rope_grad(a, s);
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "norm_rope_grad launch");
+}
+
+static int check_rope_quant(const char* who, const void* k_bf16, int64_t k_stride, const void* kv_bf16, int64_t kv_stride,
+                            const int32_t* pos, const int64_t* slot_mapping, int32_t n_tokens, const uint8_t* k_cache,
+                            const uint8_t* kv_cache, int64_t num_slots, const int64_t* turns, float amplitude,
+                            int32_t k_offset, int32_t k_layout, int32_t kv_layout) {
+  if (n_tokens < 0) return fail(DSA_ERR_INVALID_ARG, "%s: n_tokens < 0", who);
+  if (k_offset < 0 || k_offset > DSA_INDEX_DIM - 64 || k_offset % 4)
+    return fail(DSA_ERR_INVALID_ARG, "%s: k_offset must be a multiple of 4 in 0..64 (got %d)", who, k_offset);
+  if ((k_layout != DSA_ROPE_INTERLEAVED && k_layout != DSA_ROPE_HALF) ||
+      (kv_layout != DSA_ROPE_INTERLEAVED && kv_layout != DSA_ROPE_HALF))
+    return fail(DSA_ERR_INVALID_ARG, "%s: unknown layout", who);
+  if (!std::isfinite(amplitude)) return fail(DSA_ERR_INVALID_ARG, "%s: amplitude must be finite", who);
+  if (n_tokens == 0) return DSA_OK;
+  if (!pos || !slot_mapping || !turns || (!k_bf16 && !kv_bf16) || (k_bf16 && !k_cache) || (kv_bf16 && !kv_cache))
+    return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned(k_bf16, 8) || !aligned(kv_bf16, 8) || !aligned(k_cache, 16) || !aligned(kv_cache, 16) ||
+      !aligned(slot_mapping, 8) || !aligned(turns, 8) || !aligned(pos, 4))
+    return fail(DSA_ERR_INVALID_ARG, "%s: rows must be 8-byte and caches 16-byte aligned", who);
+  if ((k_bf16 && (!spans(k_stride, n_tokens) || k_stride % 4)) ||
+      (kv_bf16 && (!spans(kv_stride, n_tokens) || kv_stride % 4)))
+    return fail(DSA_ERR_INVALID_ARG, "%s: row strides must be multiples of 4 elements, all rows within 2^40", who);
+  if (num_slots <= 0 || num_slots % DSA_PAGE_SIZE)
+    return fail(DSA_ERR_INVALID_ARG, "%s: num_slots must be a positive multiple of 64", who);
+  return DSA_OK;
+}
+
 int dsa_rope_quant_kv(const void* k_bf16, int64_t k_stride, const void* kv_bf16, int64_t kv_stride,
                       const int32_t* pos, const int64_t* slot_mapping, int32_t n_tokens, uint8_t* k_cache,
                       uint8_t* kv_cache, int64_t num_slots, const int64_t* turns, float amplitude,
                       int32_t k_offset, int32_t k_layout, int32_t kv_layout, void* stream) {
-  if (n_tokens < 0) return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: n_tokens < 0");
-  if (k_offset < 0 || k_offset > DSA_INDEX_DIM - 64 || k_offset % 4)
-    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: k_offset must be a multiple of 4 in 0..64 (got %d)", k_offset);
-  if ((k_layout != DSA_ROPE_INTERLEAVED && k_layout != DSA_ROPE_HALF) ||
-      (kv_layout != DSA_ROPE_INTERLEAVED && kv_layout != DSA_ROPE_HALF))
-    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: unknown layout");
-  if (!std::isfinite(amplitude)) return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: amplitude must be finite");
-  if (n_tokens == 0) return DSA_OK;
-  if (!pos || !slot_mapping || !turns || (!k_bf16 && !kv_bf16) || (k_bf16 && !k_cache) || (kv_bf16 && !kv_cache))
-    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: null pointer");
-  if (!aligned(k_bf16, 8) || !aligned(kv_bf16, 8) || !aligned(k_cache, 16) || !aligned(kv_cache, 16) ||
-      !aligned(slot_mapping, 8) || !aligned(turns, 8) || !aligned(pos, 4))
-    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: rows must be 8-byte and caches 16-byte aligned");
-  if ((k_bf16 && (!spans(k_stride, n_tokens) || k_stride % 4)) ||
-      (kv_bf16 && (!spans(kv_stride, n_tokens) || kv_stride % 4)))
-    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: row strides must be multiples of 4 elements, all rows within 2^40");
-  if (num_slots <= 0 || num_slots % DSA_PAGE_SIZE)
-    return fail(DSA_ERR_INVALID_ARG, "rope_quant_kv: num_slots must be a positive multiple of 64");
+  const int rc = check_rope_quant("rope_quant_kv", k_bf16, k_stride, kv_bf16, kv_stride, pos, slot_mapping, n_tokens, k_cache,
+                                  kv_cache, num_slots, turns, amplitude, k_offset, k_layout, kv_layout);
+  if (rc || n_tokens == 0) return rc;
   unsigned* st = status_ptr();
   if (!st) return fail(DSA_ERR_CUDA, "rope_quant_kv: no CUDA device");
   dsa::RopeQuantArgs a{k_bf16, k_stride, kv_bf16, kv_stride, pos, slot_mapping, n_tokens, k_cache, kv_cache, num_slots,
@@ -472,6 +572,86 @@ int dsa_prefix_attn(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t*
   cudaError_t e = dsa::launch_prefix_attn(a, static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess) return why ? fail(DSA_ERR_UNSUPPORTED, "%s", why) : cuda_fail(e, "prefix_attn launch");
   return DSA_OK;
+}
+
+int dsa_norm_rope_quant_kv(const void* k_bf16, int64_t k_stride, const float* k_weight, const float* k_bias,
+                           int32_t k_center, const void* kv_bf16, int64_t kv_stride, const float* kv_weight, float eps,
+                           const int32_t* pos, const int64_t* slot_mapping, int32_t n_tokens, uint8_t* k_cache,
+                           uint8_t* kv_cache, int64_t num_slots, const int64_t* turns, float amplitude,
+                           int32_t k_offset, int32_t k_layout, int32_t kv_layout, void* stream) {
+  const int rc = check_rope_quant("norm_rope_quant_kv", k_bf16, k_stride, kv_bf16, kv_stride, pos, slot_mapping, n_tokens,
+                                  k_cache, kv_cache, num_slots, turns, amplitude, k_offset, k_layout, kv_layout);
+  if (rc) return rc;
+  if (k_center != 0 && k_center != 1) return fail(DSA_ERR_INVALID_ARG, "norm_rope_quant_kv: k_center must be 0 or 1");
+  if (!std::isfinite(eps) || eps < 0.f)
+    return fail(DSA_ERR_INVALID_ARG, "norm_rope_quant_kv: eps must be finite and not negative");
+  if (!aligned(k_weight, 16) || !aligned(k_bias, 16) || !aligned(kv_weight, 16))
+    return fail(DSA_ERR_INVALID_ARG, "norm_rope_quant_kv: weights and bias must be 16-byte aligned");
+  if (n_tokens == 0) return DSA_OK;
+  unsigned* st = status_ptr();
+  if (!st) return fail(DSA_ERR_CUDA, "norm_rope_quant_kv: no CUDA device");
+  dsa::NormQuantArgs a{{k_bf16, k_stride, kv_bf16, kv_stride, pos, slot_mapping, n_tokens, k_cache, kv_cache, num_slots,
+                        turns, amplitude, k_offset, k_layout, kv_layout, st},
+                       k_weight, k_bias, kv_weight, k_center, eps};
+  cudaError_t e = dsa::launch_norm_rope_quant(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "norm_rope_quant_kv launch");
+}
+
+int dsa_evict_select(const int64_t* mass, int64_t mass_stride, const int32_t* seq_lens, int32_t n_seq, int32_t max_ctx,
+                     int32_t budget, int32_t sinks, int32_t recent, int32_t* kept, int32_t* new_lens,
+                     int64_t* kept_mass, void* stream) {
+  if (n_seq < 0) return fail(DSA_ERR_INVALID_ARG, "evict_select: n_seq < 0");
+  if (max_ctx < 1 || max_ctx > 1048576) return fail(DSA_ERR_UNSUPPORTED, "evict_select: max_ctx must be 1..1048576");
+  if (budget < 1 || budget > 1048576) return fail(DSA_ERR_UNSUPPORTED, "evict_select: budget must be 1..1048576");
+  if (sinks < 0 || recent < 0 || static_cast<int64_t>(sinks) + recent > budget)
+    return fail(DSA_ERR_INVALID_ARG, "evict_select: sinks and recent must not be negative, nor more than budget together");
+  if (n_seq > INT32_MAX / 16) return fail(DSA_ERR_UNSUPPORTED, "evict_select: n_seq must be below 2^27");
+  if (n_seq == 0) return DSA_OK;
+  if (!spans(mass_stride, n_seq) || (n_seq > 1 && mass_stride < max_ctx))
+    return fail(DSA_ERR_INVALID_ARG, "evict_select: mass_stride must be max_ctx or more, all rows within 2^40 elements");
+  if (!mass || !seq_lens || !kept || !new_lens) return fail(DSA_ERR_INVALID_ARG, "evict_select: null pointer");
+  if (!aligned(mass, 8) || !aligned(kept_mass, 8) || !aligned(seq_lens, 4) || !aligned(kept, 4) || !aligned(new_lens, 4))
+    return fail(DSA_ERR_INVALID_ARG, "evict_select: a pointer is not aligned to its element");
+  unsigned* st = status_ptr();
+  if (!st) return fail(DSA_ERR_CUDA, "evict_select: no CUDA device");
+  dsa::EvictSelectArgs a{mass, mass_stride, seq_lens, n_seq, max_ctx, budget, sinks, recent, kept, new_lens, kept_mass, st};
+  cudaError_t e = dsa::launch_evict_select(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "evict_select launch");
+}
+
+size_t dsa_evict_compact_workspace_size(int32_t n_seq, int32_t budget) {
+  return n_seq < 1 || budget < 1 ? 0 : dsa::evict_workspace_bytes(n_seq, budget);
+}
+
+int dsa_evict_compact(const int32_t* kept, int32_t n_seq, int32_t budget, const int32_t* page_table, int32_t max_pages,
+                      const int32_t* dst_table, int32_t dst_max_pages, uint8_t* k_cache, uint8_t* kv_cache,
+                      int64_t num_pages, void* workspace, size_t workspace_bytes, void* stream) {
+  if (n_seq < 0) return fail(DSA_ERR_INVALID_ARG, "evict_compact: n_seq < 0");
+  if (budget < 1 || budget > 1048576) return fail(DSA_ERR_UNSUPPORTED, "evict_compact: budget must be 1..1048576");
+  if (max_pages < 1 || num_pages < 1 || num_pages > INT64_MAX / 65536)
+    return fail(DSA_ERR_INVALID_ARG, "evict_compact: max_pages and num_pages must be >= 1");
+  if (n_seq == 0) return DSA_OK;
+  if (!kept || !page_table || (!k_cache && !kv_cache)) return fail(DSA_ERR_INVALID_ARG, "evict_compact: null pointer");
+  const bool in_place = !dst_table || dst_table == page_table;
+  if (in_place) {
+    if (dst_table && dst_max_pages != max_pages)
+      return fail(DSA_ERR_INVALID_ARG, "evict_compact: one table with two widths");
+    dst_table = page_table;
+    dst_max_pages = max_pages;
+  }
+  if (dst_max_pages < (budget + DSA_PAGE_SIZE - 1) / DSA_PAGE_SIZE)
+    return fail(DSA_ERR_INVALID_ARG, "evict_compact: the pages that receive must hold budget positions");
+  if (!aligned(kept, 4) || !aligned(page_table, 4) || !aligned(dst_table, 4) || !aligned(k_cache, 16) || !aligned(kv_cache, 16))
+    return fail(DSA_ERR_INVALID_ARG, "evict_compact: tables must be 4-byte and caches 16-byte aligned");
+  const size_t need = dsa::evict_workspace_bytes(n_seq, budget);
+  if (in_place && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return fail(DSA_ERR_INVALID_ARG, "evict_compact: in place, workspace must be >= %zu bytes and 256-byte aligned", need);
+  unsigned* st = status_ptr();
+  if (!st) return fail(DSA_ERR_CUDA, "evict_compact: no CUDA device");
+  dsa::EvictCompactArgs a{kept, n_seq, budget, page_table, max_pages, dst_table, dst_max_pages, k_cache, kv_cache, num_pages,
+                          static_cast<uint8_t*>(workspace), st};
+  cudaError_t e = dsa::launch_evict_compact(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "evict_compact launch");
 }
 
 int dsa_topk_merge(const int32_t* cand_idx, const float* cand_scores, const int32_t* part_offsets, int32_t n_parts,

@@ -148,6 +148,68 @@ struct RopeQuantArgs {
 };
 cudaError_t launch_rope_quant(const RopeQuantArgs& a, cudaStream_t s);
 
+// dsa_norm_rope, and its gradient where dy is given: x, dy and out (then dx) [n][h][d] of dtype
+struct NormArgs {
+  const void* x;
+  const void* dy;
+  void* out;
+  int dtype, n, h, d;
+  int64_t x_stride_t, x_stride_h, dy_stride_t, dy_stride_h, out_stride_t, out_stride_h;
+  const int32_t* pos;        // [n]
+  const int64_t* turns;      // [rot / 2]
+  int rot, offset, layout;   // rotary part, as RopeArgs
+  float amplitude;
+  int span, center;          // dims [0, span) are normed, with their mean taken off
+  float eps;
+  const void* weight;        // [span] of w_dtype, or null
+  const void* bias;
+  int w_dtype;
+  float* dweight;            // [span] or null
+  float* dbias;
+  float* workspace;          // partial sums of the two
+};
+cudaError_t launch_norm_rope(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_norm_rope_grad(const NormArgs& a, cudaStream_t s);
+size_t norm_grad_workspace_bytes(int span);
+
+struct NormQuantArgs {
+  RopeQuantArgs r;           // rows, positions, slots, caches and the rotation
+  const float* k_weight;     // [128] or null
+  const float* k_bias;
+  const float* kv_weight;    // [512] or null
+  int k_center;
+  float eps;
+};
+cudaError_t launch_norm_rope_quant(const NormQuantArgs& a, cudaStream_t s);
+
+struct EvictSelectArgs {
+  const int64_t* mass;       // [n_seq] rows of max_ctx, mass_stride apart
+  int64_t mass_stride;
+  const int32_t* seq_lens;
+  int n_seq, max_ctx, budget, sinks, recent;
+  int32_t* kept;             // [n_seq][budget]
+  int32_t* new_lens;         // [n_seq]
+  int64_t* kept_mass;        // [n_seq][budget] or null
+  unsigned* status;
+};
+cudaError_t launch_evict_select(const EvictSelectArgs& a, cudaStream_t s);
+
+struct EvictCompactArgs {
+  const int32_t* kept;       // [n_seq][budget]
+  int n_seq, budget;
+  const int32_t* page_table; // [n_seq][max_pages]
+  int max_pages;
+  const int32_t* dst_table;  // [n_seq][dst_max_pages]; == page_table: in place
+  int dst_max_pages;
+  uint8_t* k_cache;          // or null
+  uint8_t* kv_cache;         // or null
+  int64_t num_pages;
+  uint8_t* workspace;        // in place
+  unsigned* status;
+};
+cudaError_t launch_evict_compact(const EvictCompactArgs& a, cudaStream_t s);
+size_t evict_workspace_bytes(int n_seq, int budget);
+
 struct PrefixArgs {
   const void* q;              // bf16 [n_q][h_s][576]
   int n_q, h_s;

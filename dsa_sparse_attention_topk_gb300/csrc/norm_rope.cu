@@ -1,0 +1,316 @@
+// Queries and keys normed per head and turned by their positions in one pass (dsa_norm_rope), and the cache
+// writers with both on the way (dsa_norm_rope_quant_kv).
+//
+// The first `span` dims of a head become (x - mu) / sqrt(mean (x - mu)^2 + eps) * w + b, mu their mean or
+// zero; then pairs of the rotary part are turned as in rope.cu.  Sums, the normed values and the turn are
+// fp32, and the result is rounded once: a value is good to a few roundings of fp32 of the row's size.  The
+// mean is taken off before anything is squared, so that a row far from zero loses nothing.
+//
+// Bound: memory, each value read and written once.  A row stays in the registers of 8 to 32 lanes between the
+// sums and the turn.
+
+#include "norm_rope.cuh"
+
+namespace dsa {
+namespace {
+
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(kNormThreads)
+norm_rope_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
+  using W = typename Word<V * sizeof(T)>::type;
+  extern __shared__ __align__(16) unsigned char raw[];
+  pdl_launch_dependents();
+  pdl_wait();
+  NormShared sh = norm_shared(a, g, raw);
+  const int lane = threadIdx.x & (g.lanes - 1), grp = threadIdx.x / g.lanes;
+  float* ex = sh.ex + grp * a.rot;
+  const int64_t rows = static_cast<int64_t>(a.n) * a.h;
+  const int64_t begin = blockIdx.x * rows_block, end = min(begin + rows_block, rows);
+  const float inv_span = 1.0f / static_cast<float>(a.span);
+  Vec<T, V> next[NV];
+  auto load = [&](int64_t row) {
+    if (row >= end) return;
+    const int t = static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(a.h));
+    const int hh = static_cast<int>(static_cast<uint32_t>(row) - static_cast<uint32_t>(t) * static_cast<uint32_t>(a.h));
+    const T* src = static_cast<const T*>(a.x) + t * a.x_stride_t + hh * a.x_stride_h;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int vec = j * g.lanes + lane;
+      if (vec < g.vectors) next[j].u = *reinterpret_cast<const W*>(src + vec * V);
+    }
+  };
+  load(begin + grp);
+  norm_fill_params(a, sh);
+  for (int64_t r0 = begin; r0 < end; r0 += g.rows_step) {
+    const int64_t row = r0 + grp;
+    float y[NV * V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool there = j * g.lanes + lane < g.vectors;
+#pragma unroll
+      for (int i = 0; i < V; ++i) y[j * V + i] = there ? Elem<T>::get(next[j].e[i]) : 0.f;
+    }
+    load(row + g.rows_step);
+    norm_fill_cs(a, g, sh, r0, rows);
+    // (a vector is normed as a whole or not at all: V divides span)
+    float mean = 0.f;
+    if (a.center) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if ((j * g.lanes + lane) * V < a.span)
+#pragma unroll
+          for (int i = 0; i < V; ++i) s += y[j * V + i];
+      mean = row_sum(s, g.lanes) * inv_span;
+    }
+    float s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if ((j * g.lanes + lane) * V < a.span)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          y[j * V + i] -= mean;
+          s2 = fmaf(y[j * V + i], y[j * V + i], s2);
+        }
+    const float r = rsqrtf(fmaf(row_sum(s2, g.lanes), inv_span, a.eps));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e0 = (j * g.lanes + lane) * V;
+      if (e0 < a.span)
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[j * V + i] = fmaf(y[j * V + i] * r, sh.weight[e0 + i], sh.bias[e0 + i]);
+    }
+    const int t = static_cast<int>(static_cast<uint32_t>(min(row, rows - 1)) / static_cast<uint32_t>(a.h));
+    const int hh = static_cast<int>(static_cast<uint32_t>(row) - static_cast<uint32_t>(t) * static_cast<uint32_t>(a.h));
+    turn_row<V, NV, false>(a, g, y, sh.cs + (row < end ? t - sh.first : 0) * ((a.rot / 2 + 1) & ~1), ex, lane);
+    if (row < end) {
+      T* dst = static_cast<T*>(a.out) + t * a.out_stride_t + hh * a.out_stride_h;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int vec = j * g.lanes + lane;
+        Vec<T, V> o;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o.e[i] = Elem<T>::put(y[j * V + i]);
+        if (vec < g.vectors) *reinterpret_cast<W*>(dst + vec * V) = o.u;
+      }
+    }
+  }
+}
+
+template <typename T, int V, int NV>
+cudaError_t launch_fwd(const NormArgs& a, const NormGeom& g, cudaStream_t s) {
+  const size_t smem = norm_shared_bytes(a, g);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<T, V, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t steps = (static_cast<int64_t>(a.n) * a.h + g.rows_step - 1) / g.rows_step;
+  const int64_t most = static_cast<int64_t>(multiprocessors()) * 16;
+  const int64_t per = (steps + most - 1) / most;
+  return launch_pdl(norm_rope_kernel<T, V, NV>, dim3(static_cast<unsigned>((steps + per - 1) / per)), dim3(kNormThreads),
+                    smem, s, 1, a, g, per * g.rows_step);
+}
+
+template <typename T>
+cudaError_t launch_fwd_t(const NormArgs& a, cudaStream_t s) {
+  constexpr int kMost = 16 / sizeof(T);
+  const int v = norm_vector(reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out),
+                            static_cast<uint64_t>(a.x_stride_t | a.x_stride_h | a.out_stride_t | a.out_stride_h), a, sizeof(T));
+  const NormGeom g = norm_geom(a, v, sizeof(T));
+  const int nv = (g.vectors + g.lanes - 1) / g.lanes;
+  if (v == kMost) {
+    if (nv == 1) return launch_fwd<T, kMost, 1>(a, g, s);
+    if (nv == 2) return launch_fwd<T, kMost, 2>(a, g, s);
+    if (nv == 3) return launch_fwd<T, kMost, 3>(a, g, s);
+    if (nv == 4) return launch_fwd<T, kMost, 4>(a, g, s);
+    if constexpr (kMost == 4) {
+      if (nv == 5) return launch_fwd<T, kMost, 5>(a, g, s);
+      return launch_fwd<T, kMost, 8>(a, g, s);
+    }
+  }
+  if constexpr (kMost == 8) {
+    if (v >= 4) return nv <= 1 ? launch_fwd<T, 4, 1>(a, g, s) : nv <= 2 ? launch_fwd<T, 4, 2>(a, g, s) : launch_fwd<T, 4, 8>(a, g, s);
+  }
+  if (v == 2) return nv <= 2 ? launch_fwd<T, 2, 2>(a, g, s) : launch_fwd<T, 2, 16>(a, g, s);
+  return nv <= 4 ? launch_fwd<T, 1, 4>(a, g, s) : launch_fwd<T, 1, 32>(a, g, s);
+}
+
+// ---- the cache writers with norm and rotation on the way -----------------------------
+// One warp per token, lane i the sine and cosine of frequency i, as in the other writers.  The normed and turned
+// values are quantised from fp32: a code is the nearest of a value that is good to some 2^-21 of its
+// size and its pair's, so a value that close to the border between two codes may land on either side.  A row whose sum of squares is
+// not finite has no norm: it is stored as NaN.
+constexpr int kWarpsPerBlock = 8;
+constexpr int kRot = 64;
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// 1 / sqrt(mean square + eps), NaN where that has no finite value
+__device__ __forceinline__ float norm_factor(float sum, float inv_n, float eps) {
+  const float m = fmaf(sum, inv_n, eps);
+  return m < INFINITY ? rsqrtf(m) : NAN;
+}
+
+__device__ __forceinline__ void norm_store_k(uint2 raw, float4 w, float4 b, float2 cs, const NormQuantArgs& a, int64_t slot) {
+  const int lane = threadIdx.x & 31;
+  const float2 r0 = bf16x2_to_f32(raw.x), r1 = bf16x2_to_f32(raw.y);
+  float x[4] = {r0.x, r0.y, r1.x, r1.y};
+  if (a.k_center) {
+    const float mean = warp_sum((x[0] + x[1]) + (x[2] + x[3])) * (1.0f / kIdxDim);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] -= mean;
+  }
+  const float r = norm_factor(warp_sum(fmaf(x[0], x[0], x[1] * x[1]) + fmaf(x[2], x[2], x[3] * x[3])), 1.0f / kIdxDim, a.eps);
+  x[0] = fmaf(x[0] * r, w.x, b.x);
+  x[1] = fmaf(x[1] * r, w.y, b.y);
+  x[2] = fmaf(x[2] * r, w.z, b.z);
+  x[3] = fmaf(x[3] * r, w.w, b.w);
+  const int li = lane - (a.r.k_offset >> 2);  // 0..15 inside the rotary part
+  const bool mine = li >= 0 && li < kRot / 4;
+  float y[4];
+  if (a.r.k_layout == DSA_ROPE_HALF) {
+    const bool first = li < 8;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float other = __shfl_sync(0xffffffffu, x[j], first ? lane + 8 : lane - 8);
+      const float c = __shfl_sync(0xffffffffu, cs.x, 4 * (li & 7) + j), s = __shfl_sync(0xffffffffu, cs.y, 4 * (li & 7) + j);
+      y[j] = fmaf(x[j], c, other * (first ? -s : s));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float c = __shfl_sync(0xffffffffu, cs.x, 2 * li + j), s = __shfl_sync(0xffffffffu, cs.y, 2 * li + j);
+      y[2 * j] = fmaf(x[2 * j], c, -x[2 * j + 1] * s);
+      y[2 * j + 1] = fmaf(x[2 * j + 1], c, x[2 * j] * s);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = mine ? y[j] : x[j];
+  float amax = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const int e = amax < INFINITY ? mx_shared_exp(amax) : 0;
+  const float inv = exp2i(-e);  // exact power of two
+  const uint32_t codes = codes4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+  uint8_t* page = a.r.k_cache + (slot / kPage) * kKPageBytes;
+  const int row = static_cast<int>(slot % kPage);
+  *reinterpret_cast<uint32_t*>(page + row * kIdxDim + 4 * lane) = amax == 0.f ? 0u : codes;
+  if ((lane & 7) == 0) page[kKScaleOff + row * 4 + (lane >> 3)] = static_cast<uint8_t>(e + 127);
+}
+
+__device__ __forceinline__ void norm_store_kv(const uint2 (&raws)[4], uint32_t rope, const float4 (&w)[4], float2 cs,
+                                              const NormQuantArgs& a, int64_t slot) {
+  const int lane = threadIdx.x & 31;
+  uint8_t* rec = a.r.kv_cache + slot * kKvTokBytes;
+  float y[16];
+  float s2 = 0.f;
+#pragma unroll
+  for (int tile = 0; tile < 4; ++tile) {
+    const float2 p = bf16x2_to_f32(raws[tile].x), q = bf16x2_to_f32(raws[tile].y);
+    y[4 * tile] = p.x;
+    y[4 * tile + 1] = p.y;
+    y[4 * tile + 2] = q.x;
+    y[4 * tile + 3] = q.y;
+    s2 += fmaf(p.x, p.x, p.y * p.y) + fmaf(q.x, q.x, q.y * q.y);
+  }
+  const float r = norm_factor(warp_sum(s2), 1.0f / kVDim, a.eps);
+  const float2 x = bf16x2_to_f32(rope);
+  float t0, t1;
+  if (a.r.kv_layout == DSA_ROPE_HALF) {
+    const float o0 = __shfl_xor_sync(0xffffffffu, x.x, 16), o1 = __shfl_xor_sync(0xffffffffu, x.y, 16);
+    const float c0 = __shfl_sync(0xffffffffu, cs.x, 2 * lane), c1 = __shfl_sync(0xffffffffu, cs.x, 2 * lane + 1);
+    const float s0 = __shfl_sync(0xffffffffu, cs.y, 2 * lane), s1 = __shfl_sync(0xffffffffu, cs.y, 2 * lane + 1);
+    t0 = fmaf(x.x, c0, o0 * (lane < 16 ? -s0 : s0));
+    t1 = fmaf(x.y, c1, o1 * (lane < 16 ? -s1 : s1));
+  } else {
+    t0 = fmaf(x.x, cs.x, -x.y * cs.y);
+    t1 = fmaf(x.y, cs.x, x.x * cs.y);
+  }
+  // lane t works out tile t's scale and its reciprocal, so that the five cost one division
+  float amax = warp_amax(fmaxf(fabsf(t0), fabsf(t1)));
+#pragma unroll
+  for (int tile = 0; tile < 4; ++tile) {
+    const float f[4] = {w[tile].x, w[tile].y, w[tile].z, w[tile].w};
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[4 * tile + i] *= r * f[i];
+      m = fmaxf(m, fabsf(y[4 * tile + i]));
+    }
+    m = warp_amax(r == r ? m : NAN);
+    if (lane == tile) amax = m;
+  }
+  const float s = __fdiv_rn(amax, 448.0f);
+  const bool usable = s > 1e-30f && s < 1e30f;  // 1 / s and s itself are far from the range's ends
+  const float inv = usable ? __frcp_rn(s) : 0.f;
+  const uint32_t fast = __ballot_sync(0xffffffffu, usable);
+  auto quotient = [](float v, float ts) { return ts > 0.f ? __fdiv_rn(v, ts) : 0.f; };
+#pragma unroll
+  for (int tile = 0; tile < 4; ++tile) {
+    const float ti = __shfl_sync(0xffffffffu, inv, tile), ts = __shfl_sync(0xffffffffu, s, tile);
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (fast >> tile) & 1u ? y[4 * tile + i] * ti : quotient(y[4 * tile + i], ts);
+    *reinterpret_cast<uint32_t*>(rec + tile * 128 + 4 * lane) = codes4(v[0], v[1], v[2], v[3]);
+  }
+  const float ti = __shfl_sync(0xffffffffu, inv, 4), ts = __shfl_sync(0xffffffffu, s, 4);
+  *reinterpret_cast<uint16_t*>(rec + 512 + 2 * lane) =
+      (fast >> 4) & 1u ? f32x2_to_e4m3x2(t0 * ti, t1 * ti) : f32x2_to_e4m3x2(quotient(t0, ts), quotient(t1, ts));
+  if (lane < 8) *reinterpret_cast<float*>(rec + kKvScaleOff + 4 * lane) = lane < 5 ? s : 0.f;
+}
+
+__global__ void __launch_bounds__(kWarpsPerBlock * 32)
+norm_rope_quant_kernel(NormQuantArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t turns = a.r.turns[lane];
+  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
+  float4 kw = one, kb = make_float4(0.f, 0.f, 0.f, 0.f), vw[4] = {one, one, one, one};
+  if (a.k_weight) kw = *reinterpret_cast<const float4*>(a.k_weight + 4 * lane);
+  if (a.k_bias) kb = *reinterpret_cast<const float4*>(a.k_bias + 4 * lane);
+  if (a.kv_weight)
+#pragma unroll
+    for (int tile = 0; tile < 4; ++tile) vw[tile] = *reinterpret_cast<const float4*>(a.kv_weight + tile * 128 + 4 * lane);
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarpsPerBlock + (threadIdx.x >> 5); t < a.r.n_tokens;
+       t += static_cast<int64_t>(gridDim.x) * kWarpsPerBlock) {
+    const int64_t slot = a.r.slots[t];
+    const int pos = a.r.pos[t];
+    uint2 k, kv[4];
+    uint32_t rope;
+    if (a.r.k) k = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.r.k) + t * a.r.k_stride + 4 * lane);
+    if (a.r.kv) {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.r.kv) + t * a.r.kv_stride;
+#pragma unroll
+      for (int tile = 0; tile < 4; ++tile) kv[tile] = *reinterpret_cast<const uint2*>(src + tile * 128 + 4 * lane);
+      rope = *reinterpret_cast<const uint32_t*>(src + 512 + 2 * lane);
+    }
+    if (slot >= a.r.num_slots) {
+      if (lane == 0) flag(a.r.status, DSA_STATUS_BAD_PAGE);
+    } else if (slot >= 0) {
+      const float2 cs = phase_cs(pos, turns, a.r.amplitude);
+      if (a.r.k) norm_store_k(k, kw, kb, cs, a, slot);
+      if (a.r.kv) norm_store_kv(kv, rope, vw, cs, a, slot);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const NormArgs& a, cudaStream_t s) {
+  if (a.dtype == DSA_DTYPE_BF16) return launch_fwd_t<__nv_bfloat16>(a, s);
+  if (a.dtype == DSA_DTYPE_FP16) return launch_fwd_t<__half>(a, s);
+  return launch_fwd_t<float>(a, s);
+}
+
+cudaError_t launch_norm_rope_quant(const NormQuantArgs& a, cudaStream_t s) {
+  const int cap = multiprocessors() * 16;
+  const int blocks = a.r.n_tokens / kWarpsPerBlock + (a.r.n_tokens % kWarpsPerBlock != 0);
+  return launch_pdl(norm_rope_quant_kernel, dim3(blocks < cap ? blocks : cap), dim3(kWarpsPerBlock * 32), 0, s, 1, a);
+}
+
+}  // namespace dsa

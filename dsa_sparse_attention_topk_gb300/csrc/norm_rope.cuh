@@ -1,0 +1,157 @@
+// What the per-head norm with rotation (norm_rope.cu) and its gradient (norm_rope_grad.cu) share: how the
+// rows of a call are laid over lanes, the tables of a block, and the turn of a row's rotary part.
+//
+// A row is one head of one token.  A group of G lanes holds a whole row in registers, vector
+// j G + lane of it in lane `lane`'s j-th word, so that it is read once however often it is summed over.
+// With vectors of 16 bytes eight lanes cover 128 consecutive bytes, as much as a memory request wants,
+// and a warp has four rows under way; longer rows take 16 or 32 lanes so that a lane holds at most 32
+// elements in fp32.
+#pragma once
+
+#include "dsa_common.cuh"
+#include "dsa_launch.h"
+#include "rope_math.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kNormThreads = 256;
+
+struct NormGeom {
+  int lanes;          // G: lanes a row, a power of two of 8..32
+  int vectors;        // of one row
+  int rows_step;      // rows of a block at a time: kNormThreads / lanes
+  int tokens_step;    // tokens that those can touch, the sines' table
+  int span_pad;       // norm_dim rounded up to 4, floats of the weights' table
+};
+
+// one float of the weight or bias
+__device__ __forceinline__ float norm_param(const void* p, int dtype, int i) {
+  if (dtype == DSA_DTYPE_FP32) return static_cast<const float*>(p)[i];
+  if (dtype == DSA_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+
+// A block's shared memory: weights (ones where there are none) and biases (zeros) in fp32, the sines of the
+// tokens at hand, and each row's rotary part for exchange.
+struct NormShared {
+  float* weight;
+  float* bias;
+  float2* cs;
+  float* ex;
+  int first, last;  // tokens in cs
+};
+__device__ __forceinline__ NormShared norm_shared(const NormArgs& a, const NormGeom& g, unsigned char* raw) {
+  NormShared s;
+  s.weight = reinterpret_cast<float*>(raw);
+  s.bias = s.weight + g.span_pad;
+  s.cs = reinterpret_cast<float2*>(s.bias + g.span_pad);
+  s.ex = reinterpret_cast<float*>(s.cs + g.tokens_step * ((a.rot / 2 + 1) & ~1));
+  s.first = 0;
+  s.last = -1;
+  return s;
+}
+__device__ __forceinline__ void norm_fill_params(const NormArgs& a, const NormShared& s) {
+  for (int i = threadIdx.x; i < a.span; i += kNormThreads) {
+    s.weight[i] = a.weight ? norm_param(a.weight, a.w_dtype, i) : 1.f;
+    s.bias[i] = a.bias ? norm_param(a.bias, a.w_dtype, i) : 0.f;
+  }
+}
+// the sines of the tokens of rows [r0, r0 + rows_step); every thread of the block calls it, and it synchronises them
+// whenever the table changes
+__device__ __forceinline__ void norm_fill_cs(const NormArgs& a, const NormGeom& g, NormShared& s, int64_t r0, int64_t rows) {
+  const int first = static_cast<int>(static_cast<uint32_t>(r0) / static_cast<uint32_t>(a.h));
+  const int last = static_cast<int>(static_cast<uint32_t>(min(r0 + g.rows_step, rows) - 1) / static_cast<uint32_t>(a.h));
+  if (first >= s.first && last <= s.last) return;
+  __syncthreads();
+  const int half = a.rot >> 1, pitch = (half + 1) & ~1, count = (last - first + 1) * half;
+  for (int i = threadIdx.x; i < count; i += kNormThreads) {
+    const int t = i / half, f = i - t * half;
+    s.cs[t * pitch + f] = phase_cs(a.pos[first + t], a.turns[f], a.amplitude);
+  }
+  s.first = first;
+  s.last = last;
+  __syncthreads();
+}
+
+// The sum over a row's lanes, in every one of them.
+__device__ __forceinline__ float row_sum(float v, int lanes) {
+  for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Turn the rotary part of the row in y (fp32, in the lanes' layout); TRANSPOSE turns back.  Pairs of neighbours
+// lie in one vector; a partner half a rotary part away (or, with vectors of one element, beside) is
+// fetched through shared memory, ex: the row's own rot floats there.
+template <int V, int NV, bool TRANSPOSE>
+__device__ __forceinline__ void turn_row(const NormArgs& a, const NormGeom& g, float (&y)[NV * V], const float2* cs,
+                                         float* ex, int lane) {
+  const bool half_layout = a.layout == DSA_ROPE_HALF;
+  const int half = a.rot >> 1;
+  if (half_layout || V == 1) {
+    __syncwarp();  // (the row before has been read)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int rel = (j * g.lanes + lane) * V - a.offset;
+      if (rel >= 0 && rel < a.rot) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) ex[rel + i] = y[j * V + i];
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int rel = (j * g.lanes + lane) * V - a.offset;
+      if (rel >= 0 && rel < a.rot) {
+        const bool second = half_layout ? rel >= half : rel & 1;
+        const int f = half_layout ? (second ? rel - half : rel) : rel >> 1;
+        const int other = half_layout ? (second ? rel - half : rel + half) : rel ^ 1;
+        const float sign = second == TRANSPOSE ? -1.f : 1.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float2 c = cs[f + i];
+          // a c - b s for the first of a pair, b c + a s for the second
+          y[j * V + i] = y[j * V + i] * c.x + sign * c.y * ex[other + i];
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int rel = (j * g.lanes + lane) * V - a.offset;
+      if (rel >= 0 && rel < a.rot) {
+#pragma unroll
+        for (int i = 0; i + 1 < V; i += 2) {
+          const float2 c = cs[(rel + i) >> 1];
+          const float p = y[j * V + i], q = y[j * V + i + 1], s = TRANSPOSE ? -c.y : c.y;
+          y[j * V + i] = p * c.x - q * s;
+          y[j * V + i + 1] = p * s + q * c.x;
+        }
+      }
+    }
+  }
+}
+
+// The widest vector, in elements, that divides every address, stride and part of a row, at most 16 bytes.
+inline int norm_vector(uint64_t address_bits, uint64_t stride_bits, const NormArgs& a, int size) {
+  const uint64_t all = address_bits / size | stride_bits | static_cast<uint64_t>(a.d | a.span | a.offset) |
+                       static_cast<uint64_t>(a.layout == DSA_ROPE_HALF ? a.rot / 2 : a.rot) | static_cast<uint64_t>(16 / size);
+  return static_cast<int>(all & (~all + 1));
+}
+inline NormGeom norm_geom(const NormArgs& a, int v, int size) {
+  NormGeom g;
+  g.vectors = a.d / v;
+  g.lanes = v * size < 16 ? 32 : g.vectors <= 32 ? 8 : g.vectors <= 64 ? 16 : 32;
+  g.rows_step = kNormThreads / g.lanes;
+  const int64_t most = (g.rows_step + a.h - 2) / a.h + 1;
+  g.tokens_step = static_cast<int>(most < a.n ? most : a.n);
+  g.span_pad = (a.span + 3) & ~3;
+  return g;
+}
+inline size_t norm_shared_bytes(const NormArgs& a, const NormGeom& g) {
+  return 2 * sizeof(float) * g.span_pad + sizeof(float2) * g.tokens_step * ((a.rot / 2 + 1) & ~1) +
+         sizeof(float) * g.rows_step * a.rot;
+}
+
+}  // namespace
+}  // namespace dsa

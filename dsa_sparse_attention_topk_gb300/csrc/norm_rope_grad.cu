@@ -1,0 +1,228 @@
+// The gradient of dsa_norm_rope (dsa_norm_rope_grad).
+//
+// With g the output's gradient turned back, u = (x - mu) r the normed value and du = g w:
+//     dx = r (du - u mean(du u) [- mean(du), with a mean]),   dw = sum g u,   db = sum g,
+// sums of dw and db over all rows; dims that are not normed have dx = g.  u is formed again from x, which
+// costs no memory that the sums would not read anyway; nothing is kept from the forward pass.
+//
+// Bound: memory, dy and x read and dx written once.  A block takes a run of rows and each lane keeps the sums of its
+// own dims in registers; the blocks' sums go to the workspace and a second kernel adds them, always in the same
+// order, so that equal inputs give equal bits.
+
+#include "norm_rope.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kMostBlocks = 1024;  // partial sums in the workspace
+
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(kNormThreads)
+norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
+  using W = typename Word<V * sizeof(T)>::type;
+  extern __shared__ __align__(16) unsigned char raw[];
+  pdl_launch_dependents();
+  pdl_wait();
+  NormShared sh = norm_shared(a, g, raw);
+  const int lane = threadIdx.x & (g.lanes - 1), grp = threadIdx.x / g.lanes;
+  float* ex = sh.ex + grp * a.rot;
+  const int64_t rows = static_cast<int64_t>(a.n) * a.h;
+  const int64_t begin = blockIdx.x * rows_block, end = min(begin + rows_block, rows);
+  const float inv_span = 1.0f / static_cast<float>(a.span);
+  norm_fill_params(a, sh);
+  float dw[NV * V], db[NV * V];
+#pragma unroll
+  for (int i = 0; i < NV * V; ++i) dw[i] = db[i] = 0.f;
+  for (int64_t r0 = begin; r0 < end; r0 += g.rows_step) {
+    const int64_t row = r0 + grp;
+    const bool live = row < end;
+    const int t = static_cast<int>(static_cast<uint32_t>(min(row, rows - 1)) / static_cast<uint32_t>(a.h));
+    const int hh = static_cast<int>(static_cast<uint32_t>(min(row, rows - 1)) - static_cast<uint32_t>(t) * static_cast<uint32_t>(a.h));
+    const T* xs = static_cast<const T*>(a.x) + t * a.x_stride_t + hh * a.x_stride_h;
+    const T* ys = static_cast<const T*>(a.dy) + t * a.dy_stride_t + hh * a.dy_stride_h;
+    float u[NV * V], d[NV * V];
+    {
+      Vec<T, V> p[NV], q[NV];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int vec = j * g.lanes + lane;
+        if (live && vec < g.vectors) {
+          p[j].u = *reinterpret_cast<const W*>(xs + vec * V);
+          q[j].u = *reinterpret_cast<const W*>(ys + vec * V);
+        } else {
+          p[j].u = W{};
+          q[j].u = W{};
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          u[j * V + i] = Elem<T>::get(p[j].e[i]);
+          d[j * V + i] = Elem<T>::get(q[j].e[i]);
+        }
+    }
+    norm_fill_cs(a, g, sh, r0, rows);
+    turn_row<V, NV, true>(a, g, d, sh.cs + (live ? t - sh.first : 0) * ((a.rot / 2 + 1) & ~1), ex, lane);
+    float mean = 0.f;
+    if (a.center) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if ((j * g.lanes + lane) * V < a.span)
+#pragma unroll
+          for (int i = 0; i < V; ++i) s += u[j * V + i];
+      mean = row_sum(s, g.lanes) * inv_span;
+    }
+    float s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if ((j * g.lanes + lane) * V < a.span)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          u[j * V + i] -= mean;
+          s2 = fmaf(u[j * V + i], u[j * V + i], s2);
+        }
+    const float r = rsqrtf(fmaf(row_sum(s2, g.lanes), inv_span, a.eps));
+    float c1 = 0.f, c2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e0 = (j * g.lanes + lane) * V;
+      if (e0 < a.span)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int k = j * V + i;
+          u[k] *= r;
+          if (live) {  // (a row behind the last has x = 0, and with eps = 0 no factor)
+            dw[k] = fmaf(d[k], u[k], dw[k]);
+            db[k] += d[k];
+          }
+          d[k] *= sh.weight[e0 + i];
+          c1 = fmaf(d[k], u[k], c1);
+          c2 += d[k];
+        }
+    }
+    c1 = row_sum(c1, g.lanes) * inv_span;
+    c2 = a.center ? row_sum(c2, g.lanes) * inv_span : 0.f;
+    if (live) {
+      T* dst = static_cast<T*>(a.out) + t * a.out_stride_t + hh * a.out_stride_h;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int vec = j * g.lanes + lane;
+        Vec<T, V> o;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int k = j * V + i;
+          o.e[i] = Elem<T>::put(vec * V < a.span ? r * (fmaf(-u[k], c1, d[k]) - c2) : d[k]);
+        }
+        if (vec < g.vectors) *reinterpret_cast<W*>(dst + vec * V) = o.u;
+      }
+    }
+  }
+  if (!a.dweight && !a.dbias) return;
+  // the block's sums: first over the groups of a warp, then over the warps through shared memory
+  float* sums = reinterpret_cast<float*>(raw);  // [2][warps][span], over the tables
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, in_warp = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < NV * V; ++k) {
+    for (int o = g.lanes; o < 32; o <<= 1) {
+      dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], o);
+      db[k] += __shfl_xor_sync(0xffffffffu, db[k], o);
+    }
+    const int e = ((k / V) * g.lanes + lane) * V + k % V;
+    if (in_warp < g.lanes && e < a.span) {
+      sums[warp * a.span + e] = dw[k];
+      sums[(kNormThreads / 32 + warp) * a.span + e] = db[k];
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.span; i += kNormThreads) {
+    const int which = i >= a.span, e = i - which * a.span;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kNormThreads / 32; ++w) v += sums[(which * (kNormThreads / 32) + w) * a.span + e];
+    a.workspace[static_cast<int64_t>(blockIdx.x) * 2 * a.span + i] = v;
+  }
+}
+
+// The sums of `blocks` partial sums: 32 columns a block, 32 rows of threads that each take every 32nd partial.
+__global__ void __launch_bounds__(1024)
+norm_grad_sum_kernel(const float* part, int blocks, int span, float* dweight, float* dbias) {
+  __shared__ float s[32][33];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int col = blockIdx.x * 32 + threadIdx.x;
+  float v = 0.f;
+  if (col < 2 * span)
+#pragma unroll 8
+    for (int b = threadIdx.y; b < blocks; b += 32) v += part[static_cast<int64_t>(b) * 2 * span + col];
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  v = s[threadIdx.x][threadIdx.y];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int mine = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && mine < 2 * span) {
+    if (mine < span && dweight) dweight[mine] = v;
+    if (mine >= span && dbias) dbias[mine - span] = v;
+  }
+}
+
+template <typename T, int V, int NV>
+cudaError_t launch_bwd(const NormArgs& a, const NormGeom& g, cudaStream_t s) {
+  size_t smem = norm_shared_bytes(a, g);
+  const size_t sums = sizeof(float) * 2 * (kNormThreads / 32) * a.span;
+  smem = smem > sums ? smem : sums;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_rope_grad_kernel<T, V, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t steps = (static_cast<int64_t>(a.n) * a.h + g.rows_step - 1) / g.rows_step;
+  int64_t most = static_cast<int64_t>(multiprocessors()) * 4;
+  most = most < kMostBlocks ? most : kMostBlocks;
+  const int64_t per = (steps + most - 1) / most;
+  const int blocks = static_cast<int>((steps + per - 1) / per);
+  cudaError_t e = launch_pdl(norm_rope_grad_kernel<T, V, NV>, dim3(blocks), dim3(kNormThreads), smem, s, 1, a, g, per * g.rows_step);
+  if (e != cudaSuccess || (!a.dweight && !a.dbias)) return e;
+  return launch_pdl(norm_grad_sum_kernel, dim3((2 * a.span + 31) / 32), dim3(32, 32), 0, s, 1,
+                    static_cast<const float*>(a.workspace), blocks, a.span, a.dweight, a.dbias);
+}
+
+template <typename T>
+cudaError_t launch_bwd_t(const NormArgs& a, cudaStream_t s) {
+  constexpr int kMost = 16 / sizeof(T);
+  const int v = norm_vector(reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.dy),
+                            static_cast<uint64_t>(a.x_stride_t | a.x_stride_h | a.out_stride_t | a.out_stride_h | a.dy_stride_t | a.dy_stride_h),
+                            a, sizeof(T));
+  const NormGeom g = norm_geom(a, v, sizeof(T));
+  const int nv = (g.vectors + g.lanes - 1) / g.lanes;
+  if (v == kMost) {
+    if (nv == 1) return launch_bwd<T, kMost, 1>(a, g, s);
+    if (nv == 2) return launch_bwd<T, kMost, 2>(a, g, s);
+    if (nv == 3) return launch_bwd<T, kMost, 3>(a, g, s);
+    if (nv == 4) return launch_bwd<T, kMost, 4>(a, g, s);
+    if constexpr (kMost == 4) {
+      if (nv == 5) return launch_bwd<T, kMost, 5>(a, g, s);
+      return launch_bwd<T, kMost, 8>(a, g, s);
+    }
+  }
+  if constexpr (kMost == 8) {
+    if (v >= 4) return nv <= 1 ? launch_bwd<T, 4, 1>(a, g, s) : nv <= 2 ? launch_bwd<T, 4, 2>(a, g, s) : launch_bwd<T, 4, 8>(a, g, s);
+  }
+  if (v == 2) return nv <= 2 ? launch_bwd<T, 2, 2>(a, g, s) : launch_bwd<T, 2, 16>(a, g, s);
+  return nv <= 4 ? launch_bwd<T, 1, 4>(a, g, s) : launch_bwd<T, 1, 32>(a, g, s);
+}
+
+}  // namespace
+
+size_t norm_grad_workspace_bytes(int span) { return sizeof(float) * 2 * kMostBlocks * static_cast<size_t>(span); }
+
+cudaError_t launch_norm_rope_grad(const NormArgs& a, cudaStream_t s) {
+  if (a.dtype == DSA_DTYPE_BF16) return launch_bwd_t<__nv_bfloat16>(a, s);
+  if (a.dtype == DSA_DTYPE_FP16) return launch_bwd_t<__half>(a, s);
+  return launch_bwd_t<float>(a, s);
+}
+
+}  // namespace dsa

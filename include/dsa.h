@@ -188,6 +188,65 @@ int dsa_rope_quant_kv(const void* k_bf16, int64_t k_stride, const void* kv_bf16,
                       int32_t k_offset, int32_t k_layout, int32_t kv_layout, void* stream);
 
 /*
+ * dsa_norm_rope -- queries or keys normed per head and turned by their positions, in one pass.
+ * Of every head of x the first norm_dim dims become
+ *     (x - mu) / sqrt(mean((x - mu)^2) + eps) * weight + bias,
+ * mu their mean with center = 1 (a layer norm) and 0 with center = 0 (a root-mean-square norm); then the dims
+ * [offset, offset + rot) are turned as dsa_rope turns them.  The pages give neither.
+ *   x, out     [n][h][d] of `dtype`, d 2..1024; strides as for dsa_rope.  out == x with the same strides
+ *              works in place; otherwise out must not overlap x.
+ *   weight     nullable (1) [norm_dim] of w_dtype; bias  nullable (0) [norm_dim] of w_dtype.
+ *   norm_dim   1..d; the dims behind it are not normed (but turned, where the rotary part holds them).
+ *   eps        not negative.
+ *   pos, turns, rot, offset, layout, amplitude   as for dsa_rope.
+ * Computed in fp32 and rounded once to dtype.  A row whose sum of squares leaves the range of fp32, or
+ * holds NaN or infinities, becomes NaN or zero in its normed dims as the formula does in fp32; no other row is
+ * touched by it.  16-byte loads and stores where x, out, their strides, d, norm_dim, offset and rot allow;
+ * any alignment of whole elements works.  n * h must be below 2^31.
+ */
+int dsa_norm_rope(const void* x, void* out, int32_t dtype, int32_t n, int32_t h, int32_t d, int64_t x_stride_t,
+                  int64_t x_stride_h, int64_t out_stride_t, int64_t out_stride_h, const void* weight, const void* bias,
+                  int32_t w_dtype, int32_t norm_dim, int32_t center, float eps, const int32_t* pos, const int64_t* turns,
+                  int32_t rot, int32_t offset, int32_t layout, float amplitude, void* stream);
+
+/*
+ * dsa_norm_rope_grad -- the gradient of dsa_norm_rope, from its input and the gradient of its result.
+ *   dy, x, dx  [n][h][d] of `dtype`, each with its strides (those of dy and x may be 0: broadcast).  dx may be
+ *              dy or x (with the same strides), and otherwise overlaps neither.  Where x was broadcast,
+ *              its gradient is the sum of dx over that axis.
+ *   weight .. amplitude   as given to dsa_norm_rope (the bias does not matter).
+ *   dweight, dbias   nullable [norm_dim] fp32: the sums over all rows, overwritten.  Added up in an order
+ *              that only the sizes decide, so that equal inputs give equal bits.
+ *   workspace  where dweight or dbias is given: dsa_norm_rope_grad_workspace_size bytes, 256-byte aligned.
+ * The normed values are formed again from x; sums are fp32, dx is rounded once to dtype.
+ */
+size_t dsa_norm_rope_grad_workspace_size(int32_t norm_dim);
+int dsa_norm_rope_grad(const void* dy, const void* x, void* dx, int32_t dtype, int32_t n, int32_t h, int32_t d,
+                       int64_t dy_stride_t, int64_t dy_stride_h, int64_t x_stride_t, int64_t x_stride_h,
+                       int64_t dx_stride_t, int64_t dx_stride_h, const void* weight, int32_t w_dtype, int32_t norm_dim,
+                       int32_t center, float eps, const int32_t* pos, const int64_t* turns, int32_t rot, int32_t offset,
+                       int32_t layout, float amplitude, float* dweight, float* dbias, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * dsa_norm_rope_quant_kv -- the cache writers with norm and rotation on the way: token i's key is normed over
+ * its 128 dims (k_center, k_weight, k_bias as center, weight and bias of dsa_norm_rope) and its latent row over
+ * its first 512 (root mean square, kv_weight); both are turned to pos[i] and stored in the formats of
+ * dsa_quant_kv.  Nothing is rounded in between: a code is the nearest of a value that fp32 arithmetic gives,
+ * good to 2^-20 of its own and its pair's size, so that a value that close to the border between two codes may get
+ * either; scales are good to 2^-20.  A key, or the normed 512 dims of a row, whose sum of squares is not finite is
+ * stored as NaN.
+ *   k_weight, k_bias  nullable [128] fp32, kv_weight nullable [512] fp32, 16-byte aligned.
+ *   eps               not negative; both norms'.
+ *   the others        as for dsa_rope_quant_kv.
+ */
+int dsa_norm_rope_quant_kv(const void* k_bf16, int64_t k_stride, const float* k_weight, const float* k_bias,
+                           int32_t k_center, const void* kv_bf16, int64_t kv_stride, const float* kv_weight, float eps,
+                           const int32_t* pos, const int64_t* slot_mapping, int32_t n_tokens, uint8_t* k_cache,
+                           uint8_t* kv_cache, int64_t num_slots, const int64_t* turns, float amplitude,
+                           int32_t k_offset, int32_t k_layout, int32_t kv_layout, void* stream);
+
+/*
  * dsa_indexer_topk -- fused Lightning Indexer + Top-K over the paged MXFP8 K-cache.
  * Follows "Deep Dive into Sparse Attention ..." section 2.1 (score, weighting and Top-K
  * fused in one kernel that reads the paged K-cache directly) and "Kimi K3.1 Pro Inference
@@ -374,6 +433,47 @@ int dsa_prefix_attn(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t*
                     const int32_t* seq_lens, int32_t n_seq, const int32_t* q_seq, const int32_t* q_pos,
                     int32_t max_ctx, float sm_scale, void* out_bf16, float* out_lse, void* workspace,
                     size_t workspace_bytes, void* stream);
+
+/*
+ * Eviction.  A cache that has outgrown its room gives up the positions that attention has used least: their
+ * accumulated weights decide which stay (dsa_evict_select), and the records that stay move to the sequence's first
+ * positions (dsa_evict_compact), so that the pages behind them are free.  The pages do not describe it.  A
+ * position's keys keep the rotation they were written with: from then on its place in the sequence
+ * and the position it was turned to are two numbers.
+ */
+
+/*
+ * dsa_evict_select -- the positions of each sequence that stay: all of them if they are `budget` or fewer;
+ * otherwise the first `sinks`, the last `recent`, and of those between the budget - sinks - recent with the
+ * largest weights, equal weights going to the lower position.
+ *   mass       [n_seq] rows of max_ctx int64, mass_stride elements apart: accumulated weights, as
+ *              dsa_attn_mass leaves them; any values, compared as whole numbers.
+ *   seq_lens   [n_seq] int32 in [0, max_ctx]; any other flags DSA_STATUS_BAD_LEN and counts as 0.
+ *   max_ctx    1..1048576.      budget  1..1048576, at least sinks + recent.
+ *   kept       [n_seq][budget] int32: the positions in ascending order, -1 behind the last.
+ *   new_lens   [n_seq] int32: how many stay.  It must not be seq_lens.
+ *   kept_mass  nullable [n_seq][budget] int64: their weights, 0 behind the last; must not overlap mass.
+ */
+int dsa_evict_select(const int64_t* mass, int64_t mass_stride, const int32_t* seq_lens, int32_t n_seq, int32_t max_ctx,
+                     int32_t budget, int32_t sinks, int32_t recent, int32_t* kept, int32_t* new_lens,
+                     int64_t* kept_mass, void* stream);
+
+/*
+ * dsa_evict_compact -- copy the records of position kept[b][i] of every sequence to its position i, in both
+ * caches.
+ *   kept       [n_seq][budget] int32 positions (for instance dsa_evict_select's), -1: none.  Any order.
+ *   page_table [n_seq][max_pages] int32: the pages the positions lie in.
+ *   dst_table  [n_seq][dst_max_pages] int32: the pages that receive them, dst_max_pages >= ceil(budget / 64); none of
+ *              them may be a page that is read.  Null (or page_table itself): in place, and no two
+ *              sequences may share a page that is written.
+ *   k_cache, kv_cache   num_pages pages each, 16-byte aligned; one of them may be null.
+ *   workspace  in place: dsa_evict_compact_workspace_size bytes (752 a kept position), 256-byte aligned.
+ * A position or page out of range flags DSA_STATUS_BAD_INDEX or _BAD_PAGE, and that record is not copied.
+ */
+size_t dsa_evict_compact_workspace_size(int32_t n_seq, int32_t budget);
+int dsa_evict_compact(const int32_t* kept, int32_t n_seq, int32_t budget, const int32_t* page_table, int32_t max_pages,
+                      const int32_t* dst_table, int32_t dst_max_pages, uint8_t* k_cache, uint8_t* kv_cache,
+                      int64_t num_pages, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * dsa_device_status -- synchronise `stream`, return the device status word (an OR of
