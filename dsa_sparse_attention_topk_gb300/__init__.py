@@ -25,6 +25,8 @@ Functions (same names as the C entry points, without the ``dsa_`` prefix):
 * ``indexer_scores(...)``                        -- the same scores written in full
 * ``sparse_attn(...)``                           -- Sparse Flash Attention
 * ``prefix_attn(...)``                           -- dense attention of a batch that shares a prefix
+* ``attn_mass(...)``                             -- attention weights added up per cached position
+* ``sparse_attn_mass(...)``                      -- the same of the entries each row selected
 * ``evict_select(mass, seq_lens, budget, ...)``  -- the positions that stay, by accumulated weight
 * ``evict_compact(kept, page_table, ...)``       -- their records moved to the first positions
 * ``rope_turns(rot, ...)``                       -- the frequency table the two rotary calls
@@ -100,6 +102,11 @@ _SIGS = {
                                           _I32, _I32, _F32, _P, _P, _I32, _I32, _I32, _F32, _P, _P, _P, _SZ, _P]),
     "dsa_norm_rope_quant_kv": (ctypes.c_int, [_P, _I64, _P, _P, _I32, _P, _I64, _P, _F32, _P, _P, _I32, _P, _P, _I64, _P,
                                               _F32, _I32, _I32, _I32, _P]),
+    "dsa_attn_mass_workspace_size": (_SZ, [_I32, _I32, _I32]),
+    "dsa_attn_mass": (ctypes.c_int, [_P, _I32, _I32, _P, _I64, _P, _I32, _P, _I32, _P, _P, _I32, _F32, _P, _P, _I64, _P, _SZ,
+                                     _P]),
+    "dsa_sparse_attn_mass": (ctypes.c_int, [_P, _I32, _I32, _P, _I64, _P, _I32, _P, _I32, _P, _P, _I32, _I32, _F32, _P, _P,
+                                            _I64, _P, _P, _SZ, _P]),
     "dsa_evict_select": (ctypes.c_int, [_P, _I64, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P]),
     "dsa_evict_compact_workspace_size": (_SZ, [_I32, _I32]),
     "dsa_evict_compact": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _I64, _P, _SZ, _P]),
@@ -668,6 +675,86 @@ def prefix_attn(q, kv_cache, prefix_pages, prefix_len, page_table, seq_lens, q_s
              q_seq.data_ptr(), q_pos.data_ptr(), max_ctx, sm_scale, out.data_ptr(),
              None if out_lse is None else out_lse.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     return out, out_lse
+
+
+MASS_ONE = 1 << 36  # a weight of 1 in accumulated weights
+
+
+def attn_mass_workspace_size(n_q, h_s, n_seq):
+    return int(lib().dsa_attn_mass_workspace_size(n_q, h_s, n_seq))
+
+
+def _mass_args(what, q, kv_cache, page_table, seq_lens, q_seq, lse, mass, workspace, stream, *others):
+    """What the two kinds of accumulated weights check alike: (device number, pages of the cache, workspace)."""
+    if q.requires_grad or lse.requires_grad or _tangents():
+        _need_no_grad(what, "there is no backward pass", q, lse)
+    if q.dim() != 3 or q.shape[2] != LATENT_DIM:
+        raise ValueError(f"{what}: q must be [n_q, h_s, 576]")
+    n_q, h_s, _ = q.shape
+    n_seq = seq_lens.shape[0]
+    dev = _same_device(what, q, kv_cache, page_table, seq_lens, q_seq, lse, mass, workspace, *others)
+    _need_shaped(q, torch.bfloat16, q.shape, f"{what}: q")
+    _need_shaped(kv_cache, torch.uint8, kv_cache.shape, f"{what}: kv_cache")
+    _need_shaped(page_table, torch.int32, (n_seq, page_table.shape[-1]), f"{what}: page_table")
+    _need_shaped(seq_lens, torch.int32, (n_seq,), f"{what}: seq_lens")
+    _need_shaped(q_seq, torch.int32, (n_q,), f"{what}: q_seq")
+    _need_shaped(lse, torch.float32, (n_q, h_s), f"{what}: lse")
+    if mass is not None and (mass.dtype != torch.int64 or mass.dim() != 2 or mass.shape[0] != n_seq or
+                             (mass.stride(1) != 1 and mass.shape[1] > 1)):
+        raise ValueError(f"{what}: mass must be int64 [n_seq, max_ctx] with contiguous rows")
+    if workspace is None:
+        workspace = _scratch(stream, attn_mass_workspace_size(n_q, h_s, n_seq), q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError(f"{what}: workspace must be contiguous")
+    return dev, kv_cache.numel() // (PAGE_SIZE * KVCACHE_TOKEN_BYTES), workspace
+
+
+def attn_mass(q, kv_cache, page_table, seq_lens, q_seq, q_pos, lse, max_ctx, sm_scale, mass=None, workspace=None, stream=None):
+    """Add up how much every cached position was attended to: mass[b, p] += sum over the rows t of sequence b with
+    q_pos[t] >= p, and their heads, of exp(sm_scale q . kv[p] - lse[t, h]), in whole numbers of 1 / MASS_ONE.  q: bf16
+    [n_q, h_s, 576]; lse: fp32 [n_q, h_s], as the attention returned it; page_table: int32 [n_seq, max_pages];
+    seq_lens: int32 [n_seq], at most max_ctx; q_seq, q_pos: int32 [n_q]; mass: int64 [n_seq, max_ctx or more], or None
+    for a new one of zeros.  Returns mass."""
+    if mass is None:
+        mass = _result(stream, (seq_lens.shape[0], max_ctx), torch.int64, q.device)
+        if stream is None:
+            mass.zero_()
+        else:
+            with torch.cuda.stream(stream):
+                mass.zero_()
+    elif mass.dim() == 2 and mass.shape[1] < max_ctx:
+        raise ValueError("attn_mass: mass must have max_ctx columns")
+    dev, pages, workspace = _mass_args("attn_mass", q, kv_cache, page_table, seq_lens, q_seq, lse, mass, workspace, stream, q_pos)
+    _need_shaped(q_pos, torch.int32, q_seq.shape, "attn_mass: q_pos")
+    _call_on(dev, stream, lib().dsa_attn_mass, q.data_ptr(), q.shape[0], q.shape[1], kv_cache.data_ptr(), pages,
+             page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), seq_lens.shape[0], q_seq.data_ptr(),
+             q_pos.data_ptr(), max_ctx, sm_scale, lse.data_ptr(), mass.data_ptr(), mass.stride(0), workspace.data_ptr(),
+             workspace.nbytes)
+    return mass
+
+
+def sparse_attn_mass(q, kv_cache, page_table, seq_lens, q_seq, topk_idx, lse, sm_scale, mass=None, out=None, workspace=None,
+                     stream=None):
+    """The weights of the entries that each row selected, sum over its heads of exp(sm_scale q . kv - lse), 0 at empty
+    (negative) entries; added to mass[q_seq[t], topk_idx[t, e]] too where mass (int64 [n_seq, max_ctx]) is given.
+    topk_idx: int32 [n_q, K], as indexer_topk and decode_step return it; the others as for attn_mass.  Returns the
+    weights, fp32 [n_q, K]."""
+    dev, pages, workspace = _mass_args("sparse_attn_mass", q, kv_cache, page_table, seq_lens, q_seq, lse, mass, workspace,
+                                       stream, topk_idx, out)
+    n_q = q.shape[0]
+    _need_shaped(topk_idx, torch.int32, (n_q, topk_idx.shape[-1]), "sparse_attn_mass: topk_idx")
+    if out is None:
+        out = _result(stream, topk_idx.shape, torch.float32, q.device)
+    _need_shaped(out, torch.float32, topk_idx.shape, "sparse_attn_mass: out")
+    max_ctx = min(page_table.shape[1] * PAGE_SIZE, 1 << 20)
+    if mass is not None:
+        max_ctx = min(max_ctx, mass.shape[1])
+    _call_on(dev, stream, lib().dsa_sparse_attn_mass, q.data_ptr(), n_q, q.shape[1], kv_cache.data_ptr(), pages,
+             page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), seq_lens.shape[0], q_seq.data_ptr(),
+             topk_idx.data_ptr(), topk_idx.shape[1], max_ctx, sm_scale, lse.data_ptr(),
+             None if mass is None else mass.data_ptr(), 0 if mass is None else mass.stride(0), out.data_ptr(),
+             workspace.data_ptr(), workspace.nbytes)
+    return out
 
 
 def evict_select(mass, seq_lens, budget, sinks=0, recent=0, kept=None, new_lens=None, kept_mass=None, stream=None):

@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdsa.so")
 SOURCES = ["api.cu", "quant.cu", "indexer_tc.cu", "sfa_tc.cu", "cp_merge.cu", "rope.cu", "prefix_attn.cu", "prefix_few.cu",
-           "norm_rope.cu", "norm_rope_grad.cu", "evict.cu"]
+           "norm_rope.cu", "norm_rope_grad.cu", "evict.cu", "attn_mass.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",

@@ -597,6 +597,72 @@ int dsa_norm_rope_quant_kv(const void* k_bf16, int64_t k_stride, const float* k_
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "norm_rope_quant_kv launch");
 }
 
+static bool mass_sizes_ok(int32_t n_q, int32_t h_s) { return n_q >= 1 && n_q <= 65536 && h_s >= 1 && h_s <= 128; }
+
+// What the two kinds of accumulated weights check alike.
+static int check_mass(const char* who, const dsa::MassArgs& a, size_t workspace_bytes) {
+  if (a.n_q < 0 || a.n_seq < 0) return fail(DSA_ERR_INVALID_ARG, "%s: negative n_q or n_seq", who);
+  if (a.h_s < 1 || a.h_s > 128) return fail(DSA_ERR_UNSUPPORTED, "%s: h_s must be 1..128 (got %d)", who, a.h_s);
+  if (a.n_q > 65536) return fail(DSA_ERR_UNSUPPORTED, "%s: at most 65536 query rows a call", who);
+  if (a.max_ctx < 1 || a.max_ctx > 1048576) return fail(DSA_ERR_UNSUPPORTED, "%s: max_ctx must be 1..1048576", who);
+  if (a.max_pages < (a.max_ctx + DSA_PAGE_SIZE - 1) / DSA_PAGE_SIZE)
+    return fail(DSA_ERR_INVALID_ARG, "%s: max_pages < ceil(max_ctx / 64)", who);
+  if (a.num_pages < 1 || a.num_pages > INT64_MAX / 65536) return fail(DSA_ERR_INVALID_ARG, "%s: num_pages must be >= 1", who);
+  if (!(a.sm_scale > 0.f) || !std::isfinite(a.sm_scale))
+    return fail(DSA_ERR_INVALID_ARG, "%s: sm_scale must be positive and finite", who);
+  if (a.mass && (!spans(a.mass_stride, a.n_seq) || (a.n_seq > 1 && a.mass_stride < a.max_ctx)))
+    return fail(DSA_ERR_INVALID_ARG, "%s: mass_stride must be max_ctx or more, all rows within 2^40 elements", who);
+  if (a.n_q == 0) return DSA_OK;
+  if (a.n_seq == 0) return fail(DSA_ERR_INVALID_ARG, "%s: query rows without sequences", who);
+  if (!a.q || !a.kv_cache || !a.page_table || !a.seq_lens || !a.q_seq || !a.lse || !a.workspace)
+    return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned(a.q, 16) || !aligned(a.kv_cache, 16) || !aligned(a.page_table, 4) || !aligned(a.seq_lens, 4) ||
+      !aligned(a.q_seq, 4) || !aligned(a.q_pos, 4) || !aligned(a.idx, 4) || !aligned(a.lse, 4) || !aligned(a.mass, 8) ||
+      !aligned(a.weights, 4))
+    return fail(DSA_ERR_INVALID_ARG, "%s: q and kv_cache must be 16-byte aligned, the others to their elements", who);
+  const size_t need = dsa::mass_workspace_bytes(a.n_q, a.h_s, a.n_seq);
+  if (workspace_bytes < need || !aligned(a.workspace, 256))
+    return fail(DSA_ERR_INVALID_ARG, "%s: workspace must be >= %zu bytes and 256-byte aligned", who, need);
+  return DSA_OK;
+}
+static int run_mass(const char* who, dsa::MassArgs& a, void* stream) {
+  if (!(a.status = status_ptr())) return fail(DSA_ERR_CUDA, "%s: no CUDA device", who);
+  const char* why = nullptr;
+  cudaError_t e = dsa::launch_attn_mass(a, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return why ? fail(DSA_ERR_UNSUPPORTED, "%s", why) : cuda_fail(e, who);
+  return DSA_OK;
+}
+
+size_t dsa_attn_mass_workspace_size(int32_t n_q, int32_t h_s, int32_t n_seq) {
+  return mass_sizes_ok(n_q, h_s) && n_seq >= 1 ? dsa::mass_workspace_bytes(n_q, h_s, n_seq) : 0;
+}
+
+int dsa_attn_mass(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t* kv_cache, int64_t num_pages,
+                  const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens, int32_t n_seq,
+                  const int32_t* q_seq, const int32_t* q_pos, int32_t max_ctx, float sm_scale, const float* lse,
+                  int64_t* mass, int64_t mass_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  dsa::MassArgs a{q_bf16, n_q, h_s, kv_cache, num_pages, page_table, max_pages, seq_lens, n_seq, q_seq, q_pos, nullptr, 0,
+                  max_ctx, sm_scale, lse, mass, mass_stride, nullptr, workspace, nullptr};
+  const int rc = check_mass("attn_mass", a, workspace_bytes);
+  if (rc || n_q == 0) return rc;
+  if (!q_pos || !mass) return fail(DSA_ERR_INVALID_ARG, "attn_mass: null pointer");
+  return run_mass("attn_mass", a, stream);
+}
+
+int dsa_sparse_attn_mass(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t* kv_cache, int64_t num_pages,
+                         const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens, int32_t n_seq,
+                         const int32_t* q_seq, const int32_t* topk_idx, int32_t topk, int32_t max_ctx, float sm_scale,
+                         const float* lse, int64_t* mass, int64_t mass_stride, float* out_weights, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  dsa::MassArgs a{q_bf16, n_q, h_s, kv_cache, num_pages, page_table, max_pages, seq_lens, n_seq, q_seq, nullptr, topk_idx, topk,
+                  max_ctx, sm_scale, lse, mass, mass_stride, out_weights, workspace, nullptr};
+  if (topk < 1 || topk > 65536) return fail(DSA_ERR_UNSUPPORTED, "sparse_attn_mass: topk must be 1..65536");
+  const int rc = check_mass("sparse_attn_mass", a, workspace_bytes);
+  if (rc || n_q == 0) return rc;
+  if (!topk_idx || (!mass && !out_weights)) return fail(DSA_ERR_INVALID_ARG, "sparse_attn_mass: null pointer");
+  return run_mass("sparse_attn_mass", a, stream);
+}
+
 int dsa_evict_select(const int64_t* mass, int64_t mass_stride, const int32_t* seq_lens, int32_t n_seq, int32_t max_ctx,
                      int32_t budget, int32_t sinks, int32_t recent, int32_t* kept, int32_t* new_lens,
                      int64_t* kept_mass, void* stream) {

@@ -182,6 +182,30 @@ struct NormQuantArgs {
 };
 cudaError_t launch_norm_rope_quant(const NormQuantArgs& a, cudaStream_t s);
 
+struct MassArgs {
+  const void* q;             // bf16 [n_q][h_s][576]
+  int n_q, h_s;
+  const uint8_t* kv_cache;
+  int64_t num_pages;
+  const int32_t* page_table; // [n_seq][max_pages]
+  int max_pages;
+  const int32_t* seq_lens;
+  int n_seq;
+  const int32_t* q_seq;
+  const int32_t* q_pos;      // every position up to it; null: the entries of idx
+  const int32_t* idx;        // [n_q][topk] or null
+  int topk, max_ctx;         // max_ctx bounds the lengths
+  float sm_scale;
+  const float* lse;          // [n_q][h_s]
+  int64_t* mass;             // [n_seq] rows mass_stride apart, or null
+  int64_t mass_stride;
+  float* weights;            // [n_q][topk] or null
+  void* workspace;
+  unsigned* status;
+};
+cudaError_t launch_attn_mass(const MassArgs& a, cudaStream_t s, const char** err);
+size_t mass_workspace_bytes(int n_q, int h_s, int n_seq);
+
 struct EvictSelectArgs {
   const int64_t* mass;       // [n_seq] rows of max_ctx, mass_stride apart
   int64_t mass_stride;

@@ -435,6 +435,52 @@ int dsa_prefix_attn(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t*
                     size_t workspace_bytes, void* stream);
 
 /*
+ * Accumulated attention weights: how much each cached position was attended to.  The pages do not describe
+ * it; it is what an eviction goes by (dsa_evict_select).  Both calls take the queries and the log-sum-exps of an
+ * attention that has run (dsa_prefix_attn, dsa_sparse_attn: its out_lse) and form its probabilities again,
+ *     w[t, p] = sum_h exp(sm_scale q[t, h] . kv[p] - lse[t, h]),
+ * from the exact dequantised kv[p], with fp32 roundings alone: a weight is good to some 2^-19 times the size of
+ * its logits.  (lse as an attention returns it may hold that attention's own roundings.)
+ * mass holds whole numbers of 2^-36 (DSA_MASS_ONE is a weight of 1): additions to it are atomic, and equal calls
+ * give equal bits whatever their order.  A sum of rows is rounded to that unit for each part of the work, some
+ * hundreds of heads; the sum must stay below 2^27, one position's weight in a call counts as 2^26 at most.
+ * A head whose query or lse is NaN (or query infinite) has no weights; a position with NaN or infinite values has
+ * none either (NaN in out_weights); both flag DSA_STATUS_NAN_SCORE.  An lse of -inf (a row that saw nothing)
+ * adds nothing.  Rows whose sequence or length is out of range add nothing and flag DSA_STATUS_BAD_SEQ or
+ * _BAD_LEN; positions whose page is out of range have no weight and flag DSA_STATUS_BAD_PAGE.
+ *   q_bf16      [n_q][h_s][576] bfloat16, 16-byte aligned; n_q up to 65536, h_s 1..128.
+ *   kv_cache .. q_seq   as for dsa_prefix_attn; page_table rows from position 0 on.
+ *   max_ctx     host-side bound of seq_lens, 1..1048576; max_pages >= ceil(max_ctx / 64).
+ *   lse         [n_q][h_s] fp32, natural log.
+ *   mass        [n_seq] rows of max_ctx int64, mass_stride elements apart, added to.
+ *   workspace   dsa_attn_mass_workspace_size bytes, 256-byte aligned; nothing in it outlives the call.
+ */
+#define DSA_MASS_ONE (1ll << 36)
+
+/*
+ * dsa_attn_mass -- of every position that the rows see: row t those p < min(q_pos[t] + 1, seq_lens[b]) of its
+ * sequence b.  mass[b][p] += the sum of w[t, p] over the rows t of b.  Rows may come in any number and order.
+ */
+size_t dsa_attn_mass_workspace_size(int32_t n_q, int32_t h_s, int32_t n_seq);
+int dsa_attn_mass(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t* kv_cache, int64_t num_pages,
+                  const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens, int32_t n_seq,
+                  const int32_t* q_seq, const int32_t* q_pos, int32_t max_ctx, float sm_scale, const float* lse,
+                  int64_t* mass, int64_t mass_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dsa_sparse_attn_mass -- of the entries each row selected.
+ *   topk_idx     [n_q][topk] int32 as dsa_sparse_attn takes it, topk 1..65536: negative entries are empty; those
+ *                at or behind the sequence's length flag DSA_STATUS_BAD_INDEX and have no weight.
+ *   mass         nullable: mass[b][topk_idx[t][e]] += w[t, topk_idx[t][e]].  A position named twice counts twice.
+ *   out_weights  nullable [n_q][topk] fp32: w of each entry, 0 at empty ones.  One of the two must be given.
+ */
+int dsa_sparse_attn_mass(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t* kv_cache, int64_t num_pages,
+                         const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens, int32_t n_seq,
+                         const int32_t* q_seq, const int32_t* topk_idx, int32_t topk, int32_t max_ctx, float sm_scale,
+                         const float* lse, int64_t* mass, int64_t mass_stride, float* out_weights, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
  * Eviction.  A cache that has outgrown its room gives up the positions that attention has used least: their
  * accumulated weights decide which stay (dsa_evict_select), and the records that stay move to the sequence's first
  * positions (dsa_evict_compact), so that the pages behind them are free.  The pages do not describe it.  A
