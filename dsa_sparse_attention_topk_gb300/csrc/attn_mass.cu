@@ -35,23 +35,32 @@ namespace {
 
 constexpr int kTile = 128;                        // positions of an MMA
 constexpr int kBlocks = kLatent / 64;             // 64-dim blocks of a row
-constexpr int kMaxN = 96;                         // columns of a chunk
 constexpr int kPitch = kKvTokBytes + 16;          // a staged record: lanes 16 bytes apart modulo 128 read without conflicts
 constexpr int kStageBytes = kTile * kPitch;
-constexpr int kMaxRing = 36;                      // 64-dim blocks of queries in shared memory
-constexpr int kThreads = 512;
-constexpr int kWarpB = 0, kWarpMma = 1, kWarpRec = 2, kWarpConv0 = 4, kWarpEpi0 = 8;
-// tensor memory columns: A (32 a block), two accumulators, the scales of two tiles
+constexpr int kWarpB = 0, kWarpMma = 1, kWarpRec = 2, kWarpCol = 3, kWarpEpi0 = 8;  // 4..7 convert
+// tensor memory columns: A (32 a block), two accumulators of up to 96, the scales of two tiles
 constexpr int kColD = 32 * kBlocks, kColScale = 480;
-static_assert(kColD + 2 * kMaxN <= kColScale, "tensor memory");
 constexpr float kMassOne = 68719476736.0f;        // 2^36
 constexpr float kMassMost = 67108864.0f;          // 2^26: one addition's limit
-constexpr int kSmemMost = 232448;
+
+// What the columns of a chunk (N) decide.
+template <int N> struct Shape {
+  static constexpr int width = N == 96 || N == 64 ? 32 : N / 2;  // columns of four warps
+  static constexpr int parts = N / width;                        // of them
+  static constexpr int threads = 32 * (kWarpEpi0 + 4 * parts);
+  static constexpr int stages = N <= 32 ? 2 : 1;                 // tiles of staged records
+  static constexpr int slots = N == 96 ? 1 : N == 64 ? 2 : N == 32 ? 1 : 3;  // chunks of queries in shared memory
+  static constexpr int block = N * 128;                          // bytes of 64 dims
+  static constexpr int off_stage = slots * kBlocks * block;
+  static constexpr int off_pos = off_stage + stages * kStageBytes;
+  static constexpr int off_col = off_pos + stages * kTile * 4;   // [2][N / 2] pairs of columns, 16 bytes
+  static constexpr int off_limit = off_col + 2 * N * 8;          // [2][N] positions seen
+  static constexpr int off_ctl = off_limit + 2 * N * 4;
+};
+constexpr int kMostSlots = 3, kMostParts = 3;
 
 struct MassPlan {
-  int n;             // columns of a chunk, a multiple of 16
-  int ring;          // blocks of queries in shared memory
-  int stages;        // tiles of staged records
+  int n;             // columns of a chunk: 16, 32, 64 or 96
   int groups;
   size_t off_cols, off_groups, off_rank;
 };
@@ -175,18 +184,23 @@ mass_query_kernel(MassArgs a, MassWs ws) {
 
 // ---- the kernel -----------------------------------------------------------------------------
 struct MassCtl {
-  uint64_t b_full[kMaxRing], b_empty[kMaxRing];
-  uint64_t rec_full[8], rec_empty[8];   // [stage][quarter]
-  uint64_t a_full[5], a_empty[5];       // tiles of 128 dims
+  uint64_t b_full[kMostSlots][5], b_empty[kMostSlots][5];   // a chunk's queries, 128 dims (two blocks) a barrier
+  uint64_t rec_full[8], rec_empty[8];                       // [stage][quarter]
+  uint64_t a_full[5], a_empty[5];                           // tiles of 128 dims
   uint64_t d_full[2], d_free[2];
   uint64_t part_full[2];
+  uint64_t col_full[2], col_empty[2];
   uint64_t drained;
-  float part[2][kTile];
-  long long scan[kThreads / 32];
+  float part[2][kMostParts - 1][kTile];
+  int all_seen[2];                      // every column of the chunk sees the whole tile
+  long long scan[20];
   int start_group, start_tile, start_chunk, abort;
   long long units;
   uint32_t tmem;
 };
+constexpr int kMostSmem = 232448;
+static_assert(Shape<96>::off_ctl + sizeof(MassCtl) <= kMostSmem && Shape<64>::off_ctl + sizeof(MassCtl) <= kMostSmem &&
+              Shape<32>::off_ctl + sizeof(MassCtl) <= kMostSmem && Shape<16>::off_ctl + sizeof(MassCtl) <= kMostSmem, "shared memory");
 
 // A walk over the CTA's units, tile by tile: chunks [c0, c1) of tile `tile` of group g
 struct Walk {
@@ -194,39 +208,39 @@ struct Walk {
   int g, tile, c0, c1, chunks, tiles;
   int4 grp;
 };
-__device__ __forceinline__ void open_group(const MassWs& ws, const MassPlan& pl, Walk& w) {
+template <int N>
+__device__ __forceinline__ void open_group(const MassWs& ws, Walk& w) {
   w.grp = ws.groups[w.g];
   w.tiles = (w.grp.x + kTile - 1) / kTile;
-  w.chunks = (w.grp.z + pl.n - 1) / pl.n;
+  w.chunks = (w.grp.z + N - 1) / N;
 }
-template <bool SPARSE>
-__device__ __forceinline__ bool walk_begin(const MassWs& ws, const MassPlan& pl, const MassCtl& ctl, Walk& w) {
+template <bool SPARSE, int N>
+__device__ __forceinline__ bool walk_begin(const MassWs& ws, const MassCtl& ctl, Walk& w) {
   w.left = ctl.units;
   if (w.left <= 0) return false;
   w.g = ctl.start_group;
   w.tile = ctl.start_tile;
-  open_group(ws, pl, w);
+  open_group<N>(ws, w);
   w.c0 = SPARSE ? 0 : ctl.start_chunk;
   w.c1 = SPARSE ? w.chunks : static_cast<int>(min(static_cast<long long>(w.chunks), w.c0 + w.left));
   return true;
 }
 // on to the next tile; false at the end.  (The groups behind have units as long as some are left.)
-template <bool SPARSE>
-__device__ __forceinline__ bool walk_next(const MassWs& ws, const MassPlan& pl, Walk& w) {
+template <bool SPARSE, int N>
+__device__ __forceinline__ bool walk_next(const MassWs& ws, int groups, Walk& w) {
   w.left -= SPARSE ? 1 : w.c1 - w.c0;
   if (w.left <= 0) return false;
   if (++w.tile >= w.tiles) {
     w.tile = 0;
     do {
-      if (++w.g >= pl.groups) return false;
-      open_group(ws, pl, w);
+      if (++w.g >= groups) return false;
+      open_group<N>(ws, w);
     } while (!w.tiles || !w.chunks);
   }
   w.c0 = 0;
   w.c1 = SPARSE ? w.chunks : static_cast<int>(min(static_cast<long long>(w.chunks), w.left));
   return true;
 }
-__device__ __forceinline__ bool resident(const Walk& w, const MassPlan& pl) { return w.chunks * kBlocks <= pl.ring; }
 
 __device__ __forceinline__ uint32_t elect_leader() {
   uint32_t r;
@@ -265,17 +279,43 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// pairs of floats in one instruction
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// W columns of this warp's lanes
+template <int W>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&v)[W]) {
+  if constexpr (W == 32) tc::tmem_ld32(taddr, v);
+  else if constexpr (W == 16) tc::tmem_ld16(taddr, v);
+  else tmem_ld8(taddr, v);
+}
+// a bounded wait (tc::mbar_wait) out of line, behind one attempt in line
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* status) {
+  return tc::mbar_wait(bar, parity, abort, status);
+}
 
-template <bool SPARSE>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool SPARSE, int N>
+__global__ void __launch_bounds__(Shape<N>::threads, 1)
 attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan pl, MassWs ws) {
+  using S = Shape<N>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t block_bytes = static_cast<uint32_t>(pl.n) * 128u;
-  uint8_t* s_ring = smem;
-  uint8_t* s_stage = smem + pl.ring * block_bytes;
-  int* s_pos = reinterpret_cast<int*>(s_stage + pl.stages * kStageBytes);
-  MassCtl& ctl = *reinterpret_cast<MassCtl*>(s_pos + pl.stages * kTile);
+  uint8_t* s_stage = smem + S::off_stage;
+  int* s_pos = reinterpret_cast<int*>(smem + S::off_pos);
+  MassCtl& ctl = *reinterpret_cast<MassCtl*>(smem + S::off_ctl);
   pdl_launch_dependents();
   if (smem_u32(smem) & 1023u) {  // (the swizzled blocks need it; the same in every thread)
     if (tid == 0) flag(a.status, DSA_STATUS_INTERNAL);
@@ -283,10 +323,11 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
   }
   if (tid == 0) {
     ctl.abort = 0;
-    for (int i = 0; i < pl.ring; ++i) {
-      tc::mbar_init(&ctl.b_full[i], 1);
-      tc::mbar_init(&ctl.b_empty[i], 1);
-    }
+    for (int i = 0; i < S::slots; ++i)
+      for (int k = 0; k < 5; ++k) {
+        tc::mbar_init(&ctl.b_full[i][k], 1);
+        tc::mbar_init(&ctl.b_empty[i][k], 1);
+      }
     for (int i = 0; i < 8; ++i) {
       tc::mbar_init(&ctl.rec_full[i], 1);
       tc::mbar_init(&ctl.rec_empty[i], 1);
@@ -297,8 +338,10 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&ctl.d_full[i], 1);
-      tc::mbar_init(&ctl.d_free[i], 8);
-      tc::mbar_init(&ctl.part_full[i], 4);
+      tc::mbar_init(&ctl.d_free[i], 4 * S::parts);
+      tc::mbar_init(&ctl.part_full[i], 4 * (S::parts - 1));
+      tc::mbar_init(&ctl.col_full[i], 1);
+      tc::mbar_init(&ctl.col_empty[i], 4 * S::parts);
     }
     tc::mbar_init(&ctl.drained, 1);
     tc::mbar_fence_init();
@@ -308,13 +351,13 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
   pdl_wait();
   // ---- the CTA's share of the units ----
   {
-    const int per = (pl.groups + kThreads - 1) / kThreads;
+    const int per = (pl.groups + S::threads - 1) / S::threads;
     const int g0 = min(tid * per, pl.groups), g1 = min(g0 + per, pl.groups);
     long long sum = 0;
     auto units_of = [&](int g) {
       const int4 grp = ws.groups[g];
       const long long tiles = (grp.x + kTile - 1) / kTile;
-      return grp.z == 0 ? 0ll : SPARSE ? tiles : tiles * ((grp.z + pl.n - 1) / pl.n);
+      return grp.z == 0 ? 0ll : SPARSE ? tiles : tiles * ((grp.z + N - 1) / N);
     };
     for (int g = g0; g < g1; ++g) sum += units_of(g);
     long long incl = sum;
@@ -326,7 +369,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
     if (lane == 31) ctl.scan[warp] = incl;
     __syncthreads();
     long long before = incl - sum, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < S::threads / 32; ++w) {
       if (w < warp) before += ctl.scan[w];
       total += ctl.scan[w];
     }
@@ -336,7 +379,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
       int g = g0;
       long long rest = start - before;
       for (long long u; rest >= (u = units_of(g)); ++g) rest -= u;
-      const int chunks = (ws.groups[g].z + pl.n - 1) / pl.n;
+      const int chunks = (ws.groups[g].z + N - 1) / N;
       ctl.start_group = g;
       ctl.start_tile = static_cast<int>(SPARSE ? rest : rest / chunks);
       ctl.start_chunk = static_cast<int>(SPARSE ? 0 : rest % chunks);
@@ -348,81 +391,102 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
   const uint32_t tmem = ctl.tmem;
   volatile int* abort = &ctl.abort;
   // (a warp that waits as a whole leaves as a whole: an abort may reach its lanes at different times)
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return tc::mbar_wait(bar, parity & 1u, abort, a.status); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return tc::mbar_try_wait(bar, parity & 1u) || wait_on(bar, parity & 1u, &ctl.abort, a.status);
+  };
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+  // chunk slots in order; of a group whose chunks all fit, the slots stay while its tiles last
+  auto skip = [](int& slot, uint32_t& phase, int by) {  // (by at most all slots)
+    slot += by;
+    if (slot >= S::slots) {
+      slot -= S::slots;
+      phase ^= 1u;
+    }
+  };
   Walk w;
 
   if (warp == kWarpB) {
-    // ---- the columns' queries: 64 dims of a chunk at a time ----
-    if (lane == 0 && walk_begin<SPARSE>(ws, pl, ctl, w)) {
-      long long n = 0;
-      int have = -1;
-      auto load = [&](int c, int kb) {
-        const int slot = static_cast<int>(n % pl.ring);
-        if (!wait(&ctl.b_empty[slot], static_cast<uint32_t>(n / pl.ring) ^ 1u)) return false;
-        tc::mbar_arrive_expect_tx(&ctl.b_full[slot], block_bytes);
-        tc::tma_load_3d(s_ring + slot * block_bytes, &q_map, kb * 64, w.grp.y + c * pl.n, 0, &ctl.b_full[slot]);
-        ++n;
-        return true;
-      };
+    // ---- the columns' queries: 128 dims of a chunk at a time ----
+    if (lane == 0 && walk_begin<SPARSE, N>(ws, ctl, w)) {
+      int slot = 0, have = -1;
+      uint32_t phase = 0;
       bool ok = true;
       do {
-        const bool keep = resident(w, pl);
+        const bool keep = w.chunks <= S::slots;
         if (keep && have == w.g) continue;
         have = w.g;
         const int c0 = keep ? 0 : w.c0, c1 = keep ? w.chunks : w.c1;
-        for (int c = c0; ok && c < c1; ++c)
-          for (int kb = 0; ok && kb < kBlocks; ++kb) ok = load(c, kb);
-      } while (ok && walk_next<SPARSE>(ws, pl, w));
-      // copies in flight must land before the CTA ends (a share may not use all chunks of a group that stays)
-      for (long long i = max(0ll, n - pl.ring); i < n; ++i)
-        tc::mbar_drain(&ctl.b_full[i % pl.ring], static_cast<uint32_t>(i / pl.ring) & 1u, 100000000ull);
+        for (int c = c0; ok && c < c1; ++c) {
+          for (int k = 0; k < 5; ++k) {
+            ok = wait(&ctl.b_empty[slot][k], phase ^ 1u);
+            if (!ok) break;
+            uint64_t* bar = &ctl.b_full[slot][k];
+            uint8_t* to = smem + (slot * kBlocks + 2 * k) * S::block;
+            tc::mbar_arrive_expect_tx(bar, (k < 4 ? 2 : 1) * S::block);
+            tc::tma_load_3d(to, &q_map, 128 * k, w.grp.y + c * N, 0, bar);
+            if (k < 4) tc::tma_load_3d(to + S::block, &q_map, 128 * k + 64, w.grp.y + c * N, 0, bar);
+          }
+          if (ok) skip(slot, phase, 1);
+        }
+      } while (ok && walk_next<SPARSE, N>(ws, pl.groups, w));
+      // copies in flight must land before the CTA ends (a share may not use all chunks of a group that stays); a
+      // slot that was never loaded is past the phase before its first
+      for (int i = 0; i < S::slots; ++i)
+        for (int k = 0; k < 5; ++k) tc::mbar_drain(&ctl.b_full[i][k], i < slot ? phase : phase ^ 1u, 100000000ull);
+      if (*abort) __nanosleep(1000000);  // (and those of a chunk begun)
     }
   } else if (warp == kWarpMma) {
     // ---- products ----
     const uint32_t leader = elect_leader();
-    const uint32_t idesc = idesc_f16(pl.n);
-    long long n = 0, base = 0;   // blocks of queries taken; of a resident group, its first
-    uint32_t d = 0, visit = 0;
-    if (walk_begin<SPARSE>(ws, pl, ctl, w)) {
+    constexpr uint32_t idesc = idesc_f16(N);
+    const uint64_t desc0 = tc::desc_kmajor_sw128(smem_u32(smem));
+    int slot = 0, base = 0;  // the next chunk's; of a group that stays, its first
+    uint32_t phase = 0, base_phase = 0, d = 0, visit = 0;
+    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
       bool ok = true, more = true;
       int have = -1;
       while (ok && more) {
-        const bool keep = resident(w, pl);
+        const bool keep = w.chunks <= S::slots;
         if (keep && have != w.g) {
-          base = n;
-          n += w.chunks * kBlocks;
+          base = slot;
+          base_phase = phase;
+          skip(slot, phase, w.chunks);
         }
         have = w.g;
         const int g = w.g, c0 = w.c0, c1 = w.c1, chunks = w.chunks;
-        more = walk_next<SPARSE>(ws, pl, w);
+        more = walk_next<SPARSE, N>(ws, pl.groups, w);
         const bool leave = !more || w.g != g;
         for (int c = c0; ok && c < c1; ++c) {
-          const long long first = keep ? base + c * kBlocks : n;
-          if (!keep) n += kBlocks;
-          for (int s = 0; ok && s < 5; ++s, ++d) {
-            if (c == c0) ok = wait_warp(&ctl.a_full[s], visit);
-            ok = ok && wait_warp(&ctl.d_free[d & 1], (d >> 1) ^ 1u);
-            const int blocks = s < 4 ? 2 : 1;
-            for (int j = 0; ok && j < blocks; ++j) {
-              const int kb = 2 * s + j;
-              const int slot = static_cast<int>((first + kb) % pl.ring);
-              ok = wait_warp(&ctl.b_full[slot], static_cast<uint32_t>((first + kb) / pl.ring));
-              if (!ok) break;
-              tc::fence_after_sync();
-              const uint64_t desc = tc::desc_kmajor_sw128(smem_u32(s_ring + slot * block_bytes));
+          int at = keep ? base : slot;
+          uint32_t ph = keep ? base_phase : phase;
+          if (keep) skip(at, ph, c);
+          else skip(slot, phase, 1);
+          const uint64_t desc = desc0 + static_cast<uint32_t>(at * kBlocks * S::block >> 4);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_f16_ts(tmem + kColD + (d & 1) * pl.n, tmem + 32 * kb + 8 * k, desc + 2 * k, idesc, j + k > 0, leader);
-              if (!keep || leave && c == c1 - 1 && chunks == 1) commit_if(&ctl.b_empty[slot], leader);
-            }
+          for (int s = 0; s < 5; ++s) {
+            if (c == c0) ok = ok && wait_warp(&ctl.a_full[s], visit);
+            ok = ok && wait_warp(&ctl.d_free[d & 1], (d >> 1) ^ 1u);
+            ok = ok && wait_warp(&ctl.b_full[at][s], ph);
             if (!ok) break;
+            tc::fence_after_sync();
+            const uint32_t to = tmem + kColD + (d & 1) * N;
+#pragma unroll
+            for (int k = 0; k < (s < 4 ? 8 : 4); ++k)
+              mma_f16_ts(to, tmem + 64 * s + 8 * k, desc + ((2 * s + k / 4) * S::block >> 4) + 2 * (k & 3), idesc, k > 0, leader);
             commit_if(&ctl.d_full[d & 1], leader);
+            if (!keep) commit_if(&ctl.b_empty[at][s], leader);
             if (c == c1 - 1) commit_if(&ctl.a_empty[s], leader);
+            ++d;
           }
         }
-        if (ok && keep && leave && chunks > 1)  // the group's blocks go once its last product is done
-          for (int i = 0; i < chunks * kBlocks; ++i) commit_if(&ctl.b_empty[(base + i) % pl.ring], leader);
+        if (ok && keep && leave) {  // the group's slots go once its last product is done
+          int at = base;
+          uint32_t ph = base_phase;
+          for (int c = 0; c < chunks; ++c) {
+            for (int k = 0; k < 5; ++k) commit_if(&ctl.b_empty[at][k], leader);
+            skip(at, ph, 1);
+          }
+        }
         ++visit;
       }
     }
@@ -433,70 +497,116 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
     }
   } else if (warp == kWarpRec) {
     // ---- records of a tile, 32 to a converting warp, a bulk copy a lane ----
-    if (walk_begin<SPARSE>(ws, pl, ctl, w)) {
+    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
       const int64_t table_end = static_cast<int64_t>(a.max_pages) * kPage;
-      auto find = [&](const Walk& at, int quarter, int& pos) -> const uint8_t* {
-        const int i = at.tile * kTile + quarter * 32 + lane;
-        pos = -1;
-        if (i >= at.grp.x) return nullptr;
-        int p = i;
-        if (SPARSE) {
-          p = a.idx[static_cast<int64_t>(at.g) * a.topk + i];
-          if (p < 0) return nullptr;
-          if (p >= a.seq_lens[at.grp.w] || p >= table_end) {
+      // the records of a tile, one of each quarter a lane: positions (-1: none) and where they lie.  All loads of
+      // a tile are under way together, while the copies of the tile before are.
+      auto find = [&](const Walk& at, int (&pos)[4], const uint8_t* (&src)[4]) {
+        const int len = SPARSE ? a.seq_lens[at.grp.w] : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = at.tile * kTile + k * 32 + lane;
+          pos[k] = i < at.grp.x ? (SPARSE ? a.idx[static_cast<int64_t>(at.g) * a.topk + i] : i) : -1;
+        }
+        int page[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (SPARSE && pos[k] >= 0 && (pos[k] >= len || pos[k] >= table_end)) {
             flag(a.status, DSA_STATUS_BAD_INDEX);
-            return nullptr;
+            pos[k] = -1;
           }
+          page[k] = pos[k] >= 0 ? a.page_table[static_cast<int64_t>(at.grp.w) * a.max_pages + pos[k] / kPage] : 0;
         }
-        const int page = a.page_table[static_cast<int64_t>(at.grp.w) * a.max_pages + p / kPage];
-        if (page < 0 || page >= a.num_pages) {
-          flag(a.status, DSA_STATUS_BAD_PAGE);
-          return nullptr;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (pos[k] >= 0 && (page[k] < 0 || page[k] >= a.num_pages)) {
+            flag(a.status, DSA_STATUS_BAD_PAGE);
+            pos[k] = -1;
+          }
+          pos[k] = max(pos[k], -1);
+          src[k] = a.kv_cache + (static_cast<int64_t>(page[k]) * kPage + (pos[k] & (kPage - 1))) * kKvTokBytes;
         }
-        pos = p;
-        return a.kv_cache + (static_cast<int64_t>(page) * kPage + p % kPage) * kKvTokBytes;
       };
       uint32_t visit = 0;
       bool ok = true, more = true;
       while (ok && more) {
-        const int stage = static_cast<int>(visit % pl.stages);
-        const uint32_t phase = visit / pl.stages;
-        for (int quarter = 0; ok && quarter < 4; ++quarter) {
-          int pos;
-          const uint8_t* src = find(w, quarter, pos);
-          const unsigned there = __ballot_sync(0xffffffffu, src != nullptr);
-          ok = wait_warp(&ctl.rec_empty[stage * 4 + quarter], phase ^ 1u);
+        const int stage = static_cast<int>(visit % S::stages);
+        const uint32_t phase = visit / S::stages;
+        int pos[4];
+        const uint8_t* src[4];
+        find(w, pos, src);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const unsigned there = __ballot_sync(0xffffffffu, pos[k] >= 0);
+          ok = ok && wait_warp(&ctl.rec_empty[stage * 4 + k], phase ^ 1u);
           if (!ok) break;
-          s_pos[stage * kTile + quarter * 32 + lane] = pos;
+          s_pos[stage * kTile + k * 32 + lane] = pos[k];
           __syncwarp();
-          uint64_t* bar = &ctl.rec_full[stage * 4 + quarter];
+          uint64_t* bar = &ctl.rec_full[stage * 4 + k];
           if (lane == 0) tc::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(there)) * kKvTokBytes);
           __syncwarp();
-          if (src) tc::bulk_load(s_stage + stage * kStageBytes + (quarter * 32 + lane) * kPitch, src, kKvTokBytes, bar);
+          if (pos[k] >= 0) tc::bulk_load(s_stage + stage * kStageBytes + (k * 32 + lane) * kPitch, src[k], kKvTokBytes, bar);
         }
         if (!ok) break;
-        more = walk_next<SPARSE>(ws, pl, w);
+        more = walk_next<SPARSE, N>(ws, pl.groups, w);
         ++visit;
       }
-      if (*abort && lane == 0)  // (a barrier that was never armed is past the phase before its first)
-        for (uint32_t v = visit + 1 > static_cast<uint32_t>(pl.stages) ? visit + 1 - pl.stages : 0; v < visit; ++v)
+      if (*abort && lane == 0)  // copies in flight must land before the CTA ends
+        for (uint32_t v = visit > static_cast<uint32_t>(S::stages) ? visit - S::stages : 0; v < visit; ++v)
           for (int quarter = 0; quarter < 4; ++quarter)
-            tc::mbar_drain(&ctl.rec_full[(v % pl.stages) * 4 + quarter], (v / pl.stages) & 1u, 100000000ull);
+            tc::mbar_drain(&ctl.rec_full[(v % S::stages) * 4 + quarter], (v / S::stages) & 1u, 100000000ull);
       if (*abort) __nanosleep(1000000);  // (and those of a tile begun)
     }
-  } else if (warp >= kWarpConv0 && warp < kWarpConv0 + 4) {
+  } else if (warp == kWarpCol) {
+    // ---- the columns' constants, a chunk ahead of the weights; columns behind the group's last have no weight ----
+    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
+      uint32_t n = 0;
+      bool ok = true, more = true;
+      while (ok && more) {
+        for (int c = w.c0; ok && c < w.c1; ++c, ++n) {
+          const int buf = n & 1;
+          float4 info[(N + 31) / 32];
+          int least = INT32_MAX;
+#pragma unroll
+          for (int i = 0; i < (N + 31) / 32; ++i) {
+            const int col = c * N + 32 * i + lane;
+            info[i] = make_float4(0.f, -INFINITY, __int_as_float(INT32_MAX), 0.f);
+            if (32 * i + lane < N && col < w.grp.z) info[i] = ws.cols[w.grp.y + col];
+            least = min(least, __float_as_int(info[i].z));
+          }
+          least = __reduce_min_sync(0xffffffffu, least);
+          ok = wait_warp(&ctl.col_empty[buf], (n >> 1) ^ 1u);
+          if (!ok) break;
+          float* pairs = reinterpret_cast<float*>(smem + S::off_col) + buf * 2 * N;
+          int* limits = reinterpret_cast<int*>(smem + S::off_limit) + buf * N;
+#pragma unroll
+          for (int i = 0; i < (N + 31) / 32; ++i) {
+            const int at = 32 * i + lane;
+            if (at >= N) continue;
+            pairs[4 * (at >> 1) + (at & 1)] = info[i].x;
+            pairs[4 * (at >> 1) + 2 + (at & 1)] = info[i].y;
+            limits[at] = __float_as_int(info[i].z);
+          }
+          if (lane == 0) ctl.all_seen[buf] = SPARSE || least >= (w.tile + 1) * kTile;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&ctl.col_full[buf]);
+        }
+        more = ok && walk_next<SPARSE, N>(ws, pl.groups, w);
+      }
+    }
+  } else if (warp < kWarpEpi0) {
     // ---- codes widened to fp16 into tensor memory, a position a lane ----
     const int quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     uint32_t visit = 0;
-    if (walk_begin<SPARSE>(ws, pl, ctl, w)) {
+    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
       bool ok = true, more = true;
       while (ok && more) {
-        const int stage = static_cast<int>(visit % pl.stages);
-        ok = wait_warp(&ctl.rec_full[stage * 4 + quarter], visit / pl.stages);
+        const int stage = static_cast<int>(visit % S::stages);
+        ok = wait_warp(&ctl.rec_full[stage * 4 + quarter], visit / S::stages);
+        if (!ok) break;
         const int row = quarter * 32 + lane;
         const uint8_t* rec = s_stage + stage * kStageBytes + row * kPitch;
-        const int pos = s_pos[stage * kTile + row];
         uint32_t scales[8];
         bool fine = true;
 #pragma unroll
@@ -506,10 +616,11 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
           scales[i] = __float_as_uint(v);
         }
         if (!fine) scales[0] = 0x7FC00000u;  // NaN: the position has no weight
-        scales[5] = static_cast<uint32_t>(pos);
+        scales[5] = static_cast<uint32_t>(s_pos[stage * kTile + row]);
         scales[6] = scales[7] = 0;
+#pragma unroll 1
         for (int s = 0; s < 5; ++s) {
-          ok = ok && wait_warp(&ctl.a_empty[s], visit ^ 1u);
+          ok = wait_warp(&ctl.a_empty[s], visit ^ 1u);
           if (!ok) break;
           tc::fence_after_sync();
           if (s == 0) tmem_st8(tmem + lanes + kColScale + 8 * (visit & 1), scales);
@@ -534,29 +645,27 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
           if (lane == 0) tc::mbar_arrive(&ctl.a_full[s]);
         }
         if (!ok) break;
-        __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ctl.rec_empty[stage * 4 + quarter]);
-        more = walk_next<SPARSE>(ws, pl, w);
+        more = walk_next<SPARSE, N>(ws, pl.groups, w);
         ++visit;
       }
     }
-  } else if (warp >= kWarpEpi0) {
-    // ---- weights: eight warps, a position a lane, half of a chunk's columns each four ----
+  } else {
+    // ---- weights: a position a lane, S::width of a chunk's columns each four warps ----
+    constexpr int W = S::width;
     const int quarter = warp & 3, part = (warp - kWarpEpi0) >> 2, row = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const int width = pl.n / 2;  // a multiple of 8
-    uint32_t d = 0, visit = 0;
-    if (walk_begin<SPARSE>(ws, pl, ctl, w)) {
+    uint32_t d = 0, n = 0, visit = 0;
+    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
       bool ok = true, more = true;
       while (ok && more) {
-        float scale[5], total = 0.f;
+        uint64_t scale[5];
+        float total = 0.f;
         int pos = -1;
         for (int c = w.c0; ok && c < w.c1; ++c) {
-          float acc[kMaxN / 2];
+          uint64_t acc[W / 2];
 #pragma unroll
-          for (int i = 0; i < kMaxN / 2; ++i) acc[i] = 0.f;
-#pragma unroll
-          for (int s = 0; s < 5; ++s, ++d) {
+          for (int s = 0; s < 5; ++s) {
             ok = ok && wait_warp(&ctl.d_full[d & 1], d >> 1);
             if (!ok) break;
             tc::fence_after_sync();
@@ -565,57 +674,72 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
               tmem_ld8(tmem + lanes + kColScale + 8 * (visit & 1), v);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 5; ++i) scale[i] = __uint_as_float(v[i]);
+              for (int i = 0; i < 5; ++i) scale[i] = pair(__uint_as_float(v[i]), __uint_as_float(v[i]));
               pos = static_cast<int>(v[5]);
             }
-            const uint32_t at = tmem + lanes + kColD + (d & 1) * pl.n + part * width;
-#pragma unroll
-            for (int g = 0; g < kMaxN / 16; ++g) {
-              if (8 * g >= width) break;
-              uint32_t v[8];
-              tmem_ld8(at + 8 * g, v);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 8; ++i) acc[8 * g + i] = fmaf(scale[s], __uint_as_float(v[i]), acc[8 * g + i]);
-            }
+            uint32_t v[W];
+            tmem_load<W>(tmem + lanes + kColD + (d & 1) * N + part * W, v);
+            tc::tmem_wait_ld();
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&ctl.d_free[d & 1]);
-          }
-          if (!ok) break;
-          const int col = c * pl.n + part * width;
-          const float4* info = ws.cols + w.grp.y + col;
-          float sum = 0.f;
+            ++d;
 #pragma unroll
-          for (int i = 0; i < kMaxN / 2; ++i) {
-            if (i >= width || col + i >= w.grp.z) break;
-            const float4 k = __ldg(info + i);
-            const float e = ex2(fmaf(acc[i], k.x, k.y));
-            sum += SPARSE || pos < __float_as_int(k.z) ? e : 0.f;
+            for (int i = 0; i < W / 2; ++i)
+              acc[i] = fma_pair(scale[s], pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s ? acc[i] : 0ull);
           }
+          const int buf = n & 1;
+          ok = ok && wait_warp(&ctl.col_full[buf], n >> 1);
+          if (!ok) break;
+          ++n;
+          const ulonglong2* cols = reinterpret_cast<const ulonglong2*>(smem + S::off_col) + (buf * N + part * W) / 2;
+          float sum = 0.f;
+          if (ctl.all_seen[buf]) {
+            float odd = 0.f;
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) {
+              const ulonglong2 k = cols[i];
+              const float2 x = unpair(fma_pair(acc[i], k.x, k.y));
+              sum += ex2(x.x);
+              odd += ex2(x.y);
+            }
+            sum += odd;
+          } else {
+            const int2* limits = reinterpret_cast<const int2*>(smem + S::off_limit) + (buf * N + part * W) / 2;
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) {
+              const ulonglong2 k = cols[i];
+              const int2 lim = limits[i];
+              const float2 x = unpair(fma_pair(acc[i], k.x, k.y));
+              sum += (pos < lim.x ? ex2(x.x) : 0.f) + (pos < lim.y ? ex2(x.y) : 0.f);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&ctl.col_empty[buf]);
           total += sum;
         }
         if (!ok) break;
-        // (the second four's sum of the tile before last has been read: d_free holds them within two accumulators)
-        if (part == 1) {
-          ctl.part[visit & 1][row] = total;
+        // (the other parts' sums of the tile before last have been read: d_free holds all parts within two accumulators)
+        if (part > 0) {
+          ctl.part[visit & 1][part - 1][row] = total;
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&ctl.part_full[visit & 1]);
         } else {
           ok = wait_warp(&ctl.part_full[visit & 1], visit >> 1);
           if (!ok) break;
-        }
-        if (part == 0 && pos >= 0) {
-          total += ctl.part[visit & 1][row];
-          if (SPARSE && a.weights) a.weights[static_cast<int64_t>(w.g) * a.topk + w.tile * kTile + row] = total;
-          if (a.mass) {
-            if (total != total) flag(a.status, DSA_STATUS_NAN_SCORE);
-            else if (total > 0.f)
-              atomicAdd(reinterpret_cast<unsigned long long*>(a.mass + static_cast<int64_t>(w.grp.w) * a.mass_stride + pos),
-                        static_cast<unsigned long long>(__float2ll_rn(fminf(total, kMassMost) * kMassOne)));
+          if (pos >= 0) {
+#pragma unroll
+            for (int i = 0; i < S::parts - 1; ++i) total += ctl.part[visit & 1][i][row];
+            if (SPARSE && a.weights) a.weights[static_cast<int64_t>(w.g) * a.topk + w.tile * kTile + row] = total;
+            if (a.mass) {
+              if (total != total) flag(a.status, DSA_STATUS_NAN_SCORE);
+              else if (total > 0.f)
+                atomicAdd(reinterpret_cast<unsigned long long*>(a.mass + static_cast<int64_t>(w.grp.w) * a.mass_stride + pos),
+                          static_cast<unsigned long long>(__float2ll_rn(fminf(total, kMassMost) * kMassOne)));
+            }
           }
         }
-        more = walk_next<SPARSE>(ws, pl, w);
+        more = walk_next<SPARSE, N>(ws, pl.groups, w);
         ++visit;
       }
     }
@@ -631,14 +755,9 @@ size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 MassPlan make_plan(int n_q, int h_s, int n_seq, bool sparse) {
   MassPlan p;
   p.groups = sparse ? n_q : n_seq;
-  // a chunk's columns: those of a group of average rows in as few chunks as they need, evenly
+  // a chunk's columns: all of a group of average rows where they fit; of more than 128 as many as there can be
   const int64_t cols = static_cast<int64_t>(h_s) * (sparse ? 1 : std::max(1, (n_q + n_seq - 1) / n_seq));
-  const int64_t chunks = (cols + kMaxN - 1) / kMaxN;
-  p.n = static_cast<int>(round_up(static_cast<size_t>((cols + chunks - 1) / chunks), 16));
-  // a second tile of records where the columns leave room for it
-  p.stages = cols <= 48 ? 2 : 1;
-  const int rest = kSmemMost - p.stages * (kStageBytes + kTile * 4) - static_cast<int>(round_up(sizeof(MassCtl), 128));
-  p.ring = std::min(kMaxRing, rest / (p.n * 128));
+  p.n = cols <= 16 ? 16 : cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 96 ? 96 : cols <= 128 ? 64 : 96;
   const size_t columns = static_cast<size_t>(n_q) * h_s;
   p.off_cols = round_up(columns * kLatent * 2, 256);
   p.off_groups = p.off_cols + round_up(columns * 16, 256);
@@ -659,6 +778,14 @@ EncodeFn encode_fn() {
     return static_cast<EncodeFn>(nullptr);
   }();
   return fn;
+}
+
+template <bool SPARSE, int N>
+cudaError_t launch_main(const CUtensorMap& q_map, const MassArgs& a, const MassPlan& pl, const MassWs& ws, int grid, cudaStream_t s) {
+  constexpr size_t smem = Shape<N>::off_ctl + sizeof(MassCtl);
+  const cudaError_t e = cudaFuncSetAttribute(attn_mass_kernel<SPARSE, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_mass_kernel<SPARSE, N>, dim3(static_cast<unsigned>(grid)), dim3(Shape<N>::threads), smem, s, 1, q_map, a, pl, ws);
 }
 
 }  // namespace
@@ -689,10 +816,7 @@ cudaError_t launch_attn_mass(const MassArgs& a, cudaStream_t s, const char** err
     *err = "attn_mass: tensor map encoding failed";
     return cudaErrorInvalidValue;
   }
-  const auto kernel = sparse ? attn_mass_kernel<true> : attn_mass_kernel<false>;
-  const size_t smem = static_cast<size_t>(pl.ring) * pl.n * 128 + pl.stages * (kStageBytes + kTile * 4) + round_up(sizeof(MassCtl), 128);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
   if (!sparse) {
     const int64_t threads = static_cast<int64_t>(a.n_q) + a.n_seq;
     e = launch_pdl(mass_order_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, s, 1, a, ws);
@@ -704,8 +828,13 @@ cudaError_t launch_attn_mass(const MassArgs& a, cudaStream_t s, const char** err
   const int64_t tiles = ((sparse ? a.topk : a.max_ctx) + kTile - 1) / kTile;
   const int64_t rows = sparse ? 1 : a.n_q;
   const int64_t units = tiles * (sparse ? a.n_q : static_cast<int64_t>(a.n_seq) * ((rows * a.h_s + pl.n - 1) / pl.n));
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(multiprocessors(), units));
-  return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, 1, q_map, a, pl, ws);
+  const int grid = static_cast<int>(std::min<int64_t>(multiprocessors(), units));
+  switch (pl.n) {
+    case 16: return sparse ? launch_main<true, 16>(q_map, a, pl, ws, grid, s) : launch_main<false, 16>(q_map, a, pl, ws, grid, s);
+    case 32: return sparse ? launch_main<true, 32>(q_map, a, pl, ws, grid, s) : launch_main<false, 32>(q_map, a, pl, ws, grid, s);
+    case 64: return sparse ? launch_main<true, 64>(q_map, a, pl, ws, grid, s) : launch_main<false, 64>(q_map, a, pl, ws, grid, s);
+    default: return sparse ? launch_main<true, 96>(q_map, a, pl, ws, grid, s) : launch_main<false, 96>(q_map, a, pl, ws, grid, s);
+  }
 }
 
 }  // namespace dsa
