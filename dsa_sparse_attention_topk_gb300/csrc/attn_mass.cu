@@ -14,13 +14,13 @@
 // m holds whole numbers of 2^-36 and takes additions atomically: integers add up the same in any order, so equal
 // calls give equal bits.
 //
-// Layout.  M = 128 positions (a TMEM lane each), N = up to 96 columns, a column being one head of one query
+// Layout.  M = 128 positions (a TMEM lane each), N = up to 64 columns, a column being one head of one query
 // row; the sum over columns then stays within a thread.  Positions are the A operand in tensor memory, 288
 // columns of widened codes; the columns' queries stream through shared memory by TMA in blocks of 64 dims, or stay there
 // while a group's columns fit.  A group is a sequence with its rows (dense) or one row with its entries
 // (sparse); units (group, tile of 128 positions, chunk of N columns) are shared out evenly over one CTA per SM.
 //
-// Bound: tensor cores with many columns (128 x 96 x 576 products a chunk); the cache's bytes with few.
+// Bound: tensor cores with many columns (128 x 64 x 576 products a chunk); the cache's bytes with few.
 
 #include <cuda.h>
 
@@ -37,30 +37,30 @@ constexpr int kTile = 128;                        // positions of an MMA
 constexpr int kBlocks = kLatent / 64;             // 64-dim blocks of a row
 constexpr int kPitch = kKvTokBytes + 16;          // a staged record: lanes 16 bytes apart modulo 128 read without conflicts
 constexpr int kStageBytes = kTile * kPitch;
-constexpr int kWarpB = 0, kWarpMma = 1, kWarpRec = 2, kWarpCol = 3, kWarpEpi0 = 8;  // 4..7 convert
-// tensor memory columns: A (32 a block), two accumulators of up to 96, the scales of two tiles
-constexpr int kColD = 32 * kBlocks, kColScale = 480;
+constexpr int kWarpB = 0, kWarpMma0 = 1, kWarpConv0 = 4, kWarpEpi0 = 8;  // (products: 1 and 2; 3 idles)
+// tensor memory columns: A (32 a block), three accumulators of up to 64, the scales of two tiles, partial sums
+constexpr int kColD = 32 * kBlocks, kSlotsD = 3, kColScale = 480, kColPart = 496;
+constexpr int kSets = 2;                          // sets of warps that take chunks in turn
 constexpr float kMassOne = 68719476736.0f;        // 2^36
 constexpr float kMassMost = 67108864.0f;          // 2^26: one addition's limit
 
 // What the columns of a chunk (N) decide.
 template <int N> struct Shape {
-  static constexpr int width = N == 96 || N == 64 ? 32 : N / 2;  // columns of four warps
-  static constexpr int parts = N / width;                        // of them
-  static constexpr int threads = 32 * (kWarpEpi0 + 4 * parts);
-  static constexpr int stages = N <= 32 ? 2 : 1;                 // tiles of staged records
-  static constexpr int slots = N == 96 ? 1 : N == 64 ? 2 : N == 32 ? 1 : 3;  // chunks of queries in shared memory
+  static constexpr int width = N < 32 ? N : 32;   // columns of four warps
+  static constexpr int parts = N / width;         // of them in a set
+  static constexpr int threads = 32 * (kWarpEpi0 + 4 * parts * kSets);
+  static constexpr int stages = N <= 32 ? 2 : 1;  // tiles of staged records
+  static constexpr int slots = N == 64 ? 2 : N == 32 ? 1 : 3;    // chunks of queries in shared memory
   static constexpr int block = N * 128;                          // bytes of 64 dims
   static constexpr int off_stage = slots * kBlocks * block;
-  static constexpr int off_pos = off_stage + stages * kStageBytes;
-  static constexpr int off_col = off_pos + stages * kTile * 4;   // [2][N / 2] pairs of columns, 16 bytes
+  static constexpr int off_col = off_stage + stages * kStageBytes;  // [2][N / 2] pairs of columns, 16 bytes
   static constexpr int off_limit = off_col + 2 * N * 8;          // [2][N] positions seen
   static constexpr int off_ctl = off_limit + 2 * N * 4;
 };
-constexpr int kMostSlots = 3, kMostParts = 3;
+constexpr int kMostSlots = 3;
 
 struct MassPlan {
-  int n;             // columns of a chunk: 16, 32, 64 or 96
+  int n;             // columns of a chunk: 16, 32 or 64
   int groups;
   size_t off_cols, off_groups, off_rank;
 };
@@ -185,21 +185,19 @@ mass_query_kernel(MassArgs a, MassWs ws) {
 // ---- the kernel -----------------------------------------------------------------------------
 struct MassCtl {
   uint64_t b_full[kMostSlots][5], b_empty[kMostSlots][5];   // a chunk's queries, 128 dims (two blocks) a barrier
-  uint64_t rec_full[8], rec_empty[8];                       // [stage][quarter]
   uint64_t a_full[5], a_empty[5];                           // tiles of 128 dims
-  uint64_t d_full[2], d_free[2];
+  uint64_t d_full[kSets][kSlotsD], d_free[kSlotsD];         // (a set waits for its own chunks alone)
   uint64_t part_full[2];
   uint64_t col_full[2], col_empty[2];
-  uint64_t drained;
-  float part[2][kMostParts - 1][kTile];
+  uint64_t drained[2];
   int all_seen[2];                      // every column of the chunk sees the whole tile
-  long long scan[20];
+  long long scan[24];
   int start_group, start_tile, start_chunk, abort;
   long long units;
   uint32_t tmem;
 };
 constexpr int kMostSmem = 232448;
-static_assert(Shape<96>::off_ctl + sizeof(MassCtl) <= kMostSmem && Shape<64>::off_ctl + sizeof(MassCtl) <= kMostSmem &&
+static_assert(Shape<64>::off_ctl + sizeof(MassCtl) <= kMostSmem &&
               Shape<32>::off_ctl + sizeof(MassCtl) <= kMostSmem && Shape<16>::off_ctl + sizeof(MassCtl) <= kMostSmem, "shared memory");
 
 // A walk over the CTA's units, tile by tile: chunks [c0, c1) of tile `tile` of group g
@@ -295,12 +293,13 @@ __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-// W columns of this warp's lanes
-template <int W>
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&v)[W]) {
-  if constexpr (W == 32) tc::tmem_ld32(taddr, v);
-  else if constexpr (W == 16) tc::tmem_ld16(taddr, v);
-  else tmem_ld8(taddr, v);
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" :: "r"(taddr), "r"(__float_as_uint(v)) : "memory");
 }
 // a bounded wait (tc::mbar_wait) out of line, behind one attempt in line
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* status) {
@@ -313,8 +312,6 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
   using S = Shape<N>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint8_t* s_stage = smem + S::off_stage;
-  int* s_pos = reinterpret_cast<int*>(smem + S::off_pos);
   MassCtl& ctl = *reinterpret_cast<MassCtl*>(smem + S::off_ctl);
   pdl_launch_dependents();
   if (smem_u32(smem) & 1023u) {  // (the swizzled blocks need it; the same in every thread)
@@ -328,26 +325,25 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
         tc::mbar_init(&ctl.b_full[i][k], 1);
         tc::mbar_init(&ctl.b_empty[i][k], 1);
       }
-    for (int i = 0; i < 8; ++i) {
-      tc::mbar_init(&ctl.rec_full[i], 1);
-      tc::mbar_init(&ctl.rec_empty[i], 1);
-    }
     for (int i = 0; i < 5; ++i) {
       tc::mbar_init(&ctl.a_full[i], 4);
       tc::mbar_init(&ctl.a_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&ctl.d_full[i], 1);
-      tc::mbar_init(&ctl.d_free[i], 4 * S::parts);
-      tc::mbar_init(&ctl.part_full[i], 4 * (S::parts - 1));
+      tc::mbar_init(&ctl.drained[i], 1);
+      // (sparse: the sums of the other parts, and where a row has two chunks those of the other set)
+      tc::mbar_init(&ctl.part_full[i], max(1, 4 * (a.h_s > N ? 2 * S::parts - 1 : S::parts - 1)));
       tc::mbar_init(&ctl.col_full[i], 1);
       tc::mbar_init(&ctl.col_empty[i], 4 * S::parts);
     }
-    tc::mbar_init(&ctl.drained, 1);
+    for (int i = 0; i < kSlotsD; ++i) {
+      for (int k = 0; k < kSets; ++k) tc::mbar_init(&ctl.d_full[k][i], 1);
+      tc::mbar_init(&ctl.d_free[i], 4 * S::parts);
+    }
     tc::mbar_fence_init();
     ctl.start_group = ctl.start_tile = ctl.start_chunk = 0;
   }
-  if (warp == kWarpMma) tc::tmem_alloc(&ctl.tmem, 512);
+  if (warp == kWarpMma0) tc::tmem_alloc(&ctl.tmem, 512);
   pdl_wait();
   // ---- the CTA's share of the units ----
   {
@@ -406,163 +402,31 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
   Walk w;
 
   if (warp == kWarpB) {
-    // ---- the columns' queries: 128 dims of a chunk at a time ----
-    if (lane == 0 && walk_begin<SPARSE, N>(ws, ctl, w)) {
+    // ---- a chunk's queries, 128 dims at a time, and its columns' constants; columns behind the group's last have
+    // no weight ----
+    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
       int slot = 0, have = -1;
-      uint32_t phase = 0;
-      bool ok = true;
-      do {
-        const bool keep = w.chunks <= S::slots;
-        if (keep && have == w.g) continue;
-        have = w.g;
-        const int c0 = keep ? 0 : w.c0, c1 = keep ? w.chunks : w.c1;
-        for (int c = c0; ok && c < c1; ++c) {
-          for (int k = 0; k < 5; ++k) {
-            ok = wait(&ctl.b_empty[slot][k], phase ^ 1u);
-            if (!ok) break;
+      uint32_t phase = 0, n = 0;
+      auto load = [&](int c) {
+        for (int k = 0; k < 5; ++k) {
+          if (!wait_warp(&ctl.b_empty[slot][k], phase ^ 1u)) return false;
+          if (lane == 0) {
             uint64_t* bar = &ctl.b_full[slot][k];
             uint8_t* to = smem + (slot * kBlocks + 2 * k) * S::block;
             tc::mbar_arrive_expect_tx(bar, (k < 4 ? 2 : 1) * S::block);
             tc::tma_load_3d(to, &q_map, 128 * k, w.grp.y + c * N, 0, bar);
             if (k < 4) tc::tma_load_3d(to + S::block, &q_map, 128 * k + 64, w.grp.y + c * N, 0, bar);
           }
-          if (ok) skip(slot, phase, 1);
         }
-      } while (ok && walk_next<SPARSE, N>(ws, pl.groups, w));
-      // copies in flight must land before the CTA ends (a share may not use all chunks of a group that stays); a
-      // slot that was never loaded is past the phase before its first
-      for (int i = 0; i < S::slots; ++i)
-        for (int k = 0; k < 5; ++k) tc::mbar_drain(&ctl.b_full[i][k], i < slot ? phase : phase ^ 1u, 100000000ull);
-      if (*abort) __nanosleep(1000000);  // (and those of a chunk begun)
-    }
-  } else if (warp == kWarpMma) {
-    // ---- products ----
-    const uint32_t leader = elect_leader();
-    constexpr uint32_t idesc = idesc_f16(N);
-    const uint64_t desc0 = tc::desc_kmajor_sw128(smem_u32(smem));
-    int slot = 0, base = 0;  // the next chunk's; of a group that stays, its first
-    uint32_t phase = 0, base_phase = 0, d = 0, visit = 0;
-    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
-      bool ok = true, more = true;
-      int have = -1;
-      while (ok && more) {
-        const bool keep = w.chunks <= S::slots;
-        if (keep && have != w.g) {
-          base = slot;
-          base_phase = phase;
-          skip(slot, phase, w.chunks);
-        }
-        have = w.g;
-        const int g = w.g, c0 = w.c0, c1 = w.c1, chunks = w.chunks;
-        more = walk_next<SPARSE, N>(ws, pl.groups, w);
-        const bool leave = !more || w.g != g;
-        for (int c = c0; ok && c < c1; ++c) {
-          int at = keep ? base : slot;
-          uint32_t ph = keep ? base_phase : phase;
-          if (keep) skip(at, ph, c);
-          else skip(slot, phase, 1);
-          const uint64_t desc = desc0 + static_cast<uint32_t>(at * kBlocks * S::block >> 4);
-#pragma unroll
-          for (int s = 0; s < 5; ++s) {
-            if (c == c0) ok = ok && wait_warp(&ctl.a_full[s], visit);
-            ok = ok && wait_warp(&ctl.d_free[d & 1], (d >> 1) ^ 1u);
-            ok = ok && wait_warp(&ctl.b_full[at][s], ph);
-            if (!ok) break;
-            tc::fence_after_sync();
-            const uint32_t to = tmem + kColD + (d & 1) * N;
-#pragma unroll
-            for (int k = 0; k < (s < 4 ? 8 : 4); ++k)
-              mma_f16_ts(to, tmem + 64 * s + 8 * k, desc + ((2 * s + k / 4) * S::block >> 4) + 2 * (k & 3), idesc, k > 0, leader);
-            commit_if(&ctl.d_full[d & 1], leader);
-            if (!keep) commit_if(&ctl.b_empty[at][s], leader);
-            if (c == c1 - 1) commit_if(&ctl.a_empty[s], leader);
-            ++d;
-          }
-        }
-        if (ok && keep && leave) {  // the group's slots go once its last product is done
-          int at = base;
-          uint32_t ph = base_phase;
-          for (int c = 0; c < chunks; ++c) {
-            for (int k = 0; k < 5; ++k) commit_if(&ctl.b_empty[at][k], leader);
-            skip(at, ph, 1);
-          }
-        }
-        ++visit;
-      }
-    }
-    if (*abort) {  // products in flight must end before the tensor memory is freed
-      __syncwarp();
-      commit_if(&ctl.drained, leader);
-      tc::mbar_drain(&ctl.drained, 0, 100000000ull);
-    }
-  } else if (warp == kWarpRec) {
-    // ---- records of a tile, 32 to a converting warp, a bulk copy a lane ----
-    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
-      const int64_t table_end = static_cast<int64_t>(a.max_pages) * kPage;
-      // the records of a tile, one of each quarter a lane: positions (-1: none) and where they lie.  All loads of
-      // a tile are under way together, while the copies of the tile before are.
-      auto find = [&](const Walk& at, int (&pos)[4], const uint8_t* (&src)[4]) {
-        const int len = SPARSE ? a.seq_lens[at.grp.w] : 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int i = at.tile * kTile + k * 32 + lane;
-          pos[k] = i < at.grp.x ? (SPARSE ? a.idx[static_cast<int64_t>(at.g) * a.topk + i] : i) : -1;
-        }
-        int page[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (SPARSE && pos[k] >= 0 && (pos[k] >= len || pos[k] >= table_end)) {
-            flag(a.status, DSA_STATUS_BAD_INDEX);
-            pos[k] = -1;
-          }
-          page[k] = pos[k] >= 0 ? a.page_table[static_cast<int64_t>(at.grp.w) * a.max_pages + pos[k] / kPage] : 0;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (pos[k] >= 0 && (page[k] < 0 || page[k] >= a.num_pages)) {
-            flag(a.status, DSA_STATUS_BAD_PAGE);
-            pos[k] = -1;
-          }
-          pos[k] = max(pos[k], -1);
-          src[k] = a.kv_cache + (static_cast<int64_t>(page[k]) * kPage + (pos[k] & (kPage - 1))) * kKvTokBytes;
-        }
+        skip(slot, phase, 1);
+        return true;
       };
-      uint32_t visit = 0;
-      bool ok = true, more = true;
-      while (ok && more) {
-        const int stage = static_cast<int>(visit % S::stages);
-        const uint32_t phase = visit / S::stages;
-        int pos[4];
-        const uint8_t* src[4];
-        find(w, pos, src);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const unsigned there = __ballot_sync(0xffffffffu, pos[k] >= 0);
-          ok = ok && wait_warp(&ctl.rec_empty[stage * 4 + k], phase ^ 1u);
-          if (!ok) break;
-          s_pos[stage * kTile + k * 32 + lane] = pos[k];
-          __syncwarp();
-          uint64_t* bar = &ctl.rec_full[stage * 4 + k];
-          if (lane == 0) tc::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(there)) * kKvTokBytes);
-          __syncwarp();
-          if (pos[k] >= 0) tc::bulk_load(s_stage + stage * kStageBytes + (k * 32 + lane) * kPitch, src[k], kKvTokBytes, bar);
-        }
-        if (!ok) break;
-        more = walk_next<SPARSE, N>(ws, pl.groups, w);
-        ++visit;
-      }
-      if (*abort && lane == 0)  // copies in flight must land before the CTA ends
-        for (uint32_t v = visit > static_cast<uint32_t>(S::stages) ? visit - S::stages : 0; v < visit; ++v)
-          for (int quarter = 0; quarter < 4; ++quarter)
-            tc::mbar_drain(&ctl.rec_full[(v % S::stages) * 4 + quarter], (v / S::stages) & 1u, 100000000ull);
-      if (*abort) __nanosleep(1000000);  // (and those of a tile begun)
-    }
-  } else if (warp == kWarpCol) {
-    // ---- the columns' constants, a chunk ahead of the weights; columns behind the group's last have no weight ----
-    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
-      uint32_t n = 0;
-      bool ok = true, more = true;
-      while (ok && more) {
+      bool ok = true;
+      do {
+        const bool keep = w.chunks <= S::slots;
+        if (keep && have != w.g)
+          for (int c = 0; ok && c < w.chunks; ++c) ok = load(c);
+        have = w.g;
         for (int c = w.c0; ok && c < w.c1; ++c, ++n) {
           const int buf = n & 1;
           float4 info[(N + 31) / 32];
@@ -574,8 +438,9 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
             if (32 * i + lane < N && col < w.grp.z) info[i] = ws.cols[w.grp.y + col];
             least = min(least, __float_as_int(info[i].z));
           }
+          if (!keep) ok = load(c);
           least = __reduce_min_sync(0xffffffffu, least);
-          ok = wait_warp(&ctl.col_empty[buf], (n >> 1) ^ 1u);
+          ok = ok && wait_warp(&ctl.col_empty[buf], (n >> 1) ^ 1u);
           if (!ok) break;
           float* pairs = reinterpret_cast<float*>(smem + S::off_col) + buf * 2 * N;
           int* limits = reinterpret_cast<int*>(smem + S::off_limit) + buf * N;
@@ -591,22 +456,135 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&ctl.col_full[buf]);
         }
-        more = ok && walk_next<SPARSE, N>(ws, pl.groups, w);
-      }
+      } while (ok && walk_next<SPARSE, N>(ws, pl.groups, w));
+      // copies in flight must land before the CTA ends (a share may not use all chunks of a group that stays); a
+      // slot that was never loaded is past the phase before its first
+      for (int i = 0; i < S::slots; ++i)
+        for (int k = 0; k < 5; ++k) tc::mbar_drain(&ctl.b_full[i][k], i < slot ? phase : phase ^ 1u, 100000000ull);
+      if (*abort) __nanosleep(1000000);  // (and those of a chunk begun)
     }
-  } else if (warp < kWarpEpi0) {
-    // ---- codes widened to fp16 into tensor memory, a position a lane ----
-    const int quarter = warp & 3;
-    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    uint32_t visit = 0;
+  } else if (warp == kWarpMma0 || warp == kWarpMma0 + 1) {
+    // ---- products: the two warps take turns, so that one's waits and issue pass while the other's
+    // products run.  (Products of one tile of dims in consecutive chunks may be the two warps': the second is issued
+    // when accumulators in between have been read, in order, behind the first.) ----
+    const uint32_t leader = elect_leader(), mine = warp - kWarpMma0;
+    constexpr uint32_t idesc = idesc_f16(N);
+    const uint64_t desc0 = tc::desc_kmajor_sw128(smem_u32(smem));
+    int slot = 0, base = 0;  // the next chunk's; of a group that stays, its first
+    uint32_t phase = 0, base_phase = 0, d = 0, n = 0, visit = 0;
     if (walk_begin<SPARSE, N>(ws, ctl, w)) {
       bool ok = true, more = true;
+      int have = -1;
       while (ok && more) {
-        const int stage = static_cast<int>(visit % S::stages);
-        ok = wait_warp(&ctl.rec_full[stage * 4 + quarter], visit / S::stages);
-        if (!ok) break;
-        const int row = quarter * 32 + lane;
-        const uint8_t* rec = s_stage + stage * kStageBytes + row * kPitch;
+        const bool keep = w.chunks <= S::slots, first_visit = have != w.g;
+        if (keep && first_visit) {
+          base = slot;
+          base_phase = phase;
+          skip(slot, phase, w.chunks);
+        }
+        have = w.g;
+        const int c0 = w.c0, c1 = w.c1;
+        more = walk_next<SPARSE, N>(ws, pl.groups, w);
+        for (int c = c0; ok && c < c1; ++c, ++n) {
+          int at = keep ? base : slot;
+          uint32_t ph = keep ? base_phase : phase;
+          if (keep) skip(at, ph, c);
+          else skip(slot, phase, 1);
+          const uint64_t desc = desc0 + static_cast<uint32_t>(at * kBlocks * S::block >> 4);
+#pragma unroll
+          for (int s = 0; s < 5; ++s, ++d) {
+            if ((d & 1) != mine) continue;
+            const uint32_t acc = d % kSlotsD, to = tmem + kColD + acc * N;
+            ok = ok && wait_warp(&ctl.d_free[acc], (d / kSlotsD) ^ 1u);
+            if (c == c0) ok = ok && wait_warp(&ctl.a_full[s], visit);
+            if (!keep || first_visit) ok = ok && wait_warp(&ctl.b_full[at][s], ph);
+            if (!ok) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int k = 0; k < (s < 4 ? 8 : 4); ++k)
+              mma_f16_ts(to, tmem + 64 * s + 8 * k, desc + ((2 * s + k / 4) * S::block >> 4) + 2 * (k & 3), idesc, k > 0, leader);
+            commit_if(&ctl.d_full[n & 1][acc], leader);
+            if (!keep) commit_if(&ctl.b_empty[at][s], leader);
+            if (c == c1 - 1) commit_if(&ctl.a_empty[s], leader);
+          }
+        }
+        ++visit;
+      }
+    }
+    if (*abort) {  // products in flight must end before the tensor memory is freed
+      __syncwarp();
+      commit_if(&ctl.drained[mine], leader);
+      tc::mbar_drain(&ctl.drained[mine], 0, 100000000ull);
+    }
+  } else if (warp >= kWarpConv0 && warp < kWarpEpi0) {
+    // ---- records: fetched by the warp that widens them to fp16 into tensor memory, 32 positions each, a position a
+    // lane.  (A bulk copy a record, issued by 32 lanes, took 2500 cycles for these 32 in issue alone.)  The next tile's
+    // records are on their way once this one's are read, or before where there is room for two; page
+    // and entry of those behind are looked up meanwhile. ----
+    const int quarter = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    uint8_t* stage0 = smem + S::off_stage + quarter * 32 * kPitch;
+    const int64_t table_end = static_cast<int64_t>(a.max_pages) * kPage;
+    Walk ahead;
+    // the lane's position in a tile, -1: none
+    auto entry = [&](const Walk& at) {
+      const int i = at.tile * kTile + quarter * 32 + lane;
+      return i < at.grp.x ? (SPARSE ? a.idx[static_cast<int64_t>(at.g) * a.topk + i] : i) : -1;
+    };
+    // its page; a position behind the sequence is none
+    auto lookup = [&](const Walk& at, int& pos) {
+      if (SPARSE && pos >= 0 && (pos >= a.seq_lens[at.grp.w] || pos >= table_end)) {
+        flag(a.status, DSA_STATUS_BAD_INDEX);
+        pos = -1;
+      }
+      pos = max(pos, -1);
+      return pos >= 0 ? a.page_table[static_cast<int64_t>(at.grp.w) * a.max_pages + pos / kPage] : 0;
+    };
+    // the 32 records, eight lanes 128 bytes of one at a time
+    auto fetch = [&](int& pos, int page, uint8_t* stage) {
+      if (pos >= 0 && (page < 0 || page >= a.num_pages)) {
+        flag(a.status, DSA_STATUS_BAD_PAGE);
+        pos = -1;
+      }
+      const uint8_t* src = pos >= 0 ? a.kv_cache + (static_cast<int64_t>(page) * kPage + (pos & (kPage - 1))) * kKvTokBytes : nullptr;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        const uint8_t* from = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
+        if (!from) continue;
+        const uint32_t to = smem_u32(stage + r * kPitch) + 16 * (lane & 7);
+        from += 16 * (lane & 7);
+#pragma unroll
+        for (int j = 0; j < 5; ++j)
+          if (j < 4 || (lane & 7) < (kKvTokBytes - 512) / 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to + 128 * j), "l"(from + 128 * j) : "memory");
+      }
+    };
+    uint32_t visit = 0;
+    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
+      ahead = w;
+      int pos[3], page[2];  // this tile's, the next one's and that behind it
+      pos[0] = entry(ahead);
+      page[0] = lookup(ahead, pos[0]);
+      bool have1 = walk_next<SPARSE, N>(ws, pl.groups, ahead), have2 = false;
+      pos[1] = have1 ? entry(ahead) : -1;
+      page[1] = have1 ? lookup(ahead, pos[1]) : 0;
+      fetch(pos[0], page[0], stage0);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      bool ok = true, more = true;
+      while (ok && more) {
+        const uint8_t* stage = stage0 + (visit % S::stages) * kStageBytes;
+        if (have1) have2 = walk_next<SPARSE, N>(ws, pl.groups, ahead);
+        pos[2] = have2 ? entry(ahead) : -1;
+        if (S::stages == 2) {
+          if (have1) fetch(pos[1], page[1], stage0 + ((visit + 1) % S::stages) * kStageBytes);
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        __syncwarp();
+        const uint8_t* rec = stage + lane * kPitch;
         uint32_t scales[8];
         bool fine = true;
 #pragma unroll
@@ -616,7 +594,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
           scales[i] = __float_as_uint(v);
         }
         if (!fine) scales[0] = 0x7FC00000u;  // NaN: the position has no weight
-        scales[5] = static_cast<uint32_t>(s_pos[stage * kTile + row]);
+        scales[5] = static_cast<uint32_t>(pos[0]);
         scales[6] = scales[7] = 0;
 #pragma unroll 1
         for (int s = 0; s < 5; ++s) {
@@ -645,56 +623,82 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
           if (lane == 0) tc::mbar_arrive(&ctl.a_full[s]);
         }
         if (!ok) break;
-        if (lane == 0) tc::mbar_arrive(&ctl.rec_empty[stage * 4 + quarter]);
-        more = walk_next<SPARSE, N>(ws, pl.groups, w);
+        if (S::stages == 1) {
+          if (have1) fetch(pos[1], page[1], stage0);
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        more = have1;
+        pos[0] = pos[1];
+        pos[1] = pos[2];
+        page[1] = have2 ? lookup(ahead, pos[1]) : 0;
+        have1 = have2;
+        have2 = false;
         ++visit;
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
-  } else {
-    // ---- weights: a position a lane, S::width of a chunk's columns each four warps ----
+  } else if (warp >= kWarpEpi0) {
+    // ---- weights: a position a lane, S::width of a chunk's columns each four warps; the two sets take the chunks in
+    // turn, so that one's exponentials pass while the other reads accumulators ----
     constexpr int W = S::width;
-    const int quarter = warp & 3, part = (warp - kWarpEpi0) >> 2, row = quarter * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    uint32_t d = 0, n = 0, visit = 0;
+    const int quarter = warp & 3, team = (warp - kWarpEpi0) >> 2, part = team % S::parts, row = quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16, set = team / S::parts;
+    uint32_t d = 0, n = 0, visit = 0, phases = 0;  // (phases: of the set's barriers, a bit each)
+    int slot = 0, base = 0, have = -1;  // chunk slots, as the warps of products count them
     if (walk_begin<SPARSE, N>(ws, ctl, w)) {
       bool ok = true, more = true;
       while (ok && more) {
-        uint64_t scale[5];
-        float total = 0.f;
+        const bool keep = w.chunks <= S::slots;
+        if (keep && have != w.g) base = slot;
+        if (!keep || have != w.g) slot = (slot + (keep ? w.chunks : w.c1 - w.c0)) % S::slots;
+        have = w.g;
+        float scale[5], total = 0.f;
         int pos = -1;
-        for (int c = w.c0; ok && c < w.c1; ++c) {
+        bool took = false, last = false;  // a chunk of this tile, its last one
+        for (int c = w.c0; ok && c < w.c1; ++c, ++n) {
+          last = (n & 1) == set;
+          if (!last) {
+            d += 5;
+            continue;
+          }
           uint64_t acc[W / 2];
 #pragma unroll
-          for (int s = 0; s < 5; ++s) {
-            ok = ok && wait_warp(&ctl.d_full[d & 1], d >> 1);
+          for (int s = 0; s < 5; ++s, ++d) {
+            const uint32_t at = d % kSlotsD;
+            ok = ok && wait_warp(&ctl.d_full[set][at], phases >> at);
             if (!ok) break;
+            phases ^= 1u << at;
             tc::fence_after_sync();
-            if (s == 0 && c == w.c0) {
+            if (s == 0 && !took) {
               uint32_t v[8];
               tmem_ld8(tmem + lanes + kColScale + 8 * (visit & 1), v);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 5; ++i) scale[i] = pair(__uint_as_float(v[i]), __uint_as_float(v[i]));
+              for (int i = 0; i < 5; ++i) scale[i] = __uint_as_float(v[i]);
               pos = static_cast<int>(v[5]);
+              took = true;
             }
-            uint32_t v[W];
-            tmem_load<W>(tmem + lanes + kColD + (d & 1) * N + part * W, v);
-            tc::tmem_wait_ld();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&ctl.d_free[d & 1]);
-            ++d;
+            const uint64_t both = pair(scale[s], scale[s]);
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i)
-              acc[i] = fma_pair(scale[s], pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s ? acc[i] : 0ull);
+            for (int h = 0; h < W / 16; ++h) {  // (16 columns at a time: 768 threads have 80 registers each)
+              uint32_t v[16];
+              tc::tmem_ld16(tmem + lanes + kColD + at * N + part * W + 16 * h, v);
+              tc::tmem_wait_ld();
+              if (h == W / 16 - 1) {
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&ctl.d_free[at]);
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                acc[8 * h + i] = fma_pair(both, pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s ? acc[8 * h + i] : 0ull);
+            }
           }
-          const int buf = n & 1;
-          ok = ok && wait_warp(&ctl.col_full[buf], n >> 1);
+          ok = ok && wait_warp(&ctl.col_full[set], n >> 1);
           if (!ok) break;
-          ++n;
-          const ulonglong2* cols = reinterpret_cast<const ulonglong2*>(smem + S::off_col) + (buf * N + part * W) / 2;
+          const ulonglong2* cols = reinterpret_cast<const ulonglong2*>(smem + S::off_col) + (set * N + part * W) / 2;
           float sum = 0.f;
-          if (ctl.all_seen[buf]) {
+          if (ctl.all_seen[set]) {
             float odd = 0.f;
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) {
@@ -705,7 +709,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
             }
             sum += odd;
           } else {
-            const int2* limits = reinterpret_cast<const int2*>(smem + S::off_limit) + (buf * N + part * W) / 2;
+            const int2* limits = reinterpret_cast<const int2*>(smem + S::off_limit) + (set * N + part * W) / 2;
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) {
               const ulonglong2 k = cols[i];
@@ -715,31 +719,51 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
             }
           }
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&ctl.col_empty[buf]);
+          if (lane == 0) tc::mbar_arrive(&ctl.col_empty[set]);
           total += sum;
         }
         if (!ok) break;
-        // (the other parts' sums of the tile before last have been read: d_free holds all parts within two accumulators)
-        if (part > 0) {
-          ctl.part[visit & 1][part - 1][row] = total;
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&ctl.part_full[visit & 1]);
-        } else {
-          ok = wait_warp(&ctl.part_full[visit & 1], visit >> 1);
-          if (!ok) break;
-          if (pos >= 0) {
+        if (SPARSE && took) {
+          // the row's weight is the sum of all parts' and sets': the last chunk's first part gathers it, by way of tensor
+          // memory.  (A buffer's sums have been read before the tile after next is: the accumulators hold the sets together.)
+          constexpr int kOthers = 2 * S::parts - 1;
+          const uint32_t buf = visit & 1, cell = tmem + lanes + kColPart + 4 * buf;
+          if (last && part == 0) {
+            const int others = w.chunks == 2 ? kOthers : S::parts - 1;
+            if (others > 0) {
+              ok = wait_warp(&ctl.part_full[buf], visit >> 1);
+              if (!ok) break;
+              tc::fence_after_sync();
+              float v[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < S::parts - 1; ++i) total += ctl.part[visit & 1][i][row];
-            if (SPARSE && a.weights) a.weights[static_cast<int64_t>(w.g) * a.topk + w.tile * kTile + row] = total;
-            if (a.mass) {
-              if (total != total) flag(a.status, DSA_STATUS_NAN_SCORE);
-              else if (total > 0.f)
-                atomicAdd(reinterpret_cast<unsigned long long*>(a.mass + static_cast<int64_t>(w.grp.w) * a.mass_stride + pos),
-                          static_cast<unsigned long long>(__float2ll_rn(fminf(total, kMassMost) * kMassOne)));
+              for (int i = 0; i < 3; ++i)
+                if (i < others) v[i] = tmem_ld1(cell + i);
+              tc::tmem_wait_ld();
+              total += v[0] + v[1] + v[2];
             }
+          } else {
+            // (in the order: the last set's other parts, then the first set's)
+            tmem_st1(cell + (last ? part - 1 : S::parts - 1 + part), total);
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl.part_full[buf]);
           }
         }
+        if (took && pos >= 0 && (!SPARSE || (last && part == 0))) {
+          if (SPARSE && a.weights) a.weights[static_cast<int64_t>(w.g) * a.topk + w.tile * kTile + row] = total;
+          if (a.mass) {
+            if (total != total) flag(a.status, DSA_STATUS_NAN_SCORE);
+            else if (total > 0.f)
+              atomicAdd(reinterpret_cast<unsigned long long*>(a.mass + static_cast<int64_t>(w.grp.w) * a.mass_stride + pos),
+                        static_cast<unsigned long long>(__float2ll_rn(fminf(total, kMassMost) * kMassOne)));
+          }
+        }
+        const int g = w.g, chunks = w.chunks;
         more = walk_next<SPARSE, N>(ws, pl.groups, w);
+        // a group that stayed gives its slots back: the set that read its last accumulator does
+        if (part == 0 && quarter == 0 && last && keep && more && w.g != g && lane < 5)
+          for (int c = 0; c < chunks; ++c) tc::mbar_arrive(&ctl.b_empty[(base + c) % S::slots][lane]);
         ++visit;
       }
     }
@@ -747,7 +771,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == kWarpMma) tc::tmem_dealloc(tmem, 512);
+  if (warp == kWarpMma0) tc::tmem_dealloc(tmem, 512);
 }
 
 size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
@@ -755,9 +779,9 @@ size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 MassPlan make_plan(int n_q, int h_s, int n_seq, bool sparse) {
   MassPlan p;
   p.groups = sparse ? n_q : n_seq;
-  // a chunk's columns: all of a group of average rows where they fit; of more than 128 as many as there can be
+  // a chunk's columns: all of a group of average rows where they fit
   const int64_t cols = static_cast<int64_t>(h_s) * (sparse ? 1 : std::max(1, (n_q + n_seq - 1) / n_seq));
-  p.n = cols <= 16 ? 16 : cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 96 ? 96 : cols <= 128 ? 64 : 96;
+  p.n = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
   const size_t columns = static_cast<size_t>(n_q) * h_s;
   p.off_cols = round_up(columns * kLatent * 2, 256);
   p.off_groups = p.off_cols + round_up(columns * 16, 256);
@@ -832,8 +856,7 @@ cudaError_t launch_attn_mass(const MassArgs& a, cudaStream_t s, const char** err
   switch (pl.n) {
     case 16: return sparse ? launch_main<true, 16>(q_map, a, pl, ws, grid, s) : launch_main<false, 16>(q_map, a, pl, ws, grid, s);
     case 32: return sparse ? launch_main<true, 32>(q_map, a, pl, ws, grid, s) : launch_main<false, 32>(q_map, a, pl, ws, grid, s);
-    case 64: return sparse ? launch_main<true, 64>(q_map, a, pl, ws, grid, s) : launch_main<false, 64>(q_map, a, pl, ws, grid, s);
-    default: return sparse ? launch_main<true, 96>(q_map, a, pl, ws, grid, s) : launch_main<false, 96>(q_map, a, pl, ws, grid, s);
+    default: return sparse ? launch_main<true, 64>(q_map, a, pl, ws, grid, s) : launch_main<false, 64>(q_map, a, pl, ws, grid, s);
   }
 }
 
