@@ -245,14 +245,17 @@ __device__ __forceinline__ uint32_t elect_leader() {
   asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}" : "=r"(r));
   return r;
 }
-// D (+)= A B, fp16 operands, A in tensor memory
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, bool accumulate,
+// D (+)= A B, fp16 operands, A in tensor memory; B by the low word of its descriptor (rows of 128 bytes swizzled, groups of
+// eight 1024 bytes apart)
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate,
                                            uint32_t leader) {
   asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 e, %5, 0;\n setp.ne.b32 p, %4, 0;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-      :: "r"(d), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(leader) : "memory");
+      "{\n .reg .pred p, e;\n .reg .b64 b;\n setp.ne.b32 e, %5, 0;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %6};\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}"
+      :: "r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(leader), "n"(kDescHi) : "memory");
 }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ void commit_if(uint64_t* bar, uint32_t leader) {
   asm volatile(
       "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
@@ -261,11 +264,6 @@ __device__ __forceinline__ void commit_if(uint64_t* bar, uint32_t leader) {
 }
 __host__ __device__ constexpr uint32_t idesc_f16(int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
-}
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
@@ -469,7 +467,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
     // when accumulators in between have been read, in order, behind the first.) ----
     const uint32_t leader = elect_leader(), mine = warp - kWarpMma0;
     constexpr uint32_t idesc = idesc_f16(N);
-    const uint64_t desc0 = tc::desc_kmajor_sw128(smem_u32(smem));
+    const uint32_t b_first = smem_u32(smem) >> 4 | 1u << 16;
     int slot = 0, base = 0;  // the next chunk's; of a group that stays, its first
     uint32_t phase = 0, base_phase = 0, d = 0, n = 0, visit = 0;
     if (walk_begin<SPARSE, N>(ws, ctl, w)) {
@@ -490,19 +488,24 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
           uint32_t ph = keep ? base_phase : phase;
           if (keep) skip(at, ph, c);
           else skip(slot, phase, 1);
-          const uint64_t desc = desc0 + static_cast<uint32_t>(at * kBlocks * S::block >> 4);
-#pragma unroll
+          const uint32_t b_chunk = b_first + static_cast<uint32_t>(at * kBlocks * S::block >> 4);
+          // (rolled up: the roles' loops together have to stay within the instruction cache)
+#pragma unroll 1
           for (int s = 0; s < 5; ++s, ++d) {
             if ((d & 1) != mine) continue;
-            const uint32_t acc = d % kSlotsD, to = tmem + kColD + acc * N;
+            const uint32_t acc = d % kSlotsD;
             ok = ok && wait_warp(&ctl.d_free[acc], (d / kSlotsD) ^ 1u);
             if (c == c0) ok = ok && wait_warp(&ctl.a_full[s], visit);
             if (!keep || first_visit) ok = ok && wait_warp(&ctl.b_full[at][s], ph);
             if (!ok) break;
             tc::fence_after_sync();
+            const uint32_t to = uniform(tmem + kColD + acc * N), from = uniform(tmem + 64 * s);
+            const uint32_t b_lo = uniform(b_chunk + s * (2 * S::block >> 4));
 #pragma unroll
-            for (int k = 0; k < (s < 4 ? 8 : 4); ++k)
-              mma_f16_ts(to, tmem + 64 * s + 8 * k, desc + ((2 * s + k / 4) * S::block >> 4) + 2 * (k & 3), idesc, k > 0, leader);
+            for (int k = 0; k < 4; ++k) mma_f16_ts(to, from + 8 * k, b_lo + 2 * k, idesc, k > 0, leader);
+            if (s < 4)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_f16_ts(to, from + 32 + 8 * k, b_lo + (S::block >> 4) + 2 * k, idesc, true, leader);
             commit_if(&ctl.d_full[n & 1][acc], leader);
             if (!keep) commit_if(&ctl.b_empty[at][s], leader);
             if (c == c1 - 1) commit_if(&ctl.a_empty[s], leader);
@@ -525,7 +528,6 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     uint8_t* stage0 = smem + S::off_stage + quarter * 32 * kPitch;
     const int64_t table_end = static_cast<int64_t>(a.max_pages) * kPage;
-    Walk ahead;
     // the lane's position in a tile, -1: none
     auto entry = [&](const Walk& at) {
       const int i = at.tile * kTile + quarter * 32 + lane;
@@ -547,7 +549,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
         pos = -1;
       }
       const uint8_t* src = pos >= 0 ? a.kv_cache + (static_cast<int64_t>(page) * kPage + (pos & (kPage - 1))) * kKvTokBytes : nullptr;
-#pragma unroll
+#pragma unroll 2
       for (int i = 0; i < 8; ++i) {
         const int r = 4 * i + (lane >> 3);
         const uint8_t* from = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
@@ -560,80 +562,67 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to + 128 * j), "l"(from + 128 * j) : "memory");
       }
     };
-    uint32_t visit = 0;
     if (walk_begin<SPARSE, N>(ws, ctl, w)) {
-      ahead = w;
-      int pos[3], page[2];  // this tile's, the next one's and that behind it
-      pos[0] = entry(ahead);
-      page[0] = lookup(ahead, pos[0]);
-      bool have1 = walk_next<SPARSE, N>(ws, pl.groups, ahead), have2 = false;
-      pos[1] = have1 ? entry(ahead) : -1;
-      page[1] = have1 ? lookup(ahead, pos[1]) : 0;
-      fetch(pos[0], page[0], stage0);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      bool ok = true, more = true;
-      while (ok && more) {
-        const uint8_t* stage = stage0 + (visit % S::stages) * kStageBytes;
-        if (have1) have2 = walk_next<SPARSE, N>(ws, pl.groups, ahead);
-        pos[2] = have2 ? entry(ahead) : -1;
-        if (S::stages == 2) {
-          if (have1) fetch(pos[1], page[1], stage0 + ((visit + 1) % S::stages) * kStageBytes);
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-        } else {
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-        }
-        __syncwarp();
-        const uint8_t* rec = stage + lane * kPitch;
-        uint32_t scales[8];
-        bool fine = true;
-#pragma unroll
-        for (int i = 0; i < 5; ++i) {
-          const float v = *reinterpret_cast<const float*>(rec + kKvScaleOff + 4 * i);
-          fine = fine && fabsf(v) * 448.0f < INFINITY;
-          scales[i] = __float_as_uint(v);
-        }
-        if (!fine) scales[0] = 0x7FC00000u;  // NaN: the position has no weight
-        scales[5] = static_cast<uint32_t>(pos[0]);
-        scales[6] = scales[7] = 0;
-#pragma unroll 1
-        for (int s = 0; s < 5; ++s) {
-          ok = wait_warp(&ctl.a_empty[s], visit ^ 1u);
-          if (!ok) break;
-          tc::fence_after_sync();
-          if (s == 0) tmem_st8(tmem + lanes + kColScale + 8 * (visit & 1), scales);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {  // 32 codes, 16 columns
-            if (s == 4 && j >= 2) break;
-            const uint4 lo = *reinterpret_cast<const uint4*>(rec + 128 * s + 32 * j);
-            const uint4 hi = *reinterpret_cast<const uint4*>(rec + 128 * s + 32 * j + 16);
-            const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            uint32_t o[16];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const __half2 p = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i] & 0xFFFFu)), q = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i] >> 16));
-              o[2 * i] = *reinterpret_cast<const uint32_t*>(&p);
-              o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&q);
-            }
-            tc::tmem_st16(tmem + lanes + 64 * s + 16 * j, o);
-          }
-          tc::tmem_wait_st();
-          tc::fence_before_sync();
+      // turn t fetches tile t and widens tile t - (S::stages - 1)
+      uint32_t t = 0;
+      bool ok = true, have = true;     // tile t is there
+      int pos = entry(w), behind = -1; // its positions; those of the tile to widen
+      int page = lookup(w, pos);
+      while (ok) {
+        if (have) fetch(pos, page, stage0 + (t % S::stages) * kStageBytes);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        const int fetched = pos;
+        const bool now = S::stages == 1 || t > 0;
+        const bool end = !have;
+        have = have && walk_next<SPARSE, N>(ws, pl.groups, w);
+        pos = have ? entry(w) : -1;
+        if (now) {
+          const uint32_t visit = t - (S::stages - 1);
+          if (S::stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+          else asm volatile("cp.async.wait_group 0;" ::: "memory");
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&ctl.a_full[s]);
+          const uint8_t* rec = stage0 + (visit % S::stages) * kStageBytes + lane * kPitch;
+          uint32_t scales[8];
+          bool fine = true;
+#pragma unroll
+          for (int i = 0; i < 5; ++i) {
+            const float v = *reinterpret_cast<const float*>(rec + kKvScaleOff + 4 * i);
+            fine = fine && fabsf(v) * 448.0f < INFINITY;
+            scales[i] = __float_as_uint(v);
+          }
+          if (!fine) scales[0] = 0x7FC00000u;  // NaN: the position has no weight
+          scales[5] = static_cast<uint32_t>(S::stages == 1 ? fetched : behind);
+          scales[6] = scales[7] = 0;
+#pragma unroll 1
+          for (int s = 0; s < 5; ++s) {
+            ok = wait_warp(&ctl.a_empty[s], visit ^ 1u);
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (s == 0) tmem_st8(tmem + lanes + kColScale + 8 * (visit & 1), scales);
+#pragma unroll 2
+            for (int j = 0; j < (s < 4 ? 4 : 2); ++j) {  // 32 codes, 16 columns
+              const uint4 lo = *reinterpret_cast<const uint4*>(rec + 128 * s + 32 * j);
+              const uint4 hi = *reinterpret_cast<const uint4*>(rec + 128 * s + 32 * j + 16);
+              const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+              uint32_t o[16];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const __half2 p = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i] & 0xFFFFu)), q = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i] >> 16));
+                o[2 * i] = *reinterpret_cast<const uint32_t*>(&p);
+                o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&q);
+              }
+              tc::tmem_st16(tmem + lanes + 64 * s + 16 * j, o);
+            }
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl.a_full[s]);
+          }
         }
-        if (!ok) break;
-        if (S::stages == 1) {
-          if (have1) fetch(pos[1], page[1], stage0);
-          asm volatile("cp.async.commit_group;" ::: "memory");
-        }
-        more = have1;
-        pos[0] = pos[1];
-        pos[1] = pos[2];
-        page[1] = have2 ? lookup(ahead, pos[1]) : 0;
-        have1 = have2;
-        have2 = false;
-        ++visit;
+        behind = fetched;
+        if (end || (S::stages == 1 && !have)) break;
+        page = have ? lookup(w, pos) : 0;
+        ++t;
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
@@ -652,7 +641,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
         if (keep && have != w.g) base = slot;
         if (!keep || have != w.g) slot = (slot + (keep ? w.chunks : w.c1 - w.c0)) % S::slots;
         have = w.g;
-        float scale[5], total = 0.f;
+        float total = 0.f;
         int pos = -1;
         bool took = false, last = false;  // a chunk of this tile, its last one
         for (int c = w.c0; ok && c < w.c1; ++c, ++n) {
@@ -663,22 +652,17 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
           }
           uint64_t acc[W / 2];
 #pragma unroll
+          for (int i = 0; i < W / 2; ++i) acc[i] = 0ull;
+          const uint32_t tile_info = tmem + lanes + kColScale + 8 * (visit & 1);
+#pragma unroll 1
           for (int s = 0; s < 5; ++s, ++d) {
             const uint32_t at = d % kSlotsD;
-            ok = ok && wait_warp(&ctl.d_full[set][at], phases >> at);
+            ok = wait_warp(&ctl.d_full[set][at], phases >> at);
             if (!ok) break;
             phases ^= 1u << at;
             tc::fence_after_sync();
-            if (s == 0 && !took) {
-              uint32_t v[8];
-              tmem_ld8(tmem + lanes + kColScale + 8 * (visit & 1), v);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 5; ++i) scale[i] = __uint_as_float(v[i]);
-              pos = static_cast<int>(v[5]);
-              took = true;
-            }
-            const uint64_t both = pair(scale[s], scale[s]);
+            const float scale = tmem_ld1(tile_info + s);
+            if (s == 0) pos = __float_as_int(tmem_ld1(tile_info + 5));
 #pragma unroll
             for (int h = 0; h < W / 16; ++h) {  // (16 columns at a time: 768 threads have 80 registers each)
               uint32_t v[16];
@@ -689,16 +673,18 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&ctl.d_free[at]);
               }
+              const uint64_t both = pair(scale, scale);
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                acc[8 * h + i] = fma_pair(both, pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s ? acc[8 * h + i] : 0ull);
+                acc[8 * h + i] = fma_pair(both, pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), acc[8 * h + i]);
             }
           }
+          took = true;
           ok = ok && wait_warp(&ctl.col_full[set], n >> 1);
           if (!ok) break;
           const ulonglong2* cols = reinterpret_cast<const ulonglong2*>(smem + S::off_col) + (set * N + part * W) / 2;
           float sum = 0.f;
-          if (ctl.all_seen[set]) {
+          if (SPARSE || ctl.all_seen[set]) {
             float odd = 0.f;
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) {
