@@ -27,7 +27,7 @@ norm_rope_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
   const int64_t rows = static_cast<int64_t>(a.n) * a.h;
   const int64_t begin = blockIdx.x * rows_block, end = min(begin + rows_block, rows);
   const float inv_span = 1.0f / static_cast<float>(a.span);
-  Vec<T, V> next[NV];
+  Vec<T, V> x[NV];
   auto load = [&](int64_t row) {
     if (row >= end) return;
     const int t = static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(a.h));
@@ -36,22 +36,21 @@ norm_rope_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int vec = j * g.lanes + lane;
-      if (vec < g.vectors) next[j].u = *reinterpret_cast<const W*>(src + vec * V);
+      if (vec < g.vectors) x[j].u = *reinterpret_cast<const W*>(src + vec * V);
     }
   };
-  load(begin + grp);
   norm_fill_params(a, sh);
   for (int64_t r0 = begin; r0 < end; r0 += g.rows_step) {
     const int64_t row = r0 + grp;
+    load(row);
+    norm_fill_cs(a, g, sh, r0, rows);
     float y[NV * V];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const bool there = j * g.lanes + lane < g.vectors;
 #pragma unroll
-      for (int i = 0; i < V; ++i) y[j * V + i] = there ? Elem<T>::get(next[j].e[i]) : 0.f;
+      for (int i = 0; i < V; ++i) y[j * V + i] = there ? Elem<T>::get(x[j].e[i]) : 0.f;
     }
-    load(row + g.rows_step);
-    norm_fill_cs(a, g, sh, r0, rows);
     // (a vector is normed as a whole or not at all: V divides span)
     float mean = 0.f;
     if (a.center) {
@@ -76,9 +75,15 @@ norm_rope_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int e0 = (j * g.lanes + lane) * V;
-      if (e0 < a.span)
+      if (e0 < a.span) {
+        float w[V], b[V];
+        load_floats(sh.weight + e0, w);
 #pragma unroll
-        for (int i = 0; i < V; ++i) y[j * V + i] = fmaf(y[j * V + i] * r, sh.weight[e0 + i], sh.bias[e0 + i]);
+        for (int i = 0; i < V; ++i) b[i] = 0.f;
+        if (a.bias) load_floats(sh.bias + e0, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[j * V + i] = fmaf(y[j * V + i] * r, w[i], b[i]);
+      }
     }
     const int t = static_cast<int>(static_cast<uint32_t>(min(row, rows - 1)) / static_cast<uint32_t>(a.h));
     const int hh = static_cast<int>(static_cast<uint32_t>(row) - static_cast<uint32_t>(t) * static_cast<uint32_t>(a.h));

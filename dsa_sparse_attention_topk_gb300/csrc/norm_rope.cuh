@@ -23,6 +23,7 @@ struct NormGeom {
   int rows_step;      // rows of a block at a time: kNormThreads / lanes
   int tokens_step;    // tokens that those can touch, the sines' table
   int span_pad;       // norm_dim rounded up to 4, floats of the weights' table
+  int turn_word;      // the word of the lanes that is the whole rotary part, -1: there is none
 };
 
 // one float of the weight or bias
@@ -80,15 +81,52 @@ __device__ __forceinline__ float row_sum(float v, int lanes) {
   return v;
 }
 
+// V floats from or to shared memory, 16 bytes at a time where they are aligned
+template <int V>
+__device__ __forceinline__ void load_floats(const float* p, float (&v)[V]) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p + i);
+      v[i] = q.x;
+      v[i + 1] = q.y;
+      v[i + 2] = q.z;
+      v[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = p[i];
+  }
+}
+
 // Turn the rotary part of the row in y (fp32, in the lanes' layout); TRANSPOSE turns back.  Pairs of neighbours
-// lie in one vector; a partner half a rotary part away (or, with vectors of one element, beside) is
-// fetched through shared memory, ex: the row's own rot floats there.
+// lie in one vector.  A partner half a rotary part away comes by shuffle where the whole rotary part is one word of the
+// lanes (g.turn_word: as many pairs as one exchange can carry); otherwise, and with vectors of one element, through
+// shared memory, ex: the row's own rot floats there.
 template <int V, int NV, bool TRANSPOSE>
 __device__ __forceinline__ void turn_row(const NormArgs& a, const NormGeom& g, float (&y)[NV * V], const float2* cs,
                                          float* ex, int lane) {
   const bool half_layout = a.layout == DSA_ROPE_HALF;
   const int half = a.rot >> 1;
-  if (half_layout || V == 1) {
+  if (half_layout && g.turn_word >= 0) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (j != g.turn_word) continue;  // (the same in all threads)
+      const int rel = (j * g.lanes + lane) * V - a.offset;
+      const bool mine = rel >= 0 && rel < a.rot, second = rel >= half;
+      const int from = (threadIdx.x & 31) + (second ? -half / V : half / V);
+      float c[2 * V];
+      load_floats(reinterpret_cast<const float*>(cs + (mine ? (second ? rel - half : rel) : 0)), c);
+      const float sign = second == TRANSPOSE ? -1.f : 1.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float other = __shfl_sync(0xffffffffu, y[j * V + i], from);
+        // a c - b s for the first of a pair, b c + a s for the second.  (The partner's shuffle has read y already.)
+        const float z = fmaf(y[j * V + i], c[2 * i], sign * c[2 * i + 1] * other);
+        y[j * V + i] = mine ? z : y[j * V + i];
+      }
+    }
+  } else if (half_layout || V == 1) {
     __syncwarp();  // (the row before has been read)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -110,8 +148,7 @@ __device__ __forceinline__ void turn_row(const NormArgs& a, const NormGeom& g, f
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const float2 c = cs[f + i];
-          // a c - b s for the first of a pair, b c + a s for the second
-          y[j * V + i] = y[j * V + i] * c.x + sign * c.y * ex[other + i];
+          y[j * V + i] = fmaf(y[j * V + i], c.x, sign * c.y * ex[other + i]);
         }
       }
     }
@@ -120,12 +157,13 @@ __device__ __forceinline__ void turn_row(const NormArgs& a, const NormGeom& g, f
     for (int j = 0; j < NV; ++j) {
       const int rel = (j * g.lanes + lane) * V - a.offset;
       if (rel >= 0 && rel < a.rot) {
+        float c[V];
+        load_floats(reinterpret_cast<const float*>(cs + (rel >> 1)), c);
 #pragma unroll
         for (int i = 0; i + 1 < V; i += 2) {
-          const float2 c = cs[(rel + i) >> 1];
-          const float p = y[j * V + i], q = y[j * V + i + 1], s = TRANSPOSE ? -c.y : c.y;
-          y[j * V + i] = p * c.x - q * s;
-          y[j * V + i + 1] = p * s + q * c.x;
+          const float p = y[j * V + i], q = y[j * V + i + 1], s = TRANSPOSE ? -c[i + 1] : c[i + 1];
+          y[j * V + i] = p * c[i] - q * s;
+          y[j * V + i + 1] = p * s + q * c[i];
         }
       }
     }
@@ -146,6 +184,8 @@ inline NormGeom norm_geom(const NormArgs& a, int v, int size) {
   const int64_t most = (g.rows_step + a.h - 2) / a.h + 1;
   g.tokens_step = static_cast<int>(most < a.n ? most : a.n);
   g.span_pad = (a.span + 3) & ~3;
+  const int first = a.offset / v, last = (a.offset + a.rot) / v - 1;  // (V divides both in the half layout)
+  g.turn_word = v > 1 && first / g.lanes == last / g.lanes ? first / g.lanes : -1;
   return g;
 }
 inline size_t norm_shared_bytes(const NormArgs& a, const NormGeom& g) {

@@ -88,7 +88,9 @@ norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int e0 = (j * g.lanes + lane) * V;
-      if (e0 < a.span)
+      if (e0 < a.span) {
+        float w[V];
+        load_floats(sh.weight + e0, w);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int k = j * V + i;
@@ -97,10 +99,11 @@ norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
             dw[k] = fmaf(d[k], u[k], dw[k]);
             db[k] += d[k];
           }
-          d[k] *= sh.weight[e0 + i];
+          d[k] *= w[i];
           c1 = fmaf(d[k], u[k], c1);
           c2 += d[k];
         }
+      }
     }
     c1 = row_sum(c1, g.lanes) * inv_span;
     c2 = a.center ? row_sum(c2, g.lanes) * inv_span : 0.f;
