@@ -3,7 +3,7 @@
 //
 // Selection.  A sequence's first `sinks` and last `recent` positions stay; of those between, the rest of the
 // budget goes to the largest weights, equal ones to the lower position.  One cluster a sequence, each CTA a run of
-// its positions: a radix select in digits of 11 bits, from the highest bit in which the weights differ
+// its positions: a radix select in digits of 9 bits, from the highest bit in which the weights differ
 // at all, each digit one pass over the run (shared memory, if it fits) into a histogram that all CTAs
 // read over distributed shared memory.  It ends as soon as a bin is kept whole.  Two more passes count and
 // write, in position order.  Bound: latency, some ten passes and cluster barriers in a row; the weights are
@@ -20,8 +20,9 @@ namespace dsa {
 namespace {
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
-constexpr int kDigitBits = 11, kBins = 1 << kDigitBits;
-constexpr int kBinsThread = kBins / kSelThreads;
+constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;  // a bin a thread
+constexpr int kAhead = 4;                             // keys of a thread under way together
+static_assert(kBins == kSelThreads, "a bin a thread");
 constexpr int kCacheKeys = 24 * 1024;  // keys of a CTA held in shared memory: 192 KB
 constexpr int kMostCluster = 8;
 
@@ -95,19 +96,30 @@ evict_select_kernel(EvictSelectArgs a, int ranks, int cached) {
   uint64_t threshold = ~0ull;   // keys above it stay, and the first need_equal of those on it
   unsigned need_equal = 0;
   if (need > 0) {
-    // the bits in which keys differ
+    // the bits in which keys differ; the run's keys go to shared memory
     uint64_t lo = ~0ull, hi = 0;
-    for (int p = q0 + tid; p < q1; p += kSelThreads) {
-      const uint64_t k = mass_key(mass[p]);
-      if (cached) s_keys[p - run0] = k;
-      lo = min(lo, k);
-      hi = max(hi, k);
+    for (int p0 = run0 + tid; p0 < run1; p0 += kAhead * kSelThreads) {
+      uint64_t k[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int p = p0 + j * kSelThreads;
+        k[j] = p < run1 ? mass_key(mass[p]) : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int p = p0 + j * kSelThreads;
+        if (cached && p < run1) s_keys[p - run0] = k[j];
+        if (p >= q0 && p < q1) {
+          lo = min(lo, k[j]);
+          hi = max(hi, k[j]);
+        }
+      }
     }
     if (tid == 0) {
       sh.lo = ~0ull;
       sh.hi = 0;
     }
-    for (int i = tid; i < kBins; i += kSelThreads) sh.hist[0][i] = 0;
+    sh.hist[0][tid] = 0;
     __syncthreads();
     for (int o = 16; o; o >>= 1) {
       lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -128,38 +140,38 @@ evict_select_kernel(EvictSelectArgs a, int ranks, int cached) {
     for (int pass = 0; bits > 0 && !whole; ++pass) {
       const int shift = max(bits - kDigitBits, 0), wide = bits - shift;
       unsigned* hist = sh.hist[pass & 1];
-      for (int p0 = q0; p0 < q1; p0 += kSelThreads) {
-        const int p = p0 + tid;
-        bool in = p < q1;
-        unsigned digit = 0;
-        if (in) {
-          const uint64_t k = cached ? s_keys[p - run0] : mass_key(mass[p]);
-          in = bits == 64 || (k >> bits) == (prefix >> bits);
-          digit = static_cast<unsigned>(k >> shift) & ((1u << wide) - 1u);
+      for (int p0 = q0; p0 < q1; p0 += kAhead * kSelThreads) {
+        bool in[kAhead];
+        unsigned digit[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const int p = p0 + j * kSelThreads + tid;
+          in[j] = p < q1;
+          const uint64_t k = !in[j] ? 0 : cached ? s_keys[p - run0] : mass_key(mass[p]);
+          in[j] = in[j] && (bits == 64 || (k >> bits) == (prefix >> bits));
+          digit[j] = static_cast<unsigned>(k >> shift) & ((1u << wide) - 1u);
         }
         // (the digit of a warp's first lane in one addition: positions of no weight all share theirs)
-        const unsigned ins = __ballot_sync(0xffffffffu, in);
-        if (ins) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const unsigned ins = __ballot_sync(0xffffffffu, in[j]);
+          if (!ins) continue;
           const int lead = __ffs(ins) - 1;
-          const unsigned common = __shfl_sync(0xffffffffu, digit, lead);
-          const unsigned same = __ballot_sync(0xffffffffu, in && digit == common);
+          const unsigned common = __shfl_sync(0xffffffffu, digit[j], lead);
+          const unsigned same = __ballot_sync(0xffffffffu, in[j] && digit[j] == common);
           if (lane == lead) atomicAdd(&hist[common], static_cast<unsigned>(__popc(same)));
-          if (in && digit != common) atomicAdd(&hist[digit], 1u);
+          if (in[j] && digit[j] != common) atomicAdd(&hist[digit[j]], 1u);
         }
       }
       peer_sync(ranks);
       // (every CTA has read the other histogram by now)
-      for (int i = tid; i < kBins; i += kSelThreads) sh.hist[(pass + 1) & 1][i] = 0;
-      // bins from the highest down, kBinsThread a thread
-      unsigned mine[kBinsThread], sum = 0;
+      sh.hist[(pass + 1) & 1][tid] = 0;
+      // the bins of all CTAs from the highest down, one a thread
+      const int bin = kBins - 1 - tid;
+      unsigned sum = 0;
 #pragma unroll
-      for (int j = 0; j < kBinsThread; ++j) mine[j] = 0;
-      for (int r = 0; r < ranks; ++r) {
-#pragma unroll
-        for (int j = 0; j < kBinsThread; ++j) mine[j] += peer_u32(hist + kBins - 1 - (tid * kBinsThread + j), r, ranks);
-      }
-#pragma unroll
-      for (int j = 0; j < kBinsThread; ++j) sum += mine[j];
+      for (int r = 0; r < kMostCluster; ++r)
+        if (r < ranks) sum += peer_u32(hist + bin, r, ranks);
       unsigned before = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -169,17 +181,13 @@ evict_select_kernel(EvictSelectArgs a, int ranks, int cached) {
       if (lane == 31) sh.warp[0][warp] = before;
       __syncthreads();
       before -= sum;
-      for (int w = 0; w < warp; ++w) before += sh.warp[0][w];
-      if (before < need && need <= before + sum) {
 #pragma unroll
-        for (int j = 0; j < kBinsThread; ++j) {
-          if (before < need && need <= before + mine[j]) {
-            sh.pick[0] = kBins - 1 - (tid * kBinsThread + j);
-            sh.pick[1] = before;
-            sh.pick[2] = mine[j];
-          }
-          before += mine[j];
-        }
+      for (int w = 0; w < kSelWarps; ++w)
+        if (w < warp) before += sh.warp[0][w];
+      if (before < need && need <= before + sum) {
+        sh.pick[0] = bin;
+        sh.pick[1] = before;
+        sh.pick[2] = sum;
       }
       __syncthreads();
       prefix |= static_cast<uint64_t>(sh.pick[0]) << shift;
@@ -195,27 +203,28 @@ evict_select_kernel(EvictSelectArgs a, int ranks, int cached) {
       need_equal = 0xFFFFFFFFu;
     }
   }
-  auto key_at = [&](int p) { return cached ? s_keys[p - run0] : mass_key(mass[p]); };
+  const bool chosen = a.budget > len - (c1 - c0);  // some of the candidates stay, and the keys have been read
   // how many of each warp's sub-run stay: above the threshold, and on it
   const int w0 = static_cast<int>(min(static_cast<int64_t>(run0) + static_cast<int64_t>(warp) * sub, static_cast<int64_t>(run1)));
   const int w1 = static_cast<int>(min(static_cast<int64_t>(w0) + sub, static_cast<int64_t>(run1)));
-  auto classify = [&](int p, bool& above, bool& equal) {
-    above = equal = false;
-    if (p >= w1) return;
-    if (p < c0 || p >= c1) {
-      above = true;
-    } else {
-      const uint64_t k = a.budget > len - (c1 - c0) ? key_at(p) : 0;
-      above = k > threshold;
-      equal = k == threshold && need_equal > 0;
-    }
+  auto key_of = [&](int p) { return p >= w1 ? 0ull : cached && chosen ? s_keys[p - run0] : mass_key(mass[p]); };
+  auto classify = [&](int p, uint64_t k, bool& above, bool& equal) {
+    const bool in = p < w1, candidate = in && p >= c0 && p < c1;
+    above = in && (!candidate || k > threshold);
+    equal = candidate && k == threshold && need_equal > 0;
   };
   unsigned n_above = 0, n_equal = 0;
-  for (int p0 = w0; p0 < w1; p0 += 32) {
-    bool above, equal;
-    classify(p0 + lane, above, equal);
-    n_above += __popc(__ballot_sync(0xffffffffu, above));
-    n_equal += __popc(__ballot_sync(0xffffffffu, equal));
+  for (int p0 = w0; p0 < w1; p0 += 32 * kAhead) {
+    uint64_t k[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) k[j] = key_of(p0 + 32 * j + lane);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      bool above, equal;
+      classify(p0 + 32 * j + lane, k[j], above, equal);
+      n_above += __popc(__ballot_sync(0xffffffffu, above));
+      n_equal += __popc(__ballot_sync(0xffffffffu, equal));
+    }
   }
   __syncthreads();
   if (lane == 0) {
@@ -238,22 +247,26 @@ evict_select_kernel(EvictSelectArgs a, int ranks, int cached) {
     above0 += sh.warp[0][w];
     equal0 += sh.warp[1][w];
   }
-  for (int p0 = w0; p0 < w1; p0 += 32) {
-    const int p = p0 + lane;
-    bool above, equal;
-    classify(p, above, equal);
-    const unsigned am = __ballot_sync(0xffffffffu, above), em = __ballot_sync(0xffffffffu, equal);
-    const unsigned below = (1u << lane) - 1u;
-    const unsigned ea = equal0 + __popc(em & below), ra = above0 + __popc(am & below);
-    if (above || (equal && ea < need_equal)) {
+  for (int p0 = w0; p0 < w1; p0 += 32 * kAhead) {
+    uint64_t k[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) k[j] = key_of(p0 + 32 * j + lane);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int p = p0 + 32 * j + lane;
+      bool above, equal;
+      classify(p, k[j], above, equal);
+      const unsigned am = __ballot_sync(0xffffffffu, above), em = __ballot_sync(0xffffffffu, equal);
+      const unsigned below = (1u << lane) - 1u;
+      const unsigned ea = equal0 + __popc(em & below), ra = above0 + __popc(am & below);
       const unsigned at = ra + min(ea, need_equal);
-      if (at < static_cast<unsigned>(a.budget)) {
+      if ((above || (equal && ea < need_equal)) && at < static_cast<unsigned>(a.budget)) {
         kept[at] = p;
-        if (kept_mass) kept_mass[at] = mass[p];
+        if (kept_mass) kept_mass[at] = static_cast<int64_t>(k[j] ^ (1ull << 63));
       }
+      above0 += __popc(am);
+      equal0 += __popc(em);
     }
-    above0 += __popc(am);
-    equal0 += __popc(em);
   }
   peer_sync(ranks);  // (no CTA leaves while another may read its totals)
 }
