@@ -27,30 +27,20 @@ norm_rope_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
   const int64_t rows = static_cast<int64_t>(a.n) * a.h;
   const int64_t begin = blockIdx.x * rows_block, end = min(begin + rows_block, rows);
   const float inv_span = 1.0f / static_cast<float>(a.span);
-  Vec<T, V> x[NV];
-  auto load = [&](int64_t row) {
-    if (row >= end) return;
-    const int t = static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(a.h));
-    const int hh = static_cast<int>(static_cast<uint32_t>(row) - static_cast<uint32_t>(t) * static_cast<uint32_t>(a.h));
-    const T* src = static_cast<const T*>(a.x) + t * a.x_stride_t + hh * a.x_stride_h;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int vec = j * g.lanes + lane;
-      if (vec < g.vectors) x[j].u = *reinterpret_cast<const W*>(src + vec * V);
-    }
-  };
   norm_fill_params(a, sh);
-  for (int64_t r0 = begin; r0 < end; r0 += g.rows_step) {
-    const int64_t row = r0 + grp;
-    load(row);
-    norm_fill_cs(a, g, sh, r0, rows);
+  RowAt at(min(begin + grp, rows - 1), a.h);
+  for (int64_t r0 = begin; r0 < end; r0 += g.rows_step, at.step(g, a.h)) {
+    const bool live = r0 + grp < end;
+    const T* src = static_cast<const T*>(a.x) + at.t * a.x_stride_t + at.hh * a.x_stride_h + lane * V;
+    Vec<T, V> x[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (live && j * g.lanes + lane < g.vectors) x[j].u = *reinterpret_cast<const W*>(src + j * g.lanes * V);
+      else x[j].u = W{};
+    norm_fill_cs(a, g, sh, r0, end);
     float y[NV * V];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool there = j * g.lanes + lane < g.vectors;
-#pragma unroll
-      for (int i = 0; i < V; ++i) y[j * V + i] = there ? Elem<T>::get(x[j].e[i]) : 0.f;
-    }
+    for (int j = 0; j < NV; ++j) widen<T, V>(x[j], y + j * V);
     // (a vector is normed as a whole or not at all: V divides span)
     float mean = 0.f;
     if (a.center) {
@@ -85,34 +75,28 @@ norm_rope_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
         for (int i = 0; i < V; ++i) y[j * V + i] = fmaf(y[j * V + i] * r, w[i], b[i]);
       }
     }
-    const int t = static_cast<int>(static_cast<uint32_t>(min(row, rows - 1)) / static_cast<uint32_t>(a.h));
-    const int hh = static_cast<int>(static_cast<uint32_t>(row) - static_cast<uint32_t>(t) * static_cast<uint32_t>(a.h));
-    turn_row<V, NV, false>(a, g, y, sh.cs + (row < end ? t - sh.first : 0) * ((a.rot / 2 + 1) & ~1), ex, lane);
-    if (row < end) {
-      T* dst = static_cast<T*>(a.out) + t * a.out_stride_t + hh * a.out_stride_h;
+    turn_row<V, NV, false>(a, g, y, sh.cs + (live ? at.t - sh.first : 0) * ((a.rot / 2 + 1) & ~1), ex, lane);
+    if (live) {
+      T* dst = static_cast<T*>(a.out) + at.t * a.out_stride_t + at.hh * a.out_stride_h + lane * V;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int vec = j * g.lanes + lane;
-        Vec<T, V> o;
-#pragma unroll
-        for (int i = 0; i < V; ++i) o.e[i] = Elem<T>::put(y[j * V + i]);
-        if (vec < g.vectors) *reinterpret_cast<W*>(dst + vec * V) = o.u;
-      }
+      for (int j = 0; j < NV; ++j)
+        if (j * g.lanes + lane < g.vectors) *reinterpret_cast<W*>(dst + j * g.lanes * V) = narrow<T, V>(y + j * V).u;
     }
   }
 }
 
 template <typename T, int V, int NV>
-cudaError_t launch_fwd(const NormArgs& a, const NormGeom& g, cudaStream_t s) {
+cudaError_t launch_fwd(const NormArgs& a, NormGeom g, cudaStream_t s) {
+  const int64_t steps = (static_cast<int64_t>(a.n) * a.h + g.rows_step - 1) / g.rows_step;
+  const int64_t most = static_cast<int64_t>(multiprocessors()) * 16;
+  const int64_t per = (steps + most - 1) / most;
+  norm_table(a, g, per * g.rows_step);
   const size_t smem = norm_shared_bytes(a, g);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<T, V, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  const int64_t steps = (static_cast<int64_t>(a.n) * a.h + g.rows_step - 1) / g.rows_step;
-  const int64_t most = static_cast<int64_t>(multiprocessors()) * 16;
-  const int64_t per = (steps + most - 1) / most;
   return launch_pdl(norm_rope_kernel<T, V, NV>, dim3(static_cast<unsigned>((steps + per - 1) / per)), dim3(kNormThreads),
                     smem, s, 1, a, g, per * g.rows_step);
 }
@@ -207,7 +191,7 @@ __device__ __forceinline__ void norm_store_k(uint2 raw, float4 w, float4 b, floa
   if ((lane & 7) == 0) page[kKScaleOff + row * 4 + (lane >> 3)] = static_cast<uint8_t>(e + 127);
 }
 
-__device__ __forceinline__ void norm_store_kv(const uint2 (&raws)[4], uint32_t rope, const float4 (&w)[4], float2 cs,
+__device__ __forceinline__ void norm_store_kv(const uint2 (&raws)[4], uint32_t rope, const float4 (*w)[32], float2 cs,
                                               const NormQuantArgs& a, int64_t slot) {
   const int lane = threadIdx.x & 31;
   uint8_t* rec = a.r.kv_cache + slot * kKvTokBytes;
@@ -239,7 +223,8 @@ __device__ __forceinline__ void norm_store_kv(const uint2 (&raws)[4], uint32_t r
   float amax = warp_amax(fmaxf(fabsf(t0), fabsf(t1)));
 #pragma unroll
   for (int tile = 0; tile < 4; ++tile) {
-    const float f[4] = {w[tile].x, w[tile].y, w[tile].z, w[tile].w};
+    const float4 wt = w[tile][lane];
+    const float f[4] = {wt.x, wt.y, wt.z, wt.w};
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -268,19 +253,22 @@ __device__ __forceinline__ void norm_store_kv(const uint2 (&raws)[4], uint32_t r
   if (lane < 8) *reinterpret_cast<float*>(rec + kKvScaleOff + 4 * lane) = lane < 5 ? s : 0.f;
 }
 
-__global__ void __launch_bounds__(kWarpsPerBlock * 32)
+__global__ void __launch_bounds__(kWarpsPerBlock * 32, 4)
 norm_rope_quant_kernel(NormQuantArgs a) {
   pdl_launch_dependents();
   pdl_wait();
+  // weights and bias of a token's dims, four a lane: the key's, then the latent row's tiles (in registers they left room
+  // for 16 warps an SM, and 65536 tokens took 62 us)
+  __shared__ float4 s_param[6][32];
   const int lane = threadIdx.x & 31;
   const int64_t turns = a.r.turns[lane];
-  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
-  float4 kw = one, kb = make_float4(0.f, 0.f, 0.f, 0.f), vw[4] = {one, one, one, one};
-  if (a.k_weight) kw = *reinterpret_cast<const float4*>(a.k_weight + 4 * lane);
-  if (a.k_bias) kb = *reinterpret_cast<const float4*>(a.k_bias + 4 * lane);
-  if (a.kv_weight)
-#pragma unroll
-    for (int tile = 0; tile < 4; ++tile) vw[tile] = *reinterpret_cast<const float4*>(a.kv_weight + tile * 128 + 4 * lane);
+  if (threadIdx.x < 6 * 32) {
+    const int which = threadIdx.x >> 5;
+    const float* src = which == 0 ? a.k_weight : which == 1 ? a.k_bias : a.kv_weight ? a.kv_weight + (which - 2) * 128 : nullptr;
+    s_param[which][lane] = src ? *reinterpret_cast<const float4*>(src + 4 * lane)
+                               : which == 1 ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(1.f, 1.f, 1.f, 1.f);
+  }
+  __syncthreads();
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarpsPerBlock + (threadIdx.x >> 5); t < a.r.n_tokens;
        t += static_cast<int64_t>(gridDim.x) * kWarpsPerBlock) {
     const int64_t slot = a.r.slots[t];
@@ -298,8 +286,8 @@ norm_rope_quant_kernel(NormQuantArgs a) {
       if (lane == 0) flag(a.r.status, DSA_STATUS_BAD_PAGE);
     } else if (slot >= 0) {
       const float2 cs = phase_cs(pos, turns, a.r.amplitude);
-      if (a.r.k) norm_store_k(k, kw, kb, cs, a, slot);
-      if (a.r.kv) norm_store_kv(kv, rope, vw, cs, a, slot);
+      if (a.r.k) norm_store_k(k, s_param[0][lane], s_param[1][lane], cs, a, slot);
+      if (a.r.kv) norm_store_kv(kv, rope, s_param + 2, cs, a, slot);
     }
   }
 }

@@ -8,6 +8,10 @@
 // elements in fp32.
 #pragma once
 
+#include <algorithm>
+#include <cstring>
+#include <type_traits>
+
 #include "dsa_common.cuh"
 #include "dsa_launch.h"
 #include "rope_math.cuh"
@@ -21,7 +25,9 @@ struct NormGeom {
   int lanes;          // G: lanes a row, a power of two of 8..32
   int vectors;        // of one row
   int rows_step;      // rows of a block at a time: kNormThreads / lanes
-  int tokens_step;    // tokens that those can touch, the sines' table
+  int rows_table;     // rows whose tokens' sines are in shared memory together, a multiple of rows_step
+  int tokens_table;   // tokens that those can touch
+  int step_t, step_h; // rows_step as whole tokens and heads
   int span_pad;       // norm_dim rounded up to 4, floats of the weights' table
   int turn_word;      // the word of the lanes that is the whole rotary part, -1: there is none
 };
@@ -40,16 +46,17 @@ struct NormShared {
   float* bias;
   float2* cs;
   float* ex;
-  int first, last;  // tokens in cs
+  int first;         // token of cs's first row
+  int64_t rows_end;  // rows before it have their sines there
 };
 __device__ __forceinline__ NormShared norm_shared(const NormArgs& a, const NormGeom& g, unsigned char* raw) {
   NormShared s;
   s.weight = reinterpret_cast<float*>(raw);
   s.bias = s.weight + g.span_pad;
   s.cs = reinterpret_cast<float2*>(s.bias + g.span_pad);
-  s.ex = reinterpret_cast<float*>(s.cs + g.tokens_step * ((a.rot / 2 + 1) & ~1));
+  s.ex = reinterpret_cast<float*>(s.cs + g.tokens_table * ((a.rot / 2 + 1) & ~1));
   s.first = 0;
-  s.last = -1;
+  s.rows_end = 0;
   return s;
 }
 __device__ __forceinline__ void norm_fill_params(const NormArgs& a, const NormShared& s) {
@@ -58,21 +65,65 @@ __device__ __forceinline__ void norm_fill_params(const NormArgs& a, const NormSh
     s.bias[i] = a.bias ? norm_param(a.bias, a.w_dtype, i) : 0.f;
   }
 }
-// the sines of the tokens of rows [r0, r0 + rows_step); every thread of the block calls it, and it synchronises them
-// whenever the table changes
-__device__ __forceinline__ void norm_fill_cs(const NormArgs& a, const NormGeom& g, NormShared& s, int64_t r0, int64_t rows) {
-  const int first = static_cast<int>(static_cast<uint32_t>(r0) / static_cast<uint32_t>(a.h));
-  const int last = static_cast<int>(static_cast<uint32_t>(min(r0 + g.rows_step, rows) - 1) / static_cast<uint32_t>(a.h));
-  if (first >= s.first && last <= s.last) return;
+// the sines of the tokens of the rows from r0 on, as many as the table holds; every thread of the block calls it, and it
+// synchronises them whenever the table changes
+__device__ __forceinline__ void norm_fill_cs(const NormArgs& a, const NormGeom& g, NormShared& s, int64_t r0, int64_t end) {
+  if (r0 < s.rows_end) return;
+  s.rows_end = min(r0 + g.rows_table, end);
+  s.first = static_cast<int>(static_cast<uint32_t>(r0) / static_cast<uint32_t>(a.h));
+  const int last = static_cast<int>(static_cast<uint32_t>(s.rows_end - 1) / static_cast<uint32_t>(a.h));
   __syncthreads();
-  const int half = a.rot >> 1, pitch = (half + 1) & ~1, count = (last - first + 1) * half;
+  const int half = a.rot >> 1, pitch = (half + 1) & ~1, count = (last - s.first + 1) * half;
   for (int i = threadIdx.x; i < count; i += kNormThreads) {
     const int t = i / half, f = i - t * half;
-    s.cs[t * pitch + f] = phase_cs(a.pos[first + t], a.turns[f], a.amplitude);
+    s.cs[t * pitch + f] = phase_cs(a.pos[s.first + t], a.turns[f], a.amplitude);
   }
-  s.first = first;
-  s.last = last;
   __syncthreads();
+}
+
+// A thread's place among the rows: token and head of its row
+struct RowAt {
+  int t, hh;
+  __device__ __forceinline__ RowAt(int64_t row, int h)
+      : t(static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(h))),
+        hh(static_cast<int>(static_cast<uint32_t>(row) - static_cast<uint32_t>(t) * static_cast<uint32_t>(h))) {}
+  __device__ __forceinline__ void step(const NormGeom& g, int h) {
+    t += g.step_t;
+    hh += g.step_h;
+    if (hh >= h) {
+      hh -= h;
+      ++t;
+    }
+  }
+};
+
+// V elements of T as floats, and back, pairs of 16 bits in one conversion
+template <typename T, int V>
+__device__ __forceinline__ void widen(const Vec<T, V>& x, float* y) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) y[i] = Elem<T>::get(x.e[i]);
+}
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> narrow(const float* y) {
+  Vec<T, V> o;
+  if constexpr (sizeof(T) == 2 && V > 1) {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      if constexpr (sizeof(T) == sizeof(__half) && std::is_same<T, __half>::value) {
+        const __half2 p = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&p);
+      } else {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+    }
+    memcpy(&o, w, sizeof(o));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.e[i] = Elem<T>::put(y[i]);
+  }
+  return o;
 }
 
 // The sum over a row's lanes, in every one of them.
@@ -181,16 +232,26 @@ inline NormGeom norm_geom(const NormArgs& a, int v, int size) {
   g.vectors = a.d / v;
   g.lanes = v * size < 16 ? 32 : g.vectors <= 32 ? 8 : g.vectors <= 64 ? 16 : 32;
   g.rows_step = kNormThreads / g.lanes;
-  const int64_t most = (g.rows_step + a.h - 2) / a.h + 1;
-  g.tokens_step = static_cast<int>(most < a.n ? most : a.n);
+  g.step_t = g.rows_step / a.h;
+  g.step_h = g.rows_step % a.h;
   g.span_pad = (a.span + 3) & ~3;
   const int first = a.offset / v, last = (a.offset + a.rot) / v - 1;  // (V divides both in the half layout)
   g.turn_word = v > 1 && first / g.lanes == last / g.lanes ? first / g.lanes : -1;
   return g;
 }
+// The table holds the sines of one step's tokens at least; of a block's whole share where that takes 16 KB at most.
+inline void norm_table(const NormArgs& a, NormGeom& g, int64_t rows_block) {
+  const int64_t bytes = sizeof(float2) * ((a.rot / 2 + 1) & ~1);
+  auto tokens = [&](int64_t rows) { return std::min<int64_t>((rows + a.h - 2) / a.h + 1, a.n); };
+  int64_t rows = rows_block;
+  while (rows > g.rows_step && tokens(rows) * bytes > 16384) rows = (rows / 2 + g.rows_step - 1) / g.rows_step * g.rows_step;
+  g.rows_table = static_cast<int>(std::min<int64_t>(rows, 1 << 30));
+  g.tokens_table = static_cast<int>(tokens(rows));
+}
 inline size_t norm_shared_bytes(const NormArgs& a, const NormGeom& g) {
-  return 2 * sizeof(float) * g.span_pad + sizeof(float2) * g.tokens_step * ((a.rot / 2 + 1) & ~1) +
-         sizeof(float) * g.rows_step * a.rot;
+  const bool exchange = !(a.layout == DSA_ROPE_HALF ? g.turn_word >= 0 : g.vectors < a.d);  // (see turn_row)
+  return 2 * sizeof(float) * g.span_pad + sizeof(float2) * g.tokens_table * ((a.rot / 2 + 1) & ~1) +
+         (exchange ? sizeof(float) * g.rows_step * a.rot : 0);
 }
 
 }  // namespace

@@ -15,8 +15,10 @@ namespace dsa {
 namespace {
 
 constexpr int kMostBlocks = 1024;  // partial sums in the workspace
+constexpr int kBlocksSm = 4;       // blocks an SM gets
 
-template <typename T, int V, int NV>
+// SHIFT: the bias's sums too
+template <typename T, int V, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kNormThreads)
 norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
   using W = typename Word<V * sizeof(T)>::type;
@@ -30,40 +32,36 @@ norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
   const int64_t begin = blockIdx.x * rows_block, end = min(begin + rows_block, rows);
   const float inv_span = 1.0f / static_cast<float>(a.span);
   norm_fill_params(a, sh);
-  float dw[NV * V], db[NV * V];
+  float dw[NV * V], db[SHIFT ? NV * V : 1];
 #pragma unroll
-  for (int i = 0; i < NV * V; ++i) dw[i] = db[i] = 0.f;
-  for (int64_t r0 = begin; r0 < end; r0 += g.rows_step) {
-    const int64_t row = r0 + grp;
-    const bool live = row < end;
-    const int t = static_cast<int>(static_cast<uint32_t>(min(row, rows - 1)) / static_cast<uint32_t>(a.h));
-    const int hh = static_cast<int>(static_cast<uint32_t>(min(row, rows - 1)) - static_cast<uint32_t>(t) * static_cast<uint32_t>(a.h));
-    const T* xs = static_cast<const T*>(a.x) + t * a.x_stride_t + hh * a.x_stride_h;
-    const T* ys = static_cast<const T*>(a.dy) + t * a.dy_stride_t + hh * a.dy_stride_h;
-    float u[NV * V], d[NV * V];
-    {
-      Vec<T, V> p[NV], q[NV];
+  for (int i = 0; i < NV * V; ++i) {
+    dw[i] = 0.f;
+    if (SHIFT) db[i] = 0.f;
+  }
+  RowAt at(min(begin + grp, rows - 1), a.h);
+  for (int64_t r0 = begin; r0 < end; r0 += g.rows_step, at.step(g, a.h)) {
+    const bool live = r0 + grp < end;
+    const T* xs = static_cast<const T*>(a.x) + at.t * a.x_stride_t + at.hh * a.x_stride_h + lane * V;
+    const T* ys = static_cast<const T*>(a.dy) + at.t * a.dy_stride_t + at.hh * a.dy_stride_h + lane * V;
+    Vec<T, V> p[NV], q[NV];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int vec = j * g.lanes + lane;
-        if (live && vec < g.vectors) {
-          p[j].u = *reinterpret_cast<const W*>(xs + vec * V);
-          q[j].u = *reinterpret_cast<const W*>(ys + vec * V);
-        } else {
-          p[j].u = W{};
-          q[j].u = W{};
-        }
+    for (int j = 0; j < NV; ++j) {
+      if (live && j * g.lanes + lane < g.vectors) {
+        p[j].u = *reinterpret_cast<const W*>(xs + j * g.lanes * V);
+        q[j].u = *reinterpret_cast<const W*>(ys + j * g.lanes * V);
+      } else {
+        p[j].u = W{};
+        q[j].u = W{};
       }
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          u[j * V + i] = Elem<T>::get(p[j].e[i]);
-          d[j * V + i] = Elem<T>::get(q[j].e[i]);
-        }
     }
-    norm_fill_cs(a, g, sh, r0, rows);
-    turn_row<V, NV, true>(a, g, d, sh.cs + (live ? t - sh.first : 0) * ((a.rot / 2 + 1) & ~1), ex, lane);
+    norm_fill_cs(a, g, sh, r0, end);
+    float u[NV * V], d[NV * V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      widen<T, V>(p[j], u + j * V);
+      widen<T, V>(q[j], d + j * V);
+    }
+    turn_row<V, NV, true>(a, g, d, sh.cs + (live ? at.t - sh.first : 0) * ((a.rot / 2 + 1) & ~1), ex, lane);
     float mean = 0.f;
     if (a.center) {
       float s = 0.f;
@@ -97,7 +95,7 @@ norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
           u[k] *= r;
           if (live) {  // (a row behind the last has x = 0, and with eps = 0 no factor)
             dw[k] = fmaf(d[k], u[k], dw[k]);
-            db[k] += d[k];
+            if (SHIFT) db[k] += d[k];
           }
           d[k] *= w[i];
           c1 = fmaf(d[k], u[k], c1);
@@ -108,89 +106,94 @@ norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
     c1 = row_sum(c1, g.lanes) * inv_span;
     c2 = a.center ? row_sum(c2, g.lanes) * inv_span : 0.f;
     if (live) {
-      T* dst = static_cast<T*>(a.out) + t * a.out_stride_t + hh * a.out_stride_h;
+      T* dst = static_cast<T*>(a.out) + at.t * a.out_stride_t + at.hh * a.out_stride_h + lane * V;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int vec = j * g.lanes + lane;
-        Vec<T, V> o;
+        if (vec * V < a.span)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int k = j * V + i;
-          o.e[i] = Elem<T>::put(vec * V < a.span ? r * (fmaf(-u[k], c1, d[k]) - c2) : d[k]);
-        }
-        if (vec < g.vectors) *reinterpret_cast<W*>(dst + vec * V) = o.u;
+          for (int i = 0; i < V; ++i) d[j * V + i] = r * (fmaf(-u[j * V + i], c1, d[j * V + i]) - c2);
+        if (vec < g.vectors) *reinterpret_cast<W*>(dst + j * g.lanes * V) = narrow<T, V>(d + j * V).u;
       }
     }
   }
   if (!a.dweight && !a.dbias) return;
   // the block's sums: first over the groups of a warp, then over the warps through shared memory
-  float* sums = reinterpret_cast<float*>(raw);  // [2][warps][span], over the tables
+  constexpr int kKinds = SHIFT ? 2 : 1, kWarps = kNormThreads / 32;
+  float* sums = reinterpret_cast<float*>(raw);  // [kinds][warps][span], over the tables
   __syncthreads();
   const int warp = threadIdx.x >> 5, in_warp = threadIdx.x & 31;
 #pragma unroll
   for (int k = 0; k < NV * V; ++k) {
     for (int o = g.lanes; o < 32; o <<= 1) {
       dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], o);
-      db[k] += __shfl_xor_sync(0xffffffffu, db[k], o);
+      if (SHIFT) db[k] += __shfl_xor_sync(0xffffffffu, db[k], o);
     }
     const int e = ((k / V) * g.lanes + lane) * V + k % V;
     if (in_warp < g.lanes && e < a.span) {
       sums[warp * a.span + e] = dw[k];
-      sums[(kNormThreads / 32 + warp) * a.span + e] = db[k];
+      if (SHIFT) sums[(kWarps + warp) * a.span + e] = db[k];
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * a.span; i += kNormThreads) {
+  for (int i = threadIdx.x; i < kKinds * a.span; i += kNormThreads) {
     const int which = i >= a.span, e = i - which * a.span;
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kNormThreads / 32; ++w) v += sums[(which * (kNormThreads / 32) + w) * a.span + e];
-    a.workspace[static_cast<int64_t>(blockIdx.x) * 2 * a.span + i] = v;
+    for (int w = 0; w < kWarps; ++w) v += sums[(which * kWarps + w) * a.span + e];
+    a.workspace[static_cast<int64_t>(blockIdx.x) * kKinds * a.span + i] = v;
   }
 }
 
 // The sums of `blocks` partial sums: 32 columns a block, 32 rows of threads that each take every 32nd partial.
 __global__ void __launch_bounds__(1024)
-norm_grad_sum_kernel(const float* part, int blocks, int span, float* dweight, float* dbias) {
+norm_grad_sum_kernel(const float* part, int blocks, int span, int kinds, float* dweight, float* dbias) {
   __shared__ float s[32][33];
   pdl_launch_dependents();
   pdl_wait();
   const int col = blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
-  if (col < 2 * span)
+  if (col < kinds * span)
 #pragma unroll 8
-    for (int b = threadIdx.y; b < blocks; b += 32) v += part[static_cast<int64_t>(b) * 2 * span + col];
+    for (int b = threadIdx.y; b < blocks; b += 32) v += part[static_cast<int64_t>(b) * kinds * span + col];
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   v = s[threadIdx.x][threadIdx.y];
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   const int mine = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && mine < 2 * span) {
+  if (threadIdx.x == 0 && mine < kinds * span) {
     if (mine < span && dweight) dweight[mine] = v;
     if (mine >= span && dbias) dbias[mine - span] = v;
   }
 }
 
-template <typename T, int V, int NV>
-cudaError_t launch_bwd(const NormArgs& a, const NormGeom& g, cudaStream_t s) {
-  size_t smem = norm_shared_bytes(a, g);
-  const size_t sums = sizeof(float) * 2 * (kNormThreads / 32) * a.span;
-  smem = smem > sums ? smem : sums;
+template <typename T, int V, int NV, bool SHIFT>
+cudaError_t launch_bwd_k(const NormArgs& a, NormGeom g, cudaStream_t s) {
+  const int64_t steps = (static_cast<int64_t>(a.n) * a.h + g.rows_step - 1) / g.rows_step;
+  const int64_t most = std::min<int64_t>(static_cast<int64_t>(multiprocessors()) * kBlocksSm, kMostBlocks);
+  const int64_t per = (steps + most - 1) / most;
+  const int blocks = static_cast<int>((steps + per - 1) / per), kinds = SHIFT ? 2 : 1;
+  norm_table(a, g, per * g.rows_step);
+  const size_t smem = std::max(norm_shared_bytes(a, g), sizeof(float) * kinds * (kNormThreads / 32) * a.span);
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(norm_rope_grad_kernel<T, V, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(norm_rope_grad_kernel<T, V, NV, SHIFT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  const int64_t steps = (static_cast<int64_t>(a.n) * a.h + g.rows_step - 1) / g.rows_step;
-  int64_t most = static_cast<int64_t>(multiprocessors()) * 4;
-  most = most < kMostBlocks ? most : kMostBlocks;
-  const int64_t per = (steps + most - 1) / most;
-  const int blocks = static_cast<int>((steps + per - 1) / per);
-  cudaError_t e = launch_pdl(norm_rope_grad_kernel<T, V, NV>, dim3(blocks), dim3(kNormThreads), smem, s, 1, a, g, per * g.rows_step);
+  cudaError_t e = launch_pdl(norm_rope_grad_kernel<T, V, NV, SHIFT>, dim3(blocks), dim3(kNormThreads), smem, s, 1, a, g,
+                             per * g.rows_step);
   if (e != cudaSuccess || (!a.dweight && !a.dbias)) return e;
-  return launch_pdl(norm_grad_sum_kernel, dim3((2 * a.span + 31) / 32), dim3(32, 32), 0, s, 1,
-                    static_cast<const float*>(a.workspace), blocks, a.span, a.dweight, a.dbias);
+  return launch_pdl(norm_grad_sum_kernel, dim3((kinds * a.span + 31) / 32), dim3(32, 32), 0, s, 1,
+                    static_cast<const float*>(a.workspace), blocks, a.span, kinds, a.dweight, a.dbias);
+}
+template <typename T, int V, int NV>
+cudaError_t launch_bwd(const NormArgs& a, const NormGeom& g, cudaStream_t s) {
+  // (of the narrow vectors one kernel serves both)
+  if constexpr (V * sizeof(T) == 16) {
+    if (!a.dbias) return launch_bwd_k<T, V, NV, false>(a, g, s);
+  }
+  return launch_bwd_k<T, V, NV, true>(a, g, s);
 }
 
 template <typename T>
