@@ -14,8 +14,11 @@
 namespace dsa {
 namespace {
 
+// blocks on an SM together, by the registers that a lane's elements take
+template <int E> constexpr int kBlocksSm = E <= 16 ? 4 : E <= 24 ? 3 : 2;
+
 template <typename T, int V, int NV>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, kBlocksSm<V * NV>)
 norm_rope_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
   using W = typename Word<V * sizeof(T)>::type;
   extern __shared__ __align__(16) unsigned char raw[];
@@ -27,68 +30,82 @@ norm_rope_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
   const int64_t rows = static_cast<int64_t>(a.n) * a.h;
   const int64_t begin = blockIdx.x * rows_block, end = min(begin + rows_block, rows);
   const float inv_span = 1.0f / static_cast<float>(a.span);
-  norm_fill_params(a, sh);
-  RowAt at(min(begin + grp, rows - 1), a.h);
-  for (int64_t r0 = begin; r0 < end; r0 += g.rows_step, at.step(g, a.h)) {
-    const bool live = r0 + grp < end;
-    const T* src = static_cast<const T*>(a.x) + at.t * a.x_stride_t + at.hh * a.x_stride_h + lane * V;
-    Vec<T, V> x[NV];
+  RowAt at(min(begin + grp, rows - 1), a.h), next = at;
+  RowPtr<const T> src(static_cast<const T*>(a.x) + lane * V, at, g, a.h, a.x_stride_t, a.x_stride_h);
+  RowPtr<T> dst(static_cast<T*>(a.out) + lane * V, at, g, a.h, a.out_stride_t, a.out_stride_h);
+  bool there[NV], normed[NV];  // (a vector is normed as a whole or not at all: V divides span)
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    there[j] = j * g.lanes + lane < g.vectors;
+    normed[j] = (j * g.lanes + lane) * V < a.span;
+  }
+  Vec<T, V> x[NV];  // the row at hand, then the next one
+  auto load = [&](bool live) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (live && j * g.lanes + lane < g.vectors) x[j].u = *reinterpret_cast<const W*>(src + j * g.lanes * V);
+      if (live && there[j]) x[j].u = *reinterpret_cast<const W*>(src.p + j * g.lanes * V);
       else x[j].u = W{};
-    norm_fill_cs(a, g, sh, r0, end);
+    src.step(next.step(g, a.h));
+  };
+  load(begin + grp < end);
+  norm_fill_params(a, sh);
+  for (int64_t r0 = begin; r0 < end; r0 += g.rows_step) {
+    const bool live = r0 + grp < end;
     float y[NV * V];
 #pragma unroll
     for (int j = 0; j < NV; ++j) widen<T, V>(x[j], y + j * V);
-    // (a vector is normed as a whole or not at all: V divides span)
-    float mean = 0.f;
+    load(r0 + g.rows_step + grp < end);
+    norm_fill_cs(a, g, sh, r0, end);
     if (a.center) {
       float s = 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if ((j * g.lanes + lane) * V < a.span)
+        if (normed[j])
 #pragma unroll
           for (int i = 0; i < V; ++i) s += y[j * V + i];
-      mean = row_sum(s, g.lanes) * inv_span;
-    }
-    float s2 = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if ((j * g.lanes + lane) * V < a.span)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          y[j * V + i] -= mean;
-          s2 = fmaf(y[j * V + i], y[j * V + i], s2);
-        }
-    const float r = rsqrtf(fmaf(row_sum(s2, g.lanes), inv_span, a.eps));
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e0 = (j * g.lanes + lane) * V;
-      if (e0 < a.span) {
-        float w[V], b[V];
-        load_floats(sh.weight + e0, w);
-#pragma unroll
-        for (int i = 0; i < V; ++i) b[i] = 0.f;
-        if (a.bias) load_floats(sh.bias + e0, b);
-#pragma unroll
-        for (int i = 0; i < V; ++i) y[j * V + i] = fmaf(y[j * V + i] * r, w[i], b[i]);
-      }
-    }
-    turn_row<V, NV, false>(a, g, y, sh.cs + (live ? at.t - sh.first : 0) * ((a.rot / 2 + 1) & ~1), ex, lane);
-    if (live) {
-      T* dst = static_cast<T*>(a.out) + at.t * a.out_stride_t + at.hh * a.out_stride_h + lane * V;
+      const float mean = row_sum(s, g.lanes) * inv_span;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (j * g.lanes + lane < g.vectors) *reinterpret_cast<W*>(dst + j * g.lanes * V) = narrow<T, V>(y + j * V).u;
+        if (normed[j])
+#pragma unroll
+          for (int i = 0; i < V; ++i) y[j * V + i] -= mean;
     }
+    float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (normed[j]) add_products<V>(s2, y + j * V, y + j * V);
+    const float r = rsqrtf(fmaf(row_sum(s2.x + s2.y, g.lanes), inv_span, a.eps));
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (normed[j]) {
+        const int e0 = (j * g.lanes + lane) * V;
+        scale_all<V>(y + j * V, r);
+        if (a.weight) {
+          float w[V];
+          load_floats(sh.weight + e0, w);
+          scale_by<V>(y + j * V, w);
+        }
+        if (a.bias) {
+          float b[V];
+          load_floats(sh.bias + e0, b);
+#pragma unroll
+          for (int i = 0; i < V; ++i) y[j * V + i] += b[i];
+        }
+      }
+    turn_row<V, NV, false>(a, g, y, sh.cs + (live ? at.t - sh.first : 0) * ((a.rot / 2 + 1) & ~1), ex, lane);
+    if (live)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (there[j]) *reinterpret_cast<W*>(dst.p + j * g.lanes * V) = narrow<T, V>(y + j * V).u;
+    dst.step(at.step(g, a.h));
   }
 }
 
 template <typename T, int V, int NV>
 cudaError_t launch_fwd(const NormArgs& a, NormGeom g, cudaStream_t s) {
   const int64_t steps = (static_cast<int64_t>(a.n) * a.h + g.rows_step - 1) / g.rows_step;
-  const int64_t most = static_cast<int64_t>(multiprocessors()) * 16;
+  // one wave: a block's start, two round trips to memory, is then paid once (4096 x 64 x 128: 38 us with four)
+  const int64_t most = static_cast<int64_t>(multiprocessors()) * kBlocksSm<V * NV>;
   const int64_t per = (steps + most - 1) / most;
   norm_table(a, g, per * g.rows_step);
   const size_t smem = norm_shared_bytes(a, g);

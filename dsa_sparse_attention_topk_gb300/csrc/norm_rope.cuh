@@ -87,15 +87,80 @@ struct RowAt {
   __device__ __forceinline__ RowAt(int64_t row, int h)
       : t(static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(h))),
         hh(static_cast<int>(static_cast<uint32_t>(row) - static_cast<uint32_t>(t) * static_cast<uint32_t>(h))) {}
-  __device__ __forceinline__ void step(const NormGeom& g, int h) {
+  // on by a step of rows; whether that is into a later token's first heads
+  __device__ __forceinline__ bool step(const NormGeom& g, int h) {
     t += g.step_t;
     hh += g.step_h;
-    if (hh >= h) {
+    const bool wrap = hh >= h;
+    if (wrap) {
       hh -= h;
       ++t;
     }
+    return wrap;
   }
 };
+// Its address in a tensor: kept by addition
+template <typename P>
+struct RowPtr {
+  P* p;
+  int64_t by, by_wrap;
+  __device__ __forceinline__ RowPtr(P* base, const RowAt& at, const NormGeom& g, int h, int64_t stride_t, int64_t stride_h)
+      : p(base + at.t * stride_t + at.hh * stride_h), by(g.step_t * stride_t + g.step_h * stride_h),
+        by_wrap(by + stride_t - h * stride_h) {}
+  __device__ __forceinline__ void step(bool wrap) { p += wrap ? by_wrap : by; }
+};
+
+// pairs of floats in one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+// y[i] = y[i] * w[i] (+ b[i]) over V elements, and sums of products
+template <int V>
+__device__ __forceinline__ void scale_by(float* y, const float* w) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 r = mul2(make_float2(y[i], y[i + 1]), make_float2(w[i], w[i + 1]));
+      y[i] = r.x;
+      y[i + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[i] *= w[i];
+  }
+}
+template <int V>
+__device__ __forceinline__ void scale_all(float* y, float f) {
+  const float w[2] = {f, f};
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) scale_by<2>(y + i, w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[i] *= f;
+  }
+}
+// sum += a[i] b[i], even and odd elements apart
+template <int V>
+__device__ __forceinline__ void add_products(float2& sum, const float* a, const float* b) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) sum = fma2(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), sum);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum.x = fmaf(a[i], b[i], sum.x);
+  }
+}
 
 // V elements of T as floats, and back, pairs of 16 bits in one conversion
 template <typename T, int V>
@@ -128,7 +193,10 @@ __device__ __forceinline__ Vec<T, V> narrow(const float* y) {
 
 // The sum over a row's lanes, in every one of them.
 __device__ __forceinline__ float row_sum(float v, int lanes) {
-  for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lanes > 8) v += __shfl_xor_sync(0xffffffffu, v, 8);
+  if (lanes > 16) v += __shfl_xor_sync(0xffffffffu, v, 16);
   return v;
 }
 
@@ -159,22 +227,30 @@ __device__ __forceinline__ void turn_row(const NormArgs& a, const NormGeom& g, f
                                          float* ex, int lane) {
   const bool half_layout = a.layout == DSA_ROPE_HALF;
   const int half = a.rot >> 1;
-  if (half_layout && g.turn_word >= 0) {
+  if (V > 1 && half_layout && g.turn_word >= 0) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (j != g.turn_word) continue;  // (the same in all threads)
       const int rel = (j * g.lanes + lane) * V - a.offset;
       const bool mine = rel >= 0 && rel < a.rot, second = rel >= half;
       const int from = (threadIdx.x & 31) + (second ? -half / V : half / V);
-      float c[2 * V];
-      load_floats(reinterpret_cast<const float*>(cs + (mine ? (second ? rel - half : rel) : 0)), c);
-      const float sign = second == TRANSPOSE ? -1.f : 1.f;
+      // the first of a pair becomes a c - b s, the second b c + a s: the one that sends gives the sign
+      const float sign = second == TRANSPOSE ? 1.f : -1.f;
+      float other[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float other = __shfl_sync(0xffffffffu, y[j * V + i], from);
-        // a c - b s for the first of a pair, b c + a s for the second.  (The partner's shuffle has read y already.)
-        const float z = fmaf(y[j * V + i], c[2 * i], sign * c[2 * i + 1] * other);
-        y[j * V + i] = mine ? z : y[j * V + i];
+      for (int i = 0; i < V; ++i) other[i] = sign * y[j * V + i];
+#pragma unroll
+      for (int i = 0; i < V; ++i) other[i] = __shfl_sync(0xffffffffu, other[i], from);
+      if (mine) {
+        float c[2 * V];
+        load_floats(reinterpret_cast<const float*>(cs + (second ? rel - half : rel)), c);
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {  // (a word of several elements has an even number)
+          const float2 p = mul2(make_float2(other[i], other[i + 1]), make_float2(c[2 * i + 1], c[2 * i + 3]));
+          const float2 z = fma2(make_float2(y[j * V + i], y[j * V + i + 1]), make_float2(c[2 * i], c[2 * i + 2]), p);
+          y[j * V + i] = z.x;
+          y[j * V + i + 1] = z.y;
+        }
       }
     }
   } else if (half_layout || V == 1) {

@@ -15,11 +15,11 @@ namespace dsa {
 namespace {
 
 constexpr int kMostBlocks = 1024;  // partial sums in the workspace
-constexpr int kBlocksSm = 4;       // blocks an SM gets
+constexpr int kBlocksSm = 2;       // blocks an SM gets: one wave
 
 // SHIFT: the bias's sums too
 template <typename T, int V, int NV, bool SHIFT>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, 2)
 norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
   using W = typename Word<V * sizeof(T)>::type;
   extern __shared__ __align__(16) unsigned char raw[];
@@ -31,91 +31,117 @@ norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
   const int64_t rows = static_cast<int64_t>(a.n) * a.h;
   const int64_t begin = blockIdx.x * rows_block, end = min(begin + rows_block, rows);
   const float inv_span = 1.0f / static_cast<float>(a.span);
-  norm_fill_params(a, sh);
   float dw[NV * V], db[SHIFT ? NV * V : 1];
 #pragma unroll
   for (int i = 0; i < NV * V; ++i) {
     dw[i] = 0.f;
     if (SHIFT) db[i] = 0.f;
   }
-  RowAt at(min(begin + grp, rows - 1), a.h);
-  for (int64_t r0 = begin; r0 < end; r0 += g.rows_step, at.step(g, a.h)) {
-    const bool live = r0 + grp < end;
-    const T* xs = static_cast<const T*>(a.x) + at.t * a.x_stride_t + at.hh * a.x_stride_h + lane * V;
-    const T* ys = static_cast<const T*>(a.dy) + at.t * a.dy_stride_t + at.hh * a.dy_stride_h + lane * V;
-    Vec<T, V> p[NV], q[NV];
+  RowAt at(min(begin + grp, rows - 1), a.h), next = at;
+  RowPtr<const T> xs(static_cast<const T*>(a.x) + lane * V, at, g, a.h, a.x_stride_t, a.x_stride_h);
+  RowPtr<const T> ys(static_cast<const T*>(a.dy) + lane * V, at, g, a.h, a.dy_stride_t, a.dy_stride_h);
+  RowPtr<T> dst(static_cast<T*>(a.out) + lane * V, at, g, a.h, a.out_stride_t, a.out_stride_h);
+  bool there[NV], normed[NV];  // (a vector is normed as a whole or not at all: V divides span)
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    there[j] = j * g.lanes + lane < g.vectors;
+    normed[j] = (j * g.lanes + lane) * V < a.span;
+  }
+  Vec<T, V> p[NV], q[NV];  // x and dy of the row at hand, then of the next one
+  auto load = [&](bool live) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (live && j * g.lanes + lane < g.vectors) {
-        p[j].u = *reinterpret_cast<const W*>(xs + j * g.lanes * V);
-        q[j].u = *reinterpret_cast<const W*>(ys + j * g.lanes * V);
+      if (live && there[j]) {
+        p[j].u = *reinterpret_cast<const W*>(xs.p + j * g.lanes * V);
+        q[j].u = *reinterpret_cast<const W*>(ys.p + j * g.lanes * V);
       } else {
         p[j].u = W{};
         q[j].u = W{};
       }
     }
-    norm_fill_cs(a, g, sh, r0, end);
+    const bool wrap = next.step(g, a.h);
+    xs.step(wrap);
+    ys.step(wrap);
+  };
+  load(begin + grp < end);
+  norm_fill_params(a, sh);
+  for (int64_t r0 = begin; r0 < end; r0 += g.rows_step) {
+    const bool live = r0 + grp < end;
     float u[NV * V], d[NV * V];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       widen<T, V>(p[j], u + j * V);
       widen<T, V>(q[j], d + j * V);
     }
+    load(r0 + g.rows_step + grp < end);
+    norm_fill_cs(a, g, sh, r0, end);
     turn_row<V, NV, true>(a, g, d, sh.cs + (live ? at.t - sh.first : 0) * ((a.rot / 2 + 1) & ~1), ex, lane);
-    float mean = 0.f;
     if (a.center) {
       float s = 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if ((j * g.lanes + lane) * V < a.span)
+        if (normed[j])
 #pragma unroll
           for (int i = 0; i < V; ++i) s += u[j * V + i];
-      mean = row_sum(s, g.lanes) * inv_span;
+      const float mean = row_sum(s, g.lanes) * inv_span;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (normed[j])
+#pragma unroll
+          for (int i = 0; i < V; ++i) u[j * V + i] -= mean;
     }
-    float s2 = 0.f;
+    float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if ((j * g.lanes + lane) * V < a.span)
+      if (normed[j]) add_products<V>(s2, u + j * V, u + j * V);
+    const float r = rsqrtf(fmaf(row_sum(s2.x + s2.y, g.lanes), inv_span, a.eps));
+    const float ru = live ? r : 0.f;  // (a row behind the last has x = 0, and with eps = 0 no factor)
+    float2 c1 = make_float2(0.f, 0.f);
+    float c2 = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          u[j * V + i] -= mean;
-          s2 = fmaf(u[j * V + i], u[j * V + i], s2);
-        }
-    const float r = rsqrtf(fmaf(row_sum(s2, g.lanes), inv_span, a.eps));
-    float c1 = 0.f, c2 = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e0 = (j * g.lanes + lane) * V;
-      if (e0 < a.span) {
-        float w[V];
-        load_floats(sh.weight + e0, w);
+    for (int j = 0; j < NV; ++j)
+      if (normed[j]) {
+        scale_all<V>(u + j * V, ru);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int k = j * V + i;
-          u[k] *= r;
-          if (live) {  // (a row behind the last has x = 0, and with eps = 0 no factor)
-            dw[k] = fmaf(d[k], u[k], dw[k]);
-            if (SHIFT) db[k] += d[k];
-          }
-          d[k] *= w[i];
-          c1 = fmaf(d[k], u[k], c1);
-          c2 += d[k];
+          dw[k] = fmaf(d[k], u[k], dw[k]);
+          if (SHIFT) db[k] += d[k];
         }
+        if (a.weight) {
+          float w[V];
+          load_floats(sh.weight + (j * g.lanes + lane) * V, w);
+          scale_by<V>(d + j * V, w);
+        }
+        add_products<V>(c1, d + j * V, u + j * V);
+        if (a.center)
+#pragma unroll
+          for (int i = 0; i < V; ++i) c2 += d[j * V + i];
       }
-    }
-    c1 = row_sum(c1, g.lanes) * inv_span;
-    c2 = a.center ? row_sum(c2, g.lanes) * inv_span : 0.f;
-    if (live) {
-      T* dst = static_cast<T*>(a.out) + at.t * a.out_stride_t + at.hh * a.out_stride_h + lane * V;
+    const float m1 = row_sum(c1.x + c1.y, g.lanes) * -inv_span;
+    const float m2 = a.center ? row_sum(c2, g.lanes) * inv_span : 0.f;
+    if (live)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int vec = j * g.lanes + lane;
-        if (vec * V < a.span)
+        if (normed[j]) {
+          const float2 f = make_float2(m1, m1), off = make_float2(-m2, -m2);
+          if constexpr (V % 2 == 0) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) d[j * V + i] = r * (fmaf(-u[j * V + i], c1, d[j * V + i]) - c2);
-        if (vec < g.vectors) *reinterpret_cast<W*>(dst + j * g.lanes * V) = narrow<T, V>(d + j * V).u;
+            for (int i = j * V; i < j * V + V; i += 2) {
+              float2 z = fma2(make_float2(u[i], u[i + 1]), f, make_float2(d[i], d[i + 1]));
+              z = fma2(make_float2(1.f, 1.f), z, off);
+              d[i] = z.x;
+              d[i + 1] = z.y;
+            }
+          } else {
+#pragma unroll
+            for (int i = j * V; i < j * V + V; ++i) d[i] = fmaf(u[i], m1, d[i]) - m2;
+          }
+          scale_all<V>(d + j * V, r);
+        }
+        if (there[j]) *reinterpret_cast<W*>(dst.p + j * g.lanes * V) = narrow<T, V>(d + j * V).u;
       }
-    }
+    dst.step(at.step(g, a.h));
   }
   if (!a.dweight && !a.dbias) return;
   // the block's sums: first over the groups of a warp, then over the warps through shared memory
