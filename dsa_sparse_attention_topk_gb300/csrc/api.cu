@@ -607,7 +607,8 @@ static int check_mass(const char* who, const dsa::MassArgs& a, size_t workspace_
   if (a.max_ctx < 1 || a.max_ctx > 1048576) return fail(DSA_ERR_UNSUPPORTED, "%s: max_ctx must be 1..1048576", who);
   if (a.max_pages < (a.max_ctx + DSA_PAGE_SIZE - 1) / DSA_PAGE_SIZE)
     return fail(DSA_ERR_INVALID_ARG, "%s: max_pages < ceil(max_ctx / 64)", who);
-  if (a.num_pages < 1 || a.num_pages > INT64_MAX / 65536) return fail(DSA_ERR_INVALID_ARG, "%s: num_pages must be >= 1", who);
+  if (a.num_pages < 1) return fail(DSA_ERR_INVALID_ARG, "%s: num_pages must be >= 1", who);
+  if (a.num_pages > 1 << 25) return fail(DSA_ERR_UNSUPPORTED, "%s: at most 2^25 pages", who);
   if (!(a.sm_scale > 0.f) || !std::isfinite(a.sm_scale))
     return fail(DSA_ERR_INVALID_ARG, "%s: sm_scale must be positive and finite", who);
   if (a.mass && (!spans(a.mass_stride, a.n_seq) || (a.n_seq > 1 && a.mass_stride < a.max_ctx)))

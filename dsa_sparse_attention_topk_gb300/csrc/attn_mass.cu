@@ -14,13 +14,14 @@
 // m holds whole numbers of 2^-36 and takes additions atomically: integers add up the same in any order, so equal
 // calls give equal bits.
 //
-// Layout.  M = 128 positions (a TMEM lane each), N = up to 64 columns, a column being one head of one query
-// row; the sum over columns then stays within a thread.  Positions are the A operand in tensor memory, 288
-// columns of widened codes; the columns' queries stream through shared memory by TMA in blocks of 64 dims, or stay there
-// while a group's columns fit.  A group is a sequence with its rows (dense) or one row with its entries
-// (sparse); units (group, tile of 128 positions, chunk of N columns) are shared out evenly over one CTA per SM.
+// Layout.  M = 128 positions (a TMEM lane each), N = 16..128 columns, a column being one head of one query row;
+// the sum over columns then stays within a thread.  Positions are the A operand, widened codes in tensor memory;
+// the columns' queries lie in shared memory, by TMA.  A group is a sequence with its rows (dense) or one row with its
+// entries (sparse).  Items (group, tile of 128 positions, chunk of N columns) are shared out evenly over one CTA per
+// SM.  Where a group's columns fit in one chunk, queries stay while the tiles pass and A is a ring of tiles of 128 dims;
+// with more columns (N = 96) the tile stays, 288 columns of tensor memory, while the chunks pass.
 //
-// Bound: tensor cores with many columns (128 x 64 x 576 products a chunk); the cache's bytes with few.
+// Bound: tensor cores with many columns (128 x N x 576 products an item); the cache's bytes with few.
 
 #include <cuda.h>
 
@@ -38,29 +39,35 @@ constexpr int kBlocks = kLatent / 64;             // 64-dim blocks of a row
 constexpr int kPitch = kKvTokBytes + 16;          // a staged record: lanes 16 bytes apart modulo 128 read without conflicts
 constexpr int kStageBytes = kTile * kPitch;
 constexpr int kWarpB = 0, kWarpMma0 = 1, kWarpConv0 = 4, kWarpEpi0 = 8;  // (products: 1 and 2; 3 idles)
-// tensor memory columns: A (32 a block), three accumulators of up to 64, the scales of two tiles, partial sums
-constexpr int kColD = 32 * kBlocks, kSlotsD = 3, kColScale = 480, kColPart = 496;
-constexpr int kSets = 2;                          // sets of warps that take chunks in turn
 constexpr float kMassOne = 68719476736.0f;        // 2^36
 constexpr float kMassMost = 67108864.0f;          // 2^26: one addition's limit
 
-// What the columns of a chunk (N) decide.
+// What the columns of a chunk decide.  N = 96: the tile stays and chunks pass; otherwise tiles pass.
 template <int N> struct Shape {
-  static constexpr int width = N < 32 ? N : 32;   // columns of four warps
-  static constexpr int parts = N / width;         // of them in a set
-  static constexpr int threads = 32 * (kWarpEpi0 + 4 * parts * kSets);
-  static constexpr int stages = N <= 32 ? 2 : 1;  // tiles of staged records
-  static constexpr int slots = N == 64 ? 2 : N == 32 ? 1 : 3;    // chunks of queries in shared memory
-  static constexpr int block = N * 128;                          // bytes of 64 dims
+  static constexpr bool tile_stays = N == 96;
+  static constexpr int width = N >= 96 ? 32 : 16;           // columns of four warps
+  static constexpr int parts = N / width;                   // fours of warps
+  static constexpr int threads = 32 * (kWarpEpi0 + 4 * parts);
+  static constexpr int stages = N <= 32 ? 2 : 1;            // tiles of staged records
+  static constexpr int slots = N == 64 ? 2 : N == 16 ? 3 : 1;  // chunks of queries in shared memory
+  static constexpr int block = N * 128;                     // bytes of 64 dims
   static constexpr int off_stage = slots * kBlocks * block;
   static constexpr int off_col = off_stage + stages * kStageBytes;  // [2][N / 2] pairs of columns, 16 bytes
-  static constexpr int off_limit = off_col + 2 * N * 8;          // [2][N] positions seen
+  static constexpr int off_limit = off_col + 2 * N * 8;     // [2][N] positions seen
   static constexpr int off_ctl = off_limit + 2 * N * 4;
+  // tensor memory columns: accumulators, tiles of 128 dims (64 each), scales and positions of three tiles (with two,
+  // those of the tile after next could be written while the last accumulator of this one is scaled), partial sums
+  static constexpr int accs = N >= 96 ? 2 : N == 64 ? 3 : 4;
+  static constexpr int ring = tile_stays ? 5 : N == 128 ? 3 : N == 64 ? 4 : 5;
+  static constexpr int col_a = accs * N;
+  static constexpr int col_info = col_a + (tile_stays ? 288 : 64 * ring);
+  static constexpr int col_part = col_info + 24;
+  static_assert(col_part + 2 * (parts - 1) <= 512 && ring >= accs, "tensor memory");
 };
-constexpr int kMostSlots = 3;
+constexpr int kMostSlots = 3, kMostAccs = 4;
 
 struct MassPlan {
-  int n;             // columns of a chunk: 16, 32 or 64
+  int n;             // columns of a chunk: 16, 32, 64, 96 or 128
   int groups;
   size_t off_cols, off_groups, off_rank;
 };
@@ -186,25 +193,26 @@ mass_query_kernel(MassArgs a, MassWs ws) {
 struct MassCtl {
   uint64_t b_full[kMostSlots][5], b_empty[kMostSlots][5];   // a chunk's queries, 128 dims (two blocks) a barrier
   uint64_t a_full[5], a_empty[5];                           // tiles of 128 dims
-  uint64_t d_full[kSets][kSlotsD], d_free[kSlotsD];         // (a set waits for its own chunks alone)
+  uint64_t d_full[kMostAccs], d_free[kMostAccs];
   uint64_t part_full[2];
   uint64_t col_full[2], col_empty[2];
   uint64_t drained[2];
   int all_seen[2];                      // every column of the chunk sees the whole tile
   long long scan[24];
-  int start_group, start_tile, start_chunk, abort;
-  long long units;
+  int first_group, first_tile, first_chunk, items, abort;
   uint32_t tmem;
 };
 constexpr int kMostSmem = 232448;
-static_assert(Shape<64>::off_ctl + sizeof(MassCtl) <= kMostSmem &&
-              Shape<32>::off_ctl + sizeof(MassCtl) <= kMostSmem && Shape<16>::off_ctl + sizeof(MassCtl) <= kMostSmem, "shared memory");
+static_assert(Shape<128>::off_ctl + sizeof(MassCtl) <= kMostSmem && Shape<96>::off_ctl + sizeof(MassCtl) <= kMostSmem &&
+              Shape<64>::off_ctl + sizeof(MassCtl) <= kMostSmem && Shape<32>::off_ctl + sizeof(MassCtl) <= kMostSmem &&
+              Shape<16>::off_ctl + sizeof(MassCtl) <= kMostSmem, "shared memory");
 
-// A walk over the CTA's units, tile by tile: chunks [c0, c1) of tile `tile` of group g
+// A walk over the CTA's items: chunk c of tile `tile` of group g
 struct Walk {
-  long long left;
-  int g, tile, c0, c1, chunks, tiles;
+  int left, g, tile, c, chunks, tiles;
   int4 grp;
+  __device__ __forceinline__ bool same_tile(const Walk& o) const { return g == o.g && tile == o.tile; }
+  __device__ __forceinline__ bool same_chunk(const Walk& o) const { return g == o.g && c == o.c; }
 };
 template <int N>
 __device__ __forceinline__ void open_group(const MassWs& ws, Walk& w) {
@@ -212,31 +220,39 @@ __device__ __forceinline__ void open_group(const MassWs& ws, Walk& w) {
   w.tiles = (w.grp.x + kTile - 1) / kTile;
   w.chunks = (w.grp.z + N - 1) / N;
 }
-template <bool SPARSE, int N>
+template <int N>
 __device__ __forceinline__ bool walk_begin(const MassWs& ws, const MassCtl& ctl, Walk& w) {
-  w.left = ctl.units;
+  w.left = ctl.items;
   if (w.left <= 0) return false;
-  w.g = ctl.start_group;
-  w.tile = ctl.start_tile;
+  w.g = ctl.first_group;
+  w.tile = ctl.first_tile;
+  w.c = ctl.first_chunk;
   open_group<N>(ws, w);
-  w.c0 = SPARSE ? 0 : ctl.start_chunk;
-  w.c1 = SPARSE ? w.chunks : static_cast<int>(min(static_cast<long long>(w.chunks), w.c0 + w.left));
   return true;
 }
-// on to the next tile; false at the end.  (The groups behind have units as long as some are left.)
-template <bool SPARSE, int N>
+// on to the next item; false at the end.  (The groups behind have items as long as some are left.)
+template <int N>
 __device__ __forceinline__ bool walk_next(const MassWs& ws, int groups, Walk& w) {
-  w.left -= SPARSE ? 1 : w.c1 - w.c0;
-  if (w.left <= 0) return false;
-  if (++w.tile >= w.tiles) {
-    w.tile = 0;
+  if (--w.left <= 0) return false;
+  bool wrap;
+  if (Shape<N>::tile_stays) {
+    if ((wrap = ++w.c == w.chunks)) {
+      w.c = 0;
+      wrap = ++w.tile == w.tiles;
+    }
+  } else {
+    if ((wrap = ++w.tile == w.tiles)) {
+      w.tile = 0;
+      wrap = ++w.c == w.chunks;
+    }
+  }
+  if (wrap) {
+    w.tile = w.c = 0;
     do {
       if (++w.g >= groups) return false;
       open_group<N>(ws, w);
     } while (!w.tiles || !w.chunks);
   }
-  w.c0 = 0;
-  w.c1 = SPARSE ? w.chunks : static_cast<int>(min(static_cast<long long>(w.chunks), w.left));
   return true;
 }
 
@@ -327,33 +343,31 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
       tc::mbar_init(&ctl.a_full[i], 4);
       tc::mbar_init(&ctl.a_empty[i], 1);
     }
+    for (int i = 0; i < S::accs; ++i) {
+      tc::mbar_init(&ctl.d_full[i], 1);
+      tc::mbar_init(&ctl.d_free[i], 4 * S::parts);
+    }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&ctl.drained[i], 1);
-      // (sparse: the sums of the other parts, and where a row has two chunks those of the other set)
-      tc::mbar_init(&ctl.part_full[i], max(1, 4 * (a.h_s > N ? 2 * S::parts - 1 : S::parts - 1)));
+      tc::mbar_init(&ctl.part_full[i], S::parts > 1 ? 4 * (S::parts - 1) : 1);
       tc::mbar_init(&ctl.col_full[i], 1);
       tc::mbar_init(&ctl.col_empty[i], 4 * S::parts);
     }
-    for (int i = 0; i < kSlotsD; ++i) {
-      for (int k = 0; k < kSets; ++k) tc::mbar_init(&ctl.d_full[k][i], 1);
-      tc::mbar_init(&ctl.d_free[i], 4 * S::parts);
-    }
     tc::mbar_fence_init();
-    ctl.start_group = ctl.start_tile = ctl.start_chunk = 0;
+    ctl.first_group = ctl.first_tile = ctl.first_chunk = 0;
   }
   if (warp == kWarpMma0) tc::tmem_alloc(&ctl.tmem, 512);
   pdl_wait();
-  // ---- the CTA's share of the units ----
+  // ---- the CTA's share of the items ----
   {
     const int per = (pl.groups + S::threads - 1) / S::threads;
     const int g0 = min(tid * per, pl.groups), g1 = min(g0 + per, pl.groups);
     long long sum = 0;
-    auto units_of = [&](int g) {
+    auto items_of = [&](int g) {
       const int4 grp = ws.groups[g];
-      const long long tiles = (grp.x + kTile - 1) / kTile;
-      return grp.z == 0 ? 0ll : SPARSE ? tiles : tiles * ((grp.z + N - 1) / N);
+      return static_cast<long long>((grp.x + kTile - 1) / kTile) * ((grp.z + N - 1) / N);
     };
-    for (int g = g0; g < g1; ++g) sum += units_of(g);
+    for (int g = g0; g < g1; ++g) sum += items_of(g);
     long long incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -368,15 +382,16 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
       total += ctl.scan[w];
     }
     const long long start = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
-    if (tid == 0) ctl.units = end - start;
+    if (tid == 0) ctl.items = static_cast<int>(end - start);
     if (start < end && start >= before && start < before + sum) {
       int g = g0;
       long long rest = start - before;
-      for (long long u; rest >= (u = units_of(g)); ++g) rest -= u;
-      const int chunks = (ws.groups[g].z + N - 1) / N;
-      ctl.start_group = g;
-      ctl.start_tile = static_cast<int>(SPARSE ? rest : rest / chunks);
-      ctl.start_chunk = static_cast<int>(SPARSE ? 0 : rest % chunks);
+      for (long long u; rest >= (u = items_of(g)); ++g) rest -= u;
+      const int inner = S::tile_stays ? (ws.groups[g].z + N - 1) / N : (ws.groups[g].x + kTile - 1) / kTile;
+      const int at = static_cast<int>(rest % inner), outer = static_cast<int>(rest / inner);
+      ctl.first_group = g;
+      ctl.first_tile = S::tile_stays ? outer : at;
+      ctl.first_chunk = S::tile_stays ? at : outer;
     }
   }
   tc::fence_before_sync();
@@ -389,129 +404,118 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
     return tc::mbar_try_wait(bar, parity & 1u) || wait_on(bar, parity & 1u, &ctl.abort, a.status);
   };
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-  // chunk slots in order; of a group whose chunks all fit, the slots stay while its tiles last
-  auto skip = [](int& slot, uint32_t& phase, int by) {  // (by at most all slots)
-    slot += by;
-    if (slot >= S::slots) {
-      slot -= S::slots;
-      phase ^= 1u;
-    }
-  };
   Walk w;
+  // (The roles' loops are rolled up: together they have to stay within the instruction cache.)
 
   if (warp == kWarpB) {
     // ---- a chunk's queries, 128 dims at a time, and its columns' constants; columns behind the group's last have
     // no weight ----
-    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
-      int slot = 0, have = -1;
+    if (walk_begin<N>(ws, ctl, w)) {
+      int slot = 0;
       uint32_t phase = 0, n = 0;
-      auto load = [&](int c) {
-        for (int k = 0; k < 5; ++k) {
-          if (!wait_warp(&ctl.b_empty[slot][k], phase ^ 1u)) return false;
-          if (lane == 0) {
-            uint64_t* bar = &ctl.b_full[slot][k];
-            uint8_t* to = smem + (slot * kBlocks + 2 * k) * S::block;
-            tc::mbar_arrive_expect_tx(bar, (k < 4 ? 2 : 1) * S::block);
-            tc::tma_load_3d(to, &q_map, 128 * k, w.grp.y + c * N, 0, bar);
-            if (k < 4) tc::tma_load_3d(to + S::block, &q_map, 128 * k + 64, w.grp.y + c * N, 0, bar);
-          }
-        }
-        skip(slot, phase, 1);
-        return true;
-      };
-      bool ok = true;
-      do {
-        const bool keep = w.chunks <= S::slots;
-        if (keep && have != w.g)
-          for (int c = 0; ok && c < w.chunks; ++c) ok = load(c);
-        have = w.g;
-        for (int c = w.c0; ok && c < w.c1; ++c, ++n) {
-          const int buf = n & 1;
-          float4 info[(N + 31) / 32];
-          int least = INT32_MAX;
+      bool ok = true, more = true, fresh = true;  // fresh: other columns than the item's before
+      while (ok && more) {
+        const int buf = n & 1;
+        float4 info[(N + 31) / 32];
+        int least = INT32_MAX;
 #pragma unroll
-          for (int i = 0; i < (N + 31) / 32; ++i) {
-            const int col = c * N + 32 * i + lane;
-            info[i] = make_float4(0.f, -INFINITY, __int_as_float(INT32_MAX), 0.f);
-            if (32 * i + lane < N && col < w.grp.z) info[i] = ws.cols[w.grp.y + col];
-            least = min(least, __float_as_int(info[i].z));
+        for (int i = 0; i < (N + 31) / 32; ++i) {
+          const int col = w.c * N + 32 * i + lane;
+          info[i] = make_float4(0.f, -INFINITY, __int_as_float(INT32_MAX), 0.f);
+          if (32 * i + lane < N && col < w.grp.z) info[i] = ws.cols[w.grp.y + col];
+          least = min(least, __float_as_int(info[i].z));
+        }
+        if (fresh) {
+#pragma unroll 1
+          for (int k = 0; k < 5; ++k) {
+            ok = wait_warp(&ctl.b_empty[slot][k], phase ^ 1u);
+            if (!ok) break;
+            if (lane == 0) {
+              uint64_t* bar = &ctl.b_full[slot][k];
+              uint8_t* to = smem + (slot * kBlocks + 2 * k) * S::block;
+              tc::mbar_arrive_expect_tx(bar, (k < 4 ? 2 : 1) * S::block);
+              tc::tma_load_3d(to, &q_map, 128 * k, w.grp.y + w.c * N, 0, bar);
+              if (k < 4) tc::tma_load_3d(to + S::block, &q_map, 128 * k + 64, w.grp.y + w.c * N, 0, bar);
+            }
           }
-          if (!keep) ok = load(c);
-          least = __reduce_min_sync(0xffffffffu, least);
-          ok = ok && wait_warp(&ctl.col_empty[buf], (n >> 1) ^ 1u);
           if (!ok) break;
-          float* pairs = reinterpret_cast<float*>(smem + S::off_col) + buf * 2 * N;
-          int* limits = reinterpret_cast<int*>(smem + S::off_limit) + buf * N;
-#pragma unroll
-          for (int i = 0; i < (N + 31) / 32; ++i) {
-            const int at = 32 * i + lane;
-            if (at >= N) continue;
-            pairs[4 * (at >> 1) + (at & 1)] = info[i].x;
-            pairs[4 * (at >> 1) + 2 + (at & 1)] = info[i].y;
-            limits[at] = __float_as_int(info[i].z);
+          if (++slot == S::slots) {
+            slot = 0;
+            phase ^= 1u;
           }
-          if (lane == 0) ctl.all_seen[buf] = SPARSE || least >= (w.tile + 1) * kTile;
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&ctl.col_full[buf]);
         }
-      } while (ok && walk_next<SPARSE, N>(ws, pl.groups, w));
-      // copies in flight must land before the CTA ends (a share may not use all chunks of a group that stays); a
-      // slot that was never loaded is past the phase before its first
-      for (int i = 0; i < S::slots; ++i)
-        for (int k = 0; k < 5; ++k) tc::mbar_drain(&ctl.b_full[i][k], i < slot ? phase : phase ^ 1u, 100000000ull);
-      if (*abort) __nanosleep(1000000);  // (and those of a chunk begun)
+        least = __reduce_min_sync(0xffffffffu, least);
+        ok = wait_warp(&ctl.col_empty[buf], (n >> 1) ^ 1u);
+        if (!ok) break;
+        float* pairs = reinterpret_cast<float*>(smem + S::off_col) + buf * 2 * N;
+        int* limits = reinterpret_cast<int*>(smem + S::off_limit) + buf * N;
+#pragma unroll
+        for (int i = 0; i < (N + 31) / 32; ++i) {
+          const int at = 32 * i + lane;
+          if (at >= N) continue;
+          pairs[4 * (at >> 1) + (at & 1)] = info[i].x;
+          pairs[4 * (at >> 1) + 2 + (at & 1)] = info[i].y;
+          limits[at] = __float_as_int(info[i].z);
+        }
+        if (lane == 0) ctl.all_seen[buf] = SPARSE || least >= (w.tile + 1) * kTile;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl.col_full[buf]);
+        const Walk was = w;
+        more = walk_next<N>(ws, pl.groups, w);
+        fresh = !w.same_chunk(was);
+        ++n;
+      }
+      // copies in flight must land before the CTA ends; a slot that was never loaded is past the phase before its first
+      if (*abort) {
+        for (int i = 0; i < S::slots; ++i)
+          for (int k = 0; k < 5; ++k) tc::mbar_drain(&ctl.b_full[i][k], i < slot ? phase : phase ^ 1u, 100000000ull);
+        __nanosleep(1000000);  // (and those of a chunk begun)
+      }
     }
   } else if (warp == kWarpMma0 || warp == kWarpMma0 + 1) {
-    // ---- products: the two warps take turns, so that one's waits and issue pass while the other's
-    // products run.  (Products of one tile of dims in consecutive chunks may be the two warps': the second is issued
-    // when accumulators in between have been read, in order, behind the first.) ----
+    // ---- products: the two warps take turns, so that one's waits and issue pass while the other's products run.
+    // (A buffer's phases that were the other warp's turn are over: the accumulators that were read say so, and are waited
+    // for first.) ----
     const uint32_t leader = elect_leader(), mine = warp - kWarpMma0;
     constexpr uint32_t idesc = idesc_f16(N);
     const uint32_t b_first = smem_u32(smem) >> 4 | 1u << 16;
-    int slot = 0, base = 0;  // the next chunk's; of a group that stays, its first
-    uint32_t phase = 0, base_phase = 0, d = 0, n = 0, visit = 0;
-    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
-      bool ok = true, more = true;
-      int have = -1;
+    int slot = 0;
+    uint32_t phase = 0, d = 0, visit = 0;  // visit: tiles
+    if (walk_begin<N>(ws, ctl, w)) {
+      bool ok = true, more = true, fresh_a = true, fresh_b = true;
       while (ok && more) {
-        const bool keep = w.chunks <= S::slots, first_visit = have != w.g;
-        if (keep && first_visit) {
-          base = slot;
-          base_phase = phase;
-          skip(slot, phase, w.chunks);
-        }
-        have = w.g;
-        const int c0 = w.c0, c1 = w.c1;
-        more = walk_next<SPARSE, N>(ws, pl.groups, w);
-        for (int c = c0; ok && c < c1; ++c, ++n) {
-          int at = keep ? base : slot;
-          uint32_t ph = keep ? base_phase : phase;
-          if (keep) skip(at, ph, c);
-          else skip(slot, phase, 1);
-          const uint32_t b_chunk = b_first + static_cast<uint32_t>(at * kBlocks * S::block >> 4);
-          // (rolled up: the roles' loops together have to stay within the instruction cache)
+        const Walk was = w;
+        more = walk_next<N>(ws, pl.groups, w);
+        const bool leave_b = !more || !w.same_chunk(was);
+        const bool leave_a = !S::tile_stays || !more || !w.same_tile(was);
+        const uint32_t b_chunk = b_first + static_cast<uint32_t>(slot * kBlocks * S::block >> 4);
 #pragma unroll 1
-          for (int s = 0; s < 5; ++s, ++d) {
-            if ((d & 1) != mine) continue;
-            const uint32_t acc = d % kSlotsD;
-            ok = ok && wait_warp(&ctl.d_free[acc], (d / kSlotsD) ^ 1u);
-            if (c == c0) ok = ok && wait_warp(&ctl.a_full[s], visit);
-            if (!keep || first_visit) ok = ok && wait_warp(&ctl.b_full[at][s], ph);
-            if (!ok) break;
-            tc::fence_after_sync();
-            const uint32_t to = uniform(tmem + kColD + acc * N), from = uniform(tmem + 64 * s);
-            const uint32_t b_lo = uniform(b_chunk + s * (2 * S::block >> 4));
+        for (int s = 0; s < 5; ++s, ++d) {
+          if ((d & 1) != mine) continue;
+          const uint32_t acc = d % S::accs, q = S::tile_stays ? s : d % S::ring;
+          ok = wait_warp(&ctl.d_free[acc], (d / S::accs) ^ 1u);
+          if (fresh_a) ok = ok && wait_warp(&ctl.a_full[q], S::tile_stays ? visit : d / S::ring);
+          if (fresh_b) ok = ok && wait_warp(&ctl.b_full[slot][s], phase);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t to = uniform(tmem + acc * N), from = uniform(tmem + S::col_a + 64 * q);
+          const uint32_t b_lo = uniform(b_chunk + s * (2 * S::block >> 4));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16_ts(to, from + 8 * k, b_lo + 2 * k, idesc, k > 0, leader);
-            if (s < 4)
+          for (int k = 0; k < 4; ++k) mma_f16_ts(to, from + 8 * k, b_lo + 2 * k, idesc, k > 0, leader);
+          if (s < 4)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mma_f16_ts(to, from + 32 + 8 * k, b_lo + (S::block >> 4) + 2 * k, idesc, true, leader);
-            commit_if(&ctl.d_full[n & 1][acc], leader);
-            if (!keep) commit_if(&ctl.b_empty[at][s], leader);
-            if (c == c1 - 1) commit_if(&ctl.a_empty[s], leader);
-          }
+            for (int k = 0; k < 4; ++k) mma_f16_ts(to, from + 32 + 8 * k, b_lo + (S::block >> 4) + 2 * k, idesc, true, leader);
+          commit_if(&ctl.d_full[acc], leader);
+          if (leave_a) commit_if(&ctl.a_empty[q], leader);
+          if (leave_b) commit_if(&ctl.b_empty[slot][s], leader);
         }
-        ++visit;
+        if (leave_b && ++slot == S::slots) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        if (leave_a) ++visit;
+        fresh_a = leave_a;
+        fresh_b = leave_b;
       }
     }
     if (*abort) {  // products in flight must end before the tensor memory is freed
@@ -521,235 +525,252 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
     }
   } else if (warp >= kWarpConv0 && warp < kWarpEpi0) {
     // ---- records: fetched by the warp that widens them to fp16 into tensor memory, 32 positions each, a position a
-    // lane.  (A bulk copy a record, issued by 32 lanes, took 2500 cycles for these 32 in issue alone.)  The next tile's
-    // records are on their way once this one's are read, or before where there is room for two; page
-    // and entry of those behind are looked up meanwhile. ----
+    // lane.  Once 128 dims of a tile's records are read, those of the next tile (that behind it, where there is room for
+    // two) take their place, so each piece has a tile's time to arrive and they share the memory pipe with the widening.  (A
+    // bulk copy a record, issued by 32 lanes, took 2500 cycles for these 32 in issue alone; all pieces at a tile's end 2800.)
+    // Entry, page and slot of the tiles behind are looked up meanwhile. ----
     const int quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    uint8_t* stage0 = smem + S::off_stage + quarter * 32 * kPitch;
+    const uint32_t stage0 = smem_u32(smem + S::off_stage + quarter * 32 * kPitch);
     const int64_t table_end = static_cast<int64_t>(a.max_pages) * kPage;
+    // on to the next tile
+    auto next_tile = [&] {
+      const Walk was = w;
+      bool more = walk_next<N>(ws, pl.groups, w);
+      if (S::tile_stays)
+        while (more && w.same_tile(was)) more = walk_next<N>(ws, pl.groups, w);
+      return more;
+    };
     // the lane's position in a tile, -1: none
-    auto entry = [&](const Walk& at) {
-      const int i = at.tile * kTile + quarter * 32 + lane;
-      return i < at.grp.x ? (SPARSE ? a.idx[static_cast<int64_t>(at.g) * a.topk + i] : i) : -1;
+    auto entry = [&] {
+      const int i = w.tile * kTile + quarter * 32 + lane;
+      return i < w.grp.x ? (SPARSE ? a.idx[static_cast<int64_t>(w.g) * a.topk + i] : i) : -1;
     };
     // its page; a position behind the sequence is none
-    auto lookup = [&](const Walk& at, int& pos) {
-      if (SPARSE && pos >= 0 && (pos >= a.seq_lens[at.grp.w] || pos >= table_end)) {
+    auto lookup = [&](int& pos) {
+      if (SPARSE && pos >= 0 && (pos >= a.seq_lens[w.grp.w] || pos >= table_end)) {
         flag(a.status, DSA_STATUS_BAD_INDEX);
         pos = -1;
       }
       pos = max(pos, -1);
-      return pos >= 0 ? a.page_table[static_cast<int64_t>(at.grp.w) * a.max_pages + pos / kPage] : 0;
+      return pos >= 0 ? a.page_table[static_cast<int64_t>(w.grp.w) * a.max_pages + pos / kPage] : 0;
     };
-    // the 32 records, eight lanes 128 bytes of one at a time
-    auto fetch = [&](int& pos, int page, uint8_t* stage) {
+    // the slots of the eight records of which this lane copies pieces (4 i + lane / 8), -1: none
+    int slots[8];
+    auto open = [&](int& pos, int page) {
       if (pos >= 0 && (page < 0 || page >= a.num_pages)) {
         flag(a.status, DSA_STATUS_BAD_PAGE);
         pos = -1;
       }
-      const uint8_t* src = pos >= 0 ? a.kv_cache + (static_cast<int64_t>(page) * kPage + (pos & (kPage - 1))) * kKvTokBytes : nullptr;
-#pragma unroll 2
-      for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3);
-        const uint8_t* from = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
-        if (!from) continue;
-        const uint32_t to = smem_u32(stage + r * kPitch) + 16 * (lane & 7);
-        from += 16 * (lane & 7);
+      const int slot = pos >= 0 ? page * kPage + (pos & (kPage - 1)) : -1;
 #pragma unroll
-        for (int j = 0; j < 5; ++j)
-          if (j < 4 || (lane & 7) < (kKvTokBytes - 512) / 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to + 128 * j), "l"(from + 128 * j) : "memory");
-      }
+      for (int i = 0; i < 8; ++i) slots[i] = __shfl_sync(0xffffffffu, slot, 4 * i + (lane >> 3));
     };
-    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
-      // turn t fetches tile t and widens tile t - (S::stages - 1)
-      uint32_t t = 0;
-      bool ok = true, have = true;     // tile t is there
-      int pos = entry(w), behind = -1; // its positions; those of the tile to widen
-      int page = lookup(w, pos);
-      while (ok) {
-        if (have) fetch(pos, page, stage0 + (t % S::stages) * kStageBytes);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        const int fetched = pos;
-        const bool now = S::stages == 1 || t > 0;
-        const bool end = !have;
-        have = have && walk_next<SPARSE, N>(ws, pl.groups, w);
-        pos = have ? entry(w) : -1;
-        if (now) {
-          const uint32_t visit = t - (S::stages - 1);
-          if (S::stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-          else asm volatile("cp.async.wait_group 0;" ::: "memory");
-          __syncwarp();
-          const uint8_t* rec = stage0 + (visit % S::stages) * kStageBytes + lane * kPitch;
-          uint32_t scales[8];
-          bool fine = true;
+    // 128 dims of the 32 records, eight lanes 128 bytes of one at a time; with the first the scales too
+    auto fetch = [&](int s, uint32_t stage) {
+      const uint32_t at = 128 * s + 16 * (lane & 7), to = stage + (lane >> 3) * kPitch + at;
+      const bool mine = s < 4 || (lane & 7) < 4;
 #pragma unroll
-          for (int i = 0; i < 5; ++i) {
-            const float v = *reinterpret_cast<const float*>(rec + kKvScaleOff + 4 * i);
-            fine = fine && fabsf(v) * 448.0f < INFINITY;
-            scales[i] = __float_as_uint(v);
-          }
-          if (!fine) scales[0] = 0x7FC00000u;  // NaN: the position has no weight
-          scales[5] = static_cast<uint32_t>(S::stages == 1 ? fetched : behind);
-          scales[6] = scales[7] = 0;
-#pragma unroll 1
-          for (int s = 0; s < 5; ++s) {
-            ok = wait_warp(&ctl.a_empty[s], visit ^ 1u);
-            if (!ok) break;
-            tc::fence_after_sync();
-            if (s == 0) tmem_st8(tmem + lanes + kColScale + 8 * (visit & 1), scales);
-#pragma unroll 2
-            for (int j = 0; j < (s < 4 ? 4 : 2); ++j) {  // 32 codes, 16 columns
-              const uint4 lo = *reinterpret_cast<const uint4*>(rec + 128 * s + 32 * j);
-              const uint4 hi = *reinterpret_cast<const uint4*>(rec + 128 * s + 32 * j + 16);
-              const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-              uint32_t o[16];
+      for (int i = 0; i < 8; ++i) {
+        const uint8_t* from = a.kv_cache + static_cast<int64_t>(slots[i]) * kKvTokBytes + at;
+        if (slots[i] >= 0 && mine) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to + 4 * i * kPitch), "l"(from) : "memory");
+      }
+      if (s == 0 && (lane & 7) < 2) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const __half2 p = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i] & 0xFFFFu)), q = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i] >> 16));
-                o[2 * i] = *reinterpret_cast<const uint32_t*>(&p);
-                o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&q);
-              }
-              tc::tmem_st16(tmem + lanes + 64 * s + 16 * j, o);
-            }
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&ctl.a_full[s]);
-          }
+        for (int i = 0; i < 8; ++i) {
+          const uint8_t* from = a.kv_cache + static_cast<int64_t>(slots[i]) * kKvTokBytes + kKvScaleOff + at;
+          if (slots[i] >= 0)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to + 4 * i * kPitch + kKvScaleOff), "l"(from) : "memory");
         }
-        behind = fetched;
-        if (end || (S::stages == 1 && !have)) break;
-        page = have ? lookup(w, pos) : 0;
-        ++t;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (walk_begin<N>(ws, ctl, w)) {
+      // this lane's positions: of the tile being widened, those staged behind it, and the one whose records are to
+      // be fetched, of which `page` is known
+      int pos[S::stages + 1], page;
+      bool there[S::stages + 1];
+      there[0] = true;
+      pos[0] = entry();
+      page = lookup(pos[0]);
+#pragma unroll
+      for (int k = 0; k < S::stages; ++k) {
+        open(pos[k], page);
+#pragma unroll 1
+        for (int s = 0; s < 5; ++s) fetch(s, stage0 + k * kStageBytes);
+        there[k + 1] = there[k] && next_tile();
+        pos[k + 1] = there[k + 1] ? entry() : -1;
+        page = there[k + 1] ? lookup(pos[k + 1]) : 0;
+      }
+      bool ok = true;
+      uint32_t q = 0;  // tiles of 128 dims widened
+      for (uint32_t visit = 0; ok && there[0]; ++visit) {
+        open(pos[S::stages], page);
+        const bool later = there[S::stages] && next_tile();
+        int later_pos = later ? entry() : -1;
+        const uint32_t stage_at = (visit % S::stages) * kStageBytes;
+        const uint8_t* rec = smem + S::off_stage + stage_at + (quarter * 32 + lane) * kPitch;
+#pragma unroll 1
+        for (int s = 0; s < 5; ++s, ++q) {
+          const uint32_t at = S::tile_stays ? s : q % S::ring;
+          ok = wait_warp(&ctl.a_empty[at], (S::tile_stays ? visit : q / S::ring) ^ 1u);
+          if (!ok) break;
+          tc::fence_after_sync();
+          // (five pieces a staged tile have been asked for since this one)
+          asm volatile("cp.async.wait_group %0;" :: "n"(5 * S::stages - 1) : "memory");
+          __syncwarp();
+          if (s == 0) {
+            uint32_t info[8];
+            bool fine = true;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+              const float v = *reinterpret_cast<const float*>(rec + kKvScaleOff + 4 * i);
+              fine = fine && fabsf(v) * 448.0f < INFINITY;
+              info[i] = __float_as_uint(v);
+            }
+            if (!fine) info[0] = 0x7FC00000u;  // NaN: the position has no weight
+            info[5] = static_cast<uint32_t>(pos[0]);
+            info[6] = info[7] = 0;
+            tmem_st8(tmem + lanes + S::col_info + 8 * (visit % 3), info);
+          }
+#pragma unroll 2
+          for (int j = 0; j < (s < 4 ? 4 : 2); ++j) {  // 32 codes, 16 columns
+            const uint4 lo = *reinterpret_cast<const uint4*>(rec + 128 * s + 32 * j);
+            const uint4 hi = *reinterpret_cast<const uint4*>(rec + 128 * s + 32 * j + 16);
+            const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            uint32_t o[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const __half2 x = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i] & 0xFFFFu)), y = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i] >> 16));
+              o[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
+              o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            tc::tmem_st16(tmem + lanes + S::col_a + 64 * at + 16 * j, o);
+          }
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&ctl.a_full[at]);
+          fetch(s, stage0 + stage_at);
+        }
+        page = later ? lookup(later_pos) : 0;
+#pragma unroll
+        for (int k = 0; k < S::stages; ++k) {
+          pos[k] = pos[k + 1];
+          there[k] = there[k + 1];
+        }
+        pos[S::stages] = later_pos;
+        there[S::stages] = later;
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   } else if (warp >= kWarpEpi0) {
-    // ---- weights: a position a lane, S::width of a chunk's columns each four warps; the two sets take the chunks in
-    // turn, so that one's exponentials pass while the other reads accumulators ----
+    // ---- weights: a position a lane, S::width of a chunk's columns each four warps ----
     constexpr int W = S::width;
-    const int quarter = warp & 3, team = (warp - kWarpEpi0) >> 2, part = team % S::parts, row = quarter * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16, set = team / S::parts;
-    uint32_t d = 0, n = 0, visit = 0, phases = 0;  // (phases: of the set's barriers, a bit each)
-    int slot = 0, base = 0, have = -1;  // chunk slots, as the warps of products count them
-    if (walk_begin<SPARSE, N>(ws, ctl, w)) {
+    const int quarter = warp & 3, part = (warp - kWarpEpi0) >> 2, row = quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    uint32_t d = 0, n = 0, visit = 0;
+    if (walk_begin<N>(ws, ctl, w)) {
       bool ok = true, more = true;
+      float total = 0.f, lost = 0.f;
       while (ok && more) {
-        const bool keep = w.chunks <= S::slots;
-        if (keep && have != w.g) base = slot;
-        if (!keep || have != w.g) slot = (slot + (keep ? w.chunks : w.c1 - w.c0)) % S::slots;
-        have = w.g;
-        float total = 0.f;
+        const uint32_t tile_info = tmem + lanes + S::col_info + 8 * (visit % 3);
+        uint64_t acc[W / 2];
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) acc[i] = 0ull;
         int pos = -1;
-        bool took = false, last = false;  // a chunk of this tile, its last one
-        for (int c = w.c0; ok && c < w.c1; ++c, ++n) {
-          last = (n & 1) == set;
-          if (!last) {
-            d += 5;
-            continue;
-          }
-          uint64_t acc[W / 2];
-#pragma unroll
-          for (int i = 0; i < W / 2; ++i) acc[i] = 0ull;
-          const uint32_t tile_info = tmem + lanes + kColScale + 8 * (visit & 1);
 #pragma unroll 1
-          for (int s = 0; s < 5; ++s, ++d) {
-            const uint32_t at = d % kSlotsD;
-            ok = wait_warp(&ctl.d_full[set][at], phases >> at);
-            if (!ok) break;
-            phases ^= 1u << at;
-            tc::fence_after_sync();
-            const float scale = tmem_ld1(tile_info + s);
-            if (s == 0) pos = __float_as_int(tmem_ld1(tile_info + 5));
-#pragma unroll
-            for (int h = 0; h < W / 16; ++h) {  // (16 columns at a time: 768 threads have 80 registers each)
-              uint32_t v[16];
-              tc::tmem_ld16(tmem + lanes + kColD + at * N + part * W + 16 * h, v);
-              tc::tmem_wait_ld();
-              if (h == W / 16 - 1) {
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&ctl.d_free[at]);
-              }
-              const uint64_t both = pair(scale, scale);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                acc[8 * h + i] = fma_pair(both, pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), acc[8 * h + i]);
-            }
-          }
-          took = true;
-          ok = ok && wait_warp(&ctl.col_full[set], n >> 1);
+        for (int s = 0; s < 5; ++s, ++d) {
+          const uint32_t at = d % S::accs;
+          ok = wait_warp(&ctl.d_full[at], d / S::accs);
           if (!ok) break;
-          const ulonglong2* cols = reinterpret_cast<const ulonglong2*>(smem + S::off_col) + (set * N + part * W) / 2;
-          float sum = 0.f;
-          if (SPARSE || ctl.all_seen[set]) {
-            float odd = 0.f;
-#pragma unroll
-            for (int i = 0; i < W / 2; ++i) {
-              const ulonglong2 k = cols[i];
-              const float2 x = unpair(fma_pair(acc[i], k.x, k.y));
-              sum += ex2(x.x);
-              odd += ex2(x.y);
-            }
-            sum += odd;
-          } else {
-            const int2* limits = reinterpret_cast<const int2*>(smem + S::off_limit) + (set * N + part * W) / 2;
-#pragma unroll
-            for (int i = 0; i < W / 2; ++i) {
-              const ulonglong2 k = cols[i];
-              const int2 lim = limits[i];
-              const float2 x = unpair(fma_pair(acc[i], k.x, k.y));
-              sum += (pos < lim.x ? ex2(x.x) : 0.f) + (pos < lim.y ? ex2(x.y) : 0.f);
-            }
-          }
+          tc::fence_after_sync();
+          const float scale = tmem_ld1(tile_info + s);
+          if (s == 0) pos = __float_as_int(tmem_ld1(tile_info + 5));
+          uint32_t v[W];
+          if constexpr (W == 32) tc::tmem_ld32(tmem + lanes + at * N + part * W, v);
+          else tc::tmem_ld16(tmem + lanes + at * N + part * W, v);
+          tc::tmem_wait_ld();
+          tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&ctl.col_empty[set]);
-          total += sum;
-        }
-        if (!ok) break;
-        if (SPARSE && took) {
-          // the row's weight is the sum of all parts' and sets': the last chunk's first part gathers it, by way of tensor
-          // memory.  (A buffer's sums have been read before the tile after next is: the accumulators hold the sets together.)
-          constexpr int kOthers = 2 * S::parts - 1;
-          const uint32_t buf = visit & 1, cell = tmem + lanes + kColPart + 4 * buf;
-          if (last && part == 0) {
-            const int others = w.chunks == 2 ? kOthers : S::parts - 1;
-            if (others > 0) {
-              ok = wait_warp(&ctl.part_full[buf], visit >> 1);
-              if (!ok) break;
-              tc::fence_after_sync();
-              float v[3] = {0.f, 0.f, 0.f};
+          if (lane == 0) tc::mbar_arrive(&ctl.d_free[at]);
+          const uint64_t both = pair(scale, scale);
 #pragma unroll
-              for (int i = 0; i < 3; ++i)
-                if (i < others) v[i] = tmem_ld1(cell + i);
-              tc::tmem_wait_ld();
-              total += v[0] + v[1] + v[2];
-            }
-          } else {
-            // (in the order: the last set's other parts, then the first set's)
-            tmem_st1(cell + (last ? part - 1 : S::parts - 1 + part), total);
+          for (int i = 0; i < W / 2; ++i)
+            acc[i] = fma_pair(both, pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), acc[i]);
+        }
+        const int buf = n & 1;
+        ok = ok && wait_warp(&ctl.col_full[buf], n >> 1);
+        if (!ok) break;
+        ++n;
+        const ulonglong2* cols = reinterpret_cast<const ulonglong2*>(smem + S::off_col) + (buf * N + part * W) / 2;
+        float sum = 0.f;
+        if (SPARSE || ctl.all_seen[buf]) {
+          float odd = 0.f;
+#pragma unroll
+          for (int i = 0; i < W / 2; ++i) {
+            const ulonglong2 k = cols[i];
+            const float2 x = unpair(fma_pair(acc[i], k.x, k.y));
+            sum += ex2(x.x);
+            odd += ex2(x.y);
+          }
+          sum += odd;
+        } else {
+          const int2* limits = reinterpret_cast<const int2*>(smem + S::off_limit) + (buf * N + part * W) / 2;
+#pragma unroll
+          for (int i = 0; i < W / 2; ++i) {
+            const ulonglong2 k = cols[i];
+            const int2 lim = limits[i];
+            const float2 x = unpair(fma_pair(acc[i], k.x, k.y));
+            sum += (pos < lim.x ? ex2(x.x) : 0.f) + (pos < lim.y ? ex2(x.y) : 0.f);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl.col_empty[buf]);
+        // (a tile may pass tens of thousands of chunks: what the total's rounding drops is kept.  Weights are not negative, and
+        // once their sum exceeds a chunk's it stays the larger one)
+        const float before = total;
+        total += sum;
+        if (S::tile_stays) lost += before >= sum ? sum - (total - before) : before - (total - sum);
+        const Walk was = w;
+        more = walk_next<N>(ws, pl.groups, w);
+        if (S::tile_stays && more && w.same_tile(was)) continue;
+        // the tile is done
+        if (S::tile_stays) total += lost == lost ? lost : 0.f;  // (infinite sums have none)
+        bool gives = pos >= 0;
+        if (SPARSE && S::parts > 1) {
+          // an entry's weight is the sum of all parts': the first gathers it, by way of tensor memory.  (A buffer's sums have
+          // been read before the tile after next is: the accumulators hold the parts together.)
+          const uint32_t cell = tmem + lanes + S::col_part + (S::parts - 1) * (visit & 1);
+          if (part > 0) {
+            tmem_st1(cell + part - 1, total);
             tc::tmem_wait_st();
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&ctl.part_full[buf]);
+            if (lane == 0) tc::mbar_arrive(&ctl.part_full[visit & 1]);
+            gives = false;
+          } else {
+            ok = wait_warp(&ctl.part_full[visit & 1], visit >> 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+            float v[S::parts];
+#pragma unroll
+            for (int i = 1; i < S::parts; ++i) v[i] = tmem_ld1(cell + i - 1);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 1; i < S::parts; ++i) total += v[i];
           }
         }
-        if (took && pos >= 0 && (!SPARSE || (last && part == 0))) {
-          if (SPARSE && a.weights) a.weights[static_cast<int64_t>(w.g) * a.topk + w.tile * kTile + row] = total;
+        if (gives) {
+          if (SPARSE && a.weights) a.weights[static_cast<int64_t>(was.g) * a.topk + was.tile * kTile + row] = total;
           if (a.mass) {
             if (total != total) flag(a.status, DSA_STATUS_NAN_SCORE);
             else if (total > 0.f)
-              atomicAdd(reinterpret_cast<unsigned long long*>(a.mass + static_cast<int64_t>(w.grp.w) * a.mass_stride + pos),
+              atomicAdd(reinterpret_cast<unsigned long long*>(a.mass + static_cast<int64_t>(was.grp.w) * a.mass_stride + pos),
                         static_cast<unsigned long long>(__float2ll_rn(fminf(total, kMassMost) * kMassOne)));
           }
         }
-        const int g = w.g, chunks = w.chunks;
-        more = walk_next<SPARSE, N>(ws, pl.groups, w);
-        // a group that stayed gives its slots back: the set that read its last accumulator does
-        if (part == 0 && quarter == 0 && last && keep && more && w.g != g && lane < 5)
-          for (int c = 0; c < chunks; ++c) tc::mbar_arrive(&ctl.b_empty[(base + c) % S::slots][lane]);
+        total = lost = 0.f;
         ++visit;
       }
     }
@@ -767,7 +788,7 @@ MassPlan make_plan(int n_q, int h_s, int n_seq, bool sparse) {
   p.groups = sparse ? n_q : n_seq;
   // a chunk's columns: all of a group of average rows where they fit
   const int64_t cols = static_cast<int64_t>(h_s) * (sparse ? 1 : std::max(1, (n_q + n_seq - 1) / n_seq));
-  p.n = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
+  p.n = cols <= 16 ? 16 : cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 96;
   const size_t columns = static_cast<size_t>(n_q) * h_s;
   p.off_cols = round_up(columns * kLatent * 2, 256);
   p.off_groups = p.off_cols + round_up(columns * 16, 256);
@@ -842,7 +863,9 @@ cudaError_t launch_attn_mass(const MassArgs& a, cudaStream_t s, const char** err
   switch (pl.n) {
     case 16: return sparse ? launch_main<true, 16>(q_map, a, pl, ws, grid, s) : launch_main<false, 16>(q_map, a, pl, ws, grid, s);
     case 32: return sparse ? launch_main<true, 32>(q_map, a, pl, ws, grid, s) : launch_main<false, 32>(q_map, a, pl, ws, grid, s);
-    default: return sparse ? launch_main<true, 64>(q_map, a, pl, ws, grid, s) : launch_main<false, 64>(q_map, a, pl, ws, grid, s);
+    case 64: return sparse ? launch_main<true, 64>(q_map, a, pl, ws, grid, s) : launch_main<false, 64>(q_map, a, pl, ws, grid, s);
+    case 128: return sparse ? launch_main<true, 128>(q_map, a, pl, ws, grid, s) : launch_main<false, 128>(q_map, a, pl, ws, grid, s);
+    default: return launch_main<false, 96>(q_map, a, pl, ws, grid, s);  // (a row alone has 128 columns at most)
   }
 }
 
