@@ -17,9 +17,8 @@
 // Layout.  M = 128 positions (a TMEM lane each), N = 16..128 columns, a column being one head of one query row;
 // the sum over columns then stays within a thread.  Positions are the A operand, widened codes in tensor memory;
 // the columns' queries lie in shared memory, by TMA.  A group is a sequence with its rows (dense) or one row with its
-// entries (sparse).  Items (group, tile of 128 positions, chunk of N columns) are shared out evenly over one CTA per
-// SM.  Where a group's columns fit in one chunk, queries stay while the tiles pass and A is a ring of tiles of 128 dims;
-// with more columns (N = 96) the tile stays, 288 columns of tensor memory, while the chunks pass.
+// entries (sparse).  Items (group, chunk of N columns, tile of 128 positions) are shared out evenly over one CTA per
+// SM; a chunk's queries stay while its tiles pass, each tile a ring of pieces of 128 dims.
 //
 // Bound: tensor cores with many columns (128 x N x 576 products an item); the cache's bytes with few.
 
@@ -36,16 +35,19 @@ namespace {
 
 constexpr int kTile = 128;                        // positions of an MMA
 constexpr int kBlocks = kLatent / 64;             // 64-dim blocks of a row
-constexpr int kPitch = kKvTokBytes + 16;          // a staged record: lanes 16 bytes apart modulo 128 read without conflicts
-constexpr int kStageBytes = kTile * kPitch;
-constexpr int kWarpB = 0, kWarpMma0 = 1, kWarpConv0 = 4, kWarpEpi0 = 8;  // (products: 1 and 2; 3 idles)
+// A tile's staged records, in the order in which they are worked on: piece 0 dims 512.. with the scales (96 bytes a
+// position), pieces 1..4 dims 128 (s - 1) .. of 128 bytes a position in the 128-byte swizzle, which lanes read without
+// conflicts.  dim0(s) is the piece's first.
+constexpr int kPiece = kTile * 128, kPiece0 = 96, kStageBytes = 4 * kPiece + kTile * kPiece0;
+__host__ __device__ constexpr int dim0(int s) { return s == 0 ? 512 : 128 * (s - 1); }
+__host__ __device__ constexpr int piece_at(int s) { return s == 0 ? 4 * kPiece : (s - 1) * kPiece; }
+constexpr int kWarpB = 0, kWarpMma0 = 1, kWarpRec = 3, kWarpConv0 = 4, kWarpEpi0 = 8;  // (products: 1 and 2)
 constexpr float kMassOne = 68719476736.0f;        // 2^36
 constexpr float kMassMost = 67108864.0f;          // 2^26: one addition's limit
 
-// What the columns of a chunk decide.  N = 96: the tile stays and chunks pass; otherwise tiles pass.
+// What the columns of a chunk decide.
 template <int N> struct Shape {
-  static constexpr bool tile_stays = N == 96;
-  static constexpr int width = N >= 96 ? 32 : 16;           // columns of four warps
+  static constexpr int width = N == 128 ? 32 : 16;          // columns of four warps
   static constexpr int parts = N / width;                   // fours of warps
   static constexpr int threads = 32 * (kWarpEpi0 + 4 * parts);
   static constexpr int stages = N <= 32 ? 2 : 1;            // tiles of staged records
@@ -54,20 +56,21 @@ template <int N> struct Shape {
   static constexpr int off_stage = slots * kBlocks * block;
   static constexpr int off_col = off_stage + stages * kStageBytes;  // [2][N / 2] pairs of columns, 16 bytes
   static constexpr int off_limit = off_col + 2 * N * 8;     // [2][N] positions seen
-  static constexpr int off_ctl = off_limit + 2 * N * 4;
+  static constexpr int off_slot = off_limit + 2 * N * 4;    // [stages + 1][128] slots of a tile's records, -1: none
+  static constexpr int off_ctl = off_slot + (stages + 1) * kTile * 4;
   // tensor memory columns: accumulators, tiles of 128 dims (64 each), scales and positions of three tiles (with two,
   // those of the tile after next could be written while the last accumulator of this one is scaled), partial sums
-  static constexpr int accs = N >= 96 ? 2 : N == 64 ? 3 : 4;
-  static constexpr int ring = tile_stays ? 5 : N == 128 ? 3 : N == 64 ? 4 : 5;
+  static constexpr int accs = N == 128 ? 2 : N == 64 ? 3 : 4;
+  static constexpr int ring = N == 128 ? 3 : N == 64 ? 4 : 5;
   static constexpr int col_a = accs * N;
-  static constexpr int col_info = col_a + (tile_stays ? 288 : 64 * ring);
+  static constexpr int col_info = col_a + 64 * ring;
   static constexpr int col_part = col_info + 24;
   static_assert(col_part + 2 * (parts - 1) <= 512 && ring >= accs, "tensor memory");
 };
 constexpr int kMostSlots = 3, kMostAccs = 4;
 
 struct MassPlan {
-  int n;             // columns of a chunk: 16, 32, 64, 96 or 128
+  int n;             // columns of a chunk: 16, 32, 64 or 128
   int groups;
   size_t off_cols, off_groups, off_rank;
 };
@@ -193,6 +196,7 @@ mass_query_kernel(MassArgs a, MassWs ws) {
 struct MassCtl {
   uint64_t b_full[kMostSlots][5], b_empty[kMostSlots][5];   // a chunk's queries, 128 dims (two blocks) a barrier
   uint64_t a_full[5], a_empty[5];                           // tiles of 128 dims
+  uint64_t rec_full[2][5], rec_empty[2][5];                 // of the staged records, 128 dims a barrier
   uint64_t d_full[kMostAccs], d_free[kMostAccs];
   uint64_t part_full[2];
   uint64_t col_full[2], col_empty[2];
@@ -203,15 +207,13 @@ struct MassCtl {
   uint32_t tmem;
 };
 constexpr int kMostSmem = 232448;
-static_assert(Shape<128>::off_ctl + sizeof(MassCtl) <= kMostSmem && Shape<96>::off_ctl + sizeof(MassCtl) <= kMostSmem &&
-              Shape<64>::off_ctl + sizeof(MassCtl) <= kMostSmem && Shape<32>::off_ctl + sizeof(MassCtl) <= kMostSmem &&
+static_assert(Shape<128>::off_ctl + sizeof(MassCtl) <= kMostSmem && Shape<64>::off_ctl + sizeof(MassCtl) <= kMostSmem && Shape<32>::off_ctl + sizeof(MassCtl) <= kMostSmem &&
               Shape<16>::off_ctl + sizeof(MassCtl) <= kMostSmem, "shared memory");
 
 // A walk over the CTA's items: chunk c of tile `tile` of group g
 struct Walk {
   int left, g, tile, c, chunks, tiles;
   int4 grp;
-  __device__ __forceinline__ bool same_tile(const Walk& o) const { return g == o.g && tile == o.tile; }
   __device__ __forceinline__ bool same_chunk(const Walk& o) const { return g == o.g && c == o.c; }
 };
 template <int N>
@@ -234,25 +236,14 @@ __device__ __forceinline__ bool walk_begin(const MassWs& ws, const MassCtl& ctl,
 template <int N>
 __device__ __forceinline__ bool walk_next(const MassWs& ws, int groups, Walk& w) {
   if (--w.left <= 0) return false;
-  bool wrap;
-  if (Shape<N>::tile_stays) {
-    if ((wrap = ++w.c == w.chunks)) {
-      w.c = 0;
-      wrap = ++w.tile == w.tiles;
-    }
-  } else {
-    if ((wrap = ++w.tile == w.tiles)) {
-      w.tile = 0;
-      wrap = ++w.c == w.chunks;
-    }
-  }
-  if (wrap) {
-    w.tile = w.c = 0;
-    do {
-      if (++w.g >= groups) return false;
-      open_group<N>(ws, w);
-    } while (!w.tiles || !w.chunks);
-  }
+  if (++w.tile < w.tiles) return true;
+  w.tile = 0;
+  if (++w.c < w.chunks) return true;
+  w.c = 0;
+  do {
+    if (++w.g >= groups) return false;
+    open_group<N>(ws, w);
+  } while (!w.tiles || !w.chunks);
   return true;
 }
 
@@ -315,6 +306,11 @@ __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
 __device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" :: "r"(taddr), "r"(__float_as_uint(v)) : "memory");
 }
+// 16 bytes of global to shared memory, asynchronously, where `on`
+__device__ __forceinline__ void copy16_if(bool on, uint32_t to, const void* from) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n @p cp.async.cg.shared.global [%0], [%1], 16;\n}"
+               :: "r"(to), "l"(from), "r"(static_cast<uint32_t>(on)) : "memory");
+}
 // a bounded wait (tc::mbar_wait) out of line, behind one attempt in line
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* status) {
   return tc::mbar_wait(bar, parity, abort, status);
@@ -322,7 +318,8 @@ __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile in
 
 template <bool SPARSE, int N>
 __global__ void __launch_bounds__(Shape<N>::threads, 1)
-attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan pl, MassWs ws) {
+attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap piece0_map,
+                 const __grid_constant__ CUtensorMap piece_map, MassArgs a, MassPlan pl, MassWs ws) {
   using S = Shape<N>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -343,6 +340,11 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
       tc::mbar_init(&ctl.a_full[i], 4);
       tc::mbar_init(&ctl.a_empty[i], 1);
     }
+    for (int i = 0; i < S::stages; ++i)
+      for (int k = 0; k < 5; ++k) {
+        tc::mbar_init(&ctl.rec_full[i][k], SPARSE ? 33 : 1);  // (the copies of 32 lanes, and what the warp wrote itself)
+        tc::mbar_init(&ctl.rec_empty[i][k], 4);
+      }
     for (int i = 0; i < S::accs; ++i) {
       tc::mbar_init(&ctl.d_full[i], 1);
       tc::mbar_init(&ctl.d_free[i], 4 * S::parts);
@@ -387,11 +389,10 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
       int g = g0;
       long long rest = start - before;
       for (long long u; rest >= (u = items_of(g)); ++g) rest -= u;
-      const int inner = S::tile_stays ? (ws.groups[g].z + N - 1) / N : (ws.groups[g].x + kTile - 1) / kTile;
-      const int at = static_cast<int>(rest % inner), outer = static_cast<int>(rest / inner);
+      const int tiles = (ws.groups[g].x + kTile - 1) / kTile;
       ctl.first_group = g;
-      ctl.first_tile = S::tile_stays ? outer : at;
-      ctl.first_chunk = S::tile_stays ? at : outer;
+      ctl.first_tile = static_cast<int>(rest % tiles);
+      ctl.first_chunk = static_cast<int>(rest / tiles);
     }
   }
   tc::fence_before_sync();
@@ -432,10 +433,10 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
             if (!ok) break;
             if (lane == 0) {
               uint64_t* bar = &ctl.b_full[slot][k];
-              uint8_t* to = smem + (slot * kBlocks + 2 * k) * S::block;
-              tc::mbar_arrive_expect_tx(bar, (k < 4 ? 2 : 1) * S::block);
-              tc::tma_load_3d(to, &q_map, 128 * k, w.grp.y + w.c * N, 0, bar);
-              if (k < 4) tc::tma_load_3d(to + S::block, &q_map, 128 * k + 64, w.grp.y + w.c * N, 0, bar);
+              uint8_t* to = smem + (slot * kBlocks + dim0(k) / 64) * S::block;
+              tc::mbar_arrive_expect_tx(bar, (k ? 2 : 1) * S::block);
+              tc::tma_load_3d(to, &q_map, dim0(k), w.grp.y + w.c * N, 0, bar);
+              if (k) tc::tma_load_3d(to + S::block, &q_map, dim0(k) + 64, w.grp.y + w.c * N, 0, bar);
             }
           }
           if (!ok) break;
@@ -480,41 +481,38 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
     constexpr uint32_t idesc = idesc_f16(N);
     const uint32_t b_first = smem_u32(smem) >> 4 | 1u << 16;
     int slot = 0;
-    uint32_t phase = 0, d = 0, visit = 0;  // visit: tiles
+    uint32_t phase = 0, d = 0;
     if (walk_begin<N>(ws, ctl, w)) {
-      bool ok = true, more = true, fresh_a = true, fresh_b = true;
+      bool ok = true, more = true, fresh_b = true;
       while (ok && more) {
         const Walk was = w;
         more = walk_next<N>(ws, pl.groups, w);
         const bool leave_b = !more || !w.same_chunk(was);
-        const bool leave_a = !S::tile_stays || !more || !w.same_tile(was);
         const uint32_t b_chunk = b_first + static_cast<uint32_t>(slot * kBlocks * S::block >> 4);
 #pragma unroll 1
         for (int s = 0; s < 5; ++s, ++d) {
           if ((d & 1) != mine) continue;
-          const uint32_t acc = d % S::accs, q = S::tile_stays ? s : d % S::ring;
+          const uint32_t acc = d % S::accs, q = d % S::ring;
           ok = wait_warp(&ctl.d_free[acc], (d / S::accs) ^ 1u);
-          if (fresh_a) ok = ok && wait_warp(&ctl.a_full[q], S::tile_stays ? visit : d / S::ring);
+          ok = ok && wait_warp(&ctl.a_full[q], d / S::ring);
           if (fresh_b) ok = ok && wait_warp(&ctl.b_full[slot][s], phase);
           if (!ok) break;
           tc::fence_after_sync();
           const uint32_t to = uniform(tmem + acc * N), from = uniform(tmem + S::col_a + 64 * q);
-          const uint32_t b_lo = uniform(b_chunk + s * (2 * S::block >> 4));
+          const uint32_t b_lo = uniform(b_chunk + dim0(s) / 64 * (S::block >> 4));
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma_f16_ts(to, from + 8 * k, b_lo + 2 * k, idesc, k > 0, leader);
-          if (s < 4)
+          if (s > 0)
 #pragma unroll
             for (int k = 0; k < 4; ++k) mma_f16_ts(to, from + 32 + 8 * k, b_lo + (S::block >> 4) + 2 * k, idesc, true, leader);
           commit_if(&ctl.d_full[acc], leader);
-          if (leave_a) commit_if(&ctl.a_empty[q], leader);
+          commit_if(&ctl.a_empty[q], leader);
           if (leave_b) commit_if(&ctl.b_empty[slot][s], leader);
         }
         if (leave_b && ++slot == S::slots) {
           slot = 0;
           phase ^= 1u;
         }
-        if (leave_a) ++visit;
-        fresh_a = leave_a;
         fresh_b = leave_b;
       }
     }
@@ -523,120 +521,129 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
       commit_if(&ctl.drained[mine], leader);
       tc::mbar_drain(&ctl.drained[mine], 0, 100000000ull);
     }
-  } else if (warp >= kWarpConv0 && warp < kWarpEpi0) {
-    // ---- records: fetched by the warp that widens them to fp16 into tensor memory, 32 positions each, a position a
-    // lane.  Once 128 dims of a tile's records are read, those of the next tile (that behind it, where there is room for
-    // two) take their place, so each piece has a tile's time to arrive and they share the memory pipe with the widening.  (A
-    // bulk copy a record, issued by 32 lanes, took 2500 cycles for these 32 in issue alone; all pieces at a tile's end 2800.)
-    // Entry, page and slot of the tiles behind are looked up meanwhile. ----
-    const int quarter = warp & 3;
-    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t stage0 = smem_u32(smem + S::off_stage + quarter * 32 * kPitch);
-    const int64_t table_end = static_cast<int64_t>(a.max_pages) * kPage;
-    // on to the next tile
-    auto next_tile = [&] {
-      const Walk was = w;
-      bool more = walk_next<N>(ws, pl.groups, w);
-      if (S::tile_stays)
-        while (more && w.same_tile(was)) more = walk_next<N>(ws, pl.groups, w);
-      return more;
-    };
-    // the lane's position in a tile, -1: none
-    auto entry = [&] {
-      const int i = w.tile * kTile + quarter * 32 + lane;
-      return i < w.grp.x ? (SPARSE ? a.idx[static_cast<int64_t>(w.g) * a.topk + i] : i) : -1;
-    };
-    // its page; a position behind the sequence is none
-    auto lookup = [&](int& pos) {
-      if (SPARSE && pos >= 0 && (pos >= a.seq_lens[w.grp.w] || pos >= table_end)) {
-        flag(a.status, DSA_STATUS_BAD_INDEX);
-        pos = -1;
-      }
-      pos = max(pos, -1);
-      return pos >= 0 ? a.page_table[static_cast<int64_t>(w.grp.w) * a.max_pages + pos / kPage] : 0;
-    };
-    // the slots of the eight records of which this lane copies pieces (4 i + lane / 8), -1: none
-    int slots[8];
-    auto open = [&](int& pos, int page) {
-      if (pos >= 0 && (page < 0 || page >= a.num_pages)) {
-        flag(a.status, DSA_STATUS_BAD_PAGE);
-        pos = -1;
-      }
-      const int slot = pos >= 0 ? page * kPage + (pos & (kPage - 1)) : -1;
+  } else if (warp == kWarpRec) {
+    // ---- records, a piece of a tile at a time: of whole pages by TMA, entries by eight lanes 128 bytes of one.  (A bulk
+    // copy a record, issued by 32 lanes, took 2500 cycles for 32 records in issue alone.)  Entry and page of the
+    // tile behind are looked up meanwhile. ----
+    if (walk_begin<N>(ws, ctl, w)) {
+      const int64_t table_end = static_cast<int64_t>(a.max_pages) * kPage;
+      int pos[4], page[4];  // of positions 32 k + lane of a tile, -1: none
+      auto entry = [&] {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) slots[i] = __shfl_sync(0xffffffffu, slot, 4 * i + (lane >> 3));
-    };
-    // 128 dims of the 32 records, eight lanes 128 bytes of one at a time; with the first the scales too
-    auto fetch = [&](int s, uint32_t stage) {
-      const uint32_t at = 128 * s + 16 * (lane & 7), to = stage + (lane >> 3) * kPitch + at;
-      const bool mine = s < 4 || (lane & 7) < 4;
+        for (int k = 0; k < 4; ++k) {
+          const int i = w.tile * kTile + 32 * k + lane;
+          pos[k] = i < w.grp.x ? (SPARSE ? a.idx[static_cast<int64_t>(w.g) * a.topk + i] : i) : -1;
+        }
+      };
+      auto lookup = [&] {
+        const int len = SPARSE ? a.seq_lens[w.grp.w] : 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint8_t* from = a.kv_cache + static_cast<int64_t>(slots[i]) * kKvTokBytes + at;
-        if (slots[i] >= 0 && mine) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to + 4 * i * kPitch), "l"(from) : "memory");
-      }
-      if (s == 0 && (lane & 7) < 2) {
+        for (int k = 0; k < 4; ++k) {
+          if (SPARSE && pos[k] >= 0 && (pos[k] >= len || pos[k] >= table_end)) {
+            flag(a.status, DSA_STATUS_BAD_INDEX);
+            pos[k] = -1;
+          }
+          page[k] = pos[k] >= 0 ? a.page_table[static_cast<int64_t>(w.grp.w) * a.max_pages + pos[k] / kPage] : 0;
+        }
+      };
+      entry();
+      lookup();
+      bool ok = true, more = true;
+      for (uint32_t t = 0; ok && more; ++t) {
+        int* s_slot = reinterpret_cast<int*>(smem + S::off_slot) + (t % (S::stages + 1)) * kTile;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint8_t* from = a.kv_cache + static_cast<int64_t>(slots[i]) * kKvTokBytes + kKvScaleOff + at;
-          if (slots[i] >= 0)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to + 4 * i * kPitch + kKvScaleOff), "l"(from) : "memory");
+        for (int k = 0; k < 4; ++k) {
+          if (pos[k] >= 0 && (page[k] < 0 || page[k] >= a.num_pages)) {
+            flag(a.status, DSA_STATUS_BAD_PAGE);
+            pos[k] = -1;
+          }
+          // (read by the warps that widen before the tile's first piece is given back)
+          s_slot[32 * k + lane] = pos[k] >= 0 ? page[k] * kPage + (pos[k] & (kPage - 1)) : -1;
+        }
+        __syncwarp();
+        const int first_page = s_slot[0], second_page = s_slot[64];  // dense: the tile's two pages, if they are there
+        more = walk_next<N>(ws, pl.groups, w);
+        if (more) entry();
+        const int stage = t % S::stages;
+        uint8_t* to = smem + S::off_stage + stage * kStageBytes;
+#pragma unroll 1
+        for (int s = 0; s < 5; ++s) {
+          ok = wait_warp(&ctl.rec_empty[stage][s], (t / S::stages) ^ 1u);
+          if (!ok) break;
+          uint64_t* bar = &ctl.rec_full[stage][s];
+          if constexpr (SPARSE) {
+            const int piece = lane & 7, width = s ? 128 : kPiece0;
+            const uint8_t* cache = a.kv_cache + dim0(s) + 16 * piece;
+            const uint32_t to32 = smem_u32(to) + piece_at(s) + (lane >> 3) * width;
+            const int least = s || piece < kPiece0 / 16 ? 0 : INT32_MAX;
+#pragma unroll 1
+            for (int i0 = 0; i0 < 32; i0 += 8) {
+              int slot[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) slot[i] = s_slot[4 * (i0 + i) + (lane >> 3)];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t at = s ? (piece ^ ((4 * i + (lane >> 3)) & 7)) << 4 : piece << 4;
+                copy16_if(slot[i] >= least, to32 + 4 * (i0 + i) * width + at, cache + static_cast<int64_t>(slot[i]) * kKvTokBytes);
+              }
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar);
+          } else if (lane == 0) {
+            // (what lies behind the sequence in its last page comes with it and is not looked at)
+            const int bytes = (s ? 128 : kPiece0) * kPage;
+            tc::mbar_arrive_expect_tx(bar, ((first_page >= 0) + (second_page >= 0)) * bytes);
+            const CUtensorMap* map = s ? &piece_map : &piece0_map;
+            if (first_page >= 0) tc::tma_load_3d(to + piece_at(s), map, dim0(s) / 4, first_page, 0, bar);
+            if (second_page >= 0) tc::tma_load_3d(to + piece_at(s) + bytes, map, dim0(s) / 4, second_page, 0, bar);
+          }
+          if (s == 0 && more) lookup();
         }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
+      if (SPARSE) asm volatile("cp.async.wait_all;" ::: "memory");
+      else if (*abort) __nanosleep(1000000);  // copies in flight must land before the CTA ends
+    }
+  } else if (warp >= kWarpConv0 && warp < kWarpEpi0) {
+    // ---- codes widened to fp16 into tensor memory, a position a lane ----
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     if (walk_begin<N>(ws, ctl, w)) {
-      // this lane's positions: of the tile being widened, those staged behind it, and the one whose records are to
-      // be fetched, of which `page` is known
-      int pos[S::stages + 1], page;
-      bool there[S::stages + 1];
-      there[0] = true;
-      pos[0] = entry();
-      page = lookup(pos[0]);
-#pragma unroll
-      for (int k = 0; k < S::stages; ++k) {
-        open(pos[k], page);
-#pragma unroll 1
-        for (int s = 0; s < 5; ++s) fetch(s, stage0 + k * kStageBytes);
-        there[k + 1] = there[k] && next_tile();
-        pos[k + 1] = there[k + 1] ? entry() : -1;
-        page = there[k + 1] ? lookup(pos[k + 1]) : 0;
-      }
-      bool ok = true;
+      bool ok = true, more = true;
       uint32_t q = 0;  // tiles of 128 dims widened
-      for (uint32_t visit = 0; ok && there[0]; ++visit) {
-        open(pos[S::stages], page);
-        const bool later = there[S::stages] && next_tile();
-        int later_pos = later ? entry() : -1;
-        const uint32_t stage_at = (visit % S::stages) * kStageBytes;
-        const uint8_t* rec = smem + S::off_stage + stage_at + (quarter * 32 + lane) * kPitch;
+      for (uint32_t visit = 0; ok && more; ++visit) {
+        const int stage = visit % S::stages;
+        const uint8_t* rec = smem + S::off_stage + stage * kStageBytes;
 #pragma unroll 1
         for (int s = 0; s < 5; ++s, ++q) {
-          const uint32_t at = S::tile_stays ? s : q % S::ring;
-          ok = wait_warp(&ctl.a_empty[at], (S::tile_stays ? visit : q / S::ring) ^ 1u);
+          const uint32_t at = q % S::ring;
+          ok = wait_warp(&ctl.rec_full[stage][s], visit / S::stages);
+          ok = ok && wait_warp(&ctl.a_empty[at], (q / S::ring) ^ 1u);
           if (!ok) break;
           tc::fence_after_sync();
-          // (five pieces a staged tile have been asked for since this one)
-          asm volatile("cp.async.wait_group %0;" :: "n"(5 * S::stages - 1) : "memory");
-          __syncwarp();
+          const uint8_t* mine = rec + piece_at(s) + row * (s ? 128 : kPiece0);
           if (s == 0) {
             uint32_t info[8];
             bool fine = true;
+            const uint4 four = *reinterpret_cast<const uint4*>(mine + 64);
+            info[0] = four.x;
+            info[1] = four.y;
+            info[2] = four.z;
+            info[3] = four.w;
+            info[4] = *reinterpret_cast<const uint32_t*>(mine + 80);
 #pragma unroll
-            for (int i = 0; i < 5; ++i) {
-              const float v = *reinterpret_cast<const float*>(rec + kKvScaleOff + 4 * i);
-              fine = fine && fabsf(v) * 448.0f < INFINITY;
-              info[i] = __float_as_uint(v);
-            }
+            for (int i = 0; i < 5; ++i) fine = fine && fabsf(__uint_as_float(info[i])) * 448.0f < INFINITY;
             if (!fine) info[0] = 0x7FC00000u;  // NaN: the position has no weight
-            info[5] = static_cast<uint32_t>(pos[0]);
+            info[5] = reinterpret_cast<const uint32_t*>(smem + S::off_slot)[(visit % (S::stages + 1)) * kTile + row];
             info[6] = info[7] = 0;
             tmem_st8(tmem + lanes + S::col_info + 8 * (visit % 3), info);
           }
-#pragma unroll 2
-          for (int j = 0; j < (s < 4 ? 4 : 2); ++j) {  // 32 codes, 16 columns
-            const uint4 lo = *reinterpret_cast<const uint4*>(rec + 128 * s + 32 * j);
-            const uint4 hi = *reinterpret_cast<const uint4*>(rec + 128 * s + 32 * j + 16);
+          const int turn = s ? (row & 7) << 4 : 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // 32 codes, 16 columns
+            if (s == 0 && j >= 2) break;
+            const uint4 lo = *reinterpret_cast<const uint4*>(mine + ((32 * j) ^ turn));
+            const uint4 hi = *reinterpret_cast<const uint4*>(mine + ((32 * j + 16) ^ turn));
             const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             uint32_t o[16];
 #pragma unroll
@@ -647,74 +654,74 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
             }
             tc::tmem_st16(tmem + lanes + S::col_a + 64 * at + 16 * j, o);
           }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&ctl.rec_empty[stage][s]);
           tc::tmem_wait_st();
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&ctl.a_full[at]);
-          fetch(s, stage0 + stage_at);
         }
-        page = later ? lookup(later_pos) : 0;
-#pragma unroll
-        for (int k = 0; k < S::stages; ++k) {
-          pos[k] = pos[k + 1];
-          there[k] = there[k + 1];
-        }
-        pos[S::stages] = later_pos;
-        there[S::stages] = later;
+        more = walk_next<N>(ws, pl.groups, w);
       }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   } else if (warp >= kWarpEpi0) {
     // ---- weights: a position a lane, S::width of a chunk's columns each four warps ----
     constexpr int W = S::width;
     const int quarter = warp & 3, part = (warp - kWarpEpi0) >> 2, row = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    uint32_t d = 0, n = 0, visit = 0;
+    uint32_t d = 0;
     if (walk_begin<N>(ws, ctl, w)) {
       bool ok = true, more = true;
-      float total = 0.f, lost = 0.f;
-      while (ok && more) {
+      for (uint32_t visit = 0; ok && more; ++visit) {
         const uint32_t tile_info = tmem + lanes + S::col_info + 8 * (visit % 3);
         uint64_t acc[W / 2];
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) acc[i] = 0ull;
-        int pos = -1;
+        int pos = -1, entry = 0;
+        if (SPARSE && part == 0 && w.tile * kTile + row < w.grp.x)
+          entry = a.idx[static_cast<int64_t>(w.g) * a.topk + w.tile * kTile + row];
 #pragma unroll 1
         for (int s = 0; s < 5; ++s, ++d) {
           const uint32_t at = d % S::accs;
           ok = wait_warp(&ctl.d_full[at], d / S::accs);
           if (!ok) break;
           tc::fence_after_sync();
-          const float scale = tmem_ld1(tile_info + s);
+          const float scale = tmem_ld1(tile_info + (s ? s - 1 : 4));
           if (s == 0) pos = __float_as_int(tmem_ld1(tile_info + 5));
-          uint32_t v[W];
-          if constexpr (W == 32) tc::tmem_ld32(tmem + lanes + at * N + part * W, v);
-          else tc::tmem_ld16(tmem + lanes + at * N + part * W, v);
-          tc::tmem_wait_ld();
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&ctl.d_free[at]);
-          const uint64_t both = pair(scale, scale);
 #pragma unroll
-          for (int i = 0; i < W / 2; ++i)
-            acc[i] = fma_pair(both, pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), acc[i]);
+          for (int h = 0; h < W / 16; ++h) {  // (16 columns at a time: 768 threads have 80 registers each)
+            uint32_t v[16];
+            tc::tmem_ld16(tmem + lanes + at * N + part * W + 16 * h, v);
+            tc::tmem_wait_ld();
+            if (h == W / 16 - 1) {
+              tc::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(&ctl.d_free[at]);
+            }
+            const uint64_t both = pair(scale, scale);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              acc[8 * h + i] = fma_pair(both, pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), acc[8 * h + i]);
+          }
         }
-        const int buf = n & 1;
-        ok = ok && wait_warp(&ctl.col_full[buf], n >> 1);
+        const int buf = visit & 1;
+        ok = ok && wait_warp(&ctl.col_full[buf], visit >> 1);
         if (!ok) break;
-        ++n;
+        // (the slot says whether there is a position; which one, its place or its entry)
+        const int place = w.tile * kTile + row;
+        if (pos >= 0) pos = SPARSE ? entry : place;
         const ulonglong2* cols = reinterpret_cast<const ulonglong2*>(smem + S::off_col) + (buf * N + part * W) / 2;
-        float sum = 0.f;
+        float total = 0.f;
         if (SPARSE || ctl.all_seen[buf]) {
           float odd = 0.f;
 #pragma unroll
           for (int i = 0; i < W / 2; ++i) {
             const ulonglong2 k = cols[i];
             const float2 x = unpair(fma_pair(acc[i], k.x, k.y));
-            sum += ex2(x.x);
+            total += ex2(x.x);
             odd += ex2(x.y);
           }
-          sum += odd;
+          total += odd;
         } else {
           const int2* limits = reinterpret_cast<const int2*>(smem + S::off_limit) + (buf * N + part * W) / 2;
 #pragma unroll
@@ -722,21 +729,13 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
             const ulonglong2 k = cols[i];
             const int2 lim = limits[i];
             const float2 x = unpair(fma_pair(acc[i], k.x, k.y));
-            sum += (pos < lim.x ? ex2(x.x) : 0.f) + (pos < lim.y ? ex2(x.y) : 0.f);
+            total += (pos < lim.x ? ex2(x.x) : 0.f) + (pos < lim.y ? ex2(x.y) : 0.f);
           }
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ctl.col_empty[buf]);
-        // (a tile may pass tens of thousands of chunks: what the total's rounding drops is kept.  Weights are not negative, and
-        // once their sum exceeds a chunk's it stays the larger one)
-        const float before = total;
-        total += sum;
-        if (S::tile_stays) lost += before >= sum ? sum - (total - before) : before - (total - sum);
         const Walk was = w;
         more = walk_next<N>(ws, pl.groups, w);
-        if (S::tile_stays && more && w.same_tile(was)) continue;
-        // the tile is done
-        if (S::tile_stays) total += lost == lost ? lost : 0.f;  // (infinite sums have none)
         bool gives = pos >= 0;
         if (SPARSE && S::parts > 1) {
           // an entry's weight is the sum of all parts': the first gathers it, by way of tensor memory.  (A buffer's sums have
@@ -770,8 +769,6 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, MassArgs a, MassPlan
                         static_cast<unsigned long long>(__float2ll_rn(fminf(total, kMassMost) * kMassOne)));
           }
         }
-        total = lost = 0.f;
-        ++visit;
       }
     }
   }
@@ -788,7 +785,7 @@ MassPlan make_plan(int n_q, int h_s, int n_seq, bool sparse) {
   p.groups = sparse ? n_q : n_seq;
   // a chunk's columns: all of a group of average rows where they fit
   const int64_t cols = static_cast<int64_t>(h_s) * (sparse ? 1 : std::max(1, (n_q + n_seq - 1) / n_seq));
-  p.n = cols <= 16 ? 16 : cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 96;
+  p.n = cols <= 16 ? 16 : cols <= 32 ? 32 : cols <= 64 ? 64 : 128;
   const size_t columns = static_cast<size_t>(n_q) * h_s;
   p.off_cols = round_up(columns * kLatent * 2, 256);
   p.off_groups = p.off_cols + round_up(columns * 16, 256);
@@ -811,12 +808,16 @@ EncodeFn encode_fn() {
   return fn;
 }
 
+struct MassMaps {
+  CUtensorMap q, piece0, piece;
+};
 template <bool SPARSE, int N>
-cudaError_t launch_main(const CUtensorMap& q_map, const MassArgs& a, const MassPlan& pl, const MassWs& ws, int grid, cudaStream_t s) {
+cudaError_t launch_main(const MassMaps& m, const MassArgs& a, const MassPlan& pl, const MassWs& ws, int grid, cudaStream_t s) {
   constexpr size_t smem = Shape<N>::off_ctl + sizeof(MassCtl);
   const cudaError_t e = cudaFuncSetAttribute(attn_mass_kernel<SPARSE, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_mass_kernel<SPARSE, N>, dim3(static_cast<unsigned>(grid)), dim3(Shape<N>::threads), smem, s, 1, q_map, a, pl, ws);
+  return launch_pdl(attn_mass_kernel<SPARSE, N>, dim3(static_cast<unsigned>(grid)), dim3(Shape<N>::threads), smem, s, 1, m.q,
+                    m.piece0, m.piece, a, pl, ws);
 }
 
 }  // namespace
@@ -837,13 +838,21 @@ cudaError_t launch_attn_mass(const MassArgs& a, cudaStream_t s, const char** err
     *err = "attn_mass: cuTensorMapEncodeTiled is not available";
     return cudaErrorNotSupported;
   }
-  // rows of 576 fp16 in boxes of 64 dims x n columns, 128-byte swizzle; rows past the end read as zero
-  CUtensorMap q_map;
-  const cuuint64_t columns = static_cast<cuuint64_t>(a.n_q) * a.h_s;
-  const cuuint64_t dims[3] = {kLatent, columns, 1}, strides[2] = {kLatent * 2, kLatent * 2 * columns};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(pl.n), 1}, one[3] = {1, 1, 1};
-  if (enc(&q_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, ws.q, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+  // a 2-d array of rows, boxes of `box_x` x `box_rows` elements; rows past the end read as zero
+  auto map = [&](CUtensorMap* m, CUtensorMapDataType type, const void* at, uint64_t width, uint64_t pitch, uint64_t rows, int box_x,
+                 int box_rows, CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[3] = {width, rows, 1}, strides[2] = {pitch, pitch * rows};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
+    return enc(m, type, 3, const_cast<void*>(at), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  MassMaps maps{};
+  const uint64_t columns = static_cast<uint64_t>(a.n_q) * a.h_s, slots = static_cast<uint64_t>(a.num_pages) * kPage;
+  if (!map(&maps.q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws.q, kLatent, kLatent * 2, columns, 64, pl.n, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      (!sparse && !map(&maps.piece0, CU_TENSOR_MAP_DATA_TYPE_INT32, a.kv_cache, kKvTokBytes / 4, kKvTokBytes, slots, kPiece0 / 4, kPage,
+           CU_TENSOR_MAP_SWIZZLE_NONE)) ||
+      (!sparse && !map(&maps.piece, CU_TENSOR_MAP_DATA_TYPE_INT32, a.kv_cache, kKvTokBytes / 4, kKvTokBytes, slots, 32, kPage,
+           CU_TENSOR_MAP_SWIZZLE_128B))) {
     *err = "attn_mass: tensor map encoding failed";
     return cudaErrorInvalidValue;
   }
@@ -861,11 +870,10 @@ cudaError_t launch_attn_mass(const MassArgs& a, cudaStream_t s, const char** err
   const int64_t units = tiles * (sparse ? a.n_q : static_cast<int64_t>(a.n_seq) * ((rows * a.h_s + pl.n - 1) / pl.n));
   const int grid = static_cast<int>(std::min<int64_t>(multiprocessors(), units));
   switch (pl.n) {
-    case 16: return sparse ? launch_main<true, 16>(q_map, a, pl, ws, grid, s) : launch_main<false, 16>(q_map, a, pl, ws, grid, s);
-    case 32: return sparse ? launch_main<true, 32>(q_map, a, pl, ws, grid, s) : launch_main<false, 32>(q_map, a, pl, ws, grid, s);
-    case 64: return sparse ? launch_main<true, 64>(q_map, a, pl, ws, grid, s) : launch_main<false, 64>(q_map, a, pl, ws, grid, s);
-    case 128: return sparse ? launch_main<true, 128>(q_map, a, pl, ws, grid, s) : launch_main<false, 128>(q_map, a, pl, ws, grid, s);
-    default: return launch_main<false, 96>(q_map, a, pl, ws, grid, s);  // (a row alone has 128 columns at most)
+    case 16: return sparse ? launch_main<true, 16>(maps, a, pl, ws, grid, s) : launch_main<false, 16>(maps, a, pl, ws, grid, s);
+    case 32: return sparse ? launch_main<true, 32>(maps, a, pl, ws, grid, s) : launch_main<false, 32>(maps, a, pl, ws, grid, s);
+    case 64: return sparse ? launch_main<true, 64>(maps, a, pl, ws, grid, s) : launch_main<false, 64>(maps, a, pl, ws, grid, s);
+    default: return sparse ? launch_main<true, 128>(maps, a, pl, ws, grid, s) : launch_main<false, 128>(maps, a, pl, ws, grid, s);
   }
 }
 
