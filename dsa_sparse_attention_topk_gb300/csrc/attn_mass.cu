@@ -200,6 +200,7 @@ struct MassCtl {
   uint64_t d_full[kMostAccs], d_free[kMostAccs];
   uint64_t part_full[2];
   uint64_t col_full[2], col_empty[2];
+  uint64_t slot_full[3], slot_empty[3];                     // sparse: a tile's slots
   uint64_t drained[2];
   int all_seen[2];                      // every column of the chunk sees the whole tile
   long long scan[24];
@@ -342,9 +343,13 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
     }
     for (int i = 0; i < S::stages; ++i)
       for (int k = 0; k < 5; ++k) {
-        tc::mbar_init(&ctl.rec_full[i][k], SPARSE ? 33 : 1);  // (the copies of 32 lanes, and what the warp wrote itself)
+        tc::mbar_init(&ctl.rec_full[i][k], SPARSE ? 128 * S::parts : 1);
         tc::mbar_init(&ctl.rec_empty[i][k], 4);
       }
+    for (int i = 0; i < S::stages + 1; ++i) {
+      tc::mbar_init(&ctl.slot_full[i], 1);
+      tc::mbar_init(&ctl.slot_empty[i], 4 + 4 * S::parts);
+    }
     for (int i = 0; i < S::accs; ++i) {
       tc::mbar_init(&ctl.d_full[i], 1);
       tc::mbar_init(&ctl.d_free[i], 4 * S::parts);
@@ -522,9 +527,8 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       tc::mbar_drain(&ctl.drained[mine], 0, 100000000ull);
     }
   } else if (warp == kWarpRec) {
-    // ---- records, a piece of a tile at a time: of whole pages by TMA, entries by eight lanes 128 bytes of one.  (A bulk
-    // copy a record, issued by 32 lanes, took 2500 cycles for 32 records in issue alone.)  Entry and page of the
-    // tile behind are looked up meanwhile. ----
+    // ---- where a tile's records lie, and those of whole pages by TMA, a piece at a time.  Entry and page of the tile
+    // behind are looked up meanwhile. ----
     if (walk_begin<N>(ws, ctl, w)) {
       const int64_t table_end = static_cast<int64_t>(a.max_pages) * kPage;
       int pos[4], page[4];  // of positions 32 k + lane of a tile, -1: none
@@ -550,59 +554,52 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       lookup();
       bool ok = true, more = true;
       for (uint32_t t = 0; ok && more; ++t) {
-        int* s_slot = reinterpret_cast<int*>(smem + S::off_slot) + (t % (S::stages + 1)) * kTile;
+        const int buf = t % (S::stages + 1);
+        int* s_slot = reinterpret_cast<int*>(smem + S::off_slot) + buf * kTile;
+        if (SPARSE) {
+          ok = wait_warp(&ctl.slot_empty[buf], (t / (S::stages + 1)) ^ 1u);
+          if (!ok) break;
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (pos[k] >= 0 && (page[k] < 0 || page[k] >= a.num_pages)) {
             flag(a.status, DSA_STATUS_BAD_PAGE);
             pos[k] = -1;
           }
-          // (read by the warps that widen before the tile's first piece is given back)
+          // (dense: read by the warps that widen before the tile's first piece is given back)
           s_slot[32 * k + lane] = pos[k] >= 0 ? page[k] * kPage + (pos[k] & (kPage - 1)) : -1;
         }
         __syncwarp();
-        const int first_page = s_slot[0], second_page = s_slot[64];  // dense: the tile's two pages, if they are there
         more = walk_next<N>(ws, pl.groups, w);
-        if (more) entry();
-        const int stage = t % S::stages;
-        uint8_t* to = smem + S::off_stage + stage * kStageBytes;
-#pragma unroll 1
-        for (int s = 0; s < 5; ++s) {
-          ok = wait_warp(&ctl.rec_empty[stage][s], (t / S::stages) ^ 1u);
-          if (!ok) break;
-          uint64_t* bar = &ctl.rec_full[stage][s];
-          if constexpr (SPARSE) {
-            const int piece = lane & 7, width = s ? 128 : kPiece0;
-            const uint8_t* cache = a.kv_cache + dim0(s) + 16 * piece;
-            const uint32_t to32 = smem_u32(to) + piece_at(s) + (lane >> 3) * width;
-            const int least = s || piece < kPiece0 / 16 ? 0 : INT32_MAX;
-#pragma unroll 1
-            for (int i0 = 0; i0 < 32; i0 += 8) {
-              int slot[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) slot[i] = s_slot[4 * (i0 + i) + (lane >> 3)];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint32_t at = s ? (piece ^ ((4 * i + (lane >> 3)) & 7)) << 4 : piece << 4;
-                copy16_if(slot[i] >= least, to32 + 4 * (i0 + i) * width + at, cache + static_cast<int64_t>(slot[i]) * kKvTokBytes);
-              }
-            }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar);
-          } else if (lane == 0) {
-            // (what lies behind the sequence in its last page comes with it and is not looked at)
-            const int bytes = (s ? 128 : kPiece0) * kPage;
-            tc::mbar_arrive_expect_tx(bar, ((first_page >= 0) + (second_page >= 0)) * bytes);
-            const CUtensorMap* map = s ? &piece_map : &piece0_map;
-            if (first_page >= 0) tc::tma_load_3d(to + piece_at(s), map, dim0(s) / 4, first_page, 0, bar);
-            if (second_page >= 0) tc::tma_load_3d(to + piece_at(s) + bytes, map, dim0(s) / 4, second_page, 0, bar);
+        if constexpr (SPARSE) {
+          if (lane == 0) tc::mbar_arrive(&ctl.slot_full[buf]);
+          if (more) {
+            entry();
+            lookup();
           }
-          if (s == 0 && more) lookup();
+        } else {
+          const int first_page = s_slot[0], second_page = s_slot[64];  // the tile's two pages, if they are there
+          if (more) entry();
+          const int stage = t % S::stages;
+          uint8_t* to = smem + S::off_stage + stage * kStageBytes;
+#pragma unroll 1
+          for (int s = 0; s < 5; ++s) {
+            ok = wait_warp(&ctl.rec_empty[stage][s], (t / S::stages) ^ 1u);
+            if (!ok) break;
+            if (lane == 0) {
+              // (what lies behind the sequence in its last page comes with it and is not looked at)
+              uint64_t* bar = &ctl.rec_full[stage][s];
+              const int bytes = (s ? 128 : kPiece0) * kPage;
+              tc::mbar_arrive_expect_tx(bar, ((first_page >= 0) + (second_page >= 0)) * bytes);
+              const CUtensorMap* map = s ? &piece_map : &piece0_map;
+              if (first_page >= 0) tc::tma_load_3d(to + piece_at(s), map, dim0(s) / 4, first_page, 0, bar);
+              if (second_page >= 0) tc::tma_load_3d(to + piece_at(s) + bytes, map, dim0(s) / 4, second_page, 0, bar);
+            }
+            if (s == 0 && more) lookup();
+          }
         }
       }
-      if (SPARSE) asm volatile("cp.async.wait_all;" ::: "memory");
-      else if (*abort) __nanosleep(1000000);  // copies in flight must land before the CTA ends
+      if (!SPARSE && *abort) __nanosleep(1000000);  // copies in flight must land before the CTA ends
     }
   } else if (warp >= kWarpConv0 && warp < kWarpEpi0) {
     // ---- codes widened to fp16 into tensor memory, a position a lane ----
@@ -634,7 +631,13 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
 #pragma unroll
             for (int i = 0; i < 5; ++i) fine = fine && fabsf(__uint_as_float(info[i])) * 448.0f < INFINITY;
             if (!fine) info[0] = 0x7FC00000u;  // NaN: the position has no weight
-            info[5] = reinterpret_cast<const uint32_t*>(smem + S::off_slot)[(visit % (S::stages + 1)) * kTile + row];
+            const int buf = visit % (S::stages + 1);
+            if (SPARSE) ok = wait_warp(&ctl.slot_full[buf], visit / (S::stages + 1));
+            info[5] = reinterpret_cast<const uint32_t*>(smem + S::off_slot)[buf * kTile + row];
+            if (SPARSE) {
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(&ctl.slot_empty[buf]);
+            }
             info[6] = info[7] = 0;
             tmem_st8(tmem + lanes + S::col_info + 8 * (visit % 3), info);
           }
@@ -655,7 +658,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             tc::tmem_st16(tmem + lanes + S::col_a + 64 * at + 16 * j, o);
           }
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&ctl.rec_empty[stage][s]);
+          if (!SPARSE && lane == 0) tc::mbar_arrive(&ctl.rec_empty[stage][s]);
           tc::tmem_wait_st();
           tc::fence_before_sync();
           __syncwarp();
@@ -670,9 +673,40 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
     const int quarter = warp & 3, part = (warp - kWarpEpi0) >> 2, row = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     uint32_t d = 0;
+    // Sparse: these warps also fetch the records, entries wherever they lie, eight lanes 128 bytes of one: a piece of the
+    // tile S::stages behind, once the products of this tile's are done, for which it was widened.  (One warp alone took
+    // 7000 cycles to ask for a tile, the four that widen 2200 besides their own work; a bulk copy a record 10000.)
+    auto fetch = [&](int s, uint32_t tile) {
+      const int* s_slot = reinterpret_cast<const int*>(smem + S::off_slot) + (tile % (S::stages + 1)) * kTile;
+      constexpr int kWarps = 4 * S::parts, kEach = 32 / kWarps;
+      const int chunk = lane & 7, width = s ? 128 : kPiece0, least = s || chunk < kPiece0 / 16 ? 0 : INT32_MAX;
+      const uint32_t stage = smem_u32(smem + S::off_stage + (tile % S::stages) * kStageBytes + piece_at(s));
+      const uint8_t* from = a.kv_cache + dim0(s) + 16 * chunk;
+      int slot[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) slot[i] = s_slot[(i * kWarps + warp - kWarpEpi0) * 4 + (lane >> 3)];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int r = (i * kWarps + warp - kWarpEpi0) * 4 + (lane >> 3);
+        copy16_if(slot[i] >= least, stage + r * width + ((s ? chunk ^ (r & 7) : chunk) << 4),
+                  from + static_cast<int64_t>(slot[i]) * kKvTokBytes);
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(&ctl.rec_full[tile % S::stages][s])) : "memory");
+    };
     if (walk_begin<N>(ws, ctl, w)) {
       bool ok = true, more = true;
+      if (SPARSE)
+        for (uint32_t t = 0; ok && t < S::stages && static_cast<int>(t) < w.left; ++t) {
+          ok = wait_warp(&ctl.slot_full[t], 0);
+          if (!ok) break;
+#pragma unroll 1
+          for (int s = 0; s < 5; ++s) fetch(s, t);
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&ctl.slot_empty[t]);
+        }
       for (uint32_t visit = 0; ok && more; ++visit) {
+        const uint32_t behind = visit + S::stages;  // the tile to fetch, if it is there
+        const bool fetches = SPARSE && w.left > S::stages;
         const uint32_t tile_info = tmem + lanes + S::col_info + 8 * (visit % 3);
         uint64_t acc[W / 2];
 #pragma unroll
@@ -703,6 +737,15 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             for (int i = 0; i < 8; ++i)
               acc[8 * h + i] = fma_pair(both, pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), acc[8 * h + i]);
           }
+          if (fetches) {
+            if (s == 0) ok = wait_warp(&ctl.slot_full[behind % (S::stages + 1)], behind / (S::stages + 1));
+            if (!ok) break;
+            fetch(s, behind);
+          }
+        }
+        if (fetches) {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&ctl.slot_empty[behind % (S::stages + 1)]);
         }
         const int buf = visit & 1;
         ok = ok && wait_warp(&ctl.col_full[buf], visit >> 1);
@@ -770,6 +813,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           }
         }
       }
+      if (SPARSE) asm volatile("cp.async.wait_all;" ::: "memory");
     }
   }
   tc::fence_before_sync();
