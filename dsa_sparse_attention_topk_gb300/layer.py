@@ -5,8 +5,9 @@ computation is a call into the C ABI.
 
 import torch
 
-from . import (V_DIM, alloc_k_cache, alloc_kv_cache, quant_kv_mxfp8, quant_kv_fp8, decode_step, indexer_topk,
-               prefix_attn, rope, rope_quant_kv, sparse_attn, sparse_attn_workspace_size)
+from . import (V_DIM, alloc_k_cache, alloc_kv_cache, attn_mass, attn_mass_workspace_size, quant_kv_mxfp8, quant_kv_fp8,
+               decode_step, evict_compact, evict_select, indexer_topk, norm_rope, norm_rope_quant_kv, prefix_attn, rope,
+               rope_quant_kv, sparse_attn, sparse_attn_mass, sparse_attn_workspace_size)
 
 
 class DsaDecodeLayer:
@@ -19,13 +20,31 @@ class DsaDecodeLayer:
           (turns, amplitude), as rope_turns(64) returns them: they come without, and every call turns them:
           the 64 dims from index_offset of indexer queries and keys in index_layout, the last
           64 of attention queries and latent rows in latent_layout.
+    norm  with rope: the norms of norm_rope_quant_kv that indexer keys and latent rows get before they are turned, a dict
+          of its k_weight, k_bias, kv_weight, k_norm and eps, each as there if left out.  None: they come normed.
+    index_norm  with rope: the norm of norm_rope that the heads of indexer queries get before they are turned, a dict of its
+          weight, bias, norm, norm_dim and eps.  None: they come normed.
+
+    What the cache's positions are worth to the attention can be added up (``mass`` of decode, step and attend_prefix,
+    int64 [n_seq, max_ctx], zero at first) and the least used ones given up (``evict``).  The records that
+    stay move to the first positions of their sequence and keep the turns they have: from then on rope_pos, the
+    positions to turn to, differ from q_pos, the places in the cache.
     """
 
     def __init__(self, num_pages, h_i, h_s, topk, sm_scale, device="cuda", rope=None, index_offset=0,
-                 index_layout="half", latent_layout="interleaved"):
+                 index_layout="half", latent_layout="interleaved", norm=None, index_norm=None):
         self.device = torch.device(device)
         self.rope, self.index_offset = rope, index_offset
         self.index_layout, self.latent_layout = index_layout, latent_layout
+        for name, given, known in (("norm", norm, ("k_weight", "k_bias", "kv_weight", "k_norm", "eps")),
+                                   ("index_norm", index_norm, ("weight", "bias", "norm", "norm_dim", "eps"))):
+            if given is None:
+                continue
+            if rope is None:
+                raise ValueError(f"DsaDecodeLayer: {name} goes with rope")
+            if set(given) - set(known):
+                raise ValueError(f"DsaDecodeLayer: {name} knows {', '.join(known)}")
+        self.norm, self.index_norm = norm, index_norm
         self.num_pages = int(num_pages)
         self.h_i, self.h_s, self.topk, self.sm_scale = h_i, h_s, topk, float(sm_scale)
         self.k_cache = alloc_k_cache(num_pages, self.device)
@@ -43,11 +62,19 @@ class DsaDecodeLayer:
         if pos is None:
             raise ValueError("write: a layer with rope needs the tokens' positions")
         turns, amplitude = self.rope
+        if self.norm is not None:
+            norm_rope_quant_kv(k, kv, pos, slot_mapping, self.k_cache, self.kv_cache, turns, amplitude=amplitude,
+                               k_offset=self.index_offset, k_layout=self.index_layout, kv_layout=self.latent_layout,
+                               **self.norm)
+            return
         rope_quant_kv(k, kv, pos, slot_mapping, self.k_cache, self.kv_cache, turns, amplitude=amplitude,
                       k_offset=self.index_offset, k_layout=self.index_layout, kv_layout=self.latent_layout)
 
     def _turn_index(self, q, pos, out=None):
         turns, amplitude = self.rope
+        if self.index_norm is not None:
+            return norm_rope(q, pos, turns, offset=self.index_offset, layout=self.index_layout, amplitude=amplitude, out=out,
+                             **self.index_norm)
         return rope(q, pos, turns, offset=self.index_offset, layout=self.index_layout, amplitude=amplitude, out=out)
 
     def _turn_latent(self, q, pos, out=None):
@@ -71,33 +98,69 @@ class DsaDecodeLayer:
             self._bufs[n_q] = b
         return b
 
-    def decode(self, q_idx, w, q_sfa, page_table, seq_lens, q_seq, q_pos, max_ctx, q_group=1):
+    def _mass_ws(self, n_q, n_seq):
+        ws = self._ws.get((n_q, n_seq))
+        if ws is None:
+            ws = torch.empty(attn_mass_workspace_size(n_q, self.h_s, n_seq), dtype=torch.uint8, device=self.device)
+            self._ws[n_q, n_seq] = ws
+        return ws
+
+    def _weigh(self, mass, q_sfa, page_table, seq_lens, q_seq, b):
+        """Add the weights of the entries that a step selected."""
+        if "weights" not in b:
+            b["weights"] = torch.empty(b["idx"].shape, dtype=torch.float32, device=self.device)
+        sparse_attn_mass(q_sfa, self.kv_cache, page_table, seq_lens, q_seq, b["idx"], b["lse"], self.sm_scale, mass=mass,
+                         out=b["weights"], workspace=self._mass_ws(q_sfa.shape[0], seq_lens.shape[0]))
+
+    def decode(self, q_idx, w, q_sfa, page_table, seq_lens, q_seq, q_pos, max_ctx, q_group=1, rope_pos=None, mass=None):
         """Indexer + Top-K + SFA for n_q query rows.  Returns (out bf16 [n_q, h_s, 512],
         lse fp32 [n_q, h_s], idx int32 [n_q, topk]); the tensors are reused by the next
-        call with the same n_q."""
+        call with the same n_q.  rope_pos (int32 [n_q]) are the positions that queries are turned to, q_pos if left
+        out; to mass the weights of the selected positions are added."""
         n_q = q_idx.shape[0]
         b = self._buffers(n_q)
         if self.rope is not None:
-            q_idx = self._turn_index(q_idx, q_pos, b["q_idx"])
-            q_sfa = self._turn_latent(q_sfa, q_pos, b["q_sfa"])
+            rope_pos = q_pos if rope_pos is None else rope_pos
+            q_idx = self._turn_index(q_idx, rope_pos, b["q_idx"])
+            q_sfa = self._turn_latent(q_sfa, rope_pos, b["q_sfa"])
         indexer_topk(q_idx, w, self.k_cache, page_table, seq_lens, q_seq, q_pos, self.topk, max_ctx,
                      q_group=q_group, out_idx=b["idx"])
         sparse_attn(q_sfa, self.kv_cache, page_table, seq_lens, q_seq, b["idx"], self.sm_scale,
                     out=b["out"], out_lse=b["lse"], workspace=b["ws"])
+        if mass is not None:
+            self._weigh(mass, q_sfa, page_table, seq_lens, q_seq, b)
         return b["out"], b["lse"], b["idx"]
 
-    def attend_prefix(self, q_sfa, prefix_pages, prefix_len, page_table, seq_lens, q_seq, q_pos, max_ctx):
+    def attend_prefix(self, q_sfa, prefix_pages, prefix_len, page_table, seq_lens, q_seq, q_pos, max_ctx, rope_pos=None,
+                      mass=None):
         """Dense attention of n_q query rows whose sequences share their first prefix_len
         positions (prefix_pages, read once for all rows), each row then over its own ones up to
-        q_pos.  Returns (out bf16 [n_q, h_s, 512], lse fp32 [n_q, h_s]), new tensors each call."""
+        q_pos.  Returns (out bf16 [n_q, h_s, 512], lse fp32 [n_q, h_s]), new tensors each call.  rope_pos as for decode;
+        to mass the weights of every position seen are added, for which page_table names the shared pages too."""
         if self.rope is not None:
-            q_sfa = self._turn_latent(q_sfa, q_pos)
+            q_sfa = self._turn_latent(q_sfa, q_pos if rope_pos is None else rope_pos)
         lse = torch.empty(q_sfa.shape[0], self.h_s, dtype=torch.float32, device=self.device)
-        return prefix_attn(q_sfa, self.kv_cache, prefix_pages, prefix_len, page_table, seq_lens, q_seq, q_pos, max_ctx,
-                           self.sm_scale, out_lse=lse)
+        out = prefix_attn(q_sfa, self.kv_cache, prefix_pages, prefix_len, page_table, seq_lens, q_seq, q_pos, max_ctx,
+                          self.sm_scale, out_lse=lse)
+        if mass is not None:
+            attn_mass(q_sfa, self.kv_cache, page_table, seq_lens, q_seq, q_pos, lse, max_ctx, self.sm_scale, mass=mass,
+                      workspace=self._mass_ws(q_sfa.shape[0], seq_lens.shape[0]))
+        return out
+
+    def evict(self, mass, page_table, seq_lens, budget, sinks=0, recent=0, dst_table=None):
+        """Keep budget positions of each sequence: the first sinks, the last recent and those of the largest mass between
+        (evict_select); move their records to the sequence's first positions, in place or to the pages of dst_table
+        (evict_compact), and their mass with them; the rest of mass becomes 0.  Returns (kept int32 [n_seq, budget]: the
+        positions that stayed, -1 behind the last; new_lens int32 [n_seq]).  Pages behind the new lengths are free."""
+        kept, new_lens, kept_mass = evict_select(mass, seq_lens, budget, sinks=sinks, recent=recent)
+        evict_compact(kept, page_table, self.k_cache, self.kv_cache, dst_table)
+        n = min(budget, mass.shape[1])  # (what would lie further is empty)
+        mass[:, :n].copy_(kept_mass[:, :n])
+        mass[:, n:].zero_()
+        return kept, new_lens
 
     def step(self, k_new, kv_new, slots_new, q_idx, w, q_sfa, page_table, seq_lens, q_seq, q_pos,
-             max_ctx, q_group=1, pos_new=None):
+             max_ctx, q_group=1, pos_new=None, rope_pos=None, mass=None):
         """Write this step's tokens into both caches, then decode: one library call
         (dsa_decode_step).  With one new token per query row the indexer kernel writes the
         tokens itself, each before it loads the page that holds it, and SFA follows it on
@@ -106,23 +169,26 @@ class DsaDecodeLayer:
 
         With rope the new tokens are turned and written by one kernel, the queries turned by
         two more, before that call.  pos_new (int32) are the new tokens' positions; left out,
-        token i is query row i's own and has its position.
+        token i is query row i's own and is turned with it.  rope_pos and mass as for decode.
         """
         n_q = q_idx.shape[0]
         b = self._buffers(n_q)
         if self.rope is not None:
+            rope_pos = q_pos if rope_pos is None else rope_pos
             if pos_new is None:
                 if k_new.shape[0] != n_q:
                     raise ValueError("step: pos_new is needed unless there is one new token per query row")
-                pos_new = q_pos
+                pos_new = rope_pos
             self.write(k_new, kv_new, slots_new, pos_new)
-            q_idx = self._turn_index(q_idx, q_pos, b["q_idx"])
-            q_sfa = self._turn_latent(q_sfa, q_pos, b["q_sfa"])
+            q_idx = self._turn_index(q_idx, rope_pos, b["q_idx"])
+            q_sfa = self._turn_latent(q_sfa, rope_pos, b["q_sfa"])
             k_new, kv_new, slots_new = k_new[:0], kv_new[:0], slots_new[:0]
         decode_step(k_new, kv_new, slots_new, self.k_cache, self.kv_cache, q_idx, w, q_sfa, page_table,
                     seq_lens, q_seq, q_pos, self.topk, max_ctx, self.sm_scale, q_group=q_group,
                     out_idx=b["idx"], out=b["out"], out_lse=b["lse"], workspace=b["ws"],
                     stream=torch.cuda.current_stream(self.device))
+        if mass is not None:
+            self._weigh(mass, q_sfa, page_table, seq_lens, q_seq, b)
         return b["out"], b["lse"], b["idx"]
 
     def capture_step(self, inputs, max_ctx, q_group=1, stage=None, result=None):
@@ -130,8 +196,9 @@ class DsaDecodeLayer:
         and return a function that replays it on the current stream.
 
         inputs  dict with the ``step`` arguments k_new, kv_new, slots_new, q_idx, w, q_sfa,
-                page_table, seq_lens, q_seq, q_pos (and pos_new where step needs it): device
-                tensors that stay in place; a replay reads whatever they hold then.
+                page_table, seq_lens, q_seq, q_pos (and pos_new where step needs it, rope_pos,
+                mass): device tensors that stay in place; a replay reads whatever they hold
+                then and adds to mass.  Recording itself runs the step once, without mass.
         stage   optional (pinned host tensor, device tensor) pair copied host -> device at
                 the start of every replay (the step's inputs staged in one buffer).
         result  optional pinned host tensor [n_q, h_s, 512] bf16 that receives the output at
@@ -144,7 +211,7 @@ class DsaDecodeLayer:
         """
         keys = ("k_new", "kv_new", "slots_new", "q_idx", "w", "q_sfa", "page_table", "seq_lens", "q_seq", "q_pos")
         args = [inputs[k] for k in keys]
-        pos_new = inputs.get("pos_new")
+        pos_new, rope_pos, mass = (inputs.get(k) for k in ("pos_new", "rope_pos", "mass"))
         # one eager step first: per-device queries, kernel attributes and the output buffers
         # are set up outside the capture
         side = torch.cuda.Stream(self.device)
@@ -152,14 +219,14 @@ class DsaDecodeLayer:
         with torch.cuda.stream(side):
             if stage is not None:
                 stage[1].copy_(stage[0], non_blocking=True)
-            self.step(*args, max_ctx, q_group, pos_new)
+            self.step(*args, max_ctx, q_group, pos_new, rope_pos, None if mass is None else torch.zeros_like(mass))
         torch.cuda.current_stream(self.device).wait_stream(side)
         graph = torch.cuda.CUDAGraph()
         # (relaxed: the library's host-side queries during the capture are not stream work)
         with torch.cuda.graph(graph, capture_error_mode="relaxed"):
             if stage is not None:
                 stage[1].copy_(stage[0], non_blocking=True)
-            out, lse, idx = self.step(*args, max_ctx, q_group, pos_new)
+            out, lse, idx = self.step(*args, max_ctx, q_group, pos_new, rope_pos, mass)
             if result is not None:
                 result.copy_(out, non_blocking=True)
 
