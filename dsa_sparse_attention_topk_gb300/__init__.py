@@ -176,6 +176,13 @@ def _tangents():
     return getattr(forward_ad, "_current_level", -1) >= 0
 
 
+def _any_requires_grad(*tensors):
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return True
+    return False
+
+
 def _need_no_grad(what, hint, *tensors):
     """Refuse a tensor whose gradient (or tangent) is asked for: the result would come back without.
     (Called where one may be: a small call is bound by this host code.)"""
@@ -366,17 +373,22 @@ def _norm_args(what, x, pos, turns, weight, bias, norm_dim):
     shape = x.shape
     if len(shape) not in (2, 3) or x.dtype not in _DTYPES:
         raise ValueError(f"{what}: x must be [n, d] or [n, h, d] of bf16, fp16 or fp32")
-    _need_shaped(pos, torch.int32, shape[:1], f"{what}: pos")
-    _need_shaped(turns, torch.int64, turns.shape[:1], f"{what}: turns")
+    if pos.dtype != torch.int32 or pos.shape != shape[:1] or not pos.is_contiguous():
+        _need_shaped(pos, torch.int32, shape[:1], f"{what}: pos")
+    if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+        _need_shaped(turns, torch.int64, turns.shape[:1], f"{what}: turns")
     span = shape[-1] if norm_dim is None else norm_dim
     first = weight if weight is not None else bias
-    for t, name in ((weight, "weight"), (bias, "bias")):
+    if first is None:
+        return span, 2
+    for t in (weight, bias):
         if t is None:
             continue
         if t.dtype not in _DTYPES or t.dtype != first.dtype:
             raise ValueError(f"{what}: weight and bias must be bf16, fp16 or fp32, both the same")
-        _need_shaped(t, t.dtype, (span,), f"{what}: {name}")
-    return span, 2 if first is None else _DTYPES[first.dtype]
+        if t.shape != (span,) or not t.is_contiguous():
+            _need_shaped(t, t.dtype, (span,), f"{what}: {'weight' if t is weight else 'bias'}")
+    return span, _DTYPES[first.dtype]
 
 
 def _row_strides(what, t, name, shape):
@@ -395,7 +407,7 @@ def norm_rope(x, pos, turns, weight=None, bias=None, norm="rms", norm_dim=None, 
     of at most 1024 dims); weight, bias: [norm_dim] of bf16, fp16 or fp32, or None (1, 0).  out=x works in
     place; otherwise out must not overlap x.  Tensors that need a gradient are refused: call it under
     torch.no_grad(), or in an autograd function whose backward is norm_rope_grad.  Returns out."""
-    if _tangents() or torch.is_grad_enabled():
+    if x.requires_grad or _tangents() or _any_requires_grad(weight, bias, out):
         _need_no_grad("norm_rope", "norm_rope_grad gives it", x, weight, bias, out)
     span, w_code = _norm_args("norm_rope", x, pos, turns, weight, bias, norm_dim)
     shape = x.shape
@@ -423,7 +435,7 @@ def norm_rope_grad(dy, x, pos, turns, weight=None, bias=None, norm="rms", norm_d
     (dx with x's shape and dtype, dweight fp32 [norm_dim] or None, dbias fp32 [norm_dim] or None), the last two
     where weight and bias are given.  dx may be dy or x (in place), and otherwise must not overlap them.
     Equal inputs give equal bits.  There is no second derivative: tensors that need a gradient are refused."""
-    if _tangents() or torch.is_grad_enabled():
+    if x.requires_grad or _tangents() or _any_requires_grad(dy, weight, bias, dx):
         _need_no_grad("norm_rope_grad", "there is no second derivative", dy, x, weight, bias, dx)
     span, w_code = _norm_args("norm_rope_grad", x, pos, turns, weight, bias, norm_dim)
     shape = x.shape
@@ -472,9 +484,12 @@ def _writer_args(what, k, kv, pos, slot_mapping, k_cache, kv_cache, turns, *othe
             raise ValueError(f"{name}_cache must be a contiguous uint8 tensor")
         pages = min(pages, cache.numel() // page_bytes)
     dev = _same_device(what, first, k, kv, pos, slot_mapping, k_cache, kv_cache, turns, *others)
-    _need_shaped(pos, torch.int32, rows, f"{what}: pos")
-    _need_shaped(slot_mapping, torch.int64, rows, f"{what}: slot_mapping")
-    _need_shaped(turns, torch.int64, (32,), f"{what}: turns")
+    if pos.dtype != torch.int32 or pos.shape != rows or not pos.is_contiguous():
+        _need_shaped(pos, torch.int32, rows, f"{what}: pos")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != rows or not slot_mapping.is_contiguous():
+        _need_shaped(slot_mapping, torch.int64, rows, f"{what}: slot_mapping")
+    if turns.dtype != torch.int64 or turns.shape != (32,) or not turns.is_contiguous():
+        _need_shaped(turns, torch.int64, (32,), f"{what}: turns")
     return dev, rows[0], pages
 
 
@@ -500,12 +515,12 @@ def norm_rope_quant_kv(k, kv, pos, slot_mapping, k_cache, kv_cache, turns, k_wei
     """rope_quant_kv with a norm before the rotation: k over its 128 dims (k_norm "rms" or "layer"; k_weight, k_bias
     fp32 [128] or None), kv over its first 512 (rms; kv_weight fp32 [512] or None).  The others as for rope_quant_kv;
     tensors that need a gradient are refused."""
-    if _tangents() or torch.is_grad_enabled():
+    if _tangents() or _any_requires_grad(k, kv, k_weight, k_bias, kv_weight):
         _need_no_grad("norm_rope_quant_kv", "codes have none", k, kv, k_weight, k_bias, kv_weight)
     dev, n, pages = _writer_args("norm_rope_quant_kv", k, kv, pos, slot_mapping, k_cache, kv_cache, turns, k_weight, k_bias,
                                  kv_weight)
     for t, width, name in ((k_weight, INDEX_DIM, "k_weight"), (k_bias, INDEX_DIM, "k_bias"), (kv_weight, V_DIM, "kv_weight")):
-        if t is not None:
+        if t is not None and (t.dtype != torch.float32 or t.shape != (width,) or not t.is_contiguous()):
             _need_shaped(t, torch.float32, (width,), f"norm_rope_quant_kv: {name}")
     p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     _call_on(dev, stream, lib().dsa_norm_rope_quant_kv, p(k), 0 if k is None else k.stride(0), p(k_weight), p(k_bias),
@@ -693,12 +708,12 @@ def _mass_args(what, q, kv_cache, page_table, seq_lens, q_seq, lse, mass, worksp
     n_q, h_s, _ = q.shape
     n_seq = seq_lens.shape[0]
     dev = _same_device(what, q, kv_cache, page_table, seq_lens, q_seq, lse, mass, workspace, *others)
-    _need_shaped(q, torch.bfloat16, q.shape, f"{what}: q")
-    _need_shaped(kv_cache, torch.uint8, kv_cache.shape, f"{what}: kv_cache")
-    _need_shaped(page_table, torch.int32, (n_seq, page_table.shape[-1]), f"{what}: page_table")
-    _need_shaped(seq_lens, torch.int32, (n_seq,), f"{what}: seq_lens")
-    _need_shaped(q_seq, torch.int32, (n_q,), f"{what}: q_seq")
-    _need_shaped(lse, torch.float32, (n_q, h_s), f"{what}: lse")
+    for t, dtype, shape, name in ((q, torch.bfloat16, q.shape, "q"), (kv_cache, torch.uint8, kv_cache.shape, "kv_cache"),
+                                  (page_table, torch.int32, (n_seq, page_table.shape[-1]), "page_table"),
+                                  (seq_lens, torch.int32, (n_seq,), "seq_lens"), (q_seq, torch.int32, (n_q,), "q_seq"),
+                                  (lse, torch.float32, (n_q, h_s), "lse")):
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            _need_shaped(t, dtype, shape, f"{what}: {name}")
     if mass is not None and (mass.dtype != torch.int64 or mass.dim() != 2 or mass.shape[0] != n_seq or
                              (mass.stride(1) != 1 and mass.shape[1] > 1)):
         raise ValueError(f"{what}: mass must be int64 [n_seq, max_ctx] with contiguous rows")
