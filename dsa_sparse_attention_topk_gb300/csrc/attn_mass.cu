@@ -49,15 +49,20 @@ constexpr float kMassMost = 67108864.0f;          // 2^26: one addition's limit
 template <int N> struct Shape {
   static constexpr int width = N == 128 ? 32 : 16;          // columns of four warps
   static constexpr int parts = N / width;                   // fours of warps
-  static constexpr int threads = 32 * (kWarpEpi0 + 4 * parts);
-  static constexpr int stages = N <= 32 ? 2 : 1;            // tiles of staged records
-  static constexpr int slots = N == 64 ? 2 : N == 16 ? 3 : 1;  // chunks of queries in shared memory
+  static constexpr int threads = 32 * (kWarpEpi0 + 4 * parts);  // (sparse: and four warps)
+  static constexpr int pieces = N == 128 ? 5 : N == 64 ? 9 : 10;  // of staged records
+  static constexpr int tables = (pieces + 4) / 5 + 1;       // tiles whose slots are at hand
+  static constexpr int slots = N == 16 ? 3 : 1;             // chunks of queries in shared memory
   static constexpr int block = N * 128;                     // bytes of 64 dims
   static constexpr int off_stage = slots * kBlocks * block;
-  static constexpr int off_col = off_stage + stages * kStageBytes;  // [2][N / 2] pairs of columns, 16 bytes
+  static constexpr int off_col = off_stage + (pieces % 5 ? pieces * kPiece : pieces / 5 * kStageBytes);  // [2][N / 2] pairs of columns, 16 bytes
   static constexpr int off_limit = off_col + 2 * N * 8;     // [2][N] positions seen
-  static constexpr int off_slot = off_limit + 2 * N * 4;    // [stages + 1][128] slots of a tile's records, -1: none
-  static constexpr int off_ctl = off_slot + (stages + 1) * kTile * 4;
+  static constexpr int off_slot = off_limit + 2 * N * 4;    // [tables][128] slots of a tile's records, -1: none
+  static constexpr int off_ctl = off_slot + tables * kTile * 4;
+  // where piece d of all, piece s of its tile, is staged
+  __device__ static __forceinline__ int staged(uint32_t d, int s) {
+    return off_stage + (pieces % 5 ? static_cast<int>(d % pieces) * kPiece : static_cast<int>(d / 5 % (pieces / 5)) * kStageBytes + piece_at(s));
+  }
   // tensor memory columns: accumulators, tiles of 128 dims (64 each), scales and positions of three tiles (with two,
   // those of the tile after next could be written while the last accumulator of this one is scaled), partial sums
   static constexpr int accs = N == 128 ? 2 : N == 64 ? 3 : 4;
@@ -67,7 +72,7 @@ template <int N> struct Shape {
   static constexpr int col_part = col_info + 24;
   static_assert(col_part + 2 * (parts - 1) <= 512 && ring >= accs, "tensor memory");
 };
-constexpr int kMostSlots = 3, kMostAccs = 4;
+constexpr int kMostSlots = 3, kMostAccs = 4, kMostPieces = 10;
 
 struct MassPlan {
   int n;             // columns of a chunk: 16, 32, 64 or 128
@@ -196,14 +201,14 @@ mass_query_kernel(MassArgs a, MassWs ws) {
 struct MassCtl {
   uint64_t b_full[kMostSlots][5], b_empty[kMostSlots][5];   // a chunk's queries, 128 dims (two blocks) a barrier
   uint64_t a_full[5], a_empty[5];                           // tiles of 128 dims
-  uint64_t rec_full[2][5], rec_empty[2][5];                 // of the staged records, 128 dims a barrier
+  uint64_t rec_full[kMostPieces], rec_empty[kMostPieces];   // staged pieces
   uint64_t d_full[kMostAccs], d_free[kMostAccs];
   uint64_t part_full[2];
   uint64_t col_full[2], col_empty[2];
   uint64_t slot_full[3], slot_empty[3];                     // sparse: a tile's slots
   uint64_t drained[2];
   int all_seen[2];                      // every column of the chunk sees the whole tile
-  long long scan[24];
+  long long scan[28];
   int first_group, first_tile, first_chunk, items, abort;
   uint32_t tmem;
 };
@@ -318,10 +323,11 @@ __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile in
 }
 
 template <bool SPARSE, int N>
-__global__ void __launch_bounds__(Shape<N>::threads, 1)
+__global__ void __launch_bounds__(Shape<N>::threads + (SPARSE ? 128 : 0), 1)
 attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap piece0_map,
                  const __grid_constant__ CUtensorMap piece_map, MassArgs a, MassPlan pl, MassWs ws) {
   using S = Shape<N>;
+  constexpr int kThreads = S::threads + (SPARSE ? 128 : 0);
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   MassCtl& ctl = *reinterpret_cast<MassCtl*>(smem + S::off_ctl);
@@ -341,14 +347,13 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       tc::mbar_init(&ctl.a_full[i], 4);
       tc::mbar_init(&ctl.a_empty[i], 1);
     }
-    for (int i = 0; i < S::stages; ++i)
-      for (int k = 0; k < 5; ++k) {
-        tc::mbar_init(&ctl.rec_full[i][k], SPARSE ? 128 * S::parts : 1);
-        tc::mbar_init(&ctl.rec_empty[i][k], 4);
-      }
-    for (int i = 0; i < S::stages + 1; ++i) {
+    for (int i = 0; i < S::pieces; ++i) {
+      tc::mbar_init(&ctl.rec_full[i], SPARSE ? 128 : 1);
+      tc::mbar_init(&ctl.rec_empty[i], 4);
+    }
+    for (int i = 0; i < S::tables; ++i) {
       tc::mbar_init(&ctl.slot_full[i], 1);
-      tc::mbar_init(&ctl.slot_empty[i], 4 + 4 * S::parts);
+      tc::mbar_init(&ctl.slot_empty[i], 8);
     }
     for (int i = 0; i < S::accs; ++i) {
       tc::mbar_init(&ctl.d_full[i], 1);
@@ -367,7 +372,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
   pdl_wait();
   // ---- the CTA's share of the items ----
   {
-    const int per = (pl.groups + S::threads - 1) / S::threads;
+    const int per = (pl.groups + kThreads - 1) / kThreads;
     const int g0 = min(tid * per, pl.groups), g1 = min(g0 + per, pl.groups);
     long long sum = 0;
     auto items_of = [&](int g) {
@@ -384,7 +389,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
     if (lane == 31) ctl.scan[warp] = incl;
     __syncthreads();
     long long before = incl - sum, total = 0;
-    for (int w = 0; w < S::threads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += ctl.scan[w];
       total += ctl.scan[w];
     }
@@ -554,10 +559,10 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       lookup();
       bool ok = true, more = true;
       for (uint32_t t = 0; ok && more; ++t) {
-        const int buf = t % (S::stages + 1);
+        const int buf = t % S::tables;
         int* s_slot = reinterpret_cast<int*>(smem + S::off_slot) + buf * kTile;
         if (SPARSE) {
-          ok = wait_warp(&ctl.slot_empty[buf], (t / (S::stages + 1)) ^ 1u);
+          ok = wait_warp(&ctl.slot_empty[buf], (t / S::tables) ^ 1u);
           if (!ok) break;
         }
 #pragma unroll
@@ -580,20 +585,20 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         } else {
           const int first_page = s_slot[0], second_page = s_slot[64];  // the tile's two pages, if they are there
           if (more) entry();
-          const int stage = t % S::stages;
-          uint8_t* to = smem + S::off_stage + stage * kStageBytes;
 #pragma unroll 1
           for (int s = 0; s < 5; ++s) {
-            ok = wait_warp(&ctl.rec_empty[stage][s], (t / S::stages) ^ 1u);
+            const uint32_t d = 5 * t + s;
+            ok = wait_warp(&ctl.rec_empty[d % S::pieces], (d / S::pieces) ^ 1u);
             if (!ok) break;
             if (lane == 0) {
               // (what lies behind the sequence in its last page comes with it and is not looked at)
-              uint64_t* bar = &ctl.rec_full[stage][s];
+              uint64_t* bar = &ctl.rec_full[d % S::pieces];
+              uint8_t* to = smem + S::staged(d, s);
               const int bytes = (s ? 128 : kPiece0) * kPage;
               tc::mbar_arrive_expect_tx(bar, ((first_page >= 0) + (second_page >= 0)) * bytes);
               const CUtensorMap* map = s ? &piece_map : &piece0_map;
-              if (first_page >= 0) tc::tma_load_3d(to + piece_at(s), map, dim0(s) / 4, first_page, 0, bar);
-              if (second_page >= 0) tc::tma_load_3d(to + piece_at(s) + bytes, map, dim0(s) / 4, second_page, 0, bar);
+              if (first_page >= 0) tc::tma_load_3d(to, map, dim0(s) / 4, first_page, 0, bar);
+              if (second_page >= 0) tc::tma_load_3d(to + bytes, map, dim0(s) / 4, second_page, 0, bar);
             }
             if (s == 0 && more) lookup();
           }
@@ -609,16 +614,14 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       bool ok = true, more = true;
       uint32_t q = 0;  // tiles of 128 dims widened
       for (uint32_t visit = 0; ok && more; ++visit) {
-        const int stage = visit % S::stages;
-        const uint8_t* rec = smem + S::off_stage + stage * kStageBytes;
 #pragma unroll 1
         for (int s = 0; s < 5; ++s, ++q) {
           const uint32_t at = q % S::ring;
-          ok = wait_warp(&ctl.rec_full[stage][s], visit / S::stages);
+          ok = wait_warp(&ctl.rec_full[q % S::pieces], q / S::pieces);
           ok = ok && wait_warp(&ctl.a_empty[at], (q / S::ring) ^ 1u);
           if (!ok) break;
           tc::fence_after_sync();
-          const uint8_t* mine = rec + piece_at(s) + row * (s ? 128 : kPiece0);
+          const uint8_t* mine = smem + S::staged(q, s) + row * (s ? 128 : kPiece0);
           if (s == 0) {
             uint32_t info[8];
             bool fine = true;
@@ -631,8 +634,8 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
 #pragma unroll
             for (int i = 0; i < 5; ++i) fine = fine && fabsf(__uint_as_float(info[i])) * 448.0f < INFINITY;
             if (!fine) info[0] = 0x7FC00000u;  // NaN: the position has no weight
-            const int buf = visit % (S::stages + 1);
-            if (SPARSE) ok = wait_warp(&ctl.slot_full[buf], visit / (S::stages + 1));
+            const int buf = visit % S::tables;
+            if (SPARSE) ok = wait_warp(&ctl.slot_full[buf], visit / S::tables);
             info[5] = reinterpret_cast<const uint32_t*>(smem + S::off_slot)[buf * kTile + row];
             if (SPARSE) {
               __syncwarp();
@@ -658,7 +661,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             tc::tmem_st16(tmem + lanes + S::col_a + 64 * at + 16 * j, o);
           }
           __syncwarp();
-          if (!SPARSE && lane == 0) tc::mbar_arrive(&ctl.rec_empty[stage][s]);
+          if (lane == 0) tc::mbar_arrive(&ctl.rec_empty[q % S::pieces]);
           tc::tmem_wait_st();
           tc::fence_before_sync();
           __syncwarp();
@@ -667,46 +670,53 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         more = walk_next<N>(ws, pl.groups, w);
       }
     }
+  } else if (SPARSE && warp >= kWarpEpi0 + 4 * S::parts) {
+    // ---- records of entries, wherever they lie: eight lanes 128 bytes of one, asynchronously.  A warp's request for 512
+    // bytes takes it 40 cycles and more, so four warps do nothing else.  (512 rows of 128 heads over 2048 entries: one
+    // warp 311 us, the sixteen that form the weights, which then wait for it, 230; a bulk copy a record, 80 cycles each, more.) ----
+    if (walk_begin<N>(ws, ctl, w)) {
+      constexpr int kEach = 8;
+      const int chunk = lane & 7, r = (warp - kWarpEpi0 - 4 * S::parts) * 4 + (lane >> 3);
+      const uint32_t tiles = static_cast<uint32_t>(w.left);
+      const uint8_t* mine = a.kv_cache + 16 * chunk;
+      bool ok = true;
+      for (uint32_t t = 0; ok && t < tiles; ++t) {
+        const uint32_t buf = t % S::tables;
+        ok = wait_warp(&ctl.slot_full[buf], t / S::tables);
+        if (!ok) break;
+        const int* s_slot = reinterpret_cast<const int*>(smem + S::off_slot) + buf * kTile + r;
+        const uint8_t* from[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int slot = s_slot[16 * i];
+          from[i] = slot < 0 ? nullptr : mine + static_cast<int64_t>(slot) * kKvTokBytes;
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl.slot_empty[buf]);
+#pragma unroll 1
+        for (int s = 0; s < 5; ++s) {
+          const uint32_t d = 5 * t + s;
+          ok = wait_warp(&ctl.rec_empty[d % S::pieces], (d / S::pieces) ^ 1u);
+          if (!ok) break;
+          const int width = s ? 128 : kPiece0;
+          const bool on = s || chunk < kPiece0 / 16;
+          const uint32_t to = smem_u32(smem) + S::staged(d, s) + r * width + ((s ? chunk ^ (r & 7) : chunk) << 4);
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) copy16_if(on && from[i], to + 16 * width * i, from[i] + dim0(s));
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(&ctl.rec_full[d % S::pieces])) : "memory");
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
   } else if (warp >= kWarpEpi0) {
     // ---- weights: a position a lane, S::width of a chunk's columns each four warps ----
     constexpr int W = S::width;
     const int quarter = warp & 3, part = (warp - kWarpEpi0) >> 2, row = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     uint32_t d = 0;
-    // Sparse: these warps also fetch the records, entries wherever they lie, eight lanes 128 bytes of one: a piece of the
-    // tile S::stages behind, once the products of this tile's are done, for which it was widened.  (One warp alone took
-    // 7000 cycles to ask for a tile, the four that widen 2200 besides their own work; a bulk copy a record 10000.)
-    auto fetch = [&](int s, uint32_t tile) {
-      const int* s_slot = reinterpret_cast<const int*>(smem + S::off_slot) + (tile % (S::stages + 1)) * kTile;
-      constexpr int kWarps = 4 * S::parts, kEach = 32 / kWarps;
-      const int chunk = lane & 7, width = s ? 128 : kPiece0, least = s || chunk < kPiece0 / 16 ? 0 : INT32_MAX;
-      const uint32_t stage = smem_u32(smem + S::off_stage + (tile % S::stages) * kStageBytes + piece_at(s));
-      const uint8_t* from = a.kv_cache + dim0(s) + 16 * chunk;
-      int slot[kEach];
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) slot[i] = s_slot[(i * kWarps + warp - kWarpEpi0) * 4 + (lane >> 3)];
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int r = (i * kWarps + warp - kWarpEpi0) * 4 + (lane >> 3);
-        copy16_if(slot[i] >= least, stage + r * width + ((s ? chunk ^ (r & 7) : chunk) << 4),
-                  from + static_cast<int64_t>(slot[i]) * kKvTokBytes);
-      }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(&ctl.rec_full[tile % S::stages][s])) : "memory");
-    };
     if (walk_begin<N>(ws, ctl, w)) {
       bool ok = true, more = true;
-      if (SPARSE)
-        for (uint32_t t = 0; ok && t < S::stages && static_cast<int>(t) < w.left; ++t) {
-          ok = wait_warp(&ctl.slot_full[t], 0);
-          if (!ok) break;
-#pragma unroll 1
-          for (int s = 0; s < 5; ++s) fetch(s, t);
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&ctl.slot_empty[t]);
-        }
       for (uint32_t visit = 0; ok && more; ++visit) {
-        const uint32_t behind = visit + S::stages;  // the tile to fetch, if it is there
-        const bool fetches = SPARSE && w.left > S::stages;
         const uint32_t tile_info = tmem + lanes + S::col_info + 8 * (visit % 3);
         uint64_t acc[W / 2];
 #pragma unroll
@@ -737,15 +747,6 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             for (int i = 0; i < 8; ++i)
               acc[8 * h + i] = fma_pair(both, pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), acc[8 * h + i]);
           }
-          if (fetches) {
-            if (s == 0) ok = wait_warp(&ctl.slot_full[behind % (S::stages + 1)], behind / (S::stages + 1));
-            if (!ok) break;
-            fetch(s, behind);
-          }
-        }
-        if (fetches) {
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&ctl.slot_empty[behind % (S::stages + 1)]);
         }
         const int buf = visit & 1;
         ok = ok && wait_warp(&ctl.col_full[buf], visit >> 1);
@@ -813,7 +814,6 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           }
         }
       }
-      if (SPARSE) asm volatile("cp.async.wait_all;" ::: "memory");
     }
   }
   tc::fence_before_sync();
@@ -860,7 +860,7 @@ cudaError_t launch_main(const MassMaps& m, const MassArgs& a, const MassPlan& pl
   constexpr size_t smem = Shape<N>::off_ctl + sizeof(MassCtl);
   const cudaError_t e = cudaFuncSetAttribute(attn_mass_kernel<SPARSE, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_mass_kernel<SPARSE, N>, dim3(static_cast<unsigned>(grid)), dim3(Shape<N>::threads), smem, s, 1, m.q,
+  return launch_pdl(attn_mass_kernel<SPARSE, N>, dim3(static_cast<unsigned>(grid)), dim3(Shape<N>::threads + (SPARSE ? 128 : 0)), smem, s, 1, m.q,
                     m.piece0, m.piece, a, pl, ws);
 }
 
