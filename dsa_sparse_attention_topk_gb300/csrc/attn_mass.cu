@@ -57,20 +57,20 @@ template <int N> struct Shape {
   static constexpr int off_stage = slots * kBlocks * block;
   static constexpr int off_col = off_stage + (pieces % 5 ? pieces * kPiece : pieces / 5 * kStageBytes);  // [2][N / 2] pairs of columns, 16 bytes
   static constexpr int off_limit = off_col + 2 * N * 8;     // [2][N] positions seen
-  static constexpr int off_slot = off_limit + 2 * N * 4;    // [tables][128] slots of a tile's records, -1: none
+  // (the same place, sparse) [parts][128] sums of an entry's weights over a part's columns, -1: no entry
+  static constexpr int off_slot = off_limit + (2 * N > parts * kTile ? 2 * N : parts * kTile) * 4;  // [tables][128] slots of a tile's records, -1: none
   static constexpr int off_ctl = off_slot + tables * kTile * 4;
   // where piece d of all, piece s of its tile, is staged
   __device__ static __forceinline__ int staged(uint32_t d, int s) {
     return off_stage + (pieces % 5 ? static_cast<int>(d % pieces) * kPiece : static_cast<int>(d / 5 % (pieces / 5)) * kStageBytes + piece_at(s));
   }
   // tensor memory columns: accumulators, tiles of 128 dims (64 each), scales and positions of three tiles (with two,
-  // those of the tile after next could be written while the last accumulator of this one is scaled), partial sums
+  // those of the tile after next could be written while the last accumulator of this one is scaled)
   static constexpr int accs = N == 128 ? 2 : N == 64 ? 3 : 4;
   static constexpr int ring = N == 128 ? 3 : N == 64 ? 4 : 5;
   static constexpr int col_a = accs * N;
   static constexpr int col_info = col_a + 64 * ring;
-  static constexpr int col_part = col_info + 24;
-  static_assert(col_part + 2 * (parts - 1) <= 512 && ring >= accs, "tensor memory");
+  static_assert(col_info + 24 <= 512 && ring >= accs, "tensor memory");
 };
 constexpr int kMostSlots = 3, kMostAccs = 4, kMostPieces = 10;
 
@@ -203,7 +203,7 @@ struct MassCtl {
   uint64_t a_full[5], a_empty[5];                           // tiles of 128 dims
   uint64_t rec_full[kMostPieces], rec_empty[kMostPieces];   // staged pieces
   uint64_t d_full[kMostAccs], d_free[kMostAccs];
-  uint64_t part_full[2];
+  uint64_t part_full, part_empty;                           // sparse: a tile's sums
   uint64_t col_full[2], col_empty[2];
   uint64_t slot_full[3], slot_empty[3];                     // sparse: a tile's slots
   uint64_t drained[2];
@@ -322,6 +322,15 @@ __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile in
   return tc::mbar_wait(bar, parity, abort, status);
 }
 
+// weight `total` to position pos of sequence b
+__device__ __forceinline__ void add_mass(const MassArgs& a, int b, int pos, float total) {
+  if (!a.mass) return;
+  if (total != total) flag(a.status, DSA_STATUS_NAN_SCORE);
+  else if (total > 0.f)
+    atomicAdd(reinterpret_cast<unsigned long long*>(a.mass + static_cast<int64_t>(b) * a.mass_stride + pos),
+              static_cast<unsigned long long>(__float2ll_rn(fminf(total, kMassMost) * kMassOne)));
+}
+
 template <bool SPARSE, int N>
 __global__ void __launch_bounds__(Shape<N>::threads + (SPARSE ? 128 : 0), 1)
 attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap piece0_map,
@@ -361,10 +370,11 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&ctl.drained[i], 1);
-      tc::mbar_init(&ctl.part_full[i], S::parts > 1 ? 4 * (S::parts - 1) : 1);
       tc::mbar_init(&ctl.col_full[i], 1);
       tc::mbar_init(&ctl.col_empty[i], 4 * S::parts);
     }
+    tc::mbar_init(&ctl.part_full, 4 * S::parts);
+    tc::mbar_init(&ctl.part_empty, 1);
     tc::mbar_fence_init();
     ctl.first_group = ctl.first_tile = ctl.first_chunk = 0;
   }
@@ -420,8 +430,32 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
 
   if (warp == kWarpB) {
     // ---- a chunk's queries, 128 dims at a time, and its columns' constants; columns behind the group's last have
-    // no weight ----
+    // no weight.  Sparse: and the tiles' sums on their way out, two items behind (left to the first of the parts they
+    // were 2400 of its 6000 cycles a tile, for which everything waits) ----
+    Walk done;
+    uint32_t n_done = 0;
+    auto give = [&] {
+      if (!wait_warp(&ctl.part_full, n_done)) return false;
+      const float* sums = reinterpret_cast<const float*>(smem + S::off_limit);
+      const int64_t row = static_cast<int64_t>(done.g) * a.topk + done.tile * kTile;
+#pragma unroll 1
+      for (int i = lane; i < kTile; i += 32) {
+        float total = sums[i];
+        if (total < 0.f) continue;
+        const int pos = a.idx[row + i];
+#pragma unroll
+        for (int k = 1; k < S::parts; ++k) total += sums[k * kTile + i];
+        if (a.weights) a.weights[row + i] = total;
+        add_mass(a, done.grp.w, pos, total);
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&ctl.part_empty);
+      walk_next<N>(ws, pl.groups, done);
+      ++n_done;
+      return true;
+    };
     if (walk_begin<N>(ws, ctl, w)) {
+      if (SPARSE) done = w;
       int slot = 0;
       uint32_t phase = 0, n = 0;
       bool ok = true, more = true, fresh = true;  // fresh: other columns than the item's before
@@ -466,7 +500,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           if (at >= N) continue;
           pairs[4 * (at >> 1) + (at & 1)] = info[i].x;
           pairs[4 * (at >> 1) + 2 + (at & 1)] = info[i].y;
-          limits[at] = __float_as_int(info[i].z);
+          if (!SPARSE) limits[at] = __float_as_int(info[i].z);
         }
         if (lane == 0) ctl.all_seen[buf] = SPARSE || least >= (w.tile + 1) * kTile;
         __syncwarp();
@@ -475,6 +509,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         more = walk_next<N>(ws, pl.groups, w);
         fresh = !w.same_chunk(was);
         ++n;
+        while (SPARSE && ok && n_done < n && (n_done + 3 <= n || !more)) ok = give();
       }
       // copies in flight must land before the CTA ends; a slot that was never loaded is past the phase before its first
       if (*abort) {
@@ -721,9 +756,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         uint64_t acc[W / 2];
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) acc[i] = 0ull;
-        int pos = -1, entry = 0;
-        if (SPARSE && part == 0 && w.tile * kTile + row < w.grp.x)
-          entry = a.idx[static_cast<int64_t>(w.g) * a.topk + w.tile * kTile + row];
+        int pos = -1;
 #pragma unroll 1
         for (int s = 0; s < 5; ++s, ++d) {
           const uint32_t at = d % S::accs;
@@ -751,9 +784,8 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         const int buf = visit & 1;
         ok = ok && wait_warp(&ctl.col_full[buf], visit >> 1);
         if (!ok) break;
-        // (the slot says whether there is a position; which one, its place or its entry)
-        const int place = w.tile * kTile + row;
-        if (pos >= 0) pos = SPARSE ? entry : place;
+        // (the slot says whether there is a position; which one, its place)
+        if (!SPARSE && pos >= 0) pos = w.tile * kTile + row;
         const ulonglong2* cols = reinterpret_cast<const ulonglong2*>(smem + S::off_col) + (buf * N + part * W) / 2;
         float total = 0.f;
         if (SPARSE || ctl.all_seen[buf]) {
@@ -778,41 +810,16 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ctl.col_empty[buf]);
-        const Walk was = w;
+        if constexpr (SPARSE) {
+          ok = wait_warp(&ctl.part_empty, visit ^ 1u);
+          if (!ok) break;
+          reinterpret_cast<float*>(smem + S::off_limit)[part * kTile + row] = pos >= 0 ? total : -1.f;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&ctl.part_full);
+        }
+        const int b = w.grp.w;
         more = walk_next<N>(ws, pl.groups, w);
-        bool gives = pos >= 0;
-        if (SPARSE && S::parts > 1) {
-          // an entry's weight is the sum of all parts': the first gathers it, by way of tensor memory.  (A buffer's sums have
-          // been read before the tile after next is: the accumulators hold the parts together.)
-          const uint32_t cell = tmem + lanes + S::col_part + (S::parts - 1) * (visit & 1);
-          if (part > 0) {
-            tmem_st1(cell + part - 1, total);
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&ctl.part_full[visit & 1]);
-            gives = false;
-          } else {
-            ok = wait_warp(&ctl.part_full[visit & 1], visit >> 1);
-            if (!ok) break;
-            tc::fence_after_sync();
-            float v[S::parts];
-#pragma unroll
-            for (int i = 1; i < S::parts; ++i) v[i] = tmem_ld1(cell + i - 1);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int i = 1; i < S::parts; ++i) total += v[i];
-          }
-        }
-        if (gives) {
-          if (SPARSE && a.weights) a.weights[static_cast<int64_t>(was.g) * a.topk + was.tile * kTile + row] = total;
-          if (a.mass) {
-            if (total != total) flag(a.status, DSA_STATUS_NAN_SCORE);
-            else if (total > 0.f)
-              atomicAdd(reinterpret_cast<unsigned long long*>(a.mass + static_cast<int64_t>(was.grp.w) * a.mass_stride + pos),
-                        static_cast<unsigned long long>(__float2ll_rn(fminf(total, kMassMost) * kMassOne)));
-          }
-        }
+        if (!SPARSE && pos >= 0) add_mass(a, b, pos, total);
       }
     }
   }
