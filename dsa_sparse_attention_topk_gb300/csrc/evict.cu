@@ -6,12 +6,17 @@
 // its positions: a radix select in digits of 9 bits, from the highest bit in which the weights differ
 // at all, each digit one pass over the run (shared memory, if it fits) into a histogram that all CTAs
 // read over distributed shared memory.  It ends as soon as a bin is kept whole.  Two more passes count and
-// write, in position order.  Bound: latency, some ten passes and cluster barriers in a row; the weights are
-// read from memory once.
+// write, in position order.  The weights are read from memory once.  Bound: latency, three to five digits of a pass, a
+// cluster barrier and sixteen remote loads each (32 sequences of 16-32K to 2048: 23 us, one of 128K to 64K: 28, of which
+// the memory needs 1).  Digits of 8 bits with a warp finding the bin took 82 and 72.
 //
-// Moving.  A warp copies a token's 608-byte record and 132-byte key in words of 16 bytes.  Bound: memory.  In place
-// a token's new place may hold another's record that has not been read, so the records go through the
-// workspace, where the second kernel mostly finds them in L2.
+// Moving.  A warp copies four tokens' 608-byte records and 132-byte keys in words of 16 bytes, all read before any is
+// written.  Bound: memory (32 x 2048 tokens to other pages: 18.5 us, 5.3 TB/s read and written).  In place a token's
+// new place may hold another's record that has not been read, so the records go through the workspace, where
+// the second kernel mostly finds them in L2 (65536 tokens: 31 us; written once it would be 15, but a block would
+// have to wait for the blocks that read what it overwrites).
+
+#include <mutex>
 
 #include "dsa_common.cuh"
 #include "dsa_launch.h"
@@ -24,7 +29,7 @@ constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;  // a bin a thread
 constexpr int kAhead = 4;                             // keys of a thread under way together
 static_assert(kBins == kSelThreads, "a bin a thread");
 constexpr int kCacheKeys = 24 * 1024;  // keys of a CTA held in shared memory: 192 KB
-constexpr int kMostCluster = 8;
+constexpr int kCluster = 8, kWideCluster = 16;
 
 // order-preserving: a larger weight has a larger key
 __device__ __forceinline__ uint64_t mass_key(int64_t m) { return static_cast<uint64_t>(m) ^ (1ull << 63); }
@@ -55,6 +60,8 @@ __device__ __forceinline__ void peer_sync(int ranks) {
   else cluster_sync();
 }
 
+// MOST: CTAs of a sequence, at most
+template <int MOST>
 __global__ void __launch_bounds__(kSelThreads)
 evict_select_kernel(EvictSelectArgs a, int ranks, int cached) {
   extern __shared__ __align__(16) uint64_t s_keys[];
@@ -170,7 +177,7 @@ evict_select_kernel(EvictSelectArgs a, int ranks, int cached) {
       const int bin = kBins - 1 - tid;
       unsigned sum = 0;
 #pragma unroll
-      for (int r = 0; r < kMostCluster; ++r)
+      for (int r = 0; r < MOST; ++r)
         if (r < ranks) sum += peer_u32(hist + bin, r, ranks);
       unsigned before = sum;
 #pragma unroll
@@ -355,24 +362,59 @@ evict_move_kernel(EvictCompactArgs a) {
   }
 }
 
+// Clusters of sixteen CTAs, each with all the shared memory that one may take, that fit on the current device at once;
+// asked once a device.
+int wide_clusters() {
+  static std::mutex mu;
+  static int known[64] = {};  // the answer and one
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[dev] > 0) return known[dev] - 1;
+  const int smem = kCacheKeys * static_cast<int>(sizeof(uint64_t));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kWideCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kWideCluster);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(evict_select_kernel<kWideCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaFuncSetAttribute(evict_select_kernel<kWideCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, evict_select_kernel<kWideCluster>, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    n = 0;
+  }
+  known[dev] = n + 1;
+  return n;
+}
+
 }  // namespace
 
 cudaError_t launch_evict_select(const EvictSelectArgs& a, cudaStream_t s) {
-  // A CTA for each 2048 positions while all sequences' fit two to an SM, at most eight a sequence
+  // A CTA for each 2048 positions while all sequences' fit two to an SM, at most eight a sequence; sixteen where
+  // such clusters fit for all sequences at once (one of 128K: 35 us with eight)
   int ranks = 1;
-  while (ranks < kMostCluster && ranks * 2048 < a.max_ctx &&
+  while (ranks < kCluster && ranks * 2048 < a.max_ctx &&
          static_cast<int64_t>(a.n_seq) * ranks * 2 <= static_cast<int64_t>(multiprocessors()) * 2)
     ranks *= 2;
+  // (a kernel of its own: with one for both, 32 sequences of 32K took 30 us instead of 23)
+  const bool wide = ranks == kCluster && kCluster * 2048 < a.max_ctx && a.n_seq <= wide_clusters();
+  if (wide) ranks = kWideCluster;
   const int run = ((a.max_ctx + ranks * kSelWarps - 1) / (ranks * kSelWarps) + 31) / 32 * 32 * kSelWarps;
   const int cached = run <= kCacheKeys;
   const size_t smem = cached ? sizeof(uint64_t) * run : 0;
-  if (smem > 0) {
-    const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const auto kernel = wide ? evict_select_kernel<kWideCluster> : evict_select_kernel<kCluster>;
+  if (smem > 0 && !wide) {  // (the wide one's is set)
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kCacheKeys * static_cast<int>(sizeof(uint64_t)));
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(evict_select_kernel, dim3(static_cast<unsigned>(a.n_seq) * ranks), dim3(kSelThreads), smem, s, ranks, a,
-                    ranks, cached);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(a.n_seq) * ranks), dim3(kSelThreads), smem, s, ranks, a, ranks, cached);
 }
 
 size_t evict_workspace_bytes(int n_seq, int budget) {

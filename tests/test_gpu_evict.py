@@ -72,12 +72,14 @@ def test_select(dsa, kind, n_seq, ctx, budget, sinks, recent):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", KINDS)
-def test_select_of_a_context_beyond_shared_memory(dsa, kind):
-    """300,000 positions on eight CTAs: more than a CTA's 24 K keys."""
-    mass = _mass(kind, 2, 300000, 9)
-    lens = torch.tensor([300000, 250001], dtype=torch.int32)
-    got = dsa.evict_select(mass.cuda(), lens.cuda(), 100000, 4, 64)
-    for have, want in zip(got, _select(mass, lens, 100000, 4, 64)):
+@pytest.mark.parametrize("n_seq,ctx", [(2, 300000), (9, 300000), (1, 500000), (9, 20000), (7, 20000)])
+def test_select_of_long_contexts(dsa, kind, n_seq, ctx):
+    """Few sequences have sixteen CTAs each, more of them eight; a CTA holds 24 K keys in shared memory, so 300,000
+    positions are beyond that with eight, 500,000 with sixteen."""
+    mass = _mass(kind, n_seq, ctx, 9)
+    lens = torch.tensor([ctx, ctx - ctx // 6 + 1] * 5, dtype=torch.int32)[:n_seq]
+    got = dsa.evict_select(mass.cuda(), lens.cuda(), ctx // 3, 4, 64)
+    for have, want in zip(got, _select(mass, lens, ctx // 3, 4, 64)):
         assert torch.equal(have.cpu(), want)
 
 
