@@ -20,7 +20,12 @@
 // entries (sparse).  Items (group, chunk of N columns, tile of 128 positions) are shared out evenly over one CTA per
 // SM; a chunk's queries stay while its tiles pass, each tile a ring of pieces of 128 dims.
 //
-// Bound: tensor cores with many columns (128 x N x 576 products an item); the cache's bytes with few.
+// Bound.  32 rows of 128 heads over 16-32K positions each take 132 us (what has to be read 72, products 59), 64 rows of
+// 128 heads over 32K 313 (products 157), 512 rows of 128 heads over 2048 entries 196 (products 74).  A tile is 6000 to
+// 7000 cycles at 128 columns, 2304 of them products: an accumulator waits for the warps that scale and add it, two of
+// them fit beside the widened codes, and those warps also have the tile's exponentials, 500 cycles of which the
+// accumulators lie full.  Tried and slower: one read of 32 columns instead of two of 16 (145 us: spills), products of
+// floats one by one (134), a single lane that polls for its warp (143), suspended waits with a hint (137).
 
 #include <cuda.h>
 
@@ -55,14 +60,18 @@ template <int N> struct Shape {
   static constexpr int slots = N == 16 ? 3 : 1;             // chunks of queries in shared memory
   static constexpr int block = N * 128;                     // bytes of 64 dims
   static constexpr int off_stage = slots * kBlocks * block;
-  static constexpr int off_col = off_stage + (pieces % 5 ? pieces * kPiece : pieces / 5 * kStageBytes);  // [2][N / 2] pairs of columns, 16 bytes
+  // [2][N / 2] pairs of columns, 16 bytes
+  static constexpr int off_col = off_stage + (pieces % 5 ? pieces * kPiece : pieces / 5 * kStageBytes);
   static constexpr int off_limit = off_col + 2 * N * 8;     // [2][N] positions seen
-  // (the same place, sparse) [parts][128] sums of an entry's weights over a part's columns, -1: no entry
-  static constexpr int off_slot = off_limit + (2 * N > parts * kTile ? 2 * N : parts * kTile) * 4;  // [tables][128] slots of a tile's records, -1: none
+  // [parts][128] sums of a position's weights over a part's columns, -1: no position
+  static constexpr int off_sum = off_limit + 2 * N * 4;
+  // [tables][128] slots of a tile's records, -1: none
+  static constexpr int off_slot = off_sum + parts * kTile * 4;
   static constexpr int off_ctl = off_slot + tables * kTile * 4;
   // where piece d of all, piece s of its tile, is staged
   __device__ static __forceinline__ int staged(uint32_t d, int s) {
-    return off_stage + (pieces % 5 ? static_cast<int>(d % pieces) * kPiece : static_cast<int>(d / 5 % (pieces / 5)) * kStageBytes + piece_at(s));
+    return off_stage + (pieces % 5 ? static_cast<int>(d % pieces) * kPiece
+                                   : static_cast<int>(d / 5 % (pieces / 5)) * kStageBytes + piece_at(s));
   }
   // tensor memory columns: accumulators, tiles of 128 dims (64 each), scales and positions of three tiles (with two,
   // those of the tile after next could be written while the last accumulator of this one is scaled)
@@ -203,7 +212,7 @@ struct MassCtl {
   uint64_t a_full[5], a_empty[5];                           // tiles of 128 dims
   uint64_t rec_full[kMostPieces], rec_empty[kMostPieces];   // staged pieces
   uint64_t d_full[kMostAccs], d_free[kMostAccs];
-  uint64_t part_full, part_empty;                           // sparse: a tile's sums
+  uint64_t part_full, part_empty;                           // a tile's sums
   uint64_t col_full[2], col_empty[2];
   uint64_t slot_full[3], slot_empty[3];                     // sparse: a tile's slots
   uint64_t drained[2];
@@ -213,7 +222,9 @@ struct MassCtl {
   uint32_t tmem;
 };
 constexpr int kMostSmem = 232448;
-static_assert(Shape<128>::off_ctl + sizeof(MassCtl) <= kMostSmem && Shape<64>::off_ctl + sizeof(MassCtl) <= kMostSmem && Shape<32>::off_ctl + sizeof(MassCtl) <= kMostSmem &&
+static_assert(Shape<128>::off_ctl + sizeof(MassCtl) <= kMostSmem &&
+              Shape<64>::off_ctl + sizeof(MassCtl) <= kMostSmem &&
+              Shape<32>::off_ctl + sizeof(MassCtl) <= kMostSmem &&
               Shape<16>::off_ctl + sizeof(MassCtl) <= kMostSmem, "shared memory");
 
 // A walk over the CTA's items: chunk c of tile `tile` of group g
@@ -430,22 +441,22 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
 
   if (warp == kWarpB) {
     // ---- a chunk's queries, 128 dims at a time, and its columns' constants; columns behind the group's last have
-    // no weight.  Sparse: and the tiles' sums on their way out, two items behind (left to the first of the parts they
-    // were 2400 of its 6000 cycles a tile, for which everything waits) ----
+    // no weight.  And the tiles' sums on their way out, two items behind (left to the first of the parts they
+    // were 2400 of its 6000 cycles a tile of entries, for which everything waits) ----
     Walk done;
     uint32_t n_done = 0;
     auto give = [&] {
       if (!wait_warp(&ctl.part_full, n_done)) return false;
-      const float* sums = reinterpret_cast<const float*>(smem + S::off_limit);
-      const int64_t row = static_cast<int64_t>(done.g) * a.topk + done.tile * kTile;
+      const float* sums = reinterpret_cast<const float*>(smem + S::off_sum);
+      const int64_t row = SPARSE ? static_cast<int64_t>(done.g) * a.topk + done.tile * kTile : 0;
 #pragma unroll 1
       for (int i = lane; i < kTile; i += 32) {
         float total = sums[i];
         if (total < 0.f) continue;
-        const int pos = a.idx[row + i];
+        const int pos = SPARSE ? a.idx[row + i] : done.tile * kTile + i;
 #pragma unroll
         for (int k = 1; k < S::parts; ++k) total += sums[k * kTile + i];
-        if (a.weights) a.weights[row + i] = total;
+        if (SPARSE && a.weights) a.weights[row + i] = total;
         add_mass(a, done.grp.w, pos, total);
       }
       __syncwarp();
@@ -455,7 +466,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       return true;
     };
     if (walk_begin<N>(ws, ctl, w)) {
-      if (SPARSE) done = w;
+      done = w;
       int slot = 0;
       uint32_t phase = 0, n = 0;
       bool ok = true, more = true, fresh = true;  // fresh: other columns than the item's before
@@ -500,7 +511,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           if (at >= N) continue;
           pairs[4 * (at >> 1) + (at & 1)] = info[i].x;
           pairs[4 * (at >> 1) + 2 + (at & 1)] = info[i].y;
-          if (!SPARSE) limits[at] = __float_as_int(info[i].z);
+          limits[at] = __float_as_int(info[i].z);
         }
         if (lane == 0) ctl.all_seen[buf] = SPARSE || least >= (w.tile + 1) * kTile;
         __syncwarp();
@@ -509,7 +520,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         more = walk_next<N>(ws, pl.groups, w);
         fresh = !w.same_chunk(was);
         ++n;
-        while (SPARSE && ok && n_done < n && (n_done + 3 <= n || !more)) ok = give();
+        while (ok && n_done < n && (n_done + 3 <= n || !more)) ok = give();
       }
       // copies in flight must land before the CTA ends; a slot that was never loaded is past the phase before its first
       if (*abort) {
@@ -708,7 +719,8 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
   } else if (SPARSE && warp >= kWarpEpi0 + 4 * S::parts) {
     // ---- records of entries, wherever they lie: eight lanes 128 bytes of one, asynchronously.  A warp's request for 512
     // bytes takes it 40 cycles and more, so four warps do nothing else.  (512 rows of 128 heads over 2048 entries: one
-    // warp 311 us, the sixteen that form the weights, which then wait for it, 230; a bulk copy a record, 80 cycles each, more.) ----
+    // warp 311 us, the sixteen that form the weights, which then wait for it, 230; these four 213.  A bulk copy a record
+    // takes the thread that asks 80 cycles.) ----
     if (walk_begin<N>(ws, ctl, w)) {
       constexpr int kEach = 8;
       const int chunk = lane & 7, r = (warp - kWarpEpi0 - 4 * S::parts) * 4 + (lane >> 3);
@@ -756,7 +768,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         uint64_t acc[W / 2];
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) acc[i] = 0ull;
-        int pos = -1;
+        int slot = -1;
 #pragma unroll 1
         for (int s = 0; s < 5; ++s, ++d) {
           const uint32_t at = d % S::accs;
@@ -764,7 +776,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           if (!ok) break;
           tc::fence_after_sync();
           const float scale = tmem_ld1(tile_info + (s ? s - 1 : 4));
-          if (s == 0) pos = __float_as_int(tmem_ld1(tile_info + 5));
+          if (s == 0) slot = __float_as_int(tmem_ld1(tile_info + 5));
 #pragma unroll
           for (int h = 0; h < W / 16; ++h) {  // (16 columns at a time: 768 threads have 80 registers each)
             uint32_t v[16];
@@ -784,8 +796,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         const int buf = visit & 1;
         ok = ok && wait_warp(&ctl.col_full[buf], visit >> 1);
         if (!ok) break;
-        // (the slot says whether there is a position; which one, its place)
-        if (!SPARSE && pos >= 0) pos = w.tile * kTile + row;
+        const int pos = w.tile * kTile + row;
         const ulonglong2* cols = reinterpret_cast<const ulonglong2*>(smem + S::off_col) + (buf * N + part * W) / 2;
         float total = 0.f;
         if (SPARSE || ctl.all_seen[buf]) {
@@ -810,16 +821,12 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ctl.col_empty[buf]);
-        if constexpr (SPARSE) {
-          ok = wait_warp(&ctl.part_empty, visit ^ 1u);
-          if (!ok) break;
-          reinterpret_cast<float*>(smem + S::off_limit)[part * kTile + row] = pos >= 0 ? total : -1.f;
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&ctl.part_full);
-        }
-        const int b = w.grp.w;
+        ok = wait_warp(&ctl.part_empty, visit ^ 1u);
+        if (!ok) break;
+        reinterpret_cast<float*>(smem + S::off_sum)[part * kTile + row] = slot >= 0 ? total : -1.f;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl.part_full);
         more = walk_next<N>(ws, pl.groups, w);
-        if (!SPARSE && pos >= 0) add_mass(a, b, pos, total);
       }
     }
   }

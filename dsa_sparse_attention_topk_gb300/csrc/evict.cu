@@ -7,8 +7,8 @@
 // at all, each digit one pass over the run (shared memory, if it fits) into a histogram that all CTAs
 // read over distributed shared memory.  It ends as soon as a bin is kept whole.  Two more passes count and
 // write, in position order.  The weights are read from memory once.  Bound: latency, three to five digits of a pass, a
-// cluster barrier and sixteen remote loads each (32 sequences of 16-32K to 2048: 23 us, one of 128K to 64K: 28, of which
-// the memory needs 1).  Digits of 8 bits with a warp finding the bin took 82 and 72.
+// cluster barrier and remote loads each (32 sequences of 16-32K to 2048: 23 us, one of 128K to 64K: 28, for 6 MB and 1 MB
+// of weights).  Digits of 8 bits took 82 and 72.
 //
 // Moving.  A warp copies four tokens' 608-byte records and 132-byte keys in words of 16 bytes, all read before any is
 // written.  Bound: memory (32 x 2048 tokens to other pages: 18.5 us, 5.3 TB/s read and written).  In place a token's

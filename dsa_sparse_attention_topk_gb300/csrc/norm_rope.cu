@@ -7,7 +7,8 @@
 // mean is taken off before anything is squared, so that a row far from zero loses nothing.
 //
 // Bound: memory, each value read and written once.  A row stays in the registers of 8 to 32 lanes between the
-// sums and the turn.
+// sums and the turn, 8 to 32 values a lane.  4096 x 64 x 128 bf16 take 29.6 us, 4.5 TB/s (a plain copy 20): the
+// rest is issue, 337 instructions a warp of four rows, and one wave's start and end.
 
 #include "norm_rope.cuh"
 

@@ -442,14 +442,14 @@ int dsa_prefix_attn(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t*
  * from the exact dequantised kv[p], with fp32 roundings alone: a weight is good to some 2^-19 times the size of
  * its logits.  (lse as an attention returns it may hold that attention's own roundings.)
  * mass holds whole numbers of 2^-36 (DSA_MASS_ONE is a weight of 1): additions to it are atomic, and equal calls
- * give equal bits whatever their order.  A sum of rows is rounded to that unit for each part of the work, some
- * hundreds of heads; the sum must stay below 2^27, one position's weight in a call counts as 2^26 at most.
+ * give equal bits whatever their order.  A sum of rows is rounded to that unit for each part of the work, 16
+ * to 128 heads; the sum must stay below 2^27, one position's weight in a call counts as 2^26 at most.
  * A head whose query or lse is NaN (or query infinite) has no weights; a position with NaN or infinite values has
  * none either (NaN in out_weights); both flag DSA_STATUS_NAN_SCORE.  An lse of -inf (a row that saw nothing)
  * adds nothing.  Rows whose sequence or length is out of range add nothing and flag DSA_STATUS_BAD_SEQ or
  * _BAD_LEN; positions whose page is out of range have no weight and flag DSA_STATUS_BAD_PAGE.
  *   q_bf16      [n_q][h_s][576] bfloat16, 16-byte aligned; n_q up to 65536, h_s 1..128.
- *   kv_cache .. q_seq   as for dsa_prefix_attn; page_table rows from position 0 on.
+ *   kv_cache .. q_seq   as for dsa_prefix_attn; num_pages up to 2^25; page_table rows from position 0 on.
  *   max_ctx     host-side bound of seq_lens, 1..1048576; max_pages >= ceil(max_ctx / 64).
  *   lse         [n_q][h_s] fp32, natural log.
  *   mass        [n_seq] rows of max_ctx int64, mass_stride elements apart, added to.
