@@ -751,7 +751,8 @@ def attn_mass(q, kv_cache, page_table, seq_lens, q_seq, q_pos, lse, max_ctx, sm_
 def sparse_attn_mass(q, kv_cache, page_table, seq_lens, q_seq, topk_idx, lse, sm_scale, mass=None, out=None, workspace=None,
                      stream=None):
     """The weights of the entries that each row selected, sum over its heads of exp(sm_scale q . kv - lse), 0 at empty
-    (negative) entries; added to mass[q_seq[t], topk_idx[t, e]] too where mass (int64 [n_seq, max_ctx]) is given.
+    (negative) entries; added to mass[q_seq[t], topk_idx[t, e]] too where mass (int64 [n_seq, max_ctx]) is given, whose
+    width then bounds seq_lens (a longer sequence has no weights, and device_status says so).
     topk_idx: int32 [n_q, K], as indexer_topk and decode_step return it; the others as for attn_mass.  Returns the
     weights, fp32 [n_q, K]."""
     dev, pages, workspace = _mass_args("sparse_attn_mass", q, kv_cache, page_table, seq_lens, q_seq, lse, mass, workspace,

@@ -603,7 +603,8 @@ static bool mass_sizes_ok(int32_t n_q, int32_t h_s) { return n_q >= 1 && n_q <= 
 static int check_mass(const char* who, const dsa::MassArgs& a, size_t workspace_bytes) {
   if (a.n_q < 0 || a.n_seq < 0) return fail(DSA_ERR_INVALID_ARG, "%s: negative n_q or n_seq", who);
   if (a.h_s < 1 || a.h_s > 128) return fail(DSA_ERR_UNSUPPORTED, "%s: h_s must be 1..128 (got %d)", who, a.h_s);
-  if (a.n_q > 65536) return fail(DSA_ERR_UNSUPPORTED, "%s: at most 65536 query rows a call", who);
+  // (a walk over more empty sequences could outlast the waits for it)
+  if (a.n_q > 65536 || a.n_seq > 65536) return fail(DSA_ERR_UNSUPPORTED, "%s: at most 65536 query rows and sequences a call", who);
   if (a.max_ctx < 1 || a.max_ctx > 1048576) return fail(DSA_ERR_UNSUPPORTED, "%s: max_ctx must be 1..1048576", who);
   if (a.max_pages < (a.max_ctx + DSA_PAGE_SIZE - 1) / DSA_PAGE_SIZE)
     return fail(DSA_ERR_INVALID_ARG, "%s: max_pages < ceil(max_ctx / 64)", who);
@@ -635,7 +636,7 @@ static int run_mass(const char* who, dsa::MassArgs& a, void* stream) {
 }
 
 size_t dsa_attn_mass_workspace_size(int32_t n_q, int32_t h_s, int32_t n_seq) {
-  return mass_sizes_ok(n_q, h_s) && n_seq >= 1 ? dsa::mass_workspace_bytes(n_q, h_s, n_seq) : 0;
+  return mass_sizes_ok(n_q, h_s) && n_seq >= 1 && n_seq <= 65536 ? dsa::mass_workspace_bytes(n_q, h_s, n_seq) : 0;
 }
 
 int dsa_attn_mass(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t* kv_cache, int64_t num_pages,
@@ -679,6 +680,7 @@ int dsa_evict_select(const int64_t* mass, int64_t mass_stride, const int32_t* se
   if (!mass || !seq_lens || !kept || !new_lens) return fail(DSA_ERR_INVALID_ARG, "evict_select: null pointer");
   if (!aligned(mass, 8) || !aligned(kept_mass, 8) || !aligned(seq_lens, 4) || !aligned(kept, 4) || !aligned(new_lens, 4))
     return fail(DSA_ERR_INVALID_ARG, "evict_select: a pointer is not aligned to its element");
+  if (new_lens == seq_lens) return fail(DSA_ERR_INVALID_ARG, "evict_select: new_lens must not be seq_lens");
   unsigned* st = status_ptr();
   if (!st) return fail(DSA_ERR_CUDA, "evict_select: no CUDA device");
   dsa::EvictSelectArgs a{mass, mass_stride, seq_lens, n_seq, max_ctx, budget, sinks, recent, kept, new_lens, kept_mass, st};
@@ -698,6 +700,8 @@ int dsa_evict_compact(const int32_t* kept, int32_t n_seq, int32_t budget, const 
   if (max_pages < 1 || num_pages < 1 || num_pages > INT64_MAX / 65536)
     return fail(DSA_ERR_INVALID_ARG, "evict_compact: max_pages and num_pages must be >= 1");
   if (n_seq == 0) return DSA_OK;
+  if (static_cast<int64_t>(n_seq) * budget > int64_t{1} << 35)
+    return fail(DSA_ERR_UNSUPPORTED, "evict_compact: n_seq * budget must be 2^35 at most");
   if (!kept || !page_table || (!k_cache && !kv_cache)) return fail(DSA_ERR_INVALID_ARG, "evict_compact: null pointer");
   const bool in_place = !dst_table || dst_table == page_table;
   if (in_place) {

@@ -26,7 +26,7 @@ class DsaDecodeLayer:
           weight, bias, norm, norm_dim and eps.  None: they come normed.
 
     What the cache's positions are worth to the attention can be added up (``mass`` of decode, step and attend_prefix,
-    int64 [n_seq, max_ctx], zero at first) and the least used ones given up (``evict``).  The records that
+    int64 [n_seq, max_ctx], zero at first, as wide as the longest sequence) and the least used ones given up (``evict``).  The records that
     stay move to the first positions of their sequence and keep the turns they have: from then on rope_pos, the
     positions to turn to, differ from q_pos, the places in the cache.
     """
@@ -137,6 +137,8 @@ class DsaDecodeLayer:
         positions (prefix_pages, read once for all rows), each row then over its own ones up to
         q_pos.  Returns (out bf16 [n_q, h_s, 512], lse fp32 [n_q, h_s]), new tensors each call.  rope_pos as for decode;
         to mass the weights of every position seen are added, for which page_table names the shared pages too."""
+        if mass is not None and page_table is None:
+            raise ValueError("attend_prefix: mass needs a page_table")
         if self.rope is not None:
             q_sfa = self._turn_latent(q_sfa, q_pos if rope_pos is None else rope_pos)
         lse = torch.empty(q_sfa.shape[0], self.h_s, dtype=torch.float32, device=self.device)
@@ -151,7 +153,8 @@ class DsaDecodeLayer:
         """Keep budget positions of each sequence: the first sinks, the last recent and those of the largest mass between
         (evict_select); move their records to the sequence's first positions, in place or to the pages of dst_table
         (evict_compact), and their mass with them; the rest of mass becomes 0.  Returns (kept int32 [n_seq, budget]: the
-        positions that stayed, -1 behind the last; new_lens int32 [n_seq]).  Pages behind the new lengths are free."""
+        positions that stayed, -1 behind the last; new_lens int32 [n_seq]).  Pages behind the new lengths are free.
+        In place, sequences must not share pages that are written."""
         kept, new_lens, kept_mass = evict_select(mass, seq_lens, budget, sinks=sinks, recent=recent)
         evict_compact(kept, page_table, self.k_cache, self.kv_cache, dst_table)
         n = min(budget, mass.shape[1])  # (what would lie further is empty)

@@ -448,7 +448,7 @@ int dsa_prefix_attn(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t*
  * none either (NaN in out_weights); both flag DSA_STATUS_NAN_SCORE.  An lse of -inf (a row that saw nothing)
  * adds nothing.  Rows whose sequence or length is out of range add nothing and flag DSA_STATUS_BAD_SEQ or
  * _BAD_LEN; positions whose page is out of range have no weight and flag DSA_STATUS_BAD_PAGE.
- *   q_bf16      [n_q][h_s][576] bfloat16, 16-byte aligned; n_q up to 65536, h_s 1..128.
+ *   q_bf16      [n_q][h_s][576] bfloat16, 16-byte aligned; n_q and n_seq up to 65536, h_s 1..128.
  *   kv_cache .. q_seq   as for dsa_prefix_attn; num_pages up to 2^25; page_table rows from position 0 on.
  *   max_ctx     host-side bound of seq_lens, 1..1048576; max_pages >= ceil(max_ctx / 64).
  *   lse         [n_q][h_s] fp32, natural log.

@@ -397,7 +397,7 @@ def _p(v):
     (dict(cache=None), -1), (dict(table=None), -1), (dict(lens=None), -1), (dict(q_seq=None), -1), (dict(lse=None), -1),
     (dict(pick=None), -1), (dict(mass=None, out=None), -1), (dict(ws=None), -1), (dict(ws_bytes=100), -1),
     (dict(ws=9 + 2.0 ** -9), -1), (dict(q=1 + 2.0 ** -13), -1), (dict(mass=7 + 2.0 ** -14), -1), (dict(lse=6 + 2.0 ** -15), -1),
-    (dict(n_q=0, q=None), 0)])
+    (dict(n_seq=65537), -2), (dict(n_q=0, q=None), 0)])
 def test_refusals(dsa, sparse, kw, code):
     a = dict(q=1, n_q=4, h=16, cache=2, pages=20, table=3, max_pages=4, lens=4, n_seq=2, q_seq=5, pick=10, topk=8, ctx=200, sm=SM,
              lse=6, mass=7, stride=200, out=8, ws=9, ws_bytes=1 << 30)

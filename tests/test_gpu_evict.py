@@ -212,7 +212,7 @@ def _p(v):
     (dict(n=-1), -1), (dict(ctx=0), -2), (dict(ctx=1 << 21), -2), (dict(budget=0), -2), (dict(budget=1 << 21), -2),
     (dict(sinks=-1), -1), (dict(recent=-1), -1), (dict(sinks=5, recent=6), -1), (dict(stride=99), -1), (dict(stride=1 << 40), -1),
     (dict(mass=None), -1), (dict(lens=None), -1), (dict(kept=None), -1), (dict(new=None), -1), (dict(mass=1 + 2.0 ** -14), -1),
-    (dict(weights=5 + 2.0 ** -14), -1), (dict(kept=3 + 2.0 ** -15), -1), (dict(n=1 << 28), -2), (dict(n=0, mass=None), 0)])
+    (dict(weights=5 + 2.0 ** -14), -1), (dict(kept=3 + 2.0 ** -15), -1), (dict(n=1 << 28), -2), (dict(new=2), -1), (dict(n=0, mass=None), 0)])
 def test_select_refusals(dsa, kw, code):
     a = dict(mass=1, stride=100, lens=2, n=3, ctx=100, budget=10, sinks=2, recent=3, kept=3, new=4, weights=5)
     a.update(kw)
@@ -224,7 +224,7 @@ def test_select_refusals(dsa, kw, code):
     (dict(n=-1), -1), (dict(budget=0), -2), (dict(max_pages=0), -1), (dict(pages=0), -1), (dict(kept=None), -1),
     (dict(table=None), -1), (dict(k=None, kv=None), -1), (dict(dst=2, dst_pages=9), -1), (dict(dst=3, dst_pages=1), -1),
     (dict(max_pages=1), -1), (dict(kept=1 + 2.0 ** -15), -1), (dict(kv=5 + 2.0 ** -13), -1), (dict(ws=None), -1),
-    (dict(ws_bytes=1000), -1), (dict(ws=6 + 2.0 ** -9), -1), (dict(n=0, kept=None), 0)])
+    (dict(ws_bytes=1000), -1), (dict(ws=6 + 2.0 ** -9), -1), (dict(n=1 << 26, budget=1024, max_pages=64), -2), (dict(n=0, kept=None), 0)])
 def test_compact_refusals(dsa, kw, code):
     a = dict(kept=1, n=3, budget=100, table=2, max_pages=8, dst=None, dst_pages=0, k=4, kv=5, pages=20, ws=6, ws_bytes=1 << 30)
     a.update(kw)

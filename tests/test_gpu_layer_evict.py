@@ -247,3 +247,6 @@ def test_refusals():
                dict(rope=turns, index_norm={"k_weight": None})):
         with pytest.raises(ValueError):
             DsaDecodeLayer(1, H_I, H_S, TOPK, SM, device="cpu", **kw)
+    with pytest.raises(ValueError):
+        DsaDecodeLayer(1, H_I, H_S, TOPK, SM, device="cpu").attend_prefix(
+            torch.zeros(1, H_S, 576), torch.zeros(1, dtype=torch.int32), 5, None, None, None, None, 5, mass=torch.zeros(1, 5))
