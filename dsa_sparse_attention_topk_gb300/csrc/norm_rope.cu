@@ -7,16 +7,18 @@
 // mean is taken off before anything is squared, so that a row far from zero loses nothing.
 //
 // Bound: memory, each value read and written once.  A row stays in the registers of 8 to 32 lanes between the
-// sums and the turn, 8 to 32 values a lane.  4096 x 64 x 128 bf16 take 29.6 us, 4.5 TB/s (a plain copy 20): the
-// rest is issue, 337 instructions a warp of four rows, and one wave's start and end.
+// sums and the turn, 8 to 32 values a lane.  4096 x 64 x 128 bf16 take 27 us, 5 TB/s (a plain copy 20, this kernel
+// without weights, sums and turn 22.5): the rest is issue and the tables' way through shared memory.
 
 #include "norm_rope.cuh"
 
 namespace dsa {
 namespace {
 
-// blocks on an SM together, by the registers that a lane's elements take
-template <int E> constexpr int kBlocksSm = E <= 16 ? 4 : E <= 24 ? 3 : 2;
+// blocks on an SM together, by the registers that a lane's elements take; up to 16 of them leave room for the
+// weights (rows of 128, three blocks: 26.9 us; four and the weights from shared memory 28.0)
+template <int E> constexpr int kBlocksSm = E <= 8 ? 4 : E <= 24 ? 3 : 2;
+template <int E> constexpr bool kKeepWeights = E <= 16;
 
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(kNormThreads, kBlocksSm<V * NV>)
@@ -27,29 +29,41 @@ norm_rope_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
   pdl_wait();
   NormShared sh = norm_shared(a, g, raw);
   const int lane = threadIdx.x & (g.lanes - 1), grp = threadIdx.x / g.lanes;
+  const int first = norm_first<NV>(g, lane);
   float* ex = sh.ex + grp * a.rot;
   const int64_t rows = static_cast<int64_t>(a.n) * a.h;
   const int64_t begin = blockIdx.x * rows_block, end = min(begin + rows_block, rows);
   const float inv_span = 1.0f / static_cast<float>(a.span);
   RowAt at(min(begin + grp, rows - 1), a.h), next = at;
-  RowPtr<const T> src(static_cast<const T*>(a.x) + lane * V, at, g, a.h, a.x_stride_t, a.x_stride_h);
-  RowPtr<T> dst(static_cast<T*>(a.out) + lane * V, at, g, a.h, a.out_stride_t, a.out_stride_h);
+  RowPtr<const T> src(static_cast<const T*>(a.x) + first * V, at, g, a.h, a.x_stride_t, a.x_stride_h);
+  RowPtr<T> dst(static_cast<T*>(a.out) + first * V, at, g, a.h, a.out_stride_t, a.out_stride_h);
   bool there[NV], normed[NV];  // (a vector is normed as a whole or not at all: V divides span)
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    there[j] = j * g.lanes + lane < g.vectors;
-    normed[j] = (j * g.lanes + lane) * V < a.span;
+    there[j] = first + j * g.part < g.vectors;
+    normed[j] = (first + j * g.part) * V < a.span;
   }
   Vec<T, V> x[NV];  // the row at hand, then the next one
   auto load = [&](bool live) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (live && there[j]) x[j].u = *reinterpret_cast<const W*>(src.p + j * g.lanes * V);
+      if (live && there[j]) x[j].u = *reinterpret_cast<const W*>(src.p + j * g.part * V);
       else x[j].u = W{};
     src.step(next.step(g, a.h));
   };
   load(begin + grp < end);
-  norm_fill_params(a, sh);
+  norm_fill_params<V>(a, g, sh);
+  float kept[kKeepWeights<NV * V> ? NV * V : 1];
+  if constexpr (kKeepWeights<NV * V>) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float w[V];
+      load_params(g, sh.weight, min((first + j * g.part) * V, a.span - V), w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) kept[j * V + i] = w[i];
+    }
+  }
   for (int64_t r0 = begin; r0 < end; r0 += g.rows_step) {
     const bool live = r0 + grp < end;
     float y[NV * V];
@@ -79,31 +93,36 @@ norm_rope_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (normed[j]) {
-        const int e0 = (j * g.lanes + lane) * V;
+        const int e0 = (first + j * g.part) * V;
         scale_all<V>(y + j * V, r);
         if (a.weight) {
-          float w[V];
-          load_floats(sh.weight + e0, w);
-          scale_by<V>(y + j * V, w);
+          if constexpr (kKeepWeights<NV * V>) {
+            scale_by<V>(y + j * V, kept + j * V);
+          } else {
+            float w[V];
+            load_params(g, sh.weight, e0, w);
+            scale_by<V>(y + j * V, w);
+          }
         }
         if (a.bias) {
           float b[V];
-          load_floats(sh.bias + e0, b);
+          load_params(g, sh.bias, e0, b);
 #pragma unroll
           for (int i = 0; i < V; ++i) y[j * V + i] += b[i];
         }
       }
-    turn_row<V, NV, false>(a, g, y, sh.cs + (live ? at.t - sh.first : 0) * ((a.rot / 2 + 1) & ~1), ex, lane);
+    turn_row<V, NV, false>(a, g, y, sh.cs + (live ? at.t - sh.first : 0) * ((a.rot / 2 + 1) & ~1), ex, lane, first);
     if (live)
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (there[j]) *reinterpret_cast<W*>(dst.p + j * g.lanes * V) = narrow<T, V>(y + j * V).u;
+        if (there[j]) *reinterpret_cast<W*>(dst.p + j * g.part * V) = narrow<T, V>(y + j * V).u;
     dst.step(at.step(g, a.h));
   }
 }
 
 template <typename T, int V, int NV>
 cudaError_t launch_fwd(const NormArgs& a, NormGeom g, cudaStream_t s) {
+  norm_pairs<V, NV>(a, g, sizeof(T));
   const int64_t steps = (static_cast<int64_t>(a.n) * a.h + g.rows_step - 1) / g.rows_step;
   // one wave: a block's start, two round trips to memory, is then paid once (4096 x 64 x 128: 38 us with four)
   const int64_t most = static_cast<int64_t>(multiprocessors()) * kBlocksSm<V * NV>;

@@ -2,7 +2,9 @@
 // rows of a call are laid over lanes, the tables of a block, and the turn of a row's rotary part.
 //
 // A row is one head of one token.  A group of G lanes holds a whole row in registers, vector
-// j G + lane of it in lane `lane`'s j-th word, so that it is read once however often it is summed over.
+// first + j part of it in a lane's j-th word, so that it is read once however often it is summed over.  Ordinarily
+// first is the lane and part is G; where the layout turns vectors of 16 bytes half a rotary part of 2^k of them
+// apart, part is that distance and a lane holds both of a pair (norm_pairs).
 // With vectors of 16 bytes eight lanes cover 128 consecutive bytes, as much as a memory request wants,
 // and a warp has four rows under way; longer rows take 16 or 32 lanes so that a lane holds at most 32
 // elements in fp32.
@@ -29,6 +31,8 @@ struct NormGeom {
   int tokens_table;   // tokens that those can touch
   int step_t, step_h; // rows_step as whole tokens and heads
   int span_pad;       // norm_dim rounded up to 4, floats of the weights' table
+  int part;           // vectors between a lane's words
+  int pair_word, pair_block;  // the word whose pairs are in the next, and the block of `part` lanes that has them; -1: none
   int turn_word;      // the word of the lanes that is the whole rotary part, -1: there is none
 };
 
@@ -59,10 +63,18 @@ __device__ __forceinline__ NormShared norm_shared(const NormArgs& a, const NormG
   s.rows_end = 0;
   return s;
 }
-__device__ __forceinline__ void norm_fill_params(const NormArgs& a, const NormShared& s) {
+// Where the tables have dim e: vectors of eight in two halves, so that eight lanes read 128 bytes next to one another (from
+// vectors as they are, every second bank twice, 4096 x 64 rows of 128 took 28.9 us instead of 28.0).
+template <int V>
+__device__ __forceinline__ int norm_param_at(const NormGeom& g, int e) {
+  return V == 8 ? (e & 4 ? g.span_pad >> 1 : 0) + (e >> 3) * 4 + (e & 3) : e;
+}
+template <int V>
+__device__ __forceinline__ void norm_fill_params(const NormArgs& a, const NormGeom& g, const NormShared& s) {
   for (int i = threadIdx.x; i < a.span; i += kNormThreads) {
-    s.weight[i] = a.weight ? norm_param(a.weight, a.w_dtype, i) : 1.f;
-    s.bias[i] = a.bias ? norm_param(a.bias, a.w_dtype, i) : 0.f;
+    const int at = norm_param_at<V>(g, i);
+    s.weight[at] = a.weight ? norm_param(a.weight, a.w_dtype, i) : 1.f;
+    s.bias[at] = a.bias ? norm_param(a.bias, a.w_dtype, i) : 0.f;
   }
 }
 // the sines of the tokens of the rows from r0 on, as many as the table holds; every thread of the block calls it, and it
@@ -76,7 +88,14 @@ __device__ __forceinline__ void norm_fill_cs(const NormArgs& a, const NormGeom& 
   const int half = a.rot >> 1, pitch = (half + 1) & ~1, count = (last - s.first + 1) * half;
   for (int i = threadIdx.x; i < count; i += kNormThreads) {
     const int t = i / half, f = i - t * half;
-    s.cs[t * pitch + f] = phase_cs(a.pos[s.first + t], a.turns[f], a.amplitude);
+    const float2 v = phase_cs(a.pos[s.first + t], a.turns[f], a.amplitude);
+    if (g.pair_word >= 0) {  // a token's cosines, then its sines
+      float* to = reinterpret_cast<float*>(s.cs + t * pitch);
+      to[f] = v.x;
+      to[half + f] = v.y;
+    } else {
+      s.cs[t * pitch + f] = v;
+    }
   }
   __syncthreads();
 }
@@ -217,21 +236,59 @@ __device__ __forceinline__ void load_floats(const float* p, float (&v)[V]) {
     for (int i = 0; i < V; ++i) v[i] = p[i];
   }
 }
+// the V weights or biases from dim e0 on
+template <int V>
+__device__ __forceinline__ void load_params(const NormGeom& g, const float* table, int e0, float (&v)[V]) {
+  if constexpr (V == 8) {
+    float lo[4], hi[4];
+    load_floats(table + (e0 >> 1), lo);
+    load_floats(table + (g.span_pad >> 1) + (e0 >> 1), hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = lo[i];
+      v[4 + i] = hi[i];
+    }
+  } else {
+    load_floats(table + e0, v);
+  }
+}
 
 // Turn the rotary part of the row in y (fp32, in the lanes' layout); TRANSPOSE turns back.  Pairs of neighbours
-// lie in one vector.  A partner half a rotary part away comes by shuffle where the whole rotary part is one word of the
+// lie in one vector, and a partner half a rotary part away in the same lane where norm_pairs could place it there.
+// Elsewhere it comes by shuffle where the whole rotary part is one word of the
 // lanes (g.turn_word: as many pairs as one exchange can carry); otherwise, and with vectors of one element, through
 // shared memory, ex: the row's own rot floats there.
 template <int V, int NV, bool TRANSPOSE>
 __device__ __forceinline__ void turn_row(const NormArgs& a, const NormGeom& g, float (&y)[NV * V], const float2* cs,
-                                         float* ex, int lane) {
+                                         float* ex, int lane, int first) {
   const bool half_layout = a.layout == DSA_ROPE_HALF;
   const int half = a.rot >> 1;
-  if (V > 1 && half_layout && g.turn_word >= 0) {
+  if (V >= 4 && NV > 1 && g.pair_word >= 0) {
+    const int at = lane & (g.part - 1);
+    if ((lane - at) != g.pair_block * g.part) return;
+    float c[V], s[V];
+    load_floats(reinterpret_cast<const float*>(cs) + at * V, c);
+    load_floats(reinterpret_cast<const float*>(cs) + half + at * V, s);
+#pragma unroll
+    for (int j = 0; j + 1 < NV; ++j) {
+      if (j != g.pair_word) continue;  // (the same in all threads)
+#pragma unroll
+      for (int i = 0; i + 1 < V; i += 2) {
+        float *p = y + j * V + i, *q = p + V;
+        const float2 x0 = make_float2(p[0], p[1]), x1 = make_float2(q[0], q[1]), co = make_float2(c[i], c[i + 1]);
+        const float2 plus = TRANSPOSE ? make_float2(-s[i], -s[i + 1]) : make_float2(s[i], s[i + 1]);
+        const float2 z0 = fma2(x1, make_float2(-plus.x, -plus.y), mul2(x0, co)), z1 = fma2(x0, plus, mul2(x1, co));
+        p[0] = z0.x;
+        p[1] = z0.y;
+        q[0] = z1.x;
+        q[1] = z1.y;
+      }
+    }
+  } else if (V > 1 && half_layout && g.turn_word >= 0) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (j != g.turn_word) continue;  // (the same in all threads)
-      const int rel = (j * g.lanes + lane) * V - a.offset;
+      const int rel = (first + j * g.part) * V - a.offset;
       const bool mine = rel >= 0 && rel < a.rot, second = rel >= half;
       const int from = (threadIdx.x & 31) + (second ? -half / V : half / V);
       // the first of a pair becomes a c - b s, the second b c + a s: the one that sends gives the sign
@@ -257,7 +314,7 @@ __device__ __forceinline__ void turn_row(const NormArgs& a, const NormGeom& g, f
     __syncwarp();  // (the row before has been read)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int rel = (j * g.lanes + lane) * V - a.offset;
+      const int rel = (first + j * g.part) * V - a.offset;
       if (rel >= 0 && rel < a.rot) {
 #pragma unroll
         for (int i = 0; i < V; ++i) ex[rel + i] = y[j * V + i];
@@ -266,7 +323,7 @@ __device__ __forceinline__ void turn_row(const NormArgs& a, const NormGeom& g, f
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int rel = (j * g.lanes + lane) * V - a.offset;
+      const int rel = (first + j * g.part) * V - a.offset;
       if (rel >= 0 && rel < a.rot) {
         const bool second = half_layout ? rel >= half : rel & 1;
         const int f = half_layout ? (second ? rel - half : rel) : rel >> 1;
@@ -282,7 +339,7 @@ __device__ __forceinline__ void turn_row(const NormArgs& a, const NormGeom& g, f
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int rel = (j * g.lanes + lane) * V - a.offset;
+      const int rel = (first + j * g.part) * V - a.offset;
       if (rel >= 0 && rel < a.rot) {
         float c[V];
         load_floats(reinterpret_cast<const float*>(cs + (rel >> 1)), c);
@@ -312,8 +369,31 @@ inline NormGeom norm_geom(const NormArgs& a, int v, int size) {
   g.step_h = g.rows_step % a.h;
   g.span_pad = (a.span + 3) & ~3;
   const int first = a.offset / v, last = (a.offset + a.rot) / v - 1;  // (V divides both in the half layout)
+  g.part = g.lanes;
+  g.pair_word = g.pair_block = -1;
   g.turn_word = v > 1 && first / g.lanes == last / g.lanes ? first / g.lanes : -1;
   return g;
+}
+// Whether a lane can hold both of a pair: vectors half a rotary part apart then are its words j and j + 1.  (Rows of 128 with
+// 64 turned, 4096 x 64 bf16: 28.9 us, by shuffle 29.6.)  Vectors of 16 bytes alone, two next to one another, so that no
+// sector of memory is asked for twice.
+template <int V, int NV>
+void norm_pairs(const NormArgs& a, NormGeom& g, int size) {
+  const int apart = a.rot / 2 / V;
+  if (V * size != 16 || a.layout != DSA_ROPE_HALF || (a.rot / 2) % V || apart < 2 || apart > g.lanes || (apart & (apart - 1)) ||
+      (g.vectors + g.lanes - 1) / g.lanes != NV || a.offset / V % apart)
+    return;
+  const int word = a.offset / V / apart % NV;
+  if (word + 1 >= NV) return;
+  g.part = apart;
+  g.pair_word = word;
+  g.pair_block = a.offset / V / apart / NV;
+}
+// a lane's first vector
+template <int NV>
+__device__ __forceinline__ int norm_first(const NormGeom& g, int lane) {
+  const int at = lane & (g.part - 1);
+  return (lane - at) * NV + at;
 }
 // The table holds the sines of one step's tokens at least; of a block's whole share where that takes 16 KB at most.
 inline void norm_table(const NormArgs& a, NormGeom& g, int64_t rows_block) {
@@ -325,7 +405,7 @@ inline void norm_table(const NormArgs& a, NormGeom& g, int64_t rows_block) {
   g.tokens_table = static_cast<int>(tokens(rows));
 }
 inline size_t norm_shared_bytes(const NormArgs& a, const NormGeom& g) {
-  const bool exchange = !(a.layout == DSA_ROPE_HALF ? g.turn_word >= 0 : g.vectors < a.d);  // (see turn_row)
+  const bool exchange = !(a.layout == DSA_ROPE_HALF ? g.turn_word >= 0 || g.pair_word >= 0 : g.vectors < a.d);  // (see turn_row)
   return 2 * sizeof(float) * g.span_pad + sizeof(float2) * g.tokens_table * ((a.rot / 2 + 1) & ~1) +
          (exchange ? sizeof(float) * g.rows_step * a.rot : 0);
 }

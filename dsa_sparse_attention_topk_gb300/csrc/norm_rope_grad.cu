@@ -28,6 +28,7 @@ norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
   pdl_wait();
   NormShared sh = norm_shared(a, g, raw);
   const int lane = threadIdx.x & (g.lanes - 1), grp = threadIdx.x / g.lanes;
+  const int first = norm_first<NV>(g, lane);
   float* ex = sh.ex + grp * a.rot;
   const int64_t rows = static_cast<int64_t>(a.n) * a.h;
   const int64_t begin = blockIdx.x * rows_block, end = min(begin + rows_block, rows);
@@ -39,22 +40,22 @@ norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
     if (SHIFT) db[i] = 0.f;
   }
   RowAt at(min(begin + grp, rows - 1), a.h), next = at;
-  RowPtr<const T> xs(static_cast<const T*>(a.x) + lane * V, at, g, a.h, a.x_stride_t, a.x_stride_h);
-  RowPtr<const T> ys(static_cast<const T*>(a.dy) + lane * V, at, g, a.h, a.dy_stride_t, a.dy_stride_h);
-  RowPtr<T> dst(static_cast<T*>(a.out) + lane * V, at, g, a.h, a.out_stride_t, a.out_stride_h);
+  RowPtr<const T> xs(static_cast<const T*>(a.x) + first * V, at, g, a.h, a.x_stride_t, a.x_stride_h);
+  RowPtr<const T> ys(static_cast<const T*>(a.dy) + first * V, at, g, a.h, a.dy_stride_t, a.dy_stride_h);
+  RowPtr<T> dst(static_cast<T*>(a.out) + first * V, at, g, a.h, a.out_stride_t, a.out_stride_h);
   bool there[NV], normed[NV];  // (a vector is normed as a whole or not at all: V divides span)
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    there[j] = j * g.lanes + lane < g.vectors;
-    normed[j] = (j * g.lanes + lane) * V < a.span;
+    there[j] = first + j * g.part < g.vectors;
+    normed[j] = (first + j * g.part) * V < a.span;
   }
   Vec<T, V> p[NV], q[NV];  // x and dy of the row at hand, then of the next one
   auto load = [&](bool live) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (live && there[j]) {
-        p[j].u = *reinterpret_cast<const W*>(xs.p + j * g.lanes * V);
-        q[j].u = *reinterpret_cast<const W*>(ys.p + j * g.lanes * V);
+        p[j].u = *reinterpret_cast<const W*>(xs.p + j * g.part * V);
+        q[j].u = *reinterpret_cast<const W*>(ys.p + j * g.part * V);
       } else {
         p[j].u = W{};
         q[j].u = W{};
@@ -65,7 +66,7 @@ norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
     ys.step(wrap);
   };
   load(begin + grp < end);
-  norm_fill_params(a, sh);
+  norm_fill_params<V>(a, g, sh);
   for (int64_t r0 = begin; r0 < end; r0 += g.rows_step) {
     const bool live = r0 + grp < end;
     float u[NV * V], d[NV * V];
@@ -76,7 +77,7 @@ norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
     }
     load(r0 + g.rows_step + grp < end);
     norm_fill_cs(a, g, sh, r0, end);
-    turn_row<V, NV, true>(a, g, d, sh.cs + (live ? at.t - sh.first : 0) * ((a.rot / 2 + 1) & ~1), ex, lane);
+    turn_row<V, NV, true>(a, g, d, sh.cs + (live ? at.t - sh.first : 0) * ((a.rot / 2 + 1) & ~1), ex, lane, first);
     if (a.center) {
       float s = 0.f;
 #pragma unroll
@@ -111,7 +112,7 @@ norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
         }
         if (a.weight) {
           float w[V];
-          load_floats(sh.weight + (j * g.lanes + lane) * V, w);
+          load_params(g, sh.weight, (first + j * g.part) * V, w);
           scale_by<V>(d + j * V, w);
         }
         add_products<V>(c1, d + j * V, u + j * V);
@@ -140,7 +141,7 @@ norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
           }
           scale_all<V>(d + j * V, r);
         }
-        if (there[j]) *reinterpret_cast<W*>(dst.p + j * g.lanes * V) = narrow<T, V>(d + j * V).u;
+        if (there[j]) *reinterpret_cast<W*>(dst.p + j * g.part * V) = narrow<T, V>(d + j * V).u;
       }
     dst.step(at.step(g, a.h));
   }
@@ -156,7 +157,7 @@ norm_rope_grad_kernel(NormArgs a, NormGeom g, int64_t rows_block) {
       dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], o);
       if (SHIFT) db[k] += __shfl_xor_sync(0xffffffffu, db[k], o);
     }
-    const int e = ((k / V) * g.lanes + lane) * V + k % V;
+    const int e = (first + (k / V) * g.part) * V + k % V;
     if (in_warp < g.lanes && e < a.span) {
       sums[warp * a.span + e] = dw[k];
       if (SHIFT) sums[(kWarps + warp) * a.span + e] = db[k];
@@ -197,6 +198,7 @@ norm_grad_sum_kernel(const float* part, int blocks, int span, int kinds, float* 
 
 template <typename T, int V, int NV, bool SHIFT>
 cudaError_t launch_bwd_k(const NormArgs& a, NormGeom g, cudaStream_t s) {
+  norm_pairs<V, NV>(a, g, sizeof(T));
   const int64_t steps = (static_cast<int64_t>(a.n) * a.h + g.rows_step - 1) / g.rows_step;
   const int64_t most = std::min<int64_t>(static_cast<int64_t>(multiprocessors()) * kBlocksSm, kMostBlocks);
   const int64_t per = (steps + most - 1) / most;

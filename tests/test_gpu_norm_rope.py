@@ -130,6 +130,9 @@ CASES = [
     (3, 2, 2, 1, 2, 0, "half", "rms", torch.float32, torch.float32, 0),
     (300, 3, 256, 256, 64, 192, "half", "rms", torch.bfloat16, torch.float32, 0),
     (2, 1, 514, 514, 64, 0, "half", "layer", torch.float16, torch.float32, 0),
+    (6, 5, 256, 256, 64, 96, "half", "rms", torch.bfloat16, torch.float32, 0),
+    (9, 4, 192, 128, 64, 128, "half", "layer", torch.float16, torch.float32, 8),
+    (7, 3, 320, 320, 32, 288, "half", "rms", torch.bfloat16, torch.bfloat16, 0),
 ]
 IDS = ["-".join(str(v).replace("torch.", "") for v in c) for c in CASES]
 
