@@ -92,7 +92,7 @@ struct MassWs {
   __half* q;         // [columns][576], times a power of two per column
   float4* cols;      // per column: logit per product (log2 units), -lse, positions it sees (int)
   int4* groups;      // positions or entries, first column, columns, sequence
-  int* rank;         // dense: place of a row in the order of sequences, -1: none
+  int* rank;         // dense: place of a row in the order of sequences
 };
 
 // ---- queries, columns and groups ---------------------------------------------------------
@@ -113,8 +113,8 @@ __device__ __forceinline__ int row_limit(const MassArgs& a, int t, bool report) 
   return pos < 0 ? 0 : min(pos, len - 1) + 1;
 }
 
-// Dense: rows in the order of their sequences.  A thread per row counts the rows before it, a thread per
-// sequence its rows and the furthest position they see.
+// Dense: rows in the order of their sequences, those that see nothing behind the last.  A thread per row counts the
+// rows before it, a thread per sequence its rows and the furthest position they see.
 __global__ void __launch_bounds__(256)
 mass_order_kernel(MassArgs a, MassWs ws) {
   __shared__ int s_seq[1024], s_limit[1024];
@@ -122,9 +122,8 @@ mass_order_kernel(MassArgs a, MassWs ws) {
   pdl_wait();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const bool is_row = i < a.n_q, is_group = !is_row && i < static_cast<int64_t>(a.n_q) + a.n_seq;
-  // (a row that sees nothing has no place)
   const bool live = is_row && row_limit(a, static_cast<int>(i), true) > 0;
-  const int seq = is_row ? (live ? a.q_seq[i] : -1) : static_cast<int>(i - a.n_q);
+  const int seq = is_row ? (live ? a.q_seq[i] : INT32_MAX) : static_cast<int>(i - a.n_q);
   int before = 0, own = 0, furthest = 0;
   for (int t0 = 0; t0 < a.n_q; t0 += 1024) {
     __syncthreads();
@@ -144,12 +143,13 @@ mass_order_kernel(MassArgs a, MassWs ws) {
       }
     }
   }
-  if (is_row) ws.rank[i] = live ? before : -1;
+  if (is_row) ws.rank[i] = before;
   if (is_group) ws.groups[seq] = make_int4(furthest, before * a.h_s, own * a.h_s, seq);
 }
 
 // One warp per (row, head): the query as fp16 with its largest value in [2^14, 2^15), and the column's constants.
-// A head whose query or lse is NaN (or its query infinite) gets zeros and weight 0.
+// A head whose query or lse is NaN (or its query infinite) gets zeros and weight 0; zeros too the heads of a dense row that
+// sees nothing: the last sequence's last chunk reads on into them, and what lies there has to be numbers.
 __global__ void __launch_bounds__(256)
 mass_query_kernel(MassArgs a, MassWs ws) {
   __shared__ int s_last[8];
@@ -174,7 +174,7 @@ mass_query_kernel(MassArgs a, MassWs ws) {
   }
   if (h >= a.h_s) return;
   const int rank = a.idx ? t : ws.rank[t];
-  if (rank < 0) return;
+  const int limit = a.idx ? 0 : row_limit(a, t, false);
   const int64_t from = static_cast<int64_t>(t) * a.h_s + h, to = static_cast<int64_t>(rank) * a.h_s + h;
   const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) + from * kLatent);
   uint32_t raw[kBlocks];
@@ -186,7 +186,7 @@ mass_query_kernel(MassArgs a, MassWs ws) {
   }
   top = __reduce_max_sync(0xffffffffu, top);   // bf16 bits order like the values
   const float lse = a.lse[from];
-  const bool dead = top >= 0x7F80u || lse != lse;
+  const bool unseen = !a.idx && limit == 0, dead = unseen || top >= 0x7F80u || lse != lse;
   // largest in [2^14, 2^15); a subnormal largest counts as the smallest normal one.  The factor in two powers of two
   const int k = 14 + 127 - max(static_cast<int>(top >> 7), 1);
   const float f0 = exp2i(k / 2), f1 = exp2i(k - k / 2);
@@ -198,11 +198,11 @@ mass_query_kernel(MassArgs a, MassWs ws) {
     dst[32 * i + lane] = *reinterpret_cast<const uint32_t*>(&v);
   }
   if (lane == 0) {
-    if (dead) flag(a.status, DSA_STATUS_NAN_SCORE);
+    if (dead && !unseen) flag(a.status, DSA_STATUS_NAN_SCORE);
     const float c = a.sm_scale * 1.4426950408889634f;
     const bool none = dead || lse == -INFINITY;
     ws.cols[to] = make_float4(dead ? 0.f : c * (1.0f / f0) * (1.0f / f1), none ? -INFINITY : -lse * 1.4426950408889634f,
-                              __int_as_float(a.idx ? 0 : row_limit(a, t, false)), 0.f);
+                              __int_as_float(limit), 0.f);
   }
 }
 
