@@ -9,6 +9,8 @@
 // a bf16 query times a power of two per (row, head), but for what lies 2^39 below its largest value.  So the tensor
 // cores multiply codes, each tile into an accumulator of its own, and the scales are applied to those in fp32:
 // a logit is off by fp32 roundings alone, where rounding kv to 16 bits first would put the weights off by a percent.
+// A product of codes and queries is below 2^34, so that scales from 2^60 on could take a sum out of fp32 whose logit is
+// within it: such a position's are held 2^-64 as large, and the factor is put back behind the column's (kLift).
 //
 // Sums in fixed point.  A position's rows are worked on by several CTAs, and its weight is added up over calls.
 // m holds whole numbers of 2^-36 and takes additions atomically: integers add up the same in any order, so equal
@@ -49,6 +51,8 @@ __host__ __device__ constexpr int piece_at(int s) { return s == 0 ? 4 * kPiece :
 constexpr int kWarpB = 0, kWarpMma0 = 1, kWarpRec = 3, kWarpConv0 = 4, kWarpEpi0 = 8;  // (products: 1 and 2)
 constexpr float kMassOne = 68719476736.0f;        // 2^36
 constexpr float kMassMost = 67108864.0f;          // 2^26: one addition's limit
+constexpr float kLarge = 1152921504606846976.0f;  // 2^60: a position with such a scale
+constexpr float kLift = 18446744073709551616.0f;  // has them 2^-64 as large
 
 // What the columns of a chunk decide.
 template <int N> struct Shape {
@@ -187,8 +191,9 @@ mass_query_kernel(MassArgs a, MassWs ws) {
   top = __reduce_max_sync(0xffffffffu, top);   // bf16 bits order like the values
   const float lse = a.lse[from];
   const bool unseen = !a.idx && limit == 0, dead = unseen || top >= 0x7F80u || lse != lse;
-  // largest in [2^14, 2^15); a subnormal largest counts as the smallest normal one.  The factor in two powers of two
-  const int k = 14 + 127 - max(static_cast<int>(top >> 7), 1);
+  // largest in [2^14, 2^15), or the factor 2^109, which makes the smallest bf16 the smallest fp16: beyond it nothing is
+  // gained, and the column's own factor would leave the normal range.  In two powers of two
+  const int k = min(14 + 127 - max(static_cast<int>(top >> 7), 1), 109);
   const float f0 = exp2i(k / 2), f1 = exp2i(k - k / 2);
   uint32_t* dst = reinterpret_cast<uint32_t*>(ws.q + to * kLatent);
 #pragma unroll
@@ -340,6 +345,18 @@ __device__ __forceinline__ void add_mass(const MassArgs& a, int b, int pos, floa
   else if (total > 0.f)
     atomicAdd(reinterpret_cast<unsigned long long*>(a.mass + static_cast<int64_t>(b) * a.mass_stride + pos),
               static_cast<unsigned long long>(__float2ll_rn(fminf(total, kMassMost) * kMassOne)));
+}
+
+// The sum of a lane's weights where one of the warp's positions has large scales: columns without weight are left out, as their
+// products here may be no numbers.  (Out of line and rolled up: in line it took the entries' kernel 4% of its time.)
+__device__ __noinline__ float sum_lifted(const float* acc, int columns, const float* cols, const int* limits, int pos, float lift) {
+  float total = acc[0] != acc[0] ? NAN : 0.f;  // (the position's values: every column's, or none's)
+#pragma unroll 1
+  for (int i = 0; i < columns; ++i) {
+    const float* k = cols + 4 * (i >> 1) + (i & 1);
+    if (pos < limits[i]) total += ex2(fmaf(acc[i] * k[0], lift, k[2]));
+  }
+  return total;
 }
 
 template <bool SPARSE, int N>
@@ -511,7 +528,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           if (at >= N) continue;
           pairs[4 * (at >> 1) + (at & 1)] = info[i].x;
           pairs[4 * (at >> 1) + 2 + (at & 1)] = info[i].y;
-          limits[at] = __float_as_int(info[i].z);
+          limits[at] = info[i].y == -INFINITY ? 0 : SPARSE ? INT32_MAX : __float_as_int(info[i].z);
         }
         if (lane == 0) ctl.all_seen[buf] = SPARSE || least >= (w.tile + 1) * kTile;
         __syncwarp();
@@ -677,12 +694,22 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             info[2] = four.z;
             info[3] = four.w;
             info[4] = *reinterpret_cast<const uint32_t*>(mine + 80);
+            float most = 0.f;
 #pragma unroll
-            for (int i = 0; i < 5; ++i) fine = fine && fabsf(__uint_as_float(info[i])) * 448.0f < INFINITY;
+            for (int i = 0; i < 5; ++i) {
+              const float scale = fabsf(__uint_as_float(info[i]));
+              fine = fine && scale * 448.0f < INFINITY;
+              most = fmaxf(most, scale);
+            }
+            if (most >= kLarge)
+#pragma unroll
+              for (int i = 0; i < 5; ++i) info[i] = __float_as_uint(__uint_as_float(info[i]) * (1.0f / kLift));
             if (!fine) info[0] = 0x7FC00000u;  // NaN: the position has no weight
             const int buf = visit % S::tables;
             if (SPARSE) ok = wait_warp(&ctl.slot_full[buf], visit / S::tables);
-            info[5] = reinterpret_cast<const uint32_t*>(smem + S::off_slot)[buf * kTile + row];
+            // what the scales have to be multiplied by, -1: no position
+            const int slot = reinterpret_cast<const int*>(smem + S::off_slot)[buf * kTile + row];
+            info[5] = __float_as_uint(slot < 0 ? -1.f : most >= kLarge ? kLift : 1.f);
             if (SPARSE) {
               __syncwarp();
               if (lane == 0) tc::mbar_arrive(&ctl.slot_empty[buf]);
@@ -768,7 +795,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         uint64_t acc[W / 2];
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) acc[i] = 0ull;
-        int slot = -1;
+        float lift = -1.f;
 #pragma unroll 1
         for (int s = 0; s < 5; ++s, ++d) {
           const uint32_t at = d % S::accs;
@@ -776,7 +803,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           if (!ok) break;
           tc::fence_after_sync();
           const float scale = tmem_ld1(tile_info + (s ? s - 1 : 4));
-          if (s == 0) slot = __float_as_int(tmem_ld1(tile_info + 5));
+          if (s == 0) lift = tmem_ld1(tile_info + 5);
 #pragma unroll
           for (int h = 0; h < W / 16; ++h) {  // (16 columns at a time: 768 threads have 80 registers each)
             uint32_t v[16];
@@ -798,8 +825,17 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         if (!ok) break;
         const int pos = w.tile * kTile + row;
         const ulonglong2* cols = reinterpret_cast<const ulonglong2*>(smem + S::off_col) + (buf * N + part * W) / 2;
+        const int2* limits = reinterpret_cast<const int2*>(smem + S::off_limit) + (buf * N + part * W) / 2;
         float total = 0.f;
-        if (SPARSE || ctl.all_seen[buf]) {
+        if (__any_sync(0xffffffffu, lift > 1.f)) {
+          float each[W];
+#pragma unroll
+          for (int i = 0; i < W / 2; ++i) {
+            each[2 * i] = unpair(acc[i]).x;
+            each[2 * i + 1] = unpair(acc[i]).y;
+          }
+          total = sum_lifted(each, W, reinterpret_cast<const float*>(cols), reinterpret_cast<const int*>(limits), pos, fmaxf(lift, 1.f));
+        } else if (SPARSE || ctl.all_seen[buf]) {
           float odd = 0.f;
 #pragma unroll
           for (int i = 0; i < W / 2; ++i) {
@@ -810,7 +846,6 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           }
           total += odd;
         } else {
-          const int2* limits = reinterpret_cast<const int2*>(smem + S::off_limit) + (buf * N + part * W) / 2;
 #pragma unroll
           for (int i = 0; i < W / 2; ++i) {
             const ulonglong2 k = cols[i];
@@ -823,7 +858,7 @@ attn_mass_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         if (lane == 0) tc::mbar_arrive(&ctl.col_empty[buf]);
         ok = wait_warp(&ctl.part_empty, visit ^ 1u);
         if (!ok) break;
-        reinterpret_cast<float*>(smem + S::off_sum)[part * kTile + row] = slot >= 0 ? total : -1.f;
+        reinterpret_cast<float*>(smem + S::off_sum)[part * kTile + row] = lift > 0.f ? total : -1.f;
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ctl.part_full);
         more = walk_next<N>(ws, pl.groups, w);
