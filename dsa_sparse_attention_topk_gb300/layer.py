@@ -145,8 +145,7 @@ class DsaDecodeLayer:
         out = prefix_attn(q_sfa, self.kv_cache, prefix_pages, prefix_len, page_table, seq_lens, q_seq, q_pos, max_ctx,
                           self.sm_scale, out_lse=lse)
         if mass is not None:
-            attn_mass(q_sfa, self.kv_cache, page_table, seq_lens, q_seq, q_pos, lse, max_ctx, self.sm_scale, mass=mass,
-                      workspace=self._mass_ws(q_sfa.shape[0], seq_lens.shape[0]))
+            attn_mass(q_sfa, self.kv_cache, page_table, seq_lens, q_seq, q_pos, lse, max_ctx, self.sm_scale, mass=mass)
         return out
 
     def evict(self, mass, page_table, seq_lens, budget, sinks=0, recent=0, dst_table=None):
