@@ -49,7 +49,6 @@ class DsaDecodeLayer:
         self.h_i, self.h_s, self.topk, self.sm_scale = h_i, h_s, topk, float(sm_scale)
         self.k_cache = alloc_k_cache(num_pages, self.device)
         self.kv_cache = alloc_kv_cache(num_pages, self.device)
-        self._ws = {}
         self._bufs = {}
 
     def write(self, k, kv, slot_mapping, pos=None):
@@ -89,6 +88,7 @@ class DsaDecodeLayer:
                 "idx": torch.empty(n_q, self.topk, dtype=torch.int32, device=dev),
                 "out": torch.empty(n_q, self.h_s, 512, dtype=torch.bfloat16, device=dev),
                 "lse": torch.empty(n_q, self.h_s, dtype=torch.float32, device=dev),
+                "mass_ws": {},
             }
             ws = sparse_attn_workspace_size(n_q, self.h_s, self.topk)
             b["ws"] = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev) if ws else None
@@ -98,11 +98,14 @@ class DsaDecodeLayer:
             self._bufs[n_q] = b
         return b
 
-    def _mass_ws(self, n_q, n_seq):
-        ws = self._ws.get((n_q, n_seq))
+    def _mass_ws(self, n_q, n_seq, b):
+        """The workspace of a step's weights, one of the buffers b.  Sequences count where there are more of them than rows:
+        then by powers of two, each with a workspace that stays, for a recorded step may hold it."""
+        most = n_q if n_seq <= n_q else min(1 << (n_seq - 1).bit_length(), max(n_seq, 65536))
+        ws = b["mass_ws"].get(most)
         if ws is None:
-            ws = torch.empty(attn_mass_workspace_size(n_q, self.h_s, n_seq), dtype=torch.uint8, device=self.device)
-            self._ws[n_q, n_seq] = ws
+            ws = torch.empty(attn_mass_workspace_size(n_q, self.h_s, most), dtype=torch.uint8, device=self.device)
+            b["mass_ws"][most] = ws
         return ws
 
     def _weigh(self, mass, q_sfa, page_table, seq_lens, q_seq, b):
@@ -110,7 +113,7 @@ class DsaDecodeLayer:
         if "weights" not in b:
             b["weights"] = torch.empty(b["idx"].shape, dtype=torch.float32, device=self.device)
         sparse_attn_mass(q_sfa, self.kv_cache, page_table, seq_lens, q_seq, b["idx"], b["lse"], self.sm_scale, mass=mass,
-                         out=b["weights"], workspace=self._mass_ws(q_sfa.shape[0], seq_lens.shape[0]))
+                         out=b["weights"], workspace=self._mass_ws(q_sfa.shape[0], seq_lens.shape[0], b))
 
     def decode(self, q_idx, w, q_sfa, page_table, seq_lens, q_seq, q_pos, max_ctx, q_group=1, rope_pos=None, mass=None):
         """Indexer + Top-K + SFA for n_q query rows.  Returns (out bf16 [n_q, h_s, 512],
