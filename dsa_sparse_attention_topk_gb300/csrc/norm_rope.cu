@@ -129,11 +129,8 @@ cudaError_t launch_fwd(const NormArgs& a, NormGeom g, cudaStream_t s) {
   const int64_t per = (steps + most - 1) / most;
   norm_table(a, g, per * g.rows_step);
   const size_t smem = norm_shared_bytes(a, g);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<T, V, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = norm_allow_shared(norm_rope_kernel<T, V, NV>, smem);
+  if (e != cudaSuccess) return e;
   return launch_pdl(norm_rope_kernel<T, V, NV>, dim3(static_cast<unsigned>((steps + per - 1) / per)), dim3(kNormThreads),
                     smem, s, 1, a, g, per * g.rows_step);
 }

@@ -22,6 +22,10 @@ namespace dsa {
 namespace {
 
 constexpr int kNormThreads = 256;
+// Shared memory that a block takes at most: of 1024 dims weights and biases 8 KB, and of the rows of one step, 8192
+// elements, a sine and a cosine a pair and the exchange 32 KB each; the gradient's sums 64 KB in their place.  What a kernel may
+// ask for is always this, whatever a call needs: another thread's call may set it between this one's and its launch.
+constexpr int kNormShared = 76 * 1024;
 
 struct NormGeom {
   int lanes;          // G: lanes a row, a power of two of 8..32
@@ -403,6 +407,12 @@ inline void norm_table(const NormArgs& a, NormGeom& g, int64_t rows_block) {
   while (rows > g.rows_step && tokens(rows) * bytes > 16384) rows = (rows / 2 + g.rows_step - 1) / g.rows_step * g.rows_step;
   g.rows_table = static_cast<int>(std::min<int64_t>(rows, 1 << 30));
   g.tokens_table = static_cast<int>(tokens(rows));
+}
+template <typename K>
+cudaError_t norm_allow_shared(K kernel, size_t bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  if (bytes > kNormShared) return cudaErrorInvalidValue;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormShared);
 }
 inline size_t norm_shared_bytes(const NormArgs& a, const NormGeom& g) {
   const bool exchange = !(a.layout == DSA_ROPE_HALF ? g.turn_word >= 0 || g.pair_word >= 0 : g.vectors < a.d);  // (see turn_row)

@@ -205,12 +205,9 @@ cudaError_t launch_bwd_k(const NormArgs& a, NormGeom g, cudaStream_t s) {
   const int blocks = static_cast<int>((steps + per - 1) / per), kinds = SHIFT ? 2 : 1;
   norm_table(a, g, per * g.rows_step);
   const size_t smem = std::max(norm_shared_bytes(a, g), sizeof(float) * kinds * (kNormThreads / 32) * a.span);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(norm_rope_grad_kernel<T, V, NV, SHIFT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
-  cudaError_t e = launch_pdl(norm_rope_grad_kernel<T, V, NV, SHIFT>, dim3(blocks), dim3(kNormThreads), smem, s, 1, a, g,
+  cudaError_t e = norm_allow_shared(norm_rope_grad_kernel<T, V, NV, SHIFT>, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(norm_rope_grad_kernel<T, V, NV, SHIFT>, dim3(blocks), dim3(kNormThreads), smem, s, 1, a, g,
                              per * g.rows_step);
   if (e != cudaSuccess || (!a.dweight && !a.dbias)) return e;
   return launch_pdl(norm_grad_sum_kernel, dim3((kinds * a.span + 31) / 32), dim3(32, 32), 0, s, 1,
