@@ -163,7 +163,7 @@ cudaError_t launch_fwd_t(const NormArgs& a, cudaStream_t s) {
 // One warp per token, lane i the sine and cosine of frequency i, as in the other writers.  The normed and turned
 // values are quantised from fp32: a code is the nearest of a value that is good to some 2^-21 of its
 // size and its pair's, so a value that close to the border between two codes may land on either side.  A row whose sum of squares is
-// not finite has no norm: it is stored as NaN.
+// not finite, or 0 without eps, has no norm: it is stored as NaN.
 constexpr int kWarpsPerBlock = 8;
 constexpr int kRot = 64;
 
@@ -172,7 +172,7 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// 1 / sqrt(mean square + eps), NaN where that has no finite value
+// 1 / sqrt(mean square + eps), NaN where that sum is not finite; infinite where it is 0
 __device__ __forceinline__ float norm_factor(float sum, float inv_n, float eps) {
   const float m = fmaf(sum, inv_n, eps);
   return m < INFINITY ? rsqrtf(m) : NAN;
@@ -205,7 +205,8 @@ __device__ __forceinline__ void norm_store_k(uint2 raw, float4 w, float4 b, floa
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] -= mean;
   }
-  const float r = norm_factor(warp_sum(fmaf(x[0], x[0], x[1] * x[1]) + fmaf(x[2], x[2], x[3] * x[3])), 1.0f / kIdxDim, a.eps);
+  float r = norm_factor(warp_sum(fmaf(x[0], x[0], x[1] * x[1]) + fmaf(x[2], x[2], x[3] * x[3])), 1.0f / kIdxDim, a.eps);
+  if (!(r < INFINITY)) r = NAN;
   x[0] = fmaf(x[0] * r, w.x, b.x);
   x[1] = fmaf(x[1] * r, w.y, b.y);
   x[2] = fmaf(x[2] * r, w.z, b.z);
@@ -285,7 +286,7 @@ __device__ __forceinline__ void norm_store_kv(const uint2 (&raws)[4], uint32_t r
       y[4 * tile + i + 1] = z.y;
       m = fmaxf(m, fmaxf(fabsf(z.x), fabsf(z.y)));
     }
-    m = warp_amax(r == r ? m : NAN);
+    m = warp_amax(r < INFINITY ? m : NAN);
     if (lane == tile) amax = m;
   }
   const float s = __fdiv_rn(amax, 448.0f);

@@ -234,8 +234,8 @@ int dsa_norm_rope_grad(const void* dy, const void* x, void* dx, int32_t dtype, i
  * its first 512 (root mean square, kv_weight); both are turned to pos[i] and stored in the formats of
  * dsa_quant_kv.  Nothing is rounded in between: a code is the nearest of a value that fp32 arithmetic gives,
  * good to 2^-20 of its own and its pair's size, so that a value that close to the border between two codes may get
- * either; scales are good to 2^-20.  A key, or the normed 512 dims of a row, whose sum of squares is not finite is
- * stored as NaN.
+ * either; scales are good to 2^-20.  A key, or the normed 512 dims of a row, whose sum of squares in fp32 is not
+ * finite, or 0 with eps = 0, is stored as NaN.
  *   k_weight, k_bias  nullable [128] fp32, kv_weight nullable [512] fp32, 16-byte aligned.
  *   eps               not negative; both norms'.
  *   the others        as for dsa_rope_quant_kv.
