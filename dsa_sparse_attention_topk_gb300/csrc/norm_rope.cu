@@ -178,12 +178,13 @@ __device__ __forceinline__ float norm_factor(float sum, float inv_n, float eps) 
   return m < INFINITY ? rsqrtf(m) : NAN;
 }
 
-// phase_cs to within 2^-22 of the amplitude, a third of its instructions: the norm in front of the turn is no better.  The
-// rest of the phase in 2^-33 turns, Taylor sums of one float
+// phase_cs to within 2^-22 of each value, a third of its instructions: the norm in front of the turn is no better.  Taylor
+// sums of one float, of the rest of the phase rounded as a whole: cut off at a fixed place, a small angle's sine, which may be
+// all that a key's group of 32 holds, would have lost what lies behind it
 __device__ __forceinline__ float2 phase_cs_near(int pos, int64_t turns, float amp) {
   uint32_t quarter;
-  const float x = static_cast<float>(static_cast<int>(phase_rest(pos, turns, quarter) >> 31)) *
-                  static_cast<float>(6.283185307179586476925 / 8589934592.0);  // 2 pi 2^-33
+  const float x = static_cast<float>(phase_rest(pos, turns, quarter)) *
+                  static_cast<float>(6.283185307179586476925 / 18446744073709551616.0);  // 2 pi 2^-64
   const float z = x * x;
   float S = fmaf(1.0f / 362880.0f, z, -1.0f / 5040.0f), C = fmaf(-1.0f / 3628800.0f, z, 1.0f / 40320.0f);
   S = fmaf(S, z, 1.0f / 120.0f);
