@@ -161,8 +161,8 @@ cudaError_t launch_fwd_t(const NormArgs& a, cudaStream_t s) {
 
 // ---- the cache writers with norm and rotation on the way -----------------------------
 // One warp per token, lane i the sine and cosine of frequency i, as in the other writers.  The normed and turned
-// values are quantised from fp32: a code is the nearest of a value that is good to some 2^-21 of its
-// size and its pair's, so a value that close to the border between two codes may land on either side.  A row whose sum of squares is
+// values are quantised from fp32: a code is the nearest of a value that is good to 2^-19 of the sizes of its parts and
+// its pair's (a mean adds 2^-21 of what it takes off), so one that close to the border between two codes may land on either side.  A row whose sum of squares is
 // not finite, or 0 without eps, has no norm: it is stored as NaN.
 constexpr int kWarpsPerBlock = 8;
 constexpr int kRot = 64;
@@ -178,7 +178,7 @@ __device__ __forceinline__ float norm_factor(float sum, float inv_n, float eps) 
   return m < INFINITY ? rsqrtf(m) : NAN;
 }
 
-// phase_cs to within 2^-22 of each value, a third of its instructions: the norm in front of the turn is no better.  Taylor
+// phase_cs to within 2^-21 of each value, a third of its instructions: the norm in front of the turn is no better.  Taylor
 // sums of one float, of the rest of the phase rounded as a whole: cut off at a fixed place, a small angle's sine, which may be
 // all that a key's group of 32 holds, would have lost what lies behind it
 __device__ __forceinline__ float2 phase_cs_near(int pos, int64_t turns, float amp) {

@@ -232,9 +232,11 @@ int dsa_norm_rope_grad(const void* dy, const void* x, void* dx, int32_t dtype, i
  * dsa_norm_rope_quant_kv -- the cache writers with norm and rotation on the way: token i's key is normed over
  * its 128 dims (k_center, k_weight, k_bias as center, weight and bias of dsa_norm_rope) and its latent row over
  * its first 512 (root mean square, kv_weight); both are turned to pos[i] and stored in the formats of
- * dsa_quant_kv.  Nothing is rounded in between: a code is the nearest of a value that fp32 arithmetic gives,
- * good to 2^-20 of its own and its pair's size, so that a value that close to the border between two codes may get
- * either; scales are good to 2^-20.  A key, or the normed 512 dims of a row, whose sum of squares in fp32 is not
+ * dsa_quant_kv.  Nothing is rounded in between: a code is the nearest of a value that fp32 arithmetic gives, so
+ * that a value close to the border between two codes may get either.  With u the normed value, a key's dim is good to
+ * 2^-19 (|u w| + |b|), its own and, where it is turned, its pair's, times the amplitude; with k_center the mean adds
+ * 2^-21 |w| mean|x| / sigma (sigma the key's deviation), again for both; a latent row's dims and scales are good to
+ * 2^-20 of theirs.  A key, or the normed 512 dims of a row, whose sum of squares in fp32 is not
  * finite, or 0 with eps = 0, is stored as NaN.
  *   k_weight, k_bias  nullable [128] fp32, kv_weight nullable [512] fp32, 16-byte aligned.
  *   eps               not negative; both norms'.
@@ -439,8 +441,8 @@ int dsa_prefix_attn(const void* q_bf16, int32_t n_q, int32_t h_s, const uint8_t*
  * it; it is what an eviction goes by (dsa_evict_select).  Both calls take the queries and the log-sum-exps of an
  * attention that has run (dsa_prefix_attn, dsa_sparse_attn: its out_lse) and form its probabilities again,
  *     w[t, p] = sum_h exp(sm_scale q[t, h] . kv[p] - lse[t, h]),
- * from the exact dequantised kv[p], with fp32 roundings alone: a weight is good to some 2^-19 times the size of
- * its logits.  (lse as an attention returns it may hold that attention's own roundings.)
+ * from the exact dequantised kv[p], with fp32 roundings alone: a weight is good to some 2^-19 times
+ * sm_scale sum |q[i] kv[p][i]|.  (lse as an attention returns it may hold that attention's own roundings.)
  * mass holds whole numbers of 2^-36 (DSA_MASS_ONE is a weight of 1): additions to it are atomic, and equal calls
  * give equal bits whatever their order.  A sum of rows is rounded to that unit for each part of the work, 16
  * to 128 heads; the sum must stay below 2^27, one position's weight in a call counts as 2^26 at most.
