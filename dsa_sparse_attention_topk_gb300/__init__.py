@@ -794,8 +794,8 @@ def evict_select(mass, seq_lens, budget, sinks=0, recent=0, kept=None, new_lens=
     _need_shaped(kept, torch.int32, (n_seq, budget), "evict_select: kept")
     _need_shaped(new_lens, torch.int32, (n_seq,), "evict_select: new_lens")
     _need_shaped(kept_mass, torch.int64, (n_seq, budget), "evict_select: kept_mass")
-    if new_lens.data_ptr() == seq_lens.data_ptr() and n_seq:
-        raise ValueError("evict_select: new_lens must not be seq_lens")
+    if n_seq and abs(new_lens.data_ptr() - seq_lens.data_ptr()) < 4 * n_seq:
+        raise ValueError("evict_select: new_lens must not share memory with seq_lens")
     _call_on(dev, stream, lib().dsa_evict_select, mass.data_ptr(), mass.stride(0), seq_lens.data_ptr(), n_seq, max_ctx,
              budget, sinks, recent, kept.data_ptr(), new_lens.data_ptr(), kept_mass.data_ptr())
     return kept, new_lens, kept_mass

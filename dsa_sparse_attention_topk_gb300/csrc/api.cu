@@ -680,7 +680,8 @@ int dsa_evict_select(const int64_t* mass, int64_t mass_stride, const int32_t* se
   if (!mass || !seq_lens || !kept || !new_lens) return fail(DSA_ERR_INVALID_ARG, "evict_select: null pointer");
   if (!aligned(mass, 8) || !aligned(kept_mass, 8) || !aligned(seq_lens, 4) || !aligned(kept, 4) || !aligned(new_lens, 4))
     return fail(DSA_ERR_INVALID_ARG, "evict_select: a pointer is not aligned to its element");
-  if (new_lens == seq_lens) return fail(DSA_ERR_INVALID_ARG, "evict_select: new_lens must not be seq_lens");
+  if (static_cast<const int32_t*>(new_lens) < seq_lens + n_seq && seq_lens < new_lens + n_seq)
+    return fail(DSA_ERR_INVALID_ARG, "evict_select: new_lens must not share memory with seq_lens");
   unsigned* st = status_ptr();
   if (!st) return fail(DSA_ERR_CUDA, "evict_select: no CUDA device");
   dsa::EvictSelectArgs a{mass, mass_stride, seq_lens, n_seq, max_ctx, budget, sinks, recent, kept, new_lens, kept_mass, st};

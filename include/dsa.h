@@ -499,7 +499,7 @@ int dsa_sparse_attn_mass(const void* q_bf16, int32_t n_q, int32_t h_s, const uin
  *   seq_lens   [n_seq] int32 in [0, max_ctx]; any other flags DSA_STATUS_BAD_LEN and counts as 0.
  *   max_ctx    1..1048576.      budget  1..1048576, at least sinks + recent.
  *   kept       [n_seq][budget] int32: the positions in ascending order, -1 behind the last.
- *   new_lens   [n_seq] int32: how many stay.  It must not be seq_lens.
+ *   new_lens   [n_seq] int32: how many stay.  It must not overlap seq_lens.
  *   kept_mass  nullable [n_seq][budget] int64: their weights, 0 behind the last; must not overlap mass.
  */
 int dsa_evict_select(const int64_t* mass, int64_t mass_stride, const int32_t* seq_lens, int32_t n_seq, int32_t max_ctx,
@@ -512,8 +512,8 @@ int dsa_evict_select(const int64_t* mass, int64_t mass_stride, const int32_t* se
  *   kept       [n_seq][budget] int32 positions (for instance dsa_evict_select's), -1: none.  Any order.
  *   page_table [n_seq][max_pages] int32: the pages the positions lie in.
  *   dst_table  [n_seq][dst_max_pages] int32: the pages that receive them, dst_max_pages >= ceil(budget / 64); none of
- *              them may be a page that is read.  Null (or page_table itself): in place, and no two
- *              sequences may share a page that is written.
+ *              them may be a page that is read.  Null (or page_table itself): in place, max_pages >=
+ *              ceil(budget / 64), and no two sequences may share a page that is written.
  *   k_cache, kv_cache   num_pages pages each, 16-byte aligned; one of them may be null.
  *   workspace  in place: dsa_evict_compact_workspace_size bytes (752 a kept position), 256-byte aligned.
  * A position or page out of range flags DSA_STATUS_BAD_INDEX or _BAD_PAGE, and that record is not copied.
