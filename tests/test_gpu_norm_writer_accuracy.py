@@ -7,6 +7,8 @@ bias one of the result: 12 (key), 13.5 (latent) of |u w| + |b|.  The sines are g
 scales one: 14.5 < 2^-20.  With a mean its sum takes 7 roundings: 7 units < 2^-21 of mean|x| / sigma |w|, and the difference one
 of |u w|, which the 2^-19 have room for.  The turned 64 dims of a latent row: 10 units of the pair's sizes, two for the quotient."""
 
+import math
+
 import pytest
 import torch
 
@@ -62,3 +64,24 @@ def test_codes_and_scales(dsa, k_norm, mean, layout):
         slack = d[:, part].amax(-1, keepdim=True) if t == 4 else 2.0 ** -20 * top
         assert ((s - top / 448).abs() <= slack / 448 + 2.0 ** -24 * s).all()
         assert _inside(vcodes[:, part], y[:, part], d[:, part], s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("exponent", [-30, -36, -45, -55])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_small_angles_of_any_bits(dsa, exponent, sign):
+    """Sines alone in their group (keys zero in the part that meets the cosines), of angles of 2^exponent turns and any
+    lower bits, on both sides of 0: good to 2^-19 of their own."""
+    n = 64
+    g = torch.Generator().manual_seed(-exponent)
+    k = torch.randn(n, 128, generator=g).to(torch.bfloat16)
+    k[:, 32:64] = 0
+    turns = sign * torch.randint(1 << (63 + exponent), 1 << (64 + exponent), (32,), generator=g)
+    kc = dsa.alloc_k_cache(1)
+    dsa.norm_rope_quant_kv(k.cuda(), None, torch.ones(n, dtype=torch.int32).cuda(), torch.arange(n).cuda(), kc, None, turns.cuda())
+    codes, e8, _, _ = _stored(kc, dsa.alloc_kv_cache(1), torch.arange(n))
+    u, _ = _unit(k.double(), 128, False, 1e-6)
+    y = u[:, :32] * torch.sin(2 * math.pi * turns.double() * 2.0 ** -64)
+    top, e = y.abs().amax(-1), e8[:, 1] - 127
+    assert ((e >= torch.frexp(top * (1 - 2.0 ** -19))[1] - 9) & (e <= torch.frexp(top * (1 + 2.0 ** -19))[1] - 9)).all()
+    assert _inside(codes[:, 32:64], y, 2.0 ** -19 * y.abs(), torch.exp2(e.double())[:, None])
