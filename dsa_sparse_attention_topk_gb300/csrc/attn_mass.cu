@@ -22,8 +22,8 @@
 // entries (sparse).  Items (group, chunk of N columns, tile of 128 positions) are shared out evenly over one CTA per
 // SM; a chunk's queries stay while its tiles pass, each tile a ring of pieces of 128 dims.
 //
-// Bound.  32 rows of 128 heads over 16-32K positions each take 132 us (what has to be read 72, products 59), 64 rows of
-// 128 heads over 32K 313 (products 157), 512 rows of 128 heads over 2048 entries 196 (products 74).  A tile is 6000 to
+// Bound.  32 rows of 128 heads over 16-32K positions each take 131 us (what has to be read 72, products 59), 64 rows of
+// 128 heads over 32K 310 (products 157), 512 rows of 128 heads over 2048 entries 199 (products 74).  A tile is 6000 to
 // 7000 cycles at 128 columns, 2304 of them products: an accumulator waits for the warps that scale and add it, two of
 // them fit beside the widened codes, and those warps also have the tile's exponentials, 500 cycles of which the
 // accumulators lie full.  Tried and slower: one read of 32 columns instead of two of 16 (145 us: spills), products of

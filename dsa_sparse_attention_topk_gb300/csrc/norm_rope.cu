@@ -7,7 +7,7 @@
 // mean is taken off before anything is squared, so that a row far from zero loses nothing.
 //
 // Bound: memory, each value read and written once.  A row stays in the registers of 8 to 32 lanes between the
-// sums and the turn, 8 to 32 values a lane.  4096 x 64 x 128 bf16 take 27 us, 5 TB/s (a plain copy 20, this kernel
+// sums and the turn, 8 to 32 values a lane.  4096 x 64 x 128 bf16 take 26 us, 5.2 TB/s (a plain copy 20, this kernel
 // without weights, sums and turn 22.5): the rest is issue and the tables' way through shared memory.
 
 #include "norm_rope.cuh"

@@ -7,8 +7,9 @@
 //
 // Bound: memory, dy and x read and dx written once.  A block takes a run of rows and each lane keeps the sums of its
 // own dims in registers; the blocks' sums go to the workspace and a second kernel adds them, always in the same
-// order, so that equal inputs give equal bits.  4096 x 64 x 128 bf16 take 41.5 us, 4.9 TB/s, 2047 x 63 x 192 fp32 52 us, 5.7
-// TB/s (at a plain copy's rate 30 and 44.5).
+// order, so that equal inputs give equal bits.  4096 x 64 x 128 bf16 take 41 us, 4.9 TB/s, 2047 x 63 x 192 fp32 52 us, 5.7
+// TB/s (at a plain copy's rate 30 and 44.5).  Where a lane has 24 or 32 elements, the two rows' values and the sums do not fit
+// its registers (16-bit heads of 256: 3.4 TB/s, with a bias 2.2).
 
 #include "norm_rope.cuh"
 
