@@ -731,8 +731,8 @@ int dsa_topk_merge(const int32_t* cand_idx, const float* cand_scores, const int3
                    const int32_t* local_lo, const int32_t* local_hi, int32_t* out_local, void* stream) {
   if (n_q < 0) return fail(DSA_ERR_INVALID_ARG, "topk_merge: n_q < 0");
   if (n_parts < 1 || k_in < 1 || topk < 1) return fail(DSA_ERR_INVALID_ARG, "topk_merge: n_parts, k_in and topk must be >= 1");
-  if (static_cast<int64_t>(n_parts) * k_in > 16384)
-    return fail(DSA_ERR_UNSUPPORTED, "topk_merge: n_parts * k_in must be <= 16384 (got %lld)",
+  if (static_cast<int64_t>(n_parts) * k_in > dsa::kMostMerged)
+    return fail(DSA_ERR_UNSUPPORTED, "topk_merge: n_parts * k_in must be <= %d (got %lld)", dsa::kMostMerged,
                 static_cast<long long>(n_parts) * k_in);
   if (n_q == 0) return DSA_OK;
   if (!cand_idx || !cand_scores || !out_idx) return fail(DSA_ERR_INVALID_ARG, "topk_merge: null pointer");

@@ -143,8 +143,9 @@ cudaError_t launch_topk_merge(const TopkMergeArgs& a, cudaStream_t s) {
   if (a.n_q == 0) return cudaSuccess;
   const int n_pow2 = topk_merge_pow2(a.n_parts * a.k_in);
   const size_t smem = static_cast<size_t>(n_pow2) * sizeof(uint64_t);
+  // (always the most that a call may need: another thread's call may set it between this one's and its launch)
   cudaError_t e = cudaFuncSetAttribute(topk_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+                                       kMostMerged * static_cast<int>(sizeof(uint64_t)));
   if (e != cudaSuccess) return e;
   return launch_pdl(topk_merge_kernel, dim3(a.n_q), dim3(kMergeThreads), smem, s, 1, a.cand_idx, a.cand_scores,
                     a.part_offsets, a.n_parts, a.n_q, a.k_in, a.topk, n_pow2, a.out_idx, a.out_scores, a.local_lo,

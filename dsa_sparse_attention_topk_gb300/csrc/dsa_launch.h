@@ -259,6 +259,7 @@ size_t prefix_workspace_bytes(int n_q, int h_s, int n_seq, int prefix_len, int m
 void prefix_plan_numbers(int n_q, int h_s, int n_seq, int prefix_len, int max_ctx, int32_t* out);
 
 int topk_merge_pow2(int n);
+constexpr int kMostMerged = 16384;  // candidates of a row, a power of two
 cudaError_t launch_topk_merge(const TopkMergeArgs& a, cudaStream_t s);
 cudaError_t launch_lse_combine(const void* o_parts, const float* lse_parts, int n_parts, int n_q, int h, void* out,
                                float* out_lse, cudaStream_t s);

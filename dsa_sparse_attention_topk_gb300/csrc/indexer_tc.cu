@@ -752,7 +752,8 @@ cudaError_t launch_gh(const IndexerArgs& a, cudaStream_t s, const char** err, in
     return cudaErrorInvalidValue;
   }
   auto kern = indexer_tc_kernel<G, HP>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // (always the device's most: another thread's call may set it between this one's and its launch)
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.smem_optin);
   if (e != cudaSuccess) return e;
   if (C > 8) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
